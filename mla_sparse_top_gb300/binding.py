@@ -1,5 +1,5 @@
 """ctypes binding of the C ABI in include/mla_sparse.h, mla_indexer.h,
-mla_cache.h and mla_prolog.h.
+mla_cache.h, mla_prolog.h, mla_pages.h and mla_rope.h.
 
 Argument marshalling only: shapes and dtypes are read off torch tensors, the
 device pointers and the current CUDA stream are passed through, and a
@@ -28,6 +28,7 @@ MLA_KV_BF16 = 0
 MLA_KV_INT8 = 1
 MLA_DEVICE_BAD_BLOCK = 0x1
 MLA_DEVICE_TIMEOUT = 0x2
+MLA_DEVICE_NO_PAGE = 0x4
 
 EXPORTED_SYMBOLS = ("mla_sparse_attn_fwd", "mla_swa_fwd", "mla_compressed_attn_fwd", "mla_sparse_last_error", "mla_sparse_device_status",
                     "mla_sparse_get_device_status", "mla_sparse_set_wait_limit_ns", "mla_sparse_launch_count",
@@ -37,6 +38,10 @@ EXPORTED_SYMBOLS = ("mla_sparse_attn_fwd", "mla_swa_fwd", "mla_compressed_attn_f
                     "mla_indexer_last_error", "mla_indexer_topk_noalloc", "mla_cache_write",
                     "mla_cache_last_error", "mla_cache_device_status", "mla_prolog_workspace_bytes", "mla_prolog",
                     "mla_prolog_last_error", "mla_prolog_device_status")
+
+# mla_pages.h and mla_rope.h: the calls around a drafted decode step
+STEP_SYMBOLS = ("mla_page_plan", "mla_page_last_error", "mla_page_device_status", "mla_rope_table", "mla_rope_apply",
+                "mla_rope_last_error", "mla_rope_device_status")
 
 
 class MlaDims(ctypes.Structure):
@@ -68,6 +73,39 @@ class PrologDims(ctypes.Structure):
 class PrologWeights(ctypes.Structure):
     """mla_prolog_weights (device pointers)."""
     _fields_ = [(name, ctypes.c_void_p) for name in ("wq_a", "gamma_cq", "wq_b", "w_uk", "wkv", "gamma_ckv")]
+
+
+class PageDims(ctypes.Structure):
+    """mla_page_dims."""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "B", "S1", "T", "block_size", "num_blocks", "max_blocks_per_seq", "num_free")]
+
+
+class PageIo(ctypes.Structure):
+    """mla_page_io (device pointers)."""
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "ctx_lens", "new_lens", "free_blocks", "parents", "block_table", "act_seqs", "cache_index", "positions",
+        "seq_ids", "cu_seqs", "tree_mask", "num_taken")]
+
+
+class RopeParams(ctypes.Structure):
+    """mla_rope_params."""
+    _fields_ = [(name, ctypes.c_double) for name in (
+        "theta", "factor", "orig_positions", "beta_fast", "beta_slow", "mscale")] + [("scaling", ctypes.c_int32)]
+
+
+class RopeTensor(ctypes.Structure):
+    """mla_rope_tensor."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("rows", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rot_off", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RopeDims(ctypes.Structure):
+    """mla_rope_dims."""
+    _fields_ = [(name, ctypes.c_int32) for name in ("T", "rot_dim", "half", "inverse", "dtype")]
 
 
 class MlaError(RuntimeError):
@@ -140,6 +178,18 @@ def load_library(path: str = LIB_PATH):
     lib.mla_prolog_last_error.restype = ctypes.c_char_p
     lib.mla_prolog_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]
     lib.mla_prolog_device_status.restype = ctypes.c_int
+    lib.mla_page_plan.argtypes = [ctypes.POINTER(PageDims), ctypes.POINTER(PageIo), vp]
+    lib.mla_rope_table.argtypes = [ctypes.POINTER(RopeParams), ctypes.c_int32, ctypes.c_int32] + [vp] * 4
+    lib.mla_rope_apply.argtypes = [ctypes.POINTER(RopeDims), ctypes.POINTER(RopeParams), vp,
+                                   ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), vp]
+    for name in STEP_SYMBOLS:
+        fn = getattr(lib, name)
+        if name.endswith("_last_error"):
+            fn.argtypes, fn.restype = [], ctypes.c_char_p
+        else:
+            fn.restype = ctypes.c_int
+        if name.endswith("_device_status"):
+            fn.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]
     _lib = lib
     return lib
 
@@ -462,4 +512,145 @@ def prolog_device_status(clear: bool = True, stream=None) -> int:
     st = lib.mla_prolog_device_status(_stream_handle(stream), ctypes.byref(flags), 1 if clear else 0)
     if st not in (MLA_OK, -7):
         raise MlaError(st, lib.mla_prolog_last_error().decode())
+    return int(flags.value)
+
+
+# ------------------------------------------------------------------ page plan and rotary positions
+def _need(t, dtype, shape, what: str):
+    """Check one tensor of the page plan and rotary calls: on the current
+    device, dense, of this type and (where given) this shape."""
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} must be a dense {dtype} tensor" + (f" of shape {tuple(shape)}" if shape is not None
+                                                                     else ""))
+    _on_current_device(t, what)
+    return t.data_ptr()
+
+
+def _on_current_device(t, what: str):
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
+
+
+def mla_page_plan(ctx_lens, new_lens, free_blocks, block_table, act_seqs, cache_index, *, S1: int, num_blocks: int,
+                  parents=None, positions=None, seq_ids=None, cu_seqs=None, tree_mask=None, num_taken=None,
+                  stream=None):
+    """Enqueue one call of the C entry point with the same name: block tables,
+    slot maps and positions of one step.
+
+    ctx_lens (B,) int32 cached positions, new_lens (B,) int32 new tokens (None:
+    S1 each), free_blocks (F,) int32, block_table (B, W) int32 updated in place;
+    outputs act_seqs (B,) int32, cache_index (T,) int64 and, where given,
+    positions (T,) int32, seq_ids (T,) int32, cu_seqs (B + 1,) int32, tree_mask
+    (T, ceil(S1 / 64)) int64 and num_taken (1,) int32.  S1 >= 1: T = B * S1
+    padded rows, parents (B, S1) int32 gives a tree of drafted tokens.  S1 = 0:
+    packed rows, T is the capacity."""
+    lib = load_library()
+    i32 = torch.int32
+    B, W = block_table.shape
+    T = cache_index.numel()
+    io = PageIo(_need(ctx_lens, i32, (B,), "ctx_lens"),
+                None if new_lens is None else _need(new_lens, i32, (B,), "new_lens"),
+                _need(free_blocks, i32, None, "free_blocks"),
+                None if parents is None else _need(parents, i32, (B, S1), "parents"),
+                _need(block_table, i32, None, "block_table"), _need(act_seqs, i32, (B,), "act_seqs"),
+                _need(cache_index, torch.int64, (T,), "cache_index"),
+                None if positions is None else _need(positions, i32, (T,), "positions"),
+                None if seq_ids is None else _need(seq_ids, i32, (T,), "seq_ids"),
+                None if cu_seqs is None else _need(cu_seqs, i32, (B + 1,), "cu_seqs"),
+                None if tree_mask is None else _need(tree_mask, torch.int64, (T, (S1 + 63) // 64), "tree_mask"),
+                None if num_taken is None else _need(num_taken, i32, (1,), "num_taken"))
+    dims = PageDims(B, S1, T, 128, num_blocks, W, free_blocks.numel())
+    st = lib.mla_page_plan(ctypes.byref(dims), ctypes.byref(io), _stream_handle(stream))
+    if st != MLA_OK:
+        raise MlaError(st, lib.mla_page_last_error().decode())
+    _debug_status(page_device_status, "mla_page_plan", stream)
+    return act_seqs, cache_index
+
+
+def page_device_status(clear: bool = True, stream=None) -> int:
+    lib = load_library()
+    flags = ctypes.c_uint32(0)
+    st = lib.mla_page_device_status(_stream_handle(stream), ctypes.byref(flags), 1 if clear else 0)
+    if st not in (MLA_OK, -7):
+        raise MlaError(st, lib.mla_page_last_error().decode())
+    return int(flags.value)
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def rope_params(theta: float = 10000.0, scaling: str = "none", factor: float = 1.0, orig_positions: float = 4096,
+                beta_fast: float = 32.0, beta_slow: float = 1.0, mscale: float = 1.0) -> RopeParams:
+    """The frequency scheme of the rotary calls (mla_rope_params); scaling is
+    one of "none", "linear", "ntk", "yarn"."""
+    return RopeParams(theta, factor, orig_positions, beta_fast, beta_slow, mscale, ROPE_SCALING[scaling])
+
+
+def mla_rope_table(positions, cos, sin, *, params: RopeParams, stream=None):
+    """Enqueue one call of the C entry point with the same name: cos and sin
+    (T, rot_dim / 2) fp32 for positions (T,) int32 (mla_prolog reads them for
+    rot_dim 64)."""
+    lib = load_library()
+    T, pairs = cos.shape
+    st = lib.mla_rope_table(ctypes.byref(params), T, 2 * pairs, _need(positions, torch.int32, (T,), "positions"),
+                            _need(cos, torch.float32, None, "cos"), _need(sin, torch.float32, (T, pairs), "sin"),
+                            _stream_handle(stream))
+    if st != MLA_OK:
+        raise MlaError(st, lib.mla_rope_last_error().decode())
+    _debug_status(rope_device_status, "mla_rope_table", stream)
+    return cos, sin
+
+
+def _rope_tensor(x, out, rows, T: int, rot_off: int, what: str) -> RopeTensor:
+    out = x if out is None else out
+    if x.dim() != 3 or out.dim() != 3 or x.shape[1:] != out.shape[1:] or x.shape[0] != T or x.dtype != out.dtype:
+        raise ValueError(f"{what} and its output must be (tokens, heads, head_dim) tensors of one type")
+    if (x.shape[2] > 1 and x.stride(2) != 1) or (out.shape[2] > 1 and out.stride(2) != 1):
+        raise ValueError(f"{what}: the values of a head must be adjacent")
+    if rows is None and out.shape[0] != T:
+        raise ValueError(f"{what}: the output has another number of tokens")
+    _on_current_device(x, what)
+    _on_current_device(out, what + "'s output")
+    return RopeTensor(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+                      None if rows is None else _need(rows, torch.int64, (T,), what + "'s rows"),
+                      out.shape[0], x.shape[1], x.shape[2], rot_off, 0)
+
+
+def mla_rope_apply(positions, q, k=None, *, params: RopeParams, rot_dim: int, rot_off: int = 0, k_rot_off: int = 0,
+                   half: bool = False, inverse: bool = False, out=None, k_out=None, k_rows=None, stream=None):
+    """Enqueue one call of the C entry point with the same name: rotate q (T,
+    H, D) and, where given, k (T, Hk, Dk), both bf16, fp16 or fp32, by the
+    angles of positions (T,) int32.
+
+    The rotated part is [rot_off, rot_off + rot_dim) of q's heads and
+    [k_rot_off, k_rot_off + rot_dim) of k's; half: pairs (i, i + rot_dim / 2)
+    instead of (2 i, 2 i + 1); inverse: the opposite angle (the gradient).
+    out / k_out None: in place.  k_rows (T,) int64 writes k's tokens to those
+    rows of k_out (rows, Hk, Dk), the index-key cache for instance; negative
+    rows are skipped."""
+    lib = load_library()
+    T = positions.numel()
+    if q.dtype not in _ROPE_DTYPES or (k is not None and k.dtype != q.dtype):
+        raise ValueError("q and k must both be bf16, fp16 or fp32")
+    if k_rows is not None and (k is None or k_out is None):
+        raise ValueError("k_rows needs k and k_out")
+    dims = RopeDims(T, rot_dim, 1 if half else 0, 1 if inverse else 0, _ROPE_DTYPES[q.dtype])
+    qt = _rope_tensor(q, out, None, T, rot_off, "q")
+    kt = None if k is None else _rope_tensor(k, k_out, k_rows, T, k_rot_off, "k")
+    st = lib.mla_rope_apply(ctypes.byref(dims), ctypes.byref(params),
+                            _need(positions, torch.int32, (T,), "positions"), ctypes.byref(qt),
+                            None if kt is None else ctypes.byref(kt), _stream_handle(stream))
+    if st != MLA_OK:
+        raise MlaError(st, lib.mla_rope_last_error().decode())
+    _debug_status(rope_device_status, "mla_rope_apply", stream)
+    return (q if out is None else out), (k if k_out is None else k_out)
+
+
+def rope_device_status(clear: bool = True, stream=None) -> int:
+    lib = load_library()
+    flags = ctypes.c_uint32(0)
+    st = lib.mla_rope_device_status(_stream_handle(stream), ctypes.byref(flags), 1 if clear else 0)
+    if st not in (MLA_OK, -7):
+        raise MlaError(st, lib.mla_rope_last_error().decode())
     return int(flags.value)

@@ -8,13 +8,15 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "mla_sparse_fwd.cu"), os.path.join(CSRC, "lightning_indexer.cu"),
-           os.path.join(CSRC, "cache_write.cu"), os.path.join(CSRC, "mla_prolog.cu")]
+           os.path.join(CSRC, "cache_write.cu"), os.path.join(CSRC, "mla_prolog.cu"),
+           os.path.join(CSRC, "page_plan.cu"), os.path.join(CSRC, "rope.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(ROOT, "include", "mla_sparse.h"),
                   os.path.join(ROOT, "include", "mla_indexer.h"), os.path.join(ROOT, "include", "mla_cache.h"),
-                  os.path.join(ROOT, "include", "mla_prolog.h")]
+                  os.path.join(ROOT, "include", "mla_prolog.h"), os.path.join(ROOT, "include", "mla_pages.h"),
+                  os.path.join(ROOT, "include", "mla_rope.h")]
 LIB_PATH = os.path.join(HERE, "libmla_sparse.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "--threads", "4"]
+              "-Xcompiler", "-fPIC", "-shared", "--threads", "8"]
 
 
 def nvcc() -> str:
