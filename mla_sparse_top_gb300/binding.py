@@ -1,5 +1,5 @@
 """ctypes binding of the C ABI in include/mla_sparse.h, mla_indexer.h,
-mla_cache.h, mla_prolog.h, mla_pages.h and mla_rope.h.
+mla_cache.h, mla_prolog.h, mla_pages.h, mla_rope.h and mla_tree.h.
 
 Argument marshalling only: shapes and dtypes are read off torch tensors, the
 device pointers and the current CUDA stream are passed through, and a
@@ -39,9 +39,10 @@ EXPORTED_SYMBOLS = ("mla_sparse_attn_fwd", "mla_swa_fwd", "mla_compressed_attn_f
                     "mla_cache_last_error", "mla_cache_device_status", "mla_prolog_workspace_bytes", "mla_prolog",
                     "mla_prolog_last_error", "mla_prolog_device_status")
 
-# mla_pages.h and mla_rope.h: the calls around a drafted decode step
+# mla_pages.h, mla_rope.h and mla_tree.h: the calls of a drafted decode step
 STEP_SYMBOLS = ("mla_page_plan", "mla_page_last_error", "mla_page_device_status", "mla_rope_table", "mla_rope_apply",
-                "mla_rope_last_error", "mla_rope_device_status")
+                "mla_rope_last_error", "mla_rope_device_status", "mla_tree_workspace_bytes", "mla_tree_attn_fwd",
+                "mla_tree_last_error", "mla_tree_device_status")
 
 
 class MlaDims(ctypes.Structure):
@@ -182,6 +183,8 @@ def load_library(path: str = LIB_PATH):
     lib.mla_rope_table.argtypes = [ctypes.POINTER(RopeParams), ctypes.c_int32, ctypes.c_int32] + [vp] * 4
     lib.mla_rope_apply.argtypes = [ctypes.POINTER(RopeDims), ctypes.POINTER(RopeParams), vp,
                                    ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), vp]
+    lib.mla_tree_attn_fwd.argtypes = [ctypes.POINTER(MlaDims)] + [vp] * 11 + [ctypes.c_float, vp, ctypes.c_size_t, vp]
+    lib.mla_tree_workspace_bytes.argtypes = [ctypes.POINTER(MlaDims)]
     for name in STEP_SYMBOLS:
         fn = getattr(lib, name)
         if name.endswith("_last_error"):
@@ -190,6 +193,7 @@ def load_library(path: str = LIB_PATH):
             fn.restype = ctypes.c_int
         if name.endswith("_device_status"):
             fn.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]
+    lib.mla_tree_workspace_bytes.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -653,4 +657,70 @@ def rope_device_status(clear: bool = True, stream=None) -> int:
     st = lib.mla_rope_device_status(_stream_handle(stream), ctypes.byref(flags), 1 if clear else 0)
     if st not in (MLA_OK, -7):
         raise MlaError(st, lib.mla_rope_last_error().decode())
+    return int(flags.value)
+
+
+# ------------------------------------------------------------------ dense attention of drafted tokens
+def tree_dims(q_nope, kv_nope, block_table, *, S1: int) -> MlaDims:
+    """MlaDims of mla_tree_attn_fwd read off the tensors (topk is unused)."""
+    T, n_q, d_nope = q_nope.shape
+    if T % S1:
+        raise ValueError("q_nope's leading dim must be B*S1")
+    return MlaDims(T // S1, S1, n_q, 1, d_nope, 64, 128, kv_nope.shape[0] // 128, block_table.shape[1], 0,
+                   MLA_KV_INT8 if kv_nope.dtype == torch.int8 else MLA_KV_BF16)
+
+
+def mla_tree_workspace_bytes(dims: MlaDims) -> int:
+    return int(load_library().mla_tree_workspace_bytes(ctypes.byref(dims)))
+
+
+def mla_tree_attn_fwd(q_nope, q_rope, kv_nope, kv_rope, kv_scales, block_table, act_seqs, out, lse, workspace, *,
+                      tree_lens=None, tree_mask=None, softmax_scale=None, S1: int = 1, stream=None,
+                      dims: MlaDims | None = None):
+    """Enqueue one call of the C entry point with the same name: attention of
+    each sequence's newest tokens over its whole cache.
+
+    q_nope (B*S1, n_q, 512) bf16, q_rope (B*S1, n_q, 64) bf16, kv_nope (rows,
+    512) bf16|int8, kv_rope (rows, 64) bf16, kv_scales (rows, 4) fp32 or None,
+    block_table (B, W) int32, act_seqs (B,) int32, out (B*S1, n_q, 512) bf16,
+    lse (B*S1, n_q) fp32 or None, workspace: at least
+    mla_tree_workspace_bytes(dims) bytes; tree_lens (B,) int32 drafted tokens
+    of each sequence (None: S1), tree_mask (B*S1 or B, S1, ceil(S1 / 64)) int64 which
+    drafted tokens each sees (None: a chain)."""
+    lib = load_library()
+    if dims is None:
+        dims = tree_dims(q_nope, kv_nope, block_table, S1=S1)
+    B, T, n_q = dims.B, dims.B * dims.S1, dims.n_q
+    bf16, i32, rows = torch.bfloat16, torch.int32, dims.num_blocks * 128
+    int8 = dims.kv_dtype == MLA_KV_INT8
+    if tree_mask is not None and tree_mask.numel() != T * ((dims.S1 + 63) // 64):
+        raise ValueError("tree_mask must hold ceil(S1 / 64) words for each of the B*S1 tokens")
+    if kv_nope.shape[0] < rows or kv_rope.shape[0] < rows:
+        raise ValueError("the cache holds fewer rows than dims.num_blocks says")
+    ptrs = (_need(q_nope, bf16, (T, n_q, 512), "q_nope"), _need(q_rope, bf16, (T, n_q, 64), "q_rope"),
+            _need(kv_nope, torch.int8 if int8 else bf16, None, "kv_nope"), _need(kv_rope, bf16, None, "kv_rope"),
+            _need(kv_scales, torch.float32, (kv_nope.shape[0], 4), "kv_scales") if int8 else None,
+            _need(block_table, i32, (B, dims.max_blocks_per_seq), "block_table"),
+            _need(act_seqs, i32, (B,), "act_seqs"),
+            None if tree_lens is None else _need(tree_lens, i32, (B,), "tree_lens"),
+            None if tree_mask is None else _need(tree_mask, torch.int64, None, "tree_mask"),
+            _need(out, bf16, (T, n_q, 512), "out"), None if lse is None else _need(lse, torch.float32, (T, n_q), "lse"))
+    if softmax_scale is None:
+        softmax_scale = (dims.d_nope + dims.d_rope) ** -0.5
+    nbytes = workspace.numel() * workspace.element_size()
+    _on_current_device(workspace, "workspace")
+    st = lib.mla_tree_attn_fwd(ctypes.byref(dims), *ptrs, softmax_scale, workspace.data_ptr(), nbytes,
+                               _stream_handle(stream))
+    if st != MLA_OK:
+        raise MlaError(st, lib.mla_tree_last_error().decode())
+    _debug_status(tree_device_status, "mla_tree_attn_fwd", stream)
+    return out, lse
+
+
+def tree_device_status(clear: bool = True, stream=None) -> int:
+    lib = load_library()
+    flags = ctypes.c_uint32(0)
+    st = lib.mla_tree_device_status(_stream_handle(stream), ctypes.byref(flags), 1 if clear else 0)
+    if st not in (MLA_OK, -7):
+        raise MlaError(st, lib.mla_tree_last_error().decode())
     return int(flags.value)

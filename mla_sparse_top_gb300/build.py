@@ -9,11 +9,12 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "mla_sparse_fwd.cu"), os.path.join(CSRC, "lightning_indexer.cu"),
            os.path.join(CSRC, "cache_write.cu"), os.path.join(CSRC, "mla_prolog.cu"),
-           os.path.join(CSRC, "page_plan.cu"), os.path.join(CSRC, "rope.cu")]
+           os.path.join(CSRC, "page_plan.cu"), os.path.join(CSRC, "rope.cu"),
+           os.path.join(CSRC, "tree_attn.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(ROOT, "include", "mla_sparse.h"),
                   os.path.join(ROOT, "include", "mla_indexer.h"), os.path.join(ROOT, "include", "mla_cache.h"),
                   os.path.join(ROOT, "include", "mla_prolog.h"), os.path.join(ROOT, "include", "mla_pages.h"),
-                  os.path.join(ROOT, "include", "mla_rope.h")]
+                  os.path.join(ROOT, "include", "mla_rope.h"), os.path.join(ROOT, "include", "mla_tree.h")]
 LIB_PATH = os.path.join(HERE, "libmla_sparse.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "--threads", "8"]

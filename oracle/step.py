@@ -91,3 +91,41 @@ def rope_apply(x, positions, freqs, *, rot_off, half, inverse=False, mscale=1.0)
         u, v = x[:, :, p], x[:, :, q]
         y[:, :, p], y[:, :, q] = u * c - v * s, u * s + v * c
     return y
+
+
+def tree_visible(act, n, s, mask_bits):
+    """Positions of one sequence that drafted token s (of n) sees; mask_bits: its tree_mask row as an integer, or None."""
+    act = max(0, int(act))
+    if s >= n:
+        return []
+    ctx = act - n
+    bits = (2 << s) - 1 if mask_bits is None else mask_bits
+    return [p for p in range(act) if p < ctx or bits >> (p - ctx) & 1]
+
+
+def tree_attention(q_nope, q_rope, latent, rope, block_table, act_seqs, tree_lens, masks, S1, scale):
+    """fp64: q_nope (T, H, 512), q_rope (T, H, 64), latent (rows, 512) and rope
+    (rows, 64) as fp64 values, masks: T integers or None.  Returns out, lse and
+    sum_p softmax_p |v_p| (what a rounding of the weights acts on)."""
+    T, H, D = q_nope.shape
+    out, mag = np.zeros((T, H, D)), np.zeros((T, H, D))
+    lse = np.full((T, H), -np.inf)
+    num_blocks = latent.shape[0] // BLOCK
+    for t in range(T):
+        b, s = divmod(t, S1)
+        n = S1 if tree_lens is None else min(S1, max(0, int(tree_lens[b])))
+        rows = []
+        for p in tree_visible(act_seqs[b], n, s, None if masks is None else masks[t]):
+            blk = int(block_table[b, p // BLOCK]) if p // BLOCK < block_table.shape[1] else -1
+            if 0 <= blk < num_blocks:
+                rows.append(blk * BLOCK + p % BLOCK)
+        if not rows:
+            continue
+        v = latent[rows]
+        z = scale * (q_nope[t] @ v.T + q_rope[t] @ rope[rows].T)
+        m = z.max(-1, keepdims=True)
+        e = np.exp(z - m)
+        l = e.sum(-1, keepdims=True)
+        out[t], mag[t] = e / l @ v, e / l @ np.abs(v)
+        lse[t] = (m + np.log(l))[:, 0]
+    return out, lse, mag

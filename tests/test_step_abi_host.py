@@ -26,8 +26,8 @@ def declared(*headers):
 
 def test_library_exports_what_the_headers_declare(lib):
     from mla_sparse_top_gb300 import binding
-    names = declared("mla_pages.h", "mla_rope.h")
-    assert names == {n for n in binding.STEP_SYMBOLS if n.startswith(("mla_page", "mla_rope"))}
+    names = declared("mla_pages.h", "mla_rope.h", "mla_tree.h")
+    assert names == set(binding.STEP_SYMBOLS)
     for n in names:
         assert hasattr(lib, n), n
 
@@ -132,3 +132,43 @@ def test_rope_apply_pointers_and_no_tokens(lib):
     assert rope_call(lib, positions=None) == -1
     assert rope_call(lib, positions=ptr(9) + 2) == -5
     assert rope_call(lib, dict(T=0), dict(x=None, out=None), positions=None) == 0
+
+
+def tree_call(lib, dims=None, **kw):
+    from mla_sparse_top_gb300.binding import MlaDims
+    d = dict(B=2, S1=3, n_q=128, n_kv=1, d_nope=512, d_rope=64, block_size=128, num_blocks=16, max_blocks_per_seq=8,
+             topk=0, kv_dtype=0)
+    d.update(dims or {})
+    names = ("q_nope", "q_rope", "kv_nope", "kv_rope", "kv_scales", "block_table", "act_seqs", "tree_lens",
+             "tree_mask", "out", "lse")
+    a = {n: ptr(i) for i, n in enumerate(names)}
+    a.update(scale=0.04, workspace=ptr(40), nbytes=1 << 40)
+    a.update(kw)
+    return lib.mla_tree_attn_fwd(ctypes.byref(MlaDims(**d)), *[a[n] for n in names], a["scale"], a["workspace"],
+                                 a["nbytes"], None)
+
+
+@pytest.mark.parametrize("dims,kw,expect", [
+    (dict(B=0), {}, -2), (dict(S1=0), {}, -2), (dict(n_q=0), {}, -2), (dict(n_q=129), {}, -2), (dict(n_kv=2), {}, -4),
+    (dict(d_nope=256), {}, -4), (dict(d_rope=32), {}, -4), (dict(block_size=64), {}, -4), (dict(num_blocks=0), {}, -2),
+    (dict(num_blocks=1 << 24), {}, -2), (dict(max_blocks_per_seq=0), {}, -2), (dict(kv_dtype=2), {}, -3),
+    (dict(kv_dtype=1), dict(kv_scales=None), -3), (dict(B=1 << 20, S1=1 << 10, n_q=2), {}, -2),
+    ({}, dict(q_nope=None), -1), ({}, dict(q_rope=None), -1), ({}, dict(kv_nope=None), -1), ({}, dict(kv_rope=None), -1),
+    ({}, dict(block_table=None), -1), ({}, dict(act_seqs=None), -1), ({}, dict(out=None), -1),
+    ({}, dict(workspace=None), -1), ({}, dict(nbytes=1), -2), ({}, dict(scale=float("nan")), -2),
+    ({}, dict(scale=float("inf")), -2), ({}, dict(q_nope=ptr(0) + 8), -5), ({}, dict(out=ptr(0) + 8), -5),
+    (dict(kv_dtype=1), dict(kv_scales=ptr(0) + 8), -5), ({}, dict(tree_mask=ptr(0) + 4), -5),
+    ({}, dict(tree_lens=ptr(0) + 2), -5), ({}, dict(workspace=ptr(40) + 128), -5), ({}, dict(lse=ptr(0) + 2), -5),
+])
+def test_tree_attention_refuses(lib, dims, kw, expect):
+    assert tree_call(lib, dims, **kw) == expect
+    assert lib.mla_tree_last_error()
+
+
+def test_tree_workspace_of_bad_dims_is_zero(lib):
+    from mla_sparse_top_gb300.binding import MlaDims
+    d = MlaDims(B=2, S1=3, n_q=129, n_kv=1, d_nope=512, d_rope=64, block_size=128, num_blocks=16, max_blocks_per_seq=8)
+    assert lib.mla_tree_workspace_bytes(ctypes.byref(d)) == 0 and lib.mla_tree_workspace_bytes(None) == 0
+    d.n_q = 128
+    assert lib.mla_tree_workspace_bytes(ctypes.byref(d)) > 0
+    assert lib.mla_tree_attn_fwd(None, *[None] * 11, 0.0, None, 0, None) == -1
