@@ -19,7 +19,8 @@
  *   r_p  = block_table[b, p / 128] * 128 + p % 128
  *
  * A token that sees nothing, and padding tokens s >= n_b, get out = 0 and
- * lse = -inf.  Rows at and beyond act_b are not read, nor are pages beyond it.
+ * lse = -inf.  What lies in rows at and beyond act_b does not matter, nor do
+ * table entries of pages beyond it.
  * A block id outside [0, num_blocks), or a position beyond the table, is
  * masked out and raises MLA_DEVICE_BAD_BLOCK.  Negative act_b and tree_lens
  * count as 0.
@@ -58,7 +59,8 @@ size_t mla_tree_workspace_bytes(const mla_dims* dims);
 
 /*
  * dims        as mla_sparse_attn_fwd (n_kv 1, d_nope 512, d_rope 64, block_size
- *             128, n_q <= 128; B * S1 * n_q < 2^31); topk is ignored
+ *             128, n_q <= 128); S1 <= 2^20, max_blocks_per_seq <= 2^23, B * S1 *
+ *             n_q < 2^31 - 256; topk is ignored
  * q_nope      bf16 [B*S1, n_q, 512], q_rope bf16 [B*S1, n_q, 64]
  * kv_nope     bf16 | int8 [num_blocks*128, 512], kv_rope bf16 [num_blocks*128, 64]
  * kv_scales   fp32 [num_blocks*128, 4] for MLA_KV_INT8, else NULL

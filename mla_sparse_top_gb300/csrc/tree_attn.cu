@@ -1,29 +1,113 @@
 // Dense MLA attention over the whole paged cache for GB300 (sm_103a): single
 // tokens, chains and trees of drafted tokens (formulas in mla_tree.h).
 //
-// First form: one warp per (token, head).  Lane l holds latent dims
-// [16 l, 16 l + 16) and rope dims 2 l, 2 l + 1 of the query and of the running
-// output; keys go one by one through an online softmax.  Bound by issue.
+// All query heads and all drafted tokens of a sequence share its keys, so the
+// rows of the problem are (token, head) pairs packed 128 to a block, and a
+// cluster of two CTAs takes one block through a range of 256-key tiles.  A
+// block's output, 128 x 512 in fp32, is half the tensor memory of two SMs;
+// the pair's MMAs (cta_group::2, M = 128, N = 256, the shape that runs at the
+// full rate of both SMs) leave rows 0-63 in CTA 0 and rows 64-127 in CTA 1,
+// each as 128 lanes: lane m holds row m for the first half of the columns and
+// lane 64 + m for the second.  No score crosses between the CTAs.
+//
+// Operands.  Q (64 rows x 576) stays in shared memory.  Keys and values stream
+// through a ring of seven 16 KB slots, each four MMAs long:
+//   key slot    64 dims of the CTA's 128 keys: CTA r takes page 2 t + r of tile t
+//   value slot  64 keys of the CTA's 128 output dims
+// The MMA reads a value from the CTA that owns its output column but a key
+// from the CTA that owns the key, so every latent value comes in twice (once
+// as a key half, once as a value half): 2176 bytes per key and pair, 62 bytes
+// per clock and SM at the full MMA rate, below the ~72 that an SM takes in.
+//
+// Warps of a CTA (512 threads):
+//   0-7   softmax: S (64 x 256 scores as 128 lanes x 128 columns) from tensor
+//         memory, mask, running maximum (lazily moved, shared by the four
+//         threads of a row) and sum, P in bf16 to shared memory, rescaling
+//         of O, the epilogue
+//   8-14  producers, one per ring slot: TMA, or loads, conversion and stores
+//         where a value has to be changed on the way (INT8 rows; the tiles at
+//         the end of a sequence, whose unwritten rows and masked drafts must
+//         not reach the second product as NaN or infinity: 0 * NaN)
+//   15    MMA issue (CTA 0) and the loads of Q (each CTA)
+// S is double buffered: S(t + 1) is computed while the softmax of tile t runs.
+//
+// Schedule.  Clusters form teams of g that take g row blocks of a sequence
+// through the same keys side by side, so a key is read from HBM once per team;
+// every team takes an equal share of the stream of tiles over all sequences.
+// A row block cut between teams leaves partial states in the workspace, and a
+// second launch merges them.  Which cluster takes what follows from the
+// lengths alone, so results do not depend on timing.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
 
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
 #include "../../include/mla_tree.h"
 #include "ptx.cuh"
+
+namespace mlasp {
+unsigned long long host_wait_limit_ns();
+}
 
 namespace mlatree {
 
 using namespace mlasp;
 
+constexpr int kThreads = 512;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kProducerWarp0 = 8;
+constexpr int kSlots = 7;  // ring slots, one producer warp each
+constexpr int kMmaWarp = 15;
+static_assert(kProducerWarp0 + kSlots == kMmaWarp && kMmaWarp * 32 + 32 == kThreads, "roles");
+
+constexpr int kRowBlock = 128;
+constexpr int kTile = 256;
+constexpr int kPage = 128;
+constexpr int kKeyItems = 9;  // 64-dim slices of 576
+constexpr int kSlotBytes = 16384;
+constexpr int kChunk = 8192;  // 64 rows of 128 bytes
+constexpr int kOffQ = 0;
+constexpr int kOffP = kOffQ + kKeyItems * kChunk;
+constexpr int kOffRing = kOffP + 4 * kChunk;
+constexpr int kOffExch = kOffRing + kSlots * kSlotBytes;  // float [2][4][64]
+constexpr int kOffScan = kOffExch + 2048;                 // int64 [kThreads / 32]
+constexpr int kOffWalk = kOffScan + 16 * 8;               // int64 first sequence, offset, tiles of the share, total
+constexpr int kOffBars = kOffWalk + 32;
+constexpr int kFull = 0;                // [kSlots], in CTA 0: both CTAs have filled the slot
+constexpr int kEmpty = kFull + kSlots;  // [kSlots] the MMAs that read the slot are complete
+constexpr int kSFull = kEmpty + kSlots;  // [2]
+constexpr int kSFree = kSFull + 2;       // [2], in CTA 0: the softmax warps have read S
+constexpr int kPReady = kSFree + 2;      // in CTA 0: P is written, O may be added to
+constexpr int kPvDone = kPReady + 1;
+constexpr int kQFull = kPvDone + 1;  // in CTA 0
+constexpr int kQFree = kQFull + 1;   // the segment's score MMAs are complete
+constexpr int kMax = kQFree + 1;     // [2] the four warps of rows 0-31 / 32-63 have posted
+constexpr int kFinal = kMax + 2;
+constexpr int kNumBars = kFinal + 1;
+constexpr int kOffTmem = kOffBars + 8 * kNumBars;
+constexpr int kOffAbort = kOffTmem + 4;
+constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // 1024: the base is aligned by hand
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kOffRing % 1024 == 0 && kOffP % 1024 == 0 && kOffBars % 8 == 0, "alignment");
+
+constexpr uint32_t kTmemO = 0;    // two blocks of 128 columns: output dims [0, 256) and [256, 512)
+constexpr uint32_t kTmemS = 256;  // two buffers of 128 columns
+constexpr int kPartFloats = 128 * 256 + 128;  // one CTA's partial state: O, then m[64], l[64]
+constexpr int kMaxClusters = 76;
+constexpr int kMinTiles = 2;  // a team's share is at least this long
+constexpr uint64_t kDrainNs = 500ull * 1000 * 1000;
+
 __device__ unsigned int g_tree_status = 0;
 
 struct Params {
-  const uint8_t* q_nope;
-  const uint8_t* q_rope;
   const uint8_t* kv_nope;
-  const uint8_t* kv_rope;
   const float* kv_scales;
   const int32_t* block_table;
   const int32_t* act_seqs;
@@ -31,102 +115,853 @@ struct Params {
   const uint64_t* tree_mask;
   uint16_t* out;
   float* lse;
-  int B, S1, n_q, W, num_blocks, int8;
+  float* parts;   // [clusters][2][2 CTAs][kPartFloats]
+  int4* records;  // [clusters] what the merge has to do for a row block that starts in this cluster
+  int B, S1, n_q, W, num_blocks;
+  int rows, blocks;  // rows of a sequence, its row blocks
+  int team, teams, passes;  // clusters of a team, teams, row-block groups of a sequence
   float scale_log2;
+  int out32;
+  unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ void unpack(uint4 v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// ------------------------------------------------------------------ schedule
+struct Seq {
+  int act, n;        // cached positions within the table, drafted tokens
+  int tiles, live;   // key tiles, passes that hold a drafted token
+  bool cut_table;    // positions beyond the table
+  __device__ int64_t len(const Params& p) const { return static_cast<int64_t>(live) * tiles + (p.passes - live); }
+};
+
+__device__ __forceinline__ Seq load_seq(const Params& p, int b) {
+  Seq s;
+  // far beyond the table a length says no more (W * 128 + S1 < 2^31)
+  s.act = min(max(0, __ldg(p.act_seqs + b)), p.W * kPage + p.S1);
+  s.n = p.tree_lens != nullptr ? min(p.S1, max(0, __ldg(p.tree_lens + b))) : p.S1;
+  const int in_table = min(s.act, p.W * kPage);
+  s.cut_table = in_table < s.act;
+  s.tiles = max(1, (in_table + kTile - 1) / kTile);
+  const int64_t group = static_cast<int64_t>(p.team) * kRowBlock;
+  s.live = static_cast<int>((static_cast<int64_t>(s.n) * p.n_q + group - 1) / group);
+  return s;
+}
+
+struct Segment {
+  int b, rb;          // sequence, row block
+  int t0, t1, tiles;  // tiles [t0, t1) of the row block's `tiles`
+  int act, n;         // 0 for a block of padding rows
+  int ctx;            // first drafted position, may be negative
+  int64_t first;      // stream position of the row block's first tile
+};
+
+// A team's share of the stream, walked row block by row block.
+struct Walk {
+  int b;
+  int64_t base;       // stream position of sequence b
+  int64_t off, left;  // position within sequence b, tiles left
+  int member;
+  __device__ bool next(const Params& p, Segment& s) {
+    while (left > 0) {
+      const Seq q = load_seq(p, b);
+      const int64_t len = q.len(p);
+      if (off >= len) {
+        ++b;
+        base += len;
+        off = 0;
+        continue;
+      }
+      const int64_t keys = static_cast<int64_t>(q.live) * q.tiles;
+      const bool live = off < keys;
+      const int pass = live ? static_cast<int>(off / q.tiles) : static_cast<int>(q.live + (off - keys));
+      s.b = b;
+      s.tiles = live ? q.tiles : 1;
+      s.t0 = live ? static_cast<int>(off - static_cast<int64_t>(pass) * q.tiles) : 0;
+      s.t1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.t0 + left));
+      s.first = base + off - s.t0;
+      s.act = live ? q.act : 0;
+      s.n = live ? q.n : 0;
+      s.ctx = s.act - s.n;
+      s.rb = pass * p.team + member;
+      off += s.t1 - s.t0;
+      left -= s.t1 - s.t0;
+      if (s.rb < p.blocks) return true;
+    }
+    return false;
+  }
+};
+
+struct Ctx {
+  uint32_t sb;
+  uint8_t* smem;
+  uint32_t tmem, rank;
+  uint64_t wait_ns;
+  volatile uint32_t* abort;
+  __device__ uint32_t bar(int i) const { return sb + kOffBars + 8 * i; }
+  __device__ uint32_t lead(int i) const { return mapa_shared(bar(i), 0); }  // the barrier in CTA 0
+};
+
+template <bool kCluster>
+__device__ __forceinline__ bool wait(const Ctx& c, int i, uint32_t parity) {
+  return mbar_wait<kCluster>(c.bar(i), parity, c.abort, c.wait_ns);
+}
+template <bool kCluster>
+__device__ __forceinline__ bool warp_wait(const Ctx& c, int i, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait<kCluster>(c, i, parity));
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;"
+               :: "r"(bar), "r"(bytes) : "memory");
+}
+// TMA load whose bytes count on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_pair(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void umma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs when the MMAs issued so far are complete.
+__device__ __forceinline__ void commit2(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ int page_id(const Params& p, int b, int lb) {
+  return lb < p.W ? __ldg(p.block_table + static_cast<int64_t>(b) * p.W + lb) : -1;
+}
+__device__ __forceinline__ bool good(const Params& p, int id) { return id >= 0 && id < p.num_blocks; }
+// Key groups of 64 that tile t of a segment has to go through.
+__device__ __forceinline__ int groups_of(const Segment& s, int t) {
+  return min(4, max(1, (s.act - kTile * t + 63) >> 6));
+}
+
+// Total of the stream and this team's start, found by the whole block.
+__device__ __forceinline__ int64_t block_sum_scan(const Ctx& c, int64_t v, int64_t& total) {
+  int64_t* part = reinterpret_cast<int64_t*>(c.smem + kOffScan);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __uint_as_float(w[k] << 16);
-    x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  return before + x - v;
+}
+
+__device__ __forceinline__ int teams_of(const Params& p, int64_t total) {
+  return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.teams), total / kMinTiles)));
+}
+
+// The walk of cluster `cid`; false when it has nothing to do.
+__device__ bool start_walk(const Params& p, const Ctx& c, int cid, Walk& w, int64_t& total, int& teams) {
+  int64_t* at = reinterpret_cast<int64_t*>(c.smem + kOffWalk);
+  const int tid = threadIdx.x;
+  const int chunks = (p.B + kThreads - 1) / kThreads;
+  int64_t mine = 0, len = 0, pre = 0;
+  for (int k = 0; k < chunks; ++k) {
+    const int b = k * kThreads + tid;
+    len = b < p.B ? load_seq(p, b).len(p) : 0;
+    mine += len;
+  }
+  pre = block_sum_scan(c, mine, total);
+  teams = teams_of(p, total);
+  const int team = cid / p.team;
+  const bool busy = team < teams;
+  const int64_t start = busy ? team * total / teams : 0, end = busy ? (team + 1) * total / teams : 0;
+  if (busy) {
+    int64_t carry = 0;
+    for (int k = 0; k < chunks; ++k) {
+      const int b = k * kThreads + tid;
+      int64_t sum = total;
+      if (chunks > 1) {
+        len = b < p.B ? load_seq(p, b).len(p) : 0;
+        pre = carry + block_sum_scan(c, len, sum);
+      }
+      if (b < p.B && start >= pre && start < pre + len) {
+        at[0] = b;
+        at[1] = pre;
+      }
+      carry += sum;
+      if (carry > start) break;
+    }
+  }
+  __syncthreads();
+  w.b = static_cast<int>(at[0]);
+  w.base = at[1];
+  w.off = start - at[1];
+  w.left = end - start;
+  w.member = cid - team * p.team;
+  return busy;
+}
+
+// ------------------------------------------------------------------ producers
+struct Maps {
+  CUtensorMap q_nope, q_rope, key, val, rope;
+};
+
+// Four codes of a word times the scale, rounded to bf16: bytes enter the
+// mantissa of 2^23 + 128 + code by a byte permutation (codes biased to
+// unsigned), which is exact and cheaper than four conversions.
+__device__ __forceinline__ void dequant4(uint32_t w, float sc, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const float bias = 8388736.f;  // 2^23 + 128
+  const float a = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)) - bias;
+  const float b = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)) - bias;
+  const float d = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)) - bias;
+  const float e = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)) - bias;
+  lo = pack_bf16x2(a * sc, b * sc);
+  hi = pack_bf16x2(d * sc, e * sc);
+}
+// NaN and infinities of a bf16 pair become zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  return w;
+}
+__device__ __forceinline__ uint4 finite8(uint4 v) {
+  return make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+}
+
+// Value item of a bf16 cache at the end of a sequence: 64 keys x 128 dims.
+// Rows at and beyond `rows` (unwritten, or of a bad page) are zero.
+__device__ void fill_value_bf16(const Params& p, uint32_t slot, int64_t row0, int rows, int dim0, int lane) {
+  const int unit = lane & 15, box = unit >> 3;
+#pragma unroll 8
+  for (int it = 0; it < 32; ++it) {
+    const int r = 2 * it + (lane >> 4);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < rows) v = finite8(__ldg(reinterpret_cast<const uint4*>(p.kv_nope + (row0 + r) * 1024 + dim0 * 2) + unit));
+    sts16(slot + box * kChunk + r * 128 + (((unit & 7) ^ (r & 7)) << 4), v);
   }
 }
 
-__global__ void __launch_bounds__(256) tree_simple_kernel(const Params p) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= static_cast<int64_t>(p.B) * p.S1 * p.n_q) return;
-  const int t = static_cast<int>(row / p.n_q), b = t / p.S1, s = t - b * p.S1;
-  float q[16], o[16], qr[2];
-  const uint4* qp = reinterpret_cast<const uint4*>(p.q_nope + row * 1024) + 2 * lane;
-  unpack(__ldg(qp), q);
-  unpack(__ldg(qp + 1), q + 8);
-  const uint32_t qw = __ldg(reinterpret_cast<const uint32_t*>(p.q_rope + row * 128) + lane);
-  qr[0] = __uint_as_float(qw << 16);
-  qr[1] = __uint_as_float(qw & 0xFFFF0000u);
+// INT8: 16 codes of a row become two 16-byte units.
+__device__ __forceinline__ void convert16(uint4 c, float sc, bool clean, uint4& a, uint4& b) {
+  dequant4(c.x, sc, a.x, a.y);
+  dequant4(c.y, sc, a.z, a.w);
+  dequant4(c.z, sc, b.x, b.y);
+  dequant4(c.w, sc, b.z, b.w);
+  if (clean) {
+    a = finite8(a);
+    b = finite8(b);
+  }
+}
+
+// One item of an INT8 cache: `kRows` rows of kUnits 16-code units each, loaded
+// before the slot is free, then converted into it.
+template <int kRows, int kUnits>
+struct Int8Item {
+  static constexpr int kIts = kRows * kUnits / 32, kStep = 32 / kUnits;
+  uint4 c[kIts];
+  float sc[kIts];
+  __device__ void load(const Params& p, int64_t row0, int rows, int dim0, int lane) {
+    const int unit = lane % kUnits;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
-  const int64_t act = max(0, __ldg(p.act_seqs + b));
-  const int n = p.tree_lens != nullptr ? min(p.S1, max(0, __ldg(p.tree_lens + b))) : p.S1;
-  const int64_t ctx = act - n;
-  const int words = (p.S1 + 63) / 64;
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  for (int64_t pos = 0; pos < act && s < n; ++pos) {
-    const int64_t j = pos - ctx;
-    if (j >= 0) {
-      const bool see = p.tree_mask != nullptr
-                           ? (__ldg(p.tree_mask + static_cast<int64_t>(t) * words + (j >> 6)) >> (j & 63)) & 1
-                           : j <= s;
-      if (!see) continue;
-    }
-    const int64_t lb = pos >> 7;
-    const int id = lb < p.W ? __ldg(p.block_table + static_cast<int64_t>(b) * p.W + lb) : -1;
-    if (id < 0 || id >= p.num_blocks) {
-      bad = true;
-      continue;
-    }
-    const int64_t r = static_cast<int64_t>(id) * 128 + (pos & 127);
-    float k[16];
-    if (p.int8) {
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(p.kv_nope + r * 512) + lane);
-      const float sc = __ldg(p.kv_scales + r * 4 + (lane >> 3));
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const int lo = static_cast<int8_t>(w[e >> 2] >> (8 * (e & 3)));
-        const int hi = static_cast<int8_t>(w[e >> 2] >> (8 * ((e & 3) + 1)));
-        const uint32_t pr = pack_bf16x2(static_cast<float>(lo) * sc, static_cast<float>(hi) * sc);
-        k[e] = __uint_as_float(pr << 16);
-        k[e + 1] = __uint_as_float(pr & 0xFFFF0000u);
+    for (int it = 0; it < kIts; ++it) {
+      const int r = it * kStep + lane / kUnits;
+      c[it] = make_uint4(0, 0, 0, 0);
+      sc[it] = 0.f;
+      if (r < rows) {
+        c[it] = __ldg(reinterpret_cast<const uint4*>(p.kv_nope + (row0 + r) * 512 + dim0) + unit);
+        sc[it] = __ldg(p.kv_scales + (row0 + r) * 4 + (dim0 >> 7));
       }
+    }
+  }
+  __device__ void store(uint32_t slot, bool clean, int lane) const {
+    const int unit = lane % kUnits, box = unit >> 2, u0 = 2 * (unit & 3);
+#pragma unroll
+    for (int it = 0; it < kIts; ++it) {
+      const int r = it * kStep + lane / kUnits;
+      uint4 a, b;
+      convert16(c[it], sc[it], clean, a, b);
+      const uint32_t base = slot + box * (kRows * 128) + r * 128;
+      sts16(base + ((u0 ^ (r & 7)) << 4), a);
+      sts16(base + (((u0 + 1) ^ (r & 7)) << 4), b);
+    }
+  }
+};
+
+// Producer warp w fills ring slot w: items w, w + 7, w + 14, ... of the order
+// in which the MMAs take them (keys of tile t + 1 before values of tile t).
+template <bool kInt8>
+__device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int w, int lane) {
+  const uint32_t slot = c.sb + kOffRing + w * kSlotBytes;
+  const uint32_t full = c.lead(kFull + w);
+  int skip = w;  // items until this warp's next one
+  uint32_t fills = 0;
+  auto take = [&](int items, int& k) {  // first item of a group that is this warp's
+    k = skip;
+    if (skip >= items) {
+      skip -= items;
+      return false;
+    }
+    return true;
+  };
+  auto done = [&](int k, int items) { skip = k - items; };  // k: the first item at or beyond `items`
+  auto free_slot = [&]() { return warp_wait<false>(c, kEmpty + w, (fills++ & 1) ^ 1); };
+  auto filled = [&]() {
+    fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
+    __syncwarp();
+    if (lane == 0) arrive_cluster(full);
+  };
+  Segment s;
+  while (walk.next(p, s)) {
+    for (int u = s.t0; u <= s.t1; ++u) {
+      int k;
+      if (u < s.t1 && take(kKeyItems, k)) {
+        const int lb = 2 * u + static_cast<int>(c.rank);
+        const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
+        const bool ok = good(p, id);
+        const int row = (ok ? id : p.num_blocks) * kPage;  // beyond the cache: TMA fills zeros
+        for (; k < kKeyItems; k += kSlots) {
+          if (kInt8 && k < 8) {
+            Int8Item<128, 4> item;
+            item.load(p, static_cast<int64_t>(row), ok ? min(kPage, s.act - lb * kPage) : 0, 64 * k, lane);
+            if (!free_slot()) return;
+            item.store(slot, false, lane);
+            filled();
+          } else {
+            if (!free_slot()) return;
+            if (lane == 0) {
+              arrive_cluster_tx(full, kSlotBytes);
+              if (k < 8) tma_pair(slot, &maps.key, 64 * k, row, full);
+              else tma_pair(slot, &maps.rope, 0, row, full);
+            }
+            __syncwarp();
+          }
+        }
+        done(k, kKeyItems);
+      }
+      if (u > s.t0) {
+        const int t = u - 1, items = 2 * groups_of(s, t);
+        if (!take(items, k)) continue;
+        const bool edge = kTile * (t + 1) > s.ctx;  // holds drafted or unwritten rows
+        for (; k < items; k += kSlots) {
+          const int g = k >> 1, dim0 = (k & 1) * 256 + static_cast<int>(c.rank) * 128;
+          const int lb = 2 * t + (g >> 1);
+          const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
+          const bool ok = good(p, id);
+          const int row = (ok ? id : p.num_blocks) * kPage + (g & 1) * 64;
+          const int rows = ok ? min(64, s.act - lb * kPage - (g & 1) * 64) : 0;
+          if (kInt8) {
+            Int8Item<64, 8> item;
+            item.load(p, row, rows, dim0, lane);
+            if (!free_slot()) return;
+            item.store(slot, edge, lane);
+            filled();
+          } else if (edge) {
+            if (!free_slot()) return;
+            fill_value_bf16(p, slot, row, rows, dim0, lane);
+            filled();
+          } else {
+            if (!free_slot()) return;
+            if (lane == 0) {
+              arrive_cluster_tx(full, kSlotBytes);
+              tma_pair(slot, &maps.val, dim0, row, full);
+              tma_pair(slot + kChunk, &maps.val, dim0 + 64, row, full);
+            }
+            __syncwarp();
+          }
+        }
+        done(k, items);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ MMA issue and Q
+__device__ __forceinline__ void load_q(const Params& p, const Ctx& c, const Maps& maps, const Segment& s) {
+  const uint32_t full = c.lead(kQFull);
+  const int row = s.b * p.rows + s.rb * kRowBlock + static_cast<int>(c.rank) * 64;
+  arrive_cluster_tx(full, kKeyItems * kChunk);
+  for (int k = 0; k < 8; ++k) tma_pair(c.sb + kOffQ + k * kChunk, &maps.q_nope, 64 * k, row, full);
+  tma_pair(c.sb + kOffQ + 8 * kChunk, &maps.q_rope, 0, row, full);
+}
+
+// One thread of each CTA; the one of CTA 0 issues the pair's MMAs.
+__device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk) {
+  constexpr uint32_t idesc_s = make_idesc_f16(128, 256, 1, 0, 0);  // A, B K-major
+  constexpr uint32_t idesc_v = make_idesc_f16(128, 256, 1, 0, 1);  // B MN-major
+  const bool lead = c.rank == 0;
+  Segment s, nx;
+  bool more = walk.next(p, s), ok = true;
+  if (more) load_q(p, c, maps, s);
+  int slot = 0, segs = 0, tile = 0;  // ring position, segments begun, tiles begun
+  uint32_t phase = 0;
+  // waits for the ring's next slot and issues its four MMAs
+  auto take_slot = [&](uint32_t d, uint32_t a, uint32_t b_step, uint32_t b_lbo, uint32_t idesc, bool first) {
+    if (!wait<true>(c, kFull + slot, phase)) return false;
+    tc_fence_after();
+    const uint32_t b = c.sb + kOffRing + slot * kSlotBytes;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+      umma2(d, make_sdesc(a + ks * 32, 16, 1024, kSwizzle128B), make_sdesc(b + ks * b_step, b_lbo, 1024, kSwizzle128B),
+            idesc, (first && ks == 0) ? 0u : 1u);
+    commit2(c.bar(kEmpty + slot));
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+    return true;
+  };
+  auto scores = [&](int t) {  // t: tiles begun before this one
+    if (!wait<true>(c, kSFree + (t & 1), ((t >> 1) & 1) ^ 1)) return false;
+    tc_fence_after();
+    for (int k = 0; k < kKeyItems; ++k)
+      if (!take_slot(c.tmem + kTmemS + 128 * (t & 1), c.sb + kOffQ + k * kChunk, 32, 16, idesc_s, k == 0)) return false;
+    commit2(c.bar(kSFull + (t & 1)));
+    return true;
+  };
+  auto values = [&](int t, int groups, bool first) {
+    if (!wait<true>(c, kPReady, t & 1)) return false;
+    tc_fence_after();
+    for (int k = 0; k < 2 * groups; ++k)
+      if (!take_slot(c.tmem + kTmemO + 128 * (k & 1), c.sb + kOffP + (k >> 1) * kChunk, 2048, kChunk, idesc_v,
+                     first && k < 2))
+        return false;
+    commit2(c.bar(kPvDone));
+    return true;
+  };
+  while (more && ok) {
+    const int n = s.t1 - s.t0;
+    if (lead) {
+      ok = wait<true>(c, kQFull, segs & 1);
+      for (int u = 0; u < n && ok; ++u) {
+        ok = scores(tile + u);
+        if (ok && u == n - 1) commit2(c.bar(kQFree));
+        if (ok && u > 0) ok = values(tile + u - 1, groups_of(s, s.t0 + u - 1), u == 1);
+      }
+      if (!ok) break;
+    }
+    // the next row block's Q as soon as this one's score MMAs are complete
+    const bool again = walk.next(p, nx);
+    if (again) {
+      ok = wait<false>(c, kQFree, segs & 1);
+      if (!ok) break;
+      load_q(p, c, maps, nx);
+    }
+    if (lead) ok = values(tile + n - 1, groups_of(s, s.t1 - 1), n == 1);
+    tile += n;
+    ++segs;
+    s = nx;
+    more = again;
+  }
+  if (lead) {  // every MMA in flight lands before the CTAs leave
+    commit2(c.bar(kFinal));
+    volatile uint32_t never = 0;
+    mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > kDrainNs ? c.wait_ns : kDrainNs);
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+// 64 bits of a mask row from bit `at` on (bits outside the row are 0).
+__device__ __forceinline__ uint64_t mask_window(const uint64_t* row, int words, int64_t at) {
+  const int64_t w = at >> 6;
+  const int sh = static_cast<int>(at & 63);
+  const uint64_t lo = w >= 0 && w < words ? __ldg(row + w) : 0ull;
+  if (sh == 0) return lo;
+  const uint64_t hi = w + 1 >= 0 && w + 1 < words ? __ldg(row + w + 1) : 0ull;
+  return (lo >> sh) | (hi << (64 - sh));
+}
+__device__ __forceinline__ uint64_t low_bits(int64_t n) {
+  return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1);
+}
+// 32-byte global store.
+__device__ __forceinline__ void stg32(void* ptr, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(ptr), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+__device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, int teams, int64_t total, int warp,
+                             int lane) {
+  const int q = warp & 3, sub = warp >> 2;  // TMEM lane quadrant, column half
+  const int L = q * 32 + lane, row = L & 63, half = L >> 6;
+  const int part = half * 2 + sub;  // which 64 keys of a tile this thread has
+  const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+  const uint32_t tO = c.tmem + lanes + kTmemO + 128 * sub;
+  float* exch = reinterpret_cast<float*>(c.smem + kOffExch);
+  const int words = (p.S1 + 63) >> 6;
+  const int maxbar = kMax + (q & 1);
+  uint32_t uses = 0;  // of the exchange
+  int tile = 0;       // tiles begun
+  bool bad = false;
+  // posts v and returns the four values of the row
+  auto share = [&](float v, float (&all)[4]) {
+    float* e = exch + (uses & 1) * 256;
+    e[part * 64 + row] = v;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar(maxbar));
+    if (!warp_wait<false>(c, maxbar, uses & 1)) return false;
+    ++uses;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) all[k] = e[k * 64 + row];
+    return true;
+  };
+  Segment s;
+  while (walk.next(p, s)) {
+    const int r = s.rb * kRowBlock + static_cast<int>(c.rank) * 64 + row;  // row of the sequence
+    const int tok = min(r / p.n_q, p.S1 - 1);
+    const bool live = r < p.rows && r / p.n_q < s.n;
+    const uint64_t* mrow =
+        p.tree_mask != nullptr ? p.tree_mask + (static_cast<int64_t>(s.b) * p.S1 + tok) * words : nullptr;
+    float m = -INFINITY, l = 0.f;
+    for (int t = s.t0; t < s.t1; ++t, ++tile) {
+      const int buf = tile & 1;
+      const int lb = 2 * t + half;
+      const bool used = lb * kPage < s.act;
+      const bool page = used && good(p, page_id(p, s.b, lb));
+      bad = bad || (used && !page);
+      uint64_t vis = page ? ~0ull : 0ull;
+      if (kTile * (t + 1) > s.ctx) {
+        const int64_t at = static_cast<int64_t>(kTile) * t + 64 * part - s.ctx;  // draft index of the first key
+        uint64_t drafted = mrow != nullptr ? mask_window(mrow, words, at) : low_bits(tok + 1 - at);
+        drafted &= low_bits(s.n - at) & ~low_bits(-at);
+        vis &= live ? (low_bits(-at) | drafted) : 0ull;
+      }
+      if (!warp_wait<false>(c, kSFull + buf, (tile >> 1) & 1)) return;
+      tc_fence_after();
+      float z[64];
+      {
+        uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(z);
+        uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(z + 32);
+        const uint32_t at = c.tmem + lanes + kTmemS + 128 * buf + 64 * sub;
+        tmem_ld_32x32b_x32(at, lo);
+        tmem_ld_32x32b_x32(at + 32, hi);
+        tmem_wait_ld();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(c.lead(kSFree + buf));
+#pragma unroll
+      for (int k = 0; k < 64; ++k) z[k] *= p.scale_log2;
+      if (__any_sync(0xffffffffu, vis != ~0ull)) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (!((vis >> k) & 1)) z[k] = -INFINITY;
+      }
+      float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+      for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], z[k]);
+      float all[4];
+      if (!share(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), all)) return;
+      const float top = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+      // the maximum moves only when a tile exceeds it by more than 2^8: P stays
+      // below 2^8 and O is rarely rescaled
+      const bool grow = top > m + 8.f;
+      const float f = grow ? fast_exp2(m - top) : 1.f;
+      if (grow) {
+        l *= f;
+        m = top;
+      }
+      const float mm = m == -INFINITY ? 0.f : m;
+      uint32_t w[32];
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float a = fast_exp2(z[2 * k] - mm), b = fast_exp2(z[2 * k + 1] - mm);
+        sum[k & 1] += a + b;
+        w[k] = pack_bf16x2(a, b);
+      }
+      l += sum[0] + sum[1];
+      // P and O are free once the tile before has been multiplied
+      if (tile > 0 && !warp_wait<false>(c, kPvDone, (tile - 1) & 1)) return;
+      if (t > s.t0 && __any_sync(0xffffffffu, grow)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tO + 32 * ch, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          tmem_st_32x32b_x32(tO + 32 * ch, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      const uint32_t pr = c.sb + kOffP + part * kChunk + row * 128;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        sts16(pr + ((u ^ (row & 7)) << 4), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(c.lead(kPReady));
+    }
+    float all[4];
+    if (!share(l, all)) return;
+    l = (all[0] + all[1]) + (all[2] + all[3]);
+    if (!live) {
+      l = 0.f;
+      m = -INFINITY;
+    }
+    if (!warp_wait<false>(c, kPvDone, (tile - 1) & 1)) return;
+    tc_fence_after();
+    const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+    const int64_t grow = static_cast<int64_t>(s.b) * p.rows + r;
+    if (whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t* o = p.out + grow * 512 + sub * 256 + half * 128;
+#pragma unroll 1
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tO + 32 * ch, v);
+        tmem_wait_ld();
+        if (r < p.rows) {
+          uint4 y[4];
+          uint32_t* yw = reinterpret_cast<uint32_t*>(y);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            yw[k] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+          if (p.out32) {
+            stg32(o + 32 * ch, y[0], y[1]);
+            stg32(o + 32 * ch + 16, y[2], y[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(o + 32 * ch)[k] = y[k];
+          }
+        }
+      }
+      if (part == 0 && r < p.rows && p.lse != nullptr)
+        p.lse[grow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     } else {
-      const uint4* kp = reinterpret_cast<const uint4*>(p.kv_nope + r * 1024) + 2 * lane;
-      unpack(__ldg(kp), k);
-      unpack(__ldg(kp + 1), k + 8);
+      // partial state: slot 0 of the cluster when the row block began before this share, else slot 1
+      const int at = s.t0 > 0 ? 0 : 1;
+      float* dst = p.parts + (static_cast<int64_t>(cid * 2 + at) * 2 + c.rank) * kPartFloats;
+#pragma unroll 1
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tO + 32 * ch, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          reinterpret_cast<uint4*>(dst)[(sub * 32 + ch * 8 + k) * 128 + L] =
+              make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      }
+      if (part == 0) {
+        dst[128 * 256 + row] = m;
+        dst[128 * 256 + 64 + row] = l;
+      }
+      if (at == 1 && warp == 0 && lane == 0 && c.rank == 0) {
+        // the teams that hold the rest: up to the one whose share has the last tile
+        const int64_t last = s.first + s.tiles - 1;
+        const int end = static_cast<int>(((last + 1) * teams + total - 1) / total - 1);
+        p.records[cid] = make_int4(s.b * p.rows + s.rb * kRowBlock, min(kRowBlock, p.rows - s.rb * kRowBlock),
+                                   end - cid / p.team, 0);
+      }
     }
-    const uint32_t kw = __ldg(reinterpret_cast<const uint32_t*>(p.kv_rope + r * 128) + lane);
-    float z = qr[0] * __uint_as_float(kw << 16) + qr[1] * __uint_as_float(kw & 0xFFFF0000u);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) z = fmaf(q[e], k[e], z);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-    z *= p.scale_log2;
-    if (!(z <= m)) {  // also for NaN
-      const float f = m == -INFINITY ? 0.f : exp2f(m - z);
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] *= f;
-      m = z;
+    tc_fence_before();  // the reads of O come before the next row block's MMAs (through kPReady)
+  }
+  if (bad) atomicOr(&g_tree_status, MLA_DEVICE_BAD_BLOCK);
+}
+
+template <bool kInt8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tree_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Ctx c;
+  c.sb = (smem_u32(raw) + 1023u) & ~1023u;  // swizzled operands need 1024-byte alignment
+  c.smem = raw + (c.sb - smem_u32(raw));
+  c.rank = cluster_ctarank();
+  c.wait_ns = p.wait_ns;
+  c.abort = reinterpret_cast<volatile uint32_t*>(c.smem + kOffAbort);
+  const int cid = blockIdx.x >> 1;
+  if (tid == 0) {
+    *c.abort = 0u;
+    if (c.rank == 0) p.records[cid] = make_int4(0, 0, 0, 0);  // nothing to merge, until this thread finds a cut
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(c.bar(kFull + i), 2);
+      mbar_init(c.bar(kEmpty + i), 1);
     }
-    const float w = m == -INFINITY ? 0.f : exp2f(z - m);
-    l += w;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = fmaf(w, k[e], o[e]);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(c.bar(kSFull + i), 1);
+      mbar_init(c.bar(kSFree + i), 2 * kSoftmaxWarps);
+      mbar_init(c.bar(kMax + i), 4);
+    }
+    mbar_init(c.bar(kPReady), 2 * kSoftmaxWarps);
+    mbar_init(c.bar(kPvDone), 1);
+    mbar_init(c.bar(kQFull), 2);
+    mbar_init(c.bar(kQFree), 1);
+    mbar_init(c.bar(kFinal), 1);
+    fence_mbarrier_init_cluster();
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t y[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  uint4* op = reinterpret_cast<uint4*>(p.out + row * 512) + 2 * lane;
-  op[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  op[1] = make_uint4(y[4], y[5], y[6], y[7]);
-  if (lane == 0) {
-    if (p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-    if (bad) atomicOr(&g_tree_status, MLA_DEVICE_BAD_BLOCK);
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
+                 :: "r"(c.sb + kOffTmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  Walk walk;
+  int64_t total;
+  int teams;
+  const bool busy = start_walk(p, c, cid, walk, total, teams);
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  c.tmem = *reinterpret_cast<volatile uint32_t*>(c.smem + kOffTmem);
+
+  if (busy) {
+    if (warp < kSoftmaxWarps) {
+      softmax_role(p, c, walk, cid, teams, total, warp, lane);
+    } else if (warp < kMmaWarp) {
+      producer_role<kInt8>(p, c, maps, walk, warp - kProducerWarp0, lane);
+    } else {
+      if (lane == 0) mma_role(p, c, maps, walk);
+      __syncwarp();
+    }
+  }
+  if (tid == 0) {  // positions beyond the table, found by the cluster that owns the sequence's number
+    bool beyond = false;
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+      const Seq q = load_seq(p, b);
+      beyond = beyond || (q.cut_table && q.n > 0);
+    }
+    if (beyond) atomicOr(&g_tree_status, MLA_DEVICE_BAD_BLOCK);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*c.abort) {
+    // a wait ran out: loads of this CTA may still be in flight to its shared
+    // memory; they take microseconds
+    if (tid == 0) atomicOr(&g_tree_status, MLA_DEVICE_TIMEOUT);
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000) {
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(c.tmem) : "memory");
+  cluster_arrive();
+  cluster_wait();
+}
+
+// ------------------------------------------------------------------ merge
+// Joins the parts of a row block that was cut between teams: block x looks at
+// the record of cluster x (the one the row block starts in), block y takes 1 of
+// the 2 CTAs' 64 float4 units.  Thread L is lane L of the units.
+__global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ Params p) {
+  const int4 rec = p.records[blockIdx.x];
+  const int L = threadIdx.x, row = L & 63, half = L >> 6;
+  const int rank = blockIdx.y >> 6, unit = blockIdx.y & 63;
+  const int r = rank * 64 + row;
+  if (r >= rec.y) return;  // no record: 0 rows
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 <= rec.z; k0 += 8) {
+    float mk[8], lk[8];
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = k0 + k <= rec.z;
+      const int cl = blockIdx.x + (in ? k0 + k : 0) * p.team;
+      const float* src = p.parts + (static_cast<int64_t>(cl * 2 + (k0 + k == 0 || !in ? 1 : 0)) * 2 + rank) * kPartFloats;
+      mk[k] = in ? __ldcg(src + 128 * 256 + row) : -INFINITY;
+      lk[k] = in ? __ldcg(src + 128 * 256 + 64 + row) : 0.f;
+      v[k] = __ldcg(reinterpret_cast<const float4*>(src) + unit * 128 + L);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (mk[k] == -INFINITY && lk[k] == 0.f) continue;  // a part in which the row sees nothing
+      if (mk[k] > m) {
+        const float f = m == -INFINITY ? 0.f : exp2f(m - mk[k]);
+        l *= f;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+        m = mk[k];
+      }
+      const float w = exp2f(mk[k] - m);
+      l = fmaf(w, lk[k], l);
+      o.x = fmaf(w, v[k].x, o.x);
+      o.y = fmaf(w, v[k].y, o.y);
+      o.z = fmaf(w, v[k].z, o.z);
+      o.w = fmaf(w, v[k].w, o.w);
+    }
+  }
+  const float inv = 1.f / l;
+  const int64_t g = rec.x + r;
+  uint2 y = make_uint2(0u, 0u);
+  if (l != 0.f) y = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  *reinterpret_cast<uint2*>(p.out + g * 512 + (unit >> 5) * 256 + half * 128 + (unit & 31) * 4) = y;
+  if (unit == 0 && half == 0 && p.lse != nullptr)
+    p.lse[g] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+// ------------------------------------------------------------------ host side
+constexpr int kMaxDevices = 64;
+struct Device {
+  bool ready = false;
+  int clusters[2] = {0, 0};
+};
+Device g_dev[kMaxDevices];
+std::mutex g_lock;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+// Clusters of a team: as many of a sequence's row blocks side by side as keep
+// the most clusters busy (whole teams, whole passes); one row block at a time
+// would read every key once per row block, which costs about 1.4 x where the
+// cache is larger than L2.
+inline int team_size(int blocks, int clusters) {
+  int best = 1;
+  double least = 1e30;
+  for (int g = 1; g <= std::min(blocks, clusters); ++g) {
+    const double passes = (blocks + g - 1) / g;
+    const double idle = passes * g / blocks * clusters / (clusters / g * g);
+    const double cost = idle * (g == 1 && blocks > 1 ? 1.4 : 1.0);
+    if (cost <= least + 1e-9) {
+      least = cost;
+      best = g;
+    }
+  }
+  return best;
+}
+
+struct Plan {
+  int rows, blocks, team, teams, passes, clusters;
+  size_t records_at, bytes;
+};
+inline Plan plan_of(const mla_dims& d, int clusters) {
+  Plan s;
+  s.rows = d.S1 * d.n_q;
+  s.blocks = static_cast<int>((static_cast<int64_t>(s.rows) + kRowBlock - 1) / kRowBlock);
+  s.team = team_size(s.blocks, clusters);
+  s.passes = (s.blocks + s.team - 1) / s.team;
+  // no more teams than shares of kMinTiles in the longest possible stream
+  const int64_t tiles = (static_cast<int64_t>(d.max_blocks_per_seq) + 1) / 2;
+  auto most = [&](int64_t passes) { return std::max<int64_t>(1, d.B * passes * tiles / kMinTiles); };
+  s.teams = static_cast<int>(std::min<int64_t>(clusters / s.team, most(s.passes)));
+  s.clusters = s.team * s.teams;
+  // the workspace has room for the schedule of any device
+  const int64_t room = std::min<int64_t>(kMaxClusters, most(s.blocks) * s.blocks);
+  s.records_at = static_cast<size_t>(room) * 4 * kPartFloats * sizeof(float);
+  s.bytes = s.records_at + static_cast<size_t>(room) * sizeof(int4);
+  return s;
 }
 
 }  // namespace mlatree
@@ -157,8 +992,70 @@ mla_status check_dims(const mla_dims& d) {
     return tree_fail(MLA_ERR_UNSUPPORTED, "d_nope=%d d_rope=%d block_size=%d: only 512/64/128 are implemented",
                      d.d_nope, d.d_rope, d.block_size);
   if (d.num_blocks >= (1 << 24)) return tree_fail(MLA_ERR_SHAPE, "num_blocks=%d must be < 2^24", d.num_blocks);
-  if (static_cast<int64_t>(d.B) * d.S1 >= (1ll << 31) || static_cast<int64_t>(d.B) * d.S1 * d.n_q >= (1ll << 31))
-    return tree_fail(MLA_ERR_SHAPE, "B * S1 * n_q must be < 2^31");
+  if (d.S1 > (1 << 20) || d.max_blocks_per_seq > (1 << 23))
+    return tree_fail(MLA_ERR_SHAPE, "S1=%d above 2^20 or max_blocks_per_seq=%d above 2^23", d.S1, d.max_blocks_per_seq);
+  if (static_cast<int64_t>(d.B) * d.S1 * d.n_q >= (1ll << 31) - 256)
+    return tree_fail(MLA_ERR_SHAPE, "B * S1 * n_q must be below 2^31 - 256");
+  return MLA_OK;
+}
+
+#define TREE_CUDA(call, what)                                                                     \
+  do {                                                                                            \
+    const cudaError_t err_ = (call);                                                              \
+    if (err_ != cudaSuccess) return tree_fail(MLA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err_)); \
+  } while (0)
+
+template <bool kInt8>
+mla_status prepare_kernel(mlatree::Device& dev) {
+  using namespace mlatree;
+  TREE_CUDA(cudaFuncSetAttribute(tree_attn_kernel<kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
+            "kernel set-up");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  TREE_CUDA(cudaOccupancyMaxActiveClusters(&n, tree_attn_kernel<kInt8>, &cfg), "kernel occupancy");
+  if (n < 1) return tree_fail(MLA_ERR_CUDA, "the kernel does not fit this device");
+  dev.clusters[kInt8 ? 1 : 0] = std::min(n, kMaxClusters);
+  return MLA_OK;
+}
+
+// Kernel attributes and the tensor-map encoder; the first call on a device.
+mla_status init_device(mlatree::Device& dev) {
+  using namespace mlatree;
+  if (dev.ready) return MLA_OK;
+  if (g_encode == nullptr) {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    TREE_CUDA(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q),
+              "looking up cuTensorMapEncodeTiled");
+    if (fn == nullptr || q != cudaDriverEntryPointSuccess)
+      return tree_fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  mla_status st = prepare_kernel<false>(dev);
+  if (st == MLA_OK) st = prepare_kernel<true>(dev);
+  dev.ready = st == MLA_OK;
+  return st;
+}
+
+// bf16 [rows, cols] in boxes of 64 columns x `box` rows, 128-byte swizzle.
+mla_status tmap(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int box, const char* what) {
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t bx[2] = {64, static_cast<cuuint32_t>(box)}, es[2] = {1, 1};
+  const CUresult r = mlatree::g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, stride, bx,
+                                       es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return tree_fail(MLA_ERR_CUDA, "tensor map of %s: error %d", what, static_cast<int>(r));
   return MLA_OK;
 }
 
@@ -169,7 +1066,7 @@ extern "C" {
 size_t mla_tree_workspace_bytes(const mla_dims* dims) {
   g_tree_error[0] = '\0';
   if (dims == nullptr || check_dims(*dims) != MLA_OK) return 0;
-  return 256;
+  return mlatree::plan_of(*dims, mlatree::kMaxClusters).bytes;
 }
 
 mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const void* q_rope, const void* kv_nope,
@@ -192,13 +1089,21 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   if (!aligned(block_table, 4) || !aligned(act_seqs, 4) || !aligned(tree_lens, 4) || !aligned(tree_mask, 8) ||
       !aligned(lse, 4) || !aligned(workspace, 256))
     return tree_fail(MLA_ERR_ALIGN, "workspace 256-byte, tree_mask 8-byte, the int32 tensors and lse 4-byte aligned");
-  const size_t need = mla_tree_workspace_bytes(dims);
+  const size_t need = mlatree::plan_of(d, mlatree::kMaxClusters).bytes;  // does not depend on the device
   if (workspace_bytes < need) return tree_fail(MLA_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  int dev = 0;
+  TREE_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev < 0 || dev >= mlatree::kMaxDevices) return tree_fail(MLA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
+  int clusters = 0;
+  {
+    std::lock_guard<std::mutex> guard(mlatree::g_lock);
+    const mla_status ist = init_device(mlatree::g_dev[dev]);
+    if (ist != MLA_OK) return ist;
+    clusters = mlatree::g_dev[dev].clusters[int8 ? 1 : 0];
+  }
+  const mlatree::Plan plan = mlatree::plan_of(d, clusters);
   mlatree::Params p;
-  p.q_nope = static_cast<const uint8_t*>(q_nope);
-  p.q_rope = static_cast<const uint8_t*>(q_rope);
   p.kv_nope = static_cast<const uint8_t*>(kv_nope);
-  p.kv_rope = static_cast<const uint8_t*>(kv_rope);
   p.kv_scales = int8 ? kv_scales : nullptr;
   p.block_table = block_table;
   p.act_seqs = act_seqs;
@@ -206,17 +1111,39 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   p.tree_mask = tree_mask;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  p.parts = static_cast<float*>(workspace);
+  p.records = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + plan.records_at);
   p.B = d.B;
   p.S1 = d.S1;
   p.n_q = d.n_q;
   p.W = d.max_blocks_per_seq;
   p.num_blocks = d.num_blocks;
-  p.int8 = int8;
+  p.rows = plan.rows;
+  p.blocks = plan.blocks;
+  p.team = plan.team;
+  p.teams = plan.teams;
+  p.passes = plan.passes;
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
-  const int64_t rows = static_cast<int64_t>(d.B) * d.S1 * d.n_q;
-  mlatree::tree_simple_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return tree_fail(MLA_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+  p.out32 = aligned(out, 32) ? 1 : 0;
+  p.wait_ns = mlasp::host_wait_limit_ns();
+  const int64_t rows = static_cast<int64_t>(d.num_blocks) * 128, tokens = static_cast<int64_t>(d.B) * plan.rows;
+  mlatree::Maps maps;
+  mla_status ms = tmap(&maps.q_nope, q_nope, 512, tokens, 64, "q_nope");
+  if (ms == MLA_OK) ms = tmap(&maps.q_rope, q_rope, 64, tokens, 64, "q_rope");
+  if (ms == MLA_OK) ms = tmap(&maps.rope, kv_rope, 64, rows, 128, "kv_rope");
+  // an INT8 latent is loaded by the producers; its maps stay unused
+  if (ms == MLA_OK) ms = tmap(&maps.key, int8 ? kv_rope : kv_nope, int8 ? 64 : 512, rows, 128, "kv_nope");
+  if (ms == MLA_OK) ms = tmap(&maps.val, int8 ? kv_rope : kv_nope, int8 ? 64 : 512, rows, 64, "kv_nope");
+  if (ms != MLA_OK) return ms;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>(2 * plan.clusters));
+  if (int8) mlatree::tree_attn_kernel<true><<<grid, mlatree::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
+  else mlatree::tree_attn_kernel<false><<<grid, mlatree::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
+  TREE_CUDA(cudaGetLastError(), "kernel launch");
+  if (plan.teams > 1) {
+    mlatree::tree_merge_kernel<<<dim3(static_cast<unsigned>(plan.clusters), 128), 128, 0, s>>>(p);
+    TREE_CUDA(cudaGetLastError(), "merge launch");
+  }
   return MLA_OK;
 }
 
