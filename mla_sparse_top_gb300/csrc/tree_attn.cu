@@ -221,6 +221,12 @@ __device__ __forceinline__ void tma_pair(uint32_t dst, const void* map, int x, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 __device__ __forceinline__ void umma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -499,57 +505,68 @@ __device__ __forceinline__ void load_q(const Params& p, const Ctx& c, const Maps
   tma_pair(c.sb + kOffQ + 8 * kChunk, &maps.q_rope, 0, row, full);
 }
 
-// One thread of each CTA; the one of CTA 0 issues the pair's MMAs.
+// One warp of each CTA; an elected lane of CTA 0's issues the pair's MMAs.  The
+// warp stays converged around them: descriptors and addresses are then uniform
+// and an MMA takes few issue slots (a single running thread issues one per ~75
+// clocks, more than the 65 that it takes to run).
 __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk) {
   constexpr uint32_t idesc_s = make_idesc_f16(128, 256, 1, 0, 0);  // A, B K-major
   constexpr uint32_t idesc_v = make_idesc_f16(128, 256, 1, 0, 1);  // B MN-major
   const bool lead = c.rank == 0;
   Segment s, nx;
   bool more = walk.next(p, s), ok = true;
-  if (more) load_q(p, c, maps, s);
+  if (more && elect_one()) load_q(p, c, maps, s);
+  __syncwarp();
   int slot = 0, segs = 0, tile = 0;  // ring position, segments begun, tiles begun
   uint32_t phase = 0;
   // waits for the ring's next slot and issues its four MMAs
   auto take_slot = [&](uint32_t d, uint32_t a, uint32_t b_step, uint32_t b_lbo, uint32_t idesc, bool first) {
-    if (!wait<true>(c, kFull + slot, phase)) return false;
+    if (!warp_wait<false>(c, kFull + slot, phase)) return false;
     tc_fence_after();
-    const uint32_t b = c.sb + kOffRing + slot * kSlotBytes;
+    const uint64_t ad = make_sdesc(a, 16, 1024, kSwizzle128B);
+    const uint64_t bd = make_sdesc(c.sb + kOffRing + slot * kSlotBytes, b_lbo, 1024, kSwizzle128B);
+    if (elect_one()) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-      umma2(d, make_sdesc(a + ks * 32, 16, 1024, kSwizzle128B), make_sdesc(b + ks * b_step, b_lbo, 1024, kSwizzle128B),
-            idesc, (first && ks == 0) ? 0u : 1u);
-    commit2(c.bar(kEmpty + slot));
+      for (int ks = 0; ks < 4; ++ks)
+        umma2(d, ad + ks * (32 >> 4), bd + ks * (b_step >> 4), idesc, (first && ks == 0) ? 0u : 1u);
+      commit2(c.bar(kEmpty + slot));
+    }
+    __syncwarp();
     if (++slot == kSlots) {
       slot = 0;
       phase ^= 1;
     }
     return true;
   };
+  auto commit = [&](int bar) {
+    if (elect_one()) commit2(c.bar(bar));
+    __syncwarp();
+  };
   auto scores = [&](int t) {  // t: tiles begun before this one
-    if (!wait<true>(c, kSFree + (t & 1), ((t >> 1) & 1) ^ 1)) return false;
+    if (!warp_wait<true>(c, kSFree + (t & 1), ((t >> 1) & 1) ^ 1)) return false;
     tc_fence_after();
     for (int k = 0; k < kKeyItems; ++k)
       if (!take_slot(c.tmem + kTmemS + 128 * (t & 1), c.sb + kOffQ + k * kChunk, 32, 16, idesc_s, k == 0)) return false;
-    commit2(c.bar(kSFull + (t & 1)));
+    commit(kSFull + (t & 1));
     return true;
   };
   auto values = [&](int t, int groups, bool first) {
-    if (!wait<true>(c, kPReady, t & 1)) return false;
+    if (!warp_wait<true>(c, kPReady, t & 1)) return false;
     tc_fence_after();
     for (int k = 0; k < 2 * groups; ++k)
       if (!take_slot(c.tmem + kTmemO + 128 * (k & 1), c.sb + kOffP + (k >> 1) * kChunk, 2048, kChunk, idesc_v,
                      first && k < 2))
         return false;
-    commit2(c.bar(kPvDone));
+    commit(kPvDone);
     return true;
   };
   while (more && ok) {
     const int n = s.t1 - s.t0;
     if (lead) {
-      ok = wait<true>(c, kQFull, segs & 1);
+      ok = warp_wait<true>(c, kQFull, segs & 1);
       for (int u = 0; u < n && ok; ++u) {
         ok = scores(tile + u);
-        if (ok && u == n - 1) commit2(c.bar(kQFree));
+        if (ok && u == n - 1) commit(kQFree);
         if (ok && u > 0) ok = values(tile + u - 1, groups_of(s, s.t0 + u - 1), u == 1);
       }
       if (!ok) break;
@@ -557,9 +574,10 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
     // the next row block's Q as soon as this one's score MMAs are complete
     const bool again = walk.next(p, nx);
     if (again) {
-      ok = wait<false>(c, kQFree, segs & 1);
+      ok = warp_wait<false>(c, kQFree, segs & 1);
       if (!ok) break;
-      load_q(p, c, maps, nx);
+      if (elect_one()) load_q(p, c, maps, nx);
+      __syncwarp();
     }
     if (lead) ok = values(tile + n - 1, groups_of(s, s.t1 - 1), n == 1);
     tile += n;
@@ -568,7 +586,7 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
     more = again;
   }
   if (lead) {  // every MMA in flight lands before the CTAs leave
-    commit2(c.bar(kFinal));
+    commit(kFinal);
     volatile uint32_t never = 0;
     mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > kDrainNs ? c.wait_ns : kDrainNs);
   }
@@ -828,8 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp < kMmaWarp) {
       producer_role<kInt8>(p, c, maps, walk, warp - kProducerWarp0, lane);
     } else {
-      if (lane == 0) mma_role(p, c, maps, walk);
-      __syncwarp();
+      mma_role(p, c, maps, walk);
     }
   }
   if (tid == 0) {  // positions beyond the table, found by the cluster that owns the sequence's number
