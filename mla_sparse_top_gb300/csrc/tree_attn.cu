@@ -200,19 +200,19 @@ struct Ctx {
   __device__ uint32_t lead(int i) const { return mapa_shared(bar(i), 0); }  // the barrier in CTA 0
 };
 
-template <bool kCluster>
-__device__ __forceinline__ bool wait(const Ctx& c, int i, uint32_t parity) {
-  return mbar_wait<kCluster>(c.bar(i), parity, c.abort, c.wait_ns);
-}
-template <bool kCluster>
 __device__ __forceinline__ bool warp_wait(const Ctx& c, int i, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait<kCluster>(c, i, parity));
+  return __all_sync(0xffffffffu, mbar_wait<false>(c.bar(i), parity, c.abort, c.wait_ns));
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+// Arrivals on a barrier of CTA 0, with release at CTA scope: what they hand over
+// is tensor memory or shared memory of the arriving CTA itself, already ordered
+// for the tensor core (tcgen05.wait, fence.proxy.async), so nothing has to be
+// made visible to threads of the other CTA.  Release at cluster scope waits for
+// a round trip to L2, ~1500 clocks under load, in the softmax's critical path.
+__device__ __forceinline__ void arrive_lead(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
 }
-__device__ __forceinline__ void arrive_cluster_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;"
+__device__ __forceinline__ void arrive_lead_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cluster.b64 _, [%0], %1;"
                :: "r"(bar), "r"(bytes) : "memory");
 }
 // TMA load whose bytes count on a barrier of either CTA of the pair.
@@ -425,11 +425,11 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, W
     return true;
   };
   auto done = [&](int k, int items) { skip = k - items; };  // k: the first item at or beyond `items`
-  auto free_slot = [&]() { return warp_wait<false>(c, kEmpty + w, (fills++ & 1) ^ 1); };
+  auto free_slot = [&]() { return warp_wait(c, kEmpty + w, (fills++ & 1) ^ 1); };
   auto filled = [&]() {
     fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
     __syncwarp();
-    if (lane == 0) arrive_cluster(full);
+    if (lane == 0) arrive_lead(full);
   };
   Segment s;
   while (walk.next(p, s)) {
@@ -450,7 +450,7 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, W
           } else {
             if (!free_slot()) return;
             if (lane == 0) {
-              arrive_cluster_tx(full, kSlotBytes);
+              arrive_lead_tx(full, kSlotBytes);
               if (k < 8) tma_pair(slot, &maps.key, 64 * k, row, full);
               else tma_pair(slot, &maps.rope, 0, row, full);
             }
@@ -483,7 +483,7 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, W
           } else {
             if (!free_slot()) return;
             if (lane == 0) {
-              arrive_cluster_tx(full, kSlotBytes);
+              arrive_lead_tx(full, kSlotBytes);
               tma_pair(slot, &maps.val, dim0, row, full);
               tma_pair(slot + kChunk, &maps.val, dim0 + 64, row, full);
             }
@@ -500,7 +500,7 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, W
 __device__ __forceinline__ void load_q(const Params& p, const Ctx& c, const Maps& maps, const Segment& s) {
   const uint32_t full = c.lead(kQFull);
   const int row = s.b * p.rows + s.rb * kRowBlock + static_cast<int>(c.rank) * 64;
-  arrive_cluster_tx(full, kKeyItems * kChunk);
+  arrive_lead_tx(full, kKeyItems * kChunk);
   for (int k = 0; k < 8; ++k) tma_pair(c.sb + kOffQ + k * kChunk, &maps.q_nope, 64 * k, row, full);
   tma_pair(c.sb + kOffQ + 8 * kChunk, &maps.q_rope, 0, row, full);
 }
@@ -519,51 +519,58 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
   __syncwarp();
   int slot = 0, segs = 0, tile = 0;  // ring position, segments begun, tiles begun
   uint32_t phase = 0;
-  // waits for the ring's next slot and issues its four MMAs
-  auto take_slot = [&](uint32_t d, uint32_t a, uint32_t b_step, uint32_t b_lbo, uint32_t idesc, bool first) {
-    if (!warp_wait<false>(c, kFull + slot, phase)) return false;
-    tc_fence_after();
-    const uint64_t ad = make_sdesc(a, 16, 1024, kSwizzle128B);
-    const uint64_t bd = make_sdesc(c.sb + kOffRing + slot * kSlotBytes, b_lbo, 1024, kSwizzle128B);
+  // descriptors once; slots, chunks and k steps are additions to their address field
+  const uint64_t desc_q = make_sdesc(c.sb + kOffQ, 16, 1024, kSwizzle128B);
+  const uint64_t desc_p = make_sdesc(c.sb + kOffP, 16, 1024, kSwizzle128B);
+  const uint64_t desc_k = make_sdesc(c.sb + kOffRing, 16, 1024, kSwizzle128B);
+  const uint64_t desc_v = make_sdesc(c.sb + kOffRing, kChunk, 1024, kSwizzle128B);
+  // waits for the ring's next slot and issues its four MMAs (no tcgen05 fence:
+  // what the wait orders is shared memory, written by TMA or fenced by its writers)
+  auto take_slot = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t b_step, uint32_t idesc, bool first) {
+    const uint32_t fb = c.bar(kFull) + 8 * slot;
+    if (!mbar_wait<false>(fb, phase, c.abort, c.wait_ns)) *c.abort = 1u;
+    __syncwarp();
+    bd += static_cast<uint32_t>(slot * (kSlotBytes >> 4));
     if (elect_one()) {
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
         umma2(d, ad + ks * (32 >> 4), bd + ks * (b_step >> 4), idesc, (first && ks == 0) ? 0u : 1u);
-      commit2(c.bar(kEmpty + slot));
+      commit2(fb + 8 * (kEmpty - kFull));
     }
     __syncwarp();
     if (++slot == kSlots) {
       slot = 0;
       phase ^= 1;
     }
-    return true;
   };
   auto commit = [&](int bar) {
     if (elect_one()) commit2(c.bar(bar));
     __syncwarp();
   };
   auto scores = [&](int t) {  // t: tiles begun before this one
-    if (!warp_wait<true>(c, kSFree + (t & 1), ((t >> 1) & 1) ^ 1)) return false;
+    if (!warp_wait(c, kSFree + (t & 1), ((t >> 1) & 1) ^ 1)) return false;
     tc_fence_after();
+#pragma unroll 1
     for (int k = 0; k < kKeyItems; ++k)
-      if (!take_slot(c.tmem + kTmemS + 128 * (t & 1), c.sb + kOffQ + k * kChunk, 32, 16, idesc_s, k == 0)) return false;
+      take_slot(c.tmem + kTmemS + 128 * (t & 1), desc_q + static_cast<uint32_t>(k * (kChunk >> 4)), desc_k, 32, idesc_s,
+                k == 0);
     commit(kSFull + (t & 1));
-    return true;
+    return !*c.abort;
   };
   auto values = [&](int t, int groups, bool first) {
-    if (!warp_wait<true>(c, kPReady, t & 1)) return false;
+    if (!warp_wait(c, kPReady, t & 1)) return false;
     tc_fence_after();
+#pragma unroll 1
     for (int k = 0; k < 2 * groups; ++k)
-      if (!take_slot(c.tmem + kTmemO + 128 * (k & 1), c.sb + kOffP + (k >> 1) * kChunk, 2048, kChunk, idesc_v,
-                     first && k < 2))
-        return false;
+      take_slot(c.tmem + kTmemO + 128 * (k & 1), desc_p + static_cast<uint32_t>((k >> 1) * (kChunk >> 4)), desc_v, 2048,
+                idesc_v, first && k < 2);
     commit(kPvDone);
-    return true;
+    return !*c.abort;
   };
   while (more && ok) {
     const int n = s.t1 - s.t0;
     if (lead) {
-      ok = warp_wait<true>(c, kQFull, segs & 1);
+      ok = warp_wait(c, kQFull, segs & 1);
       for (int u = 0; u < n && ok; ++u) {
         ok = scores(tile + u);
         if (ok && u == n - 1) commit(kQFree);
@@ -574,7 +581,7 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
     // the next row block's Q as soon as this one's score MMAs are complete
     const bool again = walk.next(p, nx);
     if (again) {
-      ok = warp_wait<false>(c, kQFree, segs & 1);
+      ok = warp_wait(c, kQFree, segs & 1);
       if (!ok) break;
       if (elect_one()) load_q(p, c, maps, nx);
       __syncwarp();
@@ -631,7 +638,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
     e[part * 64 + row] = v;
     __syncwarp();
     if (lane == 0) mbar_arrive(c.bar(maxbar));
-    if (!warp_wait<false>(c, maxbar, uses & 1)) return false;
+    if (!warp_wait(c, maxbar, uses & 1)) return false;
     ++uses;
 #pragma unroll
     for (int k = 0; k < 4; ++k) all[k] = e[k * 64 + row];
@@ -658,7 +665,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
         drafted &= low_bits(s.n - at) & ~low_bits(-at);
         vis &= live ? (low_bits(-at) | drafted) : 0ull;
       }
-      if (!warp_wait<false>(c, kSFull + buf, (tile >> 1) & 1)) return;
+      if (!warp_wait(c, kSFull + buf, (tile >> 1) & 1)) return;
       tc_fence_after();
       float z[64];
       {
@@ -671,7 +678,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(c.lead(kSFree + buf));
+      if (lane == 0) arrive_lead(c.lead(kSFree + buf));
 #pragma unroll
       for (int k = 0; k < 64; ++k) z[k] *= p.scale_log2;
       if (__any_sync(0xffffffffu, vis != ~0ull)) {
@@ -704,7 +711,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
       }
       l += sum[0] + sum[1];
       // P and O are free once the tile before has been multiplied
-      if (tile > 0 && !warp_wait<false>(c, kPvDone, (tile - 1) & 1)) return;
+      if (tile > 0 && !warp_wait(c, kPvDone, (tile - 1) & 1)) return;
       if (t > s.t0 && __any_sync(0xffffffffu, grow)) {
         tc_fence_after();
 #pragma unroll 1
@@ -725,7 +732,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
         sts16(pr + ((u ^ (row & 7)) << 4), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_cluster(c.lead(kPReady));
+      if (lane == 0) arrive_lead(c.lead(kPReady));
     }
     float all[4];
     if (!share(l, all)) return;
@@ -734,7 +741,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
       l = 0.f;
       m = -INFINITY;
     }
-    if (!warp_wait<false>(c, kPvDone, (tile - 1) & 1)) return;
+    if (!warp_wait(c, kPvDone, (tile - 1) & 1)) return;
     tc_fence_after();
     const bool whole = s.t0 == 0 && s.t1 == s.tiles;
     const int64_t grow = static_cast<int64_t>(s.b) * p.rows + r;
