@@ -505,16 +505,19 @@ __device__ __forceinline__ void load_q(const Params& p, const Ctx& c, const Maps
   tma_pair(c.sb + kOffQ + 8 * kChunk, &maps.q_rope, 0, row, full);
 }
 
+// The value of lane 0, which lets the compiler keep it in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // One warp of each CTA; an elected lane of CTA 0's issues the pair's MMAs.  The
-// warp stays converged around them: descriptors and addresses are then uniform
-// and an MMA takes few issue slots (a single running thread issues one per ~75
-// clocks, more than the 65 that it takes to run).
+// warp stays converged, and what steers it (tile counts, outcomes of waits) is
+// made uniform, so that descriptors and addresses live in uniform registers: a
+// ring slot's four MMAs take 259 clocks to run and have to be issued in less.
 __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk) {
   constexpr uint32_t idesc_s = make_idesc_f16(128, 256, 1, 0, 0);  // A, B K-major
   constexpr uint32_t idesc_v = make_idesc_f16(128, 256, 1, 0, 1);  // B MN-major
-  const bool lead = c.rank == 0;
+  const bool lead = uniform(static_cast<int>(c.rank)) == 0;
   Segment s, nx;
-  bool more = walk.next(p, s), ok = true;
+  bool more = uniform(walk.next(p, s)) != 0, ok = true;
   if (more && elect_one()) load_q(p, c, maps, s);
   __syncwarp();
   int slot = 0, segs = 0, tile = 0;  // ring position, segments begun, tiles begun
@@ -524,21 +527,36 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
   const uint64_t desc_p = make_sdesc(c.sb + kOffP, 16, 1024, kSwizzle128B);
   const uint64_t desc_k = make_sdesc(c.sb + kOffRing, 16, 1024, kSwizzle128B);
   const uint64_t desc_v = make_sdesc(c.sb + kOffRing, kChunk, 1024, kSwizzle128B);
-  // waits for the ring's next slot and issues its four MMAs (no tcgen05 fence:
-  // what the wait orders is shared memory, written by TMA or fenced by its writers)
-  auto take_slot = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t b_step, uint32_t idesc, bool first) {
-    const uint32_t fb = c.bar(kFull) + 8 * slot;
-    if (!mbar_wait<false>(fb, phase, c.abort, c.wait_ns)) *c.abort = 1u;
+  const int lane = threadIdx.x & 31;
+  // Waits for the ring's next two slots (their barriers are tested side by side,
+  // by even and odd lanes) or for one, and issues the four MMAs of each.  No
+  // tcgen05 fence: what the wait orders is shared memory, written by TMA or
+  // fenced by its writers.
+  auto take_slots = [&](bool two, uint32_t d0, uint32_t d1, uint64_t a0, uint64_t a1, uint64_t base, uint32_t b_step,
+                        uint32_t idesc, bool first0, bool first1) {
+    const int s0 = slot, s1 = slot + 1 == kSlots ? 0 : slot + 1;
+    const uint32_t ph1 = phase ^ (s1 == 0 ? 1u : 0u);
+    const bool odd = two && (lane & 1);
+    if (!mbar_wait<false>(c.bar(kFull) + 8 * (odd ? s1 : s0), odd ? ph1 : phase, c.abort, c.wait_ns)) *c.abort = 1u;
     __syncwarp();
-    bd += static_cast<uint32_t>(slot * (kSlotBytes >> 4));
     if (elect_one()) {
+      const uint64_t b0 = base + static_cast<uint32_t>(s0 * (kSlotBytes >> 4));
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        umma2(d, ad + ks * (32 >> 4), bd + ks * (b_step >> 4), idesc, (first && ks == 0) ? 0u : 1u);
-      commit2(fb + 8 * (kEmpty - kFull));
+        umma2(d0, a0 + ks * (32 >> 4), b0 + ks * (b_step >> 4), idesc, (first0 && ks == 0) ? 0u : 1u);
+      commit2(c.bar(kEmpty) + 8 * s0);
+      if (two) {
+        const uint64_t b1 = base + static_cast<uint32_t>(s1 * (kSlotBytes >> 4));
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma2(d1, a1 + ks * (32 >> 4), b1 + ks * (b_step >> 4), idesc, (first1 && ks == 0) ? 0u : 1u);
+        commit2(c.bar(kEmpty) + 8 * s1);
+      }
     }
     __syncwarp();
-    if (++slot == kSlots) {
+    slot = two ? s1 + 1 : s0 + 1;
+    phase = two ? ph1 : phase;
+    if (slot == kSlots) {
       slot = 0;
       phase ^= 1;
     }
@@ -550,43 +568,47 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
   auto scores = [&](int t) {  // t: tiles begun before this one
     if (!warp_wait(c, kSFree + (t & 1), ((t >> 1) & 1) ^ 1)) return false;
     tc_fence_after();
+    const uint32_t d = c.tmem + kTmemS + 128 * (t & 1);
 #pragma unroll 1
-    for (int k = 0; k < kKeyItems; ++k)
-      take_slot(c.tmem + kTmemS + 128 * (t & 1), desc_q + static_cast<uint32_t>(k * (kChunk >> 4)), desc_k, 32, idesc_s,
-                k == 0);
+    for (int k = 0; k < kKeyItems; k += 2) {
+      const uint64_t a = desc_q + static_cast<uint32_t>(k * (kChunk >> 4));
+      take_slots(k + 1 < kKeyItems, d, d, a, a + (kChunk >> 4), desc_k, 32, idesc_s, k == 0, false);
+    }
     commit(kSFull + (t & 1));
-    return !*c.abort;
+    return __all_sync(0xffffffffu, *c.abort == 0u) != 0;
   };
   auto values = [&](int t, int groups, bool first) {
     if (!warp_wait(c, kPReady, t & 1)) return false;
     tc_fence_after();
 #pragma unroll 1
-    for (int k = 0; k < 2 * groups; ++k)
-      take_slot(c.tmem + kTmemO + 128 * (k & 1), desc_p + static_cast<uint32_t>((k >> 1) * (kChunk >> 4)), desc_v, 2048,
-                idesc_v, first && k < 2);
+    for (int g = 0; g < groups; ++g) {
+      const uint64_t a = desc_p + static_cast<uint32_t>(g * (kChunk >> 4));
+      const bool begin = first && g == 0;
+      take_slots(true, c.tmem + kTmemO, c.tmem + kTmemO + 128, a, a, desc_v, 2048, idesc_v, begin, begin);
+    }
     commit(kPvDone);
-    return !*c.abort;
+    return __all_sync(0xffffffffu, *c.abort == 0u) != 0;
   };
   while (more && ok) {
-    const int n = s.t1 - s.t0;
+    const int n = uniform(s.t1 - s.t0);
     if (lead) {
       ok = warp_wait(c, kQFull, segs & 1);
       for (int u = 0; u < n && ok; ++u) {
         ok = scores(tile + u);
         if (ok && u == n - 1) commit(kQFree);
-        if (ok && u > 0) ok = values(tile + u - 1, groups_of(s, s.t0 + u - 1), u == 1);
+        if (ok && u > 0) ok = values(tile + u - 1, uniform(groups_of(s, s.t0 + u - 1)), u == 1);
       }
       if (!ok) break;
     }
     // the next row block's Q as soon as this one's score MMAs are complete
-    const bool again = walk.next(p, nx);
+    const bool again = uniform(walk.next(p, nx)) != 0;
     if (again) {
       ok = warp_wait(c, kQFree, segs & 1);
       if (!ok) break;
       if (elect_one()) load_q(p, c, maps, nx);
       __syncwarp();
     }
-    if (lead) ok = values(tile + n - 1, groups_of(s, s.t1 - 1), n == 1);
+    if (lead) ok = values(tile + n - 1, uniform(groups_of(s, s.t1 - 1)), n == 1);
     tile += n;
     ++segs;
     s = nx;
@@ -805,7 +827,7 @@ template <bool kInt8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ uint8_t raw[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   Ctx c;
   c.sb = (smem_u32(raw) + 1023u) & ~1023u;  // swizzled operands need 1024-byte alignment
   c.smem = raw + (c.sb - smem_u32(raw));
@@ -845,7 +867,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_arrive();
   cluster_wait();
   tc_fence_after();
-  c.tmem = *reinterpret_cast<volatile uint32_t*>(c.smem + kOffTmem);
+  c.tmem = uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(c.smem + kOffTmem)));
 
   if (busy) {
     if (warp < kSoftmaxWarps) {
