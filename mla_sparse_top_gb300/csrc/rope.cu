@@ -7,9 +7,11 @@
 // here) and no loss at far positions.  Read as a signed fraction of a turn it
 // converts to fp32 with full relative precision, and sincospif takes it.
 //
-// The rotation is bound by memory.  A block takes some tokens (their angles go
-// to shared memory once, for all heads) and some heads; each thread moves four
-// 16-byte units per pass, loaded before the angles are needed.
+// The rotation is bound by memory.  A thread keeps one unit of a head (16
+// bytes, or one pair of values where alignment forbids that) and walks over
+// the rows, (token, head) pairs, of its block, 64 bytes in flight: offsets
+// advance by additions, and the unit's angles stay in registers until the
+// token changes, so nothing is shared between threads and nothing waits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,10 +26,9 @@
 
 namespace mlarp {
 
-constexpr int kThreads = 256;
-constexpr int kMaxPairs = 128;      // rot_dim <= 256
-constexpr int kMaxBlockPairs = 1024;  // (token, pair) angles of a block
-constexpr int kUnroll = 4;
+constexpr int kThreads = 512;
+constexpr int kMaxPairs = 128;  // rot_dim <= 256
+constexpr int kMaxPasses = 16;  // rows of a thread
 
 __device__ unsigned int g_rope_status = 0;
 
@@ -72,14 +73,14 @@ struct Tensor {
   int64_t xt, xh, ot, oh;  // strides in elements
   const int64_t* rows;
   int64_t num_rows;
-  int n_heads, head_dim, rot_off;
-  int vec;          // 16-byte units
-  int in_place;     // the part outside the rotation is left alone
-  int rot_units;    // units of a head that hold rotated values
-  int units;        // all units of a head
-  int tokens;       // tokens of a block
-  int heads;        // heads of a block
-  int head_blocks;  // blocks per group of tokens
+  int n_heads, rot_off;
+  int vec;         // 16-byte units
+  int rot_units;   // units of a head that hold rotated values
+  int units;       // all units of a head (in place: the rotated ones)
+  int pass_rows;   // rows that a block takes at a time
+  int pass_t, pass_h;  // the same in tokens and heads
+  int passes;
+  int unit_blocks;  // blocks over the units of a row (more than kThreads units)
   int blocks;
 };
 
@@ -90,151 +91,183 @@ struct Params {
   int T, pairs, half, inverse;
 };
 
+// Two 16-bit values of a word as fp32, and back with one rounding each.
 template <typename E>
-__device__ __forceinline__ float to_f(E v);
-template <>
-__device__ __forceinline__ float to_f(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (sizeof(E) == 2 && __is_same(E, __half)) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
 template <typename E>
-__device__ __forceinline__ E from_f(float v);
-template <>
-__device__ __forceinline__ float from_f(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (__is_same(E, __half)) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 turn2(float a, float b, float2 cs) {
+  return make_float2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+}
 
+// V values of type E in memory; W words in registers (single 16-bit values take a word).
 template <typename E, int V>
-struct alignas(sizeof(E) * V) Pack {
-  E e[V];
-};
-
-// A unit of the half layout (both layouts for V = 1) is two packs: V values of
-// the first half and the V that turn with them; any other unit is one pack.
-template <typename E, int V>
-struct Unit {
-  Pack<E, V> a, b;
-};
-
-template <typename E, int V>
-__device__ void rotate_block(const Params& p, const Tensor& w, int block, float2* angles) {
-  const int tid = threadIdx.x;
-  const int t0 = block / w.head_blocks * w.tokens, h0 = block % w.head_blocks * w.heads;
-  const int nt = min(w.tokens, p.T - t0), nh = min(w.heads, w.n_heads - h0);
-  const bool two = V == 1 || p.half;  // rotated units are two packs
-  const int rot = w.rot_off, pairs = p.pairs;
-  const int n = nt * nh * w.units;
-  const int second = p.half ? pairs : 1;  // distance of a pair's values
-
-  // where unit u of this block starts: element offsets in x and out, its token
-  // and rotated pair (-1: copied)
-  struct Place {
-    int64_t x, o;
-    int at;  // index of its first angle, -1 when copied
-  };
-  auto place = [&](int u) {
-    const int k = u % w.units, r = u / w.units;
-    const int h = r % nh, t = r / nh;
-    Place q;
-    int d;
-    if (k < w.rot_units) {
-      const int pr = V == 1 ? k : (p.half ? k * V : k * V / 2);  // first pair
-      d = rot + (p.half ? pr : 2 * pr);
-      q.at = t * pairs + pr;
+struct Pack {
+  static constexpr int W = sizeof(E) * V < 4 ? 1 : sizeof(E) * V / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (W == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else if constexpr (sizeof(E) == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
     } else {
-      const int c = (k - w.rot_units) * V;  // copied values, in order
-      d = c < rot ? c : c + 2 * pairs;
-      q.at = -1;
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
     }
-    const int64_t tok = t0 + t;
-    q.x = tok * w.xt + static_cast<int64_t>(h0 + h) * w.xh + d;
-    int64_t row = tok;
-    if (w.rows != nullptr) row = __ldg(w.rows + tok);
-    q.o = row < 0 || (w.rows != nullptr && row >= w.num_rows)
-              ? -1
-              : row * w.ot + static_cast<int64_t>(h0 + h) * w.oh + d;
-    return q;
-  };
-  const E* x = static_cast<const E*>(w.x);
-  E* out = static_cast<E*>(w.out);
-  auto load = [&](const Place& q) {
-    Unit<E, V> v;
-    v.a = *reinterpret_cast<const Pack<E, V>*>(x + q.x);
-    v.b = v.a;
-    if (two && q.at >= 0) v.b = *reinterpret_cast<const Pack<E, V>*>(x + q.x + second);
-    return v;
-  };
-
-  // the first units are on their way while the angles are made
-  Place q[kUnroll];
-  Unit<E, V> v[kUnroll];
-#pragma unroll
-  for (int k = 0; k < kUnroll; ++k)
-    if (tid + k * kThreads < n) {
-      q[k] = place(tid + k * kThreads);
-      v[k] = load(q[k]);
-    }
-  if (w.rows != nullptr && h0 == 0)
-    for (int t = tid; t < nt; t += kThreads)
-      if (__ldg(w.rows + t0 + t) >= w.num_rows) atomicOr(&g_rope_status, MLA_DEVICE_BAD_BLOCK);
-  for (int e = tid; e < nt * pairs; e += kThreads) {
-    const int t = e / pairs;
-    float2 cs = cos_sin(__ldg(p.positions + t0 + t), p.f.turn[e - t * pairs], p.f.mscale);
-    if (p.inverse) cs.y = -cs.y;
-    angles[e] = cs;
   }
-  __syncthreads();
-  for (int u0 = tid; u0 < n; u0 += kUnroll * kThreads) {
-    if (u0 != tid) {
+  __device__ __forceinline__ void store(E* p) const {
+    if constexpr (W == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (sizeof(E) == 2) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+};
+
+// Turns the pairs of a unit: of two packs (value i of a with value i of b) or within one.
+template <typename E, int V, bool kTwo, int N>
+__device__ __forceinline__ void turn_unit(Pack<E, V>& a, Pack<E, V>& b, const float2 (&cs)[N]) {
+  constexpr int W = Pack<E, V>::W;
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k)
-        if (u0 + k * kThreads < n) {
-          q[k] = place(u0 + k * kThreads);
-          v[k] = load(q[k]);
-        }
+  for (int k = 0; k < W; ++k) {
+    if constexpr (sizeof(E) == 4) {
+      if constexpr (kTwo) {
+        const float2 y = turn2(__uint_as_float(a.w[k]), __uint_as_float(b.w[k]), cs[k]);
+        a.w[k] = __float_as_uint(y.x);
+        b.w[k] = __float_as_uint(y.y);
+      } else if (k % 2 == 0) {
+        const float2 y = turn2(__uint_as_float(a.w[k]), __uint_as_float(a.w[k + 1]), cs[k / 2]);
+        a.w[k] = __float_as_uint(y.x);
+        a.w[k + 1] = __float_as_uint(y.y);
+      }
+    } else if constexpr (kTwo) {
+      const float2 u = unpack2<E>(a.w[k]), v = unpack2<E>(b.w[k]);
+      const float2 y = turn2(u.x, v.x, cs[V == 1 ? 0 : 2 * k]);
+      if constexpr (V == 1) {
+        a.w[k] = pack2<E>(y.x, 0.f);
+        b.w[k] = pack2<E>(y.y, 0.f);
+      } else {
+        const float2 z = turn2(u.y, v.y, cs[2 * k + 1]);
+        a.w[k] = pack2<E>(y.x, z.x);
+        b.w[k] = pack2<E>(y.y, z.y);
+      }
+    } else {
+      const float2 u = unpack2<E>(a.w[k]);
+      const float2 y = turn2(u.x, u.y, cs[k]);
+      a.w[k] = pack2<E>(y.x, y.y);
+    }
+  }
+}
+
+// kTwo: a rotated unit is two packs, V values and the V that turn with them
+// (the half layout, and single pairs of either layout); otherwise one pack of
+// V / 2 adjacent pairs.
+template <typename E, int V, bool kTwo>
+__device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, int block) {
+  constexpr int kPairs = kTwo ? V : V / 2;
+  constexpr int kUnroll = kTwo && V > 1 ? 2 : 4;  // rows in flight
+  const int tid = threadIdx.x;
+  const int64_t rows = static_cast<int64_t>(p.T) * w.n_heads;
+  int r, k;
+  int64_t row;
+  if (w.unit_blocks == 1) {
+    r = tid / w.units;
+    k = tid - r * w.units;
+    if (r >= w.pass_rows) return;
+    row = static_cast<int64_t>(block) * w.passes * w.pass_rows + r;
+  } else {
+    k = block % w.unit_blocks * kThreads + tid;
+    if (k >= w.units) return;
+    row = static_cast<int64_t>(block / w.unit_blocks) * w.passes;
+  }
+  if (row >= rows) return;
+  const int n = static_cast<int>(min(static_cast<int64_t>(w.passes), (rows - row + w.pass_rows - 1) / w.pass_rows));
+  const bool rotated = k < w.rot_units;
+  const int second = p.half ? p.pairs : 1;  // distance of a pair's values (kTwo)
+  int d, pair0 = 0;
+  if (rotated) {
+    pair0 = k * kPairs;
+    d = w.rot_off + (p.half ? pair0 : 2 * pair0);
+  } else {
+    const int c = (k - w.rot_units) * V;  // copied values, in order
+    d = c < w.rot_off ? c : c + 2 * p.pairs;
+  }
+  float2 cs[kPairs];
+  int t = static_cast<int>(row / w.n_heads);
+  int h = static_cast<int>(row - static_cast<int64_t>(t) * w.n_heads);
+  int angles_of = -1;  // the token whose angles cs holds
+  const E* x = static_cast<const E*>(w.x) + d + t * w.xt + h * w.xh;
+  E* const out = static_cast<E*>(w.out) + d;
+  int64_t o = t * w.ot + h * w.oh;
+  // the next row of this thread: `step` on, or `wrap` on when it enters another token
+  const int64_t x_step = w.pass_t * w.xt + w.pass_h * w.xh, x_wrap = x_step + w.xt - w.n_heads * w.xh;
+  const int64_t o_step = w.pass_t * w.ot + w.pass_h * w.oh, o_wrap = o_step + w.ot - w.n_heads * w.oh;
+  for (int it = 0; it < n; it += kUnroll) {
+    Pack<E, V> a[kUnroll], b[kUnroll];
+    int tok[kUnroll];
+    int64_t to[kUnroll];
+    int32_t pos[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      tok[u] = t;
+      to[u] = -1;
+      if (it + u >= n) continue;
+      a[u].load(x);
+      if (kTwo && rotated) b[u].load(x + second);
+      pos[u] = rotated ? __ldg(p.positions + t) : 0;
+      to[u] = o;
+      if (w.rows != nullptr) {
+        const int64_t row_to = __ldg(w.rows + t);
+        if (row_to >= w.num_rows && k == 0 && h == 0) atomicOr(&g_rope_status, MLA_DEVICE_BAD_BLOCK);
+        to[u] = row_to < 0 || row_to >= w.num_rows ? -1 : row_to * w.ot + h * w.oh;
+      }
+      t += w.pass_t;
+      h += w.pass_h;
+      const bool next = h >= w.n_heads;
+      if (next) {
+        h -= w.n_heads;
+        ++t;
+      }
+      x += next ? x_wrap : x_step;
+      o += next ? o_wrap : o_step;
     }
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      if (u0 + k * kThreads >= n || q[k].o < 0) continue;
-      if (q[k].at < 0) {
-        *reinterpret_cast<Pack<E, V>*>(out + q[k].o) = v[k].a;
-        continue;
-      }
-      if (two) {
+    for (int u = 0; u < kUnroll; ++u) {
+      if (to[u] < 0) continue;  // no row, or none to write
+      if (rotated) {
+        if (tok[u] != angles_of) {
+          angles_of = tok[u];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 cs = angles[q[k].at + i];
-          const float a = to_f(v[k].a.e[i]), b = to_f(v[k].b.e[i]);
-          v[k].a.e[i] = from_f<E>(a * cs.x - b * cs.y);
-          v[k].b.e[i] = from_f<E>(a * cs.y + b * cs.x);
+          for (int i = 0; i < kPairs; ++i) {
+            cs[i] = cos_sin(pos[u], p.f.turn[pair0 + i], p.f.mscale);
+            if (p.inverse) cs[i].y = -cs[i].y;
+          }
         }
-        *reinterpret_cast<Pack<E, V>*>(out + q[k].o) = v[k].a;
-        *reinterpret_cast<Pack<E, V>*>(out + q[k].o + second) = v[k].b;
-      } else {
-#pragma unroll
-        for (int i = 0; i + 1 < V; i += 2) {
-          const float2 cs = angles[q[k].at + i / 2];
-          const float a = to_f(v[k].a.e[i]), b = to_f(v[k].a.e[i + 1]);
-          v[k].a.e[i] = from_f<E>(a * cs.x - b * cs.y);
-          v[k].a.e[i + 1] = from_f<E>(a * cs.y + b * cs.x);
-        }
-        *reinterpret_cast<Pack<E, V>*>(out + q[k].o) = v[k].a;
+        turn_unit<E, V, kTwo>(a[u], b[u], cs);
+        if (kTwo) b[u].store(out + to[u] + second);
       }
+      a[u].store(out + to[u]);
     }
   }
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Params p) {
-  __shared__ float2 angles[kMaxBlockPairs];
+__global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ Params p) {
   const int second = static_cast<int>(blockIdx.x) >= p.t[0].blocks;
   const int block = static_cast<int>(blockIdx.x) - (second ? p.t[0].blocks : 0);
   const Tensor& w = p.t[second];
-  if (w.vec) rotate_block<E, 16 / sizeof(E)>(p, w, block, angles);
-  else rotate_block<E, 1>(p, w, block, angles);
+  if (!w.vec) rotate_rows<E, 1, true>(p, w, block);
+  else if (p.half) rotate_rows<E, 16 / sizeof(E), true>(p, w, block);
+  else rotate_rows<E, 16 / sizeof(E), false>(p, w, block);
 }
 
 }  // namespace mlarp
@@ -290,7 +323,7 @@ mla_status make_freqs(const mla_rope_params* q, int rot, mlarp::Freqs* f) {
   return MLA_OK;
 }
 
-// Checks one tensor and splits its work into blocks of about kThreads * kUnroll units.
+// Checks one tensor and splits its rows into blocks.
 mla_status make_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const char* name, mlarp::Tensor* w) {
   if (!q->x || !q->out) return rope_fail(MLA_ERR_NULL, "%s: a required pointer is NULL", name);
   if (q->n_heads < 1 || q->rot_off < 0 || static_cast<int64_t>(q->rot_off) + d.rot_dim > q->head_dim)
@@ -331,18 +364,19 @@ mla_status make_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const c
   w->rows = q->rows;
   w->num_rows = q->num_rows;
   w->n_heads = q->n_heads;
-  w->head_dim = q->head_dim;
   w->rot_off = q->rot_off;
-  w->in_place = same;
   const int width = w->vec ? V : 1;
   w->rot_units = w->vec && !d.half ? d.rot_dim / V : d.rot_dim / 2 / width;
   w->units = w->rot_units + (same ? 0 : (q->head_dim - d.rot_dim) / width);
-  const int goal = mlarp::kThreads * mlarp::kUnroll;
-  w->heads = std::min(q->n_heads, std::max(1, goal / w->units));
-  w->head_blocks = (q->n_heads + w->heads - 1) / w->heads;
-  w->tokens = w->head_blocks > 1 ? 1 : std::max(1, goal / (w->units * w->heads));
-  w->tokens = std::min({w->tokens, mlarp::kMaxBlockPairs / (d.rot_dim / 2), d.T});
-  const int64_t blocks = (static_cast<int64_t>(d.T) + w->tokens - 1) / w->tokens * w->head_blocks;
+  w->unit_blocks = (w->units + mlarp::kThreads - 1) / mlarp::kThreads;
+  w->pass_rows = w->unit_blocks > 1 ? 1 : mlarp::kThreads / w->units;
+  w->pass_t = w->pass_rows / q->n_heads;
+  w->pass_h = w->pass_rows % q->n_heads;
+  // several rows per thread once there is a block for every SM twice over
+  const int64_t all = static_cast<int64_t>(d.T) * q->n_heads, passes = (all + w->pass_rows - 1) / w->pass_rows;
+  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(mlarp::kMaxPasses, passes / (2 * 152))));
+  if (w->passes > 4) w->passes = w->passes / 4 * 4;
+  const int64_t blocks = (passes + w->passes - 1) / w->passes * w->unit_blocks;
   if (blocks >= (1ll << 30)) return rope_fail(MLA_ERR_SHAPE, "%s: T x heads too large", name);
   w->blocks = static_cast<int>(blocks);
   return MLA_OK;
