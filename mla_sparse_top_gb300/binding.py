@@ -520,19 +520,20 @@ def prolog_device_status(clear: bool = True, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ page plan and rotary positions
-def _need(t, dtype, shape, what: str):
-    """Check one tensor of the page plan and rotary calls: on the current
-    device, dense, of this type and (where given) this shape."""
-    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} must be a dense {dtype} tensor" + (f" of shape {tuple(shape)}" if shape is not None
-                                                                     else ""))
-    _on_current_device(t, what)
+def _need(t, dtype, shape, dev: int, what: str):
+    """Pointer of one tensor of the calls below, which has to be dense, of this
+    type and (where given) shape, on the current device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or (shape is not None and t.shape != shape) or \
+            not t.is_contiguous():
+        raise ValueError(f"{what} must be a dense {dtype} tensor on cuda:{dev}"
+                         + (f" of shape {tuple(shape)}" if shape is not None else "")
+                         + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _on_current_device(t, what: str):
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, not on the current CUDA device")
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle; the current stream of device `dev` for None."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def mla_page_plan(ctx_lens, new_lens, free_blocks, block_table, act_seqs, cache_index, *, S1: int, num_blocks: int,
@@ -552,19 +553,20 @@ def mla_page_plan(ctx_lens, new_lens, free_blocks, block_table, act_seqs, cache_
     i32 = torch.int32
     B, W = block_table.shape
     T = cache_index.numel()
-    io = PageIo(_need(ctx_lens, i32, (B,), "ctx_lens"),
-                None if new_lens is None else _need(new_lens, i32, (B,), "new_lens"),
-                _need(free_blocks, i32, None, "free_blocks"),
-                None if parents is None else _need(parents, i32, (B, S1), "parents"),
-                _need(block_table, i32, None, "block_table"), _need(act_seqs, i32, (B,), "act_seqs"),
-                _need(cache_index, torch.int64, (T,), "cache_index"),
-                None if positions is None else _need(positions, i32, (T,), "positions"),
-                None if seq_ids is None else _need(seq_ids, i32, (T,), "seq_ids"),
-                None if cu_seqs is None else _need(cu_seqs, i32, (B + 1,), "cu_seqs"),
-                None if tree_mask is None else _need(tree_mask, torch.int64, (T, (S1 + 63) // 64), "tree_mask"),
-                None if num_taken is None else _need(num_taken, i32, (1,), "num_taken"))
+    dev = torch.cuda.current_device()
+    io = PageIo(_need(ctx_lens, i32, (B,), dev, "ctx_lens"),
+                None if new_lens is None else _need(new_lens, i32, (B,), dev, "new_lens"),
+                _need(free_blocks, i32, None, dev, "free_blocks"),
+                None if parents is None else _need(parents, i32, (B, S1), dev, "parents"),
+                _need(block_table, i32, None, dev, "block_table"), _need(act_seqs, i32, (B,), dev, "act_seqs"),
+                _need(cache_index, torch.int64, (T,), dev, "cache_index"),
+                None if positions is None else _need(positions, i32, (T,), dev, "positions"),
+                None if seq_ids is None else _need(seq_ids, i32, (T,), dev, "seq_ids"),
+                None if cu_seqs is None else _need(cu_seqs, i32, (B + 1,), dev, "cu_seqs"),
+                None if tree_mask is None else _need(tree_mask, torch.int64, (T, (S1 + 63) // 64), dev, "tree_mask"),
+                None if num_taken is None else _need(num_taken, i32, (1,), dev, "num_taken"))
     dims = PageDims(B, S1, T, 128, num_blocks, W, free_blocks.numel())
-    st = lib.mla_page_plan(ctypes.byref(dims), ctypes.byref(io), _stream_handle(stream))
+    st = lib.mla_page_plan(dims, io, _raw_stream(stream, dev))
     if st != MLA_OK:
         raise MlaError(st, lib.mla_page_last_error().decode())
     _debug_status(page_device_status, "mla_page_plan", stream)
@@ -597,28 +599,31 @@ def mla_rope_table(positions, cos, sin, *, params: RopeParams, stream=None):
     rot_dim 64)."""
     lib = load_library()
     T, pairs = cos.shape
-    st = lib.mla_rope_table(ctypes.byref(params), T, 2 * pairs, _need(positions, torch.int32, (T,), "positions"),
-                            _need(cos, torch.float32, None, "cos"), _need(sin, torch.float32, (T, pairs), "sin"),
-                            _stream_handle(stream))
+    dev = torch.cuda.current_device()
+    st = lib.mla_rope_table(params, T, 2 * pairs, _need(positions, torch.int32, (T,), dev, "positions"),
+                            _need(cos, torch.float32, None, dev, "cos"),
+                            _need(sin, torch.float32, (T, pairs), dev, "sin"), _raw_stream(stream, dev))
     if st != MLA_OK:
         raise MlaError(st, lib.mla_rope_last_error().decode())
     _debug_status(rope_device_status, "mla_rope_table", stream)
     return cos, sin
 
 
-def _rope_tensor(x, out, rows, T: int, rot_off: int, what: str) -> RopeTensor:
+def _rope_tensor(x, out, rows, T: int, rot_off: int, dev: int, what: str) -> RopeTensor:
     out = x if out is None else out
-    if x.dim() != 3 or out.dim() != 3 or x.shape[1:] != out.shape[1:] or x.shape[0] != T or x.dtype != out.dtype:
+    xs, os_ = x.shape, out.shape
+    if len(xs) != 3 or len(os_) != 3 or xs[1:] != os_[1:] or xs[0] != T or x.dtype is not out.dtype:
         raise ValueError(f"{what} and its output must be (tokens, heads, head_dim) tensors of one type")
-    if (x.shape[2] > 1 and x.stride(2) != 1) or (out.shape[2] > 1 and out.stride(2) != 1):
+    xst, ost = x.stride(), out.stride()
+    if xs[2] > 1 and (xst[2] != 1 or ost[2] != 1):
         raise ValueError(f"{what}: the values of a head must be adjacent")
-    if rows is None and out.shape[0] != T:
+    if rows is None and os_[0] != T:
         raise ValueError(f"{what}: the output has another number of tokens")
-    _on_current_device(x, what)
-    _on_current_device(out, what + "'s output")
-    return RopeTensor(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1),
-                      None if rows is None else _need(rows, torch.int64, (T,), what + "'s rows"),
-                      out.shape[0], x.shape[1], x.shape[2], rot_off, 0)
+    if x.get_device() != dev or out.get_device() != dev:
+        raise ValueError(f"{what} and its output must be on the current device, cuda:{dev}")
+    return RopeTensor(x.data_ptr(), out.data_ptr(), xst[0], xst[1], ost[0], ost[1],
+                      None if rows is None else _need(rows, torch.int64, (T,), dev, what + "'s rows"),
+                      os_[0], xs[1], xs[2], rot_off, 0)
 
 
 def mla_rope_apply(positions, q, k=None, *, params: RopeParams, rot_dim: int, rot_off: int = 0, k_rot_off: int = 0,
@@ -640,11 +645,11 @@ def mla_rope_apply(positions, q, k=None, *, params: RopeParams, rot_dim: int, ro
     if k_rows is not None and (k is None or k_out is None):
         raise ValueError("k_rows needs k and k_out")
     dims = RopeDims(T, rot_dim, 1 if half else 0, 1 if inverse else 0, _ROPE_DTYPES[q.dtype])
-    qt = _rope_tensor(q, out, None, T, rot_off, "q")
-    kt = None if k is None else _rope_tensor(k, k_out, k_rows, T, k_rot_off, "k")
-    st = lib.mla_rope_apply(ctypes.byref(dims), ctypes.byref(params),
-                            _need(positions, torch.int32, (T,), "positions"), ctypes.byref(qt),
-                            None if kt is None else ctypes.byref(kt), _stream_handle(stream))
+    dev = torch.cuda.current_device()
+    qt = _rope_tensor(q, out, None, T, rot_off, dev, "q")
+    kt = None if k is None else _rope_tensor(k, k_out, k_rows, T, k_rot_off, dev, "k")
+    st = lib.mla_rope_apply(dims, params, _need(positions, torch.int32, (T,), dev, "positions"), qt, kt,
+                            _raw_stream(stream, dev))
     if st != MLA_OK:
         raise MlaError(st, lib.mla_rope_last_error().decode())
     _debug_status(rope_device_status, "mla_rope_apply", stream)
@@ -695,22 +700,25 @@ def mla_tree_attn_fwd(q_nope, q_rope, kv_nope, kv_rope, kv_scales, block_table, 
     int8 = dims.kv_dtype == MLA_KV_INT8
     if tree_mask is not None and tree_mask.numel() != T * ((dims.S1 + 63) // 64):
         raise ValueError("tree_mask must hold ceil(S1 / 64) words for each of the B*S1 tokens")
-    if kv_nope.shape[0] < rows or kv_rope.shape[0] < rows:
-        raise ValueError("the cache holds fewer rows than dims.num_blocks says")
-    ptrs = (_need(q_nope, bf16, (T, n_q, 512), "q_nope"), _need(q_rope, bf16, (T, n_q, 64), "q_rope"),
-            _need(kv_nope, torch.int8 if int8 else bf16, None, "kv_nope"), _need(kv_rope, bf16, None, "kv_rope"),
-            _need(kv_scales, torch.float32, (kv_nope.shape[0], 4), "kv_scales") if int8 else None,
-            _need(block_table, i32, (B, dims.max_blocks_per_seq), "block_table"),
-            _need(act_seqs, i32, (B,), "act_seqs"),
-            None if tree_lens is None else _need(tree_lens, i32, (B,), "tree_lens"),
-            None if tree_mask is None else _need(tree_mask, torch.int64, None, "tree_mask"),
-            _need(out, bf16, (T, n_q, 512), "out"), None if lse is None else _need(lse, torch.float32, (T, n_q), "lse"))
+    if kv_nope.shape[0] < rows or kv_rope.shape[0] < rows or kv_nope.shape[1:] != (512,) or kv_rope.shape[1:] != (64,):
+        raise ValueError("the cache must be (rows, 512) and (rows, 64) with at least the rows of dims.num_blocks")
+    dev = torch.cuda.current_device()
+    ptrs = (_need(q_nope, bf16, (T, n_q, 512), dev, "q_nope"), _need(q_rope, bf16, (T, n_q, 64), dev, "q_rope"),
+            _need(kv_nope, torch.int8 if int8 else bf16, None, dev, "kv_nope"),
+            _need(kv_rope, bf16, None, dev, "kv_rope"),
+            _need(kv_scales, torch.float32, (kv_nope.shape[0], 4), dev, "kv_scales") if int8 else None,
+            _need(block_table, i32, (B, dims.max_blocks_per_seq), dev, "block_table"),
+            _need(act_seqs, i32, (B,), dev, "act_seqs"),
+            None if tree_lens is None else _need(tree_lens, i32, (B,), dev, "tree_lens"),
+            None if tree_mask is None else _need(tree_mask, torch.int64, None, dev, "tree_mask"),
+            _need(out, bf16, (T, n_q, 512), dev, "out"),
+            None if lse is None else _need(lse, torch.float32, (T, n_q), dev, "lse"))
     if softmax_scale is None:
         softmax_scale = (dims.d_nope + dims.d_rope) ** -0.5
-    nbytes = workspace.numel() * workspace.element_size()
-    _on_current_device(workspace, "workspace")
-    st = lib.mla_tree_attn_fwd(ctypes.byref(dims), *ptrs, softmax_scale, workspace.data_ptr(), nbytes,
-                               _stream_handle(stream))
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a dense tensor on cuda:{dev}")
+    st = lib.mla_tree_attn_fwd(dims, *ptrs, softmax_scale, workspace.data_ptr(), workspace.nbytes,
+                               _raw_stream(stream, dev))
     if st != MLA_OK:
         raise MlaError(st, lib.mla_tree_last_error().decode())
     _debug_status(tree_device_status, "mla_tree_attn_fwd", stream)

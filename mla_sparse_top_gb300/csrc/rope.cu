@@ -53,17 +53,25 @@ struct TableParams {
   int T, pairs;
 };
 
+// A thread keeps one pair and walks over tokens, four at a time.
 __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ TableParams p) {
-  __shared__ uint64_t turn[kMaxPairs];
-  if (threadIdx.x < p.pairs) turn[threadIdx.x] = p.f.turn[threadIdx.x];
-  __syncthreads();
-  const int64_t n = static_cast<int64_t>(p.T) * p.pairs;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; e < n;
-       e += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int t = static_cast<int>(e / p.pairs), i = static_cast<int>(e - static_cast<int64_t>(t) * p.pairs);
-    const float2 v = cos_sin(__ldg(p.positions + t), turn[i], p.f.mscale);
-    p.cos[e] = v.x;
-    p.sin[e] = v.y;
+  const int rows = kThreads / p.pairs;
+  const int r = threadIdx.x / p.pairs, i = threadIdx.x - r * p.pairs;
+  if (r >= rows) return;
+  const uint64_t turn = p.f.turn[i];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * rows + r; t < p.T; t += 4 * step) {
+    int32_t pos[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) pos[u] = t + u * step < p.T ? __ldg(p.positions + t + u * step) : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (t + u * step >= p.T) break;
+      const float2 v = cos_sin(pos[u], turn, p.f.mscale);
+      const int64_t e = (t + u * step) * p.pairs + i;
+      p.cos[e] = v.x;
+      p.sin[e] = v.y;
+    }
   }
 }
 
@@ -402,9 +410,8 @@ mla_status mla_rope_table(const mla_rope_params* params, int32_t T, int32_t rot_
   p.sin = sin;
   p.T = T;
   p.pairs = rot_dim / 2;
-  const int64_t n = static_cast<int64_t>(T) * p.pairs;
-  const int64_t want = (n + mlarp::kThreads - 1) / mlarp::kThreads;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(want, 152 * 8));
+  const int rows = mlarp::kThreads / p.pairs;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((static_cast<int64_t>(T) + rows - 1) / rows, 152 * 4));
   mlarp::rope_table_kernel<<<grid, mlarp::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return rope_fail(MLA_ERR_CUDA, "rope table launch: %s", cudaGetErrorString(e));

@@ -90,7 +90,8 @@ constexpr int kQFull = kPvDone + 1;  // in CTA 0
 constexpr int kQFree = kQFull + 1;   // the segment's score MMAs are complete
 constexpr int kMax = kQFree + 1;     // [2] the four warps of rows 0-31 / 32-63 have posted
 constexpr int kFinal = kMax + 2;
-constexpr int kNumBars = kFinal + 1;
+constexpr int kLocal = kFinal + 1;  // [kSlots] a slot's bytes have landed that the producer still has to mend
+constexpr int kNumBars = kLocal + kSlots;
 constexpr int kOffTmem = kOffBars + 8 * kNumBars;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // 1024: the base is aligned by hand
@@ -326,18 +327,46 @@ struct Maps {
   CUtensorMap q_nope, q_rope, key, val, rope;
 };
 
+// fp32 pairs (one instruction for two lanes of arithmetic).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Four codes of a word times the scale, rounded to bf16: bytes enter the
 // mantissa of 2^23 + 128 + code by a byte permutation (codes biased to
 // unsigned), which is exact and cheaper than four conversions.
 __device__ __forceinline__ void dequant4(uint32_t w, float sc, uint32_t& lo, uint32_t& hi) {
   w ^= 0x80808080u;
-  const float bias = 8388736.f;  // 2^23 + 128
-  const float a = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)) - bias;
-  const float b = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)) - bias;
-  const float d = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)) - bias;
-  const float e = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)) - bias;
-  lo = pack_bf16x2(a * sc, b * sc);
-  hi = pack_bf16x2(d * sc, e * sc);
+  const uint64_t bias = pair(-8388736.f, -8388736.f), s2 = pair(sc, sc);  // 2^23 + 128
+  const uint64_t a = pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)),
+                          __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)));
+  const uint64_t b = pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)),
+                          __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)));
+  const float2 x = unpair(mul2(add2(a, bias), s2)), y = unpair(mul2(add2(b, bias), s2));
+  lo = pack_bf16x2(x.x, x.y);
+  hi = pack_bf16x2(y.x, y.y);
 }
 // NaN and infinities of a bf16 pair become zero.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -349,150 +378,169 @@ __device__ __forceinline__ uint4 finite8(uint4 v) {
   return make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
 }
 
-// Value item of a bf16 cache at the end of a sequence: 64 keys x 128 dims.
-// Rows at and beyond `rows` (unwritten, or of a bad page) are zero.
-__device__ void fill_value_bf16(const Params& p, uint32_t slot, int64_t row0, int rows, int dim0, int lane) {
-  const int unit = lane & 15, box = unit >> 3;
-#pragma unroll 8
-  for (int it = 0; it < 32; ++it) {
-    const int r = 2 * it + (lane >> 4);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rows) v = finite8(__ldg(reinterpret_cast<const uint4*>(p.kv_nope + (row0 + r) * 1024 + dim0 * 2) + unit));
-    sts16(slot + box * kChunk + r * 128 + (((unit & 7) ^ (r & 7)) << 4), v);
-  }
-}
+// One filling of a ring slot.
+struct Item {
+  int row, rows;  // first cache row (beyond the cache for a bad page), rows that exist
+  int dim0;       // first dim
+  bool value, rope;
+  int first_draft;  // rows from here on may hold what some tokens must not see (values only)
+};
 
-// INT8: 16 codes of a row become two 16-byte units.
-__device__ __forceinline__ void convert16(uint4 c, float sc, bool clean, uint4& a, uint4& b) {
-  dequant4(c.x, sc, a.x, a.y);
-  dequant4(c.y, sc, a.z, a.w);
-  dequant4(c.z, sc, b.x, b.y);
-  dequant4(c.w, sc, b.z, b.w);
-  if (clean) {
-    a = finite8(a);
-    b = finite8(b);
+// The fillings of producer warp w: items w, w + 7, w + 14, ... of the order in
+// which the MMAs take them, keys of tile t + 1 before values of tile t.
+struct Items {
+  Walk walk;
+  Segment s;
+  bool open;
+  int u, k;  // tile that the keys come from; the warp's next item, counted within the current group
+  bool values;
+  __device__ bool next(const Params& p, int rank, Item& it) {
+    while (true) {
+      if (!open) {
+        if (!walk.next(p, s)) return false;
+        open = true;
+        u = s.t0;
+        values = false;
+      }
+      const int items = values ? (u > s.t0 ? 2 * groups_of(s, u - 1) : 0) : (u < s.t1 ? kKeyItems : 0);
+      if (k < items) break;
+      k -= items;
+      if (values && ++u > s.t1) open = false;
+      values = !values;
+    }
+    const int t = values ? u - 1 : u;
+    const int lb = 2 * t + (values ? k >> 2 : rank), sub = values ? ((k >> 1) & 1) * 64 : 0;
+    const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
+    const bool ok = good(p, id);
+    it.row = (ok ? id : p.num_blocks) * kPage + sub;  // beyond the cache: TMA fills zeros
+    const int base = lb * kPage + sub;
+    it.rows = ok ? max(0, min(values ? 64 : kPage, s.act - base)) : 0;
+    it.dim0 = values ? (k & 1) * 256 + rank * 128 : 64 * k;
+    it.value = values;
+    it.rope = !values && k == 8;
+    it.first_draft = s.ctx - base;
+    k += kSlots;
+    return true;
   }
-}
+};
 
-// One item of an INT8 cache: `kRows` rows of kUnits 16-code units each, loaded
-// before the slot is free, then converted into it.
-template <int kRows, int kUnits>
-struct Int8Item {
-  static constexpr int kIts = kRows * kUnits / 32, kStep = 32 / kUnits;
-  uint4 c[kIts];
-  float sc[kIts];
-  __device__ void load(const Params& p, int64_t row0, int rows, int dim0, int lane) {
-    const int unit = lane % kUnits;
+// Half of an INT8 item: 8 rounds of 32 units of 16 codes, in flight in registers.
+struct Half {
+  uint4 c[8];
+  float sc[8];
+  __device__ void load(const Params& p, const Item& it, int half, int lane) {
+    const int us = it.value ? 3 : 2;  // units of a row: 128 or 64 codes
+    const int unit = lane & ((1 << us) - 1);
 #pragma unroll
-    for (int it = 0; it < kIts; ++it) {
-      const int r = it * kStep + lane / kUnits;
-      c[it] = make_uint4(0, 0, 0, 0);
-      sc[it] = 0.f;
-      if (r < rows) {
-        c[it] = __ldg(reinterpret_cast<const uint4*>(p.kv_nope + (row0 + r) * 512 + dim0) + unit);
-        sc[it] = __ldg(p.kv_scales + (row0 + r) * 4 + (dim0 >> 7));
+    for (int i = 0; i < 8; ++i) {
+      const int r = ((half * 8 + i) << (5 - us)) + (lane >> us);
+      c[i] = make_uint4(0, 0, 0, 0);
+      sc[i] = 0.f;
+      if (r < it.rows) {
+        const int64_t row = it.row + r;
+        c[i] = __ldg(reinterpret_cast<const uint4*>(p.kv_nope + row * 512 + it.dim0) + unit);
+        sc[i] = __ldg(p.kv_scales + row * 4 + (it.dim0 >> 7));
       }
     }
   }
-  __device__ void store(uint32_t slot, bool clean, int lane) const {
-    const int unit = lane % kUnits, box = unit >> 2, u0 = 2 * (unit & 3);
+  __device__ void store(uint32_t slot, const Item& it, int half, int lane) const {
+    const int us = it.value ? 3 : 2;
+    const int unit = lane & ((1 << us) - 1), u0 = 2 * (unit & 3);
+    slot += (unit >> 2) * kChunk;
 #pragma unroll
-    for (int it = 0; it < kIts; ++it) {
-      const int r = it * kStep + lane / kUnits;
+    for (int i = 0; i < 8; ++i) {
+      const int r = ((half * 8 + i) << (5 - us)) + (lane >> us);
       uint4 a, b;
-      convert16(c[it], sc[it], clean, a, b);
-      const uint32_t base = slot + box * (kRows * 128) + r * 128;
-      sts16(base + ((u0 ^ (r & 7)) << 4), a);
-      sts16(base + (((u0 + 1) ^ (r & 7)) << 4), b);
+      dequant4(c[i].x, sc[i], a.x, a.y);
+      dequant4(c[i].y, sc[i], a.z, a.w);
+      dequant4(c[i].z, sc[i], b.x, b.y);
+      dequant4(c[i].w, sc[i], b.z, b.w);
+      if (it.value && r >= it.first_draft) {
+        a = finite8(a);
+        b = finite8(b);
+      }
+      sts16(slot + r * 128 + ((u0 ^ (r & 7)) << 4), a);
+      sts16(slot + r * 128 + (((u0 + 1) ^ (r & 7)) << 4), b);
     }
   }
 };
 
-// Producer warp w fills ring slot w: items w, w + 7, w + 14, ... of the order
-// in which the MMAs take them (keys of tile t + 1 before values of tile t).
+// Rows of a value item (64 keys x 128 dims, bf16, in the slot) that the second
+// product must not see as they are: unwritten ones become zero, drafted ones
+// lose their NaN and infinities (0 * NaN; a token that sees such a row gets its
+// NaN through the score).
+__device__ __forceinline__ void mend_values(uint32_t slot, const Item& it, int lane) {
+  const int unit = lane & 15;
+  for (int r = max(0, min(it.first_draft, it.rows)) + (lane >> 4); r < 64; r += 2) {
+    const uint32_t at = slot + (unit >> 3) * kChunk + r * 128 + (((unit & 7) ^ (r & 7)) << 4);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < it.rows) {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+      v = finite8(v);
+    }
+    sts16(at, v);
+  }
+}
+
+// Producer warp w fills ring slot w.
 template <bool kInt8>
-__device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int w, int lane) {
+__device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, const Walk& walk, int w, int lane) {
   const uint32_t slot = c.sb + kOffRing + w * kSlotBytes;
   const uint32_t full = c.lead(kFull + w);
-  int skip = w;  // items until this warp's next one
-  uint32_t fills = 0;
-  auto take = [&](int items, int& k) {  // first item of a group that is this warp's
-    k = skip;
-    if (skip >= items) {
-      skip -= items;
-      return false;
-    }
-    return true;
-  };
-  auto done = [&](int k, int items) { skip = k - items; };  // k: the first item at or beyond `items`
+  const int rank = static_cast<int>(c.rank);
+  uint32_t fills = 0, mended = 0;
   auto free_slot = [&]() { return warp_wait(c, kEmpty + w, (fills++ & 1) ^ 1); };
   auto filled = [&]() {
     fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
     __syncwarp();
     if (lane == 0) arrive_lead(full);
   };
-  Segment s;
-  while (walk.next(p, s)) {
-    for (int u = s.t0; u <= s.t1; ++u) {
-      int k;
-      if (u < s.t1 && take(kKeyItems, k)) {
-        const int lb = 2 * u + static_cast<int>(c.rank);
-        const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
-        const bool ok = good(p, id);
-        const int row = (ok ? id : p.num_blocks) * kPage;  // beyond the cache: TMA fills zeros
-        for (; k < kKeyItems; k += kSlots) {
-          if (kInt8 && k < 8) {
-            Int8Item<128, 4> item;
-            item.load(p, static_cast<int64_t>(row), ok ? min(kPage, s.act - lb * kPage) : 0, 64 * k, lane);
-            if (!free_slot()) return;
-            item.store(slot, false, lane);
-            filled();
-          } else {
-            if (!free_slot()) return;
-            if (lane == 0) {
-              arrive_lead_tx(full, kSlotBytes);
-              if (k < 8) tma_pair(slot, &maps.key, 64 * k, row, full);
-              else tma_pair(slot, &maps.rope, 0, row, full);
-            }
-            __syncwarp();
-          }
+  Items items;
+  items.walk = walk;
+  items.open = false;
+  items.k = w;
+  Item cur, nxt;
+  bool have = items.next(p, rank, cur);
+  Half h0, h1;
+  if (kInt8 && have && !cur.rope) h0.load(p, cur, 0, lane);
+  while (have) {
+    const bool more = items.next(p, rank, nxt);
+    if (kInt8 && !cur.rope) {
+      h1.load(p, cur, 1, lane);
+      if (!free_slot()) return;
+      h0.store(slot, cur, 0, lane);
+      if (more && !nxt.rope) h0.load(p, nxt, 0, lane);
+      h1.store(slot, cur, 1, lane);
+      filled();
+    } else {
+      if (kInt8 && more && !nxt.rope) h0.load(p, nxt, 0, lane);
+      if (!free_slot()) return;
+      if (cur.value) {
+        const bool mend = cur.first_draft < 64 || cur.rows < 64;
+        const uint32_t bar = mend ? c.bar(kLocal + w) : full;
+        if (lane == 0) {
+          if (mend) mbar_arrive_expect_tx(bar, kSlotBytes);
+          else arrive_lead_tx(bar, kSlotBytes);
+          tma_pair(slot, &maps.val, cur.dim0, cur.row, bar);
+          tma_pair(slot + kChunk, &maps.val, cur.dim0 + 64, cur.row, bar);
         }
-        done(k, kKeyItems);
-      }
-      if (u > s.t0) {
-        const int t = u - 1, items = 2 * groups_of(s, t);
-        if (!take(items, k)) continue;
-        const bool edge = kTile * (t + 1) > s.ctx;  // holds drafted or unwritten rows
-        for (; k < items; k += kSlots) {
-          const int g = k >> 1, dim0 = (k & 1) * 256 + static_cast<int>(c.rank) * 128;
-          const int lb = 2 * t + (g >> 1);
-          const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
-          const bool ok = good(p, id);
-          const int row = (ok ? id : p.num_blocks) * kPage + (g & 1) * 64;
-          const int rows = ok ? min(64, s.act - lb * kPage - (g & 1) * 64) : 0;
-          if (kInt8) {
-            Int8Item<64, 8> item;
-            item.load(p, row, rows, dim0, lane);
-            if (!free_slot()) return;
-            item.store(slot, edge, lane);
-            filled();
-          } else if (edge) {
-            if (!free_slot()) return;
-            fill_value_bf16(p, slot, row, rows, dim0, lane);
-            filled();
-          } else {
-            if (!free_slot()) return;
-            if (lane == 0) {
-              arrive_lead_tx(full, kSlotBytes);
-              tma_pair(slot, &maps.val, dim0, row, full);
-              tma_pair(slot + kChunk, &maps.val, dim0 + 64, row, full);
-            }
-            __syncwarp();
-          }
+        __syncwarp();
+        if (mend) {
+          if (!warp_wait(c, kLocal + w, mended++ & 1)) return;
+          mend_values(slot, cur, lane);
+          filled();
         }
-        done(k, items);
+      } else {
+        if (lane == 0) {
+          arrive_lead_tx(full, kSlotBytes);
+          if (cur.rope) tma_pair(slot, &maps.rope, 0, cur.row, full);
+          else tma_pair(slot, &maps.key, cur.dim0, cur.row, full);
+        }
+        __syncwarp();
       }
     }
+    cur = nxt;
+    have = more;
   }
 }
 
@@ -648,6 +696,10 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
   const int part = half * 2 + sub;  // which 64 keys of a tile this thread has
   const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
   const uint32_t tO = c.tmem + lanes + kTmemO + 128 * sub;
+  // a positive scale leaves the order of scores alone: the maximum is taken of
+  // the raw ones, and the scale goes into the exponent's multiply-add
+  const bool raw = p.scale_log2 > 0.f;
+  const float mul = raw ? p.scale_log2 : 1.f;
   float* exch = reinterpret_cast<float*>(c.smem + kOffExch);
   const int words = (p.S1 + 63) >> 6;
   const int maxbar = kMax + (q & 1);
@@ -701,8 +753,10 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_lead(c.lead(kSFree + buf));
+      if (!raw) {
 #pragma unroll
-      for (int k = 0; k < 64; ++k) z[k] *= p.scale_log2;
+        for (int k = 0; k < 64; ++k) z[k] *= p.scale_log2;
+      }
       if (__any_sync(0xffffffffu, vis != ~0ull)) {
 #pragma unroll
         for (int k = 0; k < 64; ++k)
@@ -713,7 +767,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
       for (int k = 4; k < 64; ++k) mx[k & 3] = fmaxf(mx[k & 3], z[k]);
       float all[4];
       if (!share(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), all)) return;
-      const float top = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+      const float top = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])) * mul;
       // the maximum moves only when a tile exceeds it by more than 2^8: P stays
       // below 2^8 and O is rarely rescaled
       const bool grow = top > m + 8.f;
@@ -724,14 +778,18 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
       }
       const float mm = m == -INFINITY ? 0.f : m;
       uint32_t w[32];
-      float sum[2] = {0.f, 0.f};
+      uint64_t sum[2] = {0, 0};
+      const uint64_t mul_2 = pair(mul, mul), mm_2 = pair(-mm, -mm);
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
-        const float a = fast_exp2(z[2 * k] - mm), b = fast_exp2(z[2 * k + 1] - mm);
-        sum[k & 1] += a + b;
-        w[k] = pack_bf16x2(a, b);
+        float2 e = unpair(fma2(pair(z[2 * k], z[2 * k + 1]), mul_2, mm_2));
+        e.x = fast_exp2(e.x);
+        e.y = fast_exp2(e.y);
+        sum[k & 1] = add2(sum[k & 1], pair(e.x, e.y));
+        w[k] = pack_bf16x2(e.x, e.y);
       }
-      l += sum[0] + sum[1];
+      const float2 sums = unpair(add2(sum[0], sum[1]));
+      l += sums.x + sums.y;
       // P and O are free once the tile before has been multiplied
       if (tile > 0 && !warp_wait(c, kPvDone, (tile - 1) & 1)) return;
       if (t > s.t0 && __any_sync(0xffffffffu, grow)) {
@@ -841,6 +899,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(c.bar(kFull + i), 2);
       mbar_init(c.bar(kEmpty + i), 1);
+      mbar_init(c.bar(kLocal + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(c.bar(kSFull + i), 1);
