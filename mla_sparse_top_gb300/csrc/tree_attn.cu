@@ -60,29 +60,46 @@ namespace mlatree {
 
 using namespace mlasp;
 
-constexpr int kThreads = 512;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kProducerWarp0 = 8;
-constexpr int kSlots = 7;  // ring slots, one producer warp each
-constexpr int kMmaWarp = 15;
-static_assert(kProducerWarp0 + kSlots == kMmaWarp && kMmaWarp * 32 + 32 == kThreads, "roles");
+// bf16: seven ring slots, a producer warp each.  INT8: four slots, filled from
+// five raw slots by two groups of four converter warps, and a load warp.
+template <bool kInt8>
+struct Conf {
+  static constexpr int kSlots = kInt8 ? 4 : 7;
+  static constexpr int kProducers = kInt8 ? 8 : 7;
+  static constexpr int kMmaWarp = kProducerWarp0 + kProducers;
+  static constexpr int kThreads = (kMmaWarp + (kInt8 ? 2 : 1)) * 32;
+  static constexpr int kFillers = kInt8 ? 4 : 1;  // warps of a CTA that fill one slot together
+  // INT8: the softmax warps take registers over from the converters
+  static constexpr int kRegs = kInt8 ? 96 : 128, kSoftmaxRegs = 120, kConvertRegs = 72;
+  static_assert(256 * kSoftmaxRegs + 256 * kConvertRegs <= 512 * 96, "register budget");
+};
+constexpr int kRawSlots = 5;
+constexpr int kMaxThreads = 576;
+static_assert(Conf<false>::kThreads == 512 && Conf<true>::kThreads == kMaxThreads, "roles");
 
 constexpr int kRowBlock = 128;
 constexpr int kTile = 256;
 constexpr int kPage = 128;
 constexpr int kKeyItems = 9;  // 64-dim slices of 576
 constexpr int kSlotBytes = 16384;
+constexpr int kRawCodes = 8192;                 // 128 keys x 64 codes or 64 keys x 128 codes
+constexpr int kRawBytes = kRawCodes + 128 * 16;  // and the rows' four scales
 constexpr int kChunk = 8192;  // 64 rows of 128 bytes
 constexpr int kOffQ = 0;
 constexpr int kOffP = kOffQ + kKeyItems * kChunk;
 constexpr int kOffRing = kOffP + 4 * kChunk;
-constexpr int kOffExch = kOffRing + kSlots * kSlotBytes;  // float [2][4][64]
-constexpr int kOffScan = kOffExch + 2048;                 // int64 [kThreads / 32]
-constexpr int kOffWalk = kOffScan + 16 * 8;               // int64 first sequence, offset, tiles of the share, total
+constexpr int kOffRaw = kOffRing + Conf<true>::kSlots * kSlotBytes;  // INT8 only
+constexpr int kOffExch = kOffRaw + kRawSlots * kRawBytes;            // float [2][4][64]
+static_assert(kOffExch >= kOffRing + Conf<false>::kSlots * kSlotBytes, "ring");
+constexpr int kOffScan = kOffExch + 2048;           // int64 [warps]
+constexpr int kOffWalk = kOffScan + kMaxThreads / 32 * 8;               // int64 first sequence, offset, tiles of the share, total
 constexpr int kOffBars = kOffWalk + 32;
-constexpr int kFull = 0;                // [kSlots], in CTA 0: both CTAs have filled the slot
-constexpr int kEmpty = kFull + kSlots;  // [kSlots] the MMAs that read the slot are complete
-constexpr int kSFull = kEmpty + kSlots;  // [2]
+constexpr int kMaxSlots = 7;
+constexpr int kFull = 0;                   // [kMaxSlots], in CTA 0: both CTAs have filled the slot
+constexpr int kEmpty = kFull + kMaxSlots;  // [kMaxSlots] the MMAs that read the slot are complete
+constexpr int kSFull = kEmpty + kMaxSlots;  // [2]
 constexpr int kSFree = kSFull + 2;       // [2], in CTA 0: the softmax warps have read S
 constexpr int kPReady = kSFree + 2;      // in CTA 0: P is written, O may be added to
 constexpr int kPvDone = kPReady + 1;
@@ -90,8 +107,10 @@ constexpr int kQFull = kPvDone + 1;  // in CTA 0
 constexpr int kQFree = kQFull + 1;   // the segment's score MMAs are complete
 constexpr int kMax = kQFree + 1;     // [2] the four warps of rows 0-31 / 32-63 have posted
 constexpr int kFinal = kMax + 2;
-constexpr int kLocal = kFinal + 1;  // [kSlots] a slot's bytes have landed that the producer still has to mend
-constexpr int kNumBars = kLocal + kSlots;
+constexpr int kLocal = kFinal + 1;  // [kMaxSlots] bf16: a slot's bytes have landed that the producer still has to mend
+constexpr int kRawFull = kLocal + kMaxSlots;     // [kRawSlots] INT8: codes and scales have landed
+constexpr int kRawEmpty = kRawFull + kRawSlots;  // [kRawSlots] INT8: they have been read
+constexpr int kNumBars = kRawEmpty + kRawSlots;
 constexpr int kOffTmem = kOffBars + 8 * kNumBars;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // 1024: the base is aligned by hand
@@ -119,8 +138,8 @@ struct Params {
   float* parts;   // [clusters][2][2 CTAs][kPartFloats]
   int4* records;  // [clusters] what the merge has to do for a row block that starts in this cluster
   int B, S1, n_q, W, num_blocks;
-  int rows, blocks;  // rows of a sequence, its row blocks
-  int team, teams, passes;  // clusters of a team, teams, row-block groups of a sequence
+  int rows;         // rows of a sequence
+  int team, teams;  // clusters of a team, teams
   float scale_log2;
   int out32;
   unsigned long long wait_ns;
@@ -128,10 +147,11 @@ struct Params {
 
 // ------------------------------------------------------------------ schedule
 struct Seq {
-  int act, n;        // cached positions within the table, drafted tokens
-  int tiles, live;   // key tiles, passes that hold a drafted token
-  bool cut_table;    // positions beyond the table
-  __device__ int64_t len(const Params& p) const { return static_cast<int64_t>(live) * tiles + (p.passes - live); }
+  int act, n;         // cached positions, drafted tokens
+  int blocks, tiles;  // row blocks that hold a drafted token, key tiles
+  bool cut_table;     // positions beyond the table
+  // tiles that a team goes through: passes over groups of row blocks
+  __device__ int64_t len(const Params& p) const { return static_cast<int64_t>((blocks + p.team - 1) / p.team) * tiles; }
 };
 
 __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
@@ -142,15 +162,14 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
   const int in_table = min(s.act, p.W * kPage);
   s.cut_table = in_table < s.act;
   s.tiles = max(1, (in_table + kTile - 1) / kTile);
-  const int64_t group = static_cast<int64_t>(p.team) * kRowBlock;
-  s.live = static_cast<int>((static_cast<int64_t>(s.n) * p.n_q + group - 1) / group);
+  s.blocks = static_cast<int>((static_cast<int64_t>(s.n) * p.n_q + kRowBlock - 1) / kRowBlock);
   return s;
 }
 
 struct Segment {
   int b, rb;          // sequence, row block
   int t0, t1, tiles;  // tiles [t0, t1) of the row block's `tiles`
-  int act, n;         // 0 for a block of padding rows
+  int act, n;
   int ctx;            // first drafted position, may be negative
   int64_t first;      // stream position of the row block's first tile
 };
@@ -171,21 +190,19 @@ struct Walk {
         off = 0;
         continue;
       }
-      const int64_t keys = static_cast<int64_t>(q.live) * q.tiles;
-      const bool live = off < keys;
-      const int pass = live ? static_cast<int>(off / q.tiles) : static_cast<int>(q.live + (off - keys));
+      const int pass = static_cast<int>(off / q.tiles);
       s.b = b;
-      s.tiles = live ? q.tiles : 1;
-      s.t0 = live ? static_cast<int>(off - static_cast<int64_t>(pass) * q.tiles) : 0;
+      s.tiles = q.tiles;
+      s.t0 = static_cast<int>(off - static_cast<int64_t>(pass) * q.tiles);
       s.t1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.t0 + left));
       s.first = base + off - s.t0;
-      s.act = live ? q.act : 0;
-      s.n = live ? q.n : 0;
+      s.act = q.act;
+      s.n = q.n;
       s.ctx = s.act - s.n;
       s.rb = pass * p.team + member;
       off += s.t1 - s.t0;
       left -= s.t1 - s.t0;
-      if (s.rb < p.blocks) return true;
+      if (s.rb < q.blocks) return true;
     }
     return false;
   }
@@ -253,7 +270,8 @@ __device__ __forceinline__ int groups_of(const Segment& s, int t) {
   return min(4, max(1, (s.act - kTile * t + 63) >> 6));
 }
 
-// Total of the stream and this team's start, found by the whole block.
+// Sum over the threads before this one, and over the whole block.
+template <int kThreads>
 __device__ __forceinline__ int64_t block_sum_scan(const Ctx& c, int64_t v, int64_t& total) {
   int64_t* part = reinterpret_cast<int64_t*>(c.smem + kOffScan);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -281,6 +299,7 @@ __device__ __forceinline__ int teams_of(const Params& p, int64_t total) {
 }
 
 // The walk of cluster `cid`; false when it has nothing to do.
+template <int kThreads>
 __device__ bool start_walk(const Params& p, const Ctx& c, int cid, Walk& w, int64_t& total, int& teams) {
   int64_t* at = reinterpret_cast<int64_t*>(c.smem + kOffWalk);
   const int tid = threadIdx.x;
@@ -291,7 +310,7 @@ __device__ bool start_walk(const Params& p, const Ctx& c, int cid, Walk& w, int6
     len = b < p.B ? load_seq(p, b).len(p) : 0;
     mine += len;
   }
-  pre = block_sum_scan(c, mine, total);
+  pre = block_sum_scan<kThreads>(c, mine, total);
   teams = teams_of(p, total);
   const int team = cid / p.team;
   const bool busy = team < teams;
@@ -303,7 +322,7 @@ __device__ bool start_walk(const Params& p, const Ctx& c, int cid, Walk& w, int6
       int64_t sum = total;
       if (chunks > 1) {
         len = b < p.B ? load_seq(p, b).len(p) : 0;
-        pre = carry + block_sum_scan(c, len, sum);
+        pre = carry + block_sum_scan<kThreads>(c, len, sum);
       }
       if (b < p.B && start >= pre && start < pre + len) {
         at[0] = b;
@@ -324,7 +343,8 @@ __device__ bool start_walk(const Params& p, const Ctx& c, int cid, Walk& w, int6
 
 // ------------------------------------------------------------------ producers
 struct Maps {
-  CUtensorMap q_nope, q_rope, key, val, rope;
+  CUtensorMap q_nope, q_rope, key, val, rope;  // key, val: of bf16 rows, or of codes
+  CUtensorMap key_scale, val_scale;            // INT8
 };
 
 // fp32 pairs (one instruction for two lanes of arithmetic).
@@ -386,14 +406,15 @@ struct Item {
   int first_draft;  // rows from here on may hold what some tokens must not see (values only)
 };
 
-// The fillings of producer warp w: items w, w + 7, w + 14, ... of the order in
-// which the MMAs take them, keys of tile t + 1 before values of tile t.
+// The fillings in the order in which the MMAs take them, keys of tile t + 1
+// before values of tile t: all of them, or every kStride-th from item k on.
+template <int kStride, bool kPages>
 struct Items {
   Walk walk;
   Segment s;
-  bool open;
-  int u, k;  // tile that the keys come from; the warp's next item, counted within the current group
-  bool values;
+  bool open = false, values = false;
+  int u = 0, k;  // tile that the keys come from; the next item, counted within the current group
+  __device__ Items(const Walk& from, int first) : walk(from), k(first) {}
   __device__ bool next(const Params& p, int rank, Item& it) {
     while (true) {
       if (!open) {
@@ -410,58 +431,20 @@ struct Items {
     }
     const int t = values ? u - 1 : u;
     const int lb = 2 * t + (values ? k >> 2 : rank), sub = values ? ((k >> 1) & 1) * 64 : 0;
-    const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
-    const bool ok = good(p, id);
-    it.row = (ok ? id : p.num_blocks) * kPage + sub;  // beyond the cache: TMA fills zeros
     const int base = lb * kPage + sub;
-    it.rows = ok ? max(0, min(values ? 64 : kPage, s.act - base)) : 0;
+    it.rows = max(0, min(values ? 64 : kPage, s.act - base));
+    if constexpr (kPages) {
+      const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
+      const bool ok = good(p, id);
+      it.row = (ok ? id : p.num_blocks) * kPage + sub;  // beyond the cache: TMA fills zeros
+      if (!ok) it.rows = 0;
+    }
     it.dim0 = values ? (k & 1) * 256 + rank * 128 : 64 * k;
     it.value = values;
     it.rope = !values && k == 8;
     it.first_draft = s.ctx - base;
-    k += kSlots;
+    k += kStride;
     return true;
-  }
-};
-
-// Half of an INT8 item: 8 rounds of 32 units of 16 codes, in flight in registers.
-struct Half {
-  uint4 c[8];
-  float sc[8];
-  __device__ void load(const Params& p, const Item& it, int half, int lane) {
-    const int us = it.value ? 3 : 2;  // units of a row: 128 or 64 codes
-    const int unit = lane & ((1 << us) - 1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = ((half * 8 + i) << (5 - us)) + (lane >> us);
-      c[i] = make_uint4(0, 0, 0, 0);
-      sc[i] = 0.f;
-      if (r < it.rows) {
-        const int64_t row = it.row + r;
-        c[i] = __ldg(reinterpret_cast<const uint4*>(p.kv_nope + row * 512 + it.dim0) + unit);
-        sc[i] = __ldg(p.kv_scales + row * 4 + (it.dim0 >> 7));
-      }
-    }
-  }
-  __device__ void store(uint32_t slot, const Item& it, int half, int lane) const {
-    const int us = it.value ? 3 : 2;
-    const int unit = lane & ((1 << us) - 1), u0 = 2 * (unit & 3);
-    slot += (unit >> 2) * kChunk;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = ((half * 8 + i) << (5 - us)) + (lane >> us);
-      uint4 a, b;
-      dequant4(c[i].x, sc[i], a.x, a.y);
-      dequant4(c[i].y, sc[i], a.z, a.w);
-      dequant4(c[i].z, sc[i], b.x, b.y);
-      dequant4(c[i].w, sc[i], b.z, b.w);
-      if (it.value && r >= it.first_draft) {
-        a = finite8(a);
-        b = finite8(b);
-      }
-      sts16(slot + r * 128 + ((u0 ^ (r & 7)) << 4), a);
-      sts16(slot + r * 128 + (((u0 + 1) ^ (r & 7)) << 4), b);
-    }
   }
 };
 
@@ -482,65 +465,152 @@ __device__ __forceinline__ void mend_values(uint32_t slot, const Item& it, int l
   }
 }
 
-// Producer warp w fills ring slot w.
-template <bool kInt8>
+// bf16: producer warp w fills ring slot w.
 __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, const Walk& walk, int w, int lane) {
+  constexpr int kSlots = Conf<false>::kSlots;
   const uint32_t slot = c.sb + kOffRing + w * kSlotBytes;
   const uint32_t full = c.lead(kFull + w);
   const int rank = static_cast<int>(c.rank);
   uint32_t fills = 0, mended = 0;
-  auto free_slot = [&]() { return warp_wait(c, kEmpty + w, (fills++ & 1) ^ 1); };
-  auto filled = [&]() {
-    fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
-    __syncwarp();
-    if (lane == 0) arrive_lead(full);
-  };
-  Items items;
-  items.walk = walk;
-  items.open = false;
-  items.k = w;
+  Items<kSlots, true> items(walk, w);
   Item cur, nxt;
   bool have = items.next(p, rank, cur);
-  Half h0, h1;
-  if (kInt8 && have && !cur.rope) h0.load(p, cur, 0, lane);
+  while (have) {
+    const bool more = items.next(p, rank, nxt);  // its table entry is on its way while this one waits
+    if (!warp_wait(c, kEmpty + w, (fills++ & 1) ^ 1)) return;
+    if (cur.value) {
+      const bool mend = cur.first_draft < 64 || cur.rows < 64;
+      const uint32_t bar = mend ? c.bar(kLocal + w) : full;
+      if (lane == 0) {
+        if (mend) mbar_arrive_expect_tx(bar, kSlotBytes);
+        else arrive_lead_tx(bar, kSlotBytes);
+        tma_pair(slot, &maps.val, cur.dim0, cur.row, bar);
+        tma_pair(slot + kChunk, &maps.val, cur.dim0 + 64, cur.row, bar);
+      }
+      __syncwarp();
+      if (mend) {
+        if (!warp_wait(c, kLocal + w, mended++ & 1)) return;
+        mend_values(slot, cur, lane);
+        fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
+        __syncwarp();
+        if (lane == 0) arrive_lead(full);
+      }
+    } else {
+      if (lane == 0) {
+        arrive_lead_tx(full, kSlotBytes);
+        if (cur.rope) tma_pair(slot, &maps.rope, 0, cur.row, full);
+        else tma_pair(slot, &maps.key, cur.dim0, cur.row, full);
+      }
+      __syncwarp();
+    }
+    cur = nxt;
+    have = more;
+  }
+}
+
+// INT8: one warp requests the codes and scales of every latent item.
+__device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, const Walk& walk, int lane) {
+  const int rank = static_cast<int>(c.rank);
+  Items<1, true> items(walk, 0);
+  Item cur, nxt;
+  int slot = 0;
+  uint32_t phase = 1;
+  bool have = items.next(p, rank, cur);
   while (have) {
     const bool more = items.next(p, rank, nxt);
-    if (kInt8 && !cur.rope) {
-      h1.load(p, cur, 1, lane);
-      if (!free_slot()) return;
-      h0.store(slot, cur, 0, lane);
-      if (more && !nxt.rope) h0.load(p, nxt, 0, lane);
-      h1.store(slot, cur, 1, lane);
-      filled();
-    } else {
-      if (kInt8 && more && !nxt.rope) h0.load(p, nxt, 0, lane);
-      if (!free_slot()) return;
-      if (cur.value) {
-        const bool mend = cur.first_draft < 64 || cur.rows < 64;
-        const uint32_t bar = mend ? c.bar(kLocal + w) : full;
-        if (lane == 0) {
-          if (mend) mbar_arrive_expect_tx(bar, kSlotBytes);
-          else arrive_lead_tx(bar, kSlotBytes);
-          tma_pair(slot, &maps.val, cur.dim0, cur.row, bar);
-          tma_pair(slot + kChunk, &maps.val, cur.dim0 + 64, cur.row, bar);
-        }
-        __syncwarp();
-        if (mend) {
-          if (!warp_wait(c, kLocal + w, mended++ & 1)) return;
-          mend_values(slot, cur, lane);
-          filled();
-        }
-      } else {
-        if (lane == 0) {
-          arrive_lead_tx(full, kSlotBytes);
-          if (cur.rope) tma_pair(slot, &maps.rope, 0, cur.row, full);
-          else tma_pair(slot, &maps.key, cur.dim0, cur.row, full);
-        }
-        __syncwarp();
+    if (!cur.rope) {
+      if (!warp_wait(c, kRawEmpty + slot, phase)) return;
+      if (lane == 0) {
+        const uint32_t bar = c.bar(kRawFull + slot), dst = c.sb + kOffRaw + slot * kRawBytes;
+        mbar_arrive_expect_tx(bar, kRawCodes + (cur.value ? 64 : 128) * 16);
+        tma_pair(dst, cur.value ? &maps.val : &maps.key, cur.dim0, cur.row, bar);
+        tma_pair(dst + kRawCodes, cur.value ? &maps.val_scale : &maps.key_scale, 0, cur.row, bar);
+      }
+      __syncwarp();
+      if (++slot == kRawSlots) {
+        slot = 0;
+        phase ^= 1;
       }
     }
     cur = nxt;
     have = more;
+  }
+}
+
+// INT8: converter warp w of group w / 4 turns a quarter of every other item
+// into bf16, 16 codes of a lane at a time; codes lie as TMA left them, row by
+// row, so a warp reads 512 adjacent bytes.
+__device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, const Walk& walk, int w, int lane) {
+  constexpr int kSlots = Conf<true>::kSlots;
+  const int rank = static_cast<int>(c.rank), group = w >> 2, quarter = w & 3;
+  Items<1, false> items(walk, 0);
+  Item it;
+  int raw = 0, i = 0;
+  uint32_t raw_phase = 0;
+  for (; items.next(p, rank, it); ++i) {
+    const int slot = i % kSlots;
+    const bool mine = (i & 1) == group;
+    const uint32_t dst0 = c.sb + kOffRing + slot * kSlotBytes, full = c.lead(kFull + slot);
+    if (it.rope) {
+      if (mine) {
+        if (!warp_wait(c, kEmpty + slot, ((i / kSlots) & 1) ^ 1)) return;
+        if (lane == 0) {
+          if (quarter == 0) {
+            const int lb = (items.u) * 2 + rank;
+            const int id = lb * kPage < items.s.act ? page_id(p, items.s.b, lb) : -1;
+            arrive_lead_tx(full, kSlotBytes);
+            tma_pair(dst0, &maps.rope, 0, (good(p, id) ? id : p.num_blocks) * kPage, full);
+          } else {
+            arrive_lead(full);
+          }
+        }
+        __syncwarp();
+      }
+      continue;
+    }
+    if (mine) {
+      if (!warp_wait(c, kRawFull + raw, raw_phase)) return;
+      const uint32_t src = c.sb + kOffRaw + raw * kRawBytes;
+      const int us = it.value ? 3 : 2;  // log2 of a row's units: 128 or 64 codes
+      const uint32_t scale_at = src + kRawCodes + 4 * (it.dim0 >> 7);
+      uint4 v[4];
+      float sc[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int unit = (quarter * 4 + k) * 32 + lane;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(src + unit * 16));
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc[k]) : "r"(scale_at + (unit >> us) * 16));
+      }
+      if (!warp_wait(c, kEmpty + slot, ((i / kSlots) & 1) ^ 1)) return;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int unit = (quarter * 4 + k) * 32 + lane;
+        const int r = unit >> us, col = unit & ((1 << us) - 1), u0 = 2 * (col & 3);
+        uint4 a, b;
+        dequant4(v[k].x, sc[k], a.x, a.y);
+        dequant4(v[k].y, sc[k], a.z, a.w);
+        dequant4(v[k].z, sc[k], b.x, b.y);
+        dequant4(v[k].w, sc[k], b.z, b.w);
+        if (it.value && r >= it.first_draft) {
+          a = r < it.rows ? finite8(a) : make_uint4(0, 0, 0, 0);
+          b = r < it.rows ? finite8(b) : make_uint4(0, 0, 0, 0);
+        }
+        const uint32_t dst = dst0 + (col >> 2) * kChunk + r * 128;
+        sts16(dst + ((u0 ^ (r & 7)) << 4), a);
+        sts16(dst + (((u0 + 1) ^ (r & 7)) << 4), b);
+      }
+      fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
+      __syncwarp();
+      if (lane == 0) {
+        arrive_lead(full);
+        mbar_arrive(c.bar(kRawEmpty + raw));
+      }
+    }
+    if (++raw == kRawSlots) {
+      raw = 0;
+      raw_phase ^= 1;
+    }
   }
 }
 
@@ -560,6 +630,7 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 // warp stays converged, and what steers it (tile counts, outcomes of waits) is
 // made uniform, so that descriptors and addresses live in uniform registers: a
 // ring slot's four MMAs take 259 clocks to run and have to be issued in less.
+template <int kSlots>
 __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk) {
   constexpr uint32_t idesc_s = make_idesc_f16(128, 256, 1, 0, 0);  // A, B K-major
   constexpr uint32_t idesc_v = make_idesc_f16(128, 256, 1, 0, 1);  // B MN-major
@@ -882,8 +953,9 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
 }
 
 template <bool kInt8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThreads, 1)
     tree_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  using K = Conf<kInt8>;
   extern __shared__ uint8_t raw[];
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   Ctx c;
@@ -896,8 +968,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     *c.abort = 0u;
     if (c.rank == 0) p.records[cid] = make_int4(0, 0, 0, 0);  // nothing to merge, until this thread finds a cut
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(c.bar(kFull + i), 2);
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(c.bar(kRawFull + i), 1);
+      mbar_init(c.bar(kRawEmpty + i), K::kFillers);
+    }
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(c.bar(kFull + i), 2 * K::kFillers);
       mbar_init(c.bar(kEmpty + i), 1);
       mbar_init(c.bar(kLocal + i), 1);
     }
@@ -913,7 +989,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(c.bar(kFinal), 1);
     fence_mbarrier_init_cluster();
   }
-  if (warp == kMmaWarp) {
+  if (warp == K::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
                  :: "r"(c.sb + kOffTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -921,7 +997,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Walk walk;
   int64_t total;
   int teams;
-  const bool busy = start_walk(p, c, cid, walk, total, teams);
+  const bool busy = start_walk<K::kThreads>(p, c, cid, walk, total, teams);
   tc_fence_before();
   cluster_arrive();
   cluster_wait();
@@ -930,11 +1006,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (busy) {
     if (warp < kSoftmaxWarps) {
+      if constexpr (kInt8) regs_increase<K::kSoftmaxRegs>();
       softmax_role(p, c, walk, cid, teams, total, warp, lane);
-    } else if (warp < kMmaWarp) {
-      producer_role<kInt8>(p, c, maps, walk, warp - kProducerWarp0, lane);
+    } else if (warp < K::kMmaWarp) {
+      if constexpr (kInt8) {
+        regs_decrease<K::kConvertRegs>();
+        convert_role(p, c, maps, walk, warp - kProducerWarp0, lane);
+      } else {
+        producer_role(p, c, maps, walk, warp - kProducerWarp0, lane);
+      }
+    } else if (warp == K::kMmaWarp) {
+      mma_role<K::kSlots>(p, c, maps, walk);
     } else {
-      mma_role(p, c, maps, walk);
+      if constexpr (kInt8) raw_load_role(p, c, maps, walk, lane);
     }
   }
   if (tid == 0) {  // positions beyond the table, found by the cluster that owns the sequence's number
@@ -944,6 +1028,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       beyond = beyond || (q.cut_table && q.n > 0);
     }
     if (beyond) atomicOr(&g_tree_status, MLA_DEVICE_BAD_BLOCK);
+  }
+  if (p.tree_lens != nullptr) {  // padding tokens of row blocks that nobody works on
+    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.B) * p.S1; t += gridDim.x) {
+      const int b = static_cast<int>(t / p.S1), r0 = static_cast<int>(t - static_cast<int64_t>(b) * p.S1) * p.n_q;
+      const int done = load_seq(p, b).blocks * kRowBlock;
+      for (int r = max(r0, done) + (tid >> 5); r < r0 + p.n_q; r += K::kThreads / 32) {
+        const int64_t row = static_cast<int64_t>(b) * p.rows + r;
+        for (int k = lane; k < 64; k += 32) reinterpret_cast<uint4*>(p.out + row * 512)[k] = make_uint4(0, 0, 0, 0);
+        if (lane == 0 && p.lse != nullptr) p.lse[row] = -INFINITY;
+      }
+    }
   }
 
   tc_fence_before();
@@ -959,7 +1054,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_arrive();
   cluster_wait();
   tc_fence_after();
-  if (warp == kMmaWarp)
+  if (warp == K::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(c.tmem) : "memory");
   cluster_arrive();
   cluster_wait();
@@ -1028,17 +1123,22 @@ Device g_dev[kMaxDevices];
 std::mutex g_lock;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-// Clusters of a team: as many of a sequence's row blocks side by side as keep
-// the most clusters busy (whole teams, whole passes); one row block at a time
-// would read every key once per row block, which costs about 1.4 x where the
-// cache is larger than L2.
-inline int team_size(int blocks, int clusters) {
+// Clusters of a team, for sequences of up to `blocks` row blocks: as many side
+// by side as keep the most clusters busy, counted in whole teams and whole
+// passes (where drafts differ in size, on average over all sizes).  Row blocks
+// one at a time would read every key once per row block, which costs about 1.4
+// x where the cache is larger than L2, two at a time about 1.05 x.
+inline int team_size(int blocks, int clusters, bool ragged) {
   int best = 1;
   double least = 1e30;
   for (int g = 1; g <= std::min(blocks, clusters); ++g) {
-    const double passes = (blocks + g - 1) / g;
-    const double idle = passes * g / blocks * clusters / (clusters / g * g);
-    const double cost = idle * (g == 1 && blocks > 1 ? 1.4 : 1.0);
+    double taken = 0, used = 0;
+    for (int n = ragged ? 1 : blocks; n <= blocks; n += std::max(1, blocks / 64)) {
+      taken += static_cast<double>((n + g - 1) / g) * g;
+      used += n;
+    }
+    const double reads = blocks == 1 || g > 2 ? 1.0 : (g == 1 ? 1.4 : 1.05);
+    const double cost = taken / used * clusters / (clusters / g * g) * reads;
     if (cost <= least + 1e-9) {
       least = cost;
       best = g;
@@ -1051,18 +1151,18 @@ struct Plan {
   int rows, blocks, team, teams, passes, clusters;
   size_t records_at, bytes;
 };
-inline Plan plan_of(const mla_dims& d, int clusters) {
+inline Plan plan_of(const mla_dims& d, int clusters, bool ragged) {
   Plan s;
   s.rows = d.S1 * d.n_q;
   s.blocks = static_cast<int>((static_cast<int64_t>(s.rows) + kRowBlock - 1) / kRowBlock);
-  s.team = team_size(s.blocks, clusters);
+  s.team = team_size(s.blocks, clusters, ragged);
   s.passes = (s.blocks + s.team - 1) / s.team;
   // no more teams than shares of kMinTiles in the longest possible stream
   const int64_t tiles = (static_cast<int64_t>(d.max_blocks_per_seq) + 1) / 2;
   auto most = [&](int64_t passes) { return std::max<int64_t>(1, d.B * passes * tiles / kMinTiles); };
   s.teams = static_cast<int>(std::min<int64_t>(clusters / s.team, most(s.passes)));
   s.clusters = s.team * s.teams;
-  // the workspace has room for the schedule of any device
+  // the workspace has room for the schedule of any device and any drafts
   const int64_t room = std::min<int64_t>(kMaxClusters, most(s.blocks) * s.blocks);
   s.records_at = static_cast<size_t>(room) * 4 * kPartFloats * sizeof(float);
   s.bytes = s.records_at + static_cast<size_t>(room) * sizeof(int4);
@@ -1115,6 +1215,10 @@ mla_status prepare_kernel(mlatree::Device& dev) {
   using namespace mlatree;
   TREE_CUDA(cudaFuncSetAttribute(tree_attn_kernel<kInt8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
             "kernel set-up");
+  cudaFuncAttributes fa;
+  TREE_CUDA(cudaFuncGetAttributes(&fa, tree_attn_kernel<kInt8>), "kernel attributes");
+  if (fa.numRegs < Conf<kInt8>::kRegs && kInt8)  // the registers that the warpgroups divide
+    return tree_fail(MLA_ERR_CUDA, "the kernel was built with %d registers", fa.numRegs);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1122,7 +1226,7 @@ mla_status prepare_kernel(mlatree::Device& dev) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Conf<kInt8>::kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -1152,16 +1256,21 @@ mla_status init_device(mlatree::Device& dev) {
   return st;
 }
 
-// bf16 [rows, cols] in boxes of 64 columns x `box` rows, 128-byte swizzle.
-mla_status tmap(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int box, const char* what) {
+// [rows, cols] in boxes of box_cols x box_rows.
+mla_status tmap(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, int64_t cols, int64_t rows,
+                int box_cols, int box_rows, CUtensorMapSwizzle swizzle, const char* what) {
   const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(cols) * 2};
-  const cuuint32_t bx[2] = {64, static_cast<cuuint32_t>(box)}, es[2] = {1, 1};
-  const CUresult r = mlatree::g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, stride, bx,
-                                       es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(cols) * size};
+  const cuuint32_t bx[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+  const CUresult r = mlatree::g_encode(m, type, 2, const_cast<void*>(base), dim, stride, bx, es,
+                                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return tree_fail(MLA_ERR_CUDA, "tensor map of %s: error %d", what, static_cast<int>(r));
   return MLA_OK;
+}
+// An MMA operand: bf16 in boxes of 64 columns, 128-byte swizzle.
+mla_status tmap_bf16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int box_rows, const char* what) {
+  return tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 
 }  // namespace
@@ -1171,7 +1280,7 @@ extern "C" {
 size_t mla_tree_workspace_bytes(const mla_dims* dims) {
   g_tree_error[0] = '\0';
   if (dims == nullptr || check_dims(*dims) != MLA_OK) return 0;
-  return mlatree::plan_of(*dims, mlatree::kMaxClusters).bytes;
+  return mlatree::plan_of(*dims, mlatree::kMaxClusters, false).bytes;
 }
 
 mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const void* q_rope, const void* kv_nope,
@@ -1194,7 +1303,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   if (!aligned(block_table, 4) || !aligned(act_seqs, 4) || !aligned(tree_lens, 4) || !aligned(tree_mask, 8) ||
       !aligned(lse, 4) || !aligned(workspace, 256))
     return tree_fail(MLA_ERR_ALIGN, "workspace 256-byte, tree_mask 8-byte, the int32 tensors and lse 4-byte aligned");
-  const size_t need = mlatree::plan_of(d, mlatree::kMaxClusters).bytes;  // does not depend on the device
+  const size_t need = mlatree::plan_of(d, mlatree::kMaxClusters, false).bytes;  // of any schedule
   if (workspace_bytes < need) return tree_fail(MLA_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   int dev = 0;
   TREE_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
@@ -1206,7 +1315,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
     if (ist != MLA_OK) return ist;
     clusters = mlatree::g_dev[dev].clusters[int8 ? 1 : 0];
   }
-  const mlatree::Plan plan = mlatree::plan_of(d, clusters);
+  const mlatree::Plan plan = mlatree::plan_of(d, clusters, tree_lens != nullptr);
   mlatree::Params p;
   p.kv_nope = static_cast<const uint8_t*>(kv_nope);
   p.kv_scales = int8 ? kv_scales : nullptr;
@@ -1224,26 +1333,33 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   p.W = d.max_blocks_per_seq;
   p.num_blocks = d.num_blocks;
   p.rows = plan.rows;
-  p.blocks = plan.blocks;
   p.team = plan.team;
   p.teams = plan.teams;
-  p.passes = plan.passes;
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   p.out32 = aligned(out, 32) ? 1 : 0;
   p.wait_ns = mlasp::host_wait_limit_ns();
   const int64_t rows = static_cast<int64_t>(d.num_blocks) * 128, tokens = static_cast<int64_t>(d.B) * plan.rows;
   mlatree::Maps maps;
-  mla_status ms = tmap(&maps.q_nope, q_nope, 512, tokens, 64, "q_nope");
-  if (ms == MLA_OK) ms = tmap(&maps.q_rope, q_rope, 64, tokens, 64, "q_rope");
-  if (ms == MLA_OK) ms = tmap(&maps.rope, kv_rope, 64, rows, 128, "kv_rope");
-  // an INT8 latent is loaded by the producers; its maps stay unused
-  if (ms == MLA_OK) ms = tmap(&maps.key, int8 ? kv_rope : kv_nope, int8 ? 64 : 512, rows, 128, "kv_nope");
-  if (ms == MLA_OK) ms = tmap(&maps.val, int8 ? kv_rope : kv_nope, int8 ? 64 : 512, rows, 64, "kv_nope");
+  mla_status ms = tmap_bf16(&maps.q_nope, q_nope, 512, tokens, 64, "q_nope");
+  if (ms == MLA_OK) ms = tmap_bf16(&maps.q_rope, q_rope, 64, tokens, 64, "q_rope");
+  if (ms == MLA_OK) ms = tmap_bf16(&maps.rope, kv_rope, 64, rows, 128, "kv_rope");
+  if (int8) {  // codes and scales as they lie
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const CUtensorMapSwizzle flat = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (ms == MLA_OK) ms = tmap(&maps.key, u8, 1, kv_nope, 512, rows, 64, 128, flat, "kv_nope");
+    if (ms == MLA_OK) ms = tmap(&maps.val, u8, 1, kv_nope, 512, rows, 128, 64, flat, "kv_nope");
+    if (ms == MLA_OK) ms = tmap(&maps.key_scale, f32, 4, kv_scales, 4, rows, 4, 128, flat, "kv_scales");
+    if (ms == MLA_OK) ms = tmap(&maps.val_scale, f32, 4, kv_scales, 4, rows, 4, 64, flat, "kv_scales");
+  } else {
+    if (ms == MLA_OK) ms = tmap_bf16(&maps.key, kv_nope, 512, rows, 128, "kv_nope");
+    if (ms == MLA_OK) ms = tmap_bf16(&maps.val, kv_nope, 512, rows, 64, "kv_nope");
+    maps.key_scale = maps.val_scale = maps.rope;  // not used
+  }
   if (ms != MLA_OK) return ms;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(2 * plan.clusters));
-  if (int8) mlatree::tree_attn_kernel<true><<<grid, mlatree::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
-  else mlatree::tree_attn_kernel<false><<<grid, mlatree::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
+  if (int8) mlatree::tree_attn_kernel<true><<<grid, mlatree::Conf<true>::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
+  else mlatree::tree_attn_kernel<false><<<grid, mlatree::Conf<false>::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
   TREE_CUDA(cudaGetLastError(), "kernel launch");
   if (plan.teams > 1) {
     mlatree::tree_merge_kernel<<<dim3(static_cast<unsigned>(plan.clusters), 128), 128, 0, s>>>(p);
