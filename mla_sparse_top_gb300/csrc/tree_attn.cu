@@ -48,6 +48,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/mla_tree.h"
 #include "ptx.cuh"
@@ -72,7 +73,7 @@ struct Conf {
   static constexpr int kThreads = (kMmaWarp + (kInt8 ? 2 : 1)) * 32;
   static constexpr int kFillers = kInt8 ? 4 : 1;  // warps of a CTA that fill one slot together
   // INT8: the softmax warps take registers over from the converters
-  static constexpr int kRegs = kInt8 ? 96 : 128, kSoftmaxRegs = 120, kConvertRegs = 72;
+  static constexpr int kRegs = kInt8 ? 96 : 128, kSoftmaxRegs = 112, kConvertRegs = 80;
   static_assert(256 * kSoftmaxRegs + 256 * kConvertRegs <= 512 * 96, "register budget");
 };
 constexpr int kRawSlots = 5;
@@ -398,6 +399,13 @@ __device__ __forceinline__ uint4 finite8(uint4 v) {
   return make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
 }
 
+// First row of page `lb` of the sequence; one beyond the cache, where TMA fills
+// zeros, for a page that is not used or not good.
+__device__ __forceinline__ int page_row(const Params& p, const Segment& s, int lb) {
+  const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
+  return (good(p, id) ? id : p.num_blocks) * kPage;
+}
+
 // One filling of a ring slot.
 struct Item {
   int row, rows;  // first cache row (beyond the cache for a bad page), rows that exist
@@ -407,8 +415,8 @@ struct Item {
 };
 
 // The fillings in the order in which the MMAs take them, keys of tile t + 1
-// before values of tile t: all of them, or every kStride-th from item k on.
-template <int kStride, bool kPages>
+// before values of tile t: every kStride-th from item k on.
+template <int kStride>
 struct Items {
   Walk walk;
   Segment s;
@@ -433,12 +441,9 @@ struct Items {
     const int lb = 2 * t + (values ? k >> 2 : rank), sub = values ? ((k >> 1) & 1) * 64 : 0;
     const int base = lb * kPage + sub;
     it.rows = max(0, min(values ? 64 : kPage, s.act - base));
-    if constexpr (kPages) {
-      const int id = lb * kPage < s.act ? page_id(p, s.b, lb) : -1;
-      const bool ok = good(p, id);
-      it.row = (ok ? id : p.num_blocks) * kPage + sub;  // beyond the cache: TMA fills zeros
-      if (!ok) it.rows = 0;
-    }
+    it.row = page_row(p, s, lb);
+    if (it.row >= p.num_blocks * kPage) it.rows = 0;
+    it.row += sub;
     it.dim0 = values ? (k & 1) * 256 + rank * 128 : 64 * k;
     it.value = values;
     it.rope = !values && k == 8;
@@ -472,7 +477,7 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, c
   const uint32_t full = c.lead(kFull + w);
   const int rank = static_cast<int>(c.rank);
   uint32_t fills = 0, mended = 0;
-  Items<kSlots, true> items(walk, w);
+  Items<kSlots> items(walk, w);
   Item cur, nxt;
   bool have = items.next(p, rank, cur);
   while (have) {
@@ -509,107 +514,147 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, c
 }
 
 // INT8: one warp requests the codes and scales of every latent item.
-__device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, const Walk& walk, int lane) {
+__device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int lane) {
   const int rank = static_cast<int>(c.rank);
-  Items<1, true> items(walk, 0);
-  Item cur, nxt;
   int slot = 0;
   uint32_t phase = 1;
-  bool have = items.next(p, rank, cur);
-  while (have) {
-    const bool more = items.next(p, rank, nxt);
-    if (!cur.rope) {
-      if (!warp_wait(c, kRawEmpty + slot, phase)) return;
-      if (lane == 0) {
-        const uint32_t bar = c.bar(kRawFull + slot), dst = c.sb + kOffRaw + slot * kRawBytes;
-        mbar_arrive_expect_tx(bar, kRawCodes + (cur.value ? 64 : 128) * 16);
-        tma_pair(dst, cur.value ? &maps.val : &maps.key, cur.dim0, cur.row, bar);
-        tma_pair(dst + kRawCodes, cur.value ? &maps.val_scale : &maps.key_scale, 0, cur.row, bar);
-      }
-      __syncwarp();
-      if (++slot == kRawSlots) {
-        slot = 0;
-        phase ^= 1;
-      }
+  auto load = [&](const CUtensorMap& codes, const CUtensorMap& scales, int dim0, int row, int rows) {
+    if (!warp_wait(c, kRawEmpty + slot, phase)) return false;
+    if (lane == 0) {
+      const uint32_t bar = c.bar(kRawFull + slot), dst = c.sb + kOffRaw + slot * kRawBytes;
+      mbar_arrive_expect_tx(bar, kRawCodes + rows * 16);
+      tma_pair(dst, &codes, dim0, row, bar);
+      tma_pair(dst + kRawCodes, &scales, 0, row >> 6, bar);
     }
-    cur = nxt;
-    have = more;
+    __syncwarp();
+    if (++slot == kRawSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+    return true;
+  };
+  Segment s;
+  while (walk.next(p, s)) {
+    int rows[2] = {0, 0};  // pages of the tile before
+    for (int u = s.t0; u <= s.t1; ++u) {
+      int next[2] = {0, 0};
+      if (u < s.t1) {
+        next[0] = page_row(p, s, 2 * u);
+        next[1] = page_row(p, s, 2 * u + 1);
+        for (int k = 0; k < 8; ++k)
+          if (!load(maps.key, maps.key_scale, 64 * k, next[rank], kPage)) return;
+      }
+      if (u > s.t0) {
+        const int items = 2 * groups_of(s, u - 1);
+        for (int k = 0; k < items; ++k)
+          if (!load(maps.val, maps.val_scale, (k & 1) * 256 + rank * 128, rows[k >> 2] + ((k >> 1) & 1) * 64, 64)) return;
+      }
+      rows[0] = next[0];
+      rows[1] = next[1];
+    }
   }
 }
 
-// INT8: converter warp w of group w / 4 turns a quarter of every other item
-// into bf16, 16 codes of a lane at a time; codes lie as TMA left them, row by
-// row, so a warp reads 512 adjacent bytes.
-__device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, const Walk& walk, int w, int lane) {
-  constexpr int kSlots = Conf<true>::kSlots;
-  const int rank = static_cast<int>(c.rank), group = w >> 2, quarter = w & 3;
-  Items<1, false> items(walk, 0);
-  Item it;
-  int raw = 0, i = 0;
-  uint32_t raw_phase = 0;
-  for (; items.next(p, rank, it); ++i) {
-    const int slot = i % kSlots;
-    const bool mine = (i & 1) == group;
-    const uint32_t dst0 = c.sb + kOffRing + slot * kSlotBytes, full = c.lead(kFull + slot);
-    if (it.rope) {
-      if (mine) {
-        if (!warp_wait(c, kEmpty + slot, ((i / kSlots) & 1) ^ 1)) return;
-        if (lane == 0) {
-          if (quarter == 0) {
-            const int lb = (items.u) * 2 + rank;
-            const int id = lb * kPage < items.s.act ? page_id(p, items.s.b, lb) : -1;
-            arrive_lead_tx(full, kSlotBytes);
-            tma_pair(dst0, &maps.rope, 0, (good(p, id) ? id : p.num_blocks) * kPage, full);
-          } else {
-            arrive_lead(full);
-          }
-        }
-        __syncwarp();
-      }
-      continue;
+// INT8: converter warp w of group w / 4 turns a quarter of every kGroups-th
+// item into bf16, 16 codes of a lane at a time; codes lie as TMA left them, row
+// by row, so a warp reads 512 adjacent bytes.
+__device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int w, int lane) {
+  constexpr int kSlots = Conf<true>::kSlots, kGroups = Conf<true>::kProducers / 4;
+  const int rank = static_cast<int>(c.rank), quarter = w & 3;
+  int turn = w >> 2;  // items until this group's next one
+  int slot = 0, raw = 0;
+  uint32_t phase = 1, raw_phase = 0;
+  auto pass = [&](bool latent) {  // on to the next item
+    if (turn-- == 0) turn = kGroups - 1;
+    if (++slot == kSlots) {
+      slot = 0;
+      phase ^= 1;
     }
-    if (mine) {
-      if (!warp_wait(c, kRawFull + raw, raw_phase)) return;
-      const uint32_t src = c.sb + kOffRaw + raw * kRawBytes;
-      const int us = it.value ? 3 : 2;  // log2 of a row's units: 128 or 64 codes
-      const uint32_t scale_at = src + kRawCodes + 4 * (it.dim0 >> 7);
-      uint4 v[4];
-      float sc[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int unit = (quarter * 4 + k) * 32 + lane;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(src + unit * 16));
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc[k]) : "r"(scale_at + (unit >> us) * 16));
-      }
-      if (!warp_wait(c, kEmpty + slot, ((i / kSlots) & 1) ^ 1)) return;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int unit = (quarter * 4 + k) * 32 + lane;
-        const int r = unit >> us, col = unit & ((1 << us) - 1), u0 = 2 * (col & 3);
-        uint4 a, b;
-        dequant4(v[k].x, sc[k], a.x, a.y);
-        dequant4(v[k].y, sc[k], a.z, a.w);
-        dequant4(v[k].z, sc[k], b.x, b.y);
-        dequant4(v[k].w, sc[k], b.z, b.w);
-        if (it.value && r >= it.first_draft) {
-          a = r < it.rows ? finite8(a) : make_uint4(0, 0, 0, 0);
-          b = r < it.rows ? finite8(b) : make_uint4(0, 0, 0, 0);
-        }
-        const uint32_t dst = dst0 + (col >> 2) * kChunk + r * 128;
-        sts16(dst + ((u0 ^ (r & 7)) << 4), a);
-        sts16(dst + (((u0 + 1) ^ (r & 7)) << 4), b);
-      }
-      fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
-      __syncwarp();
-      if (lane == 0) {
-        arrive_lead(full);
-        mbar_arrive(c.bar(kRawEmpty + raw));
-      }
-    }
-    if (++raw == kRawSlots) {
+    if (latent && ++raw == kRawSlots) {
       raw = 0;
       raw_phase ^= 1;
+    }
+  };
+  // rows of 64 (us = 2) or 128 codes (us = 3); from row `mend` on the value rows
+  // lose their NaN and infinities, from row `end` on they are zero
+  auto convert = [&](auto us_, int dim0, int mend, int end) {
+    constexpr int us = decltype(us_)::value;
+    if (turn != 0) {
+      pass(true);
+      return true;
+    }
+    if (!warp_wait(c, kRawFull + raw, raw_phase)) return false;
+    const uint32_t src = c.sb + kOffRaw + raw * kRawBytes;
+    const int unit0 = quarter * 128 + lane;
+    uint4 v[4];
+    float sc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int unit = unit0 + 32 * k;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(src + unit * 16));
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(sc[k]) : "r"(src + kRawCodes + (unit >> us) * 16 + 4 * (dim0 >> 7)));
+    }
+    if (!warp_wait(c, kEmpty + slot, phase)) return false;
+    // unit0 + 32 k lies 8 (us = 2) or 4 rows on, in the same column
+    const int col = unit0 & ((1 << us) - 1), u0 = 2 * (col & 3);
+    const uint32_t dst0 = c.sb + kOffRing + slot * kSlotBytes + (col >> 2) * kChunk;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = (unit0 >> us) + ((32 * k) >> us);
+      uint4 a, b;
+      dequant4(v[k].x, sc[k], a.x, a.y);
+      dequant4(v[k].y, sc[k], a.z, a.w);
+      dequant4(v[k].z, sc[k], b.x, b.y);
+      dequant4(v[k].w, sc[k], b.z, b.w);
+      if (us == 3 && r >= mend) {
+        a = r < end ? finite8(a) : make_uint4(0, 0, 0, 0);
+        b = r < end ? finite8(b) : make_uint4(0, 0, 0, 0);
+      }
+      sts16(dst0 + r * 128 + ((u0 ^ (r & 7)) << 4), a);
+      sts16(dst0 + r * 128 + (((u0 + 1) ^ (r & 7)) << 4), b);
+    }
+    fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
+    __syncwarp();
+    if (lane == 0) {
+      arrive_lead(c.lead(kFull) + 8 * slot);
+      mbar_arrive(c.bar(kRawEmpty + raw));
+    }
+    pass(true);
+    return true;
+  };
+  Segment s;
+  while (walk.next(p, s)) {
+    for (int u = s.t0; u <= s.t1; ++u) {
+      if (u < s.t1) {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k)
+          if (!convert(std::integral_constant<int, 2>(), 64 * k, 0, 0)) return;
+        if (turn == 0) {  // rope rows are bf16: straight into the slot
+          const int row = page_row(p, s, 2 * u + rank);
+          if (!warp_wait(c, kEmpty + slot, phase)) return;
+          if (lane == 0) {
+            const uint32_t full = c.lead(kFull) + 8 * slot;
+            if (quarter == 0) {
+              arrive_lead_tx(full, kSlotBytes);
+              tma_pair(c.sb + kOffRing + slot * kSlotBytes, &maps.rope, 0, row, full);
+            } else {
+              arrive_lead(full);
+            }
+          }
+          __syncwarp();
+        }
+        pass(false);
+      }
+      if (u > s.t0) {
+        const int items = 2 * groups_of(s, u - 1);
+#pragma unroll 1
+        for (int k = 0; k < items; ++k) {
+          const int base = kTile * (u - 1) + 64 * (k >> 1);
+          if (!convert(std::integral_constant<int, 3>(), (k & 1) * 256 + rank * 128, s.ctx - base, s.act - base)) return;
+        }
+      }
     }
   }
 }
@@ -1060,6 +1105,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
   cluster_wait();
 }
 
+// ------------------------------------------------------------------ INT8 rows to bf16
+// Every used page of every sequence once, 16 codes of a thread at a time, into
+// rows of the same number.  Bound by memory (656 bytes in, 1024 out per row).
+__global__ void __launch_bounds__(256) tree_dequant_kernel(const int8_t* __restrict__ codes,
+                                                           const __grid_constant__ Params p, uint16_t* out) {
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const Seq q = load_seq(p, b);
+    if (q.blocks == 0) continue;
+    const int pages = (min(q.act, p.W * kPage) + kPage - 1) / kPage;
+    for (int lb = blockIdx.x; lb < pages; lb += gridDim.x) {
+      const int id = page_id(p, b, lb);
+      if (!good(p, id)) continue;
+      const int rows = min(kPage, q.act - lb * kPage);
+      const int64_t row0 = static_cast<int64_t>(id) * kPage;
+#pragma unroll 4
+      for (int it = 0; it < 16; ++it) {
+        const int unit = it * 256 + threadIdx.x, r = unit >> 5, col = unit & 31;
+        if (r >= rows) break;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(codes + (row0 + r) * 512) + col);
+        const float sc = __ldg(p.kv_scales + (row0 + r) * 4 + (col >> 3));
+        uint4 x, y;
+        dequant4(v.x, sc, x.x, x.y);
+        dequant4(v.y, sc, x.z, x.w);
+        dequant4(v.z, sc, y.x, y.y);
+        dequant4(v.w, sc, y.z, y.w);
+        stg32(out + (row0 + r) * 512 + col * 16, x, y);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ merge
 // Joins the parts of a row block that was cut between teams: block x looks at
 // the record of cluster x (the one the row block starts in), block y takes 1 of
@@ -1147,9 +1223,16 @@ inline int team_size(int blocks, int clusters, bool ragged) {
   return best;
 }
 
+// A sequence of several row blocks has its INT8 rows converted once, into the
+// workspace, rather than by every cluster that reads them (each converts a key
+// twice: as a key and as a value).  @@MEASURED@@
+constexpr int kExpandBlocks = 2;
+constexpr size_t kExpandBytes = size_t(4) << 30;  // workspace spent on it at most
+
 struct Plan {
   int rows, blocks, team, teams, passes, clusters;
-  size_t records_at, bytes;
+  bool expand;  // INT8: the rows are turned into bf16 in the workspace first
+  size_t records_at, rows_at, bytes;
 };
 inline Plan plan_of(const mla_dims& d, int clusters, bool ragged) {
   Plan s;
@@ -1165,7 +1248,10 @@ inline Plan plan_of(const mla_dims& d, int clusters, bool ragged) {
   // the workspace has room for the schedule of any device and any drafts
   const int64_t room = std::min<int64_t>(kMaxClusters, most(s.blocks) * s.blocks);
   s.records_at = static_cast<size_t>(room) * 4 * kPartFloats * sizeof(float);
-  s.bytes = s.records_at + static_cast<size_t>(room) * sizeof(int4);
+  s.rows_at = (s.records_at + static_cast<size_t>(room) * sizeof(int4) + 1023) & ~static_cast<size_t>(1023);
+  const size_t rows = static_cast<size_t>(d.num_blocks) * kPage * 1024;
+  s.expand = d.kv_dtype == MLA_KV_INT8 && s.blocks >= kExpandBlocks && rows <= kExpandBytes;
+  s.bytes = s.rows_at + (s.expand ? rows : 0);
   return s;
 }
 
@@ -1313,7 +1399,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
     std::lock_guard<std::mutex> guard(mlatree::g_lock);
     const mla_status ist = init_device(mlatree::g_dev[dev]);
     if (ist != MLA_OK) return ist;
-    clusters = mlatree::g_dev[dev].clusters[int8 ? 1 : 0];
+    clusters = std::min(mlatree::g_dev[dev].clusters[0], mlatree::g_dev[dev].clusters[1]);
   }
   const mlatree::Plan plan = mlatree::plan_of(d, clusters, tree_lens != nullptr);
   mlatree::Params p;
@@ -1338,27 +1424,38 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   p.out32 = aligned(out, 32) ? 1 : 0;
   p.wait_ns = mlasp::host_wait_limit_ns();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const void* latent = kv_nope;
+  if (plan.expand) {
+    uint16_t* wide = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + plan.rows_at);
+    const int per_seq = std::max(1, std::min(d.max_blocks_per_seq, 152 * 8 / d.B));
+    mlatree::tree_dequant_kernel<<<dim3(static_cast<unsigned>(per_seq), static_cast<unsigned>(std::min(d.B, 65535))), 256, 0, s>>>(
+        static_cast<const int8_t*>(kv_nope), p, wide);
+    TREE_CUDA(cudaGetLastError(), "INT8 expansion launch");
+    latent = wide;
+  }
+  const bool codes = int8 && !plan.expand;  // the attention kernel reads codes
   const int64_t rows = static_cast<int64_t>(d.num_blocks) * 128, tokens = static_cast<int64_t>(d.B) * plan.rows;
   mlatree::Maps maps;
   mla_status ms = tmap_bf16(&maps.q_nope, q_nope, 512, tokens, 64, "q_nope");
   if (ms == MLA_OK) ms = tmap_bf16(&maps.q_rope, q_rope, 64, tokens, 64, "q_rope");
   if (ms == MLA_OK) ms = tmap_bf16(&maps.rope, kv_rope, 64, rows, 128, "kv_rope");
-  if (int8) {  // codes and scales as they lie
+  if (codes) {  // codes and scales as they lie
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const CUtensorMapSwizzle flat = CU_TENSOR_MAP_SWIZZLE_NONE;
     if (ms == MLA_OK) ms = tmap(&maps.key, u8, 1, kv_nope, 512, rows, 64, 128, flat, "kv_nope");
     if (ms == MLA_OK) ms = tmap(&maps.val, u8, 1, kv_nope, 512, rows, 128, 64, flat, "kv_nope");
-    if (ms == MLA_OK) ms = tmap(&maps.key_scale, f32, 4, kv_scales, 4, rows, 4, 128, flat, "kv_scales");
-    if (ms == MLA_OK) ms = tmap(&maps.val_scale, f32, 4, kv_scales, 4, rows, 4, 64, flat, "kv_scales");
+    // the scales of 64 rows as one row of the map: 1 KB at a time instead of 16 bytes
+    if (ms == MLA_OK) ms = tmap(&maps.key_scale, f32, 4, kv_scales, 256, rows / 64, 256, 2, flat, "kv_scales");
+    if (ms == MLA_OK) ms = tmap(&maps.val_scale, f32, 4, kv_scales, 256, rows / 64, 256, 1, flat, "kv_scales");
   } else {
-    if (ms == MLA_OK) ms = tmap_bf16(&maps.key, kv_nope, 512, rows, 128, "kv_nope");
-    if (ms == MLA_OK) ms = tmap_bf16(&maps.val, kv_nope, 512, rows, 64, "kv_nope");
+    if (ms == MLA_OK) ms = tmap_bf16(&maps.key, latent, 512, rows, 128, "kv_nope");
+    if (ms == MLA_OK) ms = tmap_bf16(&maps.val, latent, 512, rows, 64, "kv_nope");
     maps.key_scale = maps.val_scale = maps.rope;  // not used
   }
   if (ms != MLA_OK) return ms;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(2 * plan.clusters));
-  if (int8) mlatree::tree_attn_kernel<true><<<grid, mlatree::Conf<true>::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
+  if (codes) mlatree::tree_attn_kernel<true><<<grid, mlatree::Conf<true>::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
   else mlatree::tree_attn_kernel<false><<<grid, mlatree::Conf<false>::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
   TREE_CUDA(cudaGetLastError(), "kernel launch");
   if (plan.teams > 1) {
