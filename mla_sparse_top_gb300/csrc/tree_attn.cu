@@ -306,11 +306,18 @@ __device__ bool start_walk(const Params& p, const Ctx& c, int cid, Walk& w, int6
   const int tid = threadIdx.x;
   const int chunks = (p.B + kThreads - 1) / kThreads;
   int64_t mine = 0, len = 0, pre = 0;
+  bool beyond = false;  // positions outside the table
   for (int k = 0; k < chunks; ++k) {
     const int b = k * kThreads + tid;
-    len = b < p.B ? load_seq(p, b).len(p) : 0;
+    len = 0;
+    if (b < p.B) {
+      const Seq q = load_seq(p, b);
+      len = q.len(p);
+      beyond = beyond || (q.cut_table && q.n > 0);
+    }
     mine += len;
   }
+  if (beyond) atomicOr(&g_tree_status, MLA_DEVICE_BAD_BLOCK);
   pre = block_sum_scan<kThreads>(c, mine, total);
   teams = teams_of(p, total);
   const int team = cid / p.team;
@@ -971,12 +978,13 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
       const int at = s.t0 > 0 ? 0 : 1;
       float* dst = p.parts + (static_cast<int64_t>(cid * 2 + at) * 2 + c.rank) * kPartFloats;
 #pragma unroll 1
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(tO + 32 * ch, v);
+      for (int ch = 0; ch < 4; ch += 2) {
+        uint32_t v[64];
+        tmem_ld_32x32b_x32(tO + 32 * ch, *reinterpret_cast<uint32_t(*)[32]>(v));
+        tmem_ld_32x32b_x32(tO + 32 * ch + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 16; ++k)
           reinterpret_cast<uint4*>(dst)[(sub * 32 + ch * 8 + k) * 128 + L] =
               make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
       }
@@ -1042,9 +1050,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
   Walk walk;
   int64_t total;
   int teams;
-  const bool busy = start_walk<K::kThreads>(p, c, cid, walk, total, teams);
   tc_fence_before();
+  __syncthreads();  // barriers and the tensor memory address are in place
   cluster_arrive();
+  const bool busy = start_walk<K::kThreads>(p, c, cid, walk, total, teams);
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // rows expanded by the launch before
   cluster_wait();
   tc_fence_after();
   c.tmem = uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(c.smem + kOffTmem)));
@@ -1065,14 +1076,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
     } else {
       if constexpr (kInt8) raw_load_role(p, c, maps, walk, lane);
     }
-  }
-  if (tid == 0) {  // positions beyond the table, found by the cluster that owns the sequence's number
-    bool beyond = false;
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-      const Seq q = load_seq(p, b);
-      beyond = beyond || (q.cut_table && q.n > 0);
-    }
-    if (beyond) atomicOr(&g_tree_status, MLA_DEVICE_BAD_BLOCK);
   }
   if (p.tree_lens != nullptr) {  // padding tokens of row blocks that nobody works on
     for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.B) * p.S1; t += gridDim.x) {
@@ -1101,8 +1104,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
   tc_fence_after();
   if (warp == K::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(c.tmem) : "memory");
-  cluster_arrive();
-  cluster_wait();
 }
 
 // ------------------------------------------------------------------ INT8 rows to bf16
@@ -1110,6 +1111,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
 // rows of the same number.  Bound by memory (656 bytes in, 1024 out per row).
 __global__ void __launch_bounds__(256) tree_dequant_kernel(const int8_t* __restrict__ codes,
                                                            const __grid_constant__ Params p, uint16_t* out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     const Seq q = load_seq(p, b);
     if (q.blocks == 0) continue;
@@ -1119,72 +1121,115 @@ __global__ void __launch_bounds__(256) tree_dequant_kernel(const int8_t* __restr
       if (!good(p, id)) continue;
       const int rows = min(kPage, q.act - lb * kPage);
       const int64_t row0 = static_cast<int64_t>(id) * kPage;
-#pragma unroll 4
-      for (int it = 0; it < 16; ++it) {
-        const int unit = it * 256 + threadIdx.x, r = unit >> 5, col = unit & 31;
-        if (r >= rows) break;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(codes + (row0 + r) * 512) + col);
-        const float sc = __ldg(p.kv_scales + (row0 + r) * 4 + (col >> 3));
-        uint4 x, y;
-        dequant4(v.x, sc, x.x, x.y);
-        dequant4(v.y, sc, x.z, x.w);
-        dequant4(v.z, sc, y.x, y.y);
-        dequant4(v.w, sc, y.z, y.w);
-        stg32(out + (row0 + r) * 512 + col * 16, x, y);
+      const int col = threadIdx.x & 31, r0 = threadIdx.x >> 5;  // 16 codes of rows r0, r0 + 8, ...
+      for (int it = 0; it < 16 && 8 * it < rows; it += 8) {
+        uint4 v[8];
+        float sc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + 8 * (it + k);
+          v[k] = make_uint4(0, 0, 0, 0);
+          sc[k] = 0.f;
+          if (r < rows) {
+            v[k] = __ldg(reinterpret_cast<const uint4*>(codes + (row0 + r) * 512) + col);
+            sc[k] = __ldg(p.kv_scales + (row0 + r) * 4 + (col >> 3));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + 8 * (it + k);
+          uint4 x, y;
+          dequant4(v[k].x, sc[k], x.x, x.y);
+          dequant4(v[k].y, sc[k], x.z, x.w);
+          dequant4(v[k].z, sc[k], y.x, y.y);
+          dequant4(v[k].w, sc[k], y.z, y.w);
+          if (r < rows) stg32(out + (row0 + r) * 512 + col * 16, x, y);
+        }
       }
     }
   }
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the parts of a row block that was cut between teams: block x looks at
-// the record of cluster x (the one the row block starts in), block y takes 1 of
-// the 2 CTAs' 64 float4 units.  Thread L is lane L of the units.
-__global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ Params p) {
+// Joins the parts of a row block that was cut between teams.  Block x looks at
+// the record of cluster x (the one the row block starts in), block y takes 16
+// columns of the 256 of one CTA; thread L of each group is lane L of the parts'
+// units.  One group for the usual two or three parts; four that share out the
+// parts where a few long sequences have one from almost every team.
+template <int kMergeGroups>
+__global__ void __launch_bounds__(128 * kMergeGroups) tree_merge_kernel(const __grid_constant__ Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's stores are visible
   const int4 rec = p.records[blockIdx.x];
-  const int L = threadIdx.x, row = L & 63, half = L >> 6;
-  const int rank = blockIdx.y >> 6, unit = blockIdx.y & 63;
-  const int r = rank * 64 + row;
-  if (r >= rec.y) return;  // no record: 0 rows
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 <= rec.z; k0 += 8) {
-    float mk[8], lk[8];
-    float4 v[8];
+  if (rec.y == 0) return;
+  const int L = threadIdx.x & 127, group = threadIdx.x >> 7, row = L & 63, half = L >> 6;
+  const int rank = blockIdx.y >> 4, unit = (blockIdx.y & 15) * 4;
+  float m = -INFINITY, l = 0.f, o[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool in = k0 + k <= rec.z;
-      const int cl = blockIdx.x + (in ? k0 + k : 0) * p.team;
-      const float* src = p.parts + (static_cast<int64_t>(cl * 2 + (k0 + k == 0 || !in ? 1 : 0)) * 2 + rank) * kPartFloats;
-      mk[k] = in ? __ldcg(src + 128 * 256 + row) : -INFINITY;
-      lk[k] = in ? __ldcg(src + 128 * 256 + 64 + row) : 0.f;
-      v[k] = __ldcg(reinterpret_cast<const float4*>(src) + unit * 128 + L);
+  for (int k = 0; k < 16; ++k) o[k] = 0.f;
+  for (int k0 = group; k0 <= rec.z; k0 += 2 * kMergeGroups) {
+    float mk[2], lk[2];
+    float4 v[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = k0 + u * kMergeGroups;
+      const bool in = k <= rec.z;
+      const int cl = blockIdx.x + (in ? k : 0) * p.team;
+      const float* src = p.parts + (static_cast<int64_t>(cl * 2 + (in && k > 0 ? 0 : 1)) * 2 + rank) * kPartFloats;
+      mk[u] = in ? __ldcg(src + 128 * 256 + row) : -INFINITY;
+      lk[u] = in ? __ldcg(src + 128 * 256 + 64 + row) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[u][i] = __ldcg(reinterpret_cast<const float4*>(src) + (unit + i) * 128 + L);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (mk[k] == -INFINITY && lk[k] == 0.f) continue;  // a part in which the row sees nothing
-      if (mk[k] > m) {
-        const float f = m == -INFINITY ? 0.f : exp2f(m - mk[k]);
-        l *= f;
-        o.x *= f;
-        o.y *= f;
-        o.z *= f;
-        o.w *= f;
-        m = mk[k];
+    for (int u = 0; u < 2; ++u) {
+      if (mk[u] == -INFINITY && lk[u] == 0.f) continue;  // a part in which the row sees nothing
+      const float top = fmaxf(m, mk[u]);
+      const float f = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(mk[u] - top);
+      m = top;
+      l = l * f + w * lk[u];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[4 * i] = o[4 * i] * f + w * v[u][i].x;
+        o[4 * i + 1] = o[4 * i + 1] * f + w * v[u][i].y;
+        o[4 * i + 2] = o[4 * i + 2] * f + w * v[u][i].z;
+        o[4 * i + 3] = o[4 * i + 3] * f + w * v[u][i].w;
       }
-      const float w = exp2f(mk[k] - m);
-      l = fmaf(w, lk[k], l);
-      o.x = fmaf(w, v[k].x, o.x);
-      o.y = fmaf(w, v[k].y, o.y);
-      o.z = fmaf(w, v[k].z, o.z);
-      o.w = fmaf(w, v[k].w, o.w);
     }
   }
-  const float inv = 1.f / l;
+  const int r = rank * 64 + row;
+  if constexpr (kMergeGroups > 1) {
+    __shared__ float sm[kMergeGroups][18][128];
+    sm[group][16][L] = m;
+    sm[group][17][L] = l;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) sm[group][k][L] = o[k];
+    __syncthreads();
+    if (group != 0) return;
+    for (int g = 1; g < kMergeGroups; ++g) {
+      const float mg = sm[g][16][L], lg = sm[g][17][L];
+      if (mg == -INFINITY && lg == 0.f) continue;
+      const float top = fmaxf(m, mg);
+      const float f = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(mg - top);
+      m = top;
+      l = l * f + w * lg;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) o[k] = o[k] * f + w * sm[g][k][L];
+    }
+  }
+  if (r >= rec.y) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0u : pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
   const int64_t g = rec.x + r;
-  uint2 y = make_uint2(0u, 0u);
-  if (l != 0.f) y = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  *reinterpret_cast<uint2*>(p.out + g * 512 + (unit >> 5) * 256 + half * 128 + (unit & 31) * 4) = y;
+  uint16_t* out = p.out + g * 512 + (unit >> 5) * 256 + half * 128 + (unit & 31) * 4;
+  const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+  if (p.out32) {
+    stg32(out, a, b);
+  } else {
+    reinterpret_cast<uint4*>(out)[0] = a;
+    reinterpret_cast<uint4*>(out)[1] = b;
+  }
   if (unit == 0 && half == 0 && p.lse != nullptr)
     p.lse[g] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
@@ -1295,6 +1340,24 @@ mla_status check_dims(const mla_dims& d) {
     const cudaError_t err_ = (call);                                                              \
     if (err_ != cudaSuccess) return tree_fail(MLA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err_)); \
   } while (0)
+
+// A launch that may begin while the launch before it on the stream ends: the
+// kernel waits (griddepcontrol.wait) before it touches what that one writes.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool early,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 template <bool kInt8>
 mla_status prepare_kernel(mlatree::Device& dev) {
@@ -1455,13 +1518,22 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   }
   if (ms != MLA_OK) return ms;
   const dim3 grid(static_cast<unsigned>(2 * plan.clusters));
-  if (codes) mlatree::tree_attn_kernel<true><<<grid, mlatree::Conf<true>::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
-  else mlatree::tree_attn_kernel<false><<<grid, mlatree::Conf<false>::kThreads, mlatree::kSmemBytes, s>>>(maps, p);
-  TREE_CUDA(cudaGetLastError(), "kernel launch");
-  if (plan.teams > 1) {
-    mlatree::tree_merge_kernel<<<dim3(static_cast<unsigned>(plan.clusters), 128), 128, 0, s>>>(p);
-    TREE_CUDA(cudaGetLastError(), "merge launch");
-  }
+  if (codes)
+    TREE_CUDA(launch_after(mlatree::tree_attn_kernel<true>, grid, mlatree::Conf<true>::kThreads, mlatree::kSmemBytes, s,
+                           false, maps, p),
+              "kernel launch");
+  else
+    TREE_CUDA(launch_after(mlatree::tree_attn_kernel<false>, grid, mlatree::Conf<false>::kThreads, mlatree::kSmemBytes,
+                           s, plan.expand, maps, p),
+              "kernel launch");
+  if (plan.teams > 1)
+    // parts of a row block, if the sequences were equally long
+    TREE_CUDA(plan.teams > 6 * static_cast<int64_t>(d.B) * plan.passes
+                  ? launch_after(mlatree::tree_merge_kernel<4>, dim3(static_cast<unsigned>(plan.clusters), 32), 512, 0, s,
+                                 true, p)
+                  : launch_after(mlatree::tree_merge_kernel<1>, dim3(static_cast<unsigned>(plan.clusters), 32), 128, 0, s,
+                                 true, p),
+              "merge launch");
   return MLA_OK;
 }
 
