@@ -101,14 +101,23 @@ __device__ __forceinline__ int64_t row_of(const Params& p, int b, int64_t slot, 
 
 __device__ __forceinline__ int sat32(int64_t v) { return static_cast<int>(min(v, static_cast<int64_t>(0x7fffffff))); }
 
-// The table entries of one sequence's new pages, one warp per sequence.
-__device__ __forceinline__ void write_pages(const Params& p, int b, int have, int need, int64_t first_free,
-                                            unsigned& flags) {
-  for (int k = threadIdx.x & 31; k < need; k += 32) {
-    const int id = page_id(p, b, have + k, have, first_free);
-    p.io.block_table[static_cast<int64_t>(b) * p.W + have + k] = id;
-    if (id < 0 && first_free + k >= p.num_free) flags |= MLA_DEVICE_NO_PAGE;
-  }
+// Table entry k of one sequence's new pages.
+__device__ __forceinline__ void write_page(const Params& p, int b, int have, int k, int64_t first_free, unsigned& flags) {
+  const int id = page_id(p, b, have + k, have, first_free);
+  p.io.block_table[static_cast<int64_t>(b) * p.W + have + k] = id;
+  if (id < 0 && first_free + k >= p.num_free) flags |= MLA_DEVICE_NO_PAGE;
+}
+// A step that adds a few tokens takes a page or none: the sequence's own thread
+// writes up to kOwnPages, so all sequences of a block do at once; the pages of
+// prompts beyond those are a warp's work.
+constexpr int kOwnPages = 2;
+__device__ __forceinline__ void write_own_pages(const Params& p, int b, const Seq& s, int64_t first_free,
+                                                unsigned& flags) {
+  for (int k = 0; k < min(s.need, kOwnPages); ++k) write_page(p, b, s.have, k, first_free, flags);
+}
+__device__ __forceinline__ void write_more_pages(const Params& p, int b, int have, int need, int64_t first_free,
+                                                 unsigned& flags) {
+  for (int k = kOwnPages + (threadIdx.x & 31); k < need; k += 32) write_page(p, b, have, k, first_free, flags);
 }
 
 // Outputs of each sequence: thread's sequence b with its sums.
@@ -187,13 +196,15 @@ __global__ void __launch_bounds__(kThreads) plan_padded_kernel(const Params p) {
   longlong2 before = block_scan(make_longlong2(s.need, s.add), sh.part, total);
   before.x += prior.x;
   before.y += prior.y;
+  unsigned flags = 0;
   if (tid < nb) {
-    write_seq(p, b0 + tid, s, before);
     keep(sh, tid, s, before);
+    write_seq(p, b0 + tid, s, before);
+    write_own_pages(p, b0 + tid, s, before.x, flags);
   }
   __syncthreads();
-  unsigned flags = 0;
-  for (int q = tid >> 5; q < nb; q += kWarps) write_pages(p, b0 + q, sh.have[q], sh.need[q], sh.first_free[q], flags);
+  for (int q = tid >> 5; q < nb; q += kWarps)
+    write_more_pages(p, b0 + q, sh.have[q], sh.need[q], sh.first_free[q], flags);
   const int words = (p.S1 + 63) / 64;
   for (int r = tid; r < nb * p.S1; r += kThreads) {
     const int q = r / p.S1, i = r - q * p.S1, b = b0 + q;
@@ -215,8 +226,9 @@ __global__ void __launch_bounds__(kThreads) plan_padded_kernel(const Params p) {
 }
 
 // Packed layout: a block owns kTileTokens rows.  It runs over the sequences in
-// chunks of one per thread, up to the chunk that ends its tile; block c also
-// writes the per-sequence outputs of chunk c.
+// chunks of one per thread, up to the chunk that ends its tile, and at least up
+// to chunk blockIdx.x; block c writes the per-sequence outputs of chunk c, and
+// all the blocks that come past a chunk share out its pages.
 __global__ void __launch_bounds__(kThreads) plan_packed_kernel(const Params p) {
   __shared__ Shared sh;
   const int tid = threadIdx.x;
@@ -237,12 +249,14 @@ __global__ void __launch_bounds__(kThreads) plan_packed_kernel(const Params p) {
     const int n = min(kThreads, p.B - c * kThreads);
     if (c == static_cast<int>(blockIdx.x)) {
       if (b < p.B) write_seq(p, b, s, before);
-      __syncthreads();
-      for (int q = tid >> 5; q < n; q += kWarps)
-        write_pages(p, c * kThreads + q, sh.have[q], sh.need[q], sh.first_free[q], flags);
       if (c == chunks - 1 && carry.y + total.y > p.T) flags |= MLA_DEVICE_NO_PAGE;
-    } else {
-      __syncthreads();
+    }
+    __syncthreads();
+    if (c <= static_cast<int>(blockIdx.x)) {  // blocks c .. gridDim.x - 1 come past chunk c
+      const int sharers = static_cast<int>(gridDim.x) - c;
+      for (int q = (static_cast<int>(blockIdx.x) - c) * kWarps + (tid >> 5); q < n; q += sharers * kWarps)
+        for (int k = tid & 31; k < sh.need[q]; k += 32)
+          write_page(p, c * kThreads + q, sh.have[q], k, sh.first_free[q], flags);
     }
     // this tile's rows that belong to the chunk's sequences
     const int64_t lo = max(t0, static_cast<int64_t>(carry.y)), hi = min(t1, static_cast<int64_t>(carry.y + total.y));
