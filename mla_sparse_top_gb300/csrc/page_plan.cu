@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) plan_padded_kernel(const Params p) {
   const int b0 = blockIdx.x * p.seqs_per_block, nb = min(p.seqs_per_block, p.B - b0);
   const int tid = threadIdx.x;
   longlong2 prior = make_longlong2(0, 0), total;
+#pragma unroll 4
   for (int b = tid; b < b0; b += kThreads) {
     const Seq s = load_seq(p, b);
     prior.x += s.need;

@@ -27,6 +27,7 @@
 namespace mlarp {
 
 constexpr int kThreads = 512;
+constexpr int kTableThreads = 256;
 constexpr int kMaxPairs = 128;  // rot_dim <= 256
 constexpr int kMaxPasses = 16;  // rows of a thread
 
@@ -39,9 +40,11 @@ struct Freqs {
 
 // cos and sin of position * frequency, times mscale.
 __device__ __forceinline__ float2 cos_sin(int32_t pos, uint64_t turn, float mscale) {
-  const int64_t frac = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * turn);
+  const uint64_t frac = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turn;
+  // signed high word and unsigned low word: two 32-bit conversions are faster than one of 64 bits
+  const float hi = static_cast<float>(static_cast<int32_t>(frac >> 32)), lo = static_cast<float>(static_cast<uint32_t>(frac));
   float s, c;
-  sincospif(static_cast<float>(frac) * 0x1p-63f, &s, &c);
+  sincospif(fmaf(lo, 0x1p-63f, hi * 0x1p-31f), &s, &c);
   return make_float2(c * mscale, s * mscale);
 }
 
@@ -53,25 +56,24 @@ struct TableParams {
   int T, pairs;
 };
 
-// A thread keeps one pair and walks over tokens, four at a time.
-__global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_constant__ TableParams p) {
-  const int rows = kThreads / p.pairs;
+// A thread keeps one pair and takes kTableTokens tokens, `rows` apart.
+constexpr int kTableTokens = 4;
+__global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ TableParams p) {
+  const int rows = kTableThreads / p.pairs;
   const int r = threadIdx.x / p.pairs, i = threadIdx.x - r * p.pairs;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rows * kTableTokens + r;
   if (r >= rows) return;
+  int32_t pos[kTableTokens];
+#pragma unroll
+  for (int u = 0; u < kTableTokens; ++u) pos[u] = t0 + u * rows < p.T ? __ldg(p.positions + t0 + u * rows) : 0;
   const uint64_t turn = p.f.turn[i];
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * rows + r; t < p.T; t += 4 * step) {
-    int32_t pos[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) pos[u] = t + u * step < p.T ? __ldg(p.positions + t + u * step) : 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (t + u * step >= p.T) break;
-      const float2 v = cos_sin(pos[u], turn, p.f.mscale);
-      const int64_t e = (t + u * step) * p.pairs + i;
-      p.cos[e] = v.x;
-      p.sin[e] = v.y;
-    }
+  for (int u = 0; u < kTableTokens; ++u) {
+    const int64_t t = t0 + u * rows;
+    if (t >= p.T) return;
+    const float2 v = cos_sin(pos[u], turn, p.f.mscale);
+    p.cos[t * p.pairs + i] = v.x;
+    p.sin[t * p.pairs + i] = v.y;
   }
 }
 
@@ -410,9 +412,9 @@ mla_status mla_rope_table(const mla_rope_params* params, int32_t T, int32_t rot_
   p.sin = sin;
   p.T = T;
   p.pairs = rot_dim / 2;
-  const int rows = mlarp::kThreads / p.pairs;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((static_cast<int64_t>(T) + rows - 1) / rows, 152 * 4));
-  mlarp::rope_table_kernel<<<grid, mlarp::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const int per_block = mlarp::kTableThreads / p.pairs * mlarp::kTableTokens;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + per_block - 1) / per_block);
+  mlarp::rope_table_kernel<<<grid, mlarp::kTableThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return rope_fail(MLA_ERR_CUDA, "rope table launch: %s", cudaGetErrorString(e));
   return MLA_OK;
