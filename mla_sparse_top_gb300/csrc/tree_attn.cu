@@ -702,14 +702,17 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
   // Waits for the ring's next two slots (their barriers are tested side by side,
   // by even and odd lanes) or for one, and issues the four MMAs of each.  No
   // tcgen05 fence: what the wait orders is shared memory, written by TMA or
-  // fenced by its writers.
+  // fenced by its writers.  After a wait that ran out nothing is issued or
+  // committed: a commit would free a slot whose load is still in flight, and
+  // its producer would arrive on a barrier that has no arrival left to take.
   auto take_slots = [&](bool two, uint32_t d0, uint32_t d1, uint64_t a0, uint64_t a1, uint64_t base, uint32_t b_step,
                         uint32_t idesc, bool first0, bool first1) {
     const int s0 = slot, s1 = slot + 1 == kSlots ? 0 : slot + 1;
     const uint32_t ph1 = phase ^ (s1 == 0 ? 1u : 0u);
     const bool odd = two && (lane & 1);
-    if (!mbar_wait<false>(c.bar(kFull) + 8 * (odd ? s1 : s0), odd ? ph1 : phase, c.abort, c.wait_ns)) *c.abort = 1u;
-    __syncwarp();
+    const bool landed =
+        mbar_wait<false>(c.bar(kFull) + 8 * (odd ? s1 : s0), odd ? ph1 : phase, c.abort, c.wait_ns);
+    if (!__all_sync(0xffffffffu, landed)) return false;
     if (elect_one()) {
       const uint64_t b0 = base + static_cast<uint32_t>(s0 * (kSlotBytes >> 4));
 #pragma unroll
@@ -731,6 +734,7 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
       slot = 0;
       phase ^= 1;
     }
+    return true;
   };
   auto commit = [&](int bar) {
     if (elect_one()) commit2(c.bar(bar));
@@ -743,10 +747,10 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
 #pragma unroll 1
     for (int k = 0; k < kKeyItems; k += 2) {
       const uint64_t a = desc_q + static_cast<uint32_t>(k * (kChunk >> 4));
-      take_slots(k + 1 < kKeyItems, d, d, a, a + (kChunk >> 4), desc_k, 32, idesc_s, k == 0, false);
+      if (!take_slots(k + 1 < kKeyItems, d, d, a, a + (kChunk >> 4), desc_k, 32, idesc_s, k == 0, false)) return false;
     }
     commit(kSFull + (t & 1));
-    return __all_sync(0xffffffffu, *c.abort == 0u) != 0;
+    return true;
   };
   auto values = [&](int t, int groups, bool first) {
     if (!warp_wait(c, kPReady, t & 1)) return false;
@@ -755,10 +759,11 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
     for (int g = 0; g < groups; ++g) {
       const uint64_t a = desc_p + static_cast<uint32_t>(g * (kChunk >> 4));
       const bool begin = first && g == 0;
-      take_slots(true, c.tmem + kTmemO, c.tmem + kTmemO + 128, a, a, desc_v, 2048, idesc_v, begin, begin);
+      if (!take_slots(true, c.tmem + kTmemO, c.tmem + kTmemO + 128, a, a, desc_v, 2048, idesc_v, begin, begin))
+        return false;
     }
     commit(kPvDone);
-    return __all_sync(0xffffffffu, *c.abort == 0u) != 0;
+    return true;
   };
   while (more && ok) {
     const int n = uniform(s.t1 - s.t0);
@@ -785,11 +790,11 @@ __device__ void mma_role(const Params& p, const Ctx& c, const Maps& maps, Walk w
     s = nx;
     more = again;
   }
-  if (lead) {  // every MMA in flight lands before the CTAs leave
-    commit(kFinal);
-    volatile uint32_t never = 0;
-    mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > kDrainNs ? c.wait_ns : kDrainNs);
-  }
+  // every MMA in flight lands, and its arrivals reach both CTAs, before they leave
+  if (lead) commit(kFinal);
+  volatile uint32_t never = 0;
+  mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > kDrainNs ? c.wait_ns : kDrainNs);
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax
