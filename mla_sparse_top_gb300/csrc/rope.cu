@@ -7,11 +7,11 @@
 // here) and no loss at far positions.  Read as a signed fraction of a turn it
 // converts to fp32 with full relative precision, and sincospif takes it.
 //
-// The rotation is bound by memory.  A thread keeps one unit of a head (16
-// bytes, or one pair of values where alignment forbids that) and walks over
-// the rows, (token, head) pairs, of its block, 64 bytes in flight: offsets
-// advance by additions, and the unit's angles stay in registers until the
-// token changes, so nothing is shared between threads and nothing waits.
+// The rotation is bound by memory.  A thread keeps one token and one unit of a
+// head (16 bytes, or one pair of values where alignment forbids that) and walks
+// over heads, 64 bytes in flight: its angles are made once, while the first
+// loads are on their way, offsets advance by one addition, and nothing is
+// shared between threads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,7 +29,7 @@ namespace mlarp {
 constexpr int kThreads = 512;
 constexpr int kTableThreads = 256;
 constexpr int kMaxPairs = 128;  // rot_dim <= 256
-constexpr int kMaxPasses = 16;  // rows of a thread
+constexpr int kMaxPasses = 16;  // heads of a thread
 
 __device__ unsigned int g_rope_status = 0;
 
@@ -84,13 +84,13 @@ struct Tensor {
   const int64_t* rows;
   int64_t num_rows;
   int n_heads, rot_off;
-  int vec;         // 16-byte units
-  int rot_units;   // units of a head that hold rotated values
-  int units;       // all units of a head (in place: the rotated ones)
-  int pass_rows;   // rows that a block takes at a time
-  int pass_t, pass_h;  // the same in tokens and heads
-  int passes;
-  int unit_blocks;  // blocks over the units of a row (more than kThreads units)
+  int rot_units;    // units of a head that hold rotated values
+  int units;        // all units of a head (in place: the rotated ones)
+  int tok_rows;     // tokens of a block
+  int head_rows;    // heads that a block takes at a time
+  int passes;       // times that it does
+  int head_blocks;  // blocks over the heads
+  int unit_blocks;  // blocks over the units of a head (more than kThreads units)
   int blocks;
 };
 
@@ -184,23 +184,23 @@ __device__ __forceinline__ void turn_unit(Pack<E, V>& a, Pack<E, V>& b, const fl
 template <typename E, int V, bool kTwo>
 __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, int block) {
   constexpr int kPairs = kTwo ? V : V / 2;
-  constexpr int kUnroll = kTwo && V > 1 ? 2 : 4;  // rows in flight
+  constexpr int kUnroll = V == 1 ? 3 : (kTwo ? 2 : 4);  // heads in flight
   const int tid = threadIdx.x;
-  const int64_t rows = static_cast<int64_t>(p.T) * w.n_heads;
-  int r, k;
-  int64_t row;
+  int k, r = 0;
   if (w.unit_blocks == 1) {
     r = tid / w.units;
     k = tid - r * w.units;
-    if (r >= w.pass_rows) return;
-    row = static_cast<int64_t>(block) * w.passes * w.pass_rows + r;
+    if (r >= w.tok_rows * w.head_rows) return;
   } else {
     k = block % w.unit_blocks * kThreads + tid;
+    block /= w.unit_blocks;
     if (k >= w.units) return;
-    row = static_cast<int64_t>(block / w.unit_blocks) * w.passes;
   }
-  if (row >= rows) return;
-  const int n = static_cast<int>(min(static_cast<int64_t>(w.passes), (rows - row + w.pass_rows - 1) / w.pass_rows));
+  const int dt = r / w.head_rows;
+  const int64_t t = static_cast<int64_t>(block / w.head_blocks) * w.tok_rows + dt;
+  const int h = block % w.head_blocks * w.passes * w.head_rows + (r - dt * w.head_rows);
+  if (t >= p.T || h >= w.n_heads) return;
+  const int n = min(w.passes, (w.n_heads - h + w.head_rows - 1) / w.head_rows);
   const bool rotated = k < w.rot_units;
   const int second = p.half ? p.pairs : 1;  // distance of a pair's values (kTwo)
   int d, pair0 = 0;
@@ -211,71 +211,58 @@ __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, in
     const int c = (k - w.rot_units) * V;  // copied values, in order
     d = c < w.rot_off ? c : c + 2 * p.pairs;
   }
+  int64_t to = t;
+  if (w.rows != nullptr) {
+    to = __ldg(w.rows + t);
+    if (to >= w.num_rows && k == 0 && h == 0) atomicOr(&g_rope_status, MLA_DEVICE_BAD_BLOCK);
+    if (to < 0 || to >= w.num_rows) return;
+  }
+  const E* x = static_cast<const E*>(w.x) + t * w.xt + h * w.xh + d;
+  E* out = static_cast<E*>(w.out) + to * w.ot + h * w.oh + d;
+  const int64_t x_step = w.head_rows * w.xh, o_step = w.head_rows * w.oh;
+  const int32_t pos = rotated ? __ldg(p.positions + t) : 0;
+  Pack<E, V> a[kUnroll], b[kUnroll];
   float2 cs[kPairs];
-  int t = static_cast<int>(row / w.n_heads);
-  int h = static_cast<int>(row - static_cast<int64_t>(t) * w.n_heads);
-  int angles_of = -1;  // the token whose angles cs holds
-  const E* x = static_cast<const E*>(w.x) + d + t * w.xt + h * w.xh;
-  E* const out = static_cast<E*>(w.out) + d;
-  int64_t o = t * w.ot + h * w.oh;
-  // the next row of this thread: `step` on, or `wrap` on when it enters another token
-  const int64_t x_step = w.pass_t * w.xt + w.pass_h * w.xh, x_wrap = x_step + w.xt - w.n_heads * w.xh;
-  const int64_t o_step = w.pass_t * w.ot + w.pass_h * w.oh, o_wrap = o_step + w.ot - w.n_heads * w.oh;
   for (int it = 0; it < n; it += kUnroll) {
-    Pack<E, V> a[kUnroll], b[kUnroll];
-    int tok[kUnroll];
-    int64_t to[kUnroll];
-    int32_t pos[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      tok[u] = t;
-      to[u] = -1;
-      if (it + u >= n) continue;
-      a[u].load(x);
-      if (kTwo && rotated) b[u].load(x + second);
-      pos[u] = rotated ? __ldg(p.positions + t) : 0;
-      to[u] = o;
-      if (w.rows != nullptr) {
-        const int64_t row_to = __ldg(w.rows + t);
-        if (row_to >= w.num_rows && k == 0 && h == 0) atomicOr(&g_rope_status, MLA_DEVICE_BAD_BLOCK);
-        to[u] = row_to < 0 || row_to >= w.num_rows ? -1 : row_to * w.ot + h * w.oh;
+      if (it + u < n) {
+        a[u].load(x);
+        if (kTwo && rotated) b[u].load(x + second);
       }
-      t += w.pass_t;
-      h += w.pass_h;
-      const bool next = h >= w.n_heads;
-      if (next) {
-        h -= w.n_heads;
-        ++t;
+      x += x_step;
+    }
+    if (it == 0 && rotated) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        cs[i] = cos_sin(pos, p.f.turn[pair0 + i], p.f.mscale);
+        if (p.inverse) cs[i].y = -cs[i].y;
       }
-      x += next ? x_wrap : x_step;
-      o += next ? o_wrap : o_step;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (to[u] < 0) continue;  // no row, or none to write
-      if (rotated) {
-        if (tok[u] != angles_of) {
-          angles_of = tok[u];
-#pragma unroll
-          for (int i = 0; i < kPairs; ++i) {
-            cs[i] = cos_sin(pos[u], p.f.turn[pair0 + i], p.f.mscale);
-            if (p.inverse) cs[i].y = -cs[i].y;
-          }
+      if (it + u < n) {
+        if (rotated) {
+          turn_unit<E, V, kTwo>(a[u], b[u], cs);
+          if (kTwo) b[u].store(out + second);
         }
-        turn_unit<E, V, kTwo>(a[u], b[u], cs);
-        if (kTwo) b[u].store(out + to[u] + second);
+        a[u].store(out);
       }
-      a[u].store(out + to[u]);
+      out += o_step;
     }
   }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ Params p) {
+// kVec: both tensors in 16-byte units: 403 + 403 MB in 116 us, 98% of a copy's
+// rate.  Otherwise both go pair by pair, in a kernel of its own with half the
+// registers and twice the threads: bound by issue (4 bytes an access), 30 + 30
+// MB in 20 us; with two blocks an SM and four heads in flight 27 us.
+template <typename E, bool kVec>
+__global__ void __launch_bounds__(kThreads, kVec ? 2 : 4) rope_kernel(const __grid_constant__ Params p) {
   const int second = static_cast<int>(blockIdx.x) >= p.t[0].blocks;
   const int block = static_cast<int>(blockIdx.x) - (second ? p.t[0].blocks : 0);
   const Tensor& w = p.t[second];
-  if (!w.vec) rotate_rows<E, 1, true>(p, w, block);
+  if constexpr (!kVec) rotate_rows<E, 1, true>(p, w, block);
   else if (p.half) rotate_rows<E, 16 / sizeof(E), true>(p, w, block);
   else rotate_rows<E, 16 / sizeof(E), false>(p, w, block);
 }
@@ -333,8 +320,8 @@ mla_status make_freqs(const mla_rope_params* q, int rot, mlarp::Freqs* f) {
   return MLA_OK;
 }
 
-// Checks one tensor and splits its rows into blocks.
-mla_status make_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const char* name, mlarp::Tensor* w) {
+// Checks one tensor; *vec stays set if its rows and parts are 16-byte aligned.
+mla_status check_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const char* name, bool* vec) {
   if (!q->x || !q->out) return rope_fail(MLA_ERR_NULL, "%s: a required pointer is NULL", name);
   if (q->n_heads < 1 || q->rot_off < 0 || static_cast<int64_t>(q->rot_off) + d.rot_dim > q->head_dim)
     return rope_fail(MLA_ERR_SHAPE, "%s: n_heads=%d must be >= 1 and the head's %d values hold [rot_off, rot_off + rot_dim)",
@@ -363,8 +350,14 @@ mla_status make_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const c
     return rope_fail(MLA_ERR_ALIGN, "%s: tensors must be aligned to their elements", name);
   const int64_t parts[] = {q->x_token_stride, q->x_head_stride,  q->out_token_stride, q->out_head_stride,
                            q->head_dim,       q->rot_off,        d.half ? d.rot_dim / 2 : d.rot_dim};
-  w->vec = aligned(q->x, 16) && aligned(q->out, 16);
-  for (int64_t v : parts) w->vec = w->vec && v % V == 0;
+  *vec = *vec && aligned(q->x, 16) && aligned(q->out, 16);
+  for (int64_t v : parts) *vec = *vec && v % V == 0;
+  return MLA_OK;
+}
+
+// Splits a checked tensor's rows into blocks.
+mla_status split_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const char* name, bool vec, mlarp::Tensor* w) {
+  const bool same = q->x == q->out;
   w->x = q->x;
   w->out = q->out;
   w->xt = q->x_token_stride;
@@ -375,18 +368,21 @@ mla_status make_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const c
   w->num_rows = q->num_rows;
   w->n_heads = q->n_heads;
   w->rot_off = q->rot_off;
-  const int width = w->vec ? V : 1;
-  w->rot_units = w->vec && !d.half ? d.rot_dim / V : d.rot_dim / 2 / width;
+  const int width = !vec ? 1 : (d.dtype == MLA_ROPE_FP32 ? 4 : 8);
+  w->rot_units = vec && !d.half ? d.rot_dim / width : d.rot_dim / 2 / width;
   w->units = w->rot_units + (same ? 0 : (q->head_dim - d.rot_dim) / width);
   w->unit_blocks = (w->units + mlarp::kThreads - 1) / mlarp::kThreads;
-  w->pass_rows = w->unit_blocks > 1 ? 1 : mlarp::kThreads / w->units;
-  w->pass_t = w->pass_rows / q->n_heads;
-  w->pass_h = w->pass_rows % q->n_heads;
-  // several rows per thread once there is a block for every SM twice over
-  const int64_t all = static_cast<int64_t>(d.T) * q->n_heads, passes = (all + w->pass_rows - 1) / w->pass_rows;
-  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(mlarp::kMaxPasses, passes / (2 * 152))));
-  if (w->passes > 4) w->passes = w->passes / 4 * 4;
-  const int64_t blocks = (passes + w->passes - 1) / w->passes * w->unit_blocks;
+  const int rows = w->unit_blocks > 1 ? 1 : mlarp::kThreads / w->units;
+  w->tok_rows = std::min(rows, d.T);
+  w->head_rows = std::min(rows / w->tok_rows, q->n_heads);
+  // several heads per thread once there is a block for every SM twice over
+  const int64_t toks = (static_cast<int64_t>(d.T) + w->tok_rows - 1) / w->tok_rows;
+  const int turns = (q->n_heads + w->head_rows - 1) / w->head_rows;
+  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(turns, mlarp::kMaxPasses),
+                                                                      toks * turns / (2 * 152))));
+  w->head_blocks = (turns + w->passes - 1) / w->passes;
+  w->passes = (turns + w->head_blocks - 1) / w->head_blocks;  // even shares
+  const int64_t blocks = toks * w->head_blocks * w->unit_blocks;
   if (blocks >= (1ll << 30)) return rope_fail(MLA_ERR_SHAPE, "%s: T x heads too large", name);
   w->blocks = static_cast<int>(blocks);
   return MLA_OK;
@@ -434,14 +430,15 @@ mla_status mla_rope_apply(const mla_rope_dims* dims, const mla_rope_params* para
   if (d.T == 0) return MLA_OK;
   if (!positions) return rope_fail(MLA_ERR_NULL, "positions is NULL");
   if (!aligned(positions, 4)) return rope_fail(MLA_ERR_ALIGN, "positions must be 4-byte aligned");
-  st = make_tensor(q, d, "q", &p.t[0]);
+  bool vec = true;
+  st = check_tensor(q, d, "q", &vec);
+  if (st == MLA_OK && k != nullptr) st = check_tensor(k, d, "k", &vec);
+  if (st == MLA_OK) st = split_tensor(q, d, "q", vec, &p.t[0]);
   if (st != MLA_OK) return st;
   p.t[1] = p.t[0];
   p.t[1].blocks = 0;
-  if (k != nullptr) {
-    st = make_tensor(k, d, "k", &p.t[1]);
-    if (st != MLA_OK) return st;
-  }
+  if (k != nullptr) st = split_tensor(k, d, "k", vec, &p.t[1]);
+  if (st != MLA_OK) return st;
   p.positions = positions;
   p.T = d.T;
   p.pairs = d.rot_dim / 2;
@@ -449,9 +446,10 @@ mla_status mla_rope_apply(const mla_rope_dims* dims, const mla_rope_params* para
   p.inverse = d.inverse;
   const unsigned grid = static_cast<unsigned>(p.t[0].blocks + p.t[1].blocks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d.dtype == MLA_ROPE_BF16) mlarp::rope_kernel<__nv_bfloat16><<<grid, mlarp::kThreads, 0, s>>>(p);
-  else if (d.dtype == MLA_ROPE_FP16) mlarp::rope_kernel<__half><<<grid, mlarp::kThreads, 0, s>>>(p);
-  else mlarp::rope_kernel<float><<<grid, mlarp::kThreads, 0, s>>>(p);
+  void (*kernels[3][2])(mlarp::Params) = {{mlarp::rope_kernel<__nv_bfloat16, false>, mlarp::rope_kernel<__nv_bfloat16, true>},
+                                          {mlarp::rope_kernel<__half, false>, mlarp::rope_kernel<__half, true>},
+                                          {mlarp::rope_kernel<float, false>, mlarp::rope_kernel<float, true>}};
+  kernels[d.dtype][vec ? 1 : 0]<<<grid, mlarp::kThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return rope_fail(MLA_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
   return MLA_OK;
