@@ -143,6 +143,7 @@ struct Params {
   int team, teams;  // clusters of a team, teams
   float scale_log2;
   int out32;
+  int once;  // one cluster reads a key, once as a key and once as a value: 2% where memory binds
   unsigned long long wait_ns;
 };
 
@@ -239,6 +240,14 @@ __device__ __forceinline__ void tma_pair(uint32_t dst, const void* map, int x, i
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// The same for a box that is not read again: L2 gives its lines up first.
+__device__ __forceinline__ void tma_pair_last(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
 }
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -496,8 +505,13 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, c
       if (lane == 0) {
         if (mend) mbar_arrive_expect_tx(bar, kSlotBytes);
         else arrive_lead_tx(bar, kSlotBytes);
-        tma_pair(slot, &maps.val, cur.dim0, cur.row, bar);
-        tma_pair(slot + kChunk, &maps.val, cur.dim0 + 64, cur.row, bar);
+        if (p.once) {
+          tma_pair_last(slot, &maps.val, cur.dim0, cur.row, bar);
+          tma_pair_last(slot + kChunk, &maps.val, cur.dim0 + 64, cur.row, bar);
+        } else {
+          tma_pair(slot, &maps.val, cur.dim0, cur.row, bar);
+          tma_pair(slot + kChunk, &maps.val, cur.dim0 + 64, cur.row, bar);
+        }
       }
       __syncwarp();
       if (mend) {
@@ -1275,8 +1289,11 @@ inline int team_size(int blocks, int clusters, bool ragged) {
 
 // A sequence of several row blocks has its INT8 rows converted once, into the
 // workspace, rather than by every cluster that reads them (each converts a key
-// twice: as a key and as a value).  @@MEASURED@@
-constexpr int kExpandBlocks = 2;
+// twice: as a key and as a value).  Converted by the clusters / expanded first,
+// us: one row block, 64 sequences of 8192: 203 / 289; two, the same: 378 / 359,
+// 64 of 100 to 8192: 117 / 130, 16 of 3000: 58 / 56; 17, 13 of 500 to 20000: 425
+// / 255; 64, one of 32768: 705 / 327.
+constexpr int kExpandBlocks = 3;
 constexpr size_t kExpandBytes = size_t(4) << 30;  // workspace spent on it at most
 
 struct Plan {
@@ -1491,6 +1508,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   p.teams = plan.teams;
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   p.out32 = aligned(out, 32) ? 1 : 0;
+  p.once = plan.blocks == 1 ? 1 : 0;
   p.wait_ns = mlasp::host_wait_limit_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const void* latent = kv_nope;
