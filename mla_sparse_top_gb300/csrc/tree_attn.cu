@@ -64,7 +64,8 @@ using namespace mlasp;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kProducerWarp0 = 8;
 // bf16: seven ring slots, a producer warp each.  INT8: four slots, filled from
-// five raw slots by two groups of four converter warps, and a load warp.
+// three raw slots of two items each by two groups of four converter warps, and a
+// load warp.
 template <bool kInt8>
 struct Conf {
   static constexpr int kSlots = kInt8 ? 4 : 7;
@@ -76,7 +77,7 @@ struct Conf {
   static constexpr int kRegs = kInt8 ? 96 : 128, kSoftmaxRegs = 112, kConvertRegs = 80;
   static_assert(256 * kSoftmaxRegs + 256 * kConvertRegs <= 512 * 96, "register budget");
 };
-constexpr int kRawSlots = 5;
+constexpr int kRawSlots = 3;
 constexpr int kMaxThreads = 576;
 static_assert(Conf<false>::kThreads == 512 && Conf<true>::kThreads == kMaxThreads, "roles");
 
@@ -85,7 +86,7 @@ constexpr int kTile = 256;
 constexpr int kPage = 128;
 constexpr int kKeyItems = 9;  // 64-dim slices of 576
 constexpr int kSlotBytes = 16384;
-constexpr int kRawCodes = 8192;                 // 128 keys x 64 codes or 64 keys x 128 codes
+constexpr int kRawCodes = 16384;  // two items: 128 keys x 128 codes, or twice 64 keys x 128 codes
 constexpr int kRawBytes = kRawCodes + 128 * 16;  // and the rows' four scales
 constexpr int kChunk = 8192;  // 64 rows of 128 bytes
 constexpr int kOffQ = 0;
@@ -534,18 +535,21 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, c
   }
 }
 
-// INT8: one warp requests the codes and scales of every latent item.
+// INT8: one warp requests the codes and scales, two items at a time (rows of
+// 128 bytes: with 64 the load engine's rate per row would bind).
 __device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int lane) {
   const int rank = static_cast<int>(c.rank);
   int slot = 0;
   uint32_t phase = 1;
-  auto load = [&](const CUtensorMap& codes, const CUtensorMap& scales, int dim0, int row, int rows) {
+  // keys: 128 rows, dims [dim0, dim0 + 128); values: 64 rows, both halves of the output dims
+  auto load = [&](bool value, int dim0, int row) {
     if (!warp_wait(c, kRawEmpty + slot, phase)) return false;
     if (lane == 0) {
       const uint32_t bar = c.bar(kRawFull + slot), dst = c.sb + kOffRaw + slot * kRawBytes;
-      mbar_arrive_expect_tx(bar, kRawCodes + rows * 16);
-      tma_pair(dst, &codes, dim0, row, bar);
-      tma_pair(dst + kRawCodes, &scales, 0, row >> 6, bar);
+      mbar_arrive_expect_tx(bar, kRawCodes + (value ? 64 : 128) * 16);
+      tma_pair(dst, value ? &maps.val : &maps.key, dim0, row, bar);
+      if (value) tma_pair(dst + kChunk, &maps.val, dim0 + 256, row, bar);
+      tma_pair(dst + kRawCodes, value ? &maps.val_scale : &maps.key_scale, 0, row >> 6, bar);
     }
     __syncwarp();
     if (++slot == kRawSlots) {
@@ -562,13 +566,13 @@ __device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, W
       if (u < s.t1) {
         next[0] = page_row(p, s, 2 * u);
         next[1] = page_row(p, s, 2 * u + 1);
-        for (int k = 0; k < 8; ++k)
-          if (!load(maps.key, maps.key_scale, 64 * k, next[rank], kPage)) return;
+        for (int k = 0; k < 4; ++k)
+          if (!load(false, 128 * k, next[rank])) return;
       }
       if (u > s.t0) {
-        const int items = 2 * groups_of(s, u - 1);
-        for (int k = 0; k < items; ++k)
-          if (!load(maps.val, maps.val_scale, (k & 1) * 256 + rank * 128, rows[k >> 2] + ((k >> 1) & 1) * 64, 64)) return;
+        const int groups = groups_of(s, u - 1);
+        for (int g = 0; g < groups; ++g)
+          if (!load(true, rank * 128, rows[g >> 1] + (g & 1) * 64)) return;
       }
       rows[0] = next[0];
       rows[1] = next[1];
@@ -576,54 +580,39 @@ __device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, W
   }
 }
 
-// INT8: converter warp w of group w / 4 turns a quarter of every kGroups-th
-// item into bf16, 16 codes of a lane at a time; codes lie as TMA left them, row
-// by row, so a warp reads 512 adjacent bytes.
+// INT8: converter warp w belongs to group w / 4 and turns a quarter of one of a
+// raw slot's two items into bf16, 16 codes of a lane at a time.
 __device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int w, int lane) {
-  constexpr int kSlots = Conf<true>::kSlots, kGroups = Conf<true>::kProducers / 4;
-  const int rank = static_cast<int>(c.rank), quarter = w & 3;
-  int turn = w >> 2;  // items until this group's next one
-  int slot = 0, raw = 0;
-  uint32_t phase = 1, raw_phase = 0;
-  auto pass = [&](bool latent) {  // on to the next item
-    if (turn-- == 0) turn = kGroups - 1;
-    if (++slot == kSlots) {
-      slot = 0;
-      phase ^= 1;
-    }
-    if (latent && ++raw == kRawSlots) {
-      raw = 0;
-      raw_phase ^= 1;
-    }
-  };
+  static_assert(Conf<true>::kSlots == 4 && Conf<true>::kProducers == 8, "two groups, four slots");
+  const int rank = static_cast<int>(c.rank), group = w >> 2, quarter = w & 3;
+  uint32_t item = group;  // the group's next item, counted over all items
+  int raw = 0;
+  uint32_t raw_phase = 0;
+  auto free_slot = [&](uint32_t i) { return warp_wait(c, kEmpty + (i & 3), ((i >> 2) & 1) ^ 1); };
   // rows of 64 (us = 2) or 128 codes (us = 3); from row `mend` on the value rows
   // lose their NaN and infinities, from row `end` on they are zero
-  auto convert = [&](auto us_, int dim0, int mend, int end) {
+  auto convert = [&](auto us_, int scale, int mend, int end) {
     constexpr int us = decltype(us_)::value;
-    if (turn != 0) {
-      pass(true);
-      return true;
-    }
     if (!warp_wait(c, kRawFull + raw, raw_phase)) return false;
     const uint32_t src = c.sb + kOffRaw + raw * kRawBytes;
-    const int unit0 = quarter * 128 + lane;
+    // unit0 + 32 k lies 8 (us = 2) or 4 rows on, in the same column
+    const int unit0 = quarter * 128 + lane, r0 = unit0 >> us, col = unit0 & ((1 << us) - 1);
+    const uint32_t codes = src + (us == 2 ? group * 64 + r0 * 128 : group * kChunk + r0 * 128) + col * 16;
     uint4 v[4];
     float sc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int unit = unit0 + 32 * k;
+      const int dr = (32 * k) >> us;
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(src + unit * 16));
-      asm volatile("ld.shared.f32 %0, [%1];"
-                   : "=f"(sc[k]) : "r"(src + kRawCodes + (unit >> us) * 16 + 4 * (dim0 >> 7)));
+                   : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(codes + dr * 128));
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc[k]) : "r"(src + kRawCodes + (r0 + dr) * 16 + 4 * scale));
     }
-    if (!warp_wait(c, kEmpty + slot, phase)) return false;
-    // unit0 + 32 k lies 8 (us = 2) or 4 rows on, in the same column
-    const int col = unit0 & ((1 << us) - 1), u0 = 2 * (col & 3);
-    const uint32_t dst0 = c.sb + kOffRing + slot * kSlotBytes + (col >> 2) * kChunk;
+    if (!free_slot(item)) return false;
+    const int u0 = 2 * (col & 3);
+    const uint32_t dst0 = c.sb + kOffRing + (item & 3) * kSlotBytes + (col >> 2) * kChunk;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int r = (unit0 >> us) + ((32 * k) >> us);
+      const int r = r0 + ((32 * k) >> us);
       uint4 a, b;
       dequant4(v[k].x, sc[k], a.x, a.y);
       dequant4(v[k].y, sc[k], a.z, a.w);
@@ -639,41 +628,47 @@ __device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Wa
     fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
     __syncwarp();
     if (lane == 0) {
-      arrive_lead(c.lead(kFull) + 8 * slot);
+      arrive_lead(c.lead(kFull) + 8 * (item & 3));
       mbar_arrive(c.bar(kRawEmpty + raw));
     }
-    pass(true);
+    if (++raw == kRawSlots) {
+      raw = 0;
+      raw_phase ^= 1;
+    }
+    item += 2;
     return true;
   };
   Segment s;
   while (walk.next(p, s)) {
     for (int u = s.t0; u <= s.t1; ++u) {
       if (u < s.t1) {
+        const int row = page_row(p, s, 2 * u + rank);  // of the rope rows
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          if (!convert(std::integral_constant<int, 2>(), 64 * k, 0, 0)) return;
-        if (turn == 0) {  // rope rows are bf16: straight into the slot
-          const int row = page_row(p, s, 2 * u + rank);
-          if (!warp_wait(c, kEmpty + slot, phase)) return;
+        for (int k = 0; k < 4; ++k)
+          if (!convert(std::integral_constant<int, 2>(), k, 0, 0)) return;
+        // the rope rows are bf16: straight into the slot
+        const uint32_t i = item - group;
+        if (group == 0) {
+          if (!free_slot(i)) return;
           if (lane == 0) {
-            const uint32_t full = c.lead(kFull) + 8 * slot;
+            const uint32_t full = c.lead(kFull) + 8 * (i & 3);
             if (quarter == 0) {
               arrive_lead_tx(full, kSlotBytes);
-              tma_pair(c.sb + kOffRing + slot * kSlotBytes, &maps.rope, 0, row, full);
+              tma_pair(c.sb + kOffRing + (i & 3) * kSlotBytes, &maps.rope, 0, row, full);
             } else {
               arrive_lead(full);
             }
           }
           __syncwarp();
         }
-        pass(false);
+        ++item;
       }
       if (u > s.t0) {
-        const int items = 2 * groups_of(s, u - 1);
+        const int groups = groups_of(s, u - 1);
 #pragma unroll 1
-        for (int k = 0; k < items; ++k) {
-          const int base = kTile * (u - 1) + 64 * (k >> 1);
-          if (!convert(std::integral_constant<int, 3>(), (k & 1) * 256 + rank * 128, s.ctx - base, s.act - base)) return;
+        for (int g = 0; g < groups; ++g) {
+          const int base = kTile * (u - 1) + 64 * g;
+          if (!convert(std::integral_constant<int, 3>(), 2 * group + rank, s.ctx - base, s.act - base)) return;
         }
       }
     }
@@ -1042,7 +1037,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
     if (c.rank == 0) p.records[cid] = make_int4(0, 0, 0, 0);  // nothing to merge, until this thread finds a cut
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(c.bar(kRawFull + i), 1);
-      mbar_init(c.bar(kRawEmpty + i), K::kFillers);
+      mbar_init(c.bar(kRawEmpty + i), K::kProducers);
     }
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(c.bar(kFull + i), 2 * K::kFillers);
@@ -1529,7 +1524,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   if (codes) {  // codes and scales as they lie
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const CUtensorMapSwizzle flat = CU_TENSOR_MAP_SWIZZLE_NONE;
-    if (ms == MLA_OK) ms = tmap(&maps.key, u8, 1, kv_nope, 512, rows, 64, 128, flat, "kv_nope");
+    if (ms == MLA_OK) ms = tmap(&maps.key, u8, 1, kv_nope, 512, rows, 128, 128, flat, "kv_nope");
     if (ms == MLA_OK) ms = tmap(&maps.val, u8, 1, kv_nope, 512, rows, 128, 64, flat, "kv_nope");
     // the scales of 64 rows as one row of the map: 1 KB at a time instead of 16 bytes
     if (ms == MLA_OK) ms = tmap(&maps.key_scale, f32, 4, kv_scales, 256, rows / 64, 256, 2, flat, "kv_scales");
