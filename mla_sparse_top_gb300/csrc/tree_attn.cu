@@ -11,24 +11,25 @@
 // lane 64 + m for the second.  No score crosses between the CTAs.
 //
 // Operands.  Q (64 rows x 576) stays in shared memory.  Keys and values stream
-// through a ring of seven 16 KB slots, each four MMAs long:
+// through a ring of seven 16 KB slots, each four MMAs long (259 clocks):
 //   key slot    64 dims of the CTA's 128 keys: CTA r takes page 2 t + r of tile t
 //   value slot  64 keys of the CTA's 128 output dims
 // The MMA reads a value from the CTA that owns its output column but a key
 // from the CTA that owns the key, so every latent value comes in twice (once
 // as a key half, once as a value half): 2176 bytes per key and pair, 62 bytes
-// per clock and SM at the full MMA rate, below the ~72 that an SM takes in.
+// per clock and SM at the full MMA rate, below the ~77 that an SM's loads from
+// L2 reach.
 //
-// Warps of a CTA (512 threads):
+// Warps of a CTA:
 //   0-7   softmax: S (64 x 256 scores as 128 lanes x 128 columns) from tensor
 //         memory, mask, running maximum (lazily moved, shared by the four
 //         threads of a row) and sum, P in bf16 to shared memory, rescaling
 //         of O, the epilogue
-//   8-14  producers, one per ring slot: TMA, or loads, conversion and stores
-//         where a value has to be changed on the way (INT8 rows; the tiles at
-//         the end of a sequence, whose unwritten rows and masked drafts must
-//         not reach the second product as NaN or infinity: 0 * NaN)
-//   15    MMA issue (CTA 0) and the loads of Q (each CTA)
+//   bf16: 8-14  producers, one per ring slot: TMA; where a tile holds drafted
+//         or unwritten rows, the values are mended in shared memory, since NaN
+//         or infinity behind a weight of 0 would reach the second product
+//   INT8: 8-15  converters, one warp that loads codes and scales (Conf<true>)
+//   the last but INT8's load warp: MMA issue (CTA 0) and the loads of Q (each CTA)
 // S is double buffered: S(t + 1) is computed while the softmax of tile t runs.
 //
 // Schedule.  Clusters form teams of g that take g row blocks of a sequence
@@ -37,6 +38,20 @@
 // A row block cut between teams leaves partial states in the workspace, and a
 // second launch merges them.  Which cluster takes what follows from the
 // lengths alone, so results do not depend on timing.
+//
+// Measured (bf16).  64 sequences x 8 drafts x 128 heads over 8192 positions:
+// 837 us, 1.40 PFLOP/s, 71% of the measured bf16 rate (79% of the sustained
+// one); one sequence, 64 drafts, 131072 positions: 1.55 ms, 1.51 PFLOP/s.
+// Bound there: a tile of 256 keys takes ~5200 clocks where its MMAs take 4406,
+// and the SM clock falls to ~1.6 GHz under the power cap.  Single tokens, 64
+// sequences of 8192: 148 us, 604 MB at 4.1 TB/s: bound by memory, with ~8000
+// clocks a tile; prefetching the next tile's keys into L2, by the load engine or
+// by threads, made it 8% slower, two tiles ahead 35% (lines leave L2 before
+// they are used: 1.04 GB read instead of 0.68).
+// What shaped the kernel, at the largest case (us): arrivals on the other CTA's
+// barriers with release at CTA scope instead of cluster scope 2018 -> 1682; a
+// converged warp around an elected issuer instead of one running thread 2584 ->
+// 2081; uniform control and two ring slots per turn 1682 -> 1575.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -92,11 +107,11 @@ constexpr int kChunk = 8192;  // 64 rows of 128 bytes
 constexpr int kOffQ = 0;
 constexpr int kOffP = kOffQ + kKeyItems * kChunk;
 constexpr int kOffRing = kOffP + 4 * kChunk;
-constexpr int kOffRaw = kOffRing + Conf<true>::kSlots * kSlotBytes;  // INT8 only
+constexpr int kOffRaw = kOffRing + Conf<true>::kSlots * kSlotBytes;  // INT8
 constexpr int kOffExch = kOffRaw + kRawSlots * kRawBytes;            // float [2][4][64]
 static_assert(kOffExch >= kOffRing + Conf<false>::kSlots * kSlotBytes, "ring");
-constexpr int kOffScan = kOffExch + 2048;           // int64 [warps]
-constexpr int kOffWalk = kOffScan + kMaxThreads / 32 * 8;               // int64 first sequence, offset, tiles of the share, total
+constexpr int kOffScan = kOffExch + 2048;                    // int64 [warps]
+constexpr int kOffWalk = kOffScan + kMaxThreads / 32 * 8;  // int64 [4]: a share's first sequence and its stream position
 constexpr int kOffBars = kOffWalk + 32;
 constexpr int kMaxSlots = 7;
 constexpr int kFull = 0;                   // [kMaxSlots], in CTA 0: both CTAs have filled the slot
@@ -581,7 +596,11 @@ __device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, W
 }
 
 // INT8: converter warp w belongs to group w / 4 and turns a quarter of one of a
-// raw slot's two items into bf16, 16 codes of a lane at a time.
+// raw slot's two items into bf16, 16 codes of a lane at a time.  This binds the
+// INT8 kernel (64 single tokens over 8192 positions: 193 us, 344 MB; bf16 148
+// us, 604 MB): an item takes a group ~1700 clocks, half of it arithmetic, and
+// there is one for every 259 clocks of MMA.  Loads by the converters themselves,
+// one item ahead in registers, took 274 us; a third group of warps 201 us.
 __device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int w, int lane) {
   static_assert(Conf<true>::kSlots == 4 && Conf<true>::kProducers == 8, "two groups, four slots");
   const int rank = static_cast<int>(c.rank), group = w >> 2, quarter = w & 3;
@@ -1122,7 +1141,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
 
 // ------------------------------------------------------------------ INT8 rows to bf16
 // Every used page of every sequence once, 16 codes of a thread at a time, into
-// rows of the same number.  Bound by memory (656 bytes in, 1024 out per row).
+// rows of the same number.  Bound by memory: 656 bytes in, 1024 out per row;
+// 13 sequences of 500 to 20000 positions, 67 thousand rows, in 24 us.
 __global__ void __launch_bounds__(256) tree_dequant_kernel(const int8_t* __restrict__ codes,
                                                            const __grid_constant__ Params p, uint16_t* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1168,8 +1188,9 @@ __global__ void __launch_bounds__(256) tree_dequant_kernel(const int8_t* __restr
 // Joins the parts of a row block that was cut between teams.  Block x looks at
 // the record of cluster x (the one the row block starts in), block y takes 16
 // columns of the 256 of one CTA; thread L of each group is lane L of the parts'
-// units.  One group for the usual two or three parts; four that share out the
-// parts where a few long sequences have one from almost every team.
+// units.  One group for the usual two or three parts (75 row blocks in 8 us);
+// four that share out the parts where a few long sequences have one from almost
+// every team (with four for the former, one block an SM fits: 19 us).
 template <int kMergeGroups>
 __global__ void __launch_bounds__(128 * kMergeGroups) tree_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's stores are visible
