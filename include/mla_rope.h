@@ -63,7 +63,7 @@ typedef struct mla_rope_params {
   double orig_positions;  /* trained length (YARN), >= 1 */
   double beta_fast;       /* turns within it above which a pair keeps its angle (YARN), > 0 */
   double beta_slow;       /* turns below which it is stretched in full (YARN), in (0, beta_fast] */
-  double mscale;          /* magnitude on cosine and sine, finite and > 0 */
+  double mscale;          /* magnitude on cosine and sine, > 0 and finite in fp32 */
   int32_t scaling;        /* mla_rope_scaling */
 } mla_rope_params;
 

@@ -69,7 +69,14 @@ size_t mla_tree_workspace_bytes(const mla_dims* dims);
  * tree_mask   uint64 [B*S1, ceil(S1 / 64)] or NULL; bits at and beyond n_b are ignored
  * out         bf16 [B*S1, n_q, 512], lse fp32 [B*S1, n_q] or NULL
  * workspace   >= mla_tree_workspace_bytes(dims) bytes, 256-byte aligned
- * q, kv, out and scales 16-byte aligned, tree_mask 8-byte, the rest 4-byte.
+ * q, kv, out and scales 16-byte aligned, tree_mask 8-byte, the rest 4-byte;
+ * out, lse and the workspace may not overlap one another or the inputs.
+ * Up to three launches on `stream` (INT8 rows of calls with three or more
+ * blocks of 128 rows are turned into bf16 in the workspace first, if that
+ * takes no more than 4 GB; the attention; the merge of rows whose keys several
+ * clusters shared), capturable into a CUDA graph.  The first call on each
+ * device sets the kernels' shared-memory attribute and looks up the driver's
+ * tensor-map encoder: make it before any stream capture begins.
  */
 mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const void* q_rope, const void* kv_nope,
                              const void* kv_rope, const float* kv_scales, const int32_t* block_table,

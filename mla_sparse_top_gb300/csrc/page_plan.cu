@@ -305,6 +305,16 @@ mla_status page_fail(mla_status s, const char* fmt, ...) {
 
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 
+struct Range {
+  const void* ptr;
+  int64_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  if (!a.ptr || !b.ptr) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.ptr), y = reinterpret_cast<uintptr_t>(b.ptr);
+  return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
 }  // namespace
 
 extern "C" {
@@ -333,6 +343,16 @@ mla_status mla_page_plan(const mla_page_dims* dims, const mla_page_io* io, void*
     if (!aligned(w, 4)) return page_fail(MLA_ERR_ALIGN, "int32 tensors must be 4-byte aligned");
   if (!aligned(io->cache_index, 8) || !aligned(io->tree_mask, 8))
     return page_fail(MLA_ERR_ALIGN, "cache_index and tree_mask must be 8-byte aligned");
+  // every block adds up the lengths of the sequences before its own: nothing it reads may be an output
+  const int64_t B = d.B, T = d.T, words64 = (static_cast<int64_t>(d.S1) + 63) / 64;
+  const Range in[] = {{io->ctx_lens, 4 * B}, {io->new_lens, 4 * B}, {io->free_blocks, 4ll * d.num_free},
+                      {io->parents, 4 * T}};
+  const Range out[] = {{io->block_table, 4 * B * d.max_blocks_per_seq}, {io->act_seqs, 4 * B}, {io->cache_index, 8 * T},
+                       {io->positions, 4 * T}, {io->seq_ids, 4 * T}, {io->cu_seqs, 4 * (B + 1)},
+                       {io->tree_mask, 8 * T * words64}, {io->num_taken, 4}};
+  for (const Range& o : out)
+    for (const Range& i : in)
+      if (overlap(i, o)) return page_fail(MLA_ERR_UNSUPPORTED, "an output overlaps an input");
   mlapg::Params p;
   p.io = *io;
   p.B = d.B;

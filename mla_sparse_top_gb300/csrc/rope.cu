@@ -292,7 +292,8 @@ mla_status make_freqs(const mla_rope_params* q, int rot, mlarp::Freqs* f) {
   if (q->scaling < MLA_ROPE_NONE || q->scaling > MLA_ROPE_YARN)
     return rope_fail(MLA_ERR_SHAPE, "scaling %d unknown", q->scaling);
   if (!(q->theta > 1.0) || !isfinite(q->theta)) return rope_fail(MLA_ERR_SHAPE, "theta must be finite and above 1");
-  if (!(q->mscale > 0.0) || !isfinite(q->mscale)) return rope_fail(MLA_ERR_SHAPE, "mscale must be finite and above 0");
+  if (!(q->mscale > 0.0) || !isfinite(static_cast<float>(q->mscale)))
+    return rope_fail(MLA_ERR_SHAPE, "mscale must be above 0 and finite in fp32");
   if (q->scaling != MLA_ROPE_NONE && (!(q->factor >= 1.0) || !isfinite(q->factor)))
     return rope_fail(MLA_ERR_SHAPE, "factor must be finite and at least 1");
   const bool yarn = q->scaling == MLA_ROPE_YARN;

@@ -1110,11 +1110,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
       if constexpr (kInt8) raw_load_role(p, c, maps, walk, lane);
     }
   }
-  if (p.tree_lens != nullptr) {  // padding tokens of row blocks that nobody works on
-    for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.B) * p.S1; t += gridDim.x) {
-      const int b = static_cast<int>(t / p.S1), r0 = static_cast<int>(t - static_cast<int64_t>(b) * p.S1) * p.n_q;
-      const int done = load_seq(p, b).blocks * kRowBlock;
-      for (int r = max(r0, done) + (tid >> 5); r < r0 + p.n_q; r += K::kThreads / 32) {
+  if (p.tree_lens != nullptr) {  // rows of row blocks without a drafted token, which no cluster takes
+    const int grid = static_cast<int>(gridDim.x), sharers = max(1, grid / p.B);
+    for (int w = blockIdx.x; w < p.B * sharers; w += grid) {
+      const int b = w % p.B, part = w / p.B;
+      for (int r = load_seq(p, b).blocks * kRowBlock + part * (K::kThreads / 32) + (tid >> 5); r < p.rows;
+           r += sharers * (K::kThreads / 32)) {
         const int64_t row = static_cast<int64_t>(b) * p.rows + r;
         for (int k = lane; k < 64; k += 32) reinterpret_cast<uint4*>(p.out + row * 512)[k] = make_uint4(0, 0, 0, 0);
         if (lane == 0 && p.lse != nullptr) p.lse[row] = -INFINITY;
@@ -1312,29 +1313,43 @@ inline int team_size(int blocks, int clusters, bool ragged) {
 constexpr int kExpandBlocks = 3;
 constexpr size_t kExpandBytes = size_t(4) << 30;  // workspace spent on it at most
 
-struct Plan {
-  int rows, blocks, team, teams, passes, clusters;
-  bool expand;  // INT8: the rows are turned into bf16 in the workspace first
+inline int row_blocks(const mla_dims& d) {
+  return static_cast<int>((static_cast<int64_t>(d.S1) * d.n_q + kRowBlock - 1) / kRowBlock);
+}
+// Teams with a share of kMinTiles each in the longest stream that `passes` groups of row blocks can give.
+inline int64_t most_teams(const mla_dims& d, int64_t passes) {
+  return std::max<int64_t>(1, d.B * passes * ((static_cast<int64_t>(d.max_blocks_per_seq) + 1) / 2) / kMinTiles);
+}
+
+// The workspace: partial states, records, expanded rows.  It has room for the
+// schedule of any device and any drafts (a team has at most as many clusters, a
+// sequence at most as many passes as there are row blocks).
+struct Workspace {
+  bool expand;  // INT8: the rows are turned into bf16 first
   size_t records_at, rows_at, bytes;
+};
+inline Workspace workspace_of(const mla_dims& d) {
+  const int blocks = row_blocks(d);
+  const size_t room = static_cast<size_t>(std::min<int64_t>(kMaxClusters, most_teams(d, blocks) * blocks));
+  Workspace w;
+  w.records_at = room * 4 * kPartFloats * sizeof(float);
+  w.rows_at = (w.records_at + room * sizeof(int4) + 1023) & ~static_cast<size_t>(1023);
+  const size_t rows = static_cast<size_t>(d.num_blocks) * kPage * 1024;
+  w.expand = d.kv_dtype == MLA_KV_INT8 && blocks >= kExpandBlocks && rows <= kExpandBytes;
+  w.bytes = w.rows_at + (w.expand ? rows : 0);
+  return w;
+}
+
+struct Plan {
+  int blocks, team, teams, passes, clusters;
 };
 inline Plan plan_of(const mla_dims& d, int clusters, bool ragged) {
   Plan s;
-  s.rows = d.S1 * d.n_q;
-  s.blocks = static_cast<int>((static_cast<int64_t>(s.rows) + kRowBlock - 1) / kRowBlock);
+  s.blocks = row_blocks(d);
   s.team = team_size(s.blocks, clusters, ragged);
   s.passes = (s.blocks + s.team - 1) / s.team;
-  // no more teams than shares of kMinTiles in the longest possible stream
-  const int64_t tiles = (static_cast<int64_t>(d.max_blocks_per_seq) + 1) / 2;
-  auto most = [&](int64_t passes) { return std::max<int64_t>(1, d.B * passes * tiles / kMinTiles); };
-  s.teams = static_cast<int>(std::min<int64_t>(clusters / s.team, most(s.passes)));
+  s.teams = static_cast<int>(std::min<int64_t>(clusters / s.team, most_teams(d, s.passes)));
   s.clusters = s.team * s.teams;
-  // the workspace has room for the schedule of any device and any drafts
-  const int64_t room = std::min<int64_t>(kMaxClusters, most(s.blocks) * s.blocks);
-  s.records_at = static_cast<size_t>(room) * 4 * kPartFloats * sizeof(float);
-  s.rows_at = (s.records_at + static_cast<size_t>(room) * sizeof(int4) + 1023) & ~static_cast<size_t>(1023);
-  const size_t rows = static_cast<size_t>(d.num_blocks) * kPage * 1024;
-  s.expand = d.kv_dtype == MLA_KV_INT8 && s.blocks >= kExpandBlocks && rows <= kExpandBytes;
-  s.bytes = s.rows_at + (s.expand ? rows : 0);
   return s;
 }
 
@@ -1467,7 +1482,7 @@ extern "C" {
 size_t mla_tree_workspace_bytes(const mla_dims* dims) {
   g_tree_error[0] = '\0';
   if (dims == nullptr || check_dims(*dims) != MLA_OK) return 0;
-  return mlatree::plan_of(*dims, mlatree::kMaxClusters, false).bytes;
+  return mlatree::workspace_of(*dims).bytes;
 }
 
 mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const void* q_rope, const void* kv_nope,
@@ -1490,8 +1505,9 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   if (!aligned(block_table, 4) || !aligned(act_seqs, 4) || !aligned(tree_lens, 4) || !aligned(tree_mask, 8) ||
       !aligned(lse, 4) || !aligned(workspace, 256))
     return tree_fail(MLA_ERR_ALIGN, "workspace 256-byte, tree_mask 8-byte, the int32 tensors and lse 4-byte aligned");
-  const size_t need = mlatree::plan_of(d, mlatree::kMaxClusters, false).bytes;  // of any schedule
-  if (workspace_bytes < need) return tree_fail(MLA_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const mlatree::Workspace ws = mlatree::workspace_of(d);
+  if (workspace_bytes < ws.bytes)
+    return tree_fail(MLA_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.bytes);
   int dev = 0;
   TREE_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   if (dev < 0 || dev >= mlatree::kMaxDevices) return tree_fail(MLA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
@@ -1513,13 +1529,13 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.parts = static_cast<float*>(workspace);
-  p.records = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + plan.records_at);
+  p.records = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + ws.records_at);
   p.B = d.B;
   p.S1 = d.S1;
   p.n_q = d.n_q;
   p.W = d.max_blocks_per_seq;
   p.num_blocks = d.num_blocks;
-  p.rows = plan.rows;
+  p.rows = d.S1 * d.n_q;
   p.team = plan.team;
   p.teams = plan.teams;
   p.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
@@ -1528,16 +1544,16 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   p.wait_ns = mlasp::host_wait_limit_ns();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const void* latent = kv_nope;
-  if (plan.expand) {
-    uint16_t* wide = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + plan.rows_at);
+  if (ws.expand) {
+    uint16_t* wide = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + ws.rows_at);
     const int per_seq = std::max(1, std::min(d.max_blocks_per_seq, 152 * 8 / d.B));
     mlatree::tree_dequant_kernel<<<dim3(static_cast<unsigned>(per_seq), static_cast<unsigned>(std::min(d.B, 65535))), 256, 0, s>>>(
         static_cast<const int8_t*>(kv_nope), p, wide);
     TREE_CUDA(cudaGetLastError(), "INT8 expansion launch");
     latent = wide;
   }
-  const bool codes = int8 && !plan.expand;  // the attention kernel reads codes
-  const int64_t rows = static_cast<int64_t>(d.num_blocks) * 128, tokens = static_cast<int64_t>(d.B) * plan.rows;
+  const bool codes = int8 && !ws.expand;  // the attention kernel reads codes
+  const int64_t rows = static_cast<int64_t>(d.num_blocks) * 128, tokens = static_cast<int64_t>(d.B) * p.rows;
   mlatree::Maps maps;
   mla_status ms = tmap_bf16(&maps.q_nope, q_nope, 512, tokens, 64, "q_nope");
   if (ms == MLA_OK) ms = tmap_bf16(&maps.q_rope, q_rope, 64, tokens, 64, "q_rope");
@@ -1563,7 +1579,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
               "kernel launch");
   else
     TREE_CUDA(launch_after(mlatree::tree_attn_kernel<false>, grid, mlatree::Conf<false>::kThreads, mlatree::kSmemBytes,
-                           s, plan.expand, maps, p),
+                           s, ws.expand, maps, p),
               "kernel launch");
   if (plan.teams > 1)
     // parts of a row block, if the sequences were equally long

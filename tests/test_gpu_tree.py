@@ -236,6 +236,26 @@ def test_scales(scale):
     assert check(make(12, [600, 40], 3, 48, scale=scale)) == 0
 
 
+def test_out_aligned_to_16_bytes_only_and_nothing_behind_it():
+    m = make(20, [700, 3000], 3, 50)
+    d = upload(m)
+    n = d["q_nope"].numel()
+    room = torch.full((n + 24,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = room[8:8 + n].view(d["q_nope"].shape)
+    assert out.data_ptr() % 32 == 16
+    lse = torch.empty(out.shape[:2], device="cuda")
+    launch(m, d, out, lse)
+    check(m, (out.double().cpu().numpy(), lse.double().cpu().numpy(), 0))
+    assert (room[:8] == 7).all() and (room[8 + n:] == 7).all()
+
+
+def test_much_padding_few_sequences():
+    m = make(21, [200, 0], 90, 16, lens=[1, 0])
+    assert check(m) == 0
+    m = make(22, [150] * 200, 4, 64, lens=[b % 5 for b in range(200)])
+    assert check(m) == 0
+
+
 def test_growing_scores_rescale_the_output():
     """Keys that grow along the context: the running maximum rises from tile to tile."""
     m = make(13, [2500], 2, 64, poison=False)

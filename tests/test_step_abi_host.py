@@ -61,6 +61,13 @@ def test_page_plan_refuses(lib, change, expect):
     assert lib.mla_page_last_error()
 
 
+def test_page_plan_refuses_outputs_over_inputs(lib):
+    for change in (dict(act_seqs=ptr(0)), dict(cache_index=ptr(0)), dict(cu_seqs=ptr(1) + 4), dict(positions=ptr(2)),
+                   dict(block_table=ptr(0) + 4), dict(tree_mask=ptr(3) + 16), dict(num_taken=ptr(3) + 20)):
+        d, io = page_args(**change)
+        assert lib.mla_page_plan(ctypes.byref(d), ctypes.byref(io), None) == -4, change
+
+
 def test_page_plan_null_structs_and_no_sequences(lib):
     d, io = page_args()
     assert lib.mla_page_plan(None, ctypes.byref(io), None) == -1
@@ -78,7 +85,7 @@ def rope_params(**kw):
 
 @pytest.mark.parametrize("change,rot,T,expect", [
     (dict(theta=1.0), 64, 5, -2), (dict(theta=float("nan")), 64, 5, -2), (dict(theta=float("inf")), 64, 5, -2),
-    (dict(factor=0.5), 64, 5, -2), (dict(factor=float("nan")), 64, 5, -2), (dict(mscale=0.0), 64, 5, -2),
+    (dict(factor=0.5), 64, 5, -2), (dict(mscale=1e39), 64, 5, -2), (dict(factor=float("nan")), 64, 5, -2), (dict(mscale=0.0), 64, 5, -2),
     (dict(mscale=float("inf")), 64, 5, -2), (dict(scaling=4), 64, 5, -2), (dict(scaling=-1), 64, 5, -2),
     (dict(orig_positions=0.0), 64, 5, -2), (dict(beta_slow=0.0), 64, 5, -2), (dict(beta_fast=0.5), 64, 5, -2),
     ({}, 0, 5, -2), ({}, 63, 5, -2), ({}, 258, 5, -2), ({}, 64, -1, -2), ({}, 64, 0, 0),
