@@ -1280,11 +1280,16 @@ Device g_dev[kMaxDevices];
 std::mutex g_lock;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-// Clusters of a team, for sequences of up to `blocks` row blocks: as many side
-// by side as keep the most clusters busy, counted in whole teams and whole
-// passes (where drafts differ in size, on average over all sizes).  Row blocks
-// one at a time would read every key once per row block, which costs about 1.4
-// x where the cache is larger than L2, two at a time about 1.05 x.
+// Clusters of a team, for sequences of up to `blocks` row blocks.  Large teams
+// share each key's way through L2 and over the chip; whole teams and whole
+// passes leave clusters idle.  Measured, us, with teams of 1 / 2 / 4 / 8 (72 of
+// 76 clusters): 64 sequences x 8 row blocks x 8192 positions 1023 / 888 / 842 /
+// 815; one of 64 row blocks x 131072: 1559 / 1566 / 1590 / 1509, and 1490 with
+// teams of 12 to 64 although 16% of the clusters idle: such calls run at the
+// power cap, where idle clusters let the others run faster, so idling counts
+// 0.3.  Drafts of unequal size (1 to 17 row blocks, 13 sequences): 122 / 123 /
+// 136 / 159; what a pass leaves idle there counts in full, on average over all
+// sizes.
 inline int team_size(int blocks, int clusters, bool ragged) {
   int best = 1;
   double least = 1e30;
@@ -1294,8 +1299,9 @@ inline int team_size(int blocks, int clusters, bool ragged) {
       taken += static_cast<double>((n + g - 1) / g) * g;
       used += n;
     }
-    const double reads = blocks == 1 || g > 2 ? 1.0 : (g == 1 ? 1.4 : 1.05);
-    const double cost = taken / used * clusters / (clusters / g * g) * reads;
+    const double idle = taken / used * clusters / (clusters / g * g) - 1;
+    const double reads = blocks == 1 || g > 6 ? 1 : (g == 1 ? 1.25 : (g == 2 ? 1.09 : (g <= 4 ? 1.04 : 1.02)));
+    const double cost = reads * (1 + (ragged ? 1 : 0.3) * idle);
     if (cost <= least + 1e-9) {
       least = cost;
       best = g;
