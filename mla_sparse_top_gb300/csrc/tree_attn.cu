@@ -40,14 +40,15 @@
 // lengths alone, so results do not depend on timing.
 //
 // Measured (bf16).  64 sequences x 8 drafts x 128 heads over 8192 positions:
-// 837 us, 1.40 PFLOP/s, 71% of the measured bf16 rate (79% of the sustained
-// one); one sequence, 64 drafts, 131072 positions: 1.55 ms, 1.51 PFLOP/s.
-// Bound there: a tile of 256 keys takes ~5200 clocks where its MMAs take 4406,
-// and the SM clock falls to ~1.6 GHz under the power cap.  Single tokens, 64
-// sequences of 8192: 148 us, 604 MB at 4.1 TB/s: bound by memory, with ~8000
-// clocks a tile; prefetching the next tile's keys into L2, by the load engine or
-// by threads, made it 8% slower, two tiles ahead 35% (lines leave L2 before
-// they are used: 1.04 GB read instead of 0.68).
+// 736 us from a cool start (1.59 PFLOP/s, 81% of the measured bf16 rate), 790 to
+// 820 us back to back, where the SM clock falls to ~1.6 GHz under the power cap;
+// one sequence, 64 drafts, 131072 positions: 1.51 ms, 1.55 PFLOP/s.  Bound by
+// shared memory: a tile of 256 keys moves 278 KB in, 275 KB out as B, 136 KB as A
+// and 32 KB of P, 5630 clocks at 128 bytes a clock, against 4406 clocks of MMA;
+// measured 5200 to 6000.  Single tokens, 64 sequences of 8192: 148 us for 604 MB:
+// bound by memory, ~8000 clocks a tile.  Prefetching the next tile's keys into L2
+// gained nothing there, without an eviction priority it lost 8%, two tiles ahead
+// 35% (lines leave L2 before their use: 1.04 GB read instead of 0.68).
 // What shaped the kernel, at the largest case (us): arrivals on the other CTA's
 // barriers with release at CTA scope instead of cluster scope 2018 -> 1682; a
 // converged warp around an elected issuer instead of one running thread 2584 ->
