@@ -89,8 +89,8 @@ struct Conf {
   static constexpr int kMmaWarp = kProducerWarp0 + kProducers;
   static constexpr int kThreads = (kMmaWarp + (kInt8 ? 2 : 1)) * 32;
   static constexpr int kFillers = kInt8 ? 4 : 1;  // warps of a CTA that fill one slot together
-  // INT8: the softmax warps take registers over from the converters
-  static constexpr int kRegs = kInt8 ? 96 : 128, kSoftmaxRegs = 112, kConvertRegs = 80;
+  // INT8: the softmax warps take registers over from the converters (112 and 80: 188 us instead of 183)
+  static constexpr int kRegs = kInt8 ? 96 : 128, kSoftmaxRegs = 104, kConvertRegs = 88;
   static_assert(256 * kSoftmaxRegs + 256 * kConvertRegs <= 512 * 96, "register budget");
 };
 constexpr int kRawSlots = 3;
@@ -597,11 +597,14 @@ __device__ void raw_load_role(const Params& p, const Ctx& c, const Maps& maps, W
 }
 
 // INT8: converter warp w belongs to group w / 4 and turns a quarter of one of a
-// raw slot's two items into bf16, 16 codes of a lane at a time.  This binds the
-// INT8 kernel (64 single tokens over 8192 positions: 193 us, 344 MB; bf16 148
-// us, 604 MB): an item takes a group ~1700 clocks, half of it arithmetic, and
-// there is one for every 259 clocks of MMA.  Loads by the converters themselves,
-// one item ahead in registers, took 274 us; a third group of warps 201 us.
+// raw slot's two items into bf16, 16 codes of a lane at a time.  Shared memory
+// binds the INT8 kernel (64 single tokens over 8192 positions: 183 us, 344 MB;
+// bf16 148 us, 604 MB): codes in and out, bf16 values in and the MMA's operands
+// out are 990 KB a tile, 7.7 thousand clocks of the measured 11.6 (162 us with
+// the arithmetic left out, 136 with the stores left out).  So eight lanes' 16
+// bytes always lie in eight different banks; with two-way conflicts it took 193
+// us.  Twice the warps a group 193 us, a third group 201, all arithmetic before
+// the wait for the slot 197, loads by the converters themselves 274.
 __device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Walk walk, int w, int lane) {
   static_assert(Conf<true>::kSlots == 4 && Conf<true>::kProducers == 8, "two groups, four slots");
   const int rank = static_cast<int>(c.rank), group = w >> 2, quarter = w & 3;
@@ -615,16 +618,21 @@ __device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Wa
     constexpr int us = decltype(us_)::value;
     if (!warp_wait(c, kRawFull + raw, raw_phase)) return false;
     const uint32_t src = c.sb + kOffRaw + raw * kRawBytes;
-    // unit0 + 32 k lies 8 (us = 2) or 4 rows on, in the same column
-    const int unit0 = quarter * 128 + lane, r0 = unit0 >> us, col = unit0 & ((1 << us) - 1);
-    const uint32_t codes = src + (us == 2 ? group * 64 + r0 * 128 : group * kChunk + r0 * 128) + col * 16;
+    // eight lanes take four 16-byte units of each of two rows, whose swizzles put
+    // the loads and the stores into different banks: rows r and r ^ 5 (us = 2),
+    // or r and r ^ 1 with the other half of the columns; k moves 8 or 4 rows on
+    const int pair_row = lane >> 3, odd = (lane >> 2) & 1;
+    const int r0 = us == 2 ? quarter * 32 + (odd ? pair_row ^ 5 : pair_row) : quarter * 16 + 2 * (pair_row >> 1) + odd;
+    const int col = us == 2 ? lane & 3 : (lane & 3) + 4 * (odd ^ (pair_row & 1));
+    const uint32_t codes = src + (us == 2 ? 0 : group * kChunk) + r0 * 128;
+    const int unit = us == 2 ? 4 * group + col : col;
     uint4 v[4];
     float sc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int dr = (32 * k) >> us;
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(codes + dr * 128));
+                   : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w) : "r"(codes + dr * 128 + ((unit ^ ((r0 + dr) & 7)) << 4)));
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc[k]) : "r"(src + kRawCodes + (r0 + dr) * 16 + 4 * scale));
     }
     if (!free_slot(item)) return false;
@@ -1314,9 +1322,9 @@ inline int team_size(int blocks, int clusters, bool ragged) {
 // A sequence of several row blocks has its INT8 rows converted once, into the
 // workspace, rather than by every cluster that reads them (each converts a key
 // twice: as a key and as a value).  Converted by the clusters / expanded first,
-// us: one row block, 64 sequences of 8192: 203 / 289; two, the same: 378 / 359,
-// 64 of 100 to 8192: 117 / 130, 16 of 3000: 58 / 56; 17, 13 of 500 to 20000: 425
-// / 255; 64, one of 32768: 705 / 327.
+// us: one row block, 64 sequences of 8192: 183 / 285; two, the same: 336 / 363,
+// 64 of 100 to 8192: 107 / 128, 16 of 3000: 54 / 56; three, 64 of 8192: 496 /
+// 448; 17, 13 of 500 to 20000: 383 / 248; 64, one of 32768: 650 / 343.
 constexpr int kExpandBlocks = 3;
 constexpr size_t kExpandBytes = size_t(4) << 30;  // workspace spent on it at most
 
@@ -1565,11 +1573,11 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   mla_status ms = tmap_bf16(&maps.q_nope, q_nope, 512, tokens, 64, "q_nope");
   if (ms == MLA_OK) ms = tmap_bf16(&maps.q_rope, q_rope, 64, tokens, 64, "q_rope");
   if (ms == MLA_OK) ms = tmap_bf16(&maps.rope, kv_rope, 64, rows, 128, "kv_rope");
-  if (codes) {  // codes and scales as they lie
+  if (codes) {  // scales as they lie, codes swizzled like every other tile
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const CUtensorMapSwizzle flat = CU_TENSOR_MAP_SWIZZLE_NONE;
-    if (ms == MLA_OK) ms = tmap(&maps.key, u8, 1, kv_nope, 512, rows, 128, 128, flat, "kv_nope");
-    if (ms == MLA_OK) ms = tmap(&maps.val, u8, 1, kv_nope, 512, rows, 128, 64, flat, "kv_nope");
+    if (ms == MLA_OK) ms = tmap(&maps.key, u8, 1, kv_nope, 512, rows, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B, "kv_nope");
+    if (ms == MLA_OK) ms = tmap(&maps.val, u8, 1, kv_nope, 512, rows, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B, "kv_nope");
     // the scales of 64 rows as one row of the map: 1 KB at a time instead of 16 bytes
     if (ms == MLA_OK) ms = tmap(&maps.key_scale, f32, 4, kv_scales, 256, rows / 64, 256, 2, flat, "kv_scales");
     if (ms == MLA_OK) ms = tmap(&maps.val_scale, f32, 4, kv_scales, 256, rows / 64, 256, 1, flat, "kv_scales");
