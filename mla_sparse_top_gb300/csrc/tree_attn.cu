@@ -111,6 +111,7 @@ constexpr int kOffRing = kOffP + 4 * kChunk;
 constexpr int kOffRaw = kOffRing + Conf<true>::kSlots * kSlotBytes;  // INT8
 constexpr int kOffExch = kOffRaw + kRawSlots * kRawBytes;            // float [2][4][64]
 static_assert(kOffExch >= kOffRing + Conf<false>::kSlots * kSlotBytes, "ring");
+static_assert(kOffRing % 1024 == 0 && kOffRaw % 1024 == 0 && kRawBytes % 1024 == 0, "swizzled tiles");
 constexpr int kOffScan = kOffExch + 2048;                    // int64 [warps]
 constexpr int kOffWalk = kOffScan + kMaxThreads / 32 * 8;  // int64 [4]: a share's first sequence and its stream position
 constexpr int kOffBars = kOffWalk + 32;
