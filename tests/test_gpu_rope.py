@@ -1,7 +1,7 @@
 """Rotary positions on the GPU against the fp64 oracle.
 
 Bound of one output, with u = 2^-24 (half a step of fp32): cos and sin are off
-by at most 2 ulp of their own (sincospif), pi u from the angle's rounding to
+by at most 2 ulp of their own, pi u from the angle's rounding to
 fp32 (a fraction of a turn below 1/2, relative error u), 2 u from mscale and
 its product: below 8 u mscale together; the rotation adds 2 u per term.  So
 |error| <= 10 u mscale (|x_a| + |x_b|), plus the frequency's own error |p|
@@ -80,6 +80,23 @@ def test_table_lengths(T):
     ang = pos.cpu().numpy()[:, None] * f
     bound = 8 * U + (1 << 17) * 2.0 ** -45
     assert np.abs(c.cpu().numpy() - np.cos(ang)).max() <= bound and np.abs(s.cpu().numpy() - np.sin(ang)).max() <= bound
+
+
+@pytest.mark.parametrize("T,pairs,shift", [(777, 32, 1), (777, 32, 4), (1, 128, 0), (513, 128, 3), (65, 1, 0), (1000, 6, 0),
+                                           (300, 100, 0), (129, 4, 0), (31, 127, 2)])
+def test_table_widths(T, pairs, shift):
+    """Rows in 16-byte stores and without, no value beside them touched."""
+    import mla_sparse_top_gb300 as mla
+    _, pos = inputs(T, 1, 2, torch.float32, seed=pairs)
+    c, s = (torch.full((T * pairs + 8,), -7.0, device="cuda") for _ in range(2))
+    mla.mla_rope_table(pos, c[shift:shift + T * pairs].view(T, pairs), s[shift:shift + T * pairs].view(T, pairs),
+                       params=mla.rope_params())
+    ang = pos.cpu().numpy()[:, None] * step.rope_freqs(2 * pairs)
+    bound = 8 * U + (1 << 17) * 2.0 ** -45
+    for got, want in ((c, np.cos(ang)), (s, np.sin(ang))):
+        got = got.cpu().numpy()
+        assert np.abs(got[shift:shift + T * pairs].reshape(T, pairs) - want).max() <= bound
+        assert (got[:shift] == -7).all() and (got[shift + T * pairs:] == -7).all()
 
 
 @pytest.mark.parametrize("half", [False, True])
