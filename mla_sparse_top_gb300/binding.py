@@ -203,9 +203,15 @@ def _check(status: int):
         raise MlaError(status, load_library().mla_sparse_last_error().decode())
 
 
+# os.environ.get raises and catches a KeyError inside for a variable that is not
+# set, a tenth of a small call's time; os.environ writes through to the C library.
+_getenv = ctypes.PyDLL(None).getenv
+_getenv.argtypes, _getenv.restype = [ctypes.c_char_p], ctypes.c_char_p
+
+
 def debug_enabled() -> bool:
     """True when MLA_SPARSE_DEBUG asks for a status check after every call."""
-    return os.environ.get("MLA_SPARSE_DEBUG", "") not in ("", "0")
+    return (_getenv(b"MLA_SPARSE_DEBUG") or b"") not in (b"", b"0")
 
 
 def _debug_status(read_status, what: str, stream):
