@@ -10,9 +10,8 @@
 //
 // The rotation is bound by memory.  A thread keeps one token and one unit of a
 // head (16 bytes, or one pair of values where alignment forbids that) and walks
-// over heads, 64 bytes in flight: its angles are made once, while the first
-// loads are on their way, offsets advance by one addition, and nothing is
-// shared between threads.
+// over heads, 64 bytes in flight: its angles are made once, offsets advance by
+// one addition, and nothing is shared between threads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -22,6 +21,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/mla_rope.h"
 
@@ -30,7 +30,8 @@ namespace mlarp {
 constexpr int kThreads = 512;
 constexpr int kTableThreads = 256;
 constexpr int kMaxPairs = 128;  // rot_dim <= 256
-constexpr int kMaxPasses = 16;  // heads of a thread
+constexpr int kSingles = 192;  // threads of a block where values go one by one
+constexpr int kMaxPasses = 16, kMaxSinglePasses = 32;  // heads of a thread
 
 __device__ unsigned int g_rope_status = 0;
 
@@ -50,12 +51,12 @@ __device__ __forceinline__ float2 cos_sin(int32_t pos, uint64_t turn, float msca
   const float hi = static_cast<float>(static_cast<int32_t>(top - (quadrant & 0xC0000000u)));
   // 23 bits of the low word as the fraction of a value in [1, 2): no second conversion
   const float lo = __uint_as_float(0x3F800000u | static_cast<uint32_t>(frac) >> 9) - 1.f;
-  const float x = (hi + lo) * 0x1p-32f, z = x * x;
+  const float x = __fmul_rn(hi + lo, 0x1p-32f), z = x * x;
   float p = fmaf(z, 42.058693f, -76.705856f);
   p = fmaf(p, z, 81.605247f);
   p = fmaf(p, z, -41.341702f);
   p = fmaf(p, z, -1.7484555e-7f);
-  const float s = fmaf(x, 6.2831855f, x * p);
+  const float s = fmaf(x, 6.2831855f, __fmul_rn(x, p));
   float c = fmaf(z, -26.426256f, 60.244640f);
   c = fmaf(c, z, -85.456818f);
   c = fmaf(c, z, 64.939392f);
@@ -123,7 +124,8 @@ struct Tensor {
   int head_rows;    // heads that a block takes at a time
   int passes;       // times that it does
   int head_blocks;  // blocks over the heads
-  int unit_blocks;  // blocks over the units of a head (more than kThreads units)
+  int unit_blocks;  // blocks over the units of a head (more than a block's threads)
+  uint32_t per_unit, per_head_row;  // 2^22 / units and / head_rows, rounded up
   int blocks;
 };
 
@@ -147,8 +149,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// One fused operation each, spelt out: a pair's result is the same in every kernel and place.
 __device__ __forceinline__ float2 turn2(float a, float b, float2 cs) {
-  return make_float2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+  return make_float2(fmaf(a, cs.x, -__fmul_rn(b, cs.y)), fmaf(a, cs.y, __fmul_rn(b, cs.x)));
 }
 
 // V values of type E in memory; W words in registers (single 16-bit values take a word).
@@ -212,12 +215,11 @@ __device__ __forceinline__ void turn_unit(Pack<E, V>& a, Pack<E, V>& b, const fl
 }
 
 // kTwo: a rotated unit is two packs, V values and the V that turn with them
-// (the half layout, and single pairs of either layout); otherwise one pack of
-// V / 2 adjacent pairs.
+// (the half layout); otherwise one pack of V / 2 adjacent pairs.
 template <typename E, int V, bool kTwo>
 __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, int block) {
   constexpr int kPairs = kTwo ? V : V / 2;
-  constexpr int kUnroll = V == 1 ? 3 : (kTwo ? 2 : 4);  // heads in flight
+  constexpr int kUnroll = kTwo ? 2 : 4;  // heads in flight
   const int tid = threadIdx.x;
   int k, r = 0;
   if (w.unit_blocks == 1) {
@@ -235,11 +237,10 @@ __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, in
   if (t >= p.T || h >= w.n_heads) return;
   const int n = min(w.passes, (w.n_heads - h + w.head_rows - 1) / w.head_rows);
   const bool rotated = k < w.rot_units;
-  const int second = p.half ? p.pairs : 1;  // distance of a pair's values (kTwo)
   int d, pair0 = 0;
   if (rotated) {
     pair0 = k * kPairs;
-    d = w.rot_off + (p.half ? pair0 : 2 * pair0);
+    d = w.rot_off + (kTwo ? pair0 : 2 * pair0);
   } else {
     const int c = (k - w.rot_units) * V;  // copied values, in order
     d = c < w.rot_off ? c : c + 2 * p.pairs;
@@ -261,7 +262,7 @@ __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, in
     for (int u = 0; u < kUnroll; ++u) {
       if (it + u < n) {
         a[u].load(x);
-        if (kTwo && rotated) b[u].load(x + second);
+        if (kTwo && rotated) b[u].load(x + p.pairs);
       }
       x += x_step;
     }
@@ -277,7 +278,7 @@ __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, in
       if (it + u < n) {
         if (rotated) {
           turn_unit<E, V, kTwo>(a[u], b[u], cs);
-          if (kTwo) b[u].store(out + second);
+          if (kTwo) b[u].store(out + p.pairs);
         }
         a[u].store(out);
       }
@@ -286,18 +287,103 @@ __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, in
   }
 }
 
-// kVec: both tensors in 16-byte units: 403 + 403 MB in 116 us, 98% of a copy's
-// rate.  Otherwise both go pair by pair, in a kernel of its own with half the
-// registers and twice the threads: bound by issue (4 bytes an access), 30 + 30
-// MB in 20 us; with two blocks an SM and four heads in flight 27 us.
-template <typename E, bool kVec>
-__global__ void __launch_bounds__(kThreads, kVec ? 2 : 4) rope_kernel(const __grid_constant__ Params p) {
+// Both tensors in 16-byte units: 403 + 403 MB in 116 us, 98% of a copy's rate.
+template <typename E>
+__global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ Params p) {
   const int second = static_cast<int>(blockIdx.x) >= p.t[0].blocks;
   const int block = static_cast<int>(blockIdx.x) - (second ? p.t[0].blocks : 0);
   const Tensor& w = p.t[second];
-  if constexpr (!kVec) rotate_rows<E, 1, true>(p, w, block);
-  else if (p.half) rotate_rows<E, 16 / sizeof(E), true>(p, w, block);
+  if (p.half) rotate_rows<E, 16 / sizeof(E), true>(p, w, block);
   else rotate_rows<E, 16 / sizeof(E), false>(p, w, block);
+}
+
+// Applies `body` to `n` heads, G at a time and the rest one by one.
+template <int G, typename F>
+__device__ __forceinline__ void walk_heads(int n, F&& body) {
+  for (; n >= G; n -= G) body(std::integral_constant<int, G>());
+  for (; n > 0; --n) body(std::integral_constant<int, 1>());
+}
+
+// Rows that are not 16-byte aligned: a thread takes one value, or the two of a
+// pair.  Instructions bind it before memory does, so divisions are products with
+// reciprocals, a thread walks all heads where there are tokens enough, and the
+// heads that fill a group carry no tests: 30 + 30 MB in 18.4 us (the form above
+// with single values 20.6, 2.5 times the instructions; 6 or 9 heads in flight
+// 20.5 and 24.6, as fewer warps fit).
+template <typename E>
+__global__ void __launch_bounds__(kSingles, 8) rope_single_kernel(const __grid_constant__ Params p) {
+  const int second = static_cast<int>(blockIdx.x) >= p.t[0].blocks;
+  int block = static_cast<int>(blockIdx.x) - (second ? p.t[0].blocks : 0);
+  const Tensor& w = p.t[second];
+  const int tid = threadIdx.x;
+  int k = tid, dt = 0, dh = 0;
+  if (w.unit_blocks == 1) {
+    const int r = static_cast<int>(tid * w.per_unit >> 22);
+    k = tid - r * w.units;
+    dt = static_cast<int>(r * w.per_head_row >> 22);
+    dh = r - dt * w.head_rows;
+  } else {
+    k += block % w.unit_blocks * static_cast<int>(blockDim.x);
+    block /= w.unit_blocks;
+  }
+  if (k >= w.units || dt >= w.tok_rows) return;
+  int hb = 0;
+  if (w.head_blocks > 1) {
+    hb = block % w.head_blocks;
+    block /= w.head_blocks;
+  }
+  const int64_t t = static_cast<int64_t>(block) * w.tok_rows + dt;
+  const int h = hb * w.passes * w.head_rows + dh;
+  if (t >= p.T || h >= w.n_heads) return;
+  int n = w.passes;  // heads h, h + head_rows, ...
+  if (w.head_rows > 1 || w.head_blocks > 1) n = min(n, (w.n_heads - h + w.head_rows - 1) / w.head_rows);
+  const bool rotated = k < w.rot_units;
+  int d;
+  if (rotated) {
+    d = w.rot_off + (p.half ? k : 2 * k);
+  } else {
+    d = k - w.rot_units;
+    if (d >= w.rot_off) d += 2 * p.pairs;
+  }
+  int64_t to = t;
+  if (w.rows != nullptr) {
+    to = __ldg(w.rows + t);
+    if (to >= w.num_rows && k == 0 && h == 0) atomicOr(&g_rope_status, MLA_DEVICE_BAD_BLOCK);
+    if (to < 0 || to >= w.num_rows) return;
+  }
+  const char* x = static_cast<const char*>(w.x) + (t * w.xt + h * w.xh + d) * static_cast<int64_t>(sizeof(E));
+  char* out = static_cast<char*>(w.out) + (to * w.ot + h * w.oh + d) * static_cast<int64_t>(sizeof(E));
+  const int64_t x_step = w.head_rows * w.xh * static_cast<int64_t>(sizeof(E));
+  const int64_t o_step = w.head_rows * w.oh * static_cast<int64_t>(sizeof(E));
+  if (!rotated) {
+    walk_heads<4>(n, [&](auto group) {
+      constexpr int G = decltype(group)::value;
+      Pack<E, 1> a[G];
+#pragma unroll
+      for (int u = 0; u < G; ++u, x += x_step) a[u].load(reinterpret_cast<const E*>(x));
+#pragma unroll
+      for (int u = 0; u < G; ++u, out += o_step) a[u].store(reinterpret_cast<E*>(out));
+    });
+    return;
+  }
+  float2 cs[1] = {cos_sin(__ldg(p.positions + t), p.f.turn[k], p.f.mscale)};
+  if (p.inverse) cs[0].y = -cs[0].y;
+  const int other = (p.half ? p.pairs : 1) * static_cast<int>(sizeof(E));  // the pair's other value
+  walk_heads<3>(n, [&](auto group) {
+    constexpr int G = decltype(group)::value;
+    Pack<E, 1> a[G], b[G];
+#pragma unroll
+    for (int u = 0; u < G; ++u, x += x_step) {
+      a[u].load(reinterpret_cast<const E*>(x));
+      b[u].load(reinterpret_cast<const E*>(x + other));
+    }
+#pragma unroll
+    for (int u = 0; u < G; ++u, out += o_step) {
+      turn_unit<E, 1, true>(a[u], b[u], cs);
+      a[u].store(reinterpret_cast<E*>(out));
+      b[u].store(reinterpret_cast<E*>(out + other));
+    }
+  });
 }
 
 }  // namespace mlarp
@@ -405,17 +491,21 @@ mla_status split_tensor(const mla_rope_tensor* q, const mla_rope_dims& d, const 
   const int width = !vec ? 1 : (d.dtype == MLA_ROPE_FP32 ? 4 : 8);
   w->rot_units = vec && !d.half ? d.rot_dim / width : d.rot_dim / 2 / width;
   w->units = w->rot_units + (same ? 0 : (q->head_dim - d.rot_dim) / width);
-  w->unit_blocks = (w->units + mlarp::kThreads - 1) / mlarp::kThreads;
-  const int rows = w->unit_blocks > 1 ? 1 : mlarp::kThreads / w->units;
+  const int threads = vec ? mlarp::kThreads : mlarp::kSingles;
+  w->unit_blocks = (w->units + threads - 1) / threads;
+  const int rows = w->unit_blocks > 1 ? 1 : threads / w->units;
   w->tok_rows = std::min(rows, d.T);
   w->head_rows = std::min(rows / w->tok_rows, q->n_heads);
   // several heads per thread once there is a block for every SM twice over
   const int64_t toks = (static_cast<int64_t>(d.T) + w->tok_rows - 1) / w->tok_rows;
   const int turns = (q->n_heads + w->head_rows - 1) / w->head_rows;
-  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(turns, mlarp::kMaxPasses),
-                                                                      toks * turns / (2 * 152))));
+  const int most = std::min(turns, vec ? mlarp::kMaxPasses : mlarp::kMaxSinglePasses);
+  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, toks * turns / (2 * 152))));
   w->head_blocks = (turns + w->passes - 1) / w->passes;
   w->passes = (turns + w->head_blocks - 1) / w->head_blocks;  // even shares
+  // n * per_unit >> 22 is n / units for n and units up to 512: the product's excess is below n / 2^22
+  w->per_unit = (1u << 22) / w->units + 1;
+  w->per_head_row = (1u << 22) / w->head_rows + 1;
   const int64_t blocks = toks * w->head_blocks * w->unit_blocks;
   if (blocks >= (1ll << 30)) return rope_fail(MLA_ERR_SHAPE, "%s: T x heads too large", name);
   w->blocks = static_cast<int>(blocks);
@@ -482,10 +572,10 @@ mla_status mla_rope_apply(const mla_rope_dims* dims, const mla_rope_params* para
   p.inverse = d.inverse;
   const unsigned grid = static_cast<unsigned>(p.t[0].blocks + p.t[1].blocks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void (*kernels[3][2])(mlarp::Params) = {{mlarp::rope_kernel<__nv_bfloat16, false>, mlarp::rope_kernel<__nv_bfloat16, true>},
-                                          {mlarp::rope_kernel<__half, false>, mlarp::rope_kernel<__half, true>},
-                                          {mlarp::rope_kernel<float, false>, mlarp::rope_kernel<float, true>}};
-  kernels[d.dtype][vec ? 1 : 0]<<<grid, mlarp::kThreads, 0, s>>>(p);
+  void (*kernels[3][2])(mlarp::Params) = {{mlarp::rope_single_kernel<__nv_bfloat16>, mlarp::rope_kernel<__nv_bfloat16>},
+                                          {mlarp::rope_single_kernel<__half>, mlarp::rope_kernel<__half>},
+                                          {mlarp::rope_single_kernel<float>, mlarp::rope_kernel<float>}};
+  kernels[d.dtype][vec ? 1 : 0]<<<grid, vec ? mlarp::kThreads : mlarp::kSingles, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return rope_fail(MLA_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
   return MLA_OK;

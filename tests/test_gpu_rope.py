@@ -121,6 +121,24 @@ def test_apply_out_of_place_and_in_place(T, H, D, rot_off, rot_dim, pad, dtype, 
     assert torch.equal(z, y) and (whole[:, :, D:] == 3).all()  # the same bits in place, and nothing behind a head
 
 
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,H,D,rot_off,rot_dim", [(2001, 17, 21, 3, 10), (3001, 40, 9, 1, 8), (700, 5, 401, 0, 6)])
+def test_single_values_many_tokens(T, H, D, rot_off, rot_dim, dtype, half):
+    """Rows without a 16-byte alignment where a thread walks several heads."""
+    import mla_sparse_top_gb300 as mla
+    x, pos = inputs(T, H, D, TYPES[dtype], pad=3, seed=H)
+    scheme = SCHEMES[1]
+    kw = dict(rot_dim=rot_dim, rot_off=rot_off, half=half)
+    out = torch.full((T, H, D), float("nan"), dtype=x.dtype, device="cuda")
+    mla.mla_rope_apply(pos, x, params=mla.rope_params(**scheme), out=out, **kw)
+    check(out, x, pos, scheme, **kw)
+    y = torch.full((T, H, D + 3), -7.0, dtype=x.dtype, device="cuda")
+    y[:, :, :D] = x
+    mla.mla_rope_apply(pos, y[:, :, :D], params=mla.rope_params(**scheme), **kw)
+    assert torch.equal(y[:, :, :D], out) and (y[:, :, D:] == -7).all()
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_two_tensors_keys_to_cache_rows(dtype):
     """Queries in place, keys into their rows of a cache; other rows stay, negative rows are skipped."""
