@@ -140,7 +140,6 @@ constexpr uint32_t kTmemO = 0;    // two blocks of 128 columns: output dims [0, 
 constexpr uint32_t kTmemS = 256;  // two buffers of 128 columns
 constexpr int kPartFloats = 128 * 256 + 128;  // one CTA's partial state: O, then m[64], l[64]
 constexpr int kMaxClusters = 76;
-constexpr int kMinTiles = 2;  // a team's share is at least this long
 constexpr uint64_t kDrainNs = 500ull * 1000 * 1000;
 
 __device__ unsigned int g_tree_status = 0;
@@ -322,8 +321,15 @@ __device__ __forceinline__ int64_t block_sum_scan(const Ctx& c, int64_t v, int64
   return before + x - v;
 }
 
+// Teams that take a stream of `total` tiles: one for each tile as far as they go
+// (one sequence of 16000 positions 26.9 us, with two tiles a team at least 29.0;
+// 16 of 300 to 2000 25.2 and 29.4).  Of short shares no more than the longest
+// needs: fewer cuts for the merge (8 sequences x 8 row blocks x 1000 positions
+// 36.9 -> 29.3, 64 single tokens over 100 to 500 32.8 -> 30.7).
 __device__ __forceinline__ int teams_of(const Params& p, int64_t total) {
-  return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.teams), total / kMinTiles)));
+  const int64_t teams = max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.teams), total));
+  const int64_t share = (total + teams - 1) / teams;
+  return static_cast<int>(share > 0 && share < 8 ? (total + share - 1) / share : teams);
 }
 
 // The walk of cluster `cid`; false when it has nothing to do.
@@ -1196,88 +1202,133 @@ __global__ void __launch_bounds__(256) tree_dequant_kernel(const int8_t* __restr
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the parts of a row block that was cut between teams.  Block x looks at
-// the record of cluster x (the one the row block starts in), block y takes 16
-// columns of the 256 of one CTA; thread L of each group is lane L of the parts'
-// units.  One group for the usual two or three parts (75 row blocks in 8 us);
-// four that share out the parts where a few long sequences have one from almost
-// every team (with four for the former, one block an SM fits: 19 us).
-template <int kMergeGroups>
-__global__ void __launch_bounds__(128 * kMergeGroups) tree_merge_kernel(const __grid_constant__ Params p) {
+// Joins the parts of a row block that was cut between teams.  Thread L of each of
+// kGroups groups is lane L of the parts' units and takes kUnits of them (of four
+// columns each); a group takes every kGroups-th part, kAhead parts at a time.
+// `from`: the cluster that the row block starts in, `item`: which units.
+template <int kGroups, int kUnits, int kAhead>
+struct Merge {
+  static constexpr int kItems = 2 * 64 / kUnits;  // of a row block
+  static constexpr int kThreads = 128 * kGroups;
+  float sm[kGroups > 1 ? kGroups : 1][4 * kUnits + 2][kGroups > 1 ? 128 : 1];
+
+  __device__ void run(const Params& p, const int4& rec, int from, int item) {
+    const int L = threadIdx.x & 127, group = threadIdx.x >> 7, row = L & 63, half = L >> 6;
+    const int rank = item / (kItems / 2), unit = item % (kItems / 2) * kUnits;
+    float m = -INFINITY, l = 0.f, o[4 * kUnits];
+#pragma unroll
+    for (int k = 0; k < 4 * kUnits; ++k) o[k] = 0.f;
+    for (int k0 = group; k0 <= rec.z; k0 += kAhead * kGroups) {
+      float mk[kAhead], lk[kAhead];
+      float4 v[kAhead][kUnits];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + u * kGroups;
+        const bool in = k <= rec.z;
+        const int cl = from + (in ? k : 0) * p.team;
+        const float* src = p.parts + (static_cast<int64_t>(cl * 2 + (in && k > 0 ? 0 : 1)) * 2 + rank) * kPartFloats;
+        mk[u] = in ? __ldcg(src + 128 * 256 + row) : -INFINITY;
+        lk[u] = in ? __ldcg(src + 128 * 256 + 64 + row) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) v[u][i] = __ldcg(reinterpret_cast<const float4*>(src) + (unit + i) * 128 + L);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (mk[u] == -INFINITY && lk[u] == 0.f) continue;  // a part in which the row sees nothing
+        const float top = fmaxf(m, mk[u]);
+        const float f = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(mk[u] - top);
+        m = top;
+        l = l * f + w * lk[u];
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+          o[4 * i] = o[4 * i] * f + w * v[u][i].x;
+          o[4 * i + 1] = o[4 * i + 1] * f + w * v[u][i].y;
+          o[4 * i + 2] = o[4 * i + 2] * f + w * v[u][i].z;
+          o[4 * i + 3] = o[4 * i + 3] * f + w * v[u][i].w;
+        }
+      }
+    }
+    const int r = rank * 64 + row;
+    if constexpr (kGroups > 1) {
+      __syncthreads();  // the last item's values have been read
+      sm[group][4 * kUnits][L] = m;
+      sm[group][4 * kUnits + 1][L] = l;
+#pragma unroll
+      for (int k = 0; k < 4 * kUnits; ++k) sm[group][k][L] = o[k];
+      __syncthreads();
+      if (group != 0) return;
+      for (int g = 1; g < kGroups; ++g) {
+        const float mg = sm[g][4 * kUnits][L], lg = sm[g][4 * kUnits + 1][L];
+        if (mg == -INFINITY && lg == 0.f) continue;
+        const float top = fmaxf(m, mg);
+        const float f = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(mg - top);
+        m = top;
+        l = l * f + w * lg;
+#pragma unroll
+        for (int k = 0; k < 4 * kUnits; ++k) o[k] = o[k] * f + w * sm[g][k][L];
+      }
+    }
+    if (r >= rec.y) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t y[2 * kUnits];
+#pragma unroll
+    for (int k = 0; k < 2 * kUnits; ++k) y[k] = l == 0.f ? 0u : pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
+    const int64_t g = rec.x + r;
+    uint16_t* out = p.out + g * 512 + (unit >> 5) * 256 + half * 128 + (unit & 31) * 4;
+    if constexpr (kUnits == 4) {
+      const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
+      if (p.out32) {
+        stg32(out, a, b);
+      } else {
+        reinterpret_cast<uint4*>(out)[0] = a;
+        reinterpret_cast<uint4*>(out)[1] = b;
+      }
+    } else {
+      static_assert(kUnits == 1 || kUnits == 4, "stores");
+      *reinterpret_cast<uint2*>(out) = make_uint2(y[0], y[1]);
+    }
+    if (unit == 0 && half == 0 && p.lse != nullptr)
+      p.lse[g] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+  }
+};
+
+// The usual two or three parts (75 row blocks in 8 us): block x looks at the
+// record of cluster x, block y takes 16 columns of the 256 of one CTA.
+using MergeFew = Merge<1, 4, 2>;
+__global__ void __launch_bounds__(MergeFew::kThreads) tree_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's stores are visible
   const int4 rec = p.records[blockIdx.x];
   if (rec.y == 0) return;
-  const int L = threadIdx.x & 127, group = threadIdx.x >> 7, row = L & 63, half = L >> 6;
-  const int rank = blockIdx.y >> 4, unit = (blockIdx.y & 15) * 4;
-  float m = -INFINITY, l = 0.f, o[16];
+  MergeFew merge;
+  merge.run(p, rec, blockIdx.x, blockIdx.y);
+}
+
+// A few long sequences with a part from almost every team: four groups share out
+// the parts, the blocks the row blocks that there are, four columns at a time (one
+// sequence of 131072 positions, attention and merge, 60 us; in the form above,
+// with four groups, 68).
+using MergeMany = Merge<4, 1, 4>;
+__global__ void __launch_bounds__(MergeMany::kThreads, 2) tree_merge_many_kernel(const __grid_constant__ Params p) {
+  __shared__ MergeMany merge;
+  __shared__ int found[4], list[128];
+  static_assert(kMaxClusters <= 128, "a thread for each record");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool cut = tid < p.team * p.teams && p.records[tid].y != 0;
+  const unsigned cuts = __ballot_sync(0xffffffffu, cut);
+  if (lane == 0 && tid < 128) found[tid >> 5] = __popc(cuts);
+  __syncthreads();
+  int n = 0;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
-  for (int k0 = group; k0 <= rec.z; k0 += 2 * kMergeGroups) {
-    float mk[2], lk[2];
-    float4 v[2][4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = k0 + u * kMergeGroups;
-      const bool in = k <= rec.z;
-      const int cl = blockIdx.x + (in ? k : 0) * p.team;
-      const float* src = p.parts + (static_cast<int64_t>(cl * 2 + (in && k > 0 ? 0 : 1)) * 2 + rank) * kPartFloats;
-      mk[u] = in ? __ldcg(src + 128 * 256 + row) : -INFINITY;
-      lk[u] = in ? __ldcg(src + 128 * 256 + 64 + row) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[u][i] = __ldcg(reinterpret_cast<const float4*>(src) + (unit + i) * 128 + L);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (mk[u] == -INFINITY && lk[u] == 0.f) continue;  // a part in which the row sees nothing
-      const float top = fmaxf(m, mk[u]);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(mk[u] - top);
-      m = top;
-      l = l * f + w * lk[u];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[4 * i] = o[4 * i] * f + w * v[u][i].x;
-        o[4 * i + 1] = o[4 * i + 1] * f + w * v[u][i].y;
-        o[4 * i + 2] = o[4 * i + 2] * f + w * v[u][i].z;
-        o[4 * i + 3] = o[4 * i + 3] * f + w * v[u][i].w;
-      }
-    }
+  for (int w = 0; w < 4; ++w) {
+    if (cut && w == tid >> 5) list[n + __popc(cuts & ((1u << lane) - 1))] = tid;
+    n += found[w];
   }
-  const int r = rank * 64 + row;
-  if constexpr (kMergeGroups > 1) {
-    __shared__ float sm[kMergeGroups][18][128];
-    sm[group][16][L] = m;
-    sm[group][17][L] = l;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) sm[group][k][L] = o[k];
-    __syncthreads();
-    if (group != 0) return;
-    for (int g = 1; g < kMergeGroups; ++g) {
-      const float mg = sm[g][16][L], lg = sm[g][17][L];
-      if (mg == -INFINITY && lg == 0.f) continue;
-      const float top = fmaxf(m, mg);
-      const float f = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(mg - top);
-      m = top;
-      l = l * f + w * lg;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) o[k] = o[k] * f + w * sm[g][k][L];
-    }
+  __syncthreads();
+  for (int i = blockIdx.x; i < n * MergeMany::kItems; i += gridDim.x) {
+    const int from = list[i / MergeMany::kItems];
+    merge.run(p, p.records[from], from, i % MergeMany::kItems);
   }
-  if (r >= rec.y) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t y[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0u : pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
-  const int64_t g = rec.x + r;
-  uint16_t* out = p.out + g * 512 + (unit >> 5) * 256 + half * 128 + (unit & 31) * 4;
-  const uint4 a = make_uint4(y[0], y[1], y[2], y[3]), b = make_uint4(y[4], y[5], y[6], y[7]);
-  if (p.out32) {
-    stg32(out, a, b);
-  } else {
-    reinterpret_cast<uint4*>(out)[0] = a;
-    reinterpret_cast<uint4*>(out)[1] = b;
-  }
-  if (unit == 0 && half == 0 && p.lse != nullptr)
-    p.lse[g] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
 // ------------------------------------------------------------------ host side
@@ -1332,9 +1383,9 @@ constexpr size_t kExpandBytes = size_t(4) << 30;  // workspace spent on it at mo
 inline int row_blocks(const mla_dims& d) {
   return static_cast<int>((static_cast<int64_t>(d.S1) * d.n_q + kRowBlock - 1) / kRowBlock);
 }
-// Teams with a share of kMinTiles each in the longest stream that `passes` groups of row blocks can give.
+// Teams with a tile each in the longest stream that `passes` groups of row blocks can give.
 inline int64_t most_teams(const mla_dims& d, int64_t passes) {
-  return std::max<int64_t>(1, d.B * passes * ((static_cast<int64_t>(d.max_blocks_per_seq) + 1) / 2) / kMinTiles);
+  return std::max<int64_t>(1, d.B * passes * ((static_cast<int64_t>(d.max_blocks_per_seq) + 1) / 2));
 }
 
 // The workspace: partial states, records, expanded rows.  It has room for the
@@ -1600,10 +1651,9 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   if (plan.teams > 1)
     // parts of a row block, if the sequences were equally long
     TREE_CUDA(plan.teams > 6 * static_cast<int64_t>(d.B) * plan.passes
-                  ? launch_after(mlatree::tree_merge_kernel<4>, dim3(static_cast<unsigned>(plan.clusters), 32), 512, 0, s,
-                                 true, p)
-                  : launch_after(mlatree::tree_merge_kernel<1>, dim3(static_cast<unsigned>(plan.clusters), 32), 128, 0, s,
-                                 true, p),
+                  ? launch_after(mlatree::tree_merge_many_kernel, dim3(2 * 152), mlatree::MergeMany::kThreads, 0, s, true, p)
+                  : launch_after(mlatree::tree_merge_kernel, dim3(static_cast<unsigned>(plan.clusters), mlatree::MergeFew::kItems),
+                                 mlatree::MergeFew::kThreads, 0, s, true, p),
               "merge launch");
   return MLA_OK;
 }

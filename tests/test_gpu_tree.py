@@ -168,6 +168,14 @@ def test_long_contexts_cut_between_clusters(int8):
     assert check(make(3, [9000, 20, 4000], 5, 70, int8=int8)) == 0
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("act,S1,n_q", [([20000], 1, 128), ([20000], 1, 1), ([300], 1, 100), ([6000, 0, 130, 5000], 3, 40),
+                                        ([1000] * 8, 3, 96), ([40000], 2, 65)])
+def test_tables_wider_than_the_lengths(act, S1, n_q, int8):
+    """Room for more teams than there are tiles; row blocks with a part from almost every team."""
+    assert check(make(31, act, S1, n_q, int8=int8, W=700)) == 0
+
+
 def test_many_sequences():
     rng = np.random.default_rng(4)
     act = rng.integers(0, 400, 700).tolist()
