@@ -1158,44 +1158,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
 
 // ------------------------------------------------------------------ INT8 rows to bf16
 // Every used page of every sequence once, 16 codes of a thread at a time, into
-// rows of the same number.  Bound by memory: 656 bytes in, 1024 out per row;
-// 13 sequences of 500 to 20000 positions, 67 thousand rows, in 24 us.
-__global__ void __launch_bounds__(256) tree_dequant_kernel(const int8_t* __restrict__ codes,
-                                                           const __grid_constant__ Params p, uint16_t* out) {
+// rows of the same number.  Bound by memory: 656 bytes in, 1024 out per row; 13
+// sequences of 500 to 20000 positions, 67 thousand rows, in 14.6 us.  A block
+// takes a quarter of a page, which evens the blocks out (halves 15.8, whole
+// pages 24).
+__global__ void __launch_bounds__(256, 8)
+    tree_dequant_kernel(const int8_t* __restrict__ codes, const __grid_constant__ Params p, uint16_t* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int col = threadIdx.x & 31, r0 = threadIdx.x >> 5;  // 16 codes of rows r0, r0 + 8, ...
   for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
     const Seq q = load_seq(p, b);
     if (q.blocks == 0) continue;
     const int pages = (min(q.act, p.W * kPage) + kPage - 1) / kPage;
-    for (int lb = blockIdx.x; lb < pages; lb += gridDim.x) {
+    for (int i = blockIdx.x; i < 4 * pages; i += gridDim.x) {
+      const int lb = i / 4, first = i % 4 * 32;  // of the page's rows
       const int id = page_id(p, b, lb);
       if (!good(p, id)) continue;
-      const int rows = min(kPage, q.act - lb * kPage);
-      const int64_t row0 = static_cast<int64_t>(id) * kPage;
-      const int col = threadIdx.x & 31, r0 = threadIdx.x >> 5;  // 16 codes of rows r0, r0 + 8, ...
-      for (int it = 0; it < 16 && 8 * it < rows; it += 8) {
-        uint4 v[8];
-        float sc[8];
+      const int rows = min(32, q.act - lb * kPage - first);
+      const int64_t row0 = static_cast<int64_t>(id) * kPage + first;
+      uint4 v[4];
+      float sc[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = r0 + 8 * (it + k);
-          v[k] = make_uint4(0, 0, 0, 0);
-          sc[k] = 0.f;
-          if (r < rows) {
-            v[k] = __ldg(reinterpret_cast<const uint4*>(codes + (row0 + r) * 512) + col);
-            sc[k] = __ldg(p.kv_scales + (row0 + r) * 4 + (col >> 3));
-          }
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + 8 * k;
+        v[k] = make_uint4(0, 0, 0, 0);
+        sc[k] = 0.f;
+        if (r < rows) {
+          v[k] = __ldg(reinterpret_cast<const uint4*>(codes + (row0 + r) * 512) + col);
+          sc[k] = __ldg(p.kv_scales + (row0 + r) * 4 + (col >> 3));
         }
+      }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = r0 + 8 * (it + k);
-          uint4 x, y;
-          dequant4(v[k].x, sc[k], x.x, x.y);
-          dequant4(v[k].y, sc[k], x.z, x.w);
-          dequant4(v[k].z, sc[k], y.x, y.y);
-          dequant4(v[k].w, sc[k], y.z, y.w);
-          if (r < rows) stg32(out + (row0 + r) * 512 + col * 16, x, y);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + 8 * k;
+        uint4 x, y;
+        dequant4(v[k].x, sc[k], x.x, x.y);
+        dequant4(v[k].y, sc[k], x.z, x.w);
+        dequant4(v[k].z, sc[k], y.x, y.y);
+        dequant4(v[k].w, sc[k], y.z, y.w);
+        if (r < rows) stg32(out + (row0 + r) * 512 + col * 16, x, y);
       }
     }
   }
@@ -1374,9 +1375,9 @@ inline int team_size(int blocks, int clusters, bool ragged) {
 // A sequence of several row blocks has its INT8 rows converted once, into the
 // workspace, rather than by every cluster that reads them (each converts a key
 // twice: as a key and as a value).  Converted by the clusters / expanded first,
-// us: one row block, 64 sequences of 8192: 183 / 285; two, the same: 336 / 363,
-// 64 of 100 to 8192: 107 / 128, 16 of 3000: 54 / 56; three, 64 of 8192: 496 /
-// 448; 17, 13 of 500 to 20000: 383 / 248; 64, one of 32768: 650 / 343.
+// us: one row block, 64 sequences of 8192: 182 / 271; two, the same: 334 / 345,
+// 64 of 100 to 8192: 107 / 112, 16 of 3000: 53 / 50; three, 64 of 8192: 494 /
+// 431; up to 17, 13 of 500 to 20000: 152 / 117; 64, one of 32768: 649 / 337.
 constexpr int kExpandBlocks = 3;
 constexpr size_t kExpandBytes = size_t(4) << 30;  // workspace spent on it at most
 
@@ -1613,7 +1614,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   const void* latent = kv_nope;
   if (ws.expand) {
     uint16_t* wide = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + ws.rows_at);
-    const int per_seq = std::max(1, std::min(d.max_blocks_per_seq, 152 * 8 / d.B));
+    const int per_seq = std::max(1, std::min(4 * d.max_blocks_per_seq, 152 * 32 / d.B));
     mlatree::tree_dequant_kernel<<<dim3(static_cast<unsigned>(per_seq), static_cast<unsigned>(std::min(d.B, 65535))), 256, 0, s>>>(
         static_cast<const int8_t*>(kv_nope), p, wide);
     TREE_CUDA(cudaGetLastError(), "INT8 expansion launch");
