@@ -529,12 +529,11 @@ def prolog_device_status(clear: bool = True, stream=None) -> int:
 def _need(t, dtype, shape, dev: int, what: str):
     """Pointer of one tensor of the calls below, which has to be dense, of this
     type and (where given) shape, on the current device `dev`."""
-    if t.dtype is not dtype or t.get_device() != dev or (shape is not None and t.shape != shape) or \
-            not t.is_contiguous():
-        raise ValueError(f"{what} must be a dense {dtype} tensor on cuda:{dev}"
-                         + (f" of shape {tuple(shape)}" if shape is not None else "")
-                         + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a dense {dtype} tensor on cuda:{dev}"
+                     + (f" of shape {tuple(shape)}" if shape is not None else "")
+                     + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -560,14 +559,15 @@ def mla_page_plan(ctx_lens, new_lens, free_blocks, block_table, act_seqs, cache_
     B, W = block_table.shape
     T = cache_index.numel()
     dev = torch.cuda.current_device()
-    io = PageIo(_need(ctx_lens, i32, (B,), dev, "ctx_lens"),
-                None if new_lens is None else _need(new_lens, i32, (B,), dev, "new_lens"),
+    per_seq, per_row = (B,), (T,)
+    io = PageIo(_need(ctx_lens, i32, per_seq, dev, "ctx_lens"),
+                None if new_lens is None else _need(new_lens, i32, per_seq, dev, "new_lens"),
                 _need(free_blocks, i32, None, dev, "free_blocks"),
                 None if parents is None else _need(parents, i32, (B, S1), dev, "parents"),
-                _need(block_table, i32, None, dev, "block_table"), _need(act_seqs, i32, (B,), dev, "act_seqs"),
-                _need(cache_index, torch.int64, (T,), dev, "cache_index"),
-                None if positions is None else _need(positions, i32, (T,), dev, "positions"),
-                None if seq_ids is None else _need(seq_ids, i32, (T,), dev, "seq_ids"),
+                _need(block_table, i32, None, dev, "block_table"), _need(act_seqs, i32, per_seq, dev, "act_seqs"),
+                _need(cache_index, torch.int64, per_row, dev, "cache_index"),
+                None if positions is None else _need(positions, i32, per_row, dev, "positions"),
+                None if seq_ids is None else _need(seq_ids, i32, per_row, dev, "seq_ids"),
                 None if cu_seqs is None else _need(cu_seqs, i32, (B + 1,), dev, "cu_seqs"),
                 None if tree_mask is None else _need(tree_mask, torch.int64, (T, (S1 + 63) // 64), dev, "tree_mask"),
                 None if num_taken is None else _need(num_taken, i32, (1,), dev, "num_taken"))
