@@ -1038,7 +1038,9 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
               make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
       }
       if (part == 0) {
-        dst[128 * 256 + row] = m;
+        // -inf says that the part is not the row's; the lowest maximum joins with weight 0 and
+        // brings along the NaN of infinite values whose scores are all -inf
+        dst[128 * 256 + row] = live ? fmaxf(m, -3.402823466e38f) : m;
         dst[128 * 256 + 64 + row] = l;
       }
       if (at == 1 && warp == 0 && lane == 0 && c.rank == 0) {
