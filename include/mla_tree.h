@@ -18,9 +18,12 @@
  *   out  = sum_p softmax(z)_p kv_nope[r_p, :],   lse = ln sum_p exp(z_p)
  *   r_p  = block_table[b, p / 128] * 128 + p % 128
  *
- * A token that sees nothing, and padding tokens s >= n_b, get out = 0 and
- * lse = -inf.  What lies in rows at and beyond act_b does not matter, nor do
- * table entries of pages beyond it.
+ * A token that sees nothing, or scores -inf on all that it sees, and padding
+ * tokens s >= n_b get out = 0 and lse = -inf.  What lies in rows at and beyond
+ * act_b does not matter, nor do table entries of pages beyond it, and a NaN or
+ * infinity in a row reaches only the tokens that see it.  Those get what the
+ * formulas give: a score that is NaN or +inf makes out and lse NaN, and an
+ * infinite value whose score is -inf (weight 0) makes its column of out NaN.
  * A block id outside [0, num_blocks), or a position beyond the table, is
  * masked out and raises MLA_DEVICE_BAD_BLOCK.  Negative act_b and tree_lens
  * count as 0.

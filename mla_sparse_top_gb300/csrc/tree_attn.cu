@@ -132,7 +132,8 @@ constexpr int kRawEmpty = kRawFull + kRawSlots;  // [kRawSlots] INT8: they have 
 constexpr int kNumBars = kRawEmpty + kRawSlots;
 constexpr int kOffTmem = kOffBars + 8 * kNumBars;
 constexpr int kOffAbort = kOffTmem + 4;
-constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // 1024: the base is aligned by hand
+constexpr int kOffMended = kOffAbort + 4;  // a drafted value of either CTA was NaN or infinite
+constexpr int kSmemBytes = kOffMended + 4 + 1024;  // 1024: the base is aligned by hand
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kOffRing % 1024 == 0 && kOffP % 1024 == 0 && kOffBars % 8 == 0, "alignment");
 
@@ -233,6 +234,7 @@ struct Ctx {
   uint32_t tmem, rank;
   uint64_t wait_ns;
   volatile uint32_t* abort;
+  __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
   __device__ uint32_t bar(int i) const { return sb + kOffBars + 8 * i; }
   __device__ uint32_t lead(int i) const { return mapa_shared(bar(i), 0); }  // the barrier in CTA 0
 };
@@ -435,8 +437,18 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
   return w;
 }
-__device__ __forceinline__ uint4 finite8(uint4 v) {
-  return make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+__device__ __forceinline__ uint4 finite8(uint4 v, bool& mended) {
+  const uint4 f = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+  mended = mended || ((f.x ^ v.x) | (f.y ^ v.y) | (f.z ^ v.z) | (f.w ^ v.w)) != 0;
+  return f;
+}
+// Tells the softmax warps of both CTAs, before the barrier that hands the values
+// on: the fence returns when the other CTA's shared memory has the word.
+__device__ __noinline__ void post_mended(uint32_t sb) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    asm volatile("st.shared::cluster.u32 [%0], 1;" :: "r"(mapa_shared(sb + kOffMended, r)) : "memory");
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // First row of page `lb` of the sequence; one beyond the cache, where TMA fills
@@ -495,19 +507,22 @@ struct Items {
 
 // Rows of a value item (64 keys x 128 dims, bf16, in the slot) that the second
 // product must not see as they are: unwritten ones become zero, drafted ones
-// lose their NaN and infinities (0 * NaN; a token that sees such a row gets its
-// NaN through the score).
-__device__ __forceinline__ void mend_values(uint32_t slot, const Item& it, int lane) {
+// lose their NaN and infinities, which a weight of 0 would carry to tokens that
+// do not see them.  A token that sees such a row gets its NaN through the score,
+// or, where an infinity scores -inf, from infinite_columns().
+__device__ __forceinline__ void mend_values(const Ctx& c, uint32_t slot, const Item& it, int lane) {
   const int unit = lane & 15;
+  bool mended = false;
   for (int r = max(0, min(it.first_draft, it.rows)) + (lane >> 4); r < 64; r += 2) {
     const uint32_t at = slot + (unit >> 3) * kChunk + r * 128 + (((unit & 7) ^ (r & 7)) << 4);
     uint4 v = make_uint4(0, 0, 0, 0);
     if (r < it.rows) {
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-      v = finite8(v);
+      v = finite8(v, mended);
     }
     sts16(at, v);
   }
+  if (mended) post_mended(c.sb);
 }
 
 // bf16: producer warp w fills ring slot w.
@@ -540,7 +555,7 @@ __device__ void producer_role(const Params& p, const Ctx& c, const Maps& maps, c
       __syncwarp();
       if (mend) {
         if (!warp_wait(c, kLocal + w, mended++ & 1)) return;
-        mend_values(slot, cur, lane);
+        mend_values(c, slot, cur, lane);
         fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
         __syncwarp();
         if (lane == 0) arrive_lead(full);
@@ -645,6 +660,7 @@ __device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Wa
     if (!free_slot(item)) return false;
     const int u0 = 2 * (col & 3);
     const uint32_t dst0 = c.sb + kOffRing + (item & 3) * kSlotBytes + (col >> 2) * kChunk;
+    bool mended = false;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = r0 + ((32 * k) >> us);
@@ -654,12 +670,13 @@ __device__ void convert_role(const Params& p, const Ctx& c, const Maps& maps, Wa
       dequant4(v[k].z, sc[k], b.x, b.y);
       dequant4(v[k].w, sc[k], b.z, b.w);
       if (us == 3 && r >= mend) {
-        a = r < end ? finite8(a) : make_uint4(0, 0, 0, 0);
-        b = r < end ? finite8(b) : make_uint4(0, 0, 0, 0);
+        a = r < end ? finite8(a, mended) : make_uint4(0, 0, 0, 0);
+        b = r < end ? finite8(b, mended) : make_uint4(0, 0, 0, 0);
       }
       sts16(dst0 + r * 128 + ((u0 ^ (r & 7)) << 4), a);
       sts16(dst0 + r * 128 + (((u0 + 1) ^ (r & 7)) << 4), b);
     }
+    if (us == 3 && mended) post_mended(c.sb);
     fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
     __syncwarp();
     if (lane == 0) {
@@ -861,6 +878,42 @@ __device__ __forceinline__ void stg32(void* ptr, uint4 a, uint4 b) {
                : "memory");
 }
 
+// The NaN of 0 times infinity that mending the values took from a row: 128
+// columns from `col` of drafted positions [lo, hi) that token `tok` sees, put
+// into what the calling thread has stored: out, or its part of a partial state.
+// Rare: the values of some draft were not finite.
+__device__ __noinline__ void infinite_columns(const Params& p, int b, int ctx, int lo, int hi, const uint64_t* mrow,
+                                              int tok, int col, uint16_t* out, float* part) {
+  auto spoil = [&](int k) {
+    if (out != nullptr) out[k] = 0x7FC0;
+    else part[(k >> 2) * 512 + (k & 3)] = __uint_as_float(0x7FC00000u);
+  };
+  for (int pos = lo; pos < hi; ++pos) {
+    const int j = pos - ctx, id = page_id(p, b, pos / kPage);
+    if (!(mrow != nullptr ? (__ldg(mrow + (j >> 6)) >> (j & 63)) & 1 : j <= tok) || !good(p, id)) continue;
+    const int64_t row = static_cast<int64_t>(id) * kPage + pos % kPage;
+    if (p.kv_scales != nullptr) {
+      const float scale = __ldg(p.kv_scales + row * 4 + col / 128);
+      if (fabsf(scale) < 0x1p120f) continue;  // 128 codes times it stay below 2^127
+      for (int k = 0; k < 128; ++k) {
+        const float code = static_cast<float>(static_cast<int8_t>(__ldg(p.kv_nope + row * 512 + col + k)));
+        if ((pack_bf16x2(code * scale, 0.f) & 0x7F80u) == 0x7F80u) spoil(k);
+      }
+    } else {
+      const uint4* v = reinterpret_cast<const uint4*>(p.kv_nope + (row * 512 + col) * 2);
+      for (int u = 0; u < 16; ++u) {
+        const uint4 x = __ldg(v + u);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((w[k] & 0x7F80u) == 0x7F80u) spoil(8 * u + 2 * k);
+          if ((w[k] & 0x7F800000u) == 0x7F800000u) spoil(8 * u + 2 * k + 1);
+        }
+      }
+    }
+  }
+}
+
 __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, int teams, int64_t total, int warp,
                              int lane) {
   const int q = warp & 3, sub = warp >> 2;  // TMEM lane quadrant, column half
@@ -1020,6 +1073,8 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
           }
         }
       }
+      if (*c.mended() && live && l != 0.f)
+        infinite_columns(p, s.b, s.ctx, max(0, s.ctx), s.act, mrow, tok, sub * 256 + half * 128, o, nullptr);
       if (part == 0 && r < p.rows && p.lse != nullptr)
         p.lse[grow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     } else {
@@ -1037,6 +1092,9 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
           reinterpret_cast<uint4*>(dst)[(sub * 32 + ch * 8 + k) * 128 + L] =
               make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
       }
+      if (*c.mended() && live)
+        infinite_columns(p, s.b, s.ctx, max(max(0, s.ctx), kTile * s.t0), min(s.act, kTile * s.t1), mrow, tok,
+                         sub * 256 + half * 128, nullptr, dst + (sub * 32 * 128 + L) * 4);
       if (part == 0) {
         // -inf says that the part is not the row's; the lowest maximum joins with weight 0 and
         // brings along the NaN of infinite values whose scores are all -inf
@@ -1071,6 +1129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Conf<kInt8>::kThread
   const int cid = blockIdx.x >> 1;
   if (tid == 0) {
     *c.abort = 0u;
+    *c.mended() = 0u;
     if (c.rank == 0) p.records[cid] = make_int4(0, 0, 0, 0);  // nothing to merge, until this thread finds a cut
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(c.bar(kRawFull + i), 1);

@@ -84,6 +84,33 @@ def check(m):
     return o, e
 
 
+# one row block, a row block cut among a few clusters and among many, several row blocks (INT8: rows expanded first)
+SHAPES = [dict(act=[300], S1=6, n_q=16), dict(act=[9000], S1=2, n_q=64), dict(act=[700, 20000], S1=3, n_q=5, W=700),
+          dict(act=[300, 1000], S1=4, n_q=128)]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_a_drafted_infinity_gives_what_the_formula_gives(shape, tree, value, int8):
+    m = make(40, int8=int8, tree=tree, **shape)
+    one_sided(m, slice(128, 256))
+    b, S1 = len(m["act"]) - 1, m["S1"]
+    j = S1 // 2
+    if tree:  # the last token sees it, the one before does not
+        m["masks"][b * S1 + S1 - 1] |= 1 << j
+        if S1 - 2 != j:
+            m["masks"][b * S1 + S1 - 2] &= ~(1 << j)
+    spoil(m, b, int(m["act"][b]) - S1 + j, value, 200)
+    o, e = check(m)
+    last = o[b * S1 + S1 - 1]
+    # half of the heads score -inf there: they lose that column, or group of columns, alone
+    some = np.isnan(last).any(-1) & ~np.isnan(last).all(-1)
+    assert some.sum() == m["q_nope"].shape[1] // 2 or m["q_nope"].shape[1] % 2
+    assert np.isnan(last[:, 200]).all() and np.isfinite(o[b * S1]).all()
+
+
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("act,S1", [(9000, 1), (9000, 2), (20000, 1)])
 def test_context_infinities_survive_the_merge(act, S1, int8):
@@ -94,6 +121,15 @@ def test_context_infinities_survive_the_merge(act, S1, int8):
         spoil(m, 0, pos, float("inf"), 7)
     o, _ = check(m)
     assert np.isnan(o[:, 1::2, 7]).all() and np.isfinite(o[:, 1::2, 200]).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_part_of_drafts_alone_that_all_score_minus_infinity(int8):
+    m = make(42, [8192 + 4], 4, 16, int8=int8, tree=False, W=700)
+    one_sided(m, slice(128, 256))
+    for j in range(4):
+        spoil(m, 0, 8192 + j, float("inf"), 130)
+    check(m)
 
 
 def test_tokens_whose_every_score_is_minus_infinity():
