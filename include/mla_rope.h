@@ -70,17 +70,20 @@ typedef struct mla_rope_params {
 /*
  * mla_rope_table -- cos and sin, fp32 [T, rot_dim / 2] (the prolog's inputs
  * for rot_dim 64), times mscale, for positions int32 [T].  rot_dim even, in
- * [2, 256]; T = 0 is a no-op.
+ * [2, 256]; T = 0 is a no-op.  The three may not overlap (MLA_ERR_UNSUPPORTED).
  */
 mla_status mla_rope_table(const mla_rope_params* params, int32_t T, int32_t rot_dim, const int32_t* positions,
                           float* cos, float* sin, void* stream);
 
 /* One tensor of mla_rope_apply: element (t, h, d) at t * token_stride + h *
- * head_stride + d.  out may be x with the same strides (in place); any other
- * overlap is not allowed.  With `rows`, token t is written to row rows[t] of
- * out instead of row t: a negative row is skipped, one at or beyond num_rows
+ * head_stride + d.  out may be x with the same strides (in place; the rotated
+ * part alone is read and written); otherwise no output may have a byte in common
+ * with what the call reads or with the other output (MLA_ERR_UNSUPPORTED).
+ * Views that interleave, such as the queries and keys of one fused tensor, are
+ * told apart by their strides.  With `rows`, token t is written to row rows[t]
+ * of out instead of row t: a negative row is skipped, one at or beyond num_rows
  * is skipped and raises MLA_DEVICE_BAD_BLOCK (as the cache writer does); rows
- * are expected to be distinct, and x must not overlap out. */
+ * are expected to be distinct. */
 typedef struct mla_rope_tensor {
   const void* x;
   void* out;

@@ -406,6 +406,71 @@ mla_status rope_fail(mla_status s, const char* fmt, ...) {
 
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 
+// What a call reads or writes: a run of bytes at each of n[0] x n[1] places.
+struct Area {
+  uintptr_t at;
+  int64_t n[2], stride[2], bytes;  // strides in bytes
+};
+Area run(const void* ptr, int64_t bytes) { return {reinterpret_cast<uintptr_t>(ptr), {1, 1}, {0, 0}, bytes}; }
+Area area_of(const mla_rope_tensor* q, const mla_rope_dims& d, bool out) {
+  const int64_t size = d.dtype == MLA_ROPE_FP32 ? 4 : 2;
+  const bool same = q->x == q->out;  // in place, the rotated part alone is touched
+  const int64_t first = same ? q->rot_off : 0, values = same ? d.rot_dim : q->head_dim;
+  return {reinterpret_cast<uintptr_t>(out ? q->out : q->x) + static_cast<uintptr_t>(first * size),
+          {out && q->rows ? q->num_rows : d.T, q->n_heads},
+          {(out ? q->out_token_stride : q->x_token_stride) * size, (out ? q->out_head_stride : q->x_head_stride) * size},
+          values * size};
+}
+
+// Whether the areas have a byte in common.  Views of one tensor interleave, so
+// areas whose stretches overlap are also told apart by their strides: runs of a
+// and b bytes that repeat at multiples of g miss one another when the distance
+// of their starts, modulo g, is at least a, and b short of g.  Tried for whole
+// tokens, whole heads and single runs; what none of them tells apart counts as
+// overlapping.
+bool overlap(const Area& a, const Area& b) {
+  typedef __int128 Wide;  // 2^40 places times a stride of 2^42
+  const Wide delta = static_cast<Wide>(b.at) - static_cast<Wide>(a.at);
+  auto stride = [](const Area& x, int i) { return x.n[i] > 1 ? static_cast<Wide>(x.stride[i]) : 0; };
+  auto length = [&](const Area& x, int i) { return static_cast<Wide>(x.n[i] - 1) * stride(x, i) + x.bytes; };
+  auto gcd = [](Wide x, Wide y) {
+    while (y != 0) {
+      const Wide r = x % y;
+      x = y;
+      y = r;
+    }
+    return x;
+  };
+  auto apart = [&](Wide g, Wide la, Wide lb) {
+    if (g == 0) return false;  // nothing repeats: the stretches have been compared
+    const Wide r = (delta % g + g) % g;
+    return r >= la && g - r >= lb;
+  };
+  if (delta >= length(a, 0) + length(a, 1) - a.bytes || -delta >= length(b, 0) + length(b, 1) - b.bytes) return false;
+  const Wide tokens = gcd(stride(a, 0), stride(b, 0)), heads = gcd(stride(a, 1), stride(b, 1));
+  return !(apart(tokens, length(a, 1), length(b, 1)) || apart(heads, length(a, 0), length(b, 0)) ||
+           apart(gcd(tokens, heads), a.bytes, b.bytes));
+}
+
+// Refuses outputs that overlap what the call reads, or one another: threads read and write in no order.
+mla_status check_overlaps(const mla_rope_dims& d, const int32_t* positions, const mla_rope_tensor* q,
+                          const mla_rope_tensor* k) {
+  const mla_rope_tensor* t[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    if (t[i] == nullptr) continue;
+    const Area out = area_of(t[i], d, true);
+    bool hit = overlap(out, run(positions, 4ll * d.T));
+    for (int j = 0; j < 2; ++j) {
+      if (t[j] == nullptr) continue;
+      hit = hit || ((i != j || t[i]->x != t[i]->out) && overlap(out, area_of(t[j], d, false)));
+      hit = hit || (i < j && overlap(out, area_of(t[j], d, true)));
+      hit = hit || (t[j]->rows != nullptr && overlap(out, run(t[j]->rows, 8ll * d.T)));
+    }
+    if (hit) return rope_fail(MLA_ERR_UNSUPPORTED, "%s's output overlaps an input or the other output", i ? "k" : "q");
+  }
+  return MLA_OK;
+}
+
 // Checks the scheme and fills the fixed-point turns per position.
 mla_status make_freqs(const mla_rope_params* q, int rot, mlarp::Freqs* f) {
   if (q == nullptr) return rope_fail(MLA_ERR_NULL, "params is NULL");
@@ -530,6 +595,9 @@ mla_status mla_rope_table(const mla_rope_params* params, int32_t T, int32_t rot_
   if (!positions || !cos || !sin) return rope_fail(MLA_ERR_NULL, "a required pointer is NULL");
   if (!aligned(positions, 4) || !aligned(cos, 4) || !aligned(sin, 4))
     return rope_fail(MLA_ERR_ALIGN, "tensors must be 4-byte aligned");
+  const Area table[] = {run(cos, 2ll * T * rot_dim), run(sin, 2ll * T * rot_dim), run(positions, 4ll * T)};
+  if (overlap(table[0], table[1]) || overlap(table[0], table[2]) || overlap(table[1], table[2]))
+    return rope_fail(MLA_ERR_UNSUPPORTED, "cos, sin and positions overlap");
   p.positions = positions;
   p.cos = cos;
   p.sin = sin;
@@ -562,6 +630,7 @@ mla_status mla_rope_apply(const mla_rope_dims* dims, const mla_rope_params* para
   bool vec = true;
   st = check_tensor(q, d, "q", &vec);
   if (st == MLA_OK && k != nullptr) st = check_tensor(k, d, "k", &vec);
+  if (st == MLA_OK) st = check_overlaps(d, positions, q, k);
   if (st == MLA_OK) st = split_tensor(q, d, "q", vec, &p.t[0]);
   if (st != MLA_OK) return st;
   p.t[1] = p.t[0];

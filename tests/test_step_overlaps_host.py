@@ -1,0 +1,53 @@
+"""Outputs that overlap inputs or one another are refused before any CUDA call
+(fake addresses; every call below is refused).  Skipped where there is a GPU: a
+call that was not refused would go to those addresses."""
+import ctypes
+
+import pytest
+import torch
+
+from test_step_abi_host import lib, ptr, rope_call, rope_params  # noqa: F401
+
+UNSUPPORTED = -4
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses stay off a GPU")
+
+
+# q: 8 tokens x 4 heads x 192 bf16 values from ptr(0) to ptr(1), 12288 bytes each
+@pytest.mark.parametrize("tensor", [
+    dict(out=ptr(0) + 2), dict(out=ptr(0) + 128 * 2), dict(out=ptr(0) + 12286), dict(x=ptr(1) + 12286),
+    dict(out=ptr(0) + 192 * 2),                                           # a head further on
+    dict(out=ptr(0) + 4 * 192 * 2),                                       # a token further on
+    dict(x=ptr(1) + 64, x_token_stride=0, x_head_stride=0),               # a broadcast input inside the output
+    dict(out=ptr(0) + 100, out_token_stride=5 * 192, out_head_stride=240),  # other strides
+    dict(out=ptr(9) - 12288 + 16),                                        # positions in the last token
+    dict(out=ptr(9) + 28),                                                # the last position
+    dict(rows=ptr(1) + 64, num_rows=8),                                   # the list of rows in the output
+    dict(x=ptr(60), rows=ptr(5), num_rows=100, out=ptr(60) - 1536 * 99),   # the cache's last row is the first token
+])
+def test_rope_apply_refuses_overlaps(lib, tensor):  # noqa: F811
+    assert rope_call(lib, None, tensor) == UNSUPPORTED
+    assert lib.mla_rope_last_error()
+    apart = dict(x=ptr(100), out=ptr(101))
+    assert rope_call(lib, None, apart, tensor) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("k", [
+    dict(x=ptr(50), out=ptr(1)), dict(x=ptr(50), out=ptr(1) + 12286), dict(x=ptr(1) + 12286, out=ptr(50)),
+    dict(x=ptr(50), out=ptr(0) + 1536), dict(x=ptr(0), out=ptr(0)),
+])
+def test_rope_apply_refuses_overlaps_of_the_two_tensors(lib, k):  # noqa: F811
+    assert rope_call(lib, None, None, k) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("first", [64, 32, 127, 1])
+def test_rope_apply_in_place_refuses_parts_that_meet(lib, first):  # noqa: F811
+    """q turns values [128, 192) of a tensor in place, k values [first + 64, first + 128) of the same one."""
+    k = dict(x=ptr(0) + 2 * first, out=ptr(0) + 2 * first, rot_off=64, head_dim=128)
+    assert rope_call(lib, None, dict(x=ptr(0), out=ptr(0)), k) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("a", [(ptr(0), ptr(1), ptr(1) + 4 * 127), (ptr(0), ptr(1), ptr(1)), (ptr(0), ptr(0) + 12, ptr(2)),
+                               (ptr(0), ptr(2), ptr(0) + 8), (ptr(0) + 500, ptr(0), ptr(2))])
+def test_rope_table_refuses_overlaps(lib, a):  # noqa: F811
+    assert lib.mla_rope_table(ctypes.byref(rope_params()), 4, 64, *a, None) == UNSUPPORTED
+    assert lib.mla_rope_last_error()
