@@ -73,7 +73,8 @@ size_t mla_tree_workspace_bytes(const mla_dims* dims);
  * out         bf16 [B*S1, n_q, 512], lse fp32 [B*S1, n_q] or NULL
  * workspace   >= mla_tree_workspace_bytes(dims) bytes, 256-byte aligned
  * q, kv, out and scales 16-byte aligned, tree_mask 8-byte, the rest 4-byte;
- * out, lse and the workspace may not overlap one another or the inputs.
+ * out, lse and the workspace may not overlap one another or the inputs
+ * (MLA_ERR_UNSUPPORTED).
  * Up to three launches on `stream` (INT8 rows of calls with three or more
  * blocks of 128 rows are turned into bf16 in the workspace first, if that
  * takes no more than 4 GB; the attention; the merge of rows whose keys several

@@ -1499,6 +1499,16 @@ mla_status tree_fail(mla_status s, const char* fmt, ...) {
 
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
 
+struct Range {
+  const void* ptr;
+  uint64_t bytes;
+};
+bool overlap(const Range& a, const Range& b) {
+  if (!a.ptr || !b.ptr || !a.bytes || !b.bytes) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.ptr), y = reinterpret_cast<uintptr_t>(b.ptr);
+  return x < y ? y - x < a.bytes : x - y < b.bytes;
+}
+
 mla_status check_dims(const mla_dims& d) {
   if (d.kv_dtype != MLA_KV_BF16 && d.kv_dtype != MLA_KV_INT8)
     return tree_fail(MLA_ERR_DTYPE, "kv_dtype %d is neither MLA_KV_BF16 nor MLA_KV_INT8", d.kv_dtype);
@@ -1637,6 +1647,18 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
   const mlatree::Workspace ws = mlatree::workspace_of(d);
   if (workspace_bytes < ws.bytes)
     return tree_fail(MLA_ERR_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.bytes);
+  // clusters read and write in no order: nothing that a call reads may be an output
+  const uint64_t toks = static_cast<uint64_t>(d.B) * d.S1, heads = toks * d.n_q, pool = 128ull * d.num_blocks;
+  const Range in[] = {{q_nope, heads * 1024}, {q_rope, heads * 128}, {kv_nope, pool * (int8 ? 512 : 1024)},
+                      {kv_rope, pool * 128}, {int8 ? kv_scales : nullptr, pool * 16},
+                      {block_table, 4ull * d.B * d.max_blocks_per_seq}, {act_seqs, 4ull * d.B}, {tree_lens, 4ull * d.B},
+                      {tree_mask, 8 * toks * ((d.S1 + 63) / 64)}};
+  const Range outs[] = {{out, heads * 1024}, {lse, heads * 4}, {workspace, ws.bytes}};
+  for (const Range& o : outs)
+    for (const Range& i : in)
+      if (overlap(o, i)) return tree_fail(MLA_ERR_UNSUPPORTED, "an output or the workspace overlaps an input");
+  if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2]))
+    return tree_fail(MLA_ERR_UNSUPPORTED, "out, lse and the workspace overlap");
   int dev = 0;
   TREE_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   if (dev < 0 || dev >= mlatree::kMaxDevices) return tree_fail(MLA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);

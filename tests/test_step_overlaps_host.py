@@ -6,7 +6,7 @@ import ctypes
 import pytest
 import torch
 
-from test_step_abi_host import lib, ptr, rope_call, rope_params  # noqa: F401
+from test_step_abi_host import lib, ptr, rope_call, rope_params, tree_call  # noqa: F401
 
 UNSUPPORTED = -4
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses stay off a GPU")
@@ -51,3 +51,26 @@ def test_rope_apply_in_place_refuses_parts_that_meet(lib, first):  # noqa: F811
 def test_rope_table_refuses_overlaps(lib, a):  # noqa: F811
     assert lib.mla_rope_table(ctypes.byref(rope_params()), 4, 64, *a, None) == UNSUPPORTED
     assert lib.mla_rope_last_error()
+
+
+# 6 tokens x 128 heads, 16 pages, tables of 8 pages: every tensor at a place of its own, with room
+APART = {n: ptr(1000 * (i + 1)) for i, n in enumerate((
+    "q_nope", "q_rope", "kv_nope", "kv_rope", "kv_scales", "block_table", "act_seqs", "tree_lens", "tree_mask", "out",
+    "lse", "workspace"))}
+SIZES = dict(q_nope=6 * 128 * 1024, q_rope=6 * 128 * 128, kv_nope=2048 * 1024, kv_rope=2048 * 128, kv_scales=2048 * 16,
+             block_table=64, act_seqs=8, tree_lens=8, tree_mask=48, out=6 * 128 * 1024, lse=6 * 128 * 4)
+BIG = 1 << 40  # bytes given as workspace; the call needs some 10 MB of them
+
+
+@pytest.mark.parametrize("written", ["out", "lse", "workspace"])
+@pytest.mark.parametrize("other", [n for n in APART if n != "workspace"])
+def test_tree_attention_refuses_overlaps(lib, other, written):  # noqa: F811
+    if other == written:
+        return
+    int8 = dict(kv_dtype=1) if other == "kv_scales" else None
+    size = SIZES.get(written, 1 << 20)
+    for at in (APART[other], APART[other] + -(-SIZES[other] // 256) * 256 - 256, APART[other] - size // 256 * 256 + 256):
+        if at >= APART[other] + SIZES[other] or at + size <= APART[other]:
+            continue
+        assert tree_call(lib, int8, **{**APART, written: at}, nbytes=BIG) == UNSUPPORTED, (other, written, at)
+        assert lib.mla_tree_last_error()
