@@ -37,8 +37,8 @@
  * Conventions are those of mla_sparse.h: device pointers owned by the caller,
  * asynchronous on `stream` (one launch, nothing allocated), argument errors
  * returned before any launch with mla_page_last_error() describing them.
- * Outputs may not overlap inputs (act_seqs is not ctx_lens:
- * MLA_ERR_UNSUPPORTED).
+ * Outputs may not overlap inputs (act_seqs is not ctx_lens) or one another:
+ * MLA_ERR_UNSUPPORTED.
  */
 #ifndef MLA_PAGES_H_
 #define MLA_PAGES_H_

@@ -353,6 +353,9 @@ mla_status mla_page_plan(const mla_page_dims* dims, const mla_page_io* io, void*
   for (const Range& o : out)
     for (const Range& i : in)
       if (overlap(i, o)) return page_fail(MLA_ERR_UNSUPPORTED, "an output overlaps an input");
+  for (const Range& o : out)
+    for (const Range* q = out; q != &o; ++q)
+      if (overlap(*q, o)) return page_fail(MLA_ERR_UNSUPPORTED, "two outputs overlap");
   mlapg::Params p;
   p.io = *io;
   p.B = d.B;

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 import torch
 
-from test_step_abi_host import lib, ptr, rope_call, rope_params, tree_call  # noqa: F401
+from test_step_abi_host import lib, page_args, ptr, rope_call, rope_params, tree_call  # noqa: F401
 
 UNSUPPORTED = -4
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses stay off a GPU")
@@ -74,3 +74,19 @@ def test_tree_attention_refuses_overlaps(lib, other, written):  # noqa: F811
             continue
         assert tree_call(lib, int8, **{**APART, written: at}, nbytes=BIG) == UNSUPPORTED, (other, written, at)
         assert lib.mla_tree_last_error()
+
+
+# B = 2, S1 = 3, T = 6, W = 4
+WRITTEN = dict(block_table=32, act_seqs=8, cache_index=48, positions=24, seq_ids=24, cu_seqs=12, tree_mask=48, num_taken=4)
+
+
+@pytest.mark.parametrize("first", WRITTEN)
+@pytest.mark.parametrize("second", WRITTEN)
+def test_page_plan_refuses_outputs_over_one_another(lib, first, second):  # noqa: F811
+    if first == second:
+        return
+    base = ptr(500)
+    for at in (base, base + (WRITTEN[first] - 1) // 8 * 8):  # the same place, and the first one's last bytes
+        d, io = page_args(**{first: base, second: at})
+        assert lib.mla_page_plan(ctypes.byref(d), ctypes.byref(io), None) == UNSUPPORTED, at
+        assert lib.mla_page_last_error()
