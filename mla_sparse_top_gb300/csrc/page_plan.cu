@@ -310,7 +310,7 @@ struct Range {
   int64_t bytes;
 };
 bool overlap(const Range& a, const Range& b) {
-  if (!a.ptr || !b.ptr) return false;
+  if (!a.ptr || !b.ptr || !a.bytes || !b.bytes) return false;  // an empty list is nowhere
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.ptr), y = reinterpret_cast<uintptr_t>(b.ptr);
   return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
 }

@@ -90,3 +90,9 @@ def test_page_plan_refuses_outputs_over_one_another(lib, first, second):  # noqa
         d, io = page_args(**{first: base, second: at})
         assert lib.mla_page_plan(ctypes.byref(d), ctypes.byref(io), None) == UNSUPPORTED, at
         assert lib.mla_page_last_error()
+
+
+def test_page_plan_takes_an_empty_free_list_from_anywhere(lib):  # noqa: F811
+    """A list that has been used up may point into what the step writes: nothing of it is read."""
+    d, io = page_args(num_free=0, free_blocks=page_args()[1].block_table + 4)
+    assert lib.mla_page_plan(ctypes.byref(d), ctypes.byref(io), None) == -6, lib.mla_page_last_error()  # no device
