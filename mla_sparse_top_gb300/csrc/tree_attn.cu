@@ -1459,7 +1459,9 @@ struct Workspace {
 };
 inline Workspace workspace_of(const mla_dims& d) {
   const int blocks = row_blocks(d);
-  const size_t room = static_cast<size_t>(std::min<int64_t>(kMaxClusters, most_teams(d, blocks) * blocks));
+  // each factor bounded first: their product passes 64 bits for the largest dims
+  const size_t room = static_cast<size_t>(
+      std::min<int64_t>(kMaxClusters, std::min<int64_t>(kMaxClusters, most_teams(d, blocks)) * blocks));
   Workspace w;
   w.records_at = room * 4 * kPartFloats * sizeof(float);
   w.rows_at = (w.records_at + room * sizeof(int4) + 1023) & ~static_cast<size_t>(1023);
