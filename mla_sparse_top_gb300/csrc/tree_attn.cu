@@ -1354,8 +1354,9 @@ struct Merge {
   }
 };
 
-// The usual two or three parts (75 row blocks in 8 us): block x looks at the
-// record of cluster x, block y takes 16 columns of the 256 of one CTA.
+// The usual two or three parts (75 row blocks in 8 us), and up to some fifteen:
+// block x looks at the record of cluster x, block y takes 16 columns of the 256
+// of one CTA.
 using MergeFew = Merge<1, 4, 2>;
 __global__ void __launch_bounds__(MergeFew::kThreads) tree_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's stores are visible
@@ -1449,6 +1450,17 @@ inline int row_blocks(const mla_dims& d) {
 inline int64_t most_teams(const mla_dims& d, int64_t passes) {
   return std::max<int64_t>(1, d.B * passes * ((static_cast<int64_t>(d.max_blocks_per_seq) + 1) / 2));
 }
+
+// Which merge runs: the one for many parts where a row block has more than these
+// from equally long sequences.  One for few / for many parts, us, single tokens
+// of B sequences, 72 teams:
+//   B                     1          2          4          5          8          10
+//   4096 positions    20.7/18.7  20.8/18.9  23.4/23.0  27.0/29.0  28.2/32.1  29.2/35.4
+//   8192              23.6/20.7  26.8/20.9  29.6/29.2  27.0/28.9  35.0/39.0  39.0/44.6
+//   32768             36.3/25.8  36.8/31.1  54.3/53.6  62.9/64.0  83.6/87.0  96.2/101.2
+// and one sequence of 8 row blocks over 8192 (9 parts) 30.8/33.5.  With tables
+// much wider than the lengths the same; 300 positions there 18.6/16.9 (B = 1).
+constexpr int kManyParts = 16;
 
 // The workspace: partial states, records, expanded rows.  It has room for the
 // schedule of any device and any drafts (a team has at most as many clusters, a
@@ -1735,8 +1747,7 @@ mla_status mla_tree_attn_fwd(const mla_dims* dims, const void* q_nope, const voi
                            s, ws.expand, maps, p),
               "kernel launch");
   if (plan.teams > 1)
-    // parts of a row block, if the sequences were equally long
-    TREE_CUDA(plan.teams > 6 * static_cast<int64_t>(d.B) * plan.passes
+    TREE_CUDA(plan.teams > mlatree::kManyParts * static_cast<int64_t>(d.B) * plan.passes
                   ? launch_after(mlatree::tree_merge_many_kernel, dim3(2 * 152), mlatree::MergeMany::kThreads, 0, s, true, p)
                   : launch_after(mlatree::tree_merge_kernel, dim3(static_cast<unsigned>(plan.clusters), mlatree::MergeFew::kItems),
                                  mlatree::MergeFew::kThreads, 0, s, true, p),
