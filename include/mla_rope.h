@@ -32,7 +32,8 @@
  * rounding to the tensor's type at the end.
  *
  * Conventions are those of mla_sparse.h: device pointers owned by the caller,
- * asynchronous on `stream` (one launch per call, nothing allocated), argument
+ * asynchronous on `stream` (one launch per call, two where only one of two
+ * tensors has 16-byte aligned rows; nothing allocated), argument
  * errors returned before any launch with mla_rope_last_error() describing
  * them.
  */
@@ -108,8 +109,9 @@ typedef struct mla_rope_dims {
 /*
  * mla_rope_apply -- rotate the heads of one or two tensors (queries, and keys
  * or NULL) of the same tokens.  positions int32 [T].  Any strides and
- * alignments of whole elements work; 16-byte aligned rows and parts run in
- * 16-byte accesses.
+ * alignments of whole elements work; a tensor whose pointers, strides, head
+ * size and rotated part are multiples of 16 bytes (the halves of the part in the
+ * half layout) runs in 16-byte accesses, whatever the other one is.
  */
 mla_status mla_rope_apply(const mla_rope_dims* dims, const mla_rope_params* params, const int32_t* positions,
                           const mla_rope_tensor* q, const mla_rope_tensor* k, void* stream);
