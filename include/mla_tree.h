@@ -32,8 +32,10 @@
  * are bf16(fp32(code) * scale), as in mla_sparse.h; the softmax runs in fp32
  * with a running maximum and sum.  The weights enter the second product
  * rounded to bf16 once (at most 2^-8 relative each, as one rounding of a bf16
- * result costs; they are summed for l and lse unrounded); out is rounded to
- * bf16 once.  The result of a call does not depend on timing: a repeated call
+ * result costs; they are summed for l and lse unrounded), so an output is off by
+ * up to 2^-8 sum_p softmax_p |kv_nope_p| on top of its own rounding:
+ * mla_sparse_attn_fwd, which keeps 16 bits of a weight, holds a tighter bound.
+ * out is rounded to bf16 once.  The result of a call does not depend on timing: a repeated call
  * gives the same bits.
  *
  * Conventions are those of mla_sparse.h: device pointers owned by the caller,
@@ -76,9 +78,14 @@ size_t mla_tree_workspace_bytes(const mla_dims* dims);
  * out, lse and the workspace may not overlap one another or the inputs
  * (MLA_ERR_UNSUPPORTED).
  * Up to three launches on `stream` (INT8 rows of calls with three or more
- * blocks of 128 rows are turned into bf16 in the workspace first, if that
- * takes no more than 4 GB; the attention; the merge of rows whose keys several
- * clusters shared), capturable into a CUDA graph.  The first call on each
+ * blocks of 128 (token, head) rows a sequence are turned into bf16 in the
+ * workspace first, if that takes no more than 4 GB; the attention; the merge of
+ * rows whose keys several clusters shared), capturable into a CUDA graph.  The
+ * expanded rows take 128 KB of workspace for every block of the pool, whether
+ * the call uses it or not; above 32,768 blocks the attention converts the rows
+ * itself, which takes 1.15 to 1.9 times as long.  Every row block goes through all
+ * key tiles of its sequence: right for drafts, up to twice the work of a causal
+ * kernel for a prompt.  The first call on each
  * device sets the kernels' shared-memory attribute and looks up the driver's
  * tensor-map encoder: make it before any stream capture begins.
  */

@@ -79,8 +79,8 @@ struct TableParams {
 
 // A thread makes V adjacent pairs of kTableTokens positions, blockDim.y apart.  V = 4
 // (16-byte stores, an index for four values) wherever rows are that aligned:
-// 65536 positions of 32 pairs in 6.2 us (one position a thread, 1.7 rounds of
-// blocks, 8.2; single values 10.2).
+// 65536 positions of 32 pairs in 6.2 to 6.9 us, box by box (one position a thread,
+// 1.7 rounds of blocks, 8.2; single values 10.2).
 template <int V>
 constexpr int kTableTokens = V == 4 ? 2 : 4;
 template <int V>
@@ -290,7 +290,7 @@ __device__ __forceinline__ void rotate_rows(const Params& p, const Tensor& w, in
   }
 }
 
-// Both tensors in 16-byte units: 403 + 403 MB in 116 us, 98% of a copy's rate.
+// Both tensors in 16-byte units: 403 + 403 MB in 123 us, 98% of a copy's rate.
 template <typename E>
 __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ Params p) {
   const int second = static_cast<int>(blockIdx.x) >= p.t[0].blocks;

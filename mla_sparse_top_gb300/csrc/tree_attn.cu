@@ -43,12 +43,15 @@
 // 736 us from a cool start (1.59 PFLOP/s, 81% of the measured bf16 rate), 790 to
 // 820 us back to back, where the SM clock falls to ~1.6 GHz under the power cap;
 // one sequence, 64 drafts, 131072 positions: 1.51 ms, 1.55 PFLOP/s.  Bound by
-// shared memory: a tile of 256 keys moves 278 KB in, 275 KB out as B, 136 KB as A
-// and 32 KB of P, 5630 clocks at 128 bytes a clock, against 4406 clocks of MMA;
-// measured 5200 to 6000.  Single tokens, 64 sequences of 8192: 148 us for 604 MB:
-// bound by memory, ~8000 clocks a tile.  Prefetching the next tile's keys into L2
-// gained nothing there, without an eviction priority it lost 8%, two tiles ahead
-// 35% (lines leave L2 before their use: 1.04 GB read instead of 0.68).
+// shared memory: counted once each, a tile of 256 keys moves 279 KB in, 279 KB out
+// as B, 139 KB as A and 33 KB of P, 5700 clocks at 128 bytes a clock, against 4406
+// clocks of MMA; ~5900 by the cycle counter of a small case, set-up taken off.
+// Single tokens, 64 sequences of 8192: 145 to 154 us for 604 MB, 4.1 TB/s or 61% of
+// the copy rate, ~8000 clocks a tile: neither memory nor the tensor cores (40%
+// active) bind, but the latency from a load to its use over seven ring slots.
+// Prefetching the next tile's keys into L2 gained nothing there, without an
+// eviction priority it lost 8%, two tiles ahead 35% (lines leave L2 before their
+// use: 1.04 GB read instead of 0.68).
 // What shaped the kernel, at the largest case (us): arrivals on the other CTA's
 // barriers with release at CTA scope instead of cluster scope 2018 -> 1682; a
 // converged warp around an elected issuer instead of one running thread 2584 ->
@@ -1011,6 +1014,8 @@ __device__ void softmax_role(const Params& p, const Ctx& c, Walk walk, int cid, 
         e.x = fast_exp2(e.x);
         e.y = fast_exp2(e.y);
         sum[k & 1] = add2(sum[k & 1], pair(e.x, e.y));
+        // one bf16 term, off by 2^-8 of the weight at most: the second product and its operand
+        // in shared memory are half of what a second term for the rest would make them
         w[k] = pack_bf16x2(e.x, e.y);
       }
       const float2 sums = unpair(add2(sum[0], sum[1]));
@@ -1413,7 +1418,9 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 // power cap, where idle clusters let the others run faster, so idling counts
 // 0.3.  Drafts of unequal size (1 to 17 row blocks, 13 sequences): 122 / 123 /
 // 136 / 159; what a pass leaves idle there counts in full, on average over all
-// sizes.
+// sizes.  The host does not see the lengths, so equal drafts given with tree_lens
+// get the smaller teams too, with tree_lens / without it: 64 x 8 row blocks x 8192
+// 864 / 735 (short bursts), 16 x 4 x 4096 75.8 / 70.5, one of 64 x 131072 1575 / 1472.
 inline int team_size(int blocks, int clusters, bool ragged) {
   int best = 1;
   double least = 1e30;
@@ -1440,6 +1447,8 @@ inline int team_size(int blocks, int clusters, bool ragged) {
 // us: one row block, 64 sequences of 8192: 182 / 271; two, the same: 334 / 345,
 // 64 of 100 to 8192: 107 / 112, 16 of 3000: 53 / 50; three, 64 of 8192: 494 /
 // 431; up to 17, 13 of 500 to 20000: 152 / 117; 64, one of 32768: 649 / 337.
+// Expanded rows keep their numbers, so they take 128 KB for each block of the
+// pool, used or not; above 32,768 blocks the clusters convert.
 constexpr int kExpandBlocks = 3;
 constexpr size_t kExpandBytes = size_t(4) << 30;  // workspace spent on it at most
 
