@@ -536,14 +536,11 @@ def _need(t, dtype, shape, dev: int, what: str):
                      + f", not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _sizes(what: str, *values):
-    """The values, none of which may lose bits as a C int32 (ctypes would drop them and say nothing)."""
-    bits = 0
-    for v in values:
-        bits |= v
-    if bits >> 31 and not all(-0x80000000 <= v <= 0x7FFFFFFF for v in values):
+def _check_sizes(what: str, *values) -> None:
+    """Refuses values that would lose bits as a C int32 (ctypes drops them and says nothing).  Called
+    where the upper bits of `a | b | ...` say that one may: small calls feel every microsecond."""
+    if not all(-0x80000000 <= v <= 0x7FFFFFFF for v in values):
         raise ValueError(f"{what}: a size beyond 32 bits in {values}")
-    return values
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -581,7 +578,10 @@ def mla_page_plan(ctx_lens, new_lens, free_blocks, block_table, act_seqs, cache_
                 None if cu_seqs is None else _need(cu_seqs, i32, (B + 1,), dev, "cu_seqs"),
                 None if tree_mask is None else _need(tree_mask, torch.int64, (T, (S1 + 63) // 64), dev, "tree_mask"),
                 None if num_taken is None else _need(num_taken, i32, (1,), dev, "num_taken"))
-    dims = PageDims(*_sizes("mla_page_plan", B, S1, T, 128, num_blocks, W, free_blocks.numel()))
+    F = free_blocks.numel()
+    if (B | S1 | T | num_blocks | W | F) >> 31:
+        _check_sizes("mla_page_plan", B, S1, T, num_blocks, W, F)
+    dims = PageDims(B, S1, T, 128, num_blocks, W, F)
     st = lib.mla_page_plan(dims, io, _raw_stream(stream, dev))
     if st != MLA_OK:
         raise MlaError(st, lib.mla_page_last_error().decode())
@@ -616,7 +616,9 @@ def mla_rope_table(positions, cos, sin, *, params: RopeParams, stream=None):
     lib = load_library()
     T, pairs = cos.shape
     dev = torch.cuda.current_device()
-    st = lib.mla_rope_table(params, *_sizes("mla_rope_table", T, 2 * pairs), _need(positions, torch.int32, (T,), dev, "positions"),
+    if (T | pairs) >> 30:
+        _check_sizes("mla_rope_table", T, 2 * pairs)
+    st = lib.mla_rope_table(params, T, 2 * pairs, _need(positions, torch.int32, (T,), dev, "positions"),
                             _need(cos, torch.float32, None, dev, "cos"),
                             _need(sin, torch.float32, (T, pairs), dev, "sin"), _raw_stream(stream, dev))
     if st != MLA_OK:
@@ -637,9 +639,11 @@ def _rope_tensor(x, out, rows, T: int, rot_off: int, dev: int, what: str) -> Rop
         raise ValueError(f"{what}: the output has another number of tokens")
     if x.get_device() != dev or out.get_device() != dev:
         raise ValueError(f"{what} and its output must be on the current device, cuda:{dev}")
+    if (xs[1] | xs[2] | rot_off) >> 31:
+        _check_sizes(what, xs[1], xs[2], rot_off)
     return RopeTensor(x.data_ptr(), out.data_ptr(), xst[0], xst[1], ost[0], ost[1],
                       None if rows is None else _need(rows, torch.int64, (T,), dev, what + "'s rows"),
-                      os_[0], *_sizes(what, xs[1], xs[2], rot_off), 0)
+                      os_[0], xs[1], xs[2], rot_off, 0)
 
 
 def mla_rope_apply(positions, q, k=None, *, params: RopeParams, rot_dim: int, rot_off: int = 0, k_rot_off: int = 0,
@@ -660,7 +664,9 @@ def mla_rope_apply(positions, q, k=None, *, params: RopeParams, rot_dim: int, ro
         raise ValueError("q and k must both be bf16, fp16 or fp32")
     if k_rows is not None and (k is None or k_out is None):
         raise ValueError("k_rows needs k and k_out")
-    dims = RopeDims(*_sizes("mla_rope_apply", T, rot_dim), 1 if half else 0, 1 if inverse else 0, _ROPE_DTYPES[q.dtype])
+    if (T | rot_dim) >> 31:
+        _check_sizes("mla_rope_apply", T, rot_dim)
+    dims = RopeDims(T, rot_dim, 1 if half else 0, 1 if inverse else 0, _ROPE_DTYPES[q.dtype])
     dev = torch.cuda.current_device()
     qt = _rope_tensor(q, out, None, T, rot_off, dev, "q")
     kt = None if k is None else _rope_tensor(k, k_out, k_rows, T, k_rot_off, dev, "k")
@@ -687,8 +693,9 @@ def tree_dims(q_nope, kv_nope, block_table, *, S1: int) -> MlaDims:
     T, n_q, d_nope = q_nope.shape
     if T % S1:
         raise ValueError("q_nope's leading dim must be B*S1")
-    return MlaDims(*_sizes("tree_dims", T // S1, S1, n_q, 1, d_nope, 64, 128, kv_nope.shape[0] // 128,
-                           block_table.shape[1]), 0, MLA_KV_INT8 if kv_nope.dtype == torch.int8 else MLA_KV_BF16)
+    sizes = (T // S1, S1, n_q, 1, d_nope, 64, 128, kv_nope.shape[0] // 128, block_table.shape[1])
+    _check_sizes("tree_dims", *sizes)
+    return MlaDims(*sizes, 0, MLA_KV_INT8 if kv_nope.dtype == torch.int8 else MLA_KV_BF16)
 
 
 def mla_tree_workspace_bytes(dims: MlaDims) -> int:
