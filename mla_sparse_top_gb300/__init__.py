@@ -16,7 +16,9 @@ from .binding import (MLA_DEVICE_BAD_BLOCK, MlaCmpCache, cache_device_status, ml
                       prolog_device_status, prolog_dims, MLA_DEVICE_NO_PAGE, PageDims, PageIo, RopeDims, RopeParams,
                       RopeTensor, mla_page_plan, mla_rope_apply, mla_rope_table, page_device_status,
                       rope_device_status, rope_params, mla_tree_attn_fwd, mla_tree_workspace_bytes, tree_device_status,
-                      tree_dims)
+                      tree_dims, MLA_DEVICE_BAD_LENGTH, AppendDims, HeadNorm, HeadsTensor, KvCache, PagedDims, PromptDims,
+                      head_norm, heads_device_status, mla_kv_append, mla_norm_rope, mla_paged_attn_fwd,
+                      mla_paged_workspace_bytes, mla_prompt_attn_fwd, mla_prompt_workspace_bytes, paged_dims, prompt_dims)
 
 __all__ = ["mla_sparse_attn_fwd", "mla_swa_fwd", "mla_compressed_attn_fwd", "MlaCmpCache", "mla_cache_write", "cache_device_status", "device_status", "abi_version", "set_wait_limit_ns", "DEFAULT_WAIT_LIMIT_NS", "launch_count", "allow_cut_tokens", "load_library", "MlaDims", "MlaError", "dims_from_workload",
            "mla_indexer_topk", "mla_indexer_topk_noalloc", "mla_indexer_scores", "mla_indexer_select", "mla_indexer_workspace_bytes", "indexer_device_status", "indexer_dims_from_workload",
@@ -26,4 +28,7 @@ __all__ = ["mla_sparse_attn_fwd", "mla_swa_fwd", "mla_compressed_attn_fwd", "Mla
            "MLA_DEVICE_TIMEOUT", "MLA_DEVICE_NO_PAGE",
            "mla_page_plan", "page_device_status", "PageDims", "PageIo",
            "mla_rope_table", "mla_rope_apply", "rope_device_status", "rope_params", "RopeParams", "RopeDims",
-           "RopeTensor", "mla_tree_attn_fwd", "mla_tree_workspace_bytes", "tree_device_status", "tree_dims"]
+           "RopeTensor", "mla_tree_attn_fwd", "mla_tree_workspace_bytes", "tree_device_status", "tree_dims",
+           "MLA_DEVICE_BAD_LENGTH", "head_norm", "HeadNorm", "mla_norm_rope", "mla_kv_append", "AppendDims", "HeadsTensor",
+           "KvCache", "mla_prompt_attn_fwd", "mla_prompt_workspace_bytes", "prompt_dims", "PromptDims",
+           "mla_paged_attn_fwd", "mla_paged_workspace_bytes", "paged_dims", "PagedDims", "heads_device_status"]

@@ -1,5 +1,5 @@
 """ctypes binding of the C ABI in include/mla_sparse.h, mla_indexer.h,
-mla_cache.h, mla_prolog.h, mla_pages.h, mla_rope.h and mla_tree.h.
+mla_cache.h, mla_prolog.h, mla_pages.h, mla_rope.h, mla_tree.h and mla_heads.h.
 
 Argument marshalling only: shapes and dtypes are read off torch tensors, the
 device pointers and the current CUDA stream are passed through, and a
@@ -29,6 +29,7 @@ MLA_KV_INT8 = 1
 MLA_DEVICE_BAD_BLOCK = 0x1
 MLA_DEVICE_TIMEOUT = 0x2
 MLA_DEVICE_NO_PAGE = 0x4
+MLA_DEVICE_BAD_LENGTH = 0x8
 
 EXPORTED_SYMBOLS = ("mla_sparse_attn_fwd", "mla_swa_fwd", "mla_compressed_attn_fwd", "mla_sparse_last_error", "mla_sparse_device_status",
                     "mla_sparse_get_device_status", "mla_sparse_set_wait_limit_ns", "mla_sparse_launch_count",
@@ -43,6 +44,11 @@ EXPORTED_SYMBOLS = ("mla_sparse_attn_fwd", "mla_swa_fwd", "mla_compressed_attn_f
 STEP_SYMBOLS = ("mla_page_plan", "mla_page_last_error", "mla_page_device_status", "mla_rope_table", "mla_rope_apply",
                 "mla_rope_last_error", "mla_rope_device_status", "mla_tree_workspace_bytes", "mla_tree_attn_fwd",
                 "mla_tree_last_error", "mla_tree_device_status")
+
+
+# mla_heads.h: norms, paged append and attention of ordinary heads
+HEADS_SYMBOLS = ("mla_norm_rope", "mla_kv_append", "mla_prompt_workspace_bytes", "mla_prompt_attn_fwd",
+                 "mla_paged_workspace_bytes", "mla_paged_attn_fwd", "mla_heads_last_error", "mla_heads_device_status")
 
 
 class MlaDims(ctypes.Structure):
@@ -107,6 +113,41 @@ class RopeTensor(ctypes.Structure):
 class RopeDims(ctypes.Structure):
     """mla_rope_dims."""
     _fields_ = [(name, ctypes.c_int32) for name in ("T", "rot_dim", "half", "inverse", "dtype")]
+
+
+class HeadNorm(ctypes.Structure):
+    """mla_head_norm; made by head_norm(), which keeps the tensors alive."""
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("kind", ctypes.c_int32),
+                ("fp32", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class AppendDims(ctypes.Structure):
+    """mla_append_dims."""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "T", "n_kv", "d_qk", "d_v", "rot_dim", "rot_off", "half", "dtype", "num_blocks")]
+
+
+class HeadsTensor(ctypes.Structure):
+    """mla_heads_tensor and mla_append_input."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KvCache(ctypes.Structure):
+    """mla_kv_cache."""
+    _fields_ = [("data", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class PromptDims(ctypes.Structure):
+    """mla_prompt_dims."""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "B", "T", "Tk", "n_q", "n_kv", "d_qk", "d_v", "dtype", "causal", "num_blocks", "max_blocks_per_seq")]
+
+
+class PagedDims(ctypes.Structure):
+    """mla_paged_dims."""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "B", "S1", "n_q", "n_kv", "d_qk", "d_v", "dtype", "num_blocks", "max_blocks_per_seq")]
 
 
 class MlaError(RuntimeError):
@@ -185,7 +226,18 @@ def load_library(path: str = LIB_PATH):
                                    ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), vp]
     lib.mla_tree_attn_fwd.argtypes = [ctypes.POINTER(MlaDims)] + [vp] * 11 + [ctypes.c_float, vp, ctypes.c_size_t, vp]
     lib.mla_tree_workspace_bytes.argtypes = [ctypes.POINTER(MlaDims)]
-    for name in STEP_SYMBOLS:
+    pt = ctypes.POINTER
+    lib.mla_norm_rope.argtypes = [pt(RopeDims), pt(RopeParams), vp, pt(RopeTensor), pt(HeadNorm), pt(RopeTensor),
+                                  pt(HeadNorm), vp]
+    lib.mla_kv_append.argtypes = [pt(AppendDims), pt(RopeParams), vp, vp, pt(HeadsTensor), pt(HeadNorm), pt(KvCache),
+                                  pt(HeadsTensor), pt(KvCache), pt(RopeTensor), pt(HeadNorm), vp]
+    lib.mla_prompt_workspace_bytes.argtypes = [pt(PromptDims)]
+    lib.mla_prompt_attn_fwd.argtypes = [pt(PromptDims), pt(HeadsTensor), pt(KvCache), pt(KvCache)] + [vp] * 6 + [
+        ctypes.c_float, vp, ctypes.c_size_t, vp]
+    lib.mla_paged_workspace_bytes.argtypes = [pt(PagedDims)]
+    lib.mla_paged_attn_fwd.argtypes = [pt(PagedDims), pt(HeadsTensor), pt(KvCache), pt(KvCache)] + [vp] * 5 + [
+        ctypes.c_float, vp, ctypes.c_size_t, vp]
+    for name in STEP_SYMBOLS + HEADS_SYMBOLS:
         fn = getattr(lib, name)
         if name.endswith("_last_error"):
             fn.argtypes, fn.restype = [], ctypes.c_char_p
@@ -193,7 +245,8 @@ def load_library(path: str = LIB_PATH):
             fn.restype = ctypes.c_int
         if name.endswith("_device_status"):
             fn.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32]
-    lib.mla_tree_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("mla_tree_workspace_bytes", "mla_prompt_workspace_bytes", "mla_paged_workspace_bytes"):
+        getattr(lib, name).restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -754,4 +807,267 @@ def tree_device_status(clear: bool = True, stream=None) -> int:
     st = lib.mla_tree_device_status(_stream_handle(stream), ctypes.byref(flags), 1 if clear else 0)
     if st not in (MLA_OK, -7):
         raise MlaError(st, lib.mla_tree_last_error().decode())
+    return int(flags.value)
+
+
+# ------------------------------------------------------------------ ordinary heads
+def _heads_fail(st: int):
+    raise MlaError(st, load_library().mla_heads_last_error().decode())
+
+
+_NORM_KINDS = {"rms": 1, "layer": 2}
+
+
+def head_norm(kind: str, weight=None, bias=None, eps: float = 1e-6) -> HeadNorm:
+    """The norm of a tensor's heads (mla_head_norm): kind "rms" or "layer",
+    weight and bias (head_dim,) in fp32 or in the heads' type, None for ones and
+    zeros.  Made once and kept; it holds on to its tensors."""
+    given = [t for t in (weight, bias) if t is not None]
+    for t in given:
+        if t.dtype not in _ROPE_DTYPES or t.dim() != 1 or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError("weight and bias must be dense vectors of bf16, fp16 or fp32 on a GPU")
+    if len(given) == 2 and (given[0].dtype != given[1].dtype or given[0].shape != given[1].shape
+                            or given[0].device != given[1].device):
+        raise ValueError("weight and bias must have one type, one size and one device")
+    fp32 = bool(given) and given[0].dtype == torch.float32
+    norm = HeadNorm(None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                    _NORM_KINDS[kind], fp32, eps, 0)
+    norm.tensors = given
+    return norm
+
+
+def _check_norm(norm, x, dev: int, what: str):
+    if norm is not None:
+        for t in norm.tensors:
+            if t.numel() != x.shape[2] or t.get_device() != dev or (t.dtype is not torch.float32 and t.dtype is not x.dtype):
+                raise ValueError(f"{what}'s norm must have {x.shape[2]} weights of fp32 or {x.dtype} on cuda:{dev}")
+    return norm
+
+
+def mla_norm_rope(positions, q, k=None, *, params: RopeParams | None = None, rot_dim: int = 0, rot_off: int = 0,
+                  k_rot_off: int = 0, half: bool = False, q_norm: HeadNorm | None = None,
+                  k_norm: HeadNorm | None = None, out=None, k_out=None, k_rows=None, stream=None):
+    """Enqueue one call of the C entry point with the same name: norm the heads
+    of q (T, H, D) and, where given, k (T, Hk, Dk), then rotate them, in one pass.
+
+    q_norm and k_norm are made by head_norm() (None: none); the other arguments
+    are those of mla_rope_apply.  rot_dim 0 rotates nothing (positions and
+    params may be None)."""
+    lib = load_library()
+    T = q.shape[0]
+    if q.dtype not in _ROPE_DTYPES or (k is not None and k.dtype != q.dtype):
+        raise ValueError("q and k must both be bf16, fp16 or fp32")
+    if k_rows is not None and (k is None or k_out is None):
+        raise ValueError("k_rows needs k and k_out")
+    if (T | rot_dim) >> 31:
+        _check_sizes("mla_norm_rope", T, rot_dim)
+    dims = RopeDims(T, rot_dim, 1 if half else 0, 0, _ROPE_DTYPES[q.dtype])
+    dev = torch.cuda.current_device()
+    qt = _rope_tensor(q, out, None, T, rot_off, dev, "q")
+    kt = None if k is None else _rope_tensor(k, k_out, k_rows, T, k_rot_off, dev, "k")
+    pos = None if positions is None else _need(positions, torch.int32, (T,), dev, "positions")
+    st = lib.mla_norm_rope(dims, params, pos, qt, _check_norm(q_norm, q, dev, "q"), kt,
+                           None if k is None else _check_norm(k_norm, k, dev, "k"), _raw_stream(stream, dev))
+    if st != MLA_OK:
+        _heads_fail(st)
+    _debug_status(heads_device_status, "mla_norm_rope", stream)
+    return (q if out is None else out), (k if k_out is None else k_out)
+
+
+def _heads_tensor(x, dtype, dev: int, what: str) -> HeadsTensor:
+    if x.dim() != 3 or x.dtype is not dtype or x.get_device() != dev:
+        raise ValueError(f"{what} must be a (tokens, heads, values) tensor of {dtype} on cuda:{dev}")
+    st = x.stride()
+    if st[2] != 1 and x.shape[2] > 1:
+        raise ValueError(f"{what}: the values of a head must be adjacent")
+    return HeadsTensor(x.data_ptr(), st[0], st[1])
+
+
+def _kv_cache(x, heads: int, dtype, dev: int, what: str) -> KvCache:
+    sh = x.shape
+    if len(sh) != 4 or sh[1] != 128 or sh[2] != heads or x.dtype is not dtype or x.get_device() != dev:
+        raise ValueError(f"{what} must be a (blocks, 128, {heads}, values) tensor of {dtype} on cuda:{dev}")
+    st = x.stride()
+    if st[3] != 1 and sh[3] > 1:
+        raise ValueError(f"{what}: the values of a head must be adjacent")
+    return KvCache(x.data_ptr(), st[0], st[1], st[2])
+
+
+def mla_kv_append(positions, rows, k, v, k_cache, v_cache, *, params: RopeParams | None = None, rot_dim: int = 0,
+                  rot_off: int = 0, half: bool = False, k_norm: HeadNorm | None = None, q=None, q_out=None,
+                  q_rot_off: int = 0, q_norm: HeadNorm | None = None, stream=None):
+    """Enqueue one call of the C entry point with the same name: the keys k (T,
+    Hkv, D), normed and rotated, and the values v (T, Hkv, Dv) of T tokens into
+    rows (T,) int64 of the caches (blocks, 128, Hkv, D) and (blocks, 128, Hkv,
+    Dv), whose memory may be ordered by token or by head; negative rows are
+    skipped.  q (T, H, Dq): the tokens' queries, normed and rotated in the same
+    launch to q_out (None: in place).  Norms are made by head_norm()."""
+    lib = load_library()
+    T, heads = k.shape[0], k.shape[1]
+    if k.dtype not in _ROPE_DTYPES:
+        raise ValueError("k must be bf16, fp16 or fp32")
+    dev, dtype = torch.cuda.current_device(), k.dtype
+    kt, vt = _heads_tensor(k, dtype, dev, "k"), _heads_tensor(v, dtype, dev, "v")
+    kc, vc = _kv_cache(k_cache, heads, dtype, dev, "k_cache"), _kv_cache(v_cache, heads, dtype, dev, "v_cache")
+    if v.shape[:2] != k.shape[:2] or k_cache.shape[3] != k.shape[2] or v_cache.shape[3] != v.shape[2] \
+            or k_cache.shape[0] != v_cache.shape[0]:
+        raise ValueError("k, v and the caches must agree in tokens, heads, values and blocks")
+    sizes = (T, heads, k.shape[2], v.shape[2], rot_dim, rot_off, k_cache.shape[0])
+    if (T | heads | sizes[2] | sizes[3] | rot_dim | rot_off | sizes[6] | q_rot_off) >> 31:
+        _check_sizes("mla_kv_append", *sizes, q_rot_off)
+    dims = AppendDims(T, heads, sizes[2], sizes[3], rot_dim, rot_off, 1 if half else 0, _ROPE_DTYPES[dtype], sizes[6])
+    qt = None
+    if q is not None:
+        if q.dtype is not dtype:
+            raise ValueError("q and k must have one type")
+        qt = _rope_tensor(q, q_out, None, T, q_rot_off, dev, "q")
+    pos = None if positions is None else _need(positions, torch.int32, (T,), dev, "positions")
+    st = lib.mla_kv_append(dims, params, pos, _need(rows, torch.int64, (T,), dev, "rows"), kt,
+                           _check_norm(k_norm, k, dev, "k"), kc, vt, vc, qt,
+                           None if q is None else _check_norm(q_norm, q, dev, "q"), _raw_stream(stream, dev))
+    if st != MLA_OK:
+        _heads_fail(st)
+    _debug_status(heads_device_status, "mla_kv_append", stream)
+    return k_cache, v_cache, (q if q_out is None else q_out)
+
+
+_ATTN_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _attn_dtype(q) -> int:
+    if q.dtype not in _ATTN_DTYPES:
+        raise ValueError("q, k and v must be bf16 or fp16")
+    return _ATTN_DTYPES[q.dtype]
+
+
+def prompt_dims(q, k, v, cu_q, *, block_table=None, causal: bool = True) -> PromptDims:
+    """PromptDims read off the tensors of mla_prompt_attn_fwd: q (T, n_q, D),
+    cu_q (B + 1,), and k, v (Tk, n_kv, .) packed, or (blocks, 128, n_kv, .) with a
+    block_table (B, W)."""
+    paged = block_table is not None
+    sizes = (cu_q.numel() - 1, q.shape[0], 0 if paged else k.shape[0], q.shape[1], k.shape[-2], q.shape[2], v.shape[-1],
+             _attn_dtype(q), 1 if causal else 0, k.shape[0] if paged else 0, block_table.shape[1] if paged else 0)
+    _check_sizes("prompt_dims", *sizes)
+    return PromptDims(*sizes)
+
+
+def mla_prompt_workspace_bytes(dims: PromptDims) -> int:
+    return int(load_library().mla_prompt_workspace_bytes(dims))
+
+
+def _need_output(out, lse, q, d_v: int, dev: int):
+    T, H = q.shape[0], q.shape[1]
+    return (_need(out, q.dtype, (T, H, d_v), dev, "out"),
+            None if lse is None else _need(lse, torch.float32, (T, H), dev, "lse"))
+
+
+def _need_cache(x, d: int, dims, dtype, dev: int, what: str) -> KvCache:
+    t = _kv_cache(x, dims.n_kv, dtype, dev, what)
+    if x.shape[0] < dims.num_blocks or x.shape[3] != d:
+        raise ValueError(f"{what} must hold dims.num_blocks pages of {d} values to a head")
+    return t
+
+
+def _need_workspace(workspace, dev: int):
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a dense tensor on cuda:{dev}")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def mla_prompt_attn_fwd(q, k, v, cu_q, out, lse, workspace, *, cu_k=None, block_table=None, act_seqs=None,
+                        causal: bool = True, softmax_scale=None, stream=None, dims: PromptDims | None = None):
+    """Enqueue one call of the C entry point with the same name: attention of
+    whole prompts, or of chunks of them over a paged context.
+
+    q (T, n_q, D) bf16|fp16, sequence b's queries in rows [cu_q[b], cu_q[b + 1])
+    (int32); k (Tk, n_kv, D) and v (Tk, n_kv, Dv) packed the same way by cu_k
+    (None: cu_q), or paged, (blocks, 128, n_kv, .) with block_table (B, W) and
+    act_seqs (B,) int32 keys; out (T, n_q, Dv), lse (T, n_q) fp32 or None,
+    workspace: at least mla_prompt_workspace_bytes(dims) bytes.  q, k and v may
+    be views with any strides of 8 values.  `causal` is dims' where dims is
+    given; softmax_scale None: D^-0.5."""
+    lib = load_library()
+    if dims is None:
+        dims = prompt_dims(q, k, v, cu_q, block_table=block_table, causal=causal)
+    dev, i32, dtype, B, D, Dv = torch.cuda.current_device(), torch.int32, q.dtype, dims.B, dims.d_qk, dims.d_v
+    if _attn_dtype(q) != dims.dtype or q.shape != (dims.T, dims.n_q, D):
+        raise ValueError("q must be (T, n_q, d_qk) of dims and of its type")
+    qt = _heads_tensor(q, dtype, dev, "q")
+    if dims.num_blocks > 0:
+        kt, vt = _need_cache(k, D, dims, dtype, dev, "k"), _need_cache(v, Dv, dims, dtype, dev, "v")
+    else:
+        if k.shape != (dims.Tk, dims.n_kv, D) or v.shape != (dims.Tk, dims.n_kv, Dv):
+            raise ValueError("packed k and v must be (Tk, n_kv, d_qk) and (Tk, n_kv, d_v) of dims")
+        kh, vh = _heads_tensor(k, dtype, dev, "k"), _heads_tensor(v, dtype, dev, "v")
+        kt, vt = KvCache(kh.data, 0, kh.token_stride, kh.head_stride), KvCache(vh.data, 0, vh.token_stride, vh.head_stride)
+        if cu_k is None and dims.Tk < dims.T:
+            raise ValueError("without cu_k, k and v must have q's rows")
+    ptrs = (_need(cu_q, i32, (B + 1,), dev, "cu_q"), None if cu_k is None else _need(cu_k, i32, (B + 1,), dev, "cu_k"),
+            None if block_table is None else _need(block_table, i32, (B, dims.max_blocks_per_seq), dev, "block_table"),
+            None if act_seqs is None else _need(act_seqs, i32, (B,), dev, "act_seqs"))
+    o, l = _need_output(out, lse, q, Dv, dev)
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    st = lib.mla_prompt_attn_fwd(dims, qt, kt, vt, *ptrs, o, l, softmax_scale, *_need_workspace(workspace, dev),
+                                 _raw_stream(stream, dev))
+    if st != MLA_OK:
+        _heads_fail(st)
+    _debug_status(heads_device_status, "mla_prompt_attn_fwd", stream)
+    return out, lse
+
+
+def paged_dims(q, k_cache, v_cache, block_table, *, S1: int = 1) -> PagedDims:
+    """PagedDims read off the tensors of mla_paged_attn_fwd."""
+    T = q.shape[0]
+    if S1 < 1 or T % S1:
+        raise ValueError("q's leading dim must be B*S1")
+    sizes = (T // S1, S1, q.shape[1], k_cache.shape[-2], q.shape[2], v_cache.shape[-1], _attn_dtype(q),
+             k_cache.shape[0], block_table.shape[1])
+    _check_sizes("paged_dims", *sizes)
+    return PagedDims(*sizes)
+
+
+def mla_paged_workspace_bytes(dims: PagedDims) -> int:
+    return int(load_library().mla_paged_workspace_bytes(dims))
+
+
+def mla_paged_attn_fwd(q, k_cache, v_cache, block_table, act_seqs, out, lse, workspace, *, q_lens=None,
+                       softmax_scale=None, S1: int = 1, stream=None, dims: PagedDims | None = None):
+    """Enqueue one call of the C entry point with the same name: attention of
+    each sequence's newest tokens, one or a chain of S1, over its pages.
+
+    q (B*S1, n_q, D) bf16|fp16, k_cache (blocks, 128, n_kv, D), v_cache (blocks,
+    128, n_kv, Dv), block_table (B, W) and act_seqs (B,) int32 (the new tokens
+    counted), out (B*S1, n_q, Dv), lse (B*S1, n_q) fp32 or None, workspace: at
+    least mla_paged_workspace_bytes(dims) bytes; q_lens (B,) int32 new tokens of
+    each sequence (None: S1).  softmax_scale None: D^-0.5."""
+    lib = load_library()
+    if dims is None:
+        dims = paged_dims(q, k_cache, v_cache, block_table, S1=S1)
+    dev, i32, dtype, B = torch.cuda.current_device(), torch.int32, q.dtype, dims.B
+    if _attn_dtype(q) != dims.dtype or q.shape != (B * dims.S1, dims.n_q, dims.d_qk):
+        raise ValueError("q must be (B*S1, n_q, d_qk) of dims and of its type")
+    qt = _heads_tensor(q, dtype, dev, "q")
+    kt, vt = _need_cache(k_cache, dims.d_qk, dims, dtype, dev, "k_cache"), _need_cache(v_cache, dims.d_v, dims, dtype, dev, "v_cache")
+    ptrs = (_need(block_table, i32, (B, dims.max_blocks_per_seq), dev, "block_table"),
+            _need(act_seqs, i32, (B,), dev, "act_seqs"), None if q_lens is None else _need(q_lens, i32, (B,), dev, "q_lens"))
+    o, l = _need_output(out, lse, q, dims.d_v, dev)
+    if softmax_scale is None:
+        softmax_scale = dims.d_qk ** -0.5
+    st = lib.mla_paged_attn_fwd(dims, qt, kt, vt, *ptrs, o, l, softmax_scale, *_need_workspace(workspace, dev),
+                                _raw_stream(stream, dev))
+    if st != MLA_OK:
+        _heads_fail(st)
+    _debug_status(heads_device_status, "mla_paged_attn_fwd", stream)
+    return out, lse
+
+
+def heads_device_status(clear: bool = True, stream=None) -> int:
+    lib = load_library()
+    flags = ctypes.c_uint32(0)
+    st = lib.mla_heads_device_status(_stream_handle(stream), ctypes.byref(flags), 1 if clear else 0)
+    if st not in (MLA_OK, -7):
+        _heads_fail(st)
     return int(flags.value)

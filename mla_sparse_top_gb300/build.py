@@ -10,8 +10,11 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "mla_sparse_fwd.cu"), os.path.join(CSRC, "lightning_indexer.cu"),
            os.path.join(CSRC, "cache_write.cu"), os.path.join(CSRC, "mla_prolog.cu"),
            os.path.join(CSRC, "page_plan.cu"), os.path.join(CSRC, "rope.cu"),
-           os.path.join(CSRC, "tree_attn.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(ROOT, "include", "mla_sparse.h"),
+           os.path.join(CSRC, "tree_attn.cu"), os.path.join(CSRC, "head_prep.cu"),
+           os.path.join(CSRC, "prompt_attn.cu"), os.path.join(CSRC, "paged_attn.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "rope_angles.cuh"), os.path.join(CSRC, "areas.h"),
+                  os.path.join(CSRC, "heads.h"), os.path.join(ROOT, "include", "mla_heads.h"),
+                  os.path.join(ROOT, "include", "mla_sparse.h"),
                   os.path.join(ROOT, "include", "mla_indexer.h"), os.path.join(ROOT, "include", "mla_cache.h"),
                   os.path.join(ROOT, "include", "mla_prolog.h"), os.path.join(ROOT, "include", "mla_pages.h"),
                   os.path.join(ROOT, "include", "mla_rope.h"), os.path.join(ROOT, "include", "mla_tree.h")]

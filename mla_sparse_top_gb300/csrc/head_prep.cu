@@ -1,0 +1,586 @@
+// Norms and rotation of heads, and the write of keys and values into a paged
+// cache, for GB300 (sm_103a); formulas in mla_heads.h.
+//
+// A head is one group of 1 to 32 lanes: its units (16 bytes, two of them where
+// the half layout pairs them, or single values where alignment forbids that)
+// are spread over the group, the norm's sums go round it by shuffles, and the
+// rotation needs no lane but its own.  A group keeps its token and walks over
+// heads, so angles and weights are made once.  Everything is read once and
+// written once: bound by memory.
+#include <cuda_runtime.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "heads.h"
+#include "rope_angles.cuh"
+
+namespace mlaheads {
+
+using mlarp::Freqs;
+using mlarp::Pack;
+
+constexpr int kThreads = 256;
+constexpr int kMaxPasses = 16;  // heads of a group
+
+__device__ unsigned int g_prep_status = 0;
+
+struct Tensor {
+  const void* x;
+  void* out;
+  int64_t xt, xh;        // strides in elements
+  int64_t ob, orow, oh;  // of a block of 128 rows, a row, a head
+  const int64_t* rows;
+  int64_t num_rows;
+  const void* weight;
+  const void* bias;
+  float eps, inv_d;
+  int kind, weight_fp32;
+  int n_heads, rot_off, head_dim;
+  int pairs, half;     // of the rotation; 0 pairs: none
+  int rot_units;       // units of a head that hold rotated values
+  int units;           // all units of a head
+  int lanes;           // of a group, a power of two
+  int chunks;          // times that the group's lanes go over a head
+  int tok_rows;        // tokens of a block
+  int head_rows;       // heads that a block takes at a time
+  int passes;          // times that it does
+  int head_blocks;     // blocks over the heads
+  int blocks;
+};
+
+struct Params {
+  Freqs f;
+  const int32_t* positions;
+  Tensor t[3];
+  int T;
+};
+
+template <typename E>
+__device__ __forceinline__ float value(const void* p, int at, int fp32) {
+  if (fp32) return __ldg(static_cast<const float*>(p) + at);
+  if constexpr (sizeof(E) == 4) return __ldg(static_cast<const float*>(p) + at);
+  else return static_cast<float>(static_cast<const E*>(p)[at]);
+}
+
+template <typename E, int V>
+__device__ __forceinline__ void unpack(const Pack<E, V>& a, float* x) {
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __uint_as_float(a.w[i]);
+  } else if constexpr (V == 1) {
+    x[0] = mlarp::unpack2<E>(a.w[0]).x;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 v = mlarp::unpack2<E>(a.w[i]);
+      x[2 * i] = v.x;
+      x[2 * i + 1] = v.y;
+    }
+  }
+}
+template <typename E, int V>
+__device__ __forceinline__ void pack(Pack<E, V>& a, const float* x) {
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.w[i] = __float_as_uint(x[i]);
+  } else if constexpr (V == 1) {
+    a.w[0] = mlarp::pack2<E>(x[0], 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) a.w[i] = mlarp::pack2<E>(x[2 * i], x[2 * i + 1]);
+  }
+}
+
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// A lane's units of a head.  kTwo: a rotated unit is two packs, V values and the
+// V that turn with them; otherwise one pack of V / 2 adjacent pairs.
+template <typename E, int V, bool kTwo, int KU>
+struct Lane {
+  static constexpr int kVals = kTwo ? 2 * V : V;
+  static constexpr int kPairs = kTwo ? V : V / 2;
+  int d[KU];       // first value
+  int second[KU];  // distance of the other pack, 0: there is none
+  bool in[KU], rot[KU];
+  __device__ __forceinline__ void place(const Tensor& w, int first_unit, int lane) {
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      const int k = first_unit + lane + i * w.lanes;
+      in[i] = k < w.units;
+      rot[i] = k < w.rot_units;
+      if (rot[i]) {
+        d[i] = w.rot_off + (kTwo && w.half ? k * V : 2 * kPairs * k);
+        second[i] = kTwo ? (w.half ? w.pairs : 1) : 0;
+      } else {
+        const int c = (k - w.rot_units) * V;  // copied values, in order
+        d[i] = c < w.rot_off ? c : c + 2 * w.pairs;
+        second[i] = 0;
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const E* x, bool live, Pack<E, V> (&a)[KU], Pack<E, V> (&b)[KU]) const {
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+#pragma unroll
+      for (int k = 0; k < Pack<E, V>::W; ++k) a[i].w[k] = b[i].w[k] = 0;
+      if (live && in[i]) {
+        a[i].load(x + d[i]);
+        if (kTwo && rot[i]) b[i].load(x + d[i] + second[i]);
+      }
+    }
+  }
+};
+
+template <typename E, int V, bool kTwo, int KU>
+__device__ __forceinline__ void work(const Params& p, const Tensor& w, int block) {
+  using L = Lane<E, V, kTwo, KU>;
+  const int tid = threadIdx.x;
+  const int r = tid / w.lanes, lane = tid & (w.lanes - 1);
+  const int dt = r / w.head_rows;
+  const int64_t t = static_cast<int64_t>(block / w.head_blocks) * w.tok_rows + dt;
+  const int h0 = block % w.head_blocks * w.passes * w.head_rows + (r - dt * w.head_rows);
+  bool live = dt < w.tok_rows && t < p.T && h0 < w.n_heads;  // every lane stays for the shuffles
+  int64_t to = t;
+  if (live && w.rows != nullptr) {
+    to = __ldg(w.rows + t);
+    if (to >= w.num_rows && lane == 0 && h0 == 0) atomicOr(&g_prep_status, MLA_DEVICE_BAD_BLOCK);
+    live = to >= 0 && to < w.num_rows;
+  }
+  if (!live) to = 0;
+  const E* x = static_cast<const E*>(w.x) + (live ? t * w.xt + h0 * w.xh : 0);
+  E* out = static_cast<E*>(w.out) + (live ? (to >> 7) * w.ob + (to & 127) * w.orow + h0 * w.oh : 0);
+  const int32_t pos = live && w.rot_units > 0 ? __ldg(p.positions + t) : 0;
+  L at;
+  float cs[KU][2 * L::kPairs], wt[KU][L::kVals], bi[KU][L::kVals];
+  auto angles_and_weights = [&]() {
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+#pragma unroll
+      for (int j = 0; j < L::kPairs; ++j) {
+        float2 v = make_float2(1.f, 0.f);
+        if (at.rot[i]) v = mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale);
+        cs[i][2 * j] = v.x;
+        cs[i][2 * j + 1] = v.y;
+      }
+#pragma unroll
+      for (int j = 0; j < L::kVals; ++j) {
+        const int d = at.d[i] + (j < V ? j : at.second[i] + j - V);
+        const bool has = at.in[i] && (j < V || at.rot[i]) && w.kind != MLA_NORM_NONE;
+        wt[i][j] = has && w.weight != nullptr ? value<E>(w.weight, d, w.weight_fp32) : 1.f;
+        bi[i][j] = has && w.bias != nullptr ? value<E>(w.bias, d, w.weight_fp32) : 0.f;
+      }
+    }
+  };
+  at.place(w, 0, lane);
+  if (w.chunks == 1) angles_and_weights();
+  // a chunk's part of sum (x - mean)^power
+  auto part = [&](const Pack<E, V>(&a)[KU], const Pack<E, V>(&b)[KU], float mean, bool square) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      float v[L::kVals];
+      unpack<E, V>(a[i], v);
+      if constexpr (kTwo) unpack<E, V>(b[i], v + V);
+#pragma unroll
+      for (int j = 0; j < L::kVals; ++j) {
+        const bool has = at.in[i] && (j < V || at.rot[i]);
+        const float c = has ? v[j] - mean : 0.f;
+        s += square ? c * c : c;
+      }
+    }
+    return s;
+  };
+  // norm, rotation and store of a chunk
+  auto finish = [&](Pack<E, V>(&a)[KU], Pack<E, V>(&b)[KU], float mean, float inv, E* o, bool put) {
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      float v[L::kVals];
+      unpack<E, V>(a[i], v);
+      if constexpr (kTwo) unpack<E, V>(b[i], v + V);
+      if (w.kind != MLA_NORM_NONE) {
+#pragma unroll
+        for (int j = 0; j < L::kVals; ++j) v[j] = fmaf((v[j] - mean) * inv, wt[i][j], bi[i][j]);
+      }
+      if (at.rot[i]) {
+#pragma unroll
+        for (int j = 0; j < L::kPairs; ++j) {
+          float& u = v[kTwo ? j : 2 * j];
+          float& y = v[kTwo ? V + j : 2 * j + 1];
+          const float2 z = mlarp::turn2(u, y, make_float2(cs[i][2 * j], cs[i][2 * j + 1]));
+          u = z.x;
+          y = z.y;
+        }
+      }
+      if (w.kind != MLA_NORM_NONE || at.rot[i]) {
+        pack<E, V>(a[i], v);
+        if constexpr (kTwo) pack<E, V>(b[i], v + V);
+      }
+      if (put && at.in[i]) {
+        a[i].store(o + at.d[i]);
+        if (kTwo && at.rot[i]) b[i].store(o + at.d[i] + at.second[i]);
+      }
+    }
+  };
+  const int64_t x_step = w.head_rows * w.xh, o_step = w.head_rows * w.oh;
+  constexpr int kUnroll = KU * V >= 8 ? 2 : 1;  // heads in flight
+  for (int it = 0; it < w.passes; it += kUnroll) {
+    Pack<E, V> a[kUnroll][KU], b[kUnroll][KU];
+    bool has[kUnroll];
+    float mean[kUnroll], inv[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      has[u] = live && it + u < w.passes && h0 + (it + u) * w.head_rows < w.n_heads;
+      mean[u] = 0.f;
+      inv[u] = 1.f;
+      if (w.chunks == 1) at.load(x + u * x_step, has[u], a[u], b[u]);
+    }
+    for (int step = w.kind == MLA_NORM_LAYER ? 0 : 1; step < 2 && w.kind != MLA_NORM_NONE; ++step) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float s = 0.f;
+        if (w.chunks == 1) {
+          s = part(a[u], b[u], mean[u], step == 1);
+        } else {
+          for (int c = 0; c < w.chunks; ++c) {
+            at.place(w, c * KU * w.lanes, lane);
+            at.load(x + u * x_step, has[u], a[u], b[u]);
+            s += part(a[u], b[u], mean[u], step == 1);
+          }
+        }
+        s = group_sum(s, w.lanes) * w.inv_d;
+        if (step == 0) mean[u] = s;
+        else inv[u] = 1.f / sqrtf(s + w.eps);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (w.chunks == 1) {
+        finish(a[u], b[u], mean[u], inv[u], out + u * o_step, has[u]);
+      } else {
+        for (int c = 0; c < w.chunks; ++c) {  // in place, a lane has read and written its own values alone
+          at.place(w, c * KU * w.lanes, lane);
+          angles_and_weights();
+          at.load(x + u * x_step, has[u], a[u], b[u]);
+          finish(a[u], b[u], mean[u], inv[u], out + u * o_step, has[u]);
+        }
+      }
+    }
+    x += kUnroll * x_step;
+    out += kUnroll * o_step;
+  }
+}
+
+// One block works on one of the tensors.
+template <typename E, int V, int KU>
+__global__ void __launch_bounds__(kThreads) head_prep_kernel(const __grid_constant__ Params p) {
+  int block = static_cast<int>(blockIdx.x), i = 0;
+  while (i < 2 && block >= p.t[i].blocks) block -= p.t[i++].blocks;
+  const Tensor& w = p.t[i];
+  if constexpr (V > 1) {
+    if (!w.half) return work<E, V, false, KU>(p, w, block);
+  }
+  work<E, V, true, KU>(p, w, block);
+}
+
+thread_local char g_error[256] = "";
+
+mla_status fail(mla_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_error, sizeof g_error, fmt, ap);
+  va_end(ap);
+  return s;
+}
+void no_error() { g_error[0] = '\0'; }
+
+cudaError_t prep_status(unsigned int* v, bool clear) { return read_status(g_prep_status, v, clear); }
+
+namespace {
+
+// One tensor of a call as the host sees it.
+struct Job {
+  const char* name;
+  const void* x;
+  int64_t xt, xh;
+  void* out;
+  int64_t ob, orow, oh;  // block, row and head strides of out
+  const int64_t* rows;
+  int64_t num_rows;  // rows of out
+  int n_heads, head_dim, rot_off, rot_dim;
+  mla_head_norm norm;
+  bool vec;
+  Area in, to;
+};
+
+constexpr int64_t kMost = int64_t(1) << 40;
+
+// Strides and layout; *job.vec is set where 16-byte accesses fit.
+mla_status check_job(Job& j, int T, int dtype, bool half, bool paged) {
+  if (!j.x || !j.out) return fail(MLA_ERR_NULL, "%s: a required pointer is NULL", j.name);
+  if (j.n_heads < 1 || j.head_dim < 1 || j.rot_off < 0 || static_cast<int64_t>(j.rot_off) + j.rot_dim > j.head_dim)
+    return fail(MLA_ERR_SHAPE, "%s: n_heads=%d must be >= 1 and the head's %d values hold [rot_off, rot_off + rot_dim)",
+                j.name, j.n_heads, j.head_dim);
+  if (j.head_dim > (1 << 20) || static_cast<int64_t>(j.n_heads) * j.head_dim > (1 << 28))
+    return fail(MLA_ERR_SHAPE, "%s: heads of more than 2^20 values, or tokens of more than 2^28", j.name);
+  for (int64_t s : {j.xt, j.xh, j.ob, j.orow, j.oh})
+    if (s < 0 || s > kMost) return fail(MLA_ERR_SHAPE, "%s: strides must be in [0, 2^40]", j.name);
+  if (j.num_rows < 1 || j.num_rows > kMost) return fail(MLA_ERR_SHAPE, "%s: rows must be in [1, 2^40]", j.name);
+  const mla_head_norm& n = j.norm;
+  if (n.kind < MLA_NORM_NONE || n.kind > MLA_NORM_LAYER || n.fp32 < 0 || n.fp32 > 1)
+    return fail(MLA_ERR_SHAPE, "%s: norm kind %d unknown, or its fp32 neither 0 nor 1", j.name, n.kind);
+  if (n.kind != MLA_NORM_NONE && (!(n.eps >= 0.f) || !(n.eps < 3.4e38f)))
+    return fail(MLA_ERR_SHAPE, "%s: eps must be finite and >= 0", j.name);
+  if (n.kind == MLA_NORM_RMS && n.bias) return fail(MLA_ERR_UNSUPPORTED, "%s: the RMS norm has no bias", j.name);
+  const int size = dtype == MLA_ROPE_FP32 ? 4 : 2, V = 16 / size;
+  const uintptr_t wsize = n.fp32 ? 4 : static_cast<uintptr_t>(size);
+  if (!aligned(j.x, size) || !aligned(j.out, size) || (j.rows && !aligned(j.rows, 8)) ||
+      (n.kind != MLA_NORM_NONE && (!aligned(n.weight, wsize) || !aligned(n.bias, wsize))))
+    return fail(MLA_ERR_ALIGN, "%s: tensors must be aligned to their elements", j.name);
+  const bool same = j.x == j.out;
+  if (same && j.rows) return fail(MLA_ERR_UNSUPPORTED, "%s: rows of out cannot be x itself", j.name);
+  if (same && ((j.n_heads > 1 && j.xh != j.oh) || (T > 1 && j.xt != j.orow)))
+    return fail(MLA_ERR_SHAPE, "%s: in place, x and out need the same strides", j.name);
+  const int64_t bytes = static_cast<int64_t>(j.head_dim) * size;
+  j.in = {reinterpret_cast<uintptr_t>(j.x), {1, T, j.n_heads}, {0, j.xt * size, j.xh * size}, bytes};
+  if (paged)
+    j.to = {reinterpret_cast<uintptr_t>(j.out), {j.num_rows / 128, 128, j.n_heads}, {j.ob * size, j.orow * size, j.oh * size}, bytes};
+  else
+    j.to = {reinterpret_cast<uintptr_t>(j.out), {1, j.rows ? j.num_rows : T, j.n_heads}, {0, j.orow * size, j.oh * size}, bytes};
+  if (!mlasp::distinct(j.to)) return fail(MLA_ERR_SHAPE, "%s: the output's strides make heads overlap", j.name);
+  const bool heads = j.n_heads > 1, tokens = T > 1;  // strides that are taken
+  const int64_t parts[] = {tokens ? j.xt : 0, heads ? j.xh : 0, tokens || j.rows ? j.orow : 0, j.rows ? j.ob : 0,
+                           heads ? j.oh : 0, j.head_dim, j.rot_off, half ? j.rot_dim / 2 : j.rot_dim};
+  j.vec = aligned(j.x, 16) && aligned(j.out, 16);
+  for (int64_t v : parts) j.vec = j.vec && v % V == 0;
+  return MLA_OK;
+}
+
+// Refuses outputs that overlap what the call reads, or one another: blocks read and write in no order.
+mla_status check_overlaps(const Job* jobs, int n, int T, const int32_t* positions, const int64_t* rows, int dtype) {
+  const int size = dtype == MLA_ROPE_FP32 ? 4 : 2;
+  for (int i = 0; i < n; ++i) {
+    bool hit = overlap(jobs[i].to, mlasp::run(positions, 4ll * T)) || overlap(jobs[i].to, mlasp::run(rows, 8ll * T));
+    for (int k = 0; k < n; ++k) {
+      const mla_head_norm& norm = jobs[k].norm;
+      hit = hit || ((i != k || jobs[i].x != jobs[i].out) && overlap(jobs[i].to, jobs[k].in));
+      hit = hit || (i < k && overlap(jobs[i].to, jobs[k].to));
+      if (norm.kind != MLA_NORM_NONE) {
+        const int64_t bytes = static_cast<int64_t>(jobs[k].head_dim) * (norm.fp32 ? 4 : size);
+        hit = hit || overlap(jobs[i].to, mlasp::run(norm.weight, bytes)) || overlap(jobs[i].to, mlasp::run(norm.bias, bytes));
+      }
+    }
+    if (hit) return fail(MLA_ERR_UNSUPPORTED, "%s's output overlaps an input or another output", jobs[i].name);
+  }
+  return MLA_OK;
+}
+
+constexpr int kUnits = 2;         // units of a lane, 16-byte accesses
+constexpr int kSingleUnits = 4;   // single values
+
+// Splits a checked tensor's heads into groups and blocks.
+mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
+  w->x = j.x;
+  w->out = j.out;
+  w->xt = j.xt;
+  w->xh = j.xh;
+  w->ob = j.ob;
+  w->orow = j.orow;
+  w->oh = j.oh;
+  w->rows = j.rows;
+  w->num_rows = j.num_rows;
+  w->weight = j.norm.weight;
+  w->bias = j.norm.bias;
+  w->eps = j.norm.eps;
+  w->inv_d = 1.f / static_cast<float>(j.head_dim);
+  w->kind = j.norm.kind;
+  w->weight_fp32 = j.norm.fp32;
+  w->n_heads = j.n_heads;
+  w->rot_off = j.rot_off;
+  w->head_dim = j.head_dim;
+  w->pairs = j.rot_dim / 2;
+  w->half = half ? 1 : 0;
+  const int width = !j.vec ? 1 : (dtype == MLA_ROPE_FP32 ? 4 : 8);
+  w->rot_units = j.vec && !half ? j.rot_dim / width : j.rot_dim / 2 / width;
+  w->units = w->rot_units + (j.head_dim - j.rot_dim) / width;
+  const int per_lane = j.vec ? kUnits : kSingleUnits;
+  w->lanes = 1;
+  while (w->lanes < 32 && w->lanes < w->units) w->lanes *= 2;
+  w->chunks = (w->units + w->lanes * per_lane - 1) / (w->lanes * per_lane);
+  const int rows = kThreads / w->lanes;
+  w->tok_rows = std::min(rows, T);
+  w->head_rows = std::min(rows / w->tok_rows, j.n_heads);
+  // several heads per group once there is a block for every SM four times over
+  const int64_t toks = (static_cast<int64_t>(T) + w->tok_rows - 1) / w->tok_rows;
+  const int turns = (j.n_heads + w->head_rows - 1) / w->head_rows;
+  const int most = std::min(turns, kMaxPasses);
+  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, toks * turns / (4 * 152))));
+  w->head_blocks = (turns + w->passes - 1) / w->passes;
+  w->passes = (turns + w->head_blocks - 1) / w->head_blocks;  // even shares
+  const int64_t blocks = toks * w->head_blocks;
+  if (blocks >= (1ll << 29)) return fail(MLA_ERR_SHAPE, "%s: T x heads too large", j.name);
+  w->blocks = static_cast<int>(blocks);
+  return MLA_OK;
+}
+
+typedef void (*Kernel)(Params);
+
+mla_status launch(const Job* jobs, int n, int T, int dtype, bool half, Params& p, cudaStream_t s) {
+  static const Kernel kernels[3][2] = {
+      {head_prep_kernel<__nv_bfloat16, 1, kSingleUnits>, head_prep_kernel<__nv_bfloat16, 8, kUnits>},
+      {head_prep_kernel<__half, 1, kSingleUnits>, head_prep_kernel<__half, 8, kUnits>},
+      {head_prep_kernel<float, 1, kSingleUnits>, head_prep_kernel<float, 4, kUnits>}};
+  p.T = T;
+  for (int vec = 1; vec >= 0; --vec) {
+    int taken = 0;
+    int64_t grid = 0;
+    for (int i = 0; i < 3; ++i) p.t[i].blocks = 0;
+    for (int i = 0; i < n; ++i) {
+      if (jobs[i].vec != (vec != 0)) continue;
+      const mla_status st = split_job(jobs[i], T, dtype, half, &p.t[taken]);
+      if (st != MLA_OK) return st;
+      grid += p.t[taken++].blocks;
+    }
+    if (taken == 0) continue;
+    kernels[dtype][vec]<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
+    HEADS_CUDA(cudaGetLastError(), "launch");
+  }
+  return MLA_OK;
+}
+
+mla_head_norm norm_of(const mla_head_norm* n) {
+  mla_head_norm none = {nullptr, nullptr, MLA_NORM_NONE, 0, 0.f, 0};
+  return n != nullptr ? *n : none;
+}
+
+Job rope_job(const char* name, const mla_rope_tensor& q, const mla_head_norm* norm, int T, int rot_dim) {
+  Job j;
+  j.name = name;
+  j.x = q.x;
+  j.xt = q.x_token_stride;
+  j.xh = q.x_head_stride;
+  j.out = q.out;
+  j.orow = q.out_token_stride;
+  j.ob = q.out_token_stride <= kMost / 128 ? 128 * q.out_token_stride : kMost + 1;
+  j.oh = q.out_head_stride;
+  j.rows = q.rows;
+  j.num_rows = q.rows ? q.num_rows : T;
+  j.n_heads = q.n_heads;
+  j.head_dim = q.head_dim;
+  j.rot_off = q.rot_off;
+  j.rot_dim = rot_dim;
+  j.norm = norm_of(norm);
+  j.vec = false;
+  return j;
+}
+
+// The scheme of a call that may rotate nothing.
+mla_status make_scheme(const mla_rope_params* params, const int32_t* positions, int rot_dim, Freqs* f) {
+  if (rot_dim == 0) return MLA_OK;
+  const mla_status st = mlarp::make_freqs(params, rot_dim, f, fail);
+  if (st != MLA_OK) return st;
+  return MLA_OK;
+}
+
+}  // namespace
+}  // namespace mlaheads
+
+extern "C" {
+
+mla_status mla_norm_rope(const mla_rope_dims* dims, const mla_rope_params* params, const int32_t* positions,
+                         const mla_rope_tensor* q, const mla_head_norm* q_norm, const mla_rope_tensor* k,
+                         const mla_head_norm* k_norm, void* stream) {
+  using namespace mlaheads;
+  no_error();
+  if (dims == nullptr || q == nullptr) return fail(MLA_ERR_NULL, "dims or q is NULL");
+  const mla_rope_dims d = *dims;
+  if (d.dtype < MLA_ROPE_BF16 || d.dtype > MLA_ROPE_FP32) return fail(MLA_ERR_DTYPE, "dtype %d unknown", d.dtype);
+  if (d.T < 0 || d.half < 0 || d.half > 1) return fail(MLA_ERR_SHAPE, "T must be >= 0, half 0 or 1");
+  if (d.inverse != 0) return fail(MLA_ERR_UNSUPPORTED, "inverse must be 0");
+  Params p;
+  mla_status st = make_scheme(params, positions, d.rot_dim, &p.f);
+  if (st != MLA_OK) return st;
+  if (d.T == 0) return MLA_OK;
+  if (d.rot_dim > 0 && !positions) return fail(MLA_ERR_NULL, "positions is NULL");
+  if (!aligned(positions, 4)) return fail(MLA_ERR_ALIGN, "positions must be 4-byte aligned");
+  Job jobs[2] = {rope_job("q", *q, q_norm, d.T, d.rot_dim), {}};
+  const int n = k != nullptr ? 2 : 1;
+  if (n == 2) jobs[1] = rope_job("k", *k, k_norm, d.T, d.rot_dim);
+  for (int i = 0; i < n && st == MLA_OK; ++i) st = check_job(jobs[i], d.T, d.dtype, d.half != 0, false);
+  if (st == MLA_OK) st = check_overlaps(jobs, n, d.T, d.rot_dim ? positions : nullptr, q->rows, d.dtype);
+  if (st == MLA_OK && n == 2 && k->rows) st = check_overlaps(jobs, n, d.T, nullptr, k->rows, d.dtype);
+  if (st != MLA_OK) return st;
+  p.positions = positions;
+  return launch(jobs, n, d.T, d.dtype, d.half != 0, p, static_cast<cudaStream_t>(stream));
+}
+
+mla_status mla_kv_append(const mla_append_dims* dims, const mla_rope_params* params, const int32_t* positions,
+                         const int64_t* rows, const mla_append_input* k, const mla_head_norm* k_norm,
+                         const mla_kv_cache* k_cache, const mla_append_input* v, const mla_kv_cache* v_cache,
+                         const mla_rope_tensor* q, const mla_head_norm* q_norm, void* stream) {
+  using namespace mlaheads;
+  no_error();
+  if (!dims || !k || !k_cache || !v || !v_cache) return fail(MLA_ERR_NULL, "dims, k, v or a cache is NULL");
+  const mla_append_dims d = *dims;
+  if (d.dtype < MLA_ROPE_BF16 || d.dtype > MLA_ROPE_FP32) return fail(MLA_ERR_DTYPE, "dtype %d unknown", d.dtype);
+  if (d.T < 0 || d.half < 0 || d.half > 1) return fail(MLA_ERR_SHAPE, "T must be >= 0, half 0 or 1");
+  if (d.num_blocks < 1 || d.num_blocks >= (1 << 24))
+    return fail(MLA_ERR_SHAPE, "num_blocks=%d outside [1, 2^24)", d.num_blocks);
+  if (q != nullptr && q->rows != nullptr) return fail(MLA_ERR_UNSUPPORTED, "q's rows must be NULL");
+  Params p;
+  mla_status st = make_scheme(params, positions, d.rot_dim, &p.f);
+  if (st != MLA_OK) return st;
+  if (d.T == 0) return MLA_OK;
+  if (!rows || (d.rot_dim > 0 && !positions)) return fail(MLA_ERR_NULL, "rows or positions is NULL");
+  if (!aligned(positions, 4)) return fail(MLA_ERR_ALIGN, "positions must be 4-byte aligned");
+  Job jobs[3];
+  const mla_append_input* in[2] = {k, v};
+  const mla_kv_cache* cache[2] = {k_cache, v_cache};
+  for (int i = 0; i < 2; ++i) {
+    Job& j = jobs[i];
+    j.name = i == 0 ? "k" : "v";
+    j.x = in[i]->x;
+    j.xt = in[i]->token_stride;
+    j.xh = in[i]->head_stride;
+    j.out = cache[i]->data;
+    j.ob = cache[i]->block_stride;
+    j.orow = cache[i]->row_stride;
+    j.oh = cache[i]->head_stride;
+    j.rows = rows;
+    j.num_rows = 128ll * d.num_blocks;
+    j.n_heads = d.n_kv;
+    j.head_dim = i == 0 ? d.d_qk : d.d_v;
+    j.rot_off = i == 0 ? d.rot_off : 0;
+    j.rot_dim = i == 0 ? d.rot_dim : 0;
+    j.norm = norm_of(i == 0 ? k_norm : nullptr);
+    j.vec = false;
+  }
+  int n = 2;
+  if (q != nullptr) jobs[n++] = rope_job("q", *q, q_norm, d.T, d.rot_dim);
+  for (int i = 0; i < n && st == MLA_OK; ++i) st = check_job(jobs[i], d.T, d.dtype, d.half != 0, i < 2);
+  if (st == MLA_OK) st = check_overlaps(jobs, n, d.T, d.rot_dim ? positions : nullptr, rows, d.dtype);
+  if (st != MLA_OK) return st;
+  p.positions = positions;
+  return launch(jobs, n, d.T, d.dtype, d.half != 0, p, static_cast<cudaStream_t>(stream));
+}
+
+const char* mla_heads_last_error(void) { return mlaheads::g_error; }
+
+mla_status mla_heads_device_status(void* stream, uint32_t* flags, int32_t clear) {
+  using namespace mlaheads;
+  no_error();
+  HEADS_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)), "cudaStreamSynchronize");
+  unsigned int all = 0;
+  for (auto read : {prep_status, prompt_status, paged_status}) {
+    unsigned int v = 0;
+    HEADS_CUDA(read(&v, clear != 0), "the status word");
+    all |= v;
+  }
+  if (flags) *flags = all;
+  if (all != 0) return fail(MLA_ERR_DEVICE_STATUS, "heads device status 0x%x", all);
+  return MLA_OK;
+}
+
+}  // extern "C"
