@@ -1,105 +1,1092 @@
 // Attention of prompts for GB300 (sm_103a); formulas in mla_heads.h.
 //
-// A warp takes one query row through its keys, with the running maximum and sum
-// of the softmax in registers.
+// Rows are (token, head) pairs of one key head, token by token, 128 to a tile:
+// floor(128 / G) tokens and their G heads.  A CTA takes two tiles side by side
+// through the same 128-key tiles, so that the tensor cores work on one while
+// the softmax of the other runs:
+//   S_i = Q_i K^T      128 x 128 in tensor memory, both operands in shared memory
+//   P_i                over S_i in tensor memory, two 16-bit weights to a column
+//   O_i += P_i V       128 x d_v in tensor memory, P from there, V from shared memory
+// in the order P_0 V(t), Q_0 K(t+1), P_1 V(t), Q_1 K(t+1), so that a softmax has
+// the length of two products.  The 512 columns of tensor memory hold two of each.
+//
+// Keys and values stream through a ring of 16 KB slots (128 keys x 64 values of a
+// key, 64 keys x 128 or 128 keys x 64 of a value); Q stays.
+//
+// Warps: 0-3 and 4-7 softmax and epilogue of tile 0 and 1, one row to a thread;
+// 8 MMA issue; 9 TMA loads; 10 the schedule; 11 mends value rows that not every
+// token of the item sees (rows behind the sequence become zero, others lose
+// their NaN and infinities, which a weight of 0 would carry into the product).
+//
+// Schedule.  An item is (sequence, key head, two row tiles), from the last rows
+// (which see most keys) to the first, heads in groups whose keys and values fit
+// L2 side by side.  CTAs draw items from a counter.  Where there are too few for
+// the GPU, the key tiles of an item are cut into parts, whose states go to the
+// workspace and are joined by a second launch.  What is cut follows from the
+// lengths alone, so results do not depend on timing.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "heads.h"
+#include "ptx.cuh"
+
+namespace mlasp {
+unsigned long long host_wait_limit_ns();
+}
 
 namespace mlaheads {
+
+using namespace mlasp;
 
 __device__ unsigned int g_prompt_status = 0;
 
 cudaError_t prompt_status(unsigned int* v, bool clear) { return read_status(g_prompt_status, v, clear); }
 
-template <typename E>
-__global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ Problem p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int h = static_cast<int>(row % p.n_q), t = static_cast<int>(row / p.n_q);
-  if (t >= p.T) return;
-  int b = 0, first = 0, n = 0;
-  if (p.S1 > 0) {
-    b = t / p.S1;
-    first = b * p.S1;
-    n = p.q_lens != nullptr ? min(p.S1, max(0, p.q_lens[b])) : p.S1;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10, kMendWarp = 11;
+constexpr int kThreads = 384;
+constexpr int kRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kRegs, "register budget");
+constexpr int kTile = 128;
+constexpr int kSlotBytes = 16384;
+constexpr int kMaxSlots = 12;
+constexpr int kTileSmem = 14 * kSlotBytes;  // Q and ring together
+constexpr int kItemSlots = 2;
+constexpr int kItemReaders = kSoftmaxWarps + 3;  // MMA, load and mend warps
+
+constexpr int kFull = 0;                     // [kMaxSlots] the slot's bytes have landed and are mended
+constexpr int kEmpty = kFull + kMaxSlots;    // [kMaxSlots] the MMAs that read the slot are complete
+constexpr int kLocal = kEmpty + kMaxSlots;   // [kMaxSlots] bytes have landed that are still to be mended
+constexpr int kQFull = kLocal + kMaxSlots;   // [2]
+constexpr int kQFree = kQFull + 2;           // [2] the item's last score MMAs are complete
+constexpr int kSFull = kQFree + 2;           // [2] scores, and every MMA before them, are complete
+constexpr int kPReady = kSFull + 2;          // [2] weights are written, O is rescaled
+constexpr int kOFull = kPReady + 2;          // [2] the item's MMAs are complete
+constexpr int kItemFull = kOFull + 2;        // [kItemSlots]
+constexpr int kItemEmpty = kItemFull + kItemSlots;
+constexpr int kFinal = kItemEmpty + kItemSlots;
+constexpr int kNumBars = kFinal + 1;
+
+struct Item {
+  int live;        // 0: no more items
+  int b, hk, m;    // sequence, key head, pair of row tiles
+  int n, len, pos; // queries, keys within the table, position of query 0 (may be negative)
+  int q0, key0;    // first query row, first packed key row
+  int t0, ta, tb;  // key tiles [t0, ta) of row tile 0, [t0, tb) of row tile 1
+  int lo;          // keys from here on are not seen by every row
+  int part;        // slot of a partial state, -1: the item is whole
+  int pad[2];
+  __device__ __forceinline__ int t1(int h) const { return h ? tb : ta; }
+};
+
+constexpr int kOffItems = kTileSmem;
+constexpr int kOffBars = kOffItems + kItemSlots * static_cast<int>(sizeof(Item));
+constexpr int kOffTmem = kOffBars + 8 * kNumBars;
+constexpr int kOffAbort = kOffTmem + 4;
+constexpr int kOffMended = kOffAbort + 4;
+constexpr int kSmemBytes = kOffMended + 4 + 1024;  // 1024: the base is aligned by hand
+static_assert(kSmemBytes <= 232448 && kOffBars % 8 == 0, "shared memory");
+
+constexpr uint32_t kTmemS = 0, kTmemO = 256;  // two of 128 columns each
+
+// What the plan leaves for the other kernels, followed by four int32 arrays over the sequences.
+struct Head {
+  int items;    // parts of all items
+  int next;     // drawn so far
+  int merges;   // items that were cut
+  int pad[5];
+};
+
+struct Params {
+  Problem x;
+  Head* head;
+  int* first;    // [B + 1] first item of a sequence
+  int* cuts;     // [B] parts of each of its items
+  int* part0;    // [B] first partial state
+  int* merge0;   // [B + 1] first item to join
+  float* parts;
+  int part_floats, max_parts;
+  int G, tpt;    // heads to a key head, tokens of a row tile
+  int kc, vc;    // 64-column chunks of a key, slots of a value tile
+  int slots;
+  int sms;
+  uint32_t idesc_s, idesc_v;
+  int ks_qk;     // 16-wide steps of a key
+  unsigned long long wait_ns;
+};
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+struct Seq {
+  int n, len, pos, q0, key0, pairs;
+  bool bad_len, bad_table;
+};
+__device__ __forceinline__ Seq load_seq(const Params& p, int b) {
+  const Problem& x = p.x;
+  Seq s;
+  s.bad_len = s.bad_table = false;
+  s.key0 = 0;
+  auto range = [&](const int32_t* cu, int most, int& first) {
+    const int lo = __ldg(cu + b), hi = __ldg(cu + b + 1);
+    first = min(max(lo, 0), most);
+    const int end = min(max(hi, 0), most);
+    s.bad_len = s.bad_len || first != lo || end != hi || end < first;
+    return max(0, end - first);
+  };
+  if (x.S1 > 0) {
+    s.q0 = b * x.S1;
+    s.n = x.q_lens != nullptr ? min(x.S1, max(0, __ldg(x.q_lens + b))) : x.S1;
   } else {
-    bool bad = false, found = false;
-    for (int i = 0; i < p.B && !found; ++i) {
-      const int lo = min(max(p.cu_q[i], 0), p.T), hi = min(max(p.cu_q[i + 1], 0), p.T);
-      bad = bad || lo != p.cu_q[i] || hi != p.cu_q[i + 1] || hi < lo;
-      found = t >= lo && t < hi;
-      b = i;
-      first = lo;
-      n = hi - lo;
+    s.n = range(x.cu_q, x.T, s.q0);
+  }
+  int len;
+  if (x.num_blocks > 0) {
+    len = max(0, __ldg(x.act_seqs + b));
+    s.len = min(len, x.W * kPage);
+    s.bad_table = s.len < len && s.n > 0;
+  } else {
+    len = range(x.cu_k != nullptr ? x.cu_k : x.cu_q, x.Tk, s.key0);
+    s.len = len;
+  }
+  s.pos = len - s.n;
+  // padded rows are items too: they are written
+  const int tokens = x.S1 > 0 ? x.S1 : s.n;
+  s.pairs = (tokens + 2 * p.tpt - 1) / (2 * p.tpt);
+  return s;
+}
+// Keys that the first `tokens` queries see.
+__device__ __forceinline__ int seen_by(const Params& p, const Seq& s, int tokens) {
+  if (s.n == 0) return 0;
+  return p.x.causal ? min(s.len, max(0, s.pos + min(tokens, s.n))) : s.len;
+}
+__device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
+
+// ------------------------------------------------------------------ plan
+constexpr int kPlanThreads = 512;
+constexpr int kMinTiles = 4;  // key tiles of a part at least
+
+// Sums over the threads before this one, and over the block.
+template <int N>
+__device__ __forceinline__ void plan_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t (*part)[kPlanThreads / 32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    int64_t x = v[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    if (bad) atomicOr(&g_prompt_status, MLA_DEVICE_BAD_LENGTH);
-    if (!found) return;
+    if (lane == 31) part[i][warp] = x;
+    v[i] = x - v[i];
   }
-  int len, key0 = 0;
-  if (p.num_blocks > 0) {
-    len = max(0, p.act_seqs[b]);
-  } else {
-    const int32_t* cu = p.cu_k != nullptr ? p.cu_k : p.cu_q;
-    key0 = min(max(cu[b], 0), p.Tk);
-    const int end = min(max(cu[b + 1], 0), p.Tk);
-    if (key0 != cu[b] || end != cu[b + 1] || end < key0) atomicOr(&g_prompt_status, MLA_DEVICE_BAD_LENGTH);
-    len = max(0, end - key0);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    total[i] = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      if (w < warp) v[i] += part[i][w];
+      total[i] += part[i][w];
+    }
   }
-  const int i = t - first;
-  if (i >= n) len = 0;
-  const int sees = p.causal ? static_cast<int>(min(static_cast<int64_t>(len), static_cast<int64_t>(len) - n + i + 1)) : len;
-  const int hk = h / (p.n_q / p.n_kv);
-  float q[kMaxDqk / 32], o[kMaxDv / 32];
-  for (int k = 0; k < kMaxDqk / 32; ++k) {
-    const int d = lane + 32 * k;
-    q[k] = d < p.d_qk ? static_cast<float>(static_cast<const E*>(p.q.data)[t * p.q.token_stride + h * p.q.head_stride + d]) : 0.f;
+  __syncthreads();
+}
+
+// One block: counts the items, decides what is cut, numbers everything.
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_constant__ Params p) {
+  __shared__ int64_t part[3][kPlanThreads / 32];
+  const int B = p.x.B, Hkv = p.x.n_kv;
+  const int chunks = (B + kPlanThreads - 1) / kPlanThreads;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int64_t mine[2] = {0, 0}, all[2];  // items, key tiles
+  bool bad_len = false, bad_table = false;
+  for (int c = 0; c < chunks; ++c) {
+    const int b = c * kPlanThreads + threadIdx.x;
+    if (b >= B) break;
+    const Seq s = load_seq(p, b);
+    bad_len = bad_len || s.bad_len;
+    bad_table = bad_table || s.bad_table;
+    mine[0] += static_cast<int64_t>(s.pairs) * Hkv;
+    // the tiles of the first and the last pair, between which they grow evenly
+    mine[1] += static_cast<int64_t>(s.pairs) * Hkv * (tiles_of(seen_by(p, s, 2 * p.tpt)) + tiles_of(seen_by(p, s, s.n))) / 2;
   }
-  for (int k = 0; k < kMaxDv / 32; ++k) o[k] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  for (int key = 0; key < sees; ++key) {
-    int64_t ko, vo;
-    if (p.num_blocks > 0) {
-      const int page = key / kPage, id = page < p.W ? p.block_table[static_cast<int64_t>(b) * p.W + page] : -1;
-      if (id < 0 || id >= p.num_blocks) {
-        bad = true;
-        continue;
+  if (bad_len || bad_table)
+    atomicOr(&g_prompt_status, (bad_len ? MLA_DEVICE_BAD_LENGTH : 0u) | (bad_table ? MLA_DEVICE_BAD_BLOCK : 0u));
+  plan_scan(mine, all, part);
+  // parts of at most `cap` tiles, so many that every SM has some; fewer where their states would not fit
+  int64_t cap = max(static_cast<int64_t>(kMinTiles), (all[1] + p.sms - 1) / p.sms);
+  while (true) {
+    int64_t carry[3] = {0, 0, 0};  // items, partial states, items to join
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c * kPlanThreads + threadIdx.x;
+      int64_t v[3] = {0, 0, 0}, sum[3];
+      int cuts = 1;
+      if (b < B) {
+        const Seq s = load_seq(p, b);
+        const int64_t most = tiles_of(seen_by(p, s, s.n));
+        cuts = static_cast<int>(max(static_cast<int64_t>(1), (most + cap - 1) / cap));
+        v[0] = static_cast<int64_t>(s.pairs) * Hkv * cuts;
+        if (cuts > 1) {
+          v[1] = v[0];
+          v[2] = static_cast<int64_t>(s.pairs) * Hkv;
+        }
       }
-      ko = id * p.k.block_stride + (key % kPage) * p.k.row_stride + hk * p.k.head_stride;
-      vo = id * p.v.block_stride + (key % kPage) * p.v.row_stride + hk * p.v.head_stride;
+      plan_scan(v, sum, part);
+      if (b < B) {
+        p.first[b] = static_cast<int>(carry[0] + v[0]);
+        p.cuts[b] = cuts;
+        p.part0[b] = static_cast<int>(carry[1] + v[1]);
+        p.merge0[b] = static_cast<int>(carry[2] + v[2]);
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) carry[i] += sum[i];
+    }
+    if (carry[1] > p.max_parts) {
+      cap *= 2;
+      continue;
+    }
+    if (threadIdx.x == 0) {
+      p.first[B] = static_cast<int>(carry[0]);
+      p.merge0[B] = static_cast<int>(carry[2]);
+      p.head->items = static_cast<int>(carry[0]);
+      p.head->merges = static_cast<int>(carry[2]);
+      p.head->next = 0;
+    }
+    return;
+  }
+}
+
+// The sequence whose range of `first` holds i; the whole warp searches.
+__device__ __forceinline__ int find_seq(const int* first, int B, int i) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, count = B;
+  while (count > 1) {
+    const int step = (count + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = lane * step < count && __ldcg(first + at) <= i;
+    const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;
+    lo += k * step;
+    count = min(step, count - k * step);
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ roles
+struct Ctx {
+  uint32_t sb;
+  uint8_t* smem;
+  uint32_t tmem;
+  uint64_t wait_ns;
+  volatile uint32_t* abort;
+  __device__ uint32_t bar(int i) const { return sb + kOffBars + 8 * i; }
+  __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
+};
+__device__ __forceinline__ bool warp_wait(const Ctx& c, int i, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait<false>(c.bar(i), parity, c.abort, c.wait_ns));
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+               :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
+
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// A reader's walk over the items that the plan warp posts.
+struct Items {
+  uint32_t count = 0;
+  __device__ __forceinline__ bool next(const Ctx& c, Item& it) {
+    const int s = count % kItemSlots;
+    if (!warp_wait(c, kItemFull + s, (count / kItemSlots) & 1)) return false;
+    const int4* src = reinterpret_cast<const int4*>(c.smem + kOffItems) + s * (sizeof(Item) / 16);
+    int4* dst = reinterpret_cast<int4*>(&it);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(Item) / 16); ++i) dst[i] = src[i];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar(kItemEmpty + s));
+    ++count;
+    return uniform(it.live) != 0;
+  }
+};
+
+__device__ __forceinline__ int page_of(const Params& p, int b, int t) {
+  const int id = __ldg(p.x.block_table + static_cast<int64_t>(b) * p.x.W + t);
+  return id >= 0 && id < p.x.num_blocks ? id : -1;
+}
+
+__device__ void plan_role(const Params& p, const Ctx& c) {
+  const int total = __ldcg(&p.head->items), lane = threadIdx.x & 31;
+  uint32_t count = 0;
+  int i = blockIdx.x;
+  while (true) {
+    Item it;
+    it.live = i < total ? 1 : 0;
+    if (it.live) {
+      const int b = find_seq(p.first, p.x.B, i), cuts = __ldcg(p.cuts + b), Hkv = p.x.n_kv;
+      const Seq s = load_seq(p, b);
+      int k = i - __ldcg(p.first + b);
+      // heads whose keys and values fill about a third of L2 go side by side
+      const int64_t bytes = static_cast<int64_t>(max(1, s.len)) * (p.x.d_qk + p.x.d_v) * 2;
+      const int group = static_cast<int>(min(static_cast<int64_t>(Hkv), max(static_cast<int64_t>(1), (int64_t(40) << 20) / bytes)));
+      const int64_t per_group = static_cast<int64_t>(s.pairs) * group * cuts;
+      const int g = static_cast<int>(k / per_group);
+      k -= static_cast<int>(g * per_group);
+      const int heads = min(group, Hkv - g * group);
+      const int m = s.pairs - 1 - k / (heads * cuts);
+      k %= heads * cuts;
+      const int cut = k / heads, hk = g * group + k % heads;
+      it.b = b;
+      it.hk = hk;
+      it.m = m;
+      it.n = s.n;
+      it.len = s.len;
+      it.pos = s.pos;
+      it.q0 = s.q0;
+      it.key0 = s.key0;
+      const int tok = 2 * m * p.tpt;
+      int tiles[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tiles[h] = tok + h * p.tpt < s.n ? tiles_of(seen_by(p, s, tok + (h + 1) * p.tpt)) : 0;
+      const int most = max(tiles[0], tiles[1]);
+      it.t0 = static_cast<int>(static_cast<int64_t>(most) * cut / cuts);
+      const int end = static_cast<int>(static_cast<int64_t>(most) * (cut + 1) / cuts);
+      it.ta = max(it.t0, min(tiles[0], end));
+      it.tb = max(it.t0, min(tiles[1], end));
+      it.lo = seen_by(p, s, tok + 1);
+      it.part = cuts > 1 ? __ldcg(p.part0 + b) + (m * Hkv + hk) * cuts + cut : -1;
+    }
+    const int s = count % kItemSlots;
+    if (!warp_wait(c, kItemEmpty + s, ((count / kItemSlots) & 1) ^ 1)) return;
+    if (lane == 0) {
+      reinterpret_cast<Item*>(c.smem + kOffItems)[s] = it;
+      mbar_arrive(c.bar(kItemFull + s));
+    }
+    __syncwarp();
+    if (!it.live) return;
+    ++count;
+    if (lane == 0) i = static_cast<int>(gridDim.x) + atomicAdd(&p.head->next, 1);
+    i = uniform(i);
+  }
+}
+
+__device__ void load_role(const Params& p, const Ctx& c, const Maps& maps) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t ring = c.sb + 2 * p.kc * kSlotBytes;
+  const bool paged = p.x.num_blocks > 0;
+  Items items;
+  Item it;
+  Ring r;
+  uint32_t used[2] = {0, 0};  // times that a row tile's Q was loaded
+  while (items.next(c, it)) {
+    const int end = max(it.ta, it.tb);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (it.t1(h) <= it.t0) continue;
+      if (!warp_wait(c, kQFree + h, (used[h] & 1) ^ 1)) return;
+      ++used[h];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(c.bar(kQFull + h), p.kc * 128 * p.G * p.tpt);
+        for (int k = 0; k < p.kc; ++k)
+          tma_3d(c.sb + (h * p.kc + k) * kSlotBytes, &maps.q, 64 * k, it.hk * p.G, it.q0 + (2 * it.m + h) * p.tpt, c.bar(kQFull + h));
+      }
+      __syncwarp();
+    }
+    int page = paged && it.t0 < end ? page_of(p, it.b, it.t0) : 0;
+    for (int t = it.t0; t < end; ++t) {
+      const int ahead = paged && t + 1 < end ? page_of(p, it.b, t + 1) : 0;
+      const int row = paged ? 0 : it.key0 + kTile * t;
+      const int block = paged ? (page < 0 ? p.x.num_blocks : page) : 0;  // beyond the pool: zeros
+      for (int k = 0; k < p.kc; ++k) {
+        if (!warp_wait(c, kEmpty + r.slot, r.phase ^ 1)) return;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(c.bar(kFull + r.slot), kSlotBytes);
+          tma_4d(ring + r.slot * kSlotBytes, &maps.k, 64 * k, row, it.hk, block, c.bar(kFull + r.slot));
+        }
+        __syncwarp();
+        r.step(p.slots);
+      }
+      const int bars = kTile * (t + 1) > it.lo ? kLocal : kFull;
+      for (int k = 0; k < p.vc; ++k) {
+        if (!warp_wait(c, kEmpty + r.slot, r.phase ^ 1)) return;
+        if (lane == 0) {
+          const uint32_t bar = c.bar(bars + r.slot), dst = ring + r.slot * kSlotBytes;
+          mbar_arrive_expect_tx(bar, kSlotBytes);
+          tma_4d(dst, &maps.v, 0, row + 64 * k, it.hk, block, bar);
+          if (p.vc == 2) tma_4d(dst + kSlotBytes / 2, &maps.v, 64, row + 64 * k, it.hk, block, bar);
+        }
+        __syncwarp();
+        r.step(p.slots);
+      }
+      page = ahead;
+    }
+  }
+}
+
+// NaN and infinities of a pair of 16-bit values become zero.
+template <typename E>
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  constexpr uint32_t kExp = __is_same(E, __half) ? 0x7C00u : 0x7F80u;
+  if ((w & kExp) == kExp) w &= 0xFFFF0000u;
+  if ((w & kExp << 16) == kExp << 16) w &= 0x0000FFFFu;
+  return w;
+}
+template <typename E>
+__device__ __forceinline__ bool finite4(uint4 v) {
+  constexpr uint32_t kExp = __is_same(E, __half) ? 0x7C007C00u : 0x7F807F80u;
+  constexpr uint32_t kOne = __is_same(E, __half) ? 0x04000400u : 0x00800080u;  // carries out of a full exponent alone
+  const uint32_t c = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+  return (c & 0x80008000u) == 0;
+}
+
+template <typename E>
+__device__ void mend_role(const Params& p, const Ctx& c) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t ring = c.sb + 2 * p.kc * kSlotBytes;
+  Items items;
+  Item it;
+  Ring r;
+  uint32_t seen = 0;  // a bit per slot: parity of its local barrier
+  const int rows = p.vc == 2 ? 64 : 128, units = p.vc == 2 ? 16 : 8;  // keys of a slot, 16-byte units of a key
+  const int unit = lane & (units - 1);
+  while (items.next(c, it)) {
+    const int end = max(it.ta, it.tb);
+    for (int t = it.t0; t < end; ++t) {
+      for (int k = 0; k < p.kc; ++k) r.step(p.slots);
+      for (int k = 0; k < p.vc; ++k, r.step(p.slots)) {
+        if (kTile * (t + 1) <= it.lo) continue;
+        if (!warp_wait(c, kLocal + r.slot, (seen >> r.slot) & 1)) return;
+        seen ^= 1u << r.slot;
+        const int base = kTile * t + 64 * k;
+        const int first = max(0, min(it.lo - base, rows)), live = max(0, min(it.len - base, rows));
+        const uint32_t slot = ring + r.slot * kSlotBytes + (unit >> 3) * (kSlotBytes / 2);
+        auto at = [&](int row) { return slot + row * 128 + (((unit & 7) ^ (row & 7)) << 4); };
+        auto load = [&](int row) {
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(row)));
+          return v;
+        };
+        auto store = [&](int row, uint4 v) {
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at(row)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        };
+        bool good = true;
+        const int step = 32 / units;
+        for (int row = first + lane / units; row < live; row += 4 * step) {
+          uint4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) v[u] = row + u * step < live ? load(row + u * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) good = good && finite4<E>(v[u]);
+        }
+        bool wrote = live < rows;
+        for (int row = max(first, live) + lane / units; row < rows; row += step) store(row, make_uint4(0, 0, 0, 0));
+        if (__any_sync(0xffffffffu, !good)) {
+          wrote = true;
+          *c.mended() = 1u;
+          for (int row = first + lane / units; row < live; row += step) {
+            const uint4 v = load(row);
+            store(row, make_uint4(finite2<E>(v.x), finite2<E>(v.y), finite2<E>(v.z), finite2<E>(v.w)));
+          }
+        }
+        if (wrote) fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar(kFull + r.slot));
+      }
+    }
+  }
+}
+
+// The warp stays converged around an elected issuer, so that descriptors live in uniform registers.
+__device__ void mma_role(const Params& p, const Ctx& c) {
+  const uint64_t desc_q = make_sdesc(c.sb, 16, 1024, kSwizzle128B);
+  const uint64_t desc_k = make_sdesc(c.sb + 2 * p.kc * kSlotBytes, 16, 1024, kSwizzle128B);
+  const uint64_t desc_v = make_sdesc(c.sb + 2 * p.kc * kSlotBytes, kSlotBytes / 2, 1024, kSwizzle128B);
+  const int v_steps = p.vc == 2 ? 4 : 8;
+  Items items;
+  Item it;
+  Ring head;                    // next slot that no MMA has used
+  uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+  auto take = [&](int n) {  // waits for the next n slots
+    for (int k = 0; k < n; ++k) {
+      if (!warp_wait(c, kFull + head.slot, head.phase)) return false;
+      head.step(p.slots);
+    }
+    return true;
+  };
+  auto commit = [&](int bar) {
+    if (elect_one()) umma_commit(c.bar(bar));
+    __syncwarp();
+  };
+  auto release = [&](int slot, int n) {
+    for (int k = 0; k < n; ++k) {
+      commit(kEmpty + slot);
+      if (++slot == p.slots) slot = 0;
+    }
+  };
+  auto scores = [&](int h, int slot) {
+    const uint32_t d = c.tmem + kTmemS + 128 * h;
+    if (elect_one()) {
+      for (int k = 0; k < p.kc; ++k) {
+        const uint64_t a = desc_q + static_cast<uint32_t>((h * p.kc + k) * (kSlotBytes >> 4));
+        const uint64_t b = desc_k + static_cast<uint32_t>(slot * (kSlotBytes >> 4));
+        const int steps = min(4, p.ks_qk - 4 * k);
+        for (int s = 0; s < steps; ++s) umma_ss(d, a + 2 * s, b + 2 * s, p.idesc_s, (k | s) != 0 ? 1u : 0u);
+        if (++slot == p.slots) slot = 0;
+      }
+      umma_commit(c.bar(kSFull + h));
+    }
+    __syncwarp();
+  };
+  auto values = [&](int h, int slot, bool first) {
+    if (elect_one()) {
+      const uint32_t d = c.tmem + kTmemO + 128 * h;
+      uint32_t a = c.tmem + kTmemS + 128 * h;
+      for (int k = 0; k < p.vc; ++k) {
+        const uint64_t b = desc_v + static_cast<uint32_t>(slot * (kSlotBytes >> 4));
+        for (int s = 0; s < v_steps; ++s, a += 8) umma_ts(d, a, b + 128 * s, p.idesc_v, first && (k | s) == 0 ? 0u : 1u);
+        if (++slot == p.slots) slot = 0;
+      }
+    }
+    __syncwarp();
+  };
+  bool ok = true;
+  while (ok && items.next(c, it)) {
+    const int end = max(it.ta, it.tb);
+    if (it.t0 >= end) continue;
+    int key = head.slot;
+    ok = take(p.kc);
+    for (int h = 0; h < 2 && ok; ++h) {
+      if (it.t0 >= it.t1(h)) continue;
+      ok = warp_wait(c, kQFull + h, q_uses[h]++ & 1);
+      if (!ok) break;
+      scores(h, key);
+      if (it.t0 + 1 == it.t1(h)) commit(kQFree + h);
+    }
+    if (ok) release(key, p.kc);
+    for (int t = it.t0; t < end && ok; ++t) {
+      const int value = head.slot;
+      ok = take(p.vc);
+      key = head.slot;
+      if (ok && t + 1 < end) ok = take(p.kc);
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (t >= it.t1(h)) continue;
+        ok = warp_wait(c, kPReady + h, p_uses[h]++ & 1);
+        if (!ok) break;
+        tc_fence_after();
+        values(h, value, t == it.t0);
+        if (t + 1 == it.t1(h)) commit(kOFull + h);
+        if (h == (t < it.tb ? 1 : 0)) release(value, p.vc);
+        if (t + 1 < it.t1(h)) {
+          scores(h, key);
+          if (t + 2 == it.t1(h)) commit(kQFree + h);
+        }
+      }
+      if (ok && t + 1 < end) release(key, p.kc);
+    }
+  }
+  // every MMA in flight lands before the CTA leaves
+  commit(kFinal);
+  volatile uint32_t never = 0;
+  mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > 500000000ull ? c.wait_ns : 500000000ull);
+  __syncwarp();
+}
+
+// fp32 pairs (one instruction for two lanes of arithmetic).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <typename E>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if constexpr (__is_same(E, __half)) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The NaN of values that are not finite, which mending took from a row: keys [lo,
+// hi) of the sequence, put into what the calling thread has stored, its row of out
+// or of a partial state.  Rare: such values lay where not every row sees them.
+template <typename E>
+__device__ __noinline__ void infinite_columns(const Params& p, const Item& it, int lo, int hi, E* out, float* part) {
+  constexpr uint32_t kExp = __is_same(E, __half) ? 0x7C00u : 0x7F80u;
+  for (int key = lo; key < hi; ++key) {
+    int64_t at = it.hk * p.x.v.head_stride;
+    if (p.x.num_blocks > 0) {
+      const int page = page_of(p, it.b, key / kPage);
+      if (page < 0) continue;
+      at += page * p.x.v.block_stride + (key % kPage) * p.x.v.row_stride;
     } else {
-      ko = static_cast<int64_t>(key0 + key) * p.k.row_stride + hk * p.k.head_stride;
-      vo = static_cast<int64_t>(key0 + key) * p.v.row_stride + hk * p.v.head_stride;
+      at += static_cast<int64_t>(it.key0 + key) * p.x.v.row_stride;
     }
-    float z = 0.f;
-    for (int k = 0; k < kMaxDqk / 32; ++k) {
-      const int d = lane + 32 * k;
-      if (d < p.d_qk) z = fmaf(q[k], static_cast<float>(static_cast<const E*>(p.k.data)[ko + d]), z);
-    }
-    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-    z *= p.scale_log2;
-    const float top = fmaxf(m, z), mm = top == -INFINITY ? 0.f : top;
-    const float f = exp2f(m - mm), e = exp2f(z - mm);
-    m = top;
-    l = l * f + e;
-    for (int k = 0; k < kMaxDv / 32; ++k) {
-      const int d = lane + 32 * k;
-      if (d < p.d_v) o[k] = o[k] * f + e * static_cast<float>(static_cast<const E*>(p.v.data)[vo + d]);
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x.v.data) + at);
+    for (int u = 0; u < p.x.d_v / 8; ++u) {
+      const uint4 x = __ldg(v + u);
+      if (finite4<E>(x)) continue;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      for (int k = 0; k < 8; ++k) {
+        if (((w[k >> 1] >> (k & 1) * 16) & kExp) != kExp) continue;
+        const int d = 8 * u + k;
+        if (out != nullptr) reinterpret_cast<uint16_t*>(out)[d] = 0x7FFF;
+        else part[(d >> 2) * 512 + (d & 3)] = __uint_as_float(0x7FC00000u);
+      }
     }
   }
-  if (bad && lane == 0) atomicOr(&g_prompt_status, MLA_DEVICE_BAD_BLOCK);
-  for (int k = 0; k < kMaxDv / 32; ++k) {
-    const int d = lane + 32 * k;
-    if (d < p.d_v) static_cast<E*>(p.out)[(static_cast<int64_t>(t) * p.n_q + h) * p.d_v + d] = static_cast<E>(l == 0.f ? 0.f : o[k] / l);
+}
+
+template <typename E>
+__device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) {
+  const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // row tile, row of it
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t tS = c.tmem + lanes + kTmemS + 128 * h, tO = c.tmem + lanes + kTmemO + 128 * h;
+  // a positive scale leaves the order of scores alone: the maximum is taken of
+  // the raw ones, and the scale goes into the exponent's multiply-add
+  const float scale = p.x.scale_log2;
+  const bool raw = scale > 0.f;
+  const float mul = raw ? scale : 1.f;
+  const int tok_in = row / p.G, head_in = row - tok_in * p.G;
+  const bool paged = p.x.num_blocks > 0;
+  uint32_t uses = 0, outs = 0;
+  bool bad = false;
+  Items items;
+  Item it;
+  while (items.next(c, it)) {
+    const int tok = (2 * it.m + h) * p.tpt + tok_in;
+    const bool live = tok_in < p.tpt && tok < it.n;
+    const bool padded = tok_in < p.tpt && p.x.S1 > 0 && tok < p.x.S1;  // written, live or not
+    const int vis = p.x.causal ? min(it.len, max(0, it.pos + tok + 1)) : it.len;  // keys that this row sees
+    float m = -INFINITY, l = 0.f;
+    for (int t = it.t0; t < it.t1(h); ++t) {
+      const bool page = !paged || page_of(p, it.b, t) >= 0;
+      bad = bad || !page;
+      const int here = page ? vis - kTile * t : 0;
+      if (!warp_wait(c, kSFull + h, uses++ & 1)) return;
+      tc_fence_after();
+      float z[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tS + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(z + 32 * k));
+      tmem_wait_ld();
+      if (!raw) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k) z[k] *= scale;
+      }
+      if (__any_sync(0xffffffffu, here < kTile)) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k >= here) z[k] = -INFINITY;
+      }
+      float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+      for (int k = 4; k < 128; k += 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], z[k + j]), k + 4 + j < 128 ? z[k + 4 + j] : -INFINITY);
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+      // the maximum moves only when a tile exceeds it by more than 2^8: weights stay
+      // below 2^8 and O is rarely rescaled
+      const bool grow = top > m + 8.f;
+      const float f = grow ? fast_exp2(m - top) : 1.f;
+      if (grow) {
+        l *= f;
+        m = top;
+      }
+      const float mm = m == -INFINITY ? 0.f : m;
+      uint64_t sum[2] = {0, 0};
+      const uint64_t mul_2 = pair(mul, mul), mm_2 = pair(-mm, -mm);
+      uint32_t w[64];
+#pragma unroll
+      for (int k = 0; k < 64; ++k) {
+        float2 e = unpair(fma2(pair(z[2 * k], z[2 * k + 1]), mul_2, mm_2));
+        e.x = fast_exp2(e.x);
+        e.y = fast_exp2(e.y);
+        sum[k & 1] = add2(sum[k & 1], pair(e.x, e.y));
+        // one 16-bit weight: half a step of it, as one rounding of the output costs
+        w[k] = pack16<E>(e.x, e.y);
+      }
+      const float2 sums = unpair(add2(sum[0], sum[1]));
+      l += sums.x + sums.y;
+      // the MMAs before these scores are complete, the one before on O among them
+      if (t > it.t0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+        for (int k = 0; k < p.x.d_v; k += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tO + k, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+          tmem_st_32x32b_x32(tO + k, o);
+        }
+      }
+      tmem_st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(w));
+      tmem_st_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c.bar(kPReady + h));
+    }
+    const bool any = it.t1(h) > it.t0;
+    if (any) {
+      if (!warp_wait(c, kOFull + h, outs++ & 1)) return;
+      tc_fence_after();
+    }
+    if (!any || !live) {
+      l = 0.f;
+      m = -INFINITY;
+    }
+    const bool nothing = l == 0.f;
+    if (it.part < 0) {
+      const float inv = nothing ? 0.f : 1.f / l;
+      const int64_t at = static_cast<int64_t>(it.q0 + tok) * p.x.n_q + it.hk * p.G + head_in;
+      E* out = static_cast<E*>(p.x.out) + at * p.x.d_v;
+      const bool put = live || padded;
+#pragma unroll 1
+      for (int k = 0; k < p.x.d_v; k += 32) {
+        uint32_t v[32];
+        if (any) {
+          tmem_ld_32x32b_x32(tO + k, v);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            y[j] = nothing ? 0u : pack16<E>(__uint_as_float(v[8 * u + 2 * j]) * inv, __uint_as_float(v[8 * u + 2 * j + 1]) * inv);
+          if (put && k + 8 * u < p.x.d_v) *reinterpret_cast<uint4*>(out + k + 8 * u) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      if (*c.mended() && live && !nothing) infinite_columns<E>(p, it, it.lo, vis, out, nullptr);
+      if (put && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+    } else {
+      float* dst = p.parts + static_cast<int64_t>(it.part) * p.part_floats + h * (p.part_floats / 2);
+      if (any) {
+#pragma unroll 1
+        for (int k = 0; k < p.x.d_v; k += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tO + k, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (k + 4 * u < p.x.d_v)
+              reinterpret_cast<uint4*>(dst)[((k >> 2) + u) * 128 + row] = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        }
+        if (*c.mended() && live)
+          infinite_columns<E>(p, it, max(it.lo, kTile * it.t0), min(vis, kTile * it.t1(h)), nullptr, dst + row * 4);
+      }
+      // -inf says that the part is not the row's; the lowest maximum joins with weight 0 and
+      // brings along the NaN of infinite values whose scores are all -inf
+      dst[128 * p.x.d_v + row] = any && live ? fmaxf(m, -3.402823466e38f) : -INFINITY;
+      dst[128 * p.x.d_v + 128 + row] = l;
+    }
+    tc_fence_before();  // the reads of O come before the next item's MMAs (through kPReady)
   }
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[static_cast<int64_t>(t) * p.n_q + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+  if (bad) atomicOr(&g_prompt_status, MLA_DEVICE_BAD_BLOCK);
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t raw[];
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  Ctx c;
+  c.sb = (smem_u32(raw) + 1023u) & ~1023u;  // swizzled operands need 1024-byte alignment
+  c.smem = raw + (c.sb - smem_u32(raw));
+  c.wait_ns = p.wait_ns;
+  c.abort = reinterpret_cast<volatile uint32_t*>(c.smem + kOffAbort);
+  if (tid == 0) {
+    *c.abort = 0u;
+    *c.mended() = 0u;
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(c.bar(kFull + i), 1);
+      mbar_init(c.bar(kEmpty + i), 1);
+      mbar_init(c.bar(kLocal + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(c.bar(kQFull + i), 1);
+      mbar_init(c.bar(kQFree + i), 1);
+      mbar_init(c.bar(kSFull + i), 1);
+      mbar_init(c.bar(kPReady + i), 4);
+      mbar_init(c.bar(kOFull + i), 1);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(c.bar(kItemFull + i), 1);
+      mbar_init(c.bar(kItemEmpty + i), kItemReaders);
+    }
+    mbar_init(c.bar(kFinal), 1);
+    fence_mbarrier_init_cluster();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(c.sb + kOffTmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  c.tmem = uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(c.smem + kOffTmem)));
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+
+  if (warp < kSoftmaxWarps) {
+    regs_increase<kSoftmaxRegs>();
+    softmax_role<E>(p, c, warp, lane);
+  } else {
+    regs_decrease<kOtherRegs>();
+    if (warp == kMmaWarp) mma_role(p, c);
+    else if (warp == kLoadWarp) load_role(p, c, maps);
+    else if (warp == kPlanWarp) plan_role(p, c);
+    else if (warp == kMendWarp) mend_role<E>(p, c);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*c.abort) {
+    // a wait ran out: loads may still be in flight to shared memory; they take microseconds
+    if (tid == 0) atomicOr(&g_prompt_status, MLA_DEVICE_TIMEOUT);
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000) {
+    }
+  }
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(c.tmem, 512);
+}
+
+// ------------------------------------------------------------------ merge
+// Joins the parts of the items that were cut: a thread takes one row and kMergeCols columns.
+constexpr int kMergeCols = 8;
+template <typename E>
+__global__ void __launch_bounds__(128) prompt_merge_kernel(const __grid_constant__ Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int merges = __ldcg(&p.head->merges), row = threadIdx.x, slices = p.x.d_v / kMergeCols;
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(merges) * 2 * slices; w += gridDim.x) {
+    const int slice = static_cast<int>(w % slices), h = static_cast<int>(w / slices) & 1, i = static_cast<int>(w / slices >> 1);
+    const int b = find_seq(p.merge0, p.x.B, i), cuts = __ldcg(p.cuts + b);
+    const Seq s = load_seq(p, b);
+    const int k = i - __ldcg(p.merge0 + b), m = k / p.x.n_kv, hk = k % p.x.n_kv;
+    const int tok_in = row / p.G, tok = (2 * m + h) * p.tpt + tok_in;
+    const bool put = tok_in < p.tpt && tok < (p.x.S1 > 0 ? p.x.S1 : s.n);
+    const float* src = p.parts + static_cast<int64_t>(__ldcg(p.part0 + b) + k * cuts) * p.part_floats + h * (p.part_floats / 2);
+    float top = -INFINITY, l = 0.f, o[kMergeCols] = {};
+    for (int c = 0; c < cuts; ++c, src += p.part_floats) {
+      const float mk = __ldcg(src + 128 * p.x.d_v + row), lk = __ldcg(src + 128 * p.x.d_v + 128 + row);
+      if (mk == -INFINITY) continue;
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(src) + slice * 2 * 128 + row);
+      const float4 d = __ldcg(reinterpret_cast<const float4*>(src) + (slice * 2 + 1) * 128 + row);
+      const float next = fmaxf(top, mk), f = top == -INFINITY ? 0.f : exp2f(top - next), e = exp2f(mk - next);
+      top = next;
+      l = l * f + lk * e;
+      const float v[kMergeCols] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+      for (int j = 0; j < kMergeCols; ++j) o[j] = o[j] * f + v[j] * e;
+    }
+    if (!put) continue;
+    const bool nothing = l == 0.f;
+    const float inv = nothing ? 0.f : 1.f / l;
+    const int64_t at = static_cast<int64_t>(s.q0 + tok) * p.x.n_q + hk * p.G + (row - tok_in * p.G);
+    uint32_t y[kMergeCols / 2];
+#pragma unroll
+    for (int j = 0; j < kMergeCols / 2; ++j) y[j] = nothing ? 0u : pack16<E>(o[2 * j] * inv, o[2 * j + 1] * inv);
+    *reinterpret_cast<uint4*>(static_cast<E*>(p.x.out) + at * p.x.d_v + slice * kMergeCols) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (slice == 0 && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+namespace {
+
+constexpr int kMaxDevices = 64;
+struct Device {
+  bool ready = false;
+  int sms = 0;
+};
+Device g_dev[kMaxDevices];
+std::mutex g_lock;
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+constexpr int kMaxParts = 640;  // partial states in the workspace at most
+
+// Partial states that a call can need: none where no item has more key tiles than a part has at least.
+int parts_of(const Problem& p) {
+  const int64_t keys = p.num_blocks > 0 ? static_cast<int64_t>(p.W) * kPage : p.Tk;
+  if (keys <= kMinTiles * kTile) return 0;
+  const int64_t tpt = kTile / (p.n_q / p.n_kv), tiles = (keys + kTile - 1) / kTile;
+  const int64_t pairs = p.S1 > 0 ? p.B * ((p.S1 + 2 * tpt - 1) / (2 * tpt)) : p.T / (2 * tpt) + p.B;
+  // each factor bounded first: their product passes 64 bits for the largest dims
+  const int64_t items = std::min<int64_t>(kMaxParts, std::min<int64_t>(kMaxParts, pairs) * p.n_kv);
+  return static_cast<int>(std::min<int64_t>(kMaxParts, items * std::min<int64_t>(kMaxParts, (tiles + kMinTiles - 1) / kMinTiles)));
+}
+int part_floats(const Problem& p) { return 2 * (128 * p.d_v + 256); }
+size_t lists_bytes(const Problem& p) { return (sizeof(Head) + (4 * static_cast<size_t>(p.B) + 2) * sizeof(int) + 255) & ~size_t(255); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename E>
+mla_status prepare_kernel() {
+  HEADS_CUDA(cudaFuncSetAttribute(prompt_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes), "kernel set-up");
+  cudaFuncAttributes fa;
+  HEADS_CUDA(cudaFuncGetAttributes(&fa, prompt_attn_kernel<E>), "kernel attributes");
+  if (fa.numRegs < kRegs) return fail(MLA_ERR_CUDA, "the kernel was built with %d registers", fa.numRegs);  // what the warpgroups divide
+  return MLA_OK;
+}
+
+// Kernel attributes and the tensor-map encoder; the first call on a device.
+mla_status init_device(int* sms) {
+  int dev = 0;
+  HEADS_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  if (dev < 0 || dev >= kMaxDevices) return fail(MLA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
+  std::lock_guard<std::mutex> guard(g_lock);
+  Device& d = g_dev[dev];
+  if (!d.ready) {
+    if (g_encode == nullptr) {
+      cudaDriverEntryPointQueryResult q;
+      void* fn = nullptr;
+      HEADS_CUDA(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q), "looking up cuTensorMapEncodeTiled");
+      if (fn == nullptr || q != cudaDriverEntryPointSuccess) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    HEADS_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev), "device attributes");
+    mla_status st = prepare_kernel<__nv_bfloat16>();
+    if (st == MLA_OK) st = prepare_kernel<__half>();
+    if (st != MLA_OK) return st;
+    d.ready = true;
+  }
+  *sms = d.sms;
+  return MLA_OK;
+}
+
+// A tensor of 16-bit values, the innermost dimension adjacent; strides in elements, of dimensions 1 ...
+mla_status tmap(CUtensorMap* m, int dtype, const void* base, int rank, const int64_t* size, const int64_t* stride, const int* box, const char* what) {
+  cuuint64_t dim[4], st[3];
+  cuuint32_t bx[4], es[4];
+  for (int i = 0; i < rank; ++i) {
+    dim[i] = static_cast<cuuint64_t>(size[i]);
+    bx[i] = static_cast<cuuint32_t>(box[i]);
+    es[i] = 1;
+    // a dimension of one place is never stepped over: any legal stride will do
+    if (i > 0) st[i - 1] = size[i] > 1 ? static_cast<cuuint64_t>(stride[i - 1]) * 2 : ((static_cast<cuuint64_t>(size[0]) * 2 + 15) & ~cuuint64_t(15));
+  }
+  const CUresult r = g_encode(m, dtype == MLA_ROPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank),
+                              const_cast<void*>(base), dim, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "tensor map of %s: error %d", what, static_cast<int>(r));
+  return MLA_OK;
+}
+
+}  // namespace
+
+size_t tiles_workspace(const Problem& p) { return lists_bytes(p) + static_cast<size_t>(parts_of(p)) * part_floats(p) * sizeof(float); }
+
+mla_status launch_tiles(const Problem& x, cudaStream_t s) {
+  int sms = 0;
+  const mla_status st = init_device(&sms);
+  if (st != MLA_OK) return st;
+  Params p;
+  p.x = x;
+  uint8_t* ws = static_cast<uint8_t*>(x.workspace);
+  p.head = reinterpret_cast<Head*>(ws);
+  p.first = reinterpret_cast<int*>(ws + sizeof(Head));
+  p.cuts = p.first + x.B + 1;
+  p.part0 = p.cuts + x.B;
+  p.merge0 = p.part0 + x.B;
+  p.parts = reinterpret_cast<float*>(ws + lists_bytes(x));
+  p.part_floats = part_floats(x);
+  p.max_parts = parts_of(x);
+  p.G = x.n_q / x.n_kv;
+  p.tpt = kTile / p.G;
+  p.kc = (x.d_qk + 63) / 64;
+  p.vc = x.d_v > 64 ? 2 : 1;
+  p.slots = std::min(kMaxSlots, kTileSmem / kSlotBytes - 2 * p.kc);
+  p.sms = sms;
+  const uint32_t bf16 = x.dtype == MLA_ROPE_BF16 ? 1 : 0;
+  p.idesc_s = make_idesc_f16(128, 128, bf16, 0, 0);                                        // A, B K-major
+  p.idesc_v = make_idesc_f16(128, static_cast<uint32_t>((x.d_v + 15) & ~15), bf16, 0, 1);  // B MN-major
+  p.ks_qk = (x.d_qk + 15) / 16;
+  p.wait_ns = host_wait_limit_ns();
+  Maps maps;
+  {
+    const int64_t size[3] = {x.d_qk, x.n_q, x.T}, stride[2] = {x.q.head_stride, x.q.token_stride};
+    const int box[3] = {64, p.G, p.tpt};
+    const mla_status ms = tmap(&maps.q, x.dtype, x.q.data, 3, size, stride, box, "q");
+    if (ms != MLA_OK) return ms;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const mla_kv_cache& c = i == 0 ? x.k : x.v;
+    const bool none = x.num_blocks == 0 && x.Tk == 0;  // no key is ever loaded
+    const int64_t size[4] = {i == 0 ? x.d_qk : x.d_v, x.num_blocks > 0 ? kPage : std::max(1, x.Tk), x.n_kv, std::max(1, x.num_blocks)};
+    const int64_t stride[3] = {c.row_stride, c.head_stride, c.block_stride};
+    const int box[4] = {64, i == 1 && p.vc == 2 ? 64 : 128, 1, 1};
+    CUtensorMap* map = i == 0 ? &maps.k : &maps.v;
+    const mla_status ms = none ? MLA_OK : tmap(map, x.dtype, c.data, 4, size, stride, box, i == 0 ? "k" : "v");
+    if (ms != MLA_OK) return ms;
+    if (none) *map = maps.q;
+  }
+  const bool bf = x.dtype == MLA_ROPE_BF16;
+  prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+  HEADS_CUDA(cudaGetLastError(), "plan launch");
+  const int64_t pairs = x.S1 > 0 ? static_cast<int64_t>(x.B) * ((x.S1 + 2 * p.tpt - 1) / (2 * p.tpt)) : x.T / (2 * p.tpt) + x.B;
+  const int64_t most = std::min<int64_t>(sms, pairs) * x.n_kv + p.max_parts;
+  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, most))));
+  HEADS_CUDA(bf ? launch_after(prompt_attn_kernel<__nv_bfloat16>, grid, kThreads, kSmemBytes, s, maps, p)
+                : launch_after(prompt_attn_kernel<__half>, grid, kThreads, kSmemBytes, s, maps, p),
+             "kernel launch");
+  if (p.max_parts > 0)
+    HEADS_CUDA(bf ? launch_after(prompt_merge_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(4 * sms)), 128, 0, s, p)
+                  : launch_after(prompt_merge_kernel<__half>, dim3(static_cast<unsigned>(4 * sms)), 128, 0, s, p),
+               "merge launch");
+  return MLA_OK;
 }
 
 mla_status check_head_dims(int n_q, int n_kv, int d_qk, int d_v, int dtype) {
@@ -151,16 +1138,6 @@ mla_status check_problem(const Problem& p, size_t workspace_bytes, size_t needed
       if (overlap(o, i)) return fail(MLA_ERR_UNSUPPORTED, "an output or the workspace overlaps an input");
   if (overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2]))
     return fail(MLA_ERR_UNSUPPORTED, "out, lse and the workspace overlap");
-  return MLA_OK;
-}
-
-size_t tiles_workspace(const Problem&) { return 256; }
-
-mla_status launch_tiles(const Problem& p, cudaStream_t s) {
-  const int64_t blocks = (static_cast<int64_t>(p.T) * p.n_q + 3) / 4;
-  if (p.dtype == MLA_ROPE_BF16) rows_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
-  else rows_kernel<__half><<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
-  HEADS_CUDA(cudaGetLastError(), "launch");
   return MLA_OK;
 }
 
