@@ -91,21 +91,17 @@ __device__ __forceinline__ void pack(Pack<E, V>& a, const float* x) {
   }
 }
 
-__device__ __forceinline__ float group_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // A lane's units of a head.  kTwo: a rotated unit is two packs, V values and the
 // V that turn with them; otherwise one pack of V / 2 adjacent pairs.
 template <typename E, int V, bool kTwo, int KU>
 struct Lane {
   static constexpr int kVals = kTwo ? 2 * V : V;
   static constexpr int kPairs = kTwo ? V : V / 2;
-  int d[KU];       // first value
-  int second[KU];  // distance of the other pack, 0: there is none
+  int d[KU];   // first value
+  int second;  // distance of a rotated unit's other pack
   bool in[KU], rot[KU];
   __device__ __forceinline__ void place(const Tensor& w, int first_unit, int lane) {
+    second = kTwo ? (w.half ? w.pairs : 1) : 0;
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       const int k = first_unit + lane + i * w.lanes;
@@ -113,11 +109,9 @@ struct Lane {
       rot[i] = k < w.rot_units;
       if (rot[i]) {
         d[i] = w.rot_off + (kTwo && w.half ? k * V : 2 * kPairs * k);
-        second[i] = kTwo ? (w.half ? w.pairs : 1) : 0;
       } else {
         const int c = (k - w.rot_units) * V;  // copied values, in order
         d[i] = c < w.rot_off ? c : c + 2 * w.pairs;
-        second[i] = 0;
       }
     }
   }
@@ -128,13 +122,19 @@ struct Lane {
       for (int k = 0; k < Pack<E, V>::W; ++k) a[i].w[k] = b[i].w[k] = 0;
       if (live && in[i]) {
         a[i].load(x + d[i]);
-        if (kTwo && rot[i]) b[i].load(x + d[i] + second[i]);
+        if (kTwo && rot[i]) b[i].load(x + d[i] + second);
       }
     }
   }
 };
 
-template <typename E, int V, bool kTwo, int KU>
+// The rotation of a normed pair is linear in the pair: weights go into the
+// cosines and sines, once for a token, and the bias turns along.
+struct Coef {
+  float ca, sb, sa, cb;  // y_a = x_a ca - x_b sb,  y_b = x_a sa + x_b cb
+};
+
+template <typename E, int V, bool kTwo, int KU, bool kLayer>
 __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block) {
   using L = Lane<E, V, kTwo, KU>;
   const int tid = threadIdx.x;
@@ -153,30 +153,40 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
   const E* x = static_cast<const E*>(w.x) + (live ? t * w.xt + h0 * w.xh : 0);
   E* out = static_cast<E*>(w.out) + (live ? (to >> 7) * w.ob + (to & 127) * w.orow + h0 * w.oh : 0);
   const int32_t pos = live && w.rot_units > 0 ? __ldg(p.positions + t) : 0;
+  const bool normed = w.kind != MLA_NORM_NONE, layer = kLayer && w.kind == MLA_NORM_LAYER;
   L at;
-  float cs[KU][2 * L::kPairs], wt[KU][L::kVals], bi[KU][L::kVals];
-  auto angles_and_weights = [&]() {
+  Coef co[KU][L::kPairs];
+  float ba[kLayer ? KU : 1][L::kPairs], bb[kLayer ? KU : 1][L::kPairs];
+  auto coefficients = [&]() {
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
 #pragma unroll
       for (int j = 0; j < L::kPairs; ++j) {
-        float2 v = make_float2(1.f, 0.f);
-        if (at.rot[i]) v = mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale);
-        cs[i][2 * j] = v.x;
-        cs[i][2 * j + 1] = v.y;
-      }
-#pragma unroll
-      for (int j = 0; j < L::kVals; ++j) {
-        const int d = at.d[i] + (j < V ? j : at.second[i] + j - V);
-        const bool has = at.in[i] && (j < V || at.rot[i]) && w.kind != MLA_NORM_NONE;
-        wt[i][j] = has && w.weight != nullptr ? value<E>(w.weight, d, w.weight_fp32) : 1.f;
-        bi[i][j] = has && w.bias != nullptr ? value<E>(w.bias, d, w.weight_fp32) : 0.f;
+        float2 cs = make_float2(1.f, 0.f);
+        if (at.rot[i]) cs = mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale);
+        const int da = at.d[i] + (kTwo ? j : 2 * j), db = kTwo ? da + at.second : da + 1;
+        const bool has_b = kTwo ? at.rot[i] : at.in[i];
+        float wa = 1.f, wb = 1.f;
+        if (normed && w.weight != nullptr) {
+          if (at.in[i]) wa = value<E>(w.weight, da, w.weight_fp32);
+          if (has_b) wb = value<E>(w.weight, db, w.weight_fp32);
+        }
+        co[i][j] = {wa * cs.x, wb * cs.y, wa * cs.y, wb * cs.x};
+        if constexpr (kLayer) {
+          float va = 0.f, vb = 0.f;
+          if (normed && w.bias != nullptr) {
+            if (at.in[i]) va = value<E>(w.bias, da, w.weight_fp32);
+            if (has_b) vb = value<E>(w.bias, db, w.weight_fp32);
+          }
+          const float2 z = mlarp::turn2(va, vb, cs);
+          ba[i][j] = z.x;
+          bb[i][j] = z.y;
+        }
       }
     }
   };
   at.place(w, 0, lane);
-  if (w.chunks == 1) angles_and_weights();
-  // a chunk's part of sum (x - mean)^power
+  // a chunk's part of sum (x - mean) or its squares
   auto part = [&](const Pack<E, V>(&a)[KU], const Pack<E, V>(&b)[KU], float mean, bool square) {
     float s = 0.f;
 #pragma unroll
@@ -186,9 +196,9 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
       if constexpr (kTwo) unpack<E, V>(b[i], v + V);
 #pragma unroll
       for (int j = 0; j < L::kVals; ++j) {
-        const bool has = at.in[i] && (j < V || at.rot[i]);
-        const float c = has ? v[j] - mean : 0.f;
-        s += square ? c * c : c;
+        float c = v[j];  // places without a value hold zero
+        if constexpr (kLayer) c = at.in[i] && (j < V || at.rot[i]) ? c - mean : 0.f;
+        s = square ? fmaf(c, c, s) : s + c;
       }
     }
     return s;
@@ -197,35 +207,39 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
   auto finish = [&](Pack<E, V>(&a)[KU], Pack<E, V>(&b)[KU], float mean, float inv, E* o, bool put) {
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
-      float v[L::kVals];
-      unpack<E, V>(a[i], v);
-      if constexpr (kTwo) unpack<E, V>(b[i], v + V);
-      if (w.kind != MLA_NORM_NONE) {
-#pragma unroll
-        for (int j = 0; j < L::kVals; ++j) v[j] = fmaf((v[j] - mean) * inv, wt[i][j], bi[i][j]);
-      }
-      if (at.rot[i]) {
+      if (normed || at.rot[i]) {
+        float v[L::kVals];
+        unpack<E, V>(a[i], v);
+        if constexpr (kTwo) unpack<E, V>(b[i], v + V);
 #pragma unroll
         for (int j = 0; j < L::kPairs; ++j) {
           float& u = v[kTwo ? j : 2 * j];
           float& y = v[kTwo ? V + j : 2 * j + 1];
-          const float2 z = mlarp::turn2(u, y, make_float2(cs[i][2 * j], cs[i][2 * j + 1]));
-          u = z.x;
-          y = z.y;
+          const float xa = (kLayer ? u - mean : u) * inv, xb = (kLayer ? y - mean : y) * inv;
+          const Coef& k = co[i][j];
+          if (at.rot[i]) {
+            u = fmaf(xa, k.ca, -__fmul_rn(xb, k.sb));
+            y = fmaf(xa, k.sa, __fmul_rn(xb, k.cb));
+          } else {  // what does not turn keeps apart from its neighbour
+            u = xa * k.ca;
+            y = xb * k.cb;
+          }
+          if constexpr (kLayer) {
+            u += ba[i][j];
+            y += bb[i][j];
+          }
         }
-      }
-      if (w.kind != MLA_NORM_NONE || at.rot[i]) {
         pack<E, V>(a[i], v);
         if constexpr (kTwo) pack<E, V>(b[i], v + V);
       }
       if (put && at.in[i]) {
         a[i].store(o + at.d[i]);
-        if (kTwo && at.rot[i]) b[i].store(o + at.d[i] + at.second[i]);
+        if (kTwo && at.rot[i]) b[i].store(o + at.d[i] + at.second);
       }
     }
   };
   const int64_t x_step = w.head_rows * w.xh, o_step = w.head_rows * w.oh;
-  constexpr int kUnroll = KU * V >= 8 ? 2 : 1;  // heads in flight
+  constexpr int kUnroll = KU > 1 && V > 1 ? 1 : (kTwo ? 2 : 4);  // heads in flight
   for (int it = 0; it < w.passes; it += kUnroll) {
     Pack<E, V> a[kUnroll][KU], b[kUnroll][KU];
     bool has[kUnroll];
@@ -237,22 +251,30 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
       inv[u] = 1.f;
       if (w.chunks == 1) at.load(x + u * x_step, has[u], a[u], b[u]);
     }
-    for (int step = w.kind == MLA_NORM_LAYER ? 0 : 1; step < 2 && w.kind != MLA_NORM_NONE; ++step) {
+    if (it == 0 && w.chunks == 1 && (normed || w.rot_units > 0)) coefficients();  // while the loads are on their way
+    for (int step = layer ? 0 : 1; step < 2 && normed; ++step) {
+      float s[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        float s = 0.f;
+        s[u] = 0.f;
         if (w.chunks == 1) {
-          s = part(a[u], b[u], mean[u], step == 1);
+          s[u] = part(a[u], b[u], mean[u], step == 1);
         } else {
           for (int c = 0; c < w.chunks; ++c) {
             at.place(w, c * KU * w.lanes, lane);
             at.load(x + u * x_step, has[u], a[u], b[u]);
-            s += part(a[u], b[u], mean[u], step == 1);
+            s[u] += part(a[u], b[u], mean[u], step == 1);
           }
         }
-        s = group_sum(s, w.lanes) * w.inv_d;
-        if (step == 0) mean[u] = s;
-        else inv[u] = 1.f / sqrtf(s + w.eps);
+      }
+      for (int o = w.lanes >> 1; o > 0; o >>= 1) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (step == 0) mean[u] = s[u] * w.inv_d;
+        else inv[u] = 1.f / sqrtf(fmaf(s[u], w.inv_d, w.eps));
       }
     }
 #pragma unroll
@@ -262,7 +284,7 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
       } else {
         for (int c = 0; c < w.chunks; ++c) {  // in place, a lane has read and written its own values alone
           at.place(w, c * KU * w.lanes, lane);
-          angles_and_weights();
+          coefficients();
           at.load(x + u * x_step, has[u], a[u], b[u]);
           finish(a[u], b[u], mean[u], inv[u], out + u * o_step, has[u]);
         }
@@ -274,15 +296,15 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
 }
 
 // One block works on one of the tensors.
-template <typename E, int V, int KU>
-__global__ void __launch_bounds__(kThreads) head_prep_kernel(const __grid_constant__ Params p) {
+template <typename E, int V, int KU, bool kLayer>
+__global__ void __launch_bounds__(kThreads, kLayer || KU > 1 ? 2 : 3) head_prep_kernel(const __grid_constant__ Params p) {
   int block = static_cast<int>(blockIdx.x), i = 0;
   while (i < 2 && block >= p.t[i].blocks) block -= p.t[i++].blocks;
   const Tensor& w = p.t[i];
   if constexpr (V > 1) {
-    if (!w.half) return work<E, V, false, KU>(p, w, block);
+    if (!w.half) return work<E, V, false, KU, kLayer>(p, w, block);
   }
-  work<E, V, true, KU>(p, w, block);
+  work<E, V, true, KU, kLayer>(p, w, block);
 }
 
 thread_local char g_error[256] = "";
@@ -377,8 +399,8 @@ mla_status check_overlaps(const Job* jobs, int n, int T, const int32_t* position
   return MLA_OK;
 }
 
-constexpr int kUnits = 2;         // units of a lane, 16-byte accesses
-constexpr int kSingleUnits = 4;   // single values
+constexpr int kUnits = 1;        // units of a lane, 16-byte accesses
+constexpr int kSingleUnits = 4;  // single values
 
 // Splits a checked tensor's heads into groups and blocks.
 mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
@@ -428,23 +450,28 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
 typedef void (*Kernel)(Params);
 
 mla_status launch(const Job* jobs, int n, int T, int dtype, bool half, Params& p, cudaStream_t s) {
-  static const Kernel kernels[3][2] = {
-      {head_prep_kernel<__nv_bfloat16, 1, kSingleUnits>, head_prep_kernel<__nv_bfloat16, 8, kUnits>},
-      {head_prep_kernel<__half, 1, kSingleUnits>, head_prep_kernel<__half, 8, kUnits>},
-      {head_prep_kernel<float, 1, kSingleUnits>, head_prep_kernel<float, 4, kUnits>}};
+  static const Kernel kernels[3][2][2] = {
+      {{head_prep_kernel<__nv_bfloat16, 1, kSingleUnits, false>, head_prep_kernel<__nv_bfloat16, 1, kSingleUnits, true>},
+       {head_prep_kernel<__nv_bfloat16, 8, kUnits, false>, head_prep_kernel<__nv_bfloat16, 8, kUnits, true>}},
+      {{head_prep_kernel<__half, 1, kSingleUnits, false>, head_prep_kernel<__half, 1, kSingleUnits, true>},
+       {head_prep_kernel<__half, 8, kUnits, false>, head_prep_kernel<__half, 8, kUnits, true>}},
+      {{head_prep_kernel<float, 1, kSingleUnits, false>, head_prep_kernel<float, 1, kSingleUnits, true>},
+       {head_prep_kernel<float, 4, kUnits, false>, head_prep_kernel<float, 4, kUnits, true>}}};
   p.T = T;
   for (int vec = 1; vec >= 0; --vec) {
     int taken = 0;
     int64_t grid = 0;
+    bool layer = false;
     for (int i = 0; i < 3; ++i) p.t[i].blocks = 0;
     for (int i = 0; i < n; ++i) {
       if (jobs[i].vec != (vec != 0)) continue;
       const mla_status st = split_job(jobs[i], T, dtype, half, &p.t[taken]);
       if (st != MLA_OK) return st;
+      layer = layer || jobs[i].norm.kind == MLA_NORM_LAYER;
       grid += p.t[taken++].blocks;
     }
     if (taken == 0) continue;
-    kernels[dtype][vec]<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
+    kernels[dtype][vec][layer ? 1 : 0]<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
     HEADS_CUDA(cudaGetLastError(), "launch");
   }
   return MLA_OK;
