@@ -19,7 +19,7 @@ namespace mlaheads {
 using mlarp::Freqs;
 using mlarp::Pack;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxPasses = 16;  // heads of a group
 
 __device__ unsigned int g_prep_status = 0;
@@ -34,7 +34,7 @@ struct Tensor {
   const void* weight;
   const void* bias;
   float eps, inv_d;
-  int kind, weight_fp32;
+  int kind, weight_fp32, weight_vec;  // vec: weights are read 16 bytes at a time
   int n_heads, rot_off, head_dim;
   int pairs, half;     // of the rotation; 0 pairs: none
   int rot_units;       // units of a head that hold rotated values
@@ -54,13 +54,6 @@ struct Params {
   Tensor t[3];
   int T;
 };
-
-template <typename E>
-__device__ __forceinline__ float value(const void* p, int at, int fp32) {
-  if (fp32) return __ldg(static_cast<const float*>(p) + at);
-  if constexpr (sizeof(E) == 4) return __ldg(static_cast<const float*>(p) + at);
-  else return static_cast<float>(static_cast<const E*>(p)[at]);
-}
 
 template <typename E, int V>
 __device__ __forceinline__ void unpack(const Pack<E, V>& a, float* x) {
@@ -88,6 +81,35 @@ __device__ __forceinline__ void pack(Pack<E, V>& a, const float* x) {
   } else {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) a.w[i] = mlarp::pack2<E>(x[2 * i], x[2 * i + 1]);
+  }
+}
+
+// V weights from `at` on, in 16-byte loads where `vec` says that they are so aligned.
+template <typename E, int V>
+__device__ __forceinline__ void values(const void* p, int at, int fp32, int vec, float* v) {
+  if (fp32 || sizeof(E) == 4) {
+    const float* f = static_cast<const float*>(p) + at;
+    if (V >= 4 && vec) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(v + i) = __ldg(reinterpret_cast<const float4*>(f + i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __ldg(f + i);
+    }
+  } else {
+    const E* e = static_cast<const E*>(p) + at;
+    Pack<E, V> a;
+    if (V == 1 || vec) {
+      a.load(e);
+      unpack<E, V>(a, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        Pack<E, 1> one;
+        one.load(e + i);
+        unpack<E, 1>(one, v + i);
+      }
+    }
   }
 }
 
@@ -160,25 +182,30 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
   auto coefficients = [&]() {
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
+      float wt[L::kVals], bi[L::kVals];
+#pragma unroll
+      for (int j = 0; j < L::kVals; ++j) {
+        wt[j] = 1.f;
+        bi[j] = 0.f;
+      }
+      if (normed && at.in[i]) {
+        if (w.weight != nullptr) {
+          values<E, V>(w.weight, at.d[i], w.weight_fp32, w.weight_vec, wt);
+          if (kTwo && at.rot[i]) values<E, V>(w.weight, at.d[i] + at.second, w.weight_fp32, w.weight_vec, wt + L::kVals - V);
+        }
+        if (kLayer && w.bias != nullptr) {
+          values<E, V>(w.bias, at.d[i], w.weight_fp32, w.weight_vec, bi);
+          if (kTwo && at.rot[i]) values<E, V>(w.bias, at.d[i] + at.second, w.weight_fp32, w.weight_vec, bi + L::kVals - V);
+        }
+      }
 #pragma unroll
       for (int j = 0; j < L::kPairs; ++j) {
         float2 cs = make_float2(1.f, 0.f);
         if (at.rot[i]) cs = mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale);
-        const int da = at.d[i] + (kTwo ? j : 2 * j), db = kTwo ? da + at.second : da + 1;
-        const bool has_b = kTwo ? at.rot[i] : at.in[i];
-        float wa = 1.f, wb = 1.f;
-        if (normed && w.weight != nullptr) {
-          if (at.in[i]) wa = value<E>(w.weight, da, w.weight_fp32);
-          if (has_b) wb = value<E>(w.weight, db, w.weight_fp32);
-        }
+        const float wa = wt[kTwo ? j : 2 * j], wb = wt[kTwo ? V + j : 2 * j + 1];
         co[i][j] = {wa * cs.x, wb * cs.y, wa * cs.y, wb * cs.x};
         if constexpr (kLayer) {
-          float va = 0.f, vb = 0.f;
-          if (normed && w.bias != nullptr) {
-            if (at.in[i]) va = value<E>(w.bias, da, w.weight_fp32);
-            if (has_b) vb = value<E>(w.bias, db, w.weight_fp32);
-          }
-          const float2 z = mlarp::turn2(va, vb, cs);
+          const float2 z = mlarp::turn2(bi[kTwo ? j : 2 * j], bi[kTwo ? V + j : 2 * j + 1], cs);
           ba[i][j] = z.x;
           bb[i][j] = z.y;
         }
@@ -238,66 +265,61 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
       }
     }
   };
+  // mean and 1 / root from a head's sums
+  auto root = [&](float sum) { return 1.f / sqrtf(fmaf(sum, w.inv_d, w.eps)); };
+  auto group_sum = [&](float v) {
+    for (int o = w.lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
   const int64_t x_step = w.head_rows * w.xh, o_step = w.head_rows * w.oh;
-  constexpr int kUnroll = KU > 1 && V > 1 ? 1 : (kTwo ? 2 : 4);  // heads in flight
-  for (int it = 0; it < w.passes; it += kUnroll) {
-    Pack<E, V> a[kUnroll][KU], b[kUnroll][KU];
-    bool has[kUnroll];
-    float mean[kUnroll], inv[kUnroll];
+  const int heads = live ? min(w.passes, (w.n_heads - h0 + w.head_rows - 1) / w.head_rows) : 0;  // of this group
+  if (w.chunks == 1) {
+    // two heads ahead of the one that is worked on
+    constexpr int kSets = 3;
+    Pack<E, V> a[kSets][KU], b[kSets][KU];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      has[u] = live && it + u < w.passes && h0 + (it + u) * w.head_rows < w.n_heads;
-      mean[u] = 0.f;
-      inv[u] = 1.f;
-      if (w.chunks == 1) at.load(x + u * x_step, has[u], a[u], b[u]);
+    for (int u = 0; u < kSets - 1; ++u, x += x_step) at.load(x, u < heads, a[u], b[u]);
+    if (normed || w.rot_units > 0) coefficients();  // while the loads are on their way
+    for (int it = 0; it < w.passes; it += kSets) {
+#pragma unroll
+      for (int u = 0; u < kSets; ++u, x += x_step, out += o_step) {
+        if (it + u >= w.passes) break;
+        at.load(x, it + u + kSets - 1 < heads, a[(u + kSets - 1) % kSets], b[(u + kSets - 1) % kSets]);
+        float mean = 0.f, inv = 1.f;
+        if (layer) mean = group_sum(part(a[u], b[u], 0.f, false)) * w.inv_d;
+        if (normed) inv = root(group_sum(part(a[u], b[u], mean, true)));
+        finish(a[u], b[u], mean, inv, out, it + u < heads);
+      }
     }
-    if (it == 0 && w.chunks == 1 && (normed || w.rot_units > 0)) coefficients();  // while the loads are on their way
+    return;
+  }
+  // heads of more values than the group holds, chunk by chunk
+  for (int it = 0; it < w.passes; ++it, x += x_step, out += o_step) {
+    Pack<E, V> a[KU], b[KU];
+    float mean = 0.f, inv = 1.f;
     for (int step = layer ? 0 : 1; step < 2 && normed; ++step) {
-      float s[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        s[u] = 0.f;
-        if (w.chunks == 1) {
-          s[u] = part(a[u], b[u], mean[u], step == 1);
-        } else {
-          for (int c = 0; c < w.chunks; ++c) {
-            at.place(w, c * KU * w.lanes, lane);
-            at.load(x + u * x_step, has[u], a[u], b[u]);
-            s[u] += part(a[u], b[u], mean[u], step == 1);
-          }
-        }
+      float sum = 0.f;
+      for (int c = 0; c < w.chunks; ++c) {
+        at.place(w, c * KU * w.lanes, lane);
+        at.load(x, it < heads, a, b);
+        sum += part(a, b, mean, step == 1);
       }
-      for (int o = w.lanes >> 1; o > 0; o >>= 1) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (step == 0) mean[u] = s[u] * w.inv_d;
-        else inv[u] = 1.f / sqrtf(fmaf(s[u], w.inv_d, w.eps));
-      }
+      sum = group_sum(sum);
+      if (step == 0) mean = sum * w.inv_d;
+      else inv = root(sum);
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (w.chunks == 1) {
-        finish(a[u], b[u], mean[u], inv[u], out + u * o_step, has[u]);
-      } else {
-        for (int c = 0; c < w.chunks; ++c) {  // in place, a lane has read and written its own values alone
-          at.place(w, c * KU * w.lanes, lane);
-          coefficients();
-          at.load(x + u * x_step, has[u], a[u], b[u]);
-          finish(a[u], b[u], mean[u], inv[u], out + u * o_step, has[u]);
-        }
-      }
+    for (int c = 0; c < w.chunks; ++c) {  // in place, a lane has read and written its own values alone
+      at.place(w, c * KU * w.lanes, lane);
+      coefficients();
+      at.load(x, it < heads, a, b);
+      finish(a, b, mean, inv, out, it < heads);
     }
-    x += kUnroll * x_step;
-    out += kUnroll * o_step;
   }
 }
 
 // One block works on one of the tensors.
 template <typename E, int V, int KU, bool kLayer>
-__global__ void __launch_bounds__(kThreads, kLayer || KU > 1 ? 2 : 3) head_prep_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kLayer ? 4 : 5) head_prep_kernel(const __grid_constant__ Params p) {
   int block = static_cast<int>(blockIdx.x), i = 0;
   while (i < 2 && block >= p.t[i].blocks) block -= p.t[i++].blocks;
   const Tensor& w = p.t[i];
@@ -419,6 +441,7 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
   w->inv_d = 1.f / static_cast<float>(j.head_dim);
   w->kind = j.norm.kind;
   w->weight_fp32 = j.norm.fp32;
+  w->weight_vec = j.vec && aligned(j.norm.weight, 16) && aligned(j.norm.bias, 16) ? 1 : 0;
   w->n_heads = j.n_heads;
   w->rot_off = j.rot_off;
   w->head_dim = j.head_dim;
@@ -434,11 +457,11 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
   const int rows = kThreads / w->lanes;
   w->tok_rows = std::min(rows, T);
   w->head_rows = std::min(rows / w->tok_rows, j.n_heads);
-  // several heads per group once there is a block for every SM four times over
+  // several heads per group once there are blocks for all places of the GPU
   const int64_t toks = (static_cast<int64_t>(T) + w->tok_rows - 1) / w->tok_rows;
   const int turns = (j.n_heads + w->head_rows - 1) / w->head_rows;
   const int most = std::min(turns, kMaxPasses);
-  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, toks * turns / (4 * 152))));
+  w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (toks * turns + 607) / 608)));
   w->head_blocks = (turns + w->passes - 1) / w->passes;
   w->passes = (turns + w->head_blocks - 1) / w->head_blocks;  // even shares
   const int64_t blocks = toks * w->head_blocks;
