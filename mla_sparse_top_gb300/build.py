@@ -13,7 +13,7 @@ SOURCES = [os.path.join(CSRC, "mla_sparse_fwd.cu"), os.path.join(CSRC, "lightnin
            os.path.join(CSRC, "tree_attn.cu"), os.path.join(CSRC, "head_prep.cu"),
            os.path.join(CSRC, "prompt_attn.cu"), os.path.join(CSRC, "paged_attn.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "rope_angles.cuh"), os.path.join(CSRC, "areas.h"),
-                  os.path.join(CSRC, "heads.h"), os.path.join(ROOT, "include", "mla_heads.h"),
+                  os.path.join(CSRC, "heads.h"), os.path.join(CSRC, "heads_device.cuh"), os.path.join(ROOT, "include", "mla_heads.h"),
                   os.path.join(ROOT, "include", "mla_sparse.h"),
                   os.path.join(ROOT, "include", "mla_indexer.h"), os.path.join(ROOT, "include", "mla_cache.h"),
                   os.path.join(ROOT, "include", "mla_prolog.h"), os.path.join(ROOT, "include", "mla_pages.h"),

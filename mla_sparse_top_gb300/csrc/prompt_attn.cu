@@ -24,26 +24,18 @@
 // the GPU, the key tiles of an item are cut into parts, whose states go to the
 // workspace and are joined by a second launch.  What is cut follows from the
 // lengths alone, so results do not depend on timing.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <algorithm>
 #include <mutex>
 
 #include "heads.h"
-#include "ptx.cuh"
-
-namespace mlasp {
-unsigned long long host_wait_limit_ns();
-}
+#include "heads_device.cuh"
 
 namespace mlaheads {
-
-using namespace mlasp;
 
 __device__ unsigned int g_prompt_status = 0;
 
@@ -290,24 +282,6 @@ struct Ctx {
   __device__ uint32_t bar(int i) const { return sb + kOffBars + 8 * i; }
   __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
 };
-__device__ __forceinline__ bool warp_wait(const Ctx& c, int i, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait<false>(c.bar(i), parity, c.abort, c.wait_ns));
-}
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-  return ok != 0;
-}
-__device__ __forceinline__ void tma_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
-  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-               :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-               :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
-}
-
 struct Ring {
   int slot = 0;
   uint32_t phase = 0;
@@ -447,22 +421,6 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps) {
       page = ahead;
     }
   }
-}
-
-// NaN and infinities of a pair of 16-bit values become zero.
-template <typename E>
-__device__ __forceinline__ uint32_t finite2(uint32_t w) {
-  constexpr uint32_t kExp = __is_same(E, __half) ? 0x7C00u : 0x7F80u;
-  if ((w & kExp) == kExp) w &= 0xFFFF0000u;
-  if ((w & kExp << 16) == kExp << 16) w &= 0x0000FFFFu;
-  return w;
-}
-template <typename E>
-__device__ __forceinline__ bool finite4(uint4 v) {
-  constexpr uint32_t kExp = __is_same(E, __half) ? 0x7C007C00u : 0x7F807F80u;
-  constexpr uint32_t kOne = __is_same(E, __half) ? 0x04000400u : 0x00800080u;  // carries out of a full exponent alone
-  const uint32_t c = ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
-  return (c & 0x80008000u) == 0;
 }
 
 template <typename E>
@@ -615,35 +573,6 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
   volatile uint32_t never = 0;
   mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > 500000000ull ? c.wait_ns : 500000000ull);
   __syncwarp();
-}
-
-// fp32 pairs (one instruction for two lanes of arithmetic).
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-template <typename E>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  uint32_t r;
-  if constexpr (__is_same(E, __half)) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // The NaN of values that are not finite, which mending took from a row: keys [lo,
@@ -958,21 +887,6 @@ int parts_of(const Problem& p) {
 int part_floats(const Problem& p) { return 2 * (128 * p.d_v + 256); }
 size_t lists_bytes(const Problem& p) { return (sizeof(Head) + (4 * static_cast<size_t>(p.B) + 2) * sizeof(int) + 255) & ~size_t(255); }
 
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename E>
 mla_status prepare_kernel() {
   HEADS_CUDA(cudaFuncSetAttribute(prompt_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes), "kernel set-up");
@@ -990,38 +904,15 @@ mla_status init_device(int* sms) {
   std::lock_guard<std::mutex> guard(g_lock);
   Device& d = g_dev[dev];
   if (!d.ready) {
-    if (g_encode == nullptr) {
-      cudaDriverEntryPointQueryResult q;
-      void* fn = nullptr;
-      HEADS_CUDA(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q), "looking up cuTensorMapEncodeTiled");
-      if (fn == nullptr || q != cudaDriverEntryPointSuccess) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    }
+    mla_status st = tensor_map_encoder(&g_encode);
+    if (st != MLA_OK) return st;
     HEADS_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev), "device attributes");
-    mla_status st = prepare_kernel<__nv_bfloat16>();
+    st = prepare_kernel<__nv_bfloat16>();
     if (st == MLA_OK) st = prepare_kernel<__half>();
     if (st != MLA_OK) return st;
     d.ready = true;
   }
   *sms = d.sms;
-  return MLA_OK;
-}
-
-// A tensor of 16-bit values, the innermost dimension adjacent; strides in elements, of dimensions 1 ...
-mla_status tmap(CUtensorMap* m, int dtype, const void* base, int rank, const int64_t* size, const int64_t* stride, const int* box, const char* what) {
-  cuuint64_t dim[4], st[3];
-  cuuint32_t bx[4], es[4];
-  for (int i = 0; i < rank; ++i) {
-    dim[i] = static_cast<cuuint64_t>(size[i]);
-    bx[i] = static_cast<cuuint32_t>(box[i]);
-    es[i] = 1;
-    // a dimension of one place is never stepped over: any legal stride will do
-    if (i > 0) st[i - 1] = size[i] > 1 ? static_cast<cuuint64_t>(stride[i - 1]) * 2 : ((static_cast<cuuint64_t>(size[0]) * 2 + 15) & ~cuuint64_t(15));
-  }
-  const CUresult r = g_encode(m, dtype == MLA_ROPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank),
-                              const_cast<void*>(base), dim, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "tensor map of %s: error %d", what, static_cast<int>(r));
   return MLA_OK;
 }
 
@@ -1059,7 +950,7 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
   {
     const int64_t size[3] = {x.d_qk, x.n_q, x.T}, stride[2] = {x.q.head_stride, x.q.token_stride};
     const int box[3] = {64, p.G, p.tpt};
-    const mla_status ms = tmap(&maps.q, x.dtype, x.q.data, 3, size, stride, box, "q");
+    const mla_status ms = tmap(g_encode, &maps.q, x.dtype, x.q.data, 3, size, stride, box, "q");
     if (ms != MLA_OK) return ms;
   }
   for (int i = 0; i < 2; ++i) {
@@ -1069,7 +960,7 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
     const int64_t stride[3] = {c.row_stride, c.head_stride, c.block_stride};
     const int box[4] = {64, i == 1 && p.vc == 2 ? 64 : 128, 1, 1};
     CUtensorMap* map = i == 0 ? &maps.k : &maps.v;
-    const mla_status ms = none ? MLA_OK : tmap(map, x.dtype, c.data, 4, size, stride, box, i == 0 ? "k" : "v");
+    const mla_status ms = none ? MLA_OK : tmap(g_encode, map, x.dtype, c.data, 4, size, stride, box, i == 0 ? "k" : "v");
     if (ms != MLA_OK) return ms;
     if (none) *map = maps.q;
   }
