@@ -122,9 +122,11 @@ inline mla_status tmap(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m,
     // a dimension of one place is never stepped over: any legal stride will do
     if (i > 0) st[i - 1] = size[i] > 1 ? static_cast<cuuint64_t>(stride[i - 1]) * 2 : ((static_cast<cuuint64_t>(size[0]) * 2 + 15) & ~cuuint64_t(15));
   }
+  // L2 fetches whole lines of a run that lies together: a head's values of one token, or rows behind one another
+  const bool wide = size[0] * 2 % 256 == 0 || stride[0] == size[0];
   const CUresult r = encode(m, dtype == MLA_ROPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(rank),
                               const_cast<void*>(base), dim, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              wide ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "tensor map of %s: error %d", what, static_cast<int>(r));
   return MLA_OK;
 }

@@ -2,21 +2,21 @@
 // (sm_103a); formulas in mla_heads.h.
 //
 // The keys and values of a sequence are read once and meet few rows (the S1 new
-// tokens of the G heads that share them), so memory binds.  One warp of a CTA
-// streams units of 64 keys, key and value together, by TMA through a ring that
-// fills shared memory, on and on across sequences and heads; two groups of four
-// warps take units in turn.  The warps of a group split a unit: by 16 rows, and
-// by keys where there are fewer than 64 rows.  Each keeps its rows' running
-// maximum, sum and output in registers, as accumulators of mma.sync (m16n8k16:
-// with 16 rows the 128-row tiles of tcgen05 would be an eighth full, and a
-// unit's products take a third of the time that its bytes take to arrive); they
-// meet in shared memory when a sequence's head is through.
+// tokens of the G heads that share them), so memory binds.  A CTA holds eight
+// pipelines of two warps: one streams units of 16 keys, keys and values together,
+// by TMA into slots of shared memory that no other pipeline touches, the other
+// takes 16 rows through them with the running maximum, sum and output in
+// registers, as accumulators of mma.sync (m16n8k16: the 128-row tiles of tcgen05
+// would be an eighth full, and the products of a unit take less time than its
+// bytes take to arrive).  No pipeline waits for another, and a head that one has
+// through goes from its registers to memory.  More than 16 rows go to two or four
+// pipelines side by side, which read the same units, from L2 but for the first.
 //
-// The units of all sequences and heads are one stream of which every CTA takes
-// an equal share.  A head cut between CTAs leaves partial states in the
-// workspace, and a second launch joins them.  Which CTA takes what follows from
-// the lengths alone, so results do not depend on timing.  Calls of more than 64
-// rows to a key head go through the 128-row tiles of prompts.
+// The units of all sequences and heads are one stream of which every pipeline (or
+// group of them side by side) takes an equal share.  A head cut between them
+// leaves partial states in the workspace, and a second launch joins them.  Who
+// takes what follows from the lengths alone, so results do not depend on timing.
+// Calls of more than 64 rows to a key head go through the 128-row tiles of prompts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,73 +33,61 @@ namespace paged {
 
 __device__ unsigned int g_paged_status = 0;
 
-constexpr int kUnit = 64;        // keys
-constexpr int kConsumers = 8;    // warps
-constexpr int kGroups = 2;
-constexpr int kLoadWarp = 8;
-constexpr int kThreads = 288;
-constexpr int kChunk = 8192;     // 64 rows of 128 bytes
-constexpr int kMaxStages = 16;
+constexpr int kUnit = 32;        // keys
+constexpr int kWarps = 8;        // that compute, and as many that load
+constexpr int kThreads = 2 * 32 * kWarps;
+constexpr int kRegs = 128, kConsumerRegs = 192, kLoadRegs = 64;
+static_assert(32 * kWarps * (kConsumerRegs + kLoadRegs) <= kThreads * kRegs, "register budget");
+constexpr int kChunk = kUnit * 128;  // a unit's rows of 128 bytes
+constexpr int kMaxSlots = 48;    // of a CTA
 constexpr int kMaxRows = 64;
-constexpr int kCols = 32;        // columns that the warps join at a time
-constexpr int kPitch = kCols + 4;
+constexpr int kLeastSlots = 2;   // of a pipeline
 
-constexpr int kFull = 0;                      // [kMaxStages]
-constexpr int kEmpty = kFull + kMaxStages;    // [kMaxStages]
-constexpr int kSegFull = kEmpty + kMaxStages; // [2] a segment's Q has landed, its description is written
-constexpr int kSegEmpty = kSegFull + 2;       // [2]
-constexpr int kJoin = kSegEmpty + 2;          // the consumers have come this far
-constexpr int kNumBars = kJoin + 1;
-
-// A run of units of one sequence and key head.
-struct Segment {
-  int b, hk;         // b < 0: no more
-  int u0, u1, units; // units [u0, u1) of `units`
-  int n, len, pos;   // query tokens, keys within the table, position of token 0
-};
-
-constexpr int kOffJoin = 0;                                              // float [kConsumers][16][kPitch]
-constexpr int kOffMl = kOffJoin + kConsumers * 16 * kPitch * 4;          // float2 [kConsumers][16]
-constexpr int kOffScan = kOffMl + kConsumers * 16 * 8;                   // int64 [kThreads / 32]
-constexpr int kOffWalk = kOffScan + kThreads / 32 * 8;                   // int64 [2]
-constexpr int kOffSeg = kOffWalk + 16;                                   // Segment [2]
-constexpr int kOffGood = kOffSeg + 2 * static_cast<int>(sizeof(Segment));  // int [kMaxStages]
-constexpr int kOffBars = kOffGood + kMaxStages * 4;
-constexpr int kOffAbort = kOffBars + 8 * kNumBars;
-constexpr int kOffMended = kOffAbort + 4;
-constexpr int kOffTiles = (kOffMended + 4 + 1023) & ~1023;  // Q twice, then the ring
+constexpr int kBars = kMaxSlots;
+constexpr int kOffScan = 0;                          // int64 [kThreads / 32]
+constexpr int kOffWalk = kOffScan + kThreads / 32 * 8;  // int64 [kWarps][2]: a share's first sequence and its stream position
+constexpr int kOffBars = kOffWalk + kWarps * 16;     // [kBars] the slot's bytes have landed, [kBars] they have been read
+constexpr int kOffGood = kOffBars + 2 * 8 * kBars;   // int [kBars] the slot's page exists
+constexpr int kOffAbort = kOffGood + 4 * kBars;
+constexpr int kOffMended = kOffAbort + 4;            // a value that not every token sees was NaN or infinite
+constexpr int kOffSlots = 2048;
+static_assert(kOffMended + 4 <= kOffSlots, "shared memory");
 constexpr int kSmemMost = 232448;
-static_assert(kOffBars % 8 == 0 && kOffWalk % 8 == 0, "alignment");
 
 struct Params {
   Problem x;
-  float* parts;    // [CTAs][2][part_floats]
-  int4* records;   // [CTAs] the head whose first part is the CTA's last: sequence, key head, parts behind it
+  float* parts;    // [groups][tiles][2][part_floats]
+  int4* records;   // [groups] the head whose first part is the group's last: sequence, key head, parts behind it
   int part_floats;
   int G, rows;     // heads to a key head, rows of a key head
+  int tiles;       // 16-row tiles of them
   int kc, vc;      // 64-column chunks of keys and values
-  int ks, vs;      // 16-column steps
-  int stages, stage_bytes, q_bytes;
-  int ctas;
+  int ks;          // 16-column steps of keys
+  int slots, unit_bytes;  // of a pipeline
+  int pipes;       // pipelines of a CTA, each of a load warp and `tiles` others
+  int groups;      // pipelines of the GPU that take part
   unsigned long long wait_ns;
 };
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap k, v;
 };
 
 struct Seq {
-  int n, len, pos, units;
+  int n, len, pos, units;  // query tokens, keys within the table, position of token 0
   bool cut_table;
 };
-__device__ __forceinline__ Seq load_seq(const Params& p, int b) {
+__device__ __forceinline__ Seq make_seq(const Params& p, int act, int q_len) {
   Seq s;
-  const int act = max(0, __ldg(p.x.act_seqs + b));
-  s.n = p.x.q_lens != nullptr ? min(p.x.S1, max(0, __ldg(p.x.q_lens + b))) : p.x.S1;
+  act = max(0, act);
+  s.n = min(p.x.S1, max(0, q_len));
   s.len = min(act, p.x.W * kPage);
   s.cut_table = s.len < act && s.n > 0;
   s.pos = act - s.n;
   s.units = s.n > 0 ? max(1, (s.len + kUnit - 1) / kUnit) : 1;  // rows that see nothing are written too
   return s;
+}
+__device__ __forceinline__ Seq load_seq(const Params& p, int b) {
+  return make_seq(p, __ldg(p.x.act_seqs + b), p.x.q_lens != nullptr ? __ldg(p.x.q_lens + b) : p.x.S1);
 }
 
 struct Ctx {
@@ -111,15 +99,17 @@ struct Ctx {
   __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
 };
 
-// Units of a CTA at least: fewer parts to join where there is little to read.
+// Units of a share at least: fewer parts to join where there is little to read.
 constexpr int kMinUnits = 2;
 
-__device__ __forceinline__ int ctas_of(const Params& p, int64_t total) {
-  return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.ctas), total / kMinUnits)));
+__device__ __forceinline__ int groups_of(const Params& p, int64_t total) {
+  return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.groups), total / kMinUnits)));
 }
+// A pipeline's number: neighbours in the stream lie in different CTAs, so that few of them use many SMs.
+__device__ __forceinline__ int group_id(int pipe) { return pipe * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); }
 
-// Where the CTA's share of the stream begins; false when it has none.
-__device__ bool start(const Params& p, const Ctx& c, int& b0, int64_t& base, int64_t& from, int64_t& to, int64_t& total, int& ctas) {
+// Finds where the shares of the CTA's pipelines begin; returns the length of the stream.
+__device__ int64_t find_shares(const Params& p, const Ctx& c) {
   int64_t* part = reinterpret_cast<int64_t*>(c.smem + kOffScan);
   int64_t* at = reinterpret_cast<int64_t*>(c.smem + kOffWalk);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.x.B;
@@ -143,7 +133,7 @@ __device__ bool start(const Params& p, const Ctx& c, int& b0, int64_t& base, int
     }
     return before + x - v;
   };
-  int64_t mine = 0, len = 0, pre = 0;
+  int64_t mine = 0, len = 0, total;
   bool cut = false;
   for (int k = 0; k < chunks; ++k) {
     const int b = k * kThreads + tid;
@@ -156,12 +146,8 @@ __device__ bool start(const Params& p, const Ctx& c, int& b0, int64_t& base, int
     mine += len;
   }
   if (cut) atomicOr(&g_paged_status, MLA_DEVICE_BAD_BLOCK);
-  pre = scan(mine, total);
-  ctas = ctas_of(p, total);
-  const int cid = blockIdx.x;
-  if (cid >= ctas) return false;
-  from = cid * total / ctas;
-  to = (cid + 1) * total / ctas;
+  int64_t pre = scan(mine, total);
+  const int groups = groups_of(p, total);
   int64_t carry = 0;
   for (int k = 0; k < chunks; ++k) {
     const int b = k * kThreads + tid;
@@ -170,92 +156,54 @@ __device__ bool start(const Params& p, const Ctx& c, int& b0, int64_t& base, int
       len = b < B ? static_cast<int64_t>(load_seq(p, b).units) * p.x.n_kv : 0;
       pre = carry + scan(len, sum);
     }
-    if (b < B && from >= pre && from < pre + len) {
-      at[0] = b;
-      at[1] = pre;
+    if (b < B) {
+      for (int w = 0; w < p.pipes; ++w) {
+        const int g = group_id(w);
+        const int64_t from = g < groups ? g * total / groups : -1;
+        if (from >= pre && from < pre + len) {
+          at[2 * w] = b;
+          at[2 * w + 1] = pre;
+        }
+      }
     }
     carry += sum;
-    if (carry > from) break;
   }
   __syncthreads();
-  b0 = static_cast<int>(at[0]);
-  base = at[1];
-  return from < to;
+  return total;
 }
 
-__device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int b, int64_t base, int64_t from, int64_t to) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t ring = c.sb + kOffTiles + 2 * p.q_bytes;
-  int stage = 0;
-  uint32_t phase = 1, segs = 0;
-  bool bad = false;
-  auto publish = [&](const Segment& s) {
-    const int k = segs & 1;
-    if (!warp_wait(c, kSegEmpty + k, ((segs >> 1) & 1) ^ 1)) return false;
-    if (lane == 0) {
-      reinterpret_cast<Segment*>(c.smem + kOffSeg)[k] = s;
-      if (s.b >= 0) {
-        mbar_arrive_expect_tx(c.bar(kSegFull + k), p.kc * p.rows * 128);
-        for (int i = 0; i < p.kc; ++i)
-          tma_3d(c.sb + kOffTiles + k * p.q_bytes + i * (p.q_bytes / p.kc), &maps.q, 64 * i, s.hk * p.G, s.b * p.x.S1, c.bar(kSegFull + k));
-      } else {
-        mbar_arrive(c.bar(kSegFull + k));
-      }
-    }
-    __syncwarp();
-    ++segs;
-    return true;
-  };
-  while (from < to) {
-    const Seq q = load_seq(p, b);
-    const int64_t len = static_cast<int64_t>(q.units) * p.x.n_kv;
-    if (from - base >= len) {
-      base += len;
-      ++b;
-      continue;
-    }
-    Segment s;
-    s.b = b;
-    s.hk = static_cast<int>((from - base) / q.units);
-    s.units = q.units;
-    s.u0 = static_cast<int>(from - base - static_cast<int64_t>(s.hk) * q.units);
-    s.u1 = static_cast<int>(min(static_cast<int64_t>(q.units), s.u0 + to - from));
-    s.n = q.n;
-    s.len = q.len;
-    s.pos = q.pos;
-    if (!publish(s)) return;
-    int ids = -1;
-    for (int u = s.u0; u < s.u1; ++u) {
-      const int page = u >> 1;
-      if (u == s.u0 || ((u & 1) == 0 && ((page - (s.u0 >> 1)) & 31) == 0)) {  // the next 32 pages
-        const int at = page + lane;
-        ids = at < p.x.W && at * kPage < q.len ? __ldg(p.x.block_table + static_cast<int64_t>(b) * p.x.W + at) : -1;
-      }
-      const int id = __shfl_sync(0xffffffffu, ids, (page - (s.u0 >> 1)) & 31);
-      const bool good = id >= 0 && id < p.x.num_blocks;
-      bad = bad || (!good && u * kUnit < q.len && q.n > 0);
-      if (!warp_wait(c, kEmpty + stage, phase)) return;
-      if (lane == 0) {
-        reinterpret_cast<volatile int*>(c.smem + kOffGood)[stage] = good ? 1 : 0;
-        const uint32_t bar = c.bar(kFull + stage), dst = ring + stage * p.stage_bytes;
-        const int row = (u & 1) * kUnit, block = good ? id : p.x.num_blocks;  // beyond the pool: zeros
-        mbar_arrive_expect_tx(bar, p.stage_bytes);
-        for (int i = 0; i < p.kc; ++i) tma_4d(dst + i * kChunk, &maps.k, 64 * i, row, s.hk, block, bar);
-        for (int i = 0; i < p.vc; ++i) tma_4d(dst + (p.kc + i) * kChunk, &maps.v, 64 * i, row, s.hk, block, bar);
-      }
-      __syncwarp();
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
-    }
-    from += s.u1 - s.u0;
+// A share of the stream, unit by unit.  Lane i keeps the lengths of sequence b0 + i.
+struct Walk {
+  int b, b0, act, q_len;
+  int hk, u;       // the unit is u of sequence b's key head hk
+  int64_t left;    // units that follow, this one among them
+  Seq s;
+  __device__ __forceinline__ void load_lengths(const Params& p, int lane) {
+    const int i = min(b0 + lane, p.x.B - 1);
+    act = __ldg(p.x.act_seqs + i);
+    q_len = p.x.q_lens != nullptr ? __ldg(p.x.q_lens + i) : p.x.S1;
   }
-  Segment none = {};
-  none.b = -1;
-  publish(none);
-  if (bad && lane == 0) atomicOr(&g_paged_status, MLA_DEVICE_BAD_BLOCK);
-}
+  __device__ __forceinline__ void begin(const Params& p, int lane, int b_, int64_t off, int64_t count) {
+    b = b0 = b_;
+    left = count;
+    load_lengths(p, lane);
+    s = make_seq(p, uniform(act), uniform(q_len));
+    hk = static_cast<int>(off / s.units);
+    u = static_cast<int>(off - static_cast<int64_t>(hk) * s.units);
+  }
+  // the head's first unit, behind the current head
+  __device__ __forceinline__ void next_head(const Params& p, int lane) {
+    u = 0;
+    if (++hk < p.x.n_kv) return;
+    hk = 0;
+    if (++b >= p.x.B) return;  // the end of the stream
+    if (b - b0 == 32) {
+      b0 = b;
+      load_lengths(p, lane);
+    }
+    s = make_seq(p, __shfl_sync(0xffffffffu, act, b - b0), __shfl_sync(0xffffffffu, q_len, b - b0));
+  }
+};
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -275,90 +223,179 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Whether column `col` of a value that a row sees, key by key in [lo, hi), is not finite.
+// Whether column `col` of a value, key by key in [lo, hi), is not finite.
 template <typename E>
-__device__ __noinline__ bool infinite_column(const Params& p, const Segment& s, int lo, int hi, int col) {
+__device__ __noinline__ bool infinite_column(const Params& p, int b, int hk, int lo, int hi, int col) {
   constexpr uint32_t kExp = __is_same(E, __half) ? 0x7C00u : 0x7F80u;
   for (int key = lo; key < hi; ++key) {
-    const int id = __ldg(p.x.block_table + static_cast<int64_t>(s.b) * p.x.W + key / kPage);
+    const int id = __ldg(p.x.block_table + static_cast<int64_t>(b) * p.x.W + key / kPage);
     if (id < 0 || id >= p.x.num_blocks) continue;
     const uint16_t v = __ldg(static_cast<const uint16_t*>(p.x.v.data) + id * p.x.v.block_stride + (key % kPage) * p.x.v.row_stride +
-                             s.hk * p.x.v.head_stride + col);
+                             hk * p.x.v.head_stride + col);
     if ((v & kExp) == kExp) return true;
   }
   return false;
 }
 
-// kTiles: 16-row tiles of a key head's rows, 1, 2 or 4.  kV: 8-column tiles of the values, 8 or 16.
-template <typename E, int kTiles, int kV>
-__device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, int ctas, int64_t total) {
-  constexpr int kSplits = 4 / kTiles;        // warps of a group that share a row tile
-  constexpr int kKeys = kUnit / kSplits;     // keys of a warp
-  constexpr int kN = kKeys / 8;              // 8-key tiles of a warp
-  constexpr int kStates = kGroups * kSplits; // states of a row
-  const int group = warp >> 2, tile = (warp & 3) % kTiles, split = (warp & 3) / kTiles;
+// Rows of a unit's values that not every token sees, from row `first` on: those
+// behind the sequence (from row `live` on) become zero, the others lose their NaN
+// and infinities, which a weight of 0 would carry into the product.  Warps that
+// share a unit write the same; the flag is up before a value is gone.
+template <typename E>
+__device__ __noinline__ void mend_values(const Ctx& c, uint32_t vs, int chunks, int first, int live, int lane) {
+  const int units = 8 * chunks;
+  auto at = [&](int i) {
+    const int r = i / units, col = i - r * units;
+    return vs + (col >> 3) * kChunk + r * 128 + (((col & 7) ^ (r & 7)) << 4);
+  };
+  auto load = [&](int i) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at(i)));
+    return v;
+  };
+  auto store = [&](int i, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at(i)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  };
+  const int begin = max(0, first) * units, middle = max(max(0, first), min(live, kUnit)) * units;
+  bool good = true;
+  for (int i = begin + lane; i < middle; i += 32) good = good && finite4<E>(load(i));
+  if (__any_sync(0xffffffffu, !good)) {
+    *c.mended() = 1u;
+    __threadfence_block();
+    for (int i = begin + lane; i < middle; i += 32) {
+      const uint4 v = load(i);
+      store(i, make_uint4(finite2<E>(v.x), finite2<E>(v.y), finite2<E>(v.z), finite2<E>(v.w)));
+    }
+  }
+  for (int i = middle + lane; i < kUnit * units; i += 32) store(i, make_uint4(0, 0, 0, 0));
+  fence_proxy_async_smem();  // before the slot's next load
+  __syncwarp();
+}
+
+// The share of a pipeline; false: it has none.
+struct Share {
+  int g, groups, b;
+  int64_t from, count, off;  // of the stream, of sequence b
+};
+__device__ __forceinline__ bool share_of(const Params& p, const Ctx& c, int pipe, int64_t total, Share& s) {
+  s.g = group_id(pipe);
+  s.groups = groups_of(p, total);
+  if (pipe >= p.pipes || s.g >= s.groups) return false;
+  s.from = s.g * total / s.groups;
+  s.count = (s.g + 1) * total / s.groups - s.from;
+  const int64_t* at = reinterpret_cast<const int64_t*>(c.smem + kOffWalk) + 2 * pipe;
+  s.b = static_cast<int>(at[0]);
+  s.off = s.from - at[1];
+  return true;
+}
+
+__device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int pipe, int lane, int64_t total) {
+  Share sh;
+  if (!share_of(p, c, pipe, total, sh)) return;
+  const int slot0 = pipe * p.slots;
+  const uint32_t slots = c.sb + kOffSlots + slot0 * p.unit_bytes;
+  volatile int* good_of = reinterpret_cast<volatile int*>(c.smem + kOffGood) + slot0;
+  Walk w;
+  w.begin(p, lane, sh.b, sh.off, sh.count);
+  int ids = -1, slot = 0;
+  uint32_t phase = 1;
+  bool bad = false;
+  while (w.left > 0) {
+    const int end = static_cast<int>(min(static_cast<int64_t>(w.s.units), w.u + w.left));
+    w.left -= end - w.u;
+    const int page0 = w.u / (kPage / kUnit);
+    for (int u = w.u; u < end; ++u) {
+      const int page = u / (kPage / kUnit) - page0;
+      if (u == w.u || (page % 32 == 0 && u % (kPage / kUnit) == 0)) {  // the next 32 pages, one to a lane
+        const int i = page0 + page + lane;
+        ids = i < p.x.W && i * kPage < w.s.len ? __ldg(p.x.block_table + static_cast<int64_t>(w.b) * p.x.W + i) : -1;
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, page % 32);
+      const bool good = id >= 0 && id < p.x.num_blocks;
+      bad = bad || (!good && u * kUnit < w.s.len && w.s.n > 0);
+      const int bar = slot0 + slot;
+      if (!warp_wait(c, kBars + bar, phase)) return;
+      if (elect_one()) {
+        const uint32_t full = c.bar(bar), dst = slots + slot * p.unit_bytes;
+        const int row = u * kUnit % kPage, block = good ? id : p.x.num_blocks;  // beyond the pool: zeros
+        good_of[slot] = good ? 1 : 0;
+        mbar_arrive_expect_tx(full, p.unit_bytes);
+        for (int i = 0; i < p.kc; ++i) tma_4d(dst + i * kChunk, &maps.k, 64 * i, row, w.hk, block, full);
+        for (int i = 0; i < p.vc; ++i) tma_4d(dst + (p.kc + i) * kChunk, &maps.v, 64 * i, row, w.hk, block, full);
+      }
+      __syncwarp();
+      if (++slot == p.slots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+    w.next_head(p, lane);
+  }
+  if (bad && lane == 0) atomicOr(&g_paged_status, MLA_DEVICE_BAD_BLOCK);
+}
+
+// kS: 16-column steps of keys, 4, 8 or 12.  kV: 8-column tiles of values, 8 or 16.
+template <typename E, int kS, int kV>
+__device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, int64_t total) {
+  const int pipe = warp / p.tiles, tile = warp % p.tiles;
+  Share sh;
+  if (!share_of(p, c, pipe, total, sh)) return;
   const int quad = lane & 3, row0 = lane >> 2;  // the thread's rows: row0 and row0 + 8 of the tile
+  const int rows = min(16, p.rows - tile * 16);
   const float scale = p.x.scale_log2;
   const bool raw = scale > 0.f;
   const float mul = raw ? scale : 1.f;
-  const uint32_t ring = c.sb + kOffTiles + 2 * p.q_bytes;
-  float* join = reinterpret_cast<float*>(c.smem + kOffJoin);
-  float2* ml = reinterpret_cast<float2*>(c.smem + kOffMl);
-  uint32_t unit_count = 0, joins = 0;  // of the CTA
-  auto meet = [&]() {  // of the consumers; bounded like every wait
-    __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(kJoin));
-    return warp_wait(c, kJoin, joins++ & 1);
-  };
-  int stage = 0;
+  const int slot0 = pipe * p.slots;
+  const uint32_t slots = c.sb + kOffSlots + slot0 * p.unit_bytes;
+  const volatile int* good_of = reinterpret_cast<const volatile int*>(c.smem + kOffGood) + slot0;
+
+  // ---- heads of the share
+  Walk w;
+  w.begin(p, lane, sh.b, sh.off, sh.count);
+  int slot = 0;
   uint32_t phase = 0;
-  for (uint32_t segs = 0;; ++segs) {
-    const int k2 = segs & 1;
-    if (!warp_wait(c, kSegFull + k2, (segs >> 1) & 1)) return;
-    const Segment s = reinterpret_cast<const Segment*>(c.smem + kOffSeg)[k2];
-    if (s.b < 0) return;
-    int vis[2];
+  while (w.left > 0) {
+    const Seq s = w.s;
+    const int b = w.b, hk = w.hk, u0 = w.u, u1 = static_cast<int>(min(static_cast<int64_t>(s.units), u0 + w.left));
+    int vis[2], tok[2];
+    uint32_t q[kS][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int tok = (tile * 16 + row0 + 8 * i) / p.G;
-      vis[i] = tile * 16 + row0 + 8 * i < p.rows && tok < s.n ? min(s.len, max(0, s.pos + tok + 1)) : 0;
+      const int r = tile * 16 + row0 + 8 * i;
+      tok[i] = r / p.G;
+      const bool live = r < p.rows && tok[i] < s.n;
+      vis[i] = live ? min(s.len, max(0, s.pos + tok[i] + 1)) : 0;
+      const uint16_t* src = static_cast<const uint16_t*>(p.x.q.data) + (static_cast<int64_t>(b) * p.x.S1 + tok[i]) * p.x.q.token_stride +
+                            (hk * p.G + r - tok[i] * p.G) * p.x.q.head_stride + 2 * quad;
+#pragma unroll
+      for (int k = 0; k < kS; ++k) {
+        q[k][i] = live && 16 * k < p.x.d_qk ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k)) : 0u;
+        q[k][i + 2] = live && 16 * k + 8 < p.x.d_qk ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8)) : 0u;
+      }
     }
     const int lo = min(s.len, max(0, s.pos + 1));  // keys that every token sees
-    const uint32_t qs = c.sb + kOffTiles + k2 * p.q_bytes;
     float o[kV][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < kV; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    for (int u = s.u0; u < s.u1; ++u, ++unit_count) {
-      const int at_stage = stage;
-      const uint32_t at_phase = phase;
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1;
-      }
-      if ((unit_count & 1) != static_cast<uint32_t>(group)) continue;
-      if (!warp_wait(c, kFull + at_stage, at_phase)) return;
-      const uint32_t ks = ring + at_stage * p.stage_bytes, vs = ks + p.kc * kChunk;
-      const bool good = reinterpret_cast<volatile int*>(c.smem + kOffGood)[at_stage] != 0;
-      const int key0 = split * kKeys;            // within the unit
-      const int first = u * kUnit + key0;        // key of column 0
-      const bool edge = !good || first + kKeys > lo;
+    for (int u = u0; u < u1; ++u) {
+      if (!warp_wait(c, slot0 + slot, phase)) return;
+      const uint32_t ks = slots + slot * p.unit_bytes, vs = ks + p.kc * kChunk;
+      const bool good = good_of[slot] != 0;
+      const int first = u * kUnit;  // key of column 0
+      constexpr int kN = kUnit / 8;
       float z[kN][4];
 #pragma unroll
       for (int n = 0; n < kN; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
-      // scores: rows of Q against rows of K, 16 values at a time
-      const int q_row = tile * 16 + (lane & 15), q_half = lane >> 4;
-      const int k_row = key0 + (lane & 7) + ((lane >> 4) << 3), k_half = (lane >> 3) & 1;
-#pragma unroll 4
-      for (int k = 0; k < p.ks; ++k) {
-        uint32_t a[4];
-        ldsm(a, qs + (k >> 2) * (kTiles * 16 * 128) + q_row * 128 + (((2 * (k & 3) + q_half) ^ (q_row & 7)) << 4));
+      const int k_row = (lane & 7) + ((lane >> 4) << 3), k_half = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < kS; ++k) {
+        if (k >= p.ks) break;
 #pragma unroll
         for (int n = 0; n < kN; n += 2) {
-          uint32_t b[4];
-          const int r = k_row + 8 * n;
-          ldsm(b, ks + (k >> 2) * kChunk + r * 128 + (((2 * (k & 3) + k_half) ^ (r & 7)) << 4));
-          mma<E>(z[n], a, b[0], b[1]);
-          mma<E>(z[n + 1], a, b[2], b[3]);
+          uint32_t t[4];
+          ldsm(t, ks + (k >> 2) * kChunk + (k_row + 8 * n) * 128 + (((2 * (k & 3) + k_half) ^ (k_row & 7)) << 4));
+          mma<E>(z[n], q[k], t[0], t[1]);
+          mma<E>(z[n + 1], q[k], t[2], t[3]);
         }
       }
       if (!raw) {
@@ -367,12 +404,13 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
 #pragma unroll
           for (int j = 0; j < 4; ++j) z[n][j] *= scale;
       }
-      if (edge) {
+      if (!good || first + kUnit > lo) {
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (!good || first + 8 * n + 2 * quad + (j & 1) >= vis[j >> 1]) z[n][j] = -INFINITY;
+        mend_values<E>(c, vs, p.vc, lo - first, s.len - first, lane);
       }
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -402,148 +440,87 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
         }
       }
       const float mm[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-      uint32_t w[kN][2];
+      uint32_t a[kN / 2][4];
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[n][j] = fast_exp2(fmaf(z[n][j], mul, -mm[j >> 1]));
         l[0] += z[n][0] + z[n][1];
         l[1] += z[n][2] + z[n][3];
-        w[n][0] = pack16<E>(z[n][0], z[n][1]);
-        w[n][1] = pack16<E>(z[n][2], z[n][3]);
+        a[n / 2][2 * (n & 1)] = pack16<E>(z[n][0], z[n][1]);
+        a[n / 2][2 * (n & 1) + 1] = pack16<E>(z[n][2], z[n][3]);
       }
-      // the weighted sum of rows of V, 16 keys at a time
-      const int v_row = key0 + (lane & 15), v_half = lane >> 4;
+      const int v_row = lane & 15, v_half = lane >> 4;
 #pragma unroll
-      for (int g = 0; g < kN / 2; ++g) {
-        const uint32_t a[4] = {w[2 * g][0], w[2 * g][1], w[2 * g + 1][0], w[2 * g + 1][1]};
-        const int r = v_row + 16 * g;
-        const uint32_t row_at = vs + r * 128;
-        const int key = first + 16 * g + 2 * quad;  // the keys of a register: key and key + 1, 8 further on
-        const bool mend = edge && first + 16 * g + 16 > lo;
+      for (int j = 0; j < kV; j += 2) {
+        if (8 * j >= p.x.d_v) break;
 #pragma unroll
-        for (int j = 0; j < kV; j += 2) {
-          uint32_t b[4];
-          ldsm_t(b, row_at + (j >> 3) * kChunk + ((((j & 7) + v_half) ^ (r & 7)) << 4));
-          if (mend) {  // a weight of 0 would carry NaN and infinities into the product
-            bool found = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int kk = key + 8 * (i & 1);
-              uint32_t x = b[i];
-              if (kk >= s.len) x &= 0xFFFF0000u;
-              if (kk + 1 >= s.len) x &= 0x0000FFFFu;
-              const uint32_t y = finite2<E>(x);
-              found = found || (y != x && good);
-              if (kk >= lo) x = (x & 0xFFFF0000u) | (y & 0x0000FFFFu);
-              if (kk + 1 >= lo) x = (x & 0x0000FFFFu) | (y & 0xFFFF0000u);
-              b[i] = x;
-            }
-            if (found) *c.mended() = 1u;
-          }
-          mma<E>(o[j], a, b[0], b[1]);
-          mma<E>(o[j + 1], a, b[2], b[3]);
+        for (int g = 0; g < kN / 2; ++g) {
+          uint32_t t[4];
+          ldsm_t(t, vs + (j >> 3) * kChunk + (v_row + 16 * g) * 128 + ((((j & 7) + v_half) ^ (v_row & 7)) << 4));
+          mma<E>(o[j], a[g], t[0], t[1]);
+          mma<E>(o[j + 1], a[g], t[2], t[3]);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar(kEmpty + at_stage));
+      if (lane == 0) mbar_arrive(c.bar(kBars + slot0 + slot));
+      if (++slot == p.slots) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
-    // ---- the warps' states meet
+    // ---- the head's rows, or this part of them, leave the registers
+    const bool whole = u0 == 0 && u1 == s.units, mended = *c.mended() != 0;
+    const int part = u0 > 0 ? 0 : 1;
+    float* dst = p.parts + (static_cast<int64_t>(sh.g * p.tiles + tile) * 2 + part) * p.part_floats;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (quad == 0) ml[warp * 16 + row0 + 8 * i] = make_float2(m[i], l[i]);
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar(kSegEmpty + k2));  // Q and the description have been read
-    if (!meet()) return;
-    // state k of row tile t: group k / kSplits, split k % kSplits
-    auto state_warp = [&](int t, int k) { return (k / kSplits) * 4 + (k % kSplits) * kTiles + t; };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float most = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kStates; ++k) most = fmaxf(most, ml[state_warp(tile, k) * 16 + row0 + 8 * i].x);
-      const float f = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - most);
+      const int r = row0 + 8 * i;
+      if (r >= rows) continue;
+      if (tok[i] >= s.n) {  // padding
+        l[i] = 0.f;
+        m[i] = -INFINITY;
+      }
+      const bool nothing = l[i] == 0.f;
+      const float inv = nothing ? 0.f : 1.f / l[i];
+      const int64_t row = (static_cast<int64_t>(b) * p.x.S1 + tok[i]) * p.x.n_q + hk * p.G + (tile * 16 + r - tok[i] * p.G);
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        o[j][2 * i] *= f;
-        o[j][2 * i + 1] *= f;
+        const int d = 8 * j + 2 * quad;
+        if (8 * j >= p.x.d_v) break;
+        float x = o[j][2 * i], y = o[j][2 * i + 1];
+        if (mended && !(whole && nothing)) {
+          const int k0 = max(lo, u0 * kUnit), k1 = min(vis[i], u1 * kUnit);
+          if (infinite_column<E>(p, b, hk, k0, k1, d)) x = __uint_as_float(0x7FC00000u);
+          if (infinite_column<E>(p, b, hk, k0, k1, d + 1)) y = __uint_as_float(0x7FC00000u);
+        }
+        if (whole)
+          *reinterpret_cast<uint32_t*>(static_cast<E*>(p.x.out) + row * p.x.d_v + d) = nothing ? 0u : pack16<E>(x * inv, y * inv);
+        else
+          *reinterpret_cast<float2*>(dst + r * p.x.d_v + d) = make_float2(x, y);
       }
-    }
-    const bool whole = s.u0 == 0 && s.u1 == s.units;
-    const int slot = s.u0 > 0 ? 0 : 1;
-    float* part = p.parts + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.part_floats;
-    const bool mended = *c.mended() != 0;
-#pragma unroll
-    for (int ch = 0; ch < kV / 4; ++ch) {
-      if (ch * kCols >= p.x.d_v) break;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = 8 * j + 2 * quad;
-        float* dst = join + (warp * 16 + row0) * kPitch + col;
-        *reinterpret_cast<float2*>(dst) = make_float2(o[4 * ch + j][0], o[4 * ch + j][1]);
-        *reinterpret_cast<float2*>(dst + 8 * kPitch) = make_float2(o[4 * ch + j][2], o[4 * ch + j][3]);
-      }
-      if (!meet()) return;
-      const int tid = warp * 32 + lane, col = (tid & 7) * 4, d = ch * kCols + col;
-      for (int r = tid >> 3; r < p.rows; r += 32) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float most = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kStates; ++k) most = fmaxf(most, ml[state_warp(r >> 4, k) * 16 + (r & 15)].x);
-#pragma unroll
-        for (int k = 0; k < kStates; ++k) {
-          const int w = state_warp(r >> 4, k);
-          const float4 x = *reinterpret_cast<const float4*>(join + (w * 16 + (r & 15)) * kPitch + col);
-          v.x += x.x;
-          v.y += x.y;
-          v.z += x.z;
-          v.w += x.w;
-          const float2 t = ml[w * 16 + (r & 15)];
-          if (t.x != -INFINITY) sum += t.y * fast_exp2(t.x - most);
-          else sum += t.y;  // 0, or the NaN of a score
-        }
-        if (d >= p.x.d_v) continue;
-        const int tok = r / p.G, head = s.hk * p.G + (r - tok * p.G);
-        const int seen = tok < s.n ? min(s.len, max(0, s.pos + tok + 1)) : 0;
-        if (tok >= s.n) {  // padding: its scores were made, and are dropped here
-          sum = 0.f;
-          most = -INFINITY;
-        }
-        if (mended && lo < seen) {
-          const int a = max(lo, s.u0 * kUnit), e = min(seen, s.u1 * kUnit);
-          float* y = &v.x;
-          for (int i = 0; i < 4; ++i)
-            if (infinite_column<E>(p, s, a, e, d + i)) y[i] = __uint_as_float(0x7FC00000u);
-        }
+      if (quad == 0) {
         if (whole) {
-          const int64_t at = (static_cast<int64_t>(s.b) * p.x.S1 + tok) * p.x.n_q + head;
-          const bool nothing = sum == 0.f;
-          const float inv = nothing ? 0.f : 1.f / sum;
-          uint2 y = make_uint2(pack16<E>(v.x * inv, v.y * inv), pack16<E>(v.z * inv, v.w * inv));
-          if (nothing) y = make_uint2(0u, 0u);
-          *reinterpret_cast<uint2*>(static_cast<E*>(p.x.out) + at * p.x.d_v + d) = y;
-          if (d == 0 && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (most + log2f(sum)) * 0.69314718055994530942f;
+          if (p.x.lse != nullptr) p.x.lse[row] = nothing ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994530942f;
         } else {
-          *reinterpret_cast<float4*>(part + r * p.x.d_v + d) = v;
           // the lowest maximum joins with weight 0 and brings along the NaN of infinite values whose scores are all -inf
-          if (d == 0) *reinterpret_cast<float2*>(part + p.rows * p.x.d_v + 2 * r) = make_float2(seen > 0 ? fmaxf(most, -3.402823466e38f) : most, sum);
+          *reinterpret_cast<float2*>(dst + rows * p.x.d_v + 2 * r) = make_float2(vis[i] > 0 ? fmaxf(m[i], -3.402823466e38f) : m[i], l[i]);
         }
       }
-      if (!meet()) return;
     }
-    if (!whole && slot == 1 && warp == 0 && lane == 0) {
-      // the CTAs that hold the rest: up to the one whose share has the head's last unit
-      const int64_t end = static_cast<int64_t>(blockIdx.x + 1) * total / ctas + (s.units - s.u1);  // one behind it
-      int last = static_cast<int>((end * ctas + total - 1) / total) - 1;
-      p.records[blockIdx.x] = make_int4(s.b, s.hk, last - static_cast<int>(blockIdx.x), 1);
+    if (!whole && part == 1 && tile == 0 && lane == 0) {
+      // the groups that hold the rest: up to the one whose share has the head's last unit
+      const int64_t end = sh.from + (sh.count - w.left) + (s.units - u0);  // one behind it
+      p.records[sh.g] = make_int4(b, hk, static_cast<int>((end * sh.groups + total - 1) / total) - 1 - sh.g, 1);
     }
+    w.left -= u1 - u0;
+    w.next_head(p, lane);
   }
 }
 
-template <typename E, int kTiles, int kV>
+template <typename E, int kS, int kV>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ uint8_t raw[];
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -552,30 +529,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   c.smem = raw + (c.sb - smem_u32(raw));
   c.wait_ns = p.wait_ns;
   c.abort = reinterpret_cast<volatile uint32_t*>(c.smem + kOffAbort);
-  if (tid == 0) {
-    *c.abort = 0u;
-    *c.mended() = 0u;
-    p.records[blockIdx.x] = make_int4(0, 0, 0, 0);  // nothing to join, until this CTA finds a cut
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(c.bar(kFull + i), 1);
-      mbar_init(c.bar(kEmpty + i), kConsumers / kGroups);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(c.bar(kSegFull + i), 1);
-      mbar_init(c.bar(kSegEmpty + i), kConsumers);
-    }
-    mbar_init(c.bar(kJoin), kConsumers);
-    fence_mbarrier_init_cluster();
-  }
+  if (tid == 0) *c.abort = *c.mended() = 0u;
+  if (tid < 2 * kBars) mbar_init(c.bar(tid), tid < kBars ? 1 : p.tiles);
+  if (tid < p.pipes && group_id(tid) < p.groups) p.records[group_id(tid)] = make_int4(0, 0, 0, 0);
+  fence_mbarrier_init_cluster();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int b = 0, ctas = 1;
-  int64_t base = 0, from = 0, to = 0, total = 0;
   __syncthreads();
-  const bool busy = start(p, c, b, base, from, to, total, ctas);
-  __syncthreads();
-  if (busy) {
-    if (warp == kLoadWarp) load_role(p, c, maps, b, base, from, to);
-    else consume_role<E, kTiles, kV>(p, c, warp, lane, ctas, total);
+  const int64_t total = find_shares(p, c);
+  if (warp < kWarps) {
+    regs_increase<kConsumerRegs>();
+    consume_role<E, kS, kV>(p, c, warp, lane, total);
+  } else {
+    regs_decrease<kLoadRegs>();
+    load_role(p, c, maps, warp - kWarps, lane, total);
   }
   if (*c.abort) {
     if (lane == 0) atomicOr(&g_paged_status, MLA_DEVICE_TIMEOUT);
@@ -586,53 +552,128 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the parts of a head that was cut: block i those of the head whose first part is CTA i's last.
-constexpr int kMergeThreads = 256;
-constexpr int kAhead = 4;  // parts in flight
+// Joins the parts of the heads that were cut, 32 quads of columns at a time: a
+// warp to each where there are few parts, else a block, whose warps share them out.
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+constexpr int kAhead = 4;        // parts in flight
+constexpr int kFewParts = 8;
+constexpr int kMaxGroups = 152 * kWarps;
+
+struct State {
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void join(float m2, float l2, const float (&v)[4]) {
+    if (m2 == -INFINITY && l2 == 0.f) return;  // a part in which the row sees nothing
+    const float top = fmaxf(m, m2), f = m == -INFINITY ? 0.f : exp2f(m - top), w = exp2f(m2 - top);
+    m = top;
+    l = l * f + l2 * w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = o[j] * f + v[j] * w;
+  }
+};
+
 template <typename E>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p) {
+  __shared__ int list[2][kMaxGroups];
+  __shared__ int sums[kMergeWarps];
+  __shared__ float sm[kMergeWarps][6][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 rec = __ldcg(p.records + blockIdx.x);
-  if (rec.w == 0) return;
-  const int quads = p.x.d_v / 4;
-  for (int i = threadIdx.x; i < p.rows * quads; i += kMergeThreads) {
-    const int r = i / quads, d = (i - r * quads) * 4;
-    float top = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k0 = 0; k0 <= rec.z; k0 += kAhead) {
+  // every block makes the same lists of heads with few and with many parts: a thread counts
+  // its run of the records (both counts in a word), and numbers them behind those before it
+  const int per = (p.groups + kMergeThreads - 1) / kMergeThreads, g0 = tid * per, g1 = min(p.groups, g0 + per);
+  auto kind = [&](int g) {  // 0: nothing to join
+    const int4 rec = __ldcg(p.records + g);
+    return rec.w == 0 ? 0 : rec.z <= kFewParts ? 1 : 1 << 16;
+  };
+  int mine = 0;
+  for (int g = g0; g < g1; ++g) mine += kind(g);
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  if (lane == 31) sums[warp] = before;
+  __syncthreads();
+  before -= mine;
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  for (int g = g0; g < g1; ++g) {
+    const int k = kind(g);
+    if (k == 1) list[0][before & 0xFFFF] = g;
+    if (k > 1) list[1][before >> 16] = g;
+    before += k;
+  }
+  const int found[2] = {all & 0xFFFF, all >> 16};
+  __syncthreads();
+  const int quads = p.x.d_v / 4, slices = (min(16, p.rows) * quads + 31) / 32 * p.tiles;
+  // parts first, first + step, ... of slice `i` of group g's head
+  auto gather = [&](int g, const int4& rec, int i, int first, int step, State& st, int& r, int& d) {
+    const int tile = i % p.tiles, quad = i / p.tiles * 32 + lane, rows = min(16, p.rows - tile * 16);
+    r = quad / quads;
+    d = (quad - r * quads) * 4;
+    const bool in = r < rows;
+    if (!in) r = 0;
+    for (int k0 = first; k0 <= rec.z; k0 += kAhead * step) {
       float2 ml[kAhead];
       float4 v[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int k = min(k0 + u, rec.z);
-        const float* src = p.parts + ((static_cast<int64_t>(blockIdx.x) + k) * 2 + (k > 0 ? 0 : 1)) * p.part_floats;
-        ml[u] = __ldcg(reinterpret_cast<const float2*>(src + p.rows * p.x.d_v + 2 * r));
+        const int k = k0 + u * step <= rec.z ? k0 + u * step : first;
+        const float* src = p.parts + ((static_cast<int64_t>(g + k) * p.tiles + tile) * 2 + (k > 0 ? 0 : 1)) * p.part_floats;
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(src + rows * p.x.d_v + 2 * r));
         v[u] = __ldcg(reinterpret_cast<const float4*>(src + r * p.x.d_v + d));
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (k0 + u > rec.z || (ml[u].x == -INFINITY && ml[u].y == 0.f)) continue;  // a part in which the row sees nothing
-        const float next = fmaxf(top, ml[u].x), f = top == -INFINITY ? 0.f : exp2f(top - next), w = exp2f(ml[u].x - next);
-        top = next;
-        l = l * f + ml[u].y * w;
-        o[0] = o[0] * f + v[u].x * w;
-        o[1] = o[1] * f + v[u].y * w;
-        o[2] = o[2] * f + v[u].z * w;
-        o[3] = o[3] * f + v[u].w * w;
-      }
+      for (int u = 0; u < kAhead; ++u)
+        if (k0 + u * step <= rec.z) st.join(ml[u].x, ml[u].y, {v[u].x, v[u].y, v[u].z, v[u].w});
     }
-    const bool nothing = l == 0.f;
-    const float inv = nothing ? 0.f : 1.f / l;
+    r = in ? tile * 16 + r : -1;
+  };
+  auto put = [&](const int4& rec, const State& st, int r, int d) {
+    if (r < 0) return;
+    const bool nothing = st.l == 0.f;
+    const float inv = nothing ? 0.f : 1.f / st.l;
     const int tok = r / p.G;
     const int64_t at = (static_cast<int64_t>(rec.x) * p.x.S1 + tok) * p.x.n_q + rec.y * p.G + (r - tok * p.G);
-    uint2 y = make_uint2(pack16<E>(o[0] * inv, o[1] * inv), pack16<E>(o[2] * inv, o[3] * inv));
+    uint2 y = make_uint2(pack16<E>(st.o[0] * inv, st.o[1] * inv), pack16<E>(st.o[2] * inv, st.o[3] * inv));
     if (nothing) y = make_uint2(0u, 0u);
     *reinterpret_cast<uint2*>(static_cast<E*>(p.x.out) + at * p.x.d_v + d) = y;
-    if (d == 0 && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+    if (d == 0 && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (st.m + log2f(st.l)) * 0.69314718055994530942f;
+  };
+  for (int i = blockIdx.x + static_cast<int>(gridDim.x) * warp; i < found[0] * slices; i += static_cast<int>(gridDim.x) * kMergeWarps) {
+    const int g = list[0][i / slices];
+    const int4 rec = __ldcg(p.records + g);
+    State st;
+    int r, d;
+    gather(g, rec, i % slices, 0, 1, st, r, d);
+    put(rec, st, r, d);
+  }
+  for (int i = blockIdx.x; i < found[1] * slices; i += gridDim.x) {
+    const int g = list[1][i / slices];
+    const int4 rec = __ldcg(p.records + g);
+    State st;
+    int r, d;
+    gather(g, rec, i % slices, warp, kMergeWarps, st, r, d);
+    __syncthreads();  // the last item's states have been read
+    sm[warp][0][lane] = st.m;
+    sm[warp][1][lane] = st.l;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sm[warp][2 + j][lane] = st.o[j];
+    __syncthreads();
+    if (warp != 0) continue;
+    for (int k = 1; k < kMergeWarps; ++k)
+      st.join(sm[k][0][lane], sm[k][1][lane], {sm[k][2][lane], sm[k][3][lane], sm[k][4][lane], sm[k][5][lane]});
+    put(rec, st, r, d);
   }
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int kMaxDevices = 64, kMaxCtas = 160;
+constexpr int kMaxDevices = 64;
 struct Device {
   bool ready = false;
   int sms = 0;
@@ -643,11 +684,11 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 typedef void (*Kernel)(const Maps, const Params);
 template <typename E>
-Kernel kernel_of(int tiles, bool wide) {
-  static const Kernel all[3][2] = {{paged_attn_kernel<E, 1, 8>, paged_attn_kernel<E, 1, 16>},
-                                   {paged_attn_kernel<E, 2, 8>, paged_attn_kernel<E, 2, 16>},
-                                   {paged_attn_kernel<E, 4, 8>, paged_attn_kernel<E, 4, 16>}};
-  return all[tiles / 2][wide ? 1 : 0];
+Kernel kernel_of(int kc, int vc) {
+  static const Kernel all[3][2] = {{paged_attn_kernel<E, 4, 8>, paged_attn_kernel<E, 4, 16>},
+                                   {paged_attn_kernel<E, 8, 8>, paged_attn_kernel<E, 8, 16>},
+                                   {paged_attn_kernel<E, 12, 8>, paged_attn_kernel<E, 12, 16>}};
+  return all[kc - 1][vc - 1];
 }
 
 // Kernel attributes and the tensor-map encoder; the first call on a device.
@@ -661,10 +702,15 @@ mla_status init_device(int* sms) {
     const mla_status st = tensor_map_encoder(&g_encode);
     if (st != MLA_OK) return st;
     HEADS_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev), "device attributes");
-    for (int tiles : {1, 2, 4})
-      for (bool wide : {false, true})
-        for (Kernel k : {kernel_of<__nv_bfloat16>(tiles, wide), kernel_of<__half>(tiles, wide)})
+    for (int kc = 1; kc <= 3; ++kc)
+      for (int vc = 1; vc <= 2; ++vc)
+        for (Kernel k : {kernel_of<__nv_bfloat16>(kc, vc), kernel_of<__half>(kc, vc)})
+        {
           HEADS_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost), "kernel set-up");
+          cudaFuncAttributes fa;
+          HEADS_CUDA(cudaFuncGetAttributes(&fa, k), "kernel attributes");
+          if (fa.numRegs < kRegs) return fail(MLA_ERR_CUDA, "the kernel was built with %d registers", fa.numRegs);  // what the warps divide
+        }
     d.ready = true;
   }
   *sms = d.sms;
@@ -673,14 +719,17 @@ mla_status init_device(int* sms) {
 
 // Rows of a key head; up to kMaxRows of them go through the kernel above.
 int rows_of(const Problem& p) { return static_cast<int>(std::min<int64_t>(1 << 30, static_cast<int64_t>(p.S1) * (p.n_q / p.n_kv))); }
-int part_floats(const Problem& p) { return (rows_of(p) * (p.d_v + 2) + 3) & ~3; }
-// CTAs that the longest stream of these dims feeds.
-int64_t most_ctas(const Problem& p) {
+int tiles_of(const Problem& p) { return rows_of(p) <= 16 ? 1 : rows_of(p) <= 32 ? 2 : 4; }
+int part_floats(const Problem& p) { return (std::min(16, rows_of(p)) * (p.d_v + 2) + 3) & ~3; }
+// Groups that the longest stream of these dims feeds.
+int64_t most_groups(const Problem& p) {
   const int64_t heads = std::min<int64_t>(int64_t(1) << 20, static_cast<int64_t>(p.B) * p.n_kv);
-  return std::max<int64_t>(1, std::min<int64_t>(kMaxCtas, heads * 2 * p.W / kMinUnits));
+  return std::max<int64_t>(1, std::min<int64_t>(kMaxGroups / tiles_of(p), heads * (kPage / kUnit) * p.W / kMinUnits));
 }
-size_t records_bytes(const Problem& p) { return (most_ctas(p) * sizeof(int4) + 255) & ~size_t(255); }
-size_t workspace_of(const Problem& p) { return records_bytes(p) + static_cast<size_t>(most_ctas(p)) * 2 * part_floats(p) * sizeof(float); }
+size_t records_bytes(const Problem& p) { return (most_groups(p) * sizeof(int4) + 255) & ~size_t(255); }
+size_t workspace_of(const Problem& p) {
+  return records_bytes(p) + static_cast<size_t>(most_groups(p)) * tiles_of(p) * 2 * part_floats(p) * sizeof(float);
+}
 
 mla_status launch(const Problem& x, cudaStream_t s) {
   int sms = 0;
@@ -693,22 +742,18 @@ mla_status launch(const Problem& x, cudaStream_t s) {
   p.part_floats = part_floats(x);
   p.G = x.n_q / x.n_kv;
   p.rows = rows_of(x);
-  const int tiles = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+  p.tiles = tiles_of(x);
   p.kc = (x.d_qk + 63) / 64;
   p.vc = (x.d_v + 63) / 64;
   p.ks = (x.d_qk + 15) / 16;
-  p.q_bytes = p.kc * tiles * 16 * 128;
-  p.stage_bytes = (p.kc + p.vc) * kChunk;
-  p.stages = std::min(kMaxStages, (kSmemMost - 1024 - kOffTiles - 2 * p.q_bytes) / p.stage_bytes);
-  p.ctas = static_cast<int>(std::min<int64_t>(std::min(sms, kMaxCtas), most_ctas(x)));
+  p.unit_bytes = (p.kc + p.vc) * kChunk;
   p.wait_ns = host_wait_limit_ns();
+  const int fit = std::min(kMaxSlots, (kSmemMost - 1024 - kOffSlots) / p.unit_bytes);
+  p.pipes = std::min(kWarps / p.tiles, std::max(1, fit / kLeastSlots));
+  p.slots = fit / p.pipes;
+  p.groups = static_cast<int>(std::min<int64_t>(most_groups(x), static_cast<int64_t>(sms) * p.pipes));
+  const int ctas = std::min(sms, p.groups);
   Maps maps;
-  {
-    const int64_t size[3] = {x.d_qk, x.n_q, x.T}, stride[2] = {x.q.head_stride, x.q.token_stride};
-    const int box[3] = {64, p.G, x.S1};
-    const mla_status ms = tmap(g_encode, &maps.q, x.dtype, x.q.data, 3, size, stride, box, "q");
-    if (ms != MLA_OK) return ms;
-  }
   for (int i = 0; i < 2; ++i) {
     const mla_kv_cache& c = i == 0 ? x.k : x.v;
     const int64_t size[4] = {i == 0 ? x.d_qk : x.d_v, kPage, x.n_kv, x.num_blocks};
@@ -718,14 +763,16 @@ mla_status launch(const Problem& x, cudaStream_t s) {
     if (ms != MLA_OK) return ms;
   }
   const bool bf = x.dtype == MLA_ROPE_BF16;
-  const Kernel kernel = bf ? kernel_of<__nv_bfloat16>(tiles, p.vc == 2) : kernel_of<__half>(tiles, p.vc == 2);
-  const size_t smem = 1024 + kOffTiles + 2 * p.q_bytes + static_cast<size_t>(p.stages) * p.stage_bytes;
-  kernel<<<static_cast<unsigned>(p.ctas), kThreads, smem, s>>>(maps, p);
+  const Kernel kernel = bf ? kernel_of<__nv_bfloat16>(p.kc, p.vc) : kernel_of<__half>(p.kc, p.vc);
+  const size_t smem = 1024 + kOffSlots + static_cast<size_t>(p.pipes) * p.slots * p.unit_bytes;
+  kernel<<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(maps, p);
   HEADS_CUDA(cudaGetLastError(), "kernel launch");
-  if (p.ctas > 1)
-    HEADS_CUDA(bf ? launch_after(paged_merge_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(p.ctas)), kMergeThreads, 0, s, p)
-                  : launch_after(paged_merge_kernel<__half>, dim3(static_cast<unsigned>(p.ctas)), kMergeThreads, 0, s, p),
+  if (p.groups > 1) {
+    const dim3 grid(static_cast<unsigned>(2 * sms));
+    HEADS_CUDA(bf ? launch_after(paged_merge_kernel<__nv_bfloat16>, grid, kMergeThreads, 0, s, p)
+                  : launch_after(paged_merge_kernel<__half>, grid, kMergeThreads, 0, s, p),
                "merge launch");
+  }
   return MLA_OK;
 }
 
