@@ -62,7 +62,6 @@ struct Params {
   int G, rows;     // heads to a key head, rows of a key head
   int tiles;       // 16-row tiles of them
   int kc, vc;      // 64-column chunks of keys and values
-  int ks;          // 16-column steps of keys
   int slots, unit_bytes;  // of a pipeline
   int pipes;       // pipelines of a CTA, each of a load warp and `tiles` others
   int groups;      // pipelines of the GPU that take part
@@ -99,17 +98,39 @@ struct Ctx {
   __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
 };
 
-// Units of a share at least: fewer parts to join where there is little to read.
-constexpr int kMinUnits = 2;
+// a / b and the rest; 64-bit division is slow, and hardly ever needed.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t& rest) {
+  const int64_t q = ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+  rest = a - q * b;
+  return q;
+}
 
-__device__ __forceinline__ int groups_of(const Params& p, int64_t total) {
-  return static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.groups), total / kMinUnits)));
+// The stream in equal shares: the first `more` of them have `each` + 1 units, the others `each`.
+struct Split {
+  int64_t each, more;
+  int groups;
+  __device__ __forceinline__ int64_t begin(int g) const { return g * each + min(static_cast<int64_t>(g), more); }
+  __device__ __forceinline__ int group_of(int64_t unit) const {
+    int64_t rest;
+    const int64_t wide = more * (each + 1);
+    return static_cast<int>(unit < wide ? divide(unit, each + 1, rest) : more + divide(unit - wide, each, rest));
+  }
+};
+
+// Units of a share at least: fewer parts to join where there is little to read.
+constexpr int kMinUnits = 4;
+
+__device__ __forceinline__ Split split_of(const Params& p, int64_t total) {
+  Split s;
+  s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.groups), total / kMinUnits)));
+  s.each = divide(total, s.groups, s.more);
+  return s;
 }
 // A pipeline's number: neighbours in the stream lie in different CTAs, so that few of them use many SMs.
 __device__ __forceinline__ int group_id(int pipe) { return pipe * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); }
 
-// Finds where the shares of the CTA's pipelines begin; returns the length of the stream.
-__device__ int64_t find_shares(const Params& p, const Ctx& c) {
+// Finds where the shares of the CTA's pipelines begin, and how the stream is split.
+__device__ Split find_shares(const Params& p, const Ctx& c) {
   int64_t* part = reinterpret_cast<int64_t*>(c.smem + kOffScan);
   int64_t* at = reinterpret_cast<int64_t*>(c.smem + kOffWalk);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.x.B;
@@ -147,7 +168,7 @@ __device__ int64_t find_shares(const Params& p, const Ctx& c) {
   }
   if (cut) atomicOr(&g_paged_status, MLA_DEVICE_BAD_BLOCK);
   int64_t pre = scan(mine, total);
-  const int groups = groups_of(p, total);
+  const Split split = split_of(p, total);
   int64_t carry = 0;
   for (int k = 0; k < chunks; ++k) {
     const int b = k * kThreads + tid;
@@ -159,7 +180,7 @@ __device__ int64_t find_shares(const Params& p, const Ctx& c) {
     if (b < B) {
       for (int w = 0; w < p.pipes; ++w) {
         const int g = group_id(w);
-        const int64_t from = g < groups ? g * total / groups : -1;
+        const int64_t from = g < split.groups ? split.begin(g) : -1;
         if (from >= pre && from < pre + len) {
           at[2 * w] = b;
           at[2 * w + 1] = pre;
@@ -169,7 +190,7 @@ __device__ int64_t find_shares(const Params& p, const Ctx& c) {
     carry += sum;
   }
   __syncthreads();
-  return total;
+  return split;
 }
 
 // A share of the stream, unit by unit.  Lane i keeps the lengths of sequence b0 + i.
@@ -188,8 +209,9 @@ struct Walk {
     left = count;
     load_lengths(p, lane);
     s = make_seq(p, uniform(act), uniform(q_len));
-    hk = static_cast<int>(off / s.units);
-    u = static_cast<int>(off - static_cast<int64_t>(hk) * s.units);
+    int64_t rest;
+    hk = static_cast<int>(divide(off, s.units, rest));
+    u = static_cast<int>(rest);
   }
   // the head's first unit, behind the current head
   __device__ __forceinline__ void next_head(const Params& p, int lane) {
@@ -216,10 +238,10 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t at) {
 template <typename E>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (__is_same(E, __half))
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
@@ -274,24 +296,23 @@ __device__ __noinline__ void mend_values(const Ctx& c, uint32_t vs, int chunks, 
 
 // The share of a pipeline; false: it has none.
 struct Share {
-  int g, groups, b;
+  int g, b;
   int64_t from, count, off;  // of the stream, of sequence b
 };
-__device__ __forceinline__ bool share_of(const Params& p, const Ctx& c, int pipe, int64_t total, Share& s) {
+__device__ __forceinline__ bool share_of(const Params& p, const Ctx& c, int pipe, const Split& split, Share& s) {
   s.g = group_id(pipe);
-  s.groups = groups_of(p, total);
-  if (pipe >= p.pipes || s.g >= s.groups) return false;
-  s.from = s.g * total / s.groups;
-  s.count = (s.g + 1) * total / s.groups - s.from;
+  if (pipe >= p.pipes || s.g >= split.groups) return false;
+  s.from = split.begin(s.g);
+  s.count = split.begin(s.g + 1) - s.from;
   const int64_t* at = reinterpret_cast<const int64_t*>(c.smem + kOffWalk) + 2 * pipe;
   s.b = static_cast<int>(at[0]);
   s.off = s.from - at[1];
   return true;
 }
 
-__device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int pipe, int lane, int64_t total) {
+__device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int pipe, int lane, const Split& split) {
   Share sh;
-  if (!share_of(p, c, pipe, total, sh)) return;
+  if (!share_of(p, c, pipe, split, sh)) return;
   const int slot0 = pipe * p.slots;
   const uint32_t slots = c.sb + kOffSlots + slot0 * p.unit_bytes;
   volatile int* good_of = reinterpret_cast<volatile int*>(c.smem + kOffGood) + slot0;
@@ -334,12 +355,12 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int p
   if (bad && lane == 0) atomicOr(&g_paged_status, MLA_DEVICE_BAD_BLOCK);
 }
 
-// kS: 16-column steps of keys, 4, 8 or 12.  kV: 8-column tiles of values, 8 or 16.
+// kS: 16-column steps of keys, kV: 8-column tiles of values.
 template <typename E, int kS, int kV>
-__device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, int64_t total) {
+__device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, const Split& split) {
   const int pipe = warp / p.tiles, tile = warp % p.tiles;
   Share sh;
-  if (!share_of(p, c, pipe, total, sh)) return;
+  if (!share_of(p, c, pipe, split, sh)) return;
   const int quad = lane & 3, row0 = lane >> 2;  // the thread's rows: row0 and row0 + 8 of the tile
   const int rows = min(16, p.rows - tile * 16);
   const float scale = p.x.scale_log2;
@@ -387,15 +408,21 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
 #pragma unroll
       for (int n = 0; n < kN; ++n) z[n][0] = z[n][1] = z[n][2] = z[n][3] = 0.f;
       const int k_row = (lane & 7) + ((lane >> 4) << 3), k_half = (lane >> 3) & 1;
+      // fragments are loaded a step ahead of the products that take them
+      uint32_t t[2][kN / 2][4];
+      auto load_keys = [&](int k) {
+#pragma unroll
+        for (int n = 0; n < kN / 2; ++n)
+          ldsm(t[k & 1][n], ks + (k >> 2) * kChunk + (k_row + 16 * n) * 128 + (((2 * (k & 3) + k_half) ^ (k_row & 7)) << 4));
+      };
+      load_keys(0);
 #pragma unroll
       for (int k = 0; k < kS; ++k) {
-        if (k >= p.ks) break;
+        if (k + 1 < kS) load_keys(k + 1);
 #pragma unroll
-        for (int n = 0; n < kN; n += 2) {
-          uint32_t t[4];
-          ldsm(t, ks + (k >> 2) * kChunk + (k_row + 8 * n) * 128 + (((2 * (k & 3) + k_half) ^ (k_row & 7)) << 4));
-          mma<E>(z[n], q[k], t[0], t[1]);
-          mma<E>(z[n + 1], q[k], t[2], t[3]);
+        for (int n = 0; n < kN / 2; ++n) {
+          mma<E>(z[2 * n], q[k], t[k & 1][n][0], t[k & 1][n][1]);
+          mma<E>(z[2 * n + 1], q[k], t[k & 1][n][2], t[k & 1][n][3]);
         }
       }
       if (!raw) {
@@ -412,6 +439,13 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
             if (!good || first + 8 * n + 2 * quad + (j & 1) >= vis[j >> 1]) z[n][j] = -INFINITY;
         mend_values<E>(c, vs, p.vc, lo - first, s.len - first, lane);
       }
+      const int v_row = lane & 15, v_half = lane >> 4;
+      auto load_values = [&](int j) {
+#pragma unroll
+        for (int g = 0; g < kN / 2; ++g)
+          ldsm_t(t[j & 1][g], vs + (j >> 2) * kChunk + (v_row + 16 * g) * 128 + (((2 * (j & 3) + v_half) ^ (v_row & 7)) << 4));
+      };
+      load_values(0);
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
@@ -450,16 +484,13 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
         a[n / 2][2 * (n & 1)] = pack16<E>(z[n][0], z[n][1]);
         a[n / 2][2 * (n & 1) + 1] = pack16<E>(z[n][2], z[n][3]);
       }
-      const int v_row = lane & 15, v_half = lane >> 4;
 #pragma unroll
-      for (int j = 0; j < kV; j += 2) {
-        if (8 * j >= p.x.d_v) break;
+      for (int j = 0; j < kV / 2; ++j) {
+        if (j + 1 < kV / 2) load_values(j + 1);
 #pragma unroll
         for (int g = 0; g < kN / 2; ++g) {
-          uint32_t t[4];
-          ldsm_t(t, vs + (j >> 3) * kChunk + (v_row + 16 * g) * 128 + ((((j & 7) + v_half) ^ (v_row & 7)) << 4));
-          mma<E>(o[j], a[g], t[0], t[1]);
-          mma<E>(o[j + 1], a[g], t[2], t[3]);
+          mma<E>(o[2 * j], a[g], t[j & 1][g][0], t[j & 1][g][1]);
+          mma<E>(o[2 * j + 1], a[g], t[j & 1][g][2], t[j & 1][g][3]);
         }
       }
       __syncwarp();
@@ -489,7 +520,7 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
         const int d = 8 * j + 2 * quad;
-        if (8 * j >= p.x.d_v) break;
+        if (d >= p.x.d_v) continue;
         float x = o[j][2 * i], y = o[j][2 * i + 1];
         if (mended && !(whole && nothing)) {
           const int k0 = max(lo, u0 * kUnit), k1 = min(vis[i], u1 * kUnit);
@@ -513,7 +544,7 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
     if (!whole && part == 1 && tile == 0 && lane == 0) {
       // the groups that hold the rest: up to the one whose share has the head's last unit
       const int64_t end = sh.from + (sh.count - w.left) + (s.units - u0);  // one behind it
-      p.records[sh.g] = make_int4(b, hk, static_cast<int>((end * sh.groups + total - 1) / total) - 1 - sh.g, 1);
+      p.records[sh.g] = make_int4(b, hk, split.group_of(end - 1) - sh.g, 1);
     }
     w.left -= u1 - u0;
     w.next_head(p, lane);
@@ -535,13 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   fence_mbarrier_init_cluster();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
-  const int64_t total = find_shares(p, c);
+  const Split split = find_shares(p, c);
   if (warp < kWarps) {
     regs_increase<kConsumerRegs>();
-    consume_role<E, kS, kV>(p, c, warp, lane, total);
+    consume_role<E, kS, kV>(p, c, warp, lane, split);
   } else {
     regs_decrease<kLoadRegs>();
-    load_role(p, c, maps, warp - kWarps, lane, total);
+    load_role(p, c, maps, warp - kWarps, lane, split);
   }
   if (*c.abort) {
     if (lane == 0) atomicOr(&g_paged_status, MLA_DEVICE_TIMEOUT);
@@ -573,20 +604,24 @@ struct State {
 
 template <typename E>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p) {
-  __shared__ int list[2][kMaxGroups];
+  __shared__ int4 list[2][kMaxGroups];  // sequence, key head, parts behind the first, group
   __shared__ int sums[kMergeWarps];
   __shared__ float sm[kMergeWarps][6][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // every block makes the same lists of heads with few and with many parts: a thread counts
   // its run of the records (both counts in a word), and numbers them behind those before it
-  const int per = (p.groups + kMergeThreads - 1) / kMergeThreads, g0 = tid * per, g1 = min(p.groups, g0 + per);
-  auto kind = [&](int g) {  // 0: nothing to join
-    const int4 rec = __ldcg(p.records + g);
-    return rec.w == 0 ? 0 : rec.z <= kFewParts ? 1 : 1 << 16;
-  };
+  constexpr int kPer = (kMaxGroups + kMergeThreads - 1) / kMergeThreads;
+  const int g0 = tid * kPer;
+  int4 rec[kPer];
   int mine = 0;
-  for (int g = g0; g < g1; ++g) mine += kind(g);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) rec[i] = g0 + i < p.groups ? __ldcg(p.records + g0 + i) : make_int4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    rec[i].w = rec[i].w == 0 ? 0 : rec[i].z <= kFewParts ? 1 : 1 << 16;
+    mine += rec[i].w;
+  }
   int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -602,17 +637,18 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     if (w < warp) before += sums[w];
     all += sums[w];
   }
-  for (int g = g0; g < g1; ++g) {
-    const int k = kind(g);
-    if (k == 1) list[0][before & 0xFFFF] = g;
-    if (k > 1) list[1][before >> 16] = g;
-    before += k;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int4 entry = make_int4(rec[i].x, rec[i].y, rec[i].z, g0 + i);
+    if (rec[i].w == 1) list[0][before & 0xFFFF] = entry;
+    if (rec[i].w > 1) list[1][before >> 16] = entry;
+    before += rec[i].w;
   }
   const int found[2] = {all & 0xFFFF, all >> 16};
   __syncthreads();
   const int quads = p.x.d_v / 4, slices = (min(16, p.rows) * quads + 31) / 32 * p.tiles;
   // parts first, first + step, ... of slice `i` of group g's head
-  auto gather = [&](int g, const int4& rec, int i, int first, int step, State& st, int& r, int& d) {
+  auto gather = [&](const int4& rec, int i, int first, int step, State& st, int& r, int& d) {
     const int tile = i % p.tiles, quad = i / p.tiles * 32 + lane, rows = min(16, p.rows - tile * 16);
     r = quad / quads;
     d = (quad - r * quads) * 4;
@@ -624,7 +660,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int k = k0 + u * step <= rec.z ? k0 + u * step : first;
-        const float* src = p.parts + ((static_cast<int64_t>(g + k) * p.tiles + tile) * 2 + (k > 0 ? 0 : 1)) * p.part_floats;
+        const float* src = p.parts + ((static_cast<int64_t>(rec.w + k) * p.tiles + tile) * 2 + (k > 0 ? 0 : 1)) * p.part_floats;
         ml[u] = __ldcg(reinterpret_cast<const float2*>(src + rows * p.x.d_v + 2 * r));
         v[u] = __ldcg(reinterpret_cast<const float4*>(src + r * p.x.d_v + d));
       }
@@ -646,19 +682,17 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     if (d == 0 && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (st.m + log2f(st.l)) * 0.69314718055994530942f;
   };
   for (int i = blockIdx.x + static_cast<int>(gridDim.x) * warp; i < found[0] * slices; i += static_cast<int>(gridDim.x) * kMergeWarps) {
-    const int g = list[0][i / slices];
-    const int4 rec = __ldcg(p.records + g);
+    const int4 rec = list[0][i / slices];
     State st;
     int r, d;
-    gather(g, rec, i % slices, 0, 1, st, r, d);
+    gather(rec, i % slices, 0, 1, st, r, d);
     put(rec, st, r, d);
   }
   for (int i = blockIdx.x; i < found[1] * slices; i += gridDim.x) {
-    const int g = list[1][i / slices];
-    const int4 rec = __ldcg(p.records + g);
+    const int4 rec = list[1][i / slices];
     State st;
     int r, d;
-    gather(g, rec, i % slices, warp, kMergeWarps, st, r, d);
+    gather(rec, i % slices, warp, kMergeWarps, st, r, d);
     __syncthreads();  // the last item's states have been read
     sm[warp][0][lane] = st.m;
     sm[warp][1][lane] = st.l;
@@ -683,13 +717,15 @@ std::mutex g_lock;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 typedef void (*Kernel)(const Maps, const Params);
+// The kernels, and the sizes of keys and values up to which each goes.
+constexpr int kKernels = 7;
 template <typename E>
-Kernel kernel_of(int kc, int vc) {
-  static const Kernel all[3][2] = {{paged_attn_kernel<E, 4, 8>, paged_attn_kernel<E, 4, 16>},
-                                   {paged_attn_kernel<E, 8, 8>, paged_attn_kernel<E, 8, 16>},
-                                   {paged_attn_kernel<E, 12, 8>, paged_attn_kernel<E, 12, 16>}};
-  return all[kc - 1][vc - 1];
+Kernel kernel_of(int i) {
+  static const Kernel all[kKernels] = {paged_attn_kernel<E, 4, 8>, paged_attn_kernel<E, 4, 16>,  paged_attn_kernel<E, 6, 12>, paged_attn_kernel<E, 6, 16>,
+                                       paged_attn_kernel<E, 8, 8>, paged_attn_kernel<E, 8, 16>, paged_attn_kernel<E, 12, 16>};
+  return all[i];
 }
+constexpr int kKernelSize[kKernels][2] = {{64, 64}, {64, 128}, {96, 96}, {96, 128}, {128, 64}, {128, 128}, {192, 128}};
 
 // Kernel attributes and the tensor-map encoder; the first call on a device.
 mla_status init_device(int* sms) {
@@ -702,15 +738,14 @@ mla_status init_device(int* sms) {
     const mla_status st = tensor_map_encoder(&g_encode);
     if (st != MLA_OK) return st;
     HEADS_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev), "device attributes");
-    for (int kc = 1; kc <= 3; ++kc)
-      for (int vc = 1; vc <= 2; ++vc)
-        for (Kernel k : {kernel_of<__nv_bfloat16>(kc, vc), kernel_of<__half>(kc, vc)})
-        {
-          HEADS_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost), "kernel set-up");
-          cudaFuncAttributes fa;
-          HEADS_CUDA(cudaFuncGetAttributes(&fa, k), "kernel attributes");
-          if (fa.numRegs < kRegs) return fail(MLA_ERR_CUDA, "the kernel was built with %d registers", fa.numRegs);  // what the warps divide
-        }
+    for (int i = 0; i < kKernels; ++i) {
+      for (Kernel k : {kernel_of<__nv_bfloat16>(i), kernel_of<__half>(i)}) {
+        HEADS_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost), "kernel set-up");
+        cudaFuncAttributes fa;
+        HEADS_CUDA(cudaFuncGetAttributes(&fa, k), "kernel attributes");
+        if (fa.numRegs < kRegs) return fail(MLA_ERR_CUDA, "the kernel was built with %d registers", fa.numRegs);  // what the warps divide
+      }
+    }
     d.ready = true;
   }
   *sms = d.sms;
@@ -743,9 +778,10 @@ mla_status launch(const Problem& x, cudaStream_t s) {
   p.G = x.n_q / x.n_kv;
   p.rows = rows_of(x);
   p.tiles = tiles_of(x);
-  p.kc = (x.d_qk + 63) / 64;
-  p.vc = (x.d_v + 63) / 64;
-  p.ks = (x.d_qk + 15) / 16;
+  int kind = 0;
+  while (x.d_qk > kKernelSize[kind][0] || x.d_v > kKernelSize[kind][1]) ++kind;
+  p.kc = (kKernelSize[kind][0] + 63) / 64;
+  p.vc = (kKernelSize[kind][1] + 63) / 64;
   p.unit_bytes = (p.kc + p.vc) * kChunk;
   p.wait_ns = host_wait_limit_ns();
   const int fit = std::min(kMaxSlots, (kSmemMost - 1024 - kOffSlots) / p.unit_bytes);
@@ -763,12 +799,12 @@ mla_status launch(const Problem& x, cudaStream_t s) {
     if (ms != MLA_OK) return ms;
   }
   const bool bf = x.dtype == MLA_ROPE_BF16;
-  const Kernel kernel = bf ? kernel_of<__nv_bfloat16>(p.kc, p.vc) : kernel_of<__half>(p.kc, p.vc);
+  const Kernel kernel = bf ? kernel_of<__nv_bfloat16>(kind) : kernel_of<__half>(kind);
   const size_t smem = 1024 + kOffSlots + static_cast<size_t>(p.pipes) * p.slots * p.unit_bytes;
   kernel<<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(maps, p);
   HEADS_CUDA(cudaGetLastError(), "kernel launch");
   if (p.groups > 1) {
-    const dim3 grid(static_cast<unsigned>(2 * sms));
+    const dim3 grid(static_cast<unsigned>(4 * sms));
     HEADS_CUDA(bf ? launch_after(paged_merge_kernel<__nv_bfloat16>, grid, kMergeThreads, 0, s, p)
                   : launch_after(paged_merge_kernel<__half>, grid, kMergeThreads, 0, s, p),
                "merge launch");
