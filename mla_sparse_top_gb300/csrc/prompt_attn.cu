@@ -480,20 +480,31 @@ __device__ void mend_role(const Params& p, const Ctx& c) {
   }
 }
 
-// The warp stays converged around an elected issuer, so that descriptors live in uniform registers.
+// The warp stays converged around an elected issuer, and what steers it is made
+// uniform, so that descriptors live in uniform registers: an MMA takes 64 clocks,
+// and with loops over runtime counts its issue took 115.
+template <int kKc, int kVc>
 __device__ void mma_role(const Params& p, const Ctx& c) {
+  constexpr int kSlots = kTileSmem / kSlotBytes - 2 * kKc < kMaxSlots ? kTileSmem / kSlotBytes - 2 * kKc : kMaxSlots;
+  constexpr int kVSteps = kVc == 2 ? 4 : 8;
+  constexpr uint32_t kSlot = kSlotBytes >> 4;  // in a descriptor's address field
   const uint64_t desc_q = make_sdesc(c.sb, 16, 1024, kSwizzle128B);
-  const uint64_t desc_k = make_sdesc(c.sb + 2 * p.kc * kSlotBytes, 16, 1024, kSwizzle128B);
-  const uint64_t desc_v = make_sdesc(c.sb + 2 * p.kc * kSlotBytes, kSlotBytes / 2, 1024, kSwizzle128B);
-  const int v_steps = p.vc == 2 ? 4 : 8;
+  const uint64_t desc_k = make_sdesc(c.sb + 2 * kKc * kSlotBytes, 16, 1024, kSwizzle128B);
+  const uint64_t desc_v = make_sdesc(c.sb + 2 * kKc * kSlotBytes, kSlotBytes / 2, 1024, kSwizzle128B);
+  const uint32_t idesc_s = uniform(static_cast<int>(p.idesc_s)), idesc_v = uniform(static_cast<int>(p.idesc_v));
+  const int last_steps = uniform(p.ks_qk) - 4 * (kKc - 1);  // of the last chunk of a key
   Items items;
   Item it;
-  Ring head;                    // next slot that no MMA has used
+  int slot = 0;  // the next that no MMA has used
+  uint32_t phase = 0;
   uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+  auto after = [&](int s, int n) { return s + n >= kSlots ? s + n - kSlots : s + n; };
   auto take = [&](int n) {  // waits for the next n slots
+#pragma unroll
     for (int k = 0; k < n; ++k) {
-      if (!warp_wait(c, kFull + head.slot, head.phase)) return false;
-      head.step(p.slots);
+      if (!warp_wait(c, kFull + slot, phase)) return false;
+      phase ^= slot + 1 == kSlots ? 1u : 0u;
+      slot = after(slot, 1);
     }
     return true;
   };
@@ -501,71 +512,75 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
     if (elect_one()) umma_commit(c.bar(bar));
     __syncwarp();
   };
-  auto release = [&](int slot, int n) {
-    for (int k = 0; k < n; ++k) {
-      commit(kEmpty + slot);
-      if (++slot == p.slots) slot = 0;
-    }
-  };
-  auto scores = [&](int h, int slot) {
-    const uint32_t d = c.tmem + kTmemS + 128 * h;
+  // S_h = Q_h K^T of the keys in `at` and the slots behind it
+  auto scores = [&](int h, int at, bool free_keys, bool last) {
     if (elect_one()) {
-      for (int k = 0; k < p.kc; ++k) {
-        const uint64_t a = desc_q + static_cast<uint32_t>((h * p.kc + k) * (kSlotBytes >> 4));
-        const uint64_t b = desc_k + static_cast<uint32_t>(slot * (kSlotBytes >> 4));
-        const int steps = min(4, p.ks_qk - 4 * k);
-        for (int s = 0; s < steps; ++s) umma_ss(d, a + 2 * s, b + 2 * s, p.idesc_s, (k | s) != 0 ? 1u : 0u);
-        if (++slot == p.slots) slot = 0;
+      const uint32_t d = c.tmem + kTmemS + 128 * h;
+#pragma unroll
+      for (int k = 0; k < kKc; ++k) {
+        const uint64_t a = desc_q + (h * kKc + k) * kSlot;
+        const uint64_t b = desc_k + static_cast<uint32_t>(after(at, k)) * kSlot;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (k + 1 < kKc || s < last_steps) umma_ss(d, a + 2 * s, b + 2 * s, idesc_s, (k | s) != 0 ? 1u : 0u);
       }
       umma_commit(c.bar(kSFull + h));
+      if (free_keys) {
+#pragma unroll
+        for (int k = 0; k < kKc; ++k) umma_commit(c.bar(kEmpty) + 8 * after(at, k));
+      }
+      if (last) umma_commit(c.bar(kQFree + h));
     }
     __syncwarp();
   };
-  auto values = [&](int h, int slot, bool first) {
+  // O_h += P_h V
+  auto values = [&](int h, int at, bool first, bool free_values, bool last) {
     if (elect_one()) {
-      const uint32_t d = c.tmem + kTmemO + 128 * h;
-      uint32_t a = c.tmem + kTmemS + 128 * h;
-      for (int k = 0; k < p.vc; ++k) {
-        const uint64_t b = desc_v + static_cast<uint32_t>(slot * (kSlotBytes >> 4));
-        for (int s = 0; s < v_steps; ++s, a += 8) umma_ts(d, a, b + 128 * s, p.idesc_v, first && (k | s) == 0 ? 0u : 1u);
-        if (++slot == p.slots) slot = 0;
+      const uint32_t d = c.tmem + kTmemO + 128 * h, a = c.tmem + kTmemS + 128 * h;
+#pragma unroll
+      for (int k = 0; k < kVc; ++k) {
+        const uint64_t b = desc_v + static_cast<uint32_t>(after(at, k)) * kSlot;
+#pragma unroll
+        for (int s = 0; s < kVSteps; ++s)
+          umma_ts(d, a + 8 * (k * kVSteps + s), b + 128 * s, idesc_v, (k | s) == 0 && first ? 0u : 1u);
       }
+      if (free_values) {
+#pragma unroll
+        for (int k = 0; k < kVc; ++k) umma_commit(c.bar(kEmpty) + 8 * after(at, k));
+      }
+      if (last) umma_commit(c.bar(kOFull + h));
     }
     __syncwarp();
   };
   bool ok = true;
   while (ok && items.next(c, it)) {
-    const int end = max(it.ta, it.tb);
-    if (it.t0 >= end) continue;
-    int key = head.slot;
-    ok = take(p.kc);
-    for (int h = 0; h < 2 && ok; ++h) {
-      if (it.t0 >= it.t1(h)) continue;
+    const int t0 = uniform(it.t0), ta = uniform(it.ta), tb = uniform(it.tb), end = max(ta, tb);
+    if (t0 >= end) continue;
+    int key = slot;
+    ok = take(kKc);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t1 = h == 0 ? ta : tb;
+      if (!ok || t0 >= t1) continue;
       ok = warp_wait(c, kQFull + h, q_uses[h]++ & 1);
-      if (!ok) break;
-      scores(h, key);
-      if (it.t0 + 1 == it.t1(h)) commit(kQFree + h);
+      if (ok) scores(h, key, h == (t0 < tb ? 1 : 0), t0 + 1 == t1);
     }
-    if (ok) release(key, p.kc);
-    for (int t = it.t0; t < end && ok; ++t) {
-      const int value = head.slot;
-      ok = take(p.vc);
-      key = head.slot;
-      if (ok && t + 1 < end) ok = take(p.kc);
-      for (int h = 0; h < 2 && ok; ++h) {
-        if (t >= it.t1(h)) continue;
+    for (int t = t0; t < end && ok; ++t) {
+      const int value = slot;
+      ok = take(kVc);
+      key = slot;
+      if (ok && t + 1 < end) ok = take(kKc);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t1 = h == 0 ? ta : tb;
+        if (!ok || t >= t1) continue;
         ok = warp_wait(c, kPReady + h, p_uses[h]++ & 1);
-        if (!ok) break;
+        if (!ok) continue;
         tc_fence_after();
-        values(h, value, t == it.t0);
-        if (t + 1 == it.t1(h)) commit(kOFull + h);
-        if (h == (t < it.tb ? 1 : 0)) release(value, p.vc);
-        if (t + 1 < it.t1(h)) {
-          scores(h, key);
-          if (t + 2 == it.t1(h)) commit(kQFree + h);
-        }
+        // the last row tile that reads a key or value tile gives its slots up
+        values(h, value, t == t0, h == (t < tb ? 1 : 0), t + 1 == t1);
+        if (t + 1 < t1) scores(h, key, h == (t + 1 < tb ? 1 : 0), t + 2 == t1);
       }
-      if (ok && t + 1 < end) release(key, p.kc);
     }
   }
   // every MMA in flight lands before the CTA leaves
@@ -573,6 +588,17 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
   volatile uint32_t never = 0;
   mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > 500000000ull ? c.wait_ns : 500000000ull);
   __syncwarp();
+}
+
+__device__ __forceinline__ void mma_role(const Params& p, const Ctx& c) {
+  switch (2 * p.kc + p.vc) {
+    case 3: return mma_role<1, 1>(p, c);
+    case 4: return mma_role<1, 2>(p, c);
+    case 5: return mma_role<2, 1>(p, c);
+    case 6: return mma_role<2, 2>(p, c);
+    case 7: return mma_role<3, 1>(p, c);
+    default: return mma_role<3, 2>(p, c);
+  }
 }
 
 // The NaN of values that are not finite, which mending took from a row: keys [lo,
