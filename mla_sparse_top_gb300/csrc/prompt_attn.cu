@@ -92,16 +92,18 @@ struct Head {
   int items;    // parts of all items
   int next;     // drawn so far
   int merges;   // items that were cut
-  int pad[5];
+  int cap;      // key tiles of a part at most
+  int pad[4];
 };
 
 struct Params {
   Problem x;
   Head* head;
-  int* first;    // [B + 1] first item of a sequence
-  int* cuts;     // [B] parts of each of its items
+  // of the sequences in the order in which they are taken up
+  int* first;    // [B + 1] first part of an item
   int* part0;    // [B] first partial state
   int* merge0;   // [B + 1] first item to join
+  int* order;    // [B] the sequence
   float* parts;
   int part_floats, max_parts;
   int G, tpt;    // heads to a key head, tokens of a row tile
@@ -161,9 +163,66 @@ __device__ __forceinline__ int seen_by(const Params& p, const Seq& s, int tokens
 }
 __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 
+// How the items of a key head of a sequence are cut: the pair of row tiles m into
+// of(m) parts of at most `cap` tiles.  The later a pair, the more keys it sees, so
+// parts are numbered from the last pair to the first: all that are cut come before
+// those that are whole.
+struct Cuts {
+  int pairs, most, cap;  // pairs, parts of the last one
+  int rows, len, pos;    // tokens of a pair, keys, position of query 0
+  bool causal, none;
+  __device__ __forceinline__ Cuts(const Params& p, const Seq& s, int cap_)
+      : pairs(s.pairs), cap(cap_), rows(2 * p.tpt), len(s.len), pos(s.pos), causal(p.x.causal != 0), none(s.n == 0) {
+    most = max(1, (tiles_of(seen_by(p, s, s.n)) + cap - 1) / cap);
+  }
+  // pairs that are cut into `c` parts or more: those that see more than c - 1 parts' keys
+  __device__ __forceinline__ int at_least(int c) const {
+    if (c <= 1 || pairs <= 1) return c <= most ? pairs : 0;
+    const int64_t keys = static_cast<int64_t>(c - 1) * cap * kTile;
+    if (none || len <= keys) return 0;
+    if (!causal) return pairs;
+    const uint32_t behind = static_cast<uint32_t>(max(static_cast<int64_t>(0), keys - pos));  // below 2^32: keys < len
+    return pairs - static_cast<int>(min(static_cast<uint32_t>(pairs), behind / static_cast<uint32_t>(rows)));
+  }
+  __device__ __forceinline__ int64_t parts() const {  // of a key head
+    int64_t n = 0;
+    for (int c = 1; c <= most; ++c) n += at_least(c);
+    return n;
+  }
+  __device__ __forceinline__ int64_t cut_parts() const { return parts() - (pairs - at_least(2)); }
+  // pair, part and parts of a key head's part k
+  __device__ __forceinline__ void find(int64_t k, int& m, int& cut, int& cuts) const {
+    int behind = 0;  // pairs with more parts
+    for (int c = most;; --c) {
+      const int here = at_least(c) - behind;
+      if (c == 1 || k < static_cast<int64_t>(here) * c) {
+        m = pairs - 1 - behind - static_cast<int>(k / c);
+        cut = static_cast<int>(k % c);
+        cuts = c;
+        return;
+      }
+      k -= static_cast<int64_t>(here) * c;
+      behind += here;
+    }
+  }
+  // parts of a key head before the first one of its i-th pair from the end, and that pair's
+  __device__ __forceinline__ int64_t before(int i, int& cuts) const {
+    int64_t n = 0;
+    cuts = 0;
+    for (int c = 1; c <= most; ++c) {
+      const int there = at_least(c);
+      n += min(i, there);
+      if (i < there) cuts = c;
+    }
+    return n;
+  }
+};
+
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 512;
-constexpr int kMinTiles = 4;  // key tiles of a part at least
+constexpr int kMinTiles = 4;    // key tiles of a part at least
+constexpr int kPartCost = 5;    // of a partial state, its way out and back, in key tiles
+constexpr int kRankSeqs = 256;  // sequences of which the longest come first
 
 // Sums over the threads before this one, and over the block.
 template <int N>
@@ -193,67 +252,112 @@ __device__ __forceinline__ void plan_scan(int64_t (&v)[N], int64_t (&total)[N], 
   __syncthreads();
 }
 
-// One block: counts the items, decides what is cut, numbers everything.
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// One block: counts the work, decides what is cut, puts the sequences with the
+// longest items first, which leaves short ones to even out the end, and numbers
+// everything.  Every call waits for it, so it goes round the block three times only.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_constant__ Params p) {
-  __shared__ int64_t part[3][kPlanThreads / 32];
-  const int B = p.x.B, Hkv = p.x.n_kv;
+  constexpr int kWarps = kPlanThreads / 32, kCandidates = 4;
+  __shared__ int64_t part[3][kWarps];
+  __shared__ int64_t work_of[kWarps], cost_of[kCandidates];
+  __shared__ int most_of[kWarps], lengths[kRankSeqs], order[kRankSeqs];
+  const int B = p.x.B, Hkv = p.x.n_kv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunks = (B + kPlanThreads - 1) / kPlanThreads;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int64_t mine[2] = {0, 0}, all[2];  // items, key tiles
+  int64_t work = 0;  // key tiles
+  int most = 0;      // of an item
   bool bad_len = false, bad_table = false;
   for (int c = 0; c < chunks; ++c) {
-    const int b = c * kPlanThreads + threadIdx.x;
+    const int b = c * kPlanThreads + tid;
     if (b >= B) break;
     const Seq s = load_seq(p, b);
     bad_len = bad_len || s.bad_len;
     bad_table = bad_table || s.bad_table;
-    mine[0] += static_cast<int64_t>(s.pairs) * Hkv;
+    const int last = tiles_of(seen_by(p, s, s.n));
     // the tiles of the first and the last pair, between which they grow evenly
-    mine[1] += static_cast<int64_t>(s.pairs) * Hkv * (tiles_of(seen_by(p, s, 2 * p.tpt)) + tiles_of(seen_by(p, s, s.n))) / 2;
+    work += static_cast<int64_t>(s.pairs) * Hkv * (tiles_of(seen_by(p, s, 2 * p.tpt)) + last) / 2;
+    most = max(most, last);
+    if (B <= kRankSeqs) lengths[b] = last;
   }
   if (bad_len || bad_table)
     atomicOr(&g_prompt_status, (bad_len ? MLA_DEVICE_BAD_LENGTH : 0u) | (bad_table ? MLA_DEVICE_BAD_BLOCK : 0u));
-  plan_scan(mine, all, part);
-  // parts of at most `cap` tiles, so many that every SM has some; fewer where their states would not fit
-  int64_t cap = max(static_cast<int64_t>(kMinTiles), (all[1] + p.sms - 1) / p.sms);
-  while (true) {
-    int64_t carry[3] = {0, 0, 0};  // items, partial states, items to join
-    for (int c = 0; c < chunks; ++c) {
-      const int b = c * kPlanThreads + threadIdx.x;
-      int64_t v[3] = {0, 0, 0}, sum[3];
-      int cuts = 1;
-      if (b < B) {
-        const Seq s = load_seq(p, b);
-        const int64_t most = tiles_of(seen_by(p, s, s.n));
-        cuts = static_cast<int>(max(static_cast<int64_t>(1), (most + cap - 1) / cap));
-        v[0] = static_cast<int64_t>(s.pairs) * Hkv * cuts;
-        if (cuts > 1) {
-          v[1] = v[0];
-          v[2] = static_cast<int64_t>(s.pairs) * Hkv;
-        }
-      }
-      plan_scan(v, sum, part);
-      if (b < B) {
-        p.first[b] = static_cast<int>(carry[0] + v[0]);
-        p.cuts[b] = cuts;
-        p.part0[b] = static_cast<int>(carry[1] + v[1]);
-        p.merge0[b] = static_cast<int>(carry[2] + v[2]);
-      }
+  work = warp_sum(work);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    work_of[warp] = work;
+    most_of[warp] = most;
+  }
+  __syncthreads();
+  work = 0;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) carry[i] += sum[i];
+  for (int w = 0; w < kWarps; ++w) {
+    work += work_of[w];
+    most = max(most, most_of[w]);
+  }
+  // Parts of at most `cap` tiles.  Of no cuts and of parts of an SM's share, a half, a third or a
+  // fifth of it, what is estimated to end first: work and states shared out evenly, and half of the
+  // longest part behind that (twice that time, times SMs).  A warp to each.
+  const int share = static_cast<int>(min((work + p.sms - 1) / p.sms, static_cast<int64_t>(1) << 24));
+  auto cap_of = [&](int i) { return max(kMinTiles, share / (i == 3 ? 5 : i + 1)); };
+  if (warp < kCandidates) {
+    const int cap = cap_of(warp);
+    int64_t n = 0;
+    if (cap < most && p.max_parts > 0)
+      for (int b = lane; b < B; b += 32) n += Cuts(p, load_seq(p, b), cap).cut_parts() * Hkv;
+    n = warp_sum(n);
+    if (lane == 0)
+      cost_of[warp] = cap < most && n <= p.max_parts ? 2 * (work + kPartCost * n) + static_cast<int64_t>(cap) * p.sms : INT64_MAX;
+  } else if (warp == kCandidates) {  // ranks
+    for (int b = lane; b < B && B <= kRankSeqs; b += 32) {
+      int rank = 0;
+      for (int i = 0; i < B; ++i) rank += lengths[i] > lengths[b] || (lengths[i] == lengths[b] && i < b) ? 1 : 0;
+      order[rank] = b;
     }
-    if (carry[1] > p.max_parts) {
-      cap *= 2;
-      continue;
+  }
+  __syncthreads();
+  int cap = max(most, 1);
+  int64_t least = 2 * work + static_cast<int64_t>(most) * p.sms;
+#pragma unroll
+  for (int i = 0; i < kCandidates; ++i) {
+    if (cost_of[i] < least) {
+      least = cost_of[i];
+      cap = cap_of(i);
     }
-    if (threadIdx.x == 0) {
-      p.first[B] = static_cast<int>(carry[0]);
-      p.merge0[B] = static_cast<int>(carry[2]);
-      p.head->items = static_cast<int>(carry[0]);
-      p.head->merges = static_cast<int>(carry[2]);
-      p.head->next = 0;
+  }
+  int64_t carry[3] = {0, 0, 0};  // parts, partial states, items to join
+  for (int c = 0; c < chunks; ++c) {
+    const int i = c * kPlanThreads + tid;
+    int64_t v[3] = {0, 0, 0}, sum[3];
+    if (i < B) {
+      const int b = B <= kRankSeqs ? order[i] : i;
+      const Cuts cuts(p, load_seq(p, b), cap);
+      v[0] = cuts.parts() * Hkv;
+      v[2] = static_cast<int64_t>(cuts.at_least(2)) * Hkv;
+      v[1] = v[0] - (static_cast<int64_t>(cuts.pairs) * Hkv - v[2]);
+      p.order[i] = b;
     }
-    return;
+    plan_scan(v, sum, part);
+    if (i < B) {
+      p.first[i] = static_cast<int>(carry[0] + v[0]);
+      p.part0[i] = static_cast<int>(carry[1] + v[1]);
+      p.merge0[i] = static_cast<int>(carry[2] + v[2]);
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) carry[j] += sum[j];
+  }
+  if (tid == 0) {
+    p.first[B] = static_cast<int>(carry[0]);
+    p.merge0[B] = static_cast<int>(carry[2]);
+    p.head->items = static_cast<int>(carry[0]);
+    p.head->merges = static_cast<int>(carry[2]);
+    p.head->next = 0;
+    p.head->cap = cap;
   }
 }
 
@@ -316,26 +420,52 @@ __device__ __forceinline__ int page_of(const Params& p, int b, int t) {
 }
 
 __device__ void plan_role(const Params& p, const Ctx& c) {
-  const int total = __ldcg(&p.head->items), lane = threadIdx.x & 31;
+  const int total = __ldcg(&p.head->items), cap = __ldcg(&p.head->cap), lane = threadIdx.x & 31, B = p.x.B;
   uint32_t count = 0;
-  int i = blockIdx.x;
+  int i = blockIdx.x, drawn = 0;
+  // a lane keeps a sequence, where there are no more than 32: no item waits for its description then
+  const bool kept = B <= 32;
+  int first = 0x7FFFFFFF, part0 = 0, seq = 0;
+  Seq mine = {};
+  auto load = [&](int at) {
+    seq = __ldcg(p.order + at);
+    first = __ldcg(p.first + at);
+    part0 = __ldcg(p.part0 + at);
+    mine = load_seq(p, seq);
+  };
+  if (kept && lane < B) load(lane);
   while (true) {
     Item it;
     it.live = i < total ? 1 : 0;
     if (it.live) {
-      const int b = find_seq(p.first, p.x.B, i), cuts = __ldcg(p.cuts + b), Hkv = p.x.n_kv;
-      const Seq s = load_seq(p, b);
-      int k = i - __ldcg(p.first + b);
-      // heads whose keys and values fill about a third of L2 go side by side
-      const int64_t bytes = static_cast<int64_t>(max(1, s.len)) * (p.x.d_qk + p.x.d_v) * 2;
-      const int group = static_cast<int>(min(static_cast<int64_t>(Hkv), max(static_cast<int64_t>(1), (int64_t(40) << 20) / bytes)));
-      const int64_t per_group = static_cast<int64_t>(s.pairs) * group * cuts;
-      const int g = static_cast<int>(k / per_group);
-      k -= static_cast<int>(g * per_group);
-      const int heads = min(group, Hkv - g * group);
-      const int m = s.pairs - 1 - k / (heads * cuts);
-      k %= heads * cuts;
-      const int cut = k / heads, hk = g * group + k % heads;
+      if (lane == 0) drawn = static_cast<int>(gridDim.x) + atomicAdd(&p.head->next, 1);  // the item behind this one
+      int from = 0;  // the lane that has the sequence
+      if (kept) from = __popc(__ballot_sync(0xffffffffu, first <= i)) - 1;
+      else load(find_seq(p.first, B, i));
+      auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, from); };
+      Seq s;
+      s.n = of(mine.n);
+      s.len = of(mine.len);
+      s.pos = of(mine.pos);
+      s.q0 = of(mine.q0);
+      s.key0 = of(mine.key0);
+      s.pairs = of(mine.pairs);
+      s.bad_len = s.bad_table = false;
+      const int b = of(seq), Hkv = p.x.n_kv;
+      const Cuts how(p, s, cap);
+      int k = i - of(first), m, hk, cut = 0, cuts = 1;
+      if (how.at_least(2) > 0) {
+        how.find(k / Hkv, m, cut, cuts);
+        hk = k % Hkv;
+      } else {
+        // heads whose keys and values fill about a third of L2 go side by side
+        const int64_t bytes = static_cast<int64_t>(max(1, s.len)) * (p.x.d_qk + p.x.d_v) * 2;
+        const int group = static_cast<int>(min(static_cast<int64_t>(Hkv), max(static_cast<int64_t>(1), (int64_t(40) << 20) / bytes)));
+        const int64_t per_group = static_cast<int64_t>(s.pairs) * group;
+        const int g = static_cast<int>(k / per_group), heads = min(group, Hkv - g * group), r = static_cast<int>(k - g * per_group);
+        m = s.pairs - 1 - r / heads;
+        hk = g * group + r % heads;
+      }
       it.b = b;
       it.hk = hk;
       it.m = m;
@@ -354,7 +484,7 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
       it.ta = max(it.t0, min(tiles[0], end));
       it.tb = max(it.t0, min(tiles[1], end));
       it.lo = seen_by(p, s, tok + 1);
-      it.part = cuts > 1 ? __ldcg(p.part0 + b) + (m * Hkv + hk) * cuts + cut : -1;
+      it.part = cuts > 1 ? of(part0) + k : -1;
     }
     const int s = count % kItemSlots;
     if (!warp_wait(c, kItemEmpty + s, ((count / kItemSlots) & 1) ^ 1)) return;
@@ -365,8 +495,7 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
     __syncwarp();
     if (!it.live) return;
     ++count;
-    if (lane == 0) i = static_cast<int>(gridDim.x) + atomicAdd(&p.head->next, 1);
-    i = uniform(i);
+    i = uniform(drawn);
   }
 }
 
@@ -878,42 +1007,67 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the parts of the items that were cut: a thread takes one row and kMergeCols columns.
-constexpr int kMergeCols = 8;
+// Joins the parts of the items that were cut: a block takes the 128 rows of a row
+// tile and a quarter of the columns, a thread one row and four columns at a time.
+constexpr int kMergeThreads = 256, kMergeSlices = 4, kAhead = 2;  // parts in flight
+constexpr int kMergeQuads = kMaxDv / 4 / kMergeSlices / 2;          // four columns each, of a thread
 template <typename E>
-__global__ void __launch_bounds__(128) prompt_merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int merges = __ldcg(&p.head->merges), row = threadIdx.x, slices = p.x.d_v / kMergeCols;
-  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(merges) * 2 * slices; w += gridDim.x) {
-    const int slice = static_cast<int>(w % slices), h = static_cast<int>(w / slices) & 1, i = static_cast<int>(w / slices >> 1);
-    const int b = find_seq(p.merge0, p.x.B, i), cuts = __ldcg(p.cuts + b);
-    const Seq s = load_seq(p, b);
-    const int k = i - __ldcg(p.merge0 + b), m = k / p.x.n_kv, hk = k % p.x.n_kv;
+  const int merges = __ldcg(&p.head->merges), cap = __ldcg(&p.head->cap);
+  const int row = threadIdx.x & 127, side = threadIdx.x >> 7, quads = p.x.d_v / 4, Hkv = p.x.n_kv;
+  const int per_slice = (quads + kMergeSlices - 1) / kMergeSlices;  // at most 2 * kMergeQuads
+  const int64_t step = static_cast<int64_t>(p.part_floats) * Hkv;           // a pair's parts: heads lie between them
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(merges) * 2 * kMergeSlices; w += gridDim.x) {
+    const int slice = static_cast<int>(w % kMergeSlices), h = static_cast<int>(w / kMergeSlices) & 1, i = static_cast<int>(w / kMergeSlices >> 1);
+    const int pos = find_seq(p.merge0, p.x.B, i);
+    const Seq s = load_seq(p, __ldcg(p.order + pos));
+    const int k = i - __ldcg(p.merge0 + pos), hk = k % Hkv, m = s.pairs - 1 - k / Hkv;
+    int cuts;
+    const int64_t before = Cuts(p, s, cap).before(k / Hkv, cuts);
     const int tok_in = row / p.G, tok = (2 * m + h) * p.tpt + tok_in;
     const bool put = tok_in < p.tpt && tok < (p.x.S1 > 0 ? p.x.S1 : s.n);
-    const float* src = p.parts + static_cast<int64_t>(__ldcg(p.part0 + b) + k * cuts) * p.part_floats + h * (p.part_floats / 2);
-    float top = -INFINITY, l = 0.f, o[kMergeCols] = {};
-    for (int c = 0; c < cuts; ++c, src += p.part_floats) {
-      const float mk = __ldcg(src + 128 * p.x.d_v + row), lk = __ldcg(src + 128 * p.x.d_v + 128 + row);
-      if (mk == -INFINITY) continue;
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(src) + slice * 2 * 128 + row);
-      const float4 d = __ldcg(reinterpret_cast<const float4*>(src) + (slice * 2 + 1) * 128 + row);
-      const float next = fmaxf(top, mk), f = top == -INFINITY ? 0.f : exp2f(top - next), e = exp2f(mk - next);
-      top = next;
-      l = l * f + lk * e;
-      const float v[kMergeCols] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+    const float* src = p.parts + (__ldcg(p.part0 + pos) + before * Hkv + hk) * p.part_floats + h * (p.part_floats / 2);
+    const int quad0 = slice * per_slice + side, quad1 = min(quads, (slice + 1) * per_slice);
+    float top = -INFINITY, l = 0.f, o[kMergeQuads][4] = {};
+    for (int c0 = 0; c0 < cuts; c0 += kAhead) {
+      float mk[kAhead], lk[kAhead];
+      float4 x[kAhead][kMergeQuads];
 #pragma unroll
-      for (int j = 0; j < kMergeCols; ++j) o[j] = o[j] * f + v[j] * e;
+      for (int u = 0; u < kAhead; ++u) {
+        const float* part = src + min(c0 + u, cuts - 1) * step;
+        mk[u] = __ldcg(part + 128 * p.x.d_v + row);
+        lk[u] = __ldcg(part + 128 * p.x.d_v + 128 + row);
+#pragma unroll
+        for (int q = 0; q < kMergeQuads; ++q)
+          x[u][q] = quad0 + 2 * q < quad1 ? __ldcg(reinterpret_cast<const float4*>(part) + (quad0 + 2 * q) * 128 + row) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (c0 + u >= cuts || mk[u] == -INFINITY) continue;  // a part in which the row sees nothing
+        const float next = fmaxf(top, mk[u]), f = top == -INFINITY ? 0.f : exp2f(top - next), w = exp2f(mk[u] - next);
+        top = next;
+        l = l * f + lk[u] * w;
+#pragma unroll
+        for (int q = 0; q < kMergeQuads; ++q) {
+          o[q][0] = o[q][0] * f + x[u][q].x * w;
+          o[q][1] = o[q][1] * f + x[u][q].y * w;
+          o[q][2] = o[q][2] * f + x[u][q].z * w;
+          o[q][3] = o[q][3] * f + x[u][q].w * w;
+        }
+      }
     }
-    if (!put) continue;
     const bool nothing = l == 0.f;
     const float inv = nothing ? 0.f : 1.f / l;
     const int64_t at = static_cast<int64_t>(s.q0 + tok) * p.x.n_q + hk * p.G + (row - tok_in * p.G);
-    uint32_t y[kMergeCols / 2];
 #pragma unroll
-    for (int j = 0; j < kMergeCols / 2; ++j) y[j] = nothing ? 0u : pack16<E>(o[2 * j] * inv, o[2 * j + 1] * inv);
-    *reinterpret_cast<uint4*>(static_cast<E*>(p.x.out) + at * p.x.d_v + slice * kMergeCols) = make_uint4(y[0], y[1], y[2], y[3]);
-    if (slice == 0 && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+    for (int q = 0; q < kMergeQuads; ++q) {
+      uint2 y = make_uint2(pack16<E>(o[q][0] * inv, o[q][1] * inv), pack16<E>(o[q][2] * inv, o[q][3] * inv));
+      if (nothing) y = make_uint2(0u, 0u);
+      if (put && quad0 + 2 * q < quad1) *reinterpret_cast<uint2*>(static_cast<E*>(p.x.out) + at * p.x.d_v + (quad0 + 2 * q) * 4) = y;
+    }
+    if (put && slice == 0 && side == 0 && p.x.lse != nullptr)
+      p.x.lse[at] = nothing ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
   }
 }
 
@@ -986,9 +1140,9 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(x.workspace);
   p.head = reinterpret_cast<Head*>(ws);
   p.first = reinterpret_cast<int*>(ws + sizeof(Head));
-  p.cuts = p.first + x.B + 1;
-  p.part0 = p.cuts + x.B;
+  p.part0 = p.first + x.B + 1;
   p.merge0 = p.part0 + x.B;
+  p.order = p.merge0 + x.B + 1;
   p.parts = reinterpret_cast<float*>(ws + lists_bytes(x));
   p.part_floats = part_floats(x);
   p.max_parts = parts_of(x);
@@ -1031,8 +1185,8 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
                 : launch_after(prompt_attn_kernel<__half>, grid, kThreads, kSmemBytes, s, maps, p),
              "kernel launch");
   if (p.max_parts > 0)
-    HEADS_CUDA(bf ? launch_after(prompt_merge_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(4 * sms)), 128, 0, s, p)
-                  : launch_after(prompt_merge_kernel<__half>, dim3(static_cast<unsigned>(4 * sms)), 128, 0, s, p),
+    HEADS_CUDA(bf ? launch_after(prompt_merge_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(4 * sms)), kMergeThreads, 0, s, p)
+                  : launch_after(prompt_merge_kernel<__half>, dim3(static_cast<unsigned>(4 * sms)), kMergeThreads, 0, s, p),
                "merge launch");
   return MLA_OK;
 }
