@@ -46,11 +46,23 @@ constexpr int kThreads = 384;
 constexpr int kRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kRegs, "register budget");
 constexpr int kTile = 128;
-constexpr int kSlotBytes = 16384;
-constexpr int kMaxSlots = 12;
-constexpr int kTileSmem = 14 * kSlotBytes;  // Q and ring together
+constexpr int kChunk = 16384;  // 128 rows of 64 columns
+constexpr int kMaxSlots = 20;
+constexpr int kTileSmem = 14 * kChunk;  // Q and ring together
 constexpr int kItemSlots = 2;
 constexpr int kItemReaders = kSoftmaxWarps + 3;  // MMA, load and mend warps
+
+// A CTA alone, or a pair of them that shares the keys and values of its rows.
+template <bool kPair>
+struct Shape {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kTiles = 2 * kCtas;  // row tiles of an item
+  static constexpr int kSlotBytes = kChunk / kCtas;
+  __host__ __device__ static constexpr int slots(int kc) {
+    const int n = (kTileSmem - 2 * kc * kChunk) / kSlotBytes;
+    return n < kMaxSlots ? n : kMaxSlots;
+  }
+};
 
 constexpr int kFull = 0;                     // [kMaxSlots] the slot's bytes have landed and are mended
 constexpr int kEmpty = kFull + kMaxSlots;    // [kMaxSlots] the MMAs that read the slot are complete
@@ -67,10 +79,10 @@ constexpr int kNumBars = kFinal + 1;
 
 struct Item {
   int live;        // 0: no more items
-  int b, hk, m;    // sequence, key head, pair of row tiles
+  int b, hk, m;    // sequence, key head, group of row tiles
   int n, len, pos; // queries, keys within the table, position of query 0 (may be negative)
   int q0, key0;    // first query row, first packed key row
-  int t0, ta, tb;  // key tiles [t0, ta) of row tile 0, [t0, tb) of row tile 1
+  int t0, ta, tb;  // key tiles [t0, ta) of a CTA's row tile 0, [t0, tb) of row tile 1
   int lo;          // keys from here on are not seen by every row
   int part;        // slot of a partial state, -1: the item is whole
   int pad[2];
@@ -107,9 +119,10 @@ struct Params {
   float* parts;
   int part_floats, max_parts;
   int G, tpt;    // heads to a key head, tokens of a row tile
-  int kc, vc;    // 64-column chunks of a key, slots of a value tile
+  int tiles, span;  // row tiles of an item, tokens of them
+  int kc, vc;    // 64-column chunks of a key, of a value
   int slots;
-  int sms;
+  int sms;       // or pairs of them
   uint32_t idesc_s, idesc_v;
   int ks_qk;     // 16-wide steps of a key
   unsigned long long wait_ns;
@@ -153,7 +166,7 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
   s.pos = len - s.n;
   // padded rows are items too: they are written
   const int tokens = x.S1 > 0 ? x.S1 : s.n;
-  s.pairs = (tokens + 2 * p.tpt - 1) / (2 * p.tpt);
+  s.pairs = (tokens + p.span - 1) / p.span;
   return s;
 }
 // Keys that the first `tokens` queries see.
@@ -172,7 +185,7 @@ struct Cuts {
   int rows, len, pos;    // tokens of a pair, keys, position of query 0
   bool causal, none;
   __device__ __forceinline__ Cuts(const Params& p, const Seq& s, int cap_)
-      : pairs(s.pairs), cap(cap_), rows(2 * p.tpt), len(s.len), pos(s.pos), causal(p.x.causal != 0), none(s.n == 0) {
+      : pairs(s.pairs), cap(cap_), rows(p.span), len(s.len), pos(s.pos), causal(p.x.causal != 0), none(s.n == 0) {
     most = max(1, (tiles_of(seen_by(p, s, s.n)) + cap - 1) / cap);
   }
   // pairs that are cut into `c` parts or more: those that see more than c - 1 parts' keys
@@ -281,7 +294,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     bad_table = bad_table || s.bad_table;
     const int last = tiles_of(seen_by(p, s, s.n));
     // the tiles of the first and the last pair, between which they grow evenly
-    work += static_cast<int64_t>(s.pairs) * Hkv * (tiles_of(seen_by(p, s, 2 * p.tpt)) + last) / 2;
+    work += static_cast<int64_t>(s.pairs) * Hkv * (tiles_of(seen_by(p, s, p.span)) + last) / 2;
     most = max(most, last);
     if (B <= kRankSeqs) lengths[b] = last;
   }
@@ -380,12 +393,71 @@ __device__ __forceinline__ int find_seq(const int* first, int B, int i) {
 struct Ctx {
   uint32_t sb;
   uint8_t* smem;
-  uint32_t tmem;
+  uint32_t tmem, rank;  // of the CTA in its pair
   uint64_t wait_ns;
   volatile uint32_t* abort;
   __device__ uint32_t bar(int i) const { return sb + kOffBars + 8 * i; }
   __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
 };
+// Arrivals on a barrier of the pair's first CTA (or the only one).  Release at CTA scope:
+// what they hand over is tensor memory or shared memory of the arriving CTA, already
+// ordered for the tensor core (tcgen05.wait, fence.proxy.async).
+template <bool kPair>
+__device__ __forceinline__ uint32_t lead(uint32_t bar) {
+  return kPair ? mapa_shared(bar, 0) : bar;
+}
+template <bool kPair>
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  if constexpr (kPair) asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+  else mbar_arrive(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void arrive_tx(uint32_t bar, uint32_t bytes) {
+  if constexpr (kPair)
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cluster.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
+  else mbar_arrive_expect_tx(bar, bytes);
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar) : "memory");
+}
+// Loads whose bytes count on a barrier of either CTA of the pair.
+template <bool kPair>
+__device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+  else tma_3d(dst, map, x, y, z, bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+  else tma_4d(dst, map, x, y, z, w, bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (kPair)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+  else umma_ss(d, a, b, idesc, acc);
+}
+template <bool kPair>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (kPair)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+  else umma_ts(d, a, b, idesc, acc);
+}
+// Arrive on the barrier at this offset, of both CTAs, when the MMAs issued so far are complete.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+  else umma_commit(bar);
+}
+
 struct Ring {
   int slot = 0;
   uint32_t phase = 0;
@@ -398,17 +470,21 @@ struct Ring {
 };
 
 // A reader's walk over the items that the plan warp posts.
+template <bool kPair>
 struct Items {
   uint32_t count = 0;
   __device__ __forceinline__ bool next(const Ctx& c, Item& it) {
     const int s = count % kItemSlots;
-    if (!warp_wait(c, kItemFull + s, (count / kItemSlots) & 1)) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait<kPair>(c.bar(kItemFull + s), (count / kItemSlots) & 1, c.abort, c.wait_ns))) return false;
     const int4* src = reinterpret_cast<const int4*>(c.smem + kOffItems) + s * (sizeof(Item) / 16);
     int4* dst = reinterpret_cast<int4*>(&it);
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(Item) / 16); ++i) dst[i] = src[i];
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(c.bar(kItemEmpty + s));
+    if ((threadIdx.x & 31) == 0) {
+      if constexpr (kPair) arrive_cluster(lead<true>(c.bar(kItemEmpty + s)));
+      else mbar_arrive(c.bar(kItemEmpty + s));
+    }
     ++count;
     return uniform(it.live) != 0;
   }
@@ -419,10 +495,12 @@ __device__ __forceinline__ int page_of(const Params& p, int b, int t) {
   return id >= 0 && id < p.x.num_blocks ? id : -1;
 }
 
+template <bool kPair>
 __device__ void plan_role(const Params& p, const Ctx& c) {
   const int total = __ldcg(&p.head->items), cap = __ldcg(&p.head->cap), lane = threadIdx.x & 31, B = p.x.B;
   uint32_t count = 0;
-  int i = blockIdx.x, drawn = 0;
+  constexpr int kCtas = Shape<kPair>::kCtas;
+  int i = blockIdx.x / kCtas, drawn = 0;
   // a lane keeps a sequence, where there are no more than 32: no item waits for its description then
   const bool kept = B <= 32;
   int first = 0x7FFFFFFF, part0 = 0, seq = 0;
@@ -438,7 +516,7 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
     Item it;
     it.live = i < total ? 1 : 0;
     if (it.live) {
-      if (lane == 0) drawn = static_cast<int>(gridDim.x) + atomicAdd(&p.head->next, 1);  // the item behind this one
+      if (lane == 0) drawn = static_cast<int>(gridDim.x) / kCtas + atomicAdd(&p.head->next, 1);  // the item behind this one
       int from = 0;  // the lane that has the sequence
       if (kept) from = __popc(__ballot_sync(0xffffffffu, first <= i)) - 1;
       else load(find_seq(p.first, B, i));
@@ -474,10 +552,10 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
       it.pos = s.pos;
       it.q0 = s.q0;
       it.key0 = s.key0;
-      const int tok = 2 * m * p.tpt;
+      const int tok = m * p.span, half = p.span / 2;
       int tiles[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) tiles[h] = tok + h * p.tpt < s.n ? tiles_of(seen_by(p, s, tok + (h + 1) * p.tpt)) : 0;
+      for (int h = 0; h < 2; ++h) tiles[h] = tok + h * half < s.n ? tiles_of(seen_by(p, s, tok + (h + 1) * half)) : 0;
       const int most = max(tiles[0], tiles[1]);
       it.t0 = static_cast<int>(static_cast<int64_t>(most) * cut / cuts);
       const int end = static_cast<int>(static_cast<int64_t>(most) * (cut + 1) / cuts);
@@ -487,10 +565,18 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
       it.part = cuts > 1 ? of(part0) + k : -1;
     }
     const int s = count % kItemSlots;
-    if (!warp_wait(c, kItemEmpty + s, ((count / kItemSlots) & 1) ^ 1)) return;
+    if (!__all_sync(0xffffffffu, mbar_wait<kPair>(c.bar(kItemEmpty + s), ((count / kItemSlots) & 1) ^ 1, c.abort, c.wait_ns))) return;
     if (lane == 0) {
       reinterpret_cast<Item*>(c.smem + kOffItems)[s] = it;
       mbar_arrive(c.bar(kItemFull + s));
+      if constexpr (kPair) {
+        const uint32_t at = mapa_shared(c.sb + kOffItems + s * static_cast<uint32_t>(sizeof(Item)), 1);
+        const int* word = reinterpret_cast<const int*>(&it);
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(Item) / 4); ++k)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(at + 4 * k), "r"(word[k]) : "memory");
+        arrive_cluster(mapa_shared(c.bar(kItemFull + s), 1));
+      }
     }
     __syncwarp();
     if (!it.live) return;
@@ -499,11 +585,14 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
   }
 }
 
+template <bool kPair>
 __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t ring = c.sb + 2 * p.kc * kSlotBytes;
+  constexpr int kSlotBytes = Shape<kPair>::kSlotBytes;
+  const int lane = threadIdx.x & 31, rank = static_cast<int>(c.rank);
+  const uint32_t ring = c.sb + 2 * p.kc * kChunk;
+  const int value_slots = kPair ? 2 : p.vc;  // of a tile
   const bool paged = p.x.num_blocks > 0;
-  Items items;
+  Items<kPair> items;
   Item it;
   Ring r;
   uint32_t used[2] = {0, 0};  // times that a row tile's Q was loaded
@@ -515,9 +604,11 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps) {
       if (!warp_wait(c, kQFree + h, (used[h] & 1) ^ 1)) return;
       ++used[h];
       if (lane == 0) {
-        mbar_arrive_expect_tx(c.bar(kQFull + h), p.kc * 128 * p.G * p.tpt);
+        const uint32_t bar = lead<kPair>(c.bar(kQFull + h));
+        const int tile = kPair ? 2 * h + rank : h;
+        arrive_tx<kPair>(bar, p.kc * 128 * p.G * p.tpt);
         for (int k = 0; k < p.kc; ++k)
-          tma_3d(c.sb + (h * p.kc + k) * kSlotBytes, &maps.q, 64 * k, it.hk * p.G, it.q0 + (2 * it.m + h) * p.tpt, c.bar(kQFull + h));
+          load_3d<kPair>(c.sb + (h * p.kc + k) * kChunk, &maps.q, 64 * k, it.hk * p.G, it.q0 + it.m * p.span + tile * p.tpt, bar);
       }
       __syncwarp();
     }
@@ -529,20 +620,29 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps) {
       for (int k = 0; k < p.kc; ++k) {
         if (!warp_wait(c, kEmpty + r.slot, r.phase ^ 1)) return;
         if (lane == 0) {
-          mbar_arrive_expect_tx(c.bar(kFull + r.slot), kSlotBytes);
-          tma_4d(ring + r.slot * kSlotBytes, &maps.k, 64 * k, row, it.hk, block, c.bar(kFull + r.slot));
+          // of a pair, each CTA has half of the keys
+          const uint32_t bar = lead<kPair>(c.bar(kFull + r.slot));
+          arrive_tx<kPair>(bar, kSlotBytes);
+          load_4d<kPair>(ring + r.slot * kSlotBytes, &maps.k, 64 * k, row + 64 * rank, it.hk, block, bar);
         }
         __syncwarp();
         r.step(p.slots);
       }
       const int bars = kTile * (t + 1) > it.lo ? kLocal : kFull;
-      for (int k = 0; k < p.vc; ++k) {
+      for (int k = 0; k < value_slots; ++k) {
         if (!warp_wait(c, kEmpty + r.slot, r.phase ^ 1)) return;
         if (lane == 0) {
-          const uint32_t bar = c.bar(bars + r.slot), dst = ring + r.slot * kSlotBytes;
-          mbar_arrive_expect_tx(bar, kSlotBytes);
-          tma_4d(dst, &maps.v, 0, row + 64 * k, it.hk, block, bar);
-          if (p.vc == 2) tma_4d(dst + kSlotBytes / 2, &maps.v, 64, row + 64 * k, it.hk, block, bar);
+          const uint32_t dst = ring + r.slot * kSlotBytes;
+          if (kPair && bars == kFull) {  // and half of the values' columns
+            const uint32_t bar = lead<kPair>(c.bar(kFull + r.slot));
+            arrive_tx<kPair>(bar, kSlotBytes);
+            load_4d<kPair>(dst, &maps.v, 64 * rank, row + 64 * k, it.hk, block, bar);
+          } else {
+            const uint32_t bar = c.bar(bars + r.slot);
+            mbar_arrive_expect_tx(bar, kSlotBytes);
+            tma_4d(dst, &maps.v, 64 * rank, row + 64 * k, it.hk, block, bar);
+            if (!kPair && p.vc == 2) tma_4d(dst + kSlotBytes / 2, &maps.v, 64, row + 64 * k, it.hk, block, bar);
+          }
         }
         __syncwarp();
         r.step(p.slots);
@@ -552,21 +652,36 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps) {
   }
 }
 
-template <typename E>
+// Tells the softmax warps, of both CTAs of a pair, before the barrier that hands the values on.
+template <bool kPair>
+__device__ __noinline__ void post_mended(const Ctx& c) {
+  if constexpr (kPair) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      asm volatile("st.shared::cluster.u32 [%0], 1;" :: "r"(mapa_shared(c.sb + kOffMended, r)) : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");  // returns when the other CTA's shared memory has the word
+  } else {
+    *c.mended() = 1u;
+  }
+}
+
+template <typename E, bool kPair>
 __device__ void mend_role(const Params& p, const Ctx& c) {
+  constexpr int kSlotBytes = Shape<kPair>::kSlotBytes;
   const int lane = threadIdx.x & 31;
-  const uint32_t ring = c.sb + 2 * p.kc * kSlotBytes;
-  Items items;
+  const uint32_t ring = c.sb + 2 * p.kc * kChunk;
+  const int value_slots = kPair ? 2 : p.vc;
+  Items<kPair> items;
   Item it;
   Ring r;
   uint32_t seen = 0;  // a bit per slot: parity of its local barrier
-  const int rows = p.vc == 2 ? 64 : 128, units = p.vc == 2 ? 16 : 8;  // keys of a slot, 16-byte units of a key
+  const int rows = kPair || p.vc == 2 ? 64 : 128, units = !kPair && p.vc == 2 ? 16 : 8;  // keys of a slot, 16-byte units of a key
   const int unit = lane & (units - 1);
   while (items.next(c, it)) {
     const int end = max(it.ta, it.tb);
     for (int t = it.t0; t < end; ++t) {
       for (int k = 0; k < p.kc; ++k) r.step(p.slots);
-      for (int k = 0; k < p.vc; ++k, r.step(p.slots)) {
+      for (int k = 0; k < value_slots; ++k, r.step(p.slots)) {
         if (kTile * (t + 1) <= it.lo) continue;
         if (!warp_wait(c, kLocal + r.slot, (seen >> r.slot) & 1)) return;
         seen ^= 1u << r.slot;
@@ -595,7 +710,7 @@ __device__ void mend_role(const Params& p, const Ctx& c) {
         for (int row = max(first, live) + lane / units; row < rows; row += step) store(row, make_uint4(0, 0, 0, 0));
         if (__any_sync(0xffffffffu, !good)) {
           wrote = true;
-          *c.mended() = 1u;
+          post_mended<kPair>(c);
           for (int row = first + lane / units; row < live; row += step) {
             const uint4 v = load(row);
             store(row, make_uint4(finite2<E>(v.x), finite2<E>(v.y), finite2<E>(v.z), finite2<E>(v.w)));
@@ -603,7 +718,7 @@ __device__ void mend_role(const Params& p, const Ctx& c) {
         }
         if (wrote) fence_proxy_async_smem();  // generic-proxy stores -> tensor-core reads
         __syncwarp();
-        if (lane == 0) mbar_arrive(c.bar(kFull + r.slot));
+        if (lane == 0) arrive<kPair>(lead<kPair>(c.bar(kFull + r.slot)));
       }
     }
   }
@@ -612,17 +727,17 @@ __device__ void mend_role(const Params& p, const Ctx& c) {
 // The warp stays converged around an elected issuer, and what steers it is made
 // uniform, so that descriptors live in uniform registers: an MMA takes 64 clocks,
 // and with loops over runtime counts its issue took 115.
-template <int kKc, int kVc>
+template <bool kPair, int kKc, int kVc>
 __device__ void mma_role(const Params& p, const Ctx& c) {
-  constexpr int kSlots = kTileSmem / kSlotBytes - 2 * kKc < kMaxSlots ? kTileSmem / kSlotBytes - 2 * kKc : kMaxSlots;
+  constexpr int kSlotBytes = Shape<kPair>::kSlotBytes, kSlots = Shape<kPair>::slots(kKc);
   constexpr int kVSteps = kVc == 2 ? 4 : 8;
-  constexpr uint32_t kSlot = kSlotBytes >> 4;  // in a descriptor's address field
+  constexpr uint32_t kSlot = kSlotBytes >> 4, kQ = kChunk >> 4;  // in a descriptor's address field
   const uint64_t desc_q = make_sdesc(c.sb, 16, 1024, kSwizzle128B);
-  const uint64_t desc_k = make_sdesc(c.sb + 2 * kKc * kSlotBytes, 16, 1024, kSwizzle128B);
-  const uint64_t desc_v = make_sdesc(c.sb + 2 * kKc * kSlotBytes, kSlotBytes / 2, 1024, kSwizzle128B);
+  const uint64_t desc_k = make_sdesc(c.sb + 2 * kKc * kChunk, 16, 1024, kSwizzle128B);
+  const uint64_t desc_v = make_sdesc(c.sb + 2 * kKc * kChunk, kChunk / 2, 1024, kSwizzle128B);
   const uint32_t idesc_s = uniform(static_cast<int>(p.idesc_s)), idesc_v = uniform(static_cast<int>(p.idesc_v));
   const int last_steps = uniform(p.ks_qk) - 4 * (kKc - 1);  // of the last chunk of a key
-  Items items;
+  Items<kPair> items;
   Item it;
   int slot = 0;  // the next that no MMA has used
   uint32_t phase = 0;
@@ -637,28 +752,24 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
     }
     return true;
   };
-  auto commit = [&](int bar) {
-    if (elect_one()) umma_commit(c.bar(bar));
-    __syncwarp();
-  };
   // S_h = Q_h K^T of the keys in `at` and the slots behind it
   auto scores = [&](int h, int at, bool free_keys, bool last) {
     if (elect_one()) {
       const uint32_t d = c.tmem + kTmemS + 128 * h;
 #pragma unroll
       for (int k = 0; k < kKc; ++k) {
-        const uint64_t a = desc_q + (h * kKc + k) * kSlot;
+        const uint64_t a = desc_q + (h * kKc + k) * kQ;
         const uint64_t b = desc_k + static_cast<uint32_t>(after(at, k)) * kSlot;
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          if (k + 1 < kKc || s < last_steps) umma_ss(d, a + 2 * s, b + 2 * s, idesc_s, (k | s) != 0 ? 1u : 0u);
+          if (k + 1 < kKc || s < last_steps) mma_ss<kPair>(d, a + 2 * s, b + 2 * s, idesc_s, (k | s) != 0 ? 1u : 0u);
       }
-      umma_commit(c.bar(kSFull + h));
+      commit<kPair>(c.bar(kSFull + h));
       if (free_keys) {
 #pragma unroll
-        for (int k = 0; k < kKc; ++k) umma_commit(c.bar(kEmpty) + 8 * after(at, k));
+        for (int k = 0; k < kKc; ++k) commit<kPair>(c.bar(kEmpty) + 8 * after(at, k));
       }
-      if (last) umma_commit(c.bar(kQFree + h));
+      if (last) commit<kPair>(c.bar(kQFree + h));
     }
     __syncwarp();
   };
@@ -671,17 +782,18 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
         const uint64_t b = desc_v + static_cast<uint32_t>(after(at, k)) * kSlot;
 #pragma unroll
         for (int s = 0; s < kVSteps; ++s)
-          umma_ts(d, a + 8 * (k * kVSteps + s), b + 128 * s, idesc_v, (k | s) == 0 && first ? 0u : 1u);
+          mma_ts<kPair>(d, a + 8 * (k * kVSteps + s), b + 128 * s, idesc_v, (k | s) == 0 && first ? 0u : 1u);
       }
       if (free_values) {
 #pragma unroll
-        for (int k = 0; k < kVc; ++k) umma_commit(c.bar(kEmpty) + 8 * after(at, k));
+        for (int k = 0; k < kVc; ++k) commit<kPair>(c.bar(kEmpty) + 8 * after(at, k));
       }
-      if (last) umma_commit(c.bar(kOFull + h));
+      if (last) commit<kPair>(c.bar(kOFull + h));
     }
     __syncwarp();
   };
-  bool ok = true;
+  bool ok = !kPair || uniform(static_cast<int>(c.rank)) == 0;  // the first CTA issues for both
+  const bool issuer = ok;
   while (ok && items.next(c, it)) {
     const int t0 = uniform(it.t0), ta = uniform(it.ta), tb = uniform(it.tb), end = max(ta, tb);
     if (t0 >= end) continue;
@@ -713,20 +825,28 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
     }
   }
   // every MMA in flight lands before the CTA leaves
-  commit(kFinal);
+  if (issuer && elect_one()) commit<kPair>(c.bar(kFinal));
+  __syncwarp();
   volatile uint32_t never = 0;
   mbar_wait<false>(c.bar(kFinal), 0, &never, c.wait_ns > 500000000ull ? c.wait_ns : 500000000ull);
   __syncwarp();
 }
 
+template <bool kPair>
 __device__ __forceinline__ void mma_role(const Params& p, const Ctx& c) {
-  switch (2 * p.kc + p.vc) {
-    case 3: return mma_role<1, 1>(p, c);
-    case 4: return mma_role<1, 2>(p, c);
-    case 5: return mma_role<2, 1>(p, c);
-    case 6: return mma_role<2, 2>(p, c);
-    case 7: return mma_role<3, 1>(p, c);
-    default: return mma_role<3, 2>(p, c);
+  if constexpr (kPair) {  // values of more than 64 columns
+    if (p.kc == 1) return mma_role<true, 1, 2>(p, c);
+    if (p.kc == 2) return mma_role<true, 2, 2>(p, c);
+    return mma_role<true, 3, 2>(p, c);
+  } else {
+    switch (2 * p.kc + p.vc) {
+      case 3: return mma_role<false, 1, 1>(p, c);
+      case 4: return mma_role<false, 1, 2>(p, c);
+      case 5: return mma_role<false, 2, 1>(p, c);
+      case 6: return mma_role<false, 2, 2>(p, c);
+      case 7: return mma_role<false, 3, 1>(p, c);
+      default: return mma_role<false, 3, 2>(p, c);
+    }
   }
 }
 
@@ -779,7 +899,7 @@ __device__ __forceinline__ void turn_units(uint32_t (&y)[32], int lane) {
   }
 }
 
-template <typename E>
+template <typename E, bool kPair>
 __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) {
   const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // row tile, row of it
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -793,10 +913,11 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
   const bool paged = p.x.num_blocks > 0;
   uint32_t uses = 0, outs = 0;
   bool bad = false;
-  Items items;
+  Items<kPair> items;
   Item it;
   while (items.next(c, it)) {
-    const int tok = (2 * it.m + h) * p.tpt + tok_in;
+    const int tile = kPair ? 2 * h + static_cast<int>(c.rank) : h;  // of the item
+    const int tok = it.m * p.span + tile * p.tpt + tok_in;
     const bool live = tok_in < p.tpt && tok < it.n;
     const bool padded = tok_in < p.tpt && p.x.S1 > 0 && tok < p.x.S1;  // written, live or not
     const int vis = p.x.causal ? min(it.len, max(0, it.pos + tok + 1)) : it.len;  // keys that this row sees
@@ -867,7 +988,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(c.bar(kPReady + h));
+      if (lane == 0) arrive<kPair>(lead<kPair>(c.bar(kPReady + h)));
     }
     const bool any = it.t1(h) > it.t0;
     if (any) {
@@ -915,7 +1036,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
       if (*c.mended() && live && !nothing) infinite_columns<E>(p, it, it.lo, vis, out, nullptr);
       if (put && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     } else {
-      float* dst = p.parts + static_cast<int64_t>(it.part) * p.part_floats + h * (p.part_floats / 2);
+      float* dst = p.parts + static_cast<int64_t>(it.part) * p.part_floats + tile * (p.part_floats / Shape<kPair>::kTiles);
       if (any) {
 #pragma unroll 1
         for (int k = 0; k < p.x.d_v; k += 32) {
@@ -940,43 +1061,54 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
   if (bad) atomicOr(&g_prompt_status, MLA_DEVICE_BAD_BLOCK);
 }
 
-template <typename E>
+template <typename E, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ uint8_t raw[];
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   Ctx c;
   c.sb = (smem_u32(raw) + 1023u) & ~1023u;  // swizzled operands need 1024-byte alignment
   c.smem = raw + (c.sb - smem_u32(raw));
+  c.rank = kPair ? cluster_ctarank() : 0;
   c.wait_ns = p.wait_ns;
   c.abort = reinterpret_cast<volatile uint32_t*>(c.smem + kOffAbort);
+  constexpr int kCtas = Shape<kPair>::kCtas;
   if (tid == 0) {
     *c.abort = 0u;
     *c.mended() = 0u;
     for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(c.bar(kFull + i), 1);
+      mbar_init(c.bar(kFull + i), kCtas);
       mbar_init(c.bar(kEmpty + i), 1);
       mbar_init(c.bar(kLocal + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(c.bar(kQFull + i), 1);
+      mbar_init(c.bar(kQFull + i), kCtas);
       mbar_init(c.bar(kQFree + i), 1);
       mbar_init(c.bar(kSFull + i), 1);
-      mbar_init(c.bar(kPReady + i), 4);
+      mbar_init(c.bar(kPReady + i), 4 * kCtas);
       mbar_init(c.bar(kOFull + i), 1);
     }
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(c.bar(kItemFull + i), 1);
-      mbar_init(c.bar(kItemEmpty + i), kItemReaders);
+      mbar_init(c.bar(kItemEmpty + i), kPair ? 2 * kItemReaders - 1 : kItemReaders);  // one MMA warp
     }
     mbar_init(c.bar(kFinal), 1);
     fence_mbarrier_init_cluster();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(c.sb + kOffTmem, 512);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(c.sb + kOffTmem) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(c.sb + kOffTmem, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) {  // the other CTA's barriers are in place
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after();
   c.tmem = uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(c.smem + kOffTmem)));
   if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -984,13 +1116,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
 
   if (warp < kSoftmaxWarps) {
     regs_increase<kSoftmaxRegs>();
-    softmax_role<E>(p, c, warp, lane);
+    softmax_role<E, kPair>(p, c, warp, lane);
   } else {
     regs_decrease<kOtherRegs>();
-    if (warp == kMmaWarp) mma_role(p, c);
-    else if (warp == kLoadWarp) load_role(p, c, maps);
-    else if (warp == kPlanWarp) plan_role(p, c);
-    else if (warp == kMendWarp) mend_role<E>(p, c);
+    if (warp == kMmaWarp) {
+      mma_role<kPair>(p, c);
+    } else if (warp == kLoadWarp) {
+      load_role<kPair>(p, c, maps);
+    } else if (warp == kPlanWarp) {
+      if (c.rank == 0) plan_role<kPair>(p, c);
+    } else if (warp == kMendWarp) {
+      mend_role<E, kPair>(p, c);
+    }
   }
 
   tc_fence_before();
@@ -1002,8 +1139,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     while (globaltimer_ns() - t0 < 200000) {
     }
   }
+  if constexpr (kPair) {  // nothing of this CTA is needed by the other any more
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(c.tmem, 512);
+  if (warp == kMmaWarp) {
+    if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(c.tmem) : "memory");
+    else tmem_dealloc(c.tmem, 512);
+  }
 }
 
 // ------------------------------------------------------------------ merge
@@ -1018,16 +1162,16 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(const __gri
   const int row = threadIdx.x & 127, side = threadIdx.x >> 7, quads = p.x.d_v / 4, Hkv = p.x.n_kv;
   const int per_slice = (quads + kMergeSlices - 1) / kMergeSlices;  // at most 2 * kMergeQuads
   const int64_t step = static_cast<int64_t>(p.part_floats) * Hkv;           // a pair's parts: heads lie between them
-  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(merges) * 2 * kMergeSlices; w += gridDim.x) {
-    const int slice = static_cast<int>(w % kMergeSlices), h = static_cast<int>(w / kMergeSlices) & 1, i = static_cast<int>(w / kMergeSlices >> 1);
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(merges) * p.tiles * kMergeSlices; w += gridDim.x) {
+    const int slice = static_cast<int>(w % kMergeSlices), tile = static_cast<int>(w / kMergeSlices % p.tiles), i = static_cast<int>(w / kMergeSlices / p.tiles);
     const int pos = find_seq(p.merge0, p.x.B, i);
     const Seq s = load_seq(p, __ldcg(p.order + pos));
     const int k = i - __ldcg(p.merge0 + pos), hk = k % Hkv, m = s.pairs - 1 - k / Hkv;
     int cuts;
     const int64_t before = Cuts(p, s, cap).before(k / Hkv, cuts);
-    const int tok_in = row / p.G, tok = (2 * m + h) * p.tpt + tok_in;
+    const int tok_in = row / p.G, tok = m * p.span + tile * p.tpt + tok_in;
     const bool put = tok_in < p.tpt && tok < (p.x.S1 > 0 ? p.x.S1 : s.n);
-    const float* src = p.parts + (__ldcg(p.part0 + pos) + before * Hkv + hk) * p.part_floats + h * (p.part_floats / 2);
+    const float* src = p.parts + (__ldcg(p.part0 + pos) + before * Hkv + hk) * p.part_floats + tile * (p.part_floats / p.tiles);
     const int quad0 = slice * per_slice + side, quad1 = min(quads, (slice + 1) * per_slice);
     float top = -INFINITY, l = 0.f, o[kMergeQuads][4] = {};
     for (int c0 = 0; c0 < cuts; c0 += kAhead) {
@@ -1077,7 +1221,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 struct Device {
   bool ready = false;
-  int sms = 0;
+  int sms = 0, pairs = 0;
 };
 Device g_dev[kMaxDevices];
 std::mutex g_lock;
@@ -1085,30 +1229,65 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 constexpr int kMaxParts = 640;  // partial states in the workspace at most
 
+// Whether pairs of CTAs run: they hold half of the keys and values each, which eases
+// shared memory, the bound of a CTA alone, but take 512 rows at a time.
+bool in_pairs(const Problem& p) {
+  const int64_t rows = static_cast<int64_t>(p.T) * (p.n_q / p.n_kv);  // of a key head
+  return p.d_v > 64 && rows >= 1024 * static_cast<int64_t>(p.B) && rows * p.n_kv >= 4 * 512 * 76;
+}
+int item_tiles(const Problem& p) { return in_pairs(p) ? 4 : 2; }
+
 // Partial states that a call can need: none where no item has more key tiles than a part has at least.
 int parts_of(const Problem& p) {
   const int64_t keys = p.num_blocks > 0 ? static_cast<int64_t>(p.W) * kPage : p.Tk;
   if (keys <= kMinTiles * kTile) return 0;
-  const int64_t tpt = kTile / (p.n_q / p.n_kv), tiles = (keys + kTile - 1) / kTile;
-  const int64_t pairs = p.S1 > 0 ? p.B * ((p.S1 + 2 * tpt - 1) / (2 * tpt)) : p.T / (2 * tpt) + p.B;
+  const int64_t span = item_tiles(p) * (kTile / (p.n_q / p.n_kv)), tiles = (keys + kTile - 1) / kTile;
+  const int64_t pairs = p.S1 > 0 ? p.B * ((p.S1 + span - 1) / span) : p.T / span + p.B;
   // each factor bounded first: their product passes 64 bits for the largest dims
   const int64_t items = std::min<int64_t>(kMaxParts, std::min<int64_t>(kMaxParts, pairs) * p.n_kv);
   return static_cast<int>(std::min<int64_t>(kMaxParts, items * std::min<int64_t>(kMaxParts, (tiles + kMinTiles - 1) / kMinTiles)));
 }
-int part_floats(const Problem& p) { return 2 * (128 * p.d_v + 256); }
+int part_floats(const Problem& p) { return item_tiles(p) * (128 * p.d_v + 256); }
 size_t lists_bytes(const Problem& p) { return (sizeof(Head) + (4 * static_cast<size_t>(p.B) + 2) * sizeof(int) + 255) & ~size_t(255); }
 
-template <typename E>
-mla_status prepare_kernel() {
-  HEADS_CUDA(cudaFuncSetAttribute(prompt_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes), "kernel set-up");
+cudaLaunchConfig_t config_of(unsigned ctas, bool pair, cudaStream_t s, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair ? 2 : 1;
+  return cfg;
+}
+
+template <typename E, bool kPair>
+mla_status prepare_kernel(Device& d) {
+  HEADS_CUDA(cudaFuncSetAttribute(prompt_attn_kernel<E, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes), "kernel set-up");
   cudaFuncAttributes fa;
-  HEADS_CUDA(cudaFuncGetAttributes(&fa, prompt_attn_kernel<E>), "kernel attributes");
+  HEADS_CUDA(cudaFuncGetAttributes(&fa, prompt_attn_kernel<E, kPair>), "kernel attributes");
+  if constexpr (kPair) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config_of(2, true, nullptr, attr);
+    attr[0] = attr[1];
+    cfg.numAttrs = 1;
+    int n = 0;
+    HEADS_CUDA(cudaOccupancyMaxActiveClusters(&n, prompt_attn_kernel<E, kPair>, &cfg), "kernel occupancy");
+    if (n < 1) return fail(MLA_ERR_CUDA, "the kernel does not fit this device");
+    d.pairs = n;
+  }
   if (fa.numRegs < kRegs) return fail(MLA_ERR_CUDA, "the kernel was built with %d registers", fa.numRegs);  // what the warpgroups divide
   return MLA_OK;
 }
 
 // Kernel attributes and the tensor-map encoder; the first call on a device.
-mla_status init_device(int* sms) {
+mla_status init_device(int* sms, int* pairs) {
   int dev = 0;
   HEADS_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   if (dev < 0 || dev >= kMaxDevices) return fail(MLA_ERR_UNSUPPORTED, "device ordinal %d too large", dev);
@@ -1118,12 +1297,23 @@ mla_status init_device(int* sms) {
     mla_status st = tensor_map_encoder(&g_encode);
     if (st != MLA_OK) return st;
     HEADS_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev), "device attributes");
-    st = prepare_kernel<__nv_bfloat16>();
-    if (st == MLA_OK) st = prepare_kernel<__half>();
+    st = prepare_kernel<__nv_bfloat16, false>(d);
+    if (st == MLA_OK) st = prepare_kernel<__half, false>(d);
+    if (st == MLA_OK) st = prepare_kernel<__nv_bfloat16, true>(d);
+    if (st == MLA_OK) st = prepare_kernel<__half, true>(d);
     if (st != MLA_OK) return st;
     d.ready = true;
   }
   *sms = d.sms;
+  *pairs = d.pairs;
+  return MLA_OK;
+}
+
+template <typename E, bool kPair>
+mla_status launch_attention(unsigned ctas, const Maps& maps, const Params& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = config_of(ctas, kPair, s, attr);
+  HEADS_CUDA(cudaLaunchKernelEx(&cfg, prompt_attn_kernel<E, kPair>, maps, p), "kernel launch");
   return MLA_OK;
 }
 
@@ -1132,9 +1322,10 @@ mla_status init_device(int* sms) {
 size_t tiles_workspace(const Problem& p) { return lists_bytes(p) + static_cast<size_t>(parts_of(p)) * part_floats(p) * sizeof(float); }
 
 mla_status launch_tiles(const Problem& x, cudaStream_t s) {
-  int sms = 0;
-  const mla_status st = init_device(&sms);
+  int sms = 0, cta_pairs = 0;
+  const mla_status st = init_device(&sms, &cta_pairs);
   if (st != MLA_OK) return st;
+  const bool pair = in_pairs(x);
   Params p;
   p.x = x;
   uint8_t* ws = static_cast<uint8_t*>(x.workspace);
@@ -1148,13 +1339,16 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
   p.max_parts = parts_of(x);
   p.G = x.n_q / x.n_kv;
   p.tpt = kTile / p.G;
+  p.tiles = item_tiles(x);
+  p.span = p.tiles * p.tpt;
   p.kc = (x.d_qk + 63) / 64;
   p.vc = x.d_v > 64 ? 2 : 1;
-  p.slots = std::min(kMaxSlots, kTileSmem / kSlotBytes - 2 * p.kc);
-  p.sms = sms;
+  p.slots = pair ? Shape<true>::slots(p.kc) : Shape<false>::slots(p.kc);
+  p.sms = pair ? cta_pairs : sms;
   const uint32_t bf16 = x.dtype == MLA_ROPE_BF16 ? 1 : 0;
-  p.idesc_s = make_idesc_f16(128, 128, bf16, 0, 0);                                        // A, B K-major
-  p.idesc_v = make_idesc_f16(128, static_cast<uint32_t>((x.d_v + 15) & ~15), bf16, 0, 1);  // B MN-major
+  const uint32_t M = pair ? 256 : 128;
+  p.idesc_s = make_idesc_f16(M, 128, bf16, 0, 0);                                                       // A, B K-major
+  p.idesc_v = make_idesc_f16(M, pair ? 128 : static_cast<uint32_t>((x.d_v + 15) & ~15), bf16, 0, 1);  // B MN-major
   p.ks_qk = (x.d_qk + 15) / 16;
   p.wait_ns = host_wait_limit_ns();
   Maps maps;
@@ -1169,7 +1363,7 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
     const bool none = x.num_blocks == 0 && x.Tk == 0;  // no key is ever loaded
     const int64_t size[4] = {i == 0 ? x.d_qk : x.d_v, x.num_blocks > 0 ? kPage : std::max(1, x.Tk), x.n_kv, std::max(1, x.num_blocks)};
     const int64_t stride[3] = {c.row_stride, c.head_stride, c.block_stride};
-    const int box[4] = {64, i == 1 && p.vc == 2 ? 64 : 128, 1, 1};
+    const int box[4] = {64, pair || (i == 1 && p.vc == 2) ? 64 : 128, 1, 1};
     CUtensorMap* map = i == 0 ? &maps.k : &maps.v;
     const mla_status ms = none ? MLA_OK : tmap(g_encode, map, x.dtype, c.data, 4, size, stride, box, i == 0 ? "k" : "v");
     if (ms != MLA_OK) return ms;
@@ -1178,12 +1372,12 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
   const bool bf = x.dtype == MLA_ROPE_BF16;
   prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
   HEADS_CUDA(cudaGetLastError(), "plan launch");
-  const int64_t pairs = x.S1 > 0 ? static_cast<int64_t>(x.B) * ((x.S1 + 2 * p.tpt - 1) / (2 * p.tpt)) : x.T / (2 * p.tpt) + x.B;
-  const int64_t most = std::min<int64_t>(sms, pairs) * x.n_kv + p.max_parts;
-  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, most))));
-  HEADS_CUDA(bf ? launch_after(prompt_attn_kernel<__nv_bfloat16>, grid, kThreads, kSmemBytes, s, maps, p)
-                : launch_after(prompt_attn_kernel<__half>, grid, kThreads, kSmemBytes, s, maps, p),
-             "kernel launch");
+  const int64_t groups = x.S1 > 0 ? static_cast<int64_t>(x.B) * ((x.S1 + p.span - 1) / p.span) : x.T / p.span + x.B;
+  const int64_t most = std::min<int64_t>(p.sms, groups) * x.n_kv + p.max_parts;
+  const unsigned workers = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(p.sms, most)));
+  const mla_status ls = bf ? (pair ? launch_attention<__nv_bfloat16, true>(2 * workers, maps, p, s) : launch_attention<__nv_bfloat16, false>(workers, maps, p, s))
+                           : (pair ? launch_attention<__half, true>(2 * workers, maps, p, s) : launch_attention<__half, false>(workers, maps, p, s));
+  if (ls != MLA_OK) return ls;
   if (p.max_parts > 0)
     HEADS_CUDA(bf ? launch_after(prompt_merge_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(4 * sms)), kMergeThreads, 0, s, p)
                   : launch_after(prompt_merge_kernel<__half>, dim3(static_cast<unsigned>(4 * sms)), kMergeThreads, 0, s, p),
