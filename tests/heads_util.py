@@ -98,3 +98,34 @@ def gather(pool, table, b, length):
     """The first `length` keys of sequence b."""
     pages = table[b, :-(-length // 128)].long()
     return pool.cpu()[pages].flatten(0, 1)[:length]
+
+
+def check_gpu(got, got_lse, q, k, v, scale, causal, what):
+    """check_sequence on the GPU in fp64, head by head, for sequences that numpy takes too long over."""
+    n, H, D = q.shape
+    L, Hkv = k.shape[:2]
+    if n == 0 or L == 0:
+        assert (got == 0).all() and torch.isneginf(got_lse).all(), what
+        return
+    info = torch.finfo(got.dtype)
+    vmax = v.abs().max().double().item()
+    for h in range(H):
+        a, b, c = q[:, h].double(), k[:, h * Hkv // H].double(), v[:, h * Hkv // H].double()
+        z = a @ b.T * scale
+        hidden = torch.arange(L, device=q.device)[None] > (L - n + torch.arange(n, device=q.device))[:, None] if causal else \
+            torch.zeros((n, L), dtype=torch.bool, device=q.device)
+        z.masked_fill_(hidden, -float("inf"))
+        lse = torch.logsumexp(z, -1)
+        p = (z - lse[:, None]).exp()
+        out, mass = p @ c, p @ c.abs()
+        top = z.abs().masked_fill(hidden, 0).amax(-1)
+        terms = (a.abs() @ b.abs().T * abs(scale)).masked_fill(hidden, 0).amax(-1)
+        dz = 2 * U * D * terms + 8 * U * (top + 1)
+        bound = mass * (info.eps / 2 + 2 * dz[:, None] + 2 * U * (L + 16)) * (1 + 1e-3)
+        bound = bound + out.abs().clamp(min=info.smallest_normal) * info.eps / 2
+        if got.dtype == torch.float16:
+            bound = bound + L * vmax * 2.0 ** -25
+        err = (got[:, h].double() - out).abs()
+        assert bool((err <= bound).all()), f"{what} head {h}: worst {(err / bound).max().item()}, finite {bool(torch.isfinite(got[:, h]).all())}"
+        le = (got_lse[:, h].double() - lse).abs()
+        assert bool((le <= dz + 2 * U * (L + 16) + 4 * U * lse.abs()).all()), f"{what} head {h}: lse {le.max().item()}"

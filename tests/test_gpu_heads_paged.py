@@ -210,3 +210,23 @@ def test_two_streams_with_a_workspace_each():
     torch.cuda.synchronize()
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_runs():
+    """A bound far below the first load's latency: a launch that gives up reports it, and the next one does the whole
+    job.  (One test of a barrier may suspend the warp for longer than a wait lasts: then the launch comes through.)"""
+    import mla_sparse_top_gb300 as mla
+    m = make([3000, 500], H=8, Hkv=2)
+    want = run(m)
+    assert mla.heads_device_status(clear=True) == 0
+    mla.set_wait_limit_ns(1000)
+    try:
+        short = run(m)
+        status = mla.heads_device_status(clear=True)
+    finally:
+        mla.set_wait_limit_ns(mla.DEFAULT_WAIT_LIMIT_NS)
+    assert status in (0, mla.MLA_DEVICE_TIMEOUT)
+    assert status != 0 or torch.equal(short[0], want[0])
+    got = run(m)
+    assert mla.heads_device_status(clear=True) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from heads_util import TYPES, cache, check_sequence, gather, normal, np64, padded, page_table
+from heads_util import TYPES, cache, check_gpu, check_sequence, gather, normal, np64, padded, page_table
 
 pytestmark = pytest.mark.gpu
 
@@ -261,3 +261,68 @@ def test_other_stream_and_captured():
     torch.cuda.synchronize()
     check(m, out, lse)
     assert np.isfinite(np64(out)).all()
+
+
+# Calls with rows enough for pairs of SMs: 512 rows at a time, at least 1024 of a key head for each sequence
+LARGE = [
+    dict(lens=[1300], H=128, Hkv=128, D=192, Dv=128, pad=8), dict(lens=[2049], H=80, Hkv=2, D=128, Dv=128, spare=40, begin=3),
+    dict(lens=[1025, 1030, 2000], H=48, Hkv=16, D=96, Dv=80, dtype="fp16"), dict(lens=[5, 1500, 0, 1200], H=128, Hkv=4, D=64, Dv=72),
+    dict(lens=[1281], H=128, Hkv=1, D=64, Dv=128, causal=False), dict(lens=[700, 900], ctx=[3000, 129], H=100, Hkv=4, D=128, Dv=128, paged=True, layout="head"),
+    dict(lens=[1400], ctx=[77], H=112, Hkv=16, D=192, Dv=104, paged=True, layout="shared", dtype="fp16"),
+]
+
+
+@pytest.mark.parametrize("case", LARGE)
+def test_many_rows(case):
+    import mla_sparse_top_gb300 as mla
+    m = make(**case)
+    out, lse = run(m)
+    assert mla.heads_device_status(clear=True) == 0
+    at = m["begin"]
+    assert (out[:at] == 7).all() and (lse[:at] == 7).all()
+    for b, n in enumerate(m["lens"]):
+        k, v = keys_of(m, b)
+        check_gpu(out[at:at + n], lse[at:at + n], m["q"][at:at + n], k.cuda(), v.cuda(), m["scale"], m["causal"], f"sequence {b}")
+        at += n
+    assert (out[at:] == 7).all() and (lse[at:] == 7).all()
+    again, lse2 = run(m)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_many_rows_with_values_that_are_not_finite():
+    """A value in the half of the columns that the other SM of the pair holds reaches both SMs' rows, and no others."""
+    m = make([1400], H=112, Hkv=2, D=128, Dv=128)
+    m["k"][1400:] = 0
+    m["v"][1400:] = 0
+    clean = [x.clone() for x in run(m)]
+    for col in (3, 100):
+        m["v"][900, 1, col] = float("nan")
+    out, lse = run(m)
+    assert torch.equal(lse, clean[1]) and torch.equal(out[:, :56], clean[0][:, :56]) and torch.equal(out[:900], clean[0][:900])
+    hit = out[900:1400, 56:]
+    assert not torch.isfinite(hit[..., [3, 100]]).any()
+    rest = [d for d in range(128) if d not in (3, 100)]
+    assert torch.equal(hit[..., rest], clean[0][900:1400, 56:][..., rest])
+
+
+@pytest.mark.parametrize("case", [dict(lens=[1400, 300], H=112, Hkv=2, D=128, Dv=128), dict(lens=[900], H=4, Hkv=2)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_runs(case):
+    """A bound far below what a whole call waits: a launch that gives up reports it, and the next one does the whole job.
+
+    The bound is looked at between tests of a barrier, and one test may suspend the warp for longer than the waits of
+    a small call last: that one may come through, with its results whole."""
+    import mla_sparse_top_gb300 as mla
+    m = make(**case)
+    want = run(m)
+    assert mla.heads_device_status(clear=True) == 0
+    mla.set_wait_limit_ns(1000)
+    try:
+        short = run(m)
+        status = mla.heads_device_status(clear=True)
+    finally:
+        mla.set_wait_limit_ns(mla.DEFAULT_WAIT_LIMIT_NS)
+    assert status == mla.MLA_DEVICE_TIMEOUT or (status == 0 and m["q"].shape[0] < 1000)
+    assert status != 0 or torch.equal(short[0], want[0])
+    got = run(m)
+    assert mla.heads_device_status(clear=True) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
