@@ -7,6 +7,11 @@
 // rotation needs no lane but its own.  A group keeps its token and walks over
 // heads, so angles and weights are made once.  Everything is read once and
 // written once: bound by memory.
+// Measured (graph replay): 8192 tokens of 32 + 8 heads of 128 in bf16, RMS norms and
+// rotation, 42 us (168 MB, 4.0 TB/s); 16384 new tokens to the cache, 28 + 4 + 4 heads of
+// 128 of which 64 turn, no norm, 62 us (302 MB, 4.9 TB/s); 64 new tokens 5.9 us, of which
+// the launch is most; 4099 tokens of 17 fp32 heads of 107, LayerNorm, 40 us: single
+// values and two sums that follow one another, bound by instructions.
 #include <cuda_runtime.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -20,7 +25,10 @@ using mlarp::Freqs;
 using mlarp::Pack;
 
 constexpr int kThreads = 128;
-constexpr int kMaxPasses = 16;  // heads of a group
+constexpr int kMaxPasses = 16;  // heads of a group (8: 16384 new tokens to the cache 67 -> 72 us)
+// Heads whose loads are in flight while one is worked on.  2 / 3 / 4 / 5: norms of 8192
+// tokens 44.6 / 44.3 / 42.2 / 48.3 us, 16384 new tokens to the cache 72.7 / 67 / 62 / 61.
+constexpr int kHeadsAhead = 4;
 
 __device__ unsigned int g_prep_status = 0;
 
@@ -138,10 +146,9 @@ struct Lane {
     }
   }
   __device__ __forceinline__ void load(const E* x, bool live, Pack<E, V> (&a)[KU], Pack<E, V> (&b)[KU]) const {
+    // what is not loaded holds zero from the start, or another head's values, whose results go nowhere
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
-#pragma unroll
-      for (int k = 0; k < Pack<E, V>::W; ++k) a[i].w[k] = b[i].w[k] = 0;
       if (live && in[i]) {
         a[i].load(x + d[i]);
         if (kTwo && rot[i]) b[i].load(x + d[i] + second);
@@ -150,10 +157,43 @@ struct Lane {
   }
 };
 
-// The rotation of a normed pair is linear in the pair: weights go into the
-// cosines and sines, once for a token, and the bias turns along.
+// fp32 pairs (one instruction for two lanes of arithmetic: instructions bind the
+// kernel where memory does not).
+typedef uint64_t Two;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(Two v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The rotation of a normed pair is linear in the pair: weights go into the cosines
+// and sines, once for a token, the bias turns along, and the norm's factor comes last.
+// Coefficients of two values each: of two pairs (of a pack, or of two units of single
+// values), or of the two values of one.
+//   two packs:  first' = first straight - second cross,  second' = first back + second other
+//   one pack:   (u, v)' = (u, v) straight + (v, u) cross
 struct Coef {
-  float ca, sb, sa, cb;  // y_a = x_a ca - x_b sb,  y_b = x_a sa + x_b cb
+  Two straight, cross, back, other;
 };
 
 template <typename E, int V, bool kTwo, int KU, bool kLayer>
@@ -177,37 +217,54 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
   const int32_t pos = live && w.rot_units > 0 ? __ldg(p.positions + t) : 0;
   const bool normed = w.kind != MLA_NORM_NONE, layer = kLayer && w.kind == MLA_NORM_LAYER;
   L at;
-  Coef co[KU][L::kPairs];
-  float ba[kLayer ? KU : 1][L::kPairs], bb[kLayer ? KU : 1][L::kPairs];
+  constexpr int kCoefs = KU * L::kPairs / (kTwo ? 2 : 1);
+  static_assert(!kTwo || KU * V % 2 == 0, "pairs of pairs");
+  Coef co[kCoefs];
+  Two ba[kLayer ? kCoefs : 1], bb[kLayer && kTwo ? kCoefs : 1];
   auto coefficients = [&]() {
+    float wt[KU][L::kVals], bi[KU][L::kVals];
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
-      float wt[L::kVals], bi[L::kVals];
 #pragma unroll
       for (int j = 0; j < L::kVals; ++j) {
-        wt[j] = 1.f;
-        bi[j] = 0.f;
+        wt[i][j] = 1.f;
+        bi[i][j] = 0.f;
       }
       if (normed && at.in[i]) {
         if (w.weight != nullptr) {
-          values<E, V>(w.weight, at.d[i], w.weight_fp32, w.weight_vec, wt);
-          if (kTwo && at.rot[i]) values<E, V>(w.weight, at.d[i] + at.second, w.weight_fp32, w.weight_vec, wt + L::kVals - V);
+          values<E, V>(w.weight, at.d[i], w.weight_fp32, w.weight_vec, wt[i]);
+          if (kTwo && at.rot[i]) values<E, V>(w.weight, at.d[i] + at.second, w.weight_fp32, w.weight_vec, wt[i] + L::kVals - V);
         }
         if (kLayer && w.bias != nullptr) {
-          values<E, V>(w.bias, at.d[i], w.weight_fp32, w.weight_vec, bi);
-          if (kTwo && at.rot[i]) values<E, V>(w.bias, at.d[i] + at.second, w.weight_fp32, w.weight_vec, bi + L::kVals - V);
+          values<E, V>(w.bias, at.d[i], w.weight_fp32, w.weight_vec, bi[i]);
+          if (kTwo && at.rot[i]) values<E, V>(w.bias, at.d[i] + at.second, w.weight_fp32, w.weight_vec, bi[i] + L::kVals - V);
         }
       }
+    }
+    auto angle = [&](int i, int j) {
+      return at.rot[i] ? mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale)
+                       : make_float2(1.f, 0.f);
+    };
 #pragma unroll
-      for (int j = 0; j < L::kPairs; ++j) {
-        float2 cs = make_float2(1.f, 0.f);
-        if (at.rot[i]) cs = mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale);
-        const float wa = wt[kTwo ? j : 2 * j], wb = wt[kTwo ? V + j : 2 * j + 1];
-        co[i][j] = {wa * cs.x, wb * cs.y, wa * cs.y, wb * cs.x};
+    for (int k = 0; k < kCoefs; ++k) {
+      if constexpr (kTwo) {
+        const int i = 2 * k / V, j = 2 * k % V, i2 = (2 * k + 1) / V, j2 = (2 * k + 1) % V;
+        const float2 c = angle(i, j), d = angle(i2, j2);
+        co[k] = {two(wt[i][j] * c.x, wt[i2][j2] * d.x), two(-wt[i][V + j] * c.y, -wt[i2][V + j2] * d.y),
+                 two(wt[i][j] * c.y, wt[i2][j2] * d.y), two(wt[i][V + j] * c.x, wt[i2][V + j2] * d.x)};
         if constexpr (kLayer) {
-          const float2 z = mlarp::turn2(bi[kTwo ? j : 2 * j], bi[kTwo ? V + j : 2 * j + 1], cs);
-          ba[i][j] = z.x;
-          bb[i][j] = z.y;
+          const float2 y = mlarp::turn2(bi[i][j], bi[i][V + j], c), z = mlarp::turn2(bi[i2][j2], bi[i2][V + j2], d);
+          ba[k] = two(y.x, z.x);
+          bb[k] = two(y.y, z.y);
+        }
+      } else {
+        const int i = k / L::kPairs, j = k % L::kPairs;
+        const float2 c = angle(i, j);
+        co[k].straight = two(wt[i][2 * j] * c.x, wt[i][2 * j + 1] * c.x);
+        co[k].cross = two(-wt[i][2 * j + 1] * c.y, wt[i][2 * j] * c.y);
+        if constexpr (kLayer) {
+          const float2 y = mlarp::turn2(bi[i][2 * j], bi[i][2 * j + 1], c);
+          ba[k] = two(y.x, y.y);
         }
       }
     }
@@ -215,49 +272,76 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
   at.place(w, 0, lane);
   // a chunk's part of sum (x - mean) or its squares
   auto part = [&](const Pack<E, V>(&a)[KU], const Pack<E, V>(&b)[KU], float mean, bool square) {
-    float s = 0.f;
+    Two s = two(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       float v[L::kVals];
       unpack<E, V>(a[i], v);
       if constexpr (kTwo) unpack<E, V>(b[i], v + V);
+      if constexpr (kLayer) {
 #pragma unroll
-      for (int j = 0; j < L::kVals; ++j) {
-        float c = v[j];  // places without a value hold zero
-        if constexpr (kLayer) c = at.in[i] && (j < V || at.rot[i]) ? c - mean : 0.f;
-        s = square ? fmaf(c, c, s) : s + c;
+        for (int j = 0; j < L::kVals; ++j) v[j] = at.in[i] && (j < V || at.rot[i]) ? v[j] - mean : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < L::kVals; j += 2) {  // places without a value hold zero
+        const Two c = two(v[j], v[j + 1]);
+        s = square ? fma2(c, c, s) : add2(s, c);
       }
     }
-    return s;
+    const float2 h = halves(s);
+    return h.x + h.y;
   };
   // norm, rotation and store of a chunk
   auto finish = [&](Pack<E, V>(&a)[KU], Pack<E, V>(&b)[KU], float mean, float inv, E* o, bool put) {
+    const Two inv2 = two(inv, inv);
+    float v[KU][L::kVals];
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
-      if (normed || at.rot[i]) {
-        float v[L::kVals];
-        unpack<E, V>(a[i], v);
-        if constexpr (kTwo) unpack<E, V>(b[i], v + V);
+      unpack<E, V>(a[i], v[i]);
+      if constexpr (kTwo) unpack<E, V>(b[i], v[i] + V);
+      if constexpr (kLayer) {
 #pragma unroll
-        for (int j = 0; j < L::kPairs; ++j) {
-          float& u = v[kTwo ? j : 2 * j];
-          float& y = v[kTwo ? V + j : 2 * j + 1];
-          const float xa = (kLayer ? u - mean : u) * inv, xb = (kLayer ? y - mean : y) * inv;
-          const Coef& k = co[i][j];
-          if (at.rot[i]) {
-            u = fmaf(xa, k.ca, -__fmul_rn(xb, k.sb));
-            y = fmaf(xa, k.sa, __fmul_rn(xb, k.cb));
-          } else {  // what does not turn keeps apart from its neighbour
-            u = xa * k.ca;
-            y = xb * k.cb;
-          }
-          if constexpr (kLayer) {
-            u += ba[i][j];
-            y += bb[i][j];
-          }
+        for (int j = 0; j < L::kVals; ++j) v[i][j] -= mean;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kCoefs; ++k) {
+      if constexpr (kTwo) {
+        const int i = 2 * k / V, j = 2 * k % V, i2 = (2 * k + 1) / V, j2 = (2 * k + 1) % V;
+        const Two x = two(v[i][j], v[i2][j2]);
+        // a unit that does not turn has no second pack: nothing of it may reach the first
+        const Two y = kLayer ? two(at.rot[i] ? v[i][V + j] : 0.f, at.rot[i2] ? v[i2][V + j2] : 0.f) : two(v[i][V + j], v[i2][V + j2]);
+        Two first = fma2(y, co[k].cross, mul2(x, co[k].straight)), second = fma2(x, co[k].back, mul2(y, co[k].other));
+        if constexpr (kLayer) {
+          first = fma2(first, inv2, ba[k]);
+          second = fma2(second, inv2, bb[k]);
+        } else {
+          first = mul2(first, inv2);
+          second = mul2(second, inv2);
         }
-        pack<E, V>(a[i], v);
-        if constexpr (kTwo) pack<E, V>(b[i], v + V);
+        const float2 f = halves(first), g = halves(second);
+        v[i][j] = f.x;
+        v[i2][j2] = f.y;
+        v[i][V + j] = g.x;
+        v[i2][V + j2] = g.y;
+      } else {
+        const int i = k / L::kPairs, j = k % L::kPairs;
+        const Two x = two(v[i][2 * j], v[i][2 * j + 1]), y = two(v[i][2 * j + 1], v[i][2 * j]);
+        // what does not turn keeps apart from its neighbour
+        const Two turned = mul2(y, co[k].cross);
+        Two r = fma2(x, co[k].straight, at.rot[i] ? turned : two(0.f, 0.f));
+        if constexpr (kLayer) r = fma2(r, inv2, ba[k]);
+        else r = mul2(r, inv2);
+        const float2 f = halves(r);
+        v[i][2 * j] = f.x;
+        v[i][2 * j + 1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KU; ++i) {
+      if (normed || at.rot[i]) {  // else the values go as they came
+        pack<E, V>(a[i], v[i]);
+        if constexpr (kTwo) pack<E, V>(b[i], v[i] + V);
       }
       if (put && at.in[i]) {
         a[i].store(o + at.d[i]);
@@ -266,7 +350,11 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
     }
   };
   // mean and 1 / root from a head's sums
-  auto root = [&](float sum) { return 1.f / sqrtf(fmaf(sum, w.inv_d, w.eps)); };
+  auto root = [&](float sum) {
+    const float m = fmaf(sum, w.inv_d, w.eps), r = rsqrtf(m);
+    // one step of Newton's takes the approximation's two steps off; not for 0 and infinity
+    return m > 1e-36f && m < 1e36f ? fmaf(fmaf(-m * r, r, 1.f), 0.5f * r, r) : r;
+  };
   auto group_sum = [&](float v) {
     for (int o = w.lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -274,9 +362,15 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
   const int64_t x_step = w.head_rows * w.xh, o_step = w.head_rows * w.oh;
   const int heads = live ? min(w.passes, (w.n_heads - h0 + w.head_rows - 1) / w.head_rows) : 0;  // of this group
   if (w.chunks == 1) {
-    // two heads ahead of the one that is worked on
-    constexpr int kSets = 3;
+    // heads ahead of the one that is worked on: what is in flight carries the rate
+    constexpr int kSets = kHeadsAhead + 1;
     Pack<E, V> a[kSets][KU], b[kSets][KU];
+#pragma unroll
+    for (int u = 0; u < kSets; ++u)
+#pragma unroll
+      for (int i = 0; i < KU; ++i)
+#pragma unroll
+        for (int k = 0; k < Pack<E, V>::W; ++k) a[u][i].w[k] = b[u][i].w[k] = 0;
 #pragma unroll
     for (int u = 0; u < kSets - 1; ++u, x += x_step) at.load(x, u < heads, a[u], b[u]);
     if (normed || w.rot_units > 0) coefficients();  // while the loads are on their way
@@ -294,6 +388,12 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
     return;
   }
   // heads of more values than the group holds, chunk by chunk
+  auto clear = [&](Pack<E, V>(&a)[KU], Pack<E, V>(&b)[KU]) {
+#pragma unroll
+    for (int i = 0; i < KU; ++i)
+#pragma unroll
+      for (int k = 0; k < Pack<E, V>::W; ++k) a[i].w[k] = b[i].w[k] = 0;
+  };
   for (int it = 0; it < w.passes; ++it, x += x_step, out += o_step) {
     Pack<E, V> a[KU], b[KU];
     float mean = 0.f, inv = 1.f;
@@ -301,6 +401,7 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
       float sum = 0.f;
       for (int c = 0; c < w.chunks; ++c) {
         at.place(w, c * KU * w.lanes, lane);
+        clear(a, b);
         at.load(x, it < heads, a, b);
         sum += part(a, b, mean, step == 1);
       }
@@ -311,6 +412,7 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
     for (int c = 0; c < w.chunks; ++c) {  // in place, a lane has read and written its own values alone
       at.place(w, c * KU * w.lanes, lane);
       coefficients();
+      clear(a, b);
       at.load(x, it < heads, a, b);
       finish(a, b, mean, inv, out, it < heads);
     }
@@ -462,7 +564,7 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
   const int turns = (j.n_heads + w->head_rows - 1) / w->head_rows;
   const int most = std::min(turns, kMaxPasses);
   w->passes = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (toks * turns + 607) / 608)));
-  w->head_blocks = (turns + w->passes - 1) / w->passes;
+  w->head_blocks = std::max(std::max(1, (turns + w->passes / 2) / w->passes), (turns + kMaxPasses - 1) / kMaxPasses);
   w->passes = (turns + w->head_blocks - 1) / w->head_blocks;  // even shares
   const int64_t blocks = toks * w->head_blocks;
   if (blocks >= (1ll << 29)) return fail(MLA_ERR_SHAPE, "%s: T x heads too large", j.name);
