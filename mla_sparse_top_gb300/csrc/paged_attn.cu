@@ -3,7 +3,7 @@
 //
 // The keys and values of a sequence are read once and meet few rows (the S1 new
 // tokens of the G heads that share them), so memory binds.  A CTA holds eight
-// pipelines of two warps: one streams units of 16 keys, keys and values together,
+// pipelines of two warps: one streams units of 32 keys, keys and values together,
 // by TMA into slots of shared memory that no other pipeline touches, the other
 // takes 16 rows through them with the running maximum, sum and output in
 // registers, as accumulators of mma.sync (m16n8k16: the 128-row tiles of tcgen05

@@ -365,10 +365,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     for (int j = 0; j < 3; ++j) carry[j] += sum[j];
   }
   if (tid == 0) {
+    // more than can be numbered: only where offsets run back and forth, which is reported
+    const bool few = carry[0] < (1ll << 30);
     p.first[B] = static_cast<int>(carry[0]);
     p.merge0[B] = static_cast<int>(carry[2]);
-    p.head->items = static_cast<int>(carry[0]);
-    p.head->merges = static_cast<int>(carry[2]);
+    p.head->items = few ? static_cast<int>(carry[0]) : 0;
+    p.head->merges = few ? static_cast<int>(carry[2]) : 0;
     p.head->next = 0;
     p.head->cap = cap;
   }
