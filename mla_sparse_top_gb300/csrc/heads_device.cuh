@@ -24,6 +24,12 @@ __device__ __forceinline__ bool warp_wait(const Ctx& c, int i, uint32_t parity) 
 }
 // The value of lane 0, which lets the compiler keep it in uniform registers.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// a / b and the rest; 64-bit division is slow, and hardly ever needed.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t& rest) {
+  const int64_t q = ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+  rest = a - q * b;
+  return q;
+}
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;

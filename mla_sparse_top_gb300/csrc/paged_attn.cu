@@ -98,13 +98,6 @@ struct Ctx {
   __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
 };
 
-// a / b and the rest; 64-bit division is slow, and hardly ever needed.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t& rest) {
-  const int64_t q = ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
-  rest = a - q * b;
-  return q;
-}
-
 // The stream in equal shares: the first `more` of them have `each` + 1 units, the others `each`.
 struct Split {
   int64_t each, more;
@@ -822,8 +815,8 @@ mla_status check_dims(const mla_paged_dims& d) {
   const mla_status st = check_head_dims(d.n_q, d.n_kv, d.d_qk, d.d_v, d.dtype);
   if (st != MLA_OK) return st;
   if (d.B < 0 || d.S1 < 1 || d.S1 > (1 << 20)) return fail(MLA_ERR_SHAPE, "B must be >= 0, S1 in [1, 2^20]");
-  if (static_cast<int64_t>(d.B) * d.S1 * d.n_q >= (1ll << 31) - 256 || d.B > (1 << 24))
-    return fail(MLA_ERR_SHAPE, "B * S1 * n_q must be below 2^31 - 256, B at most 2^24");
+  if (static_cast<int64_t>(d.B) * d.S1 * d.n_q >= (1ll << 31) - 1024 || d.B > (1 << 24))
+    return fail(MLA_ERR_SHAPE, "B * S1 * n_q must be below 2^31 - 1024, B at most 2^24");
   if (d.num_blocks < 1 || d.num_blocks >= (1 << 24)) return fail(MLA_ERR_SHAPE, "num_blocks=%d outside [1, 2^24)", d.num_blocks);
   if (d.max_blocks_per_seq < 1 || d.max_blocks_per_seq > (1 << 23))
     return fail(MLA_ERR_SHAPE, "max_blocks_per_seq=%d outside [1, 2^23]", d.max_blocks_per_seq);

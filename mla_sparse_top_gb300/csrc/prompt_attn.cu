@@ -50,6 +50,7 @@ constexpr int kChunk = 16384;  // 128 rows of 64 columns
 constexpr int kMaxSlots = 20;
 constexpr int kTileSmem = 14 * kChunk;  // Q and ring together
 constexpr int kItemSlots = 2;
+constexpr int kDrawTiles = 1;  // key tiles of an item still to be loaded when the next is drawn
 constexpr int kItemReaders = kSoftmaxWarps + 3;  // MMA, load and mend warps
 
 // A CTA alone, or a pair of them that shares the keys and values of its rows.
@@ -74,7 +75,8 @@ constexpr int kPReady = kSFull + 2;          // [2] weights are written, O is re
 constexpr int kOFull = kPReady + 2;          // [2] the item's MMAs are complete
 constexpr int kItemFull = kOFull + 2;        // [kItemSlots]
 constexpr int kItemEmpty = kItemFull + kItemSlots;
-constexpr int kFinal = kItemEmpty + kItemSlots;
+constexpr int kDraw = kItemEmpty + kItemSlots;  // the item's loads are nearly all issued
+constexpr int kFinal = kDraw + 1;
 constexpr int kNumBars = kFinal + 1;
 
 struct Item {
@@ -182,47 +184,46 @@ __device__ __forceinline__ int tiles_of(int keys) { return (keys + kTile - 1) / 
 // those that are whole.
 struct Cuts {
   int pairs, most, cap;  // pairs, parts of the last one
-  int rows, len, pos;    // tokens of a pair, keys, position of query 0
-  bool causal, none;
-  __device__ __forceinline__ Cuts(const Params& p, const Seq& s, int cap_)
-      : pairs(s.pairs), cap(cap_), rows(p.span), len(s.len), pos(s.pos), causal(p.x.causal != 0), none(s.n == 0) {
-    most = max(1, (tiles_of(seen_by(p, s, s.n)) + cap - 1) / cap);
+  int all;               // parts that every pair has
+  int rows, pos;         // tokens of a pair, position of query 0
+  // `last`: key tiles of the last pair
+  __device__ __forceinline__ Cuts(const Params& p, int pairs_, int last, int pos_, int cap_) : pairs(pairs_), cap(cap_), rows(p.span), pos(pos_) {
+    most = max(1, (last + cap - 1) / cap);
+    all = p.x.causal && pairs > 1 ? min(most, static_cast<int>(static_cast<uint32_t>(max(pos, 0)) / (static_cast<uint32_t>(cap) * kTile)) + 1) : most;
   }
   // pairs that are cut into `c` parts or more: those that see more than c - 1 parts' keys
   __device__ __forceinline__ int at_least(int c) const {
-    if (c <= 1 || pairs <= 1) return c <= most ? pairs : 0;
-    const int64_t keys = static_cast<int64_t>(c - 1) * cap * kTile;
-    if (none || len <= keys) return 0;
-    if (!causal) return pairs;
-    const uint32_t behind = static_cast<uint32_t>(max(static_cast<int64_t>(0), keys - pos));  // below 2^32: keys < len
+    if (c <= all) return pairs;
+    if (c > most) return 0;
+    const uint32_t behind = static_cast<uint32_t>((c - 1) * cap * kTile) - static_cast<uint32_t>(pos);  // above 0, below 2^32
     return pairs - static_cast<int>(min(static_cast<uint32_t>(pairs), behind / static_cast<uint32_t>(rows)));
   }
   __device__ __forceinline__ int64_t parts() const {  // of a key head
-    int64_t n = 0;
-    for (int c = 1; c <= most; ++c) n += at_least(c);
+    int64_t n = static_cast<int64_t>(all) * pairs;
+#pragma unroll 1
+    for (int c = all + 1; c <= most; ++c) n += at_least(c);
     return n;
   }
-  __device__ __forceinline__ int64_t cut_parts() const { return parts() - (pairs - at_least(2)); }
   // pair, part and parts of a key head's part k
-  __device__ __forceinline__ void find(int64_t k, int& m, int& cut, int& cuts) const {
-    int behind = 0;  // pairs with more parts
-    for (int c = most;; --c) {
+  __device__ __forceinline__ void find(int k, int& m, int& cut, int& cuts) const {
+    int behind = 0, c = most;  // pairs with more parts
+#pragma unroll 1
+    for (; c > all; --c) {
       const int here = at_least(c) - behind;
-      if (c == 1 || k < static_cast<int64_t>(here) * c) {
-        m = pairs - 1 - behind - static_cast<int>(k / c);
-        cut = static_cast<int>(k % c);
-        cuts = c;
-        return;
-      }
-      k -= static_cast<int64_t>(here) * c;
+      if (k < here * c) break;
+      k -= here * c;
       behind += here;
     }
+    m = pairs - 1 - behind - k / c;
+    cut = k % c;
+    cuts = c;
   }
   // parts of a key head before the first one of its i-th pair from the end, and that pair's
   __device__ __forceinline__ int64_t before(int i, int& cuts) const {
-    int64_t n = 0;
-    cuts = 0;
-    for (int c = 1; c <= most; ++c) {
+    int64_t n = static_cast<int64_t>(all) * i;
+    cuts = all;
+#pragma unroll 1
+    for (int c = all + 1; c <= most; ++c) {
       const int there = at_least(c);
       n += min(i, there);
       if (i < there) cuts = c;
@@ -230,12 +231,14 @@ struct Cuts {
     return n;
   }
 };
+__device__ __forceinline__ Cuts cuts_of(const Params& p, const Seq& s, int cap) { return Cuts(p, s.pairs, tiles_of(seen_by(p, s, s.n)), s.pos, cap); }
 
 // ------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 512;
 constexpr int kMinTiles = 4;    // key tiles of a part at least
-constexpr int kPartCost = 5;    // of a partial state, its way out and back, in key tiles
+constexpr int64_t kMostItems = (int64_t(1) << 31) - 384;  // and drawn ones behind them
 constexpr int kRankSeqs = 256;  // sequences of which the longest come first
+constexpr int kWarpSeqs = 32;   // sequences that a warp plans, one to a lane
 
 // Sums over the threads before this one, and over the block.
 template <int N>
@@ -272,19 +275,176 @@ __device__ __forceinline__ V warp_sum(V v) {
   return v;
 }
 
-// One block: counts the work, decides what is cut, puts the sequences with the
-// longest items first, which leaves short ones to even out the end, and numbers
-// everything.  Every call waits for it, so it goes round the block three times only.
+// Parts of at most `cap` tiles.  The candidates are an SM's share of the work, a half, a third
+// and a fifth of it (long items among short ones), and as many parts to an item as one to four
+// rounds of the SMs have (items alike: chunks over long contexts); or nothing is cut.
+constexpr int kCandidates = 8;
+__device__ __forceinline__ int share_of(const Params& p, int64_t work) {
+  int64_t rest;
+  return static_cast<int>(min(divide(work + p.sms - 1, p.sms, rest), static_cast<int64_t>(1) << 24));
+}
+__device__ __forceinline__ int cap_of(const Params& p, int share, int most, int64_t items, int i) {
+  if (i < 4) return max(kMinTiles, share / (i == 3 ? 5 : i + 1));
+  const int each = max(1, (i - 3) * p.sms / static_cast<int>(max(static_cast<int64_t>(1), min(items, static_cast<int64_t>(1) << 24))));
+  return max(kMinTiles, (most + each - 1) / each);
+}
+// When a plan is estimated to end, in key tiles: an item's end costs two, that of a part three
+// more, and parts alike take whole rounds of the SMs; behind that the second launch joins the
+// states.  Against an even share of the work plus half of the longest part, which leaves
+// rounds out: 128 tokens over 100000 keys 231 -> 166 us, 512 over 30000 236 -> 209, three
+// chunks of 257 to 300 over 5000 to 60000 252 -> 225, 8 of 64 over 8000 108 -> 86.
+// Rounded step by step: the merge's plan and the attention's have to agree.
+__device__ __forceinline__ float time_of(const Params& p, int64_t work, int64_t parts, int64_t states, int longest) {
+  const int n = static_cast<int>(max(static_cast<int64_t>(1), min(parts, static_cast<int64_t>(1) << 30)));
+  const int rounds = (n + p.sms - 1) / p.sms;
+  const float all = __ll2float_rn(work + 2ll * n + 3 * states);
+  const float even = __fdiv_rn(__fmul_rn(__int2float_rn(rounds), all), __int2float_rn(n));
+  return __fadd_rn(fmaxf(even, __int2float_rn(longest + 2)), states > 0 ? __int2float_rn(2 + static_cast<int>(states / 64)) : 0.f);
+}
+// Whether a plan with cuts can end before `least`.
+__device__ __forceinline__ bool cuts_may_pay(const Params& p, int64_t work, int64_t items, int most, float least) {
+  return most > kMinTiles && p.max_parts > 0 && __fadd_rn(__fdiv_rn(__ll2float_rn(work + 2 * items), __int2float_rn(p.sms)), 2.f) < least;
+}
+// Key tiles of a sequence's items: the first and the last, between which they grow evenly.
+__device__ __forceinline__ int64_t work_of(const Params& p, const Seq& s, int last) {
+  return static_cast<int64_t>(s.pairs) * p.x.n_kv * (tiles_of(seen_by(p, s, p.span)) + last) / 2;
+}
+// Parts, partial states and items to join of a sequence.
+__device__ __forceinline__ void count_parts(const Params& p, const Seq& s, int cap, int64_t (&v)[3]) {
+  const Cuts cuts = cuts_of(p, s, cap);
+  v[0] = cuts.parts() * p.x.n_kv;
+  v[2] = static_cast<int64_t>(cuts.at_least(2)) * p.x.n_kv;
+  v[1] = v[0] - (static_cast<int64_t>(cuts.pairs) * p.x.n_kv - v[2]);
+}
+__device__ __forceinline__ void report_seq(bool bad_len, bool bad_table) {
+  if (bad_len || bad_table)
+    atomicOr(&g_prompt_status, (bad_len ? MLA_DEVICE_BAD_LENGTH : 0u) | (bad_table ? MLA_DEVICE_BAD_BLOCK : 0u));
+}
+
+// The plan of few sequences: lane i has the i-th in the order in which they are taken up.
+struct WarpPlan {
+  int items, merges, cap;
+  int seq, first, part0, merge0;
+  Seq s;
+};
+__device__ __forceinline__ WarpPlan plan_warp(const Params& p) {
+  const int B = p.x.B, lane = threadIdx.x & 31;
+  WarpPlan w;
+  Seq s = {};
+  int last = -1;
+  int64_t work = 0;
+  if (lane < B) {
+    s = load_seq(p, lane);
+    last = tiles_of(seen_by(p, s, s.n));
+    work = work_of(p, s, last);
+  }
+  work = warp_sum(work);
+  const int most = __reduce_max_sync(0xffffffffu, last);
+  w.cap = max(most, 1);
+  const int64_t items = warp_sum(static_cast<int64_t>(s.pairs) * p.x.n_kv);
+  float least = time_of(p, work, items, 0, most);
+  if (cuts_may_pay(p, work, items, most, least)) {  // four lanes to a candidate
+    const int cap = cap_of(p, share_of(p, work), most, items, lane >> 2);
+    int states = 0, extra = 0;  // parts that cuts make more
+#pragma unroll 1
+    for (int i = lane & 3; i < ((B + 3) & ~3); i += 4) {
+      const int n = __shfl_sync(0xffffffffu, s.pairs, i), end = __shfl_sync(0xffffffffu, last, i), pos = __shfl_sync(0xffffffffu, s.pos, i);
+      if (i < B) {
+        const Cuts cuts(p, n, end, pos, min(cap, most));
+        const int64_t more = (cuts.parts() - n) * p.x.n_kv;
+        extra += static_cast<int>(min(more, static_cast<int64_t>(1) << 20));
+        states += static_cast<int>(min(more + static_cast<int64_t>(cuts.at_least(2)) * p.x.n_kv, static_cast<int64_t>(1) << 20));
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      states += __shfl_xor_sync(0xffffffffu, states, o);
+      extra += __shfl_xor_sync(0xffffffffu, extra, o);
+    }
+    const float time = cap < most && states <= p.max_parts ? time_of(p, work, items + extra, states, cap) : INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < 32; i += 32 / kCandidates) {
+      const float other = __shfl_sync(0xffffffffu, time, i);
+      const int its = __shfl_sync(0xffffffffu, cap, i);
+      if (other < least) {
+        least = other;
+        w.cap = its;
+      }
+    }
+  }
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < B; ++i) {
+    const int other = __shfl_sync(0xffffffffu, last, i);
+    rank += other > last || (other == last && i < lane) ? 1 : 0;
+  }
+  w.seq = 0;
+#pragma unroll 1
+  for (int i = 0; i < B; ++i)
+    if (__shfl_sync(0xffffffffu, rank, i) == lane) w.seq = i;
+  auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, w.seq); };
+  w.s.n = of(s.n);
+  w.s.len = of(s.len);
+  w.s.pos = of(s.pos);
+  w.s.q0 = of(s.q0);
+  w.s.key0 = of(s.key0);
+  w.s.pairs = of(s.pairs);
+  w.s.bad_len = of(s.bad_len ? 1 : 0) != 0;
+  w.s.bad_table = of(s.bad_table ? 1 : 0) != 0;
+  int64_t counts[3] = {0, 0, 0};
+  if (lane < B) count_parts(p, w.s, w.cap, counts);
+  // a sequence has fewer than 2^26 items, but where offsets run back and forth, which is reported
+  constexpr int kMost = (1 << 26) - 1;
+  const int v[3] = {static_cast<int>(min(counts[0], static_cast<int64_t>(kMost))), static_cast<int>(counts[1]), static_cast<int>(counts[2])};
+  int upto[3] = {v[0], v[1], v[2]};
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int y = __shfl_up_sync(0xffffffffu, upto[j], o);
+      if (lane >= o) upto[j] += y;
+    }
+  }
+  w.first = lane < B ? upto[0] - v[0] : 0x7FFFFFFF;
+  w.part0 = upto[1] - v[1];
+  w.merge0 = upto[2] - v[2];
+  const int parts = __shfl_sync(0xffffffffu, upto[0], 31);
+  w.items = parts < kMost ? parts : 0;
+  w.merges = parts < kMost ? __shfl_sync(0xffffffffu, upto[2], 31) : 0;
+  return w;
+}
+
+// Counts the work, decides what is cut, puts the sequences with the longest items
+// first, which leaves short ones to even out the end, and numbers everything.  Few
+// sequences are a warp's work, which every CTA of the attention does again for itself
+// rather than wait for this launch and read what it wrote (5 + 5 us of a call);
+// more are a block's, which goes round three times only.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_constant__ Params p) {
-  constexpr int kWarps = kPlanThreads / 32, kCandidates = 4;
+  constexpr int kWarps = kPlanThreads / 32;
   __shared__ int64_t part[3][kWarps];
-  __shared__ int64_t work_of[kWarps], cost_of[kCandidates];
-  __shared__ int most_of[kWarps], lengths[kRankSeqs], order[kRankSeqs];
+  __shared__ int64_t works[kWarps], counts[kWarps];
+  __shared__ float times[kCandidates];
+  __shared__ int mosts[kWarps], lengths[kRankSeqs], order[kRankSeqs];
   const int B = p.x.B, Hkv = p.x.n_kv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunks = (B + kPlanThreads - 1) / kPlanThreads;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int64_t work = 0;  // key tiles
-  int most = 0;      // of an item
+  if (B <= kWarpSeqs) {  // one warp was launched
+    if (lane == 0) p.head->next = 0;
+    const WarpPlan w = plan_warp(p);
+    if (lane < B) {
+      report_seq(w.s.bad_len, w.s.bad_table);
+      p.part0[lane] = w.part0;
+      p.merge0[lane] = w.merge0;
+      p.order[lane] = w.seq;
+    }
+    if (lane == 0) {
+      p.head->merges = w.merges;
+      p.head->cap = w.cap;
+    }
+    return;
+  }
+  int64_t work = 0, items = 0;  // key tiles of all items
+  int most = 0;                 // of an item
   bool bad_len = false, bad_table = false;
   for (int c = 0; c < chunks; ++c) {
     const int b = c * kPlanThreads + tid;
@@ -293,39 +453,43 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     bad_len = bad_len || s.bad_len;
     bad_table = bad_table || s.bad_table;
     const int last = tiles_of(seen_by(p, s, s.n));
-    // the tiles of the first and the last pair, between which they grow evenly
-    work += static_cast<int64_t>(s.pairs) * Hkv * (tiles_of(seen_by(p, s, p.span)) + last) / 2;
+    work += work_of(p, s, last);
+    items += static_cast<int64_t>(s.pairs) * Hkv;
     most = max(most, last);
     if (B <= kRankSeqs) lengths[b] = last;
   }
-  if (bad_len || bad_table)
-    atomicOr(&g_prompt_status, (bad_len ? MLA_DEVICE_BAD_LENGTH : 0u) | (bad_table ? MLA_DEVICE_BAD_BLOCK : 0u));
+  report_seq(bad_len, bad_table);
   work = warp_sum(work);
+  items = warp_sum(items);
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0) {
-    work_of[warp] = work;
-    most_of[warp] = most;
+    works[warp] = work;
+    counts[warp] = items;
+    mosts[warp] = most;
   }
   __syncthreads();
-  work = 0;
+  work = items = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    work += work_of[w];
-    most = max(most, most_of[w]);
+    work += works[w];
+    items += counts[w];
+    most = max(most, mosts[w]);
   }
-  // Parts of at most `cap` tiles.  Of no cuts and of parts of an SM's share, a half, a third or a
-  // fifth of it, what is estimated to end first: work and states shared out evenly, and half of the
-  // longest part behind that (twice that time, times SMs).  A warp to each.
-  const int share = static_cast<int>(min((work + p.sms - 1) / p.sms, static_cast<int64_t>(1) << 24));
-  auto cap_of = [&](int i) { return max(kMinTiles, share / (i == 3 ? 5 : i + 1)); };
+  const int share = share_of(p, work);
   if (warp < kCandidates) {
-    const int cap = cap_of(warp);
-    int64_t n = 0;
-    if (cap < most && p.max_parts > 0)
-      for (int b = lane; b < B; b += 32) n += Cuts(p, load_seq(p, b), cap).cut_parts() * Hkv;
-    n = warp_sum(n);
-    if (lane == 0)
-      cost_of[warp] = cap < most && n <= p.max_parts ? 2 * (work + kPartCost * n) + static_cast<int64_t>(cap) * p.sms : INT64_MAX;
+    const int cap = cap_of(p, share, most, items, warp);
+    int64_t states = 0, parts = 0;
+    if (cap < most && p.max_parts > 0) {
+      for (int b = lane; b < B; b += 32) {
+        int64_t v[3];
+        count_parts(p, load_seq(p, b), cap, v);
+        parts += v[0];
+        states += v[1];
+      }
+    }
+    states = warp_sum(states);
+    parts = warp_sum(parts);
+    if (lane == 0) times[warp] = cap < most && p.max_parts > 0 && states <= p.max_parts ? time_of(p, work, parts, states, cap) : INFINITY;
   } else if (warp == kCandidates) {  // ranks
     for (int b = lane; b < B && B <= kRankSeqs; b += 32) {
       int rank = 0;
@@ -335,12 +499,12 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
   }
   __syncthreads();
   int cap = max(most, 1);
-  int64_t least = 2 * work + static_cast<int64_t>(most) * p.sms;
+  float least = time_of(p, work, items, 0, most);
 #pragma unroll
   for (int i = 0; i < kCandidates; ++i) {
-    if (cost_of[i] < least) {
-      least = cost_of[i];
-      cap = cap_of(i);
+    if (times[i] < least) {
+      least = times[i];
+      cap = cap_of(p, share, most, items, i);
     }
   }
   int64_t carry[3] = {0, 0, 0};  // parts, partial states, items to join
@@ -349,10 +513,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     int64_t v[3] = {0, 0, 0}, sum[3];
     if (i < B) {
       const int b = B <= kRankSeqs ? order[i] : i;
-      const Cuts cuts(p, load_seq(p, b), cap);
-      v[0] = cuts.parts() * Hkv;
-      v[2] = static_cast<int64_t>(cuts.at_least(2)) * Hkv;
-      v[1] = v[0] - (static_cast<int64_t>(cuts.pairs) * Hkv - v[2]);
+      count_parts(p, load_seq(p, b), cap, v);
       p.order[i] = b;
     }
     plan_scan(v, sum, part);
@@ -365,8 +526,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     for (int j = 0; j < 3; ++j) carry[j] += sum[j];
   }
   if (tid == 0) {
-    // more than can be numbered: only where offsets run back and forth, which is reported
-    const bool few = carry[0] < (1ll << 30);
+    const bool few = carry[0] < kMostItems;
     p.first[B] = static_cast<int>(carry[0]);
     p.merge0[B] = static_cast<int>(carry[2]);
     p.head->items = few ? static_cast<int>(carry[0]) : 0;
@@ -499,26 +659,37 @@ __device__ __forceinline__ int page_of(const Params& p, int b, int t) {
 
 template <bool kPair>
 __device__ void plan_role(const Params& p, const Ctx& c) {
-  const int total = __ldcg(&p.head->items), cap = __ldcg(&p.head->cap), lane = threadIdx.x & 31, B = p.x.B;
+  const int lane = threadIdx.x & 31, B = p.x.B;
   uint32_t count = 0;
   constexpr int kCtas = Shape<kPair>::kCtas;
   int i = blockIdx.x / kCtas, drawn = 0;
   // a lane keeps a sequence, where there are no more than 32: no item waits for its description then
-  const bool kept = B <= 32;
-  int first = 0x7FFFFFFF, part0 = 0, seq = 0;
-  Seq mine = {};
+  const bool kept = B <= kWarpSeqs;
+  int total, cap, first, part0, seq;
+  Seq mine;
   auto load = [&](int at) {
     seq = __ldcg(p.order + at);
     first = __ldcg(p.first + at);
     part0 = __ldcg(p.part0 + at);
     mine = load_seq(p, seq);
   };
-  if (kept && lane < B) load(lane);
+  if (kept) {
+    const WarpPlan w = plan_warp(p);
+    total = w.items;
+    cap = w.cap;
+    first = w.first;
+    part0 = w.part0;
+    seq = w.seq;
+    mine = w.s;
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
+    total = __ldcg(&p.head->items);
+    cap = __ldcg(&p.head->cap);
+  }
   while (true) {
     Item it;
     it.live = i < total ? 1 : 0;
     if (it.live) {
-      if (lane == 0) drawn = static_cast<int>(gridDim.x) / kCtas + atomicAdd(&p.head->next, 1);  // the item behind this one
       int from = 0;  // the lane that has the sequence
       if (kept) from = __popc(__ballot_sync(0xffffffffu, first <= i)) - 1;
       else load(find_seq(p.first, B, i));
@@ -532,7 +703,7 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
       s.pairs = of(mine.pairs);
       s.bad_len = s.bad_table = false;
       const int b = of(seq), Hkv = p.x.n_kv;
-      const Cuts how(p, s, cap);
+      const Cuts how = cuts_of(p, s, cap);
       int k = i - of(first), m, hk, cut = 0, cuts = 1;
       if (how.at_least(2) > 0) {
         how.find(k / Hkv, m, cut, cuts);
@@ -540,9 +711,9 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
       } else {
         // heads whose keys and values fill about a third of L2 go side by side
         const int64_t bytes = static_cast<int64_t>(max(1, s.len)) * (p.x.d_qk + p.x.d_v) * 2;
-        const int group = static_cast<int>(min(static_cast<int64_t>(Hkv), max(static_cast<int64_t>(1), (int64_t(40) << 20) / bytes)));
-        const int64_t per_group = static_cast<int64_t>(s.pairs) * group;
-        const int g = static_cast<int>(k / per_group), heads = min(group, Hkv - g * group), r = static_cast<int>(k - g * per_group);
+        const int group = bytes > (40 << 20) ? 1 : min(Hkv, (40 << 20) / static_cast<int>(bytes));
+        const int per_group = s.pairs * group;  // no more than there are items
+        const int g = k / per_group, heads = min(group, Hkv - g * group), r = k - g * per_group;
         m = s.pairs - 1 - r / heads;
         hk = g * group + r % heads;
       }
@@ -559,8 +730,9 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) tiles[h] = tok + h * half < s.n ? tiles_of(seen_by(p, s, tok + (h + 1) * half)) : 0;
       const int most = max(tiles[0], tiles[1]);
-      it.t0 = static_cast<int>(static_cast<int64_t>(most) * cut / cuts);
-      const int end = static_cast<int>(static_cast<int64_t>(most) * (cut + 1) / cuts);
+      const int each = most / cuts, more = most - each * cuts;  // the first `more` parts have a tile more
+      it.t0 = cut * each + min(cut, more);
+      const int end = it.t0 + each + (cut < more ? 1 : 0);
       it.ta = max(it.t0, min(tiles[0], end));
       it.tb = max(it.t0, min(tiles[1], end));
       it.lo = seen_by(p, s, tok + 1);
@@ -582,7 +754,11 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
     }
     __syncwarp();
     if (!it.live) return;
-    ++count;
+    // CTAs draw as late as will do, so that the one with least left to do is the next to draw:
+    // 9 prompts of 3 to 1680 tokens 62 us when they drew two items ahead, now 52
+    if (!warp_wait(c, kDraw, count & 1)) return;
+    if (count++ == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counter begins at 0
+    if (lane == 0) drawn = static_cast<int>(gridDim.x) / kCtas + atomicAdd(&p.head->next, 1);
     i = uniform(drawn);
   }
 }
@@ -614,8 +790,11 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps) {
       }
       __syncwarp();
     }
+    const bool tells = rank == 0 && lane == 0;
+    if (tells && it.t0 >= end) mbar_arrive(c.bar(kDraw));
     int page = paged && it.t0 < end ? page_of(p, it.b, it.t0) : 0;
     for (int t = it.t0; t < end; ++t) {
+      if (tells && t == max(it.t0, end - kDrawTiles)) mbar_arrive(c.bar(kDraw));
       const int ahead = paged && t + 1 < end ? page_of(p, it.b, t + 1) : 0;
       const int row = paged ? 0 : it.key0 + kTile * t;
       const int block = paged ? (page < 0 ? p.x.num_blocks : page) : 0;  // beyond the pool: zeros
@@ -882,21 +1061,18 @@ __device__ __noinline__ void infinite_columns(const Params& p, const Item& it, i
   }
 }
 
-// Among each eight lanes: lane i's unit u (four words) becomes lane u's unit i.
+// Among each two lanes: units 2i and 2i + 1 (four words each) of the two rows, so
+// that the even lane has both rows' units 2i and the odd one their units 2i + 1.
 __device__ __forceinline__ void turn_units(uint32_t (&y)[32], int lane) {
+  const bool odd = (lane & 1) != 0;
 #pragma unroll
-  for (int m = 1; m < 8; m <<= 1) {
-    const bool up = (lane & m) != 0;
+  for (int u = 0; u < 8; u += 2) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (u & m) continue;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t &lo = y[4 * u + w], &hi = y[4 * (u | m) + w];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, m);
-        if (up) lo = got;
-        else hi = got;
-      }
+    for (int w = 0; w < 4; ++w) {
+      uint32_t &lo = y[4 * u + w], &hi = y[4 * u + 4 + w];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+      if (odd) lo = got;
+      else hi = got;
     }
   }
 }
@@ -1022,13 +1198,14 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
           for (int j = 0; j < 16; ++j)
             y[16 * half + j] = nothing ? 0u : pack16<E>(__uint_as_float(v[2 * j]) * inv, __uint_as_float(v[2 * j + 1]) * inv);
         }
-        // Eight lanes turn the eight 16-byte units of their rows over among them, so that they
-        // write whole 128-byte lines of one row after the other: rows written by their own
-        // threads, 16 bytes of 32 lines a store, took 6000 clocks an item instead of 1500.
+        // Two lanes swap 16-byte units of their rows, so that a store writes whole 32-byte sectors:
+        // rows written by their own threads, halves of sectors, took 6000 clocks an item, these
+        // 4300 and whole 128-byte lines (eight lanes, three times the shuffles) no less.  The rest
+        // is the way to memory: all SMs end items at about the same time.
         turn_units(y, lane);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int to = __shfl_sync(0xffffffffu, at_row, (lane & 24) + j), col = k + 8 * (lane & 7);
+          const int to = __shfl_sync(0xffffffffu, at_row, (lane & 30) + (j & 1)), col = k + 8 * ((lane & 1) + (j & 6));
           if (to >= 0 && col < p.x.d_v)
             *reinterpret_cast<uint4*>(static_cast<E*>(p.x.out) + static_cast<int64_t>(to) * p.x.d_v + col) =
                 make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
@@ -1093,8 +1270,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       mbar_init(c.bar(kItemFull + i), 1);
       mbar_init(c.bar(kItemEmpty + i), kPair ? 2 * kItemReaders - 1 : kItemReaders);  // one MMA warp
     }
+    mbar_init(c.bar(kDraw), 1);
     mbar_init(c.bar(kFinal), 1);
     fence_mbarrier_init_cluster();
+  }
+  if (warp == kLoadWarp && lane < 3) {
+    const CUtensorMap* map = lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v;
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
   if (warp == kMmaWarp) {
     if constexpr (kPair) {
@@ -1114,7 +1296,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   tc_fence_after();
   c.tmem = uniform(static_cast<int>(*reinterpret_cast<volatile uint32_t*>(c.smem + kOffTmem)));
   if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
 
   if (warp < kSoftmaxWarps) {
     regs_increase<kSoftmaxRegs>();
@@ -1132,6 +1313,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     }
   }
 
+  // the launch behind this one reads what the plan has written: it must not end before the plan
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (*c.abort) {
@@ -1170,7 +1353,7 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(const __gri
     const Seq s = load_seq(p, __ldcg(p.order + pos));
     const int k = i - __ldcg(p.merge0 + pos), hk = k % Hkv, m = s.pairs - 1 - k / Hkv;
     int cuts;
-    const int64_t before = Cuts(p, s, cap).before(k / Hkv, cuts);
+    const int64_t before = cuts_of(p, s, cap).before(k / Hkv, cuts);
     const int tok_in = row / p.G, tok = m * p.span + tile * p.tpt + tok_in;
     const bool put = tok_in < p.tpt && tok < (p.x.S1 > 0 ? p.x.S1 : s.n);
     const float* src = p.parts + (__ldcg(p.part0 + pos) + before * Hkv + hk) * p.part_floats + tile * (p.part_floats / p.tiles);
@@ -1232,10 +1415,13 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 constexpr int kMaxParts = 640;  // partial states in the workspace at most
 
 // Whether pairs of CTAs run: they hold half of the keys and values each, which eases
-// shared memory, the bound of a CTA alone, but take 512 rows at a time.
+// shared memory, the bound of a CTA alone, but take 512 rows at a time.  Alone and in
+// pairs: one prompt of 8192, 128 heads of 192 and 128, 1888 and 1680 us; 32 heads of 128
+// on 8 key heads 382 and 366; 16 prompts of 512 (2048 rows to a key head) 77.6 and 81.1;
+// 40 of 20 to 2000 174 and 183.
 bool in_pairs(const Problem& p) {
   const int64_t rows = static_cast<int64_t>(p.T) * (p.n_q / p.n_kv);  // of a key head
-  return p.d_v > 64 && rows >= 1024 * static_cast<int64_t>(p.B) && rows * p.n_kv >= 4 * 512 * 76;
+  return p.d_v > 64 && rows >= 4096 * static_cast<int64_t>(p.B) && rows * p.n_kv >= 4 * 512 * 76;
 }
 int item_tiles(const Problem& p) { return in_pairs(p) ? 4 : 2; }
 
@@ -1372,7 +1558,7 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
     if (none) *map = maps.q;
   }
   const bool bf = x.dtype == MLA_ROPE_BF16;
-  prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+  prompt_plan_kernel<<<1, x.B <= kWarpSeqs ? 32 : kPlanThreads, 0, s>>>(p);
   HEADS_CUDA(cudaGetLastError(), "plan launch");
   const int64_t groups = x.S1 > 0 ? static_cast<int64_t>(x.B) * ((x.S1 + p.span - 1) / p.span) : x.T / p.span + x.B;
   const int64_t most = std::min<int64_t>(p.sms, groups) * x.n_kv + p.max_parts;
@@ -1462,8 +1648,9 @@ mla_status check_dims(const mla_prompt_dims& d) {
   if (st != MLA_OK) return st;
   if (d.B < 0 || d.T < 0 || d.Tk < 0 || d.causal < 0 || d.causal > 1)
     return fail(MLA_ERR_SHAPE, "B, T and Tk must be >= 0, causal 0 or 1");
-  if (static_cast<int64_t>(d.T) * d.n_q >= (1ll << 31) - 256 || d.B > (1 << 24))
-    return fail(MLA_ERR_SHAPE, "T * n_q must be below 2^31 - 256, B at most 2^24");
+  if (static_cast<int64_t>(d.T) * d.n_q >= (1ll << 31) - 1024 || d.B > (1 << 24))
+    return fail(MLA_ERR_SHAPE, "T * n_q must be below 2^31 - 1024, B at most 2^24");
+  if (d.Tk >= INT32_MAX - 256) return fail(MLA_ERR_SHAPE, "Tk=%d must be below 2^31 - 257", d.Tk);
   if (d.num_blocks < 0 || d.num_blocks >= (1 << 24)) return fail(MLA_ERR_SHAPE, "num_blocks=%d outside [0, 2^24)", d.num_blocks);
   if (d.num_blocks > 0 ? d.max_blocks_per_seq < 1 || d.max_blocks_per_seq > (1 << 23) || d.Tk != 0 : d.max_blocks_per_seq != 0)
     return fail(MLA_ERR_SHAPE, "paged keys need max_blocks_per_seq in [1, 2^23] and Tk 0, packed ones max_blocks_per_seq 0");

@@ -263,12 +263,14 @@ def test_other_stream_and_captured():
     assert np.isfinite(np64(out)).all()
 
 
-# Calls with rows enough for pairs of SMs: 512 rows at a time, at least 1024 of a key head for each sequence
+# Calls with rows enough for pairs of SMs (512 rows at a time, at least 4096 of a key head for each sequence), or nearly
 LARGE = [
     dict(lens=[1300], H=128, Hkv=128, D=192, Dv=128, pad=8), dict(lens=[2049], H=80, Hkv=2, D=128, Dv=128, spare=40, begin=3),
     dict(lens=[1025, 1030, 2000], H=48, Hkv=16, D=96, Dv=80, dtype="fp16"), dict(lens=[5, 1500, 0, 1200], H=128, Hkv=4, D=64, Dv=72),
     dict(lens=[1281], H=128, Hkv=1, D=64, Dv=128, causal=False), dict(lens=[700, 900], ctx=[3000, 129], H=100, Hkv=4, D=128, Dv=128, paged=True, layout="head"),
     dict(lens=[1400], ctx=[77], H=112, Hkv=16, D=192, Dv=104, paged=True, layout="shared", dtype="fp16"),
+    dict(lens=[4100], H=48, Hkv=48, D=192, Dv=128, spare=3), dict(lens=[1400, 1500, 1400], H=48, Hkv=16, D=96, Dv=80, dtype="fp16"),
+    dict(lens=[60, 200], ctx=[40000, 9000], H=8, Hkv=2, D=128, Dv=128, paged=True), dict(lens=[33], ctx=[20000], H=6, Hkv=1, D=64, Dv=64, paged=True),
 ]
 
 
