@@ -57,7 +57,9 @@ constexpr int kSmemMost = 232448;
 struct Params {
   Problem x;
   float* parts;    // [groups][tiles][2][part_floats]
-  int4* records;   // [groups] the head whose first part is the group's last: sequence, key head, parts behind it
+  // [groups] the cut head that a group begins, or holds a middle part of: sequence, key head,
+  // parts behind the first, 1 + the part that the group has of it (0: there is none)
+  int4* records;
   int part_floats;
   int G, rows;     // heads to a key head, rows of a key head
   int tiles;       // 16-row tiles of them
@@ -534,10 +536,10 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
         }
       }
     }
-    if (!whole && part == 1 && tile == 0 && lane == 0) {
-      // the groups that hold the rest: up to the one whose share has the head's last unit
-      const int64_t end = sh.from + (sh.count - w.left) + (s.units - u0);  // one behind it
-      p.records[sh.g] = make_int4(b, hk, split.group_of(end - 1) - sh.g, 1);
+    if (u1 < s.units && tile == 0 && lane == 0) {  // the share ends inside the head
+      const int64_t begin = sh.from + (sh.count - w.left) - u0;  // of the head in the stream
+      const int first = u0 > 0 ? split.group_of(begin) : sh.g;
+      p.records[sh.g] = make_int4(b, hk, split.group_of(begin + s.units - 1) - first, 1 + sh.g - first);
     }
     w.left -= u1 - u0;
     w.next_head(p, lane);
@@ -576,8 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the parts of the heads that were cut, 32 quads of columns at a time: a
-// warp to each where there are few parts, else a block, whose warps share them out.
+// Joins the parts of the heads that were cut, 32 quads of columns of a row tile at a
+// time: a block to each group, whose record says what it has to do, so that nothing is
+// searched for.  Few parts are a warp's work, the head's first group has it; many are
+// shared out among a block's warps, and their slices among the groups that hold them.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 constexpr int kAhead = 4;        // parts in flight
 constexpr int kFewParts = 8;
@@ -597,73 +601,39 @@ struct State {
 
 template <typename E>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p) {
-  __shared__ int4 list[2][kMaxGroups];  // sequence, key head, parts behind the first, group
-  __shared__ int sums[kMergeWarps];
   __shared__ float sm[kMergeWarps][6][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tile = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // every block makes the same lists of heads with few and with many parts: a thread counts
-  // its run of the records (both counts in a word), and numbers them behind those before it
-  constexpr int kPer = (kMaxGroups + kMergeThreads - 1) / kMergeThreads;
-  const int g0 = tid * kPer;
-  int4 rec[kPer];
-  int mine = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) rec[i] = g0 + i < p.groups ? __ldcg(p.records + g0 + i) : make_int4(0, 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    rec[i].w = rec[i].w == 0 ? 0 : rec[i].z <= kFewParts ? 1 : 1 << 16;
-    mine += rec[i].w;
-  }
-  int before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += y;
-  }
-  if (lane == 31) sums[warp] = before;
-  __syncthreads();
-  before -= mine;
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int4 entry = make_int4(rec[i].x, rec[i].y, rec[i].z, g0 + i);
-    if (rec[i].w == 1) list[0][before & 0xFFFF] = entry;
-    if (rec[i].w > 1) list[1][before >> 16] = entry;
-    before += rec[i].w;
-  }
-  const int found[2] = {all & 0xFFFF, all >> 16};
-  __syncthreads();
-  const int quads = p.x.d_v / 4, slices = (min(16, p.rows) * quads + 31) / 32 * p.tiles;
-  // parts first, first + step, ... of slice `i` of group g's head
-  auto gather = [&](const int4& rec, int i, int first, int step, State& st, int& r, int& d) {
-    const int tile = i % p.tiles, quad = i / p.tiles * 32 + lane, rows = min(16, p.rows - tile * 16);
+  const int4 rec = __ldcg(p.records + blockIdx.x);
+  if (rec.w == 0) return;
+  const int parts = rec.z + 1, mine = rec.w - 1, group0 = static_cast<int>(blockIdx.x) - mine;
+  const bool few = parts <= kFewParts;
+  if (few && mine > 0) return;
+  const int rows = min(16, p.rows - tile * 16), quads = p.x.d_v / 4, slices = (rows * quads + 31) / 32;
+  // parts first, first + step, ... of slice `i`
+  auto gather = [&](int i, int first, int step, State& st, int& r, int& d) {
+    const int quad = i * 32 + lane;
     r = quad / quads;
     d = (quad - r * quads) * 4;
     const bool in = r < rows;
     if (!in) r = 0;
-    for (int k0 = first; k0 <= rec.z; k0 += kAhead * step) {
+    for (int k0 = first; k0 < parts; k0 += kAhead * step) {
       float2 ml[kAhead];
       float4 v[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int k = k0 + u * step <= rec.z ? k0 + u * step : first;
-        const float* src = p.parts + ((static_cast<int64_t>(rec.w + k) * p.tiles + tile) * 2 + (k > 0 ? 0 : 1)) * p.part_floats;
+        const int k = k0 + u * step < parts ? k0 + u * step : first;
+        const float* src = p.parts + ((static_cast<int64_t>(group0 + k) * p.tiles + tile) * 2 + (k > 0 ? 0 : 1)) * p.part_floats;
         ml[u] = __ldcg(reinterpret_cast<const float2*>(src + rows * p.x.d_v + 2 * r));
         v[u] = __ldcg(reinterpret_cast<const float4*>(src + r * p.x.d_v + d));
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
-        if (k0 + u * step <= rec.z) st.join(ml[u].x, ml[u].y, {v[u].x, v[u].y, v[u].z, v[u].w});
+        if (k0 + u * step < parts) st.join(ml[u].x, ml[u].y, {v[u].x, v[u].y, v[u].z, v[u].w});
     }
     r = in ? tile * 16 + r : -1;
   };
-  auto put = [&](const int4& rec, const State& st, int r, int d) {
+  auto put = [&](const State& st, int r, int d) {
     if (r < 0) return;
     const bool nothing = st.l == 0.f;
     const float inv = nothing ? 0.f : 1.f / st.l;
@@ -674,19 +644,20 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     *reinterpret_cast<uint2*>(static_cast<E*>(p.x.out) + at * p.x.d_v + d) = y;
     if (d == 0 && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (st.m + log2f(st.l)) * 0.69314718055994530942f;
   };
-  for (int i = blockIdx.x + static_cast<int>(gridDim.x) * warp; i < found[0] * slices; i += static_cast<int>(gridDim.x) * kMergeWarps) {
-    const int4 rec = list[0][i / slices];
-    State st;
-    int r, d;
-    gather(rec, i % slices, 0, 1, st, r, d);
-    put(rec, st, r, d);
+  if (few) {
+    for (int i = warp; i < slices; i += kMergeWarps) {
+      State st;
+      int r, d;
+      gather(i, 0, 1, st, r, d);
+      put(st, r, d);
+    }
+    return;
   }
-  for (int i = blockIdx.x; i < found[1] * slices; i += gridDim.x) {
-    const int4 rec = list[1][i / slices];
+  for (int i = mine; i < slices; i += rec.z) {  // the first rec.z parts have groups with this record
     State st;
     int r, d;
-    gather(rec, i % slices, warp, kMergeWarps, st, r, d);
-    __syncthreads();  // the last item's states have been read
+    gather(i, warp, kMergeWarps, st, r, d);
+    __syncthreads();  // the last slice's states have been read
     sm[warp][0][lane] = st.m;
     sm[warp][1][lane] = st.l;
 #pragma unroll
@@ -695,7 +666,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     if (warp != 0) continue;
     for (int k = 1; k < kMergeWarps; ++k)
       st.join(sm[k][0][lane], sm[k][1][lane], {sm[k][2][lane], sm[k][3][lane], sm[k][4][lane], sm[k][5][lane]});
-    put(rec, st, r, d);
+    put(st, r, d);
   }
 }
 
@@ -797,7 +768,7 @@ mla_status launch(const Problem& x, cudaStream_t s) {
   kernel<<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(maps, p);
   HEADS_CUDA(cudaGetLastError(), "kernel launch");
   if (p.groups > 1) {
-    const dim3 grid(static_cast<unsigned>(4 * sms));
+    const dim3 grid(static_cast<unsigned>(p.groups), static_cast<unsigned>(p.tiles));
     HEADS_CUDA(bf ? launch_after(paged_merge_kernel<__nv_bfloat16>, grid, kMergeThreads, 0, s, p)
                   : launch_after(paged_merge_kernel<__half>, grid, kMergeThreads, 0, s, p),
                "merge launch");
