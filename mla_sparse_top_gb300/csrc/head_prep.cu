@@ -16,6 +16,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
+
 #include "heads.h"
 #include "rope_angles.cuh"
 
@@ -588,7 +590,10 @@ mla_status launch(const Job* jobs, int n, int T, int dtype, bool half, Params& p
     int64_t grid = 0;
     bool layer = false;
     for (int i = 0; i < 3; ++i) p.t[i].blocks = 0;
-    for (int i = 0; i < n; ++i) {
+    int by[3] = {0, 1, 2};
+    std::sort(by, by + n, [&](int a, int b) { return jobs[a].n_heads > jobs[b].n_heads; });
+    for (int o = 0; o < n; ++o) {
+      const int i = by[o];
       if (jobs[i].vec != (vec != 0)) continue;
       const mla_status st = split_job(jobs[i], T, dtype, half, &p.t[taken]);
       if (st != MLA_OK) return st;
