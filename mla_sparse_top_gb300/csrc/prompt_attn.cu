@@ -101,13 +101,20 @@ static_assert(kSmemBytes <= 232448 && kOffBars % 8 == 0, "shared memory");
 
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // two of 128 columns each
 
-// What the plan leaves for the other kernels, followed by four int32 arrays over the sequences.
+// What the plan leaves for the other kernels, followed by three int32 arrays over the sequences.
 struct Head {
   int items;    // parts of all items
   int next;     // drawn so far
-  int merges;   // items that were cut
+  int states;   // partial states
   int cap;      // key tiles of a part at most
   int pad[4];
+};
+// Of a partial state: the item that it is a part of.
+struct Record {
+  int row0, tokens;  // first query row, rows from there on that are written
+  int hk;
+  int cut, cuts;     // the part, of so many
+  int pad[3];
 };
 
 struct Params {
@@ -116,8 +123,8 @@ struct Params {
   // of the sequences in the order in which they are taken up
   int* first;    // [B + 1] first part of an item
   int* part0;    // [B] first partial state
-  int* merge0;   // [B + 1] first item to join
   int* order;    // [B] the sequence
+  Record* records;  // [max_parts]
   float* parts;
   int part_floats, max_parts;
   int G, tpt;    // heads to a key head, tokens of a row tile
@@ -218,18 +225,6 @@ struct Cuts {
     cut = k % c;
     cuts = c;
   }
-  // parts of a key head before the first one of its i-th pair from the end, and that pair's
-  __device__ __forceinline__ int64_t before(int i, int& cuts) const {
-    int64_t n = static_cast<int64_t>(all) * i;
-    cuts = all;
-#pragma unroll 1
-    for (int c = all + 1; c <= most; ++c) {
-      const int there = at_least(c);
-      n += min(i, there);
-      if (i < there) cuts = c;
-    }
-    return n;
-  }
 };
 __device__ __forceinline__ Cuts cuts_of(const Params& p, const Seq& s, int cap) { return Cuts(p, s.pairs, tiles_of(seen_by(p, s, s.n)), s.pos, cap); }
 
@@ -309,12 +304,11 @@ __device__ __forceinline__ bool cuts_may_pay(const Params& p, int64_t work, int6
 __device__ __forceinline__ int64_t work_of(const Params& p, const Seq& s, int last) {
   return static_cast<int64_t>(s.pairs) * p.x.n_kv * (tiles_of(seen_by(p, s, p.span)) + last) / 2;
 }
-// Parts, partial states and items to join of a sequence.
-__device__ __forceinline__ void count_parts(const Params& p, const Seq& s, int cap, int64_t (&v)[3]) {
+// Parts and partial states of a sequence.
+__device__ __forceinline__ void count_parts(const Params& p, const Seq& s, int cap, int64_t (&v)[2]) {
   const Cuts cuts = cuts_of(p, s, cap);
   v[0] = cuts.parts() * p.x.n_kv;
-  v[2] = static_cast<int64_t>(cuts.at_least(2)) * p.x.n_kv;
-  v[1] = v[0] - (static_cast<int64_t>(cuts.pairs) * p.x.n_kv - v[2]);
+  v[1] = v[0] - static_cast<int64_t>(cuts.pairs - cuts.at_least(2)) * p.x.n_kv;
 }
 __device__ __forceinline__ void report_seq(bool bad_len, bool bad_table) {
   if (bad_len || bad_table)
@@ -323,8 +317,8 @@ __device__ __forceinline__ void report_seq(bool bad_len, bool bad_table) {
 
 // The plan of few sequences: lane i has the i-th in the order in which they are taken up.
 struct WarpPlan {
-  int items, merges, cap;
-  int seq, first, part0, merge0;
+  int items, states, cap;
+  int seq, first, part0;
   Seq s;
 };
 __device__ __forceinline__ WarpPlan plan_warp(const Params& p) {
@@ -391,26 +385,25 @@ __device__ __forceinline__ WarpPlan plan_warp(const Params& p) {
   w.s.pairs = of(s.pairs);
   w.s.bad_len = of(s.bad_len ? 1 : 0) != 0;
   w.s.bad_table = of(s.bad_table ? 1 : 0) != 0;
-  int64_t counts[3] = {0, 0, 0};
+  int64_t counts[2] = {0, 0};
   if (lane < B) count_parts(p, w.s, w.cap, counts);
   // a sequence has fewer than 2^26 items, but where offsets run back and forth, which is reported
   constexpr int kMost = (1 << 26) - 1;
-  const int v[3] = {static_cast<int>(min(counts[0], static_cast<int64_t>(kMost))), static_cast<int>(counts[1]), static_cast<int>(counts[2])};
-  int upto[3] = {v[0], v[1], v[2]};
+  const int v[2] = {static_cast<int>(min(counts[0], static_cast<int64_t>(kMost))), static_cast<int>(counts[1])};
+  int upto[2] = {v[0], v[1]};
 #pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int y = __shfl_up_sync(0xffffffffu, upto[j], o);
       if (lane >= o) upto[j] += y;
     }
   }
   w.first = lane < B ? upto[0] - v[0] : 0x7FFFFFFF;
   w.part0 = upto[1] - v[1];
-  w.merge0 = upto[2] - v[2];
   const int parts = __shfl_sync(0xffffffffu, upto[0], 31);
   w.items = parts < kMost ? parts : 0;
-  w.merges = parts < kMost ? __shfl_sync(0xffffffffu, upto[2], 31) : 0;
+  w.states = parts < kMost ? __shfl_sync(0xffffffffu, upto[1], 31) : 0;
   return w;
 }
 
@@ -421,7 +414,7 @@ __device__ __forceinline__ WarpPlan plan_warp(const Params& p) {
 // more are a block's, which goes round three times only.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_constant__ Params p) {
   constexpr int kWarps = kPlanThreads / 32;
-  __shared__ int64_t part[3][kWarps];
+  __shared__ int64_t part[2][kWarps];
   __shared__ int64_t works[kWarps], counts[kWarps];
   __shared__ float times[kCandidates];
   __shared__ int mosts[kWarps], lengths[kRankSeqs], order[kRankSeqs];
@@ -431,16 +424,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
   if (B <= kWarpSeqs) {  // one warp was launched
     if (lane == 0) p.head->next = 0;
     const WarpPlan w = plan_warp(p);
-    if (lane < B) {
-      report_seq(w.s.bad_len, w.s.bad_table);
-      p.part0[lane] = w.part0;
-      p.merge0[lane] = w.merge0;
-      p.order[lane] = w.seq;
-    }
-    if (lane == 0) {
-      p.head->merges = w.merges;
-      p.head->cap = w.cap;
-    }
+    if (lane < B) report_seq(w.s.bad_len, w.s.bad_table);
+    if (lane == 0) p.head->states = w.states;
     return;
   }
   int64_t work = 0, items = 0;  // key tiles of all items
@@ -481,7 +466,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     int64_t states = 0, parts = 0;
     if (cap < most && p.max_parts > 0) {
       for (int b = lane; b < B; b += 32) {
-        int64_t v[3];
+        int64_t v[2];
         count_parts(p, load_seq(p, b), cap, v);
         parts += v[0];
         states += v[1];
@@ -507,10 +492,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
       cap = cap_of(p, share, most, items, i);
     }
   }
-  int64_t carry[3] = {0, 0, 0};  // parts, partial states, items to join
+  int64_t carry[2] = {0, 0};  // parts, partial states
   for (int c = 0; c < chunks; ++c) {
     const int i = c * kPlanThreads + tid;
-    int64_t v[3] = {0, 0, 0}, sum[3];
+    int64_t v[2] = {0, 0}, sum[2];
     if (i < B) {
       const int b = B <= kRankSeqs ? order[i] : i;
       count_parts(p, load_seq(p, b), cap, v);
@@ -520,17 +505,15 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     if (i < B) {
       p.first[i] = static_cast<int>(carry[0] + v[0]);
       p.part0[i] = static_cast<int>(carry[1] + v[1]);
-      p.merge0[i] = static_cast<int>(carry[2] + v[2]);
     }
 #pragma unroll
-    for (int j = 0; j < 3; ++j) carry[j] += sum[j];
+    for (int j = 0; j < 2; ++j) carry[j] += sum[j];
   }
   if (tid == 0) {
     const bool few = carry[0] < kMostItems;
     p.first[B] = static_cast<int>(carry[0]);
-    p.merge0[B] = static_cast<int>(carry[2]);
     p.head->items = few ? static_cast<int>(carry[0]) : 0;
-    p.head->merges = few ? static_cast<int>(carry[2]) : 0;
+    p.head->states = few ? static_cast<int>(carry[1]) : 0;
     p.head->next = 0;
     p.head->cap = cap;
   }
@@ -737,6 +720,7 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
       it.tb = max(it.t0, min(tiles[1], end));
       it.lo = seen_by(p, s, tok + 1);
       it.part = cuts > 1 ? of(part0) + k : -1;
+      if (it.part >= 0 && lane == 0) p.records[it.part] = {s.q0 + tok, (p.x.S1 > 0 ? p.x.S1 : s.n) - tok, hk, cut, cuts, {}};
     }
     const int s = count % kItemSlots;
     if (!__all_sync(0xffffffffu, mbar_wait<kPair>(c.bar(kItemEmpty + s), ((count / kItemSlots) & 1) ^ 1, c.abort, c.wait_ns))) return;
@@ -1337,66 +1321,68 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
 
 // ------------------------------------------------------------------ merge
 // Joins the parts of the items that were cut: a block takes the 128 rows of a row
-// tile and a quarter of the columns, a thread one row and four columns at a time.
+// tile and a quarter of the columns, a thread one row and four columns at a time.  The
+// parts of an item share its row tiles, and what they are a part of stands in records,
+// so that nothing is searched for.
 constexpr int kMergeThreads = 256, kMergeSlices = 4, kAhead = 2;  // parts in flight
 constexpr int kMergeQuads = kMaxDv / 4 / kMergeSlices / 2;          // four columns each, of a thread
 template <typename E>
 __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int merges = __ldcg(&p.head->merges), cap = __ldcg(&p.head->cap);
-  const int row = threadIdx.x & 127, side = threadIdx.x >> 7, quads = p.x.d_v / 4, Hkv = p.x.n_kv;
+  const int states = __ldcg(&p.head->states);
+  const int row = threadIdx.x & 127, side = threadIdx.x >> 7, quads = p.x.d_v / 4;
   const int per_slice = (quads + kMergeSlices - 1) / kMergeSlices;  // at most 2 * kMergeQuads
-  const int64_t step = static_cast<int64_t>(p.part_floats) * Hkv;           // a pair's parts: heads lie between them
-  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(merges) * p.tiles * kMergeSlices; w += gridDim.x) {
-    const int slice = static_cast<int>(w % kMergeSlices), tile = static_cast<int>(w / kMergeSlices % p.tiles), i = static_cast<int>(w / kMergeSlices / p.tiles);
-    const int pos = find_seq(p.merge0, p.x.B, i);
-    const Seq s = load_seq(p, __ldcg(p.order + pos));
-    const int k = i - __ldcg(p.merge0 + pos), hk = k % Hkv, m = s.pairs - 1 - k / Hkv;
-    int cuts;
-    const int64_t before = cuts_of(p, s, cap).before(k / Hkv, cuts);
-    const int tok_in = row / p.G, tok = m * p.span + tile * p.tpt + tok_in;
-    const bool put = tok_in < p.tpt && tok < (p.x.S1 > 0 ? p.x.S1 : s.n);
-    const float* src = p.parts + (__ldcg(p.part0 + pos) + before * Hkv + hk) * p.part_floats + tile * (p.part_floats / p.tiles);
-    const int quad0 = slice * per_slice + side, quad1 = min(quads, (slice + 1) * per_slice);
-    float top = -INFINITY, l = 0.f, o[kMergeQuads][4] = {};
-    for (int c0 = 0; c0 < cuts; c0 += kAhead) {
-      float mk[kAhead], lk[kAhead];
-      float4 x[kAhead][kMergeQuads];
+  const int64_t step = static_cast<int64_t>(p.part_floats) * p.x.n_kv;      // an item's parts: heads lie between them
+  for (int unit = blockIdx.x; unit < states * kMergeSlices; unit += gridDim.x) {
+    // quarter u % 4 of the row tiles that fall to this part, one after the other among the item's parts
+    const int index = unit / kMergeSlices, slice = unit % kMergeSlices;
+    const int4 rec = __ldcg(reinterpret_cast<const int4*>(p.records + index));  // row0, tokens, hk, cut
+    const int cuts = __ldcg(&p.records[index].cuts), cut = rec.w;
+    for (int tile = cut; tile < p.tiles; tile += cuts) {
+      const int tok_in = row / p.G, tok = tile * p.tpt + tok_in;
+      const bool put = tok_in < p.tpt && tok < rec.y;
+      const float* src = p.parts + index * static_cast<int64_t>(p.part_floats) - cut * step + tile * (p.part_floats / p.tiles);
+      const int quad0 = slice * per_slice + side, quad1 = min(quads, (slice + 1) * per_slice);
+      float top = -INFINITY, l = 0.f, o[kMergeQuads][4] = {};
+      for (int c0 = 0; c0 < cuts; c0 += kAhead) {
+        float mk[kAhead], lk[kAhead];
+        float4 x[kAhead][kMergeQuads];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const float* part = src + min(c0 + u, cuts - 1) * step;
-        mk[u] = __ldcg(part + 128 * p.x.d_v + row);
-        lk[u] = __ldcg(part + 128 * p.x.d_v + 128 + row);
+        for (int u = 0; u < kAhead; ++u) {
+          const float* part = src + min(c0 + u, cuts - 1) * step;
+          mk[u] = __ldcg(part + 128 * p.x.d_v + row);
+          lk[u] = __ldcg(part + 128 * p.x.d_v + 128 + row);
 #pragma unroll
-        for (int q = 0; q < kMergeQuads; ++q)
-          x[u][q] = quad0 + 2 * q < quad1 ? __ldcg(reinterpret_cast<const float4*>(part) + (quad0 + 2 * q) * 128 + row) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+          for (int q = 0; q < kMergeQuads; ++q)
+            x[u][q] = quad0 + 2 * q < quad1 ? __ldcg(reinterpret_cast<const float4*>(part) + (quad0 + 2 * q) * 128 + row) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (c0 + u >= cuts || mk[u] == -INFINITY) continue;  // a part in which the row sees nothing
-        const float next = fmaxf(top, mk[u]), f = top == -INFINITY ? 0.f : exp2f(top - next), w = exp2f(mk[u] - next);
-        top = next;
-        l = l * f + lk[u] * w;
+        for (int u = 0; u < kAhead; ++u) {
+          if (c0 + u >= cuts || mk[u] == -INFINITY) continue;  // a part in which the row sees nothing
+          const float next = fmaxf(top, mk[u]), f = top == -INFINITY ? 0.f : exp2f(top - next), w = exp2f(mk[u] - next);
+          top = next;
+          l = l * f + lk[u] * w;
 #pragma unroll
-        for (int q = 0; q < kMergeQuads; ++q) {
-          o[q][0] = o[q][0] * f + x[u][q].x * w;
-          o[q][1] = o[q][1] * f + x[u][q].y * w;
-          o[q][2] = o[q][2] * f + x[u][q].z * w;
-          o[q][3] = o[q][3] * f + x[u][q].w * w;
+          for (int q = 0; q < kMergeQuads; ++q) {
+            o[q][0] = o[q][0] * f + x[u][q].x * w;
+            o[q][1] = o[q][1] * f + x[u][q].y * w;
+            o[q][2] = o[q][2] * f + x[u][q].z * w;
+            o[q][3] = o[q][3] * f + x[u][q].w * w;
+          }
         }
       }
-    }
-    const bool nothing = l == 0.f;
-    const float inv = nothing ? 0.f : 1.f / l;
-    const int64_t at = static_cast<int64_t>(s.q0 + tok) * p.x.n_q + hk * p.G + (row - tok_in * p.G);
+      const bool nothing = l == 0.f;
+      const float inv = nothing ? 0.f : 1.f / l;
+      const int64_t at = static_cast<int64_t>(rec.x + tok) * p.x.n_q + rec.z * p.G + (row - tok_in * p.G);
 #pragma unroll
-    for (int q = 0; q < kMergeQuads; ++q) {
-      uint2 y = make_uint2(pack16<E>(o[q][0] * inv, o[q][1] * inv), pack16<E>(o[q][2] * inv, o[q][3] * inv));
-      if (nothing) y = make_uint2(0u, 0u);
-      if (put && quad0 + 2 * q < quad1) *reinterpret_cast<uint2*>(static_cast<E*>(p.x.out) + at * p.x.d_v + (quad0 + 2 * q) * 4) = y;
+      for (int q = 0; q < kMergeQuads; ++q) {
+        uint2 y = make_uint2(pack16<E>(o[q][0] * inv, o[q][1] * inv), pack16<E>(o[q][2] * inv, o[q][3] * inv));
+        if (nothing) y = make_uint2(0u, 0u);
+        if (put && quad0 + 2 * q < quad1) *reinterpret_cast<uint2*>(static_cast<E*>(p.x.out) + at * p.x.d_v + (quad0 + 2 * q) * 4) = y;
+      }
+      if (put && slice == 0 && side == 0 && p.x.lse != nullptr)
+        p.x.lse[at] = nothing ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
     }
-    if (put && slice == 0 && side == 0 && p.x.lse != nullptr)
-      p.x.lse[at] = nothing ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
   }
 }
 
@@ -1436,7 +1422,8 @@ int parts_of(const Problem& p) {
   return static_cast<int>(std::min<int64_t>(kMaxParts, items * std::min<int64_t>(kMaxParts, (tiles + kMinTiles - 1) / kMinTiles)));
 }
 int part_floats(const Problem& p) { return item_tiles(p) * (128 * p.d_v + 256); }
-size_t lists_bytes(const Problem& p) { return (sizeof(Head) + (4 * static_cast<size_t>(p.B) + 2) * sizeof(int) + 255) & ~size_t(255); }
+size_t lists_bytes(const Problem& p) { return (sizeof(Head) + (3 * static_cast<size_t>(p.B) + 1) * sizeof(int) + 255) & ~size_t(255); }
+size_t records_bytes(const Problem& p) { return (parts_of(p) * sizeof(Record) + 255) & ~size_t(255); }
 
 cudaLaunchConfig_t config_of(unsigned ctas, bool pair, cudaStream_t s, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
@@ -1507,7 +1494,7 @@ mla_status launch_attention(unsigned ctas, const Maps& maps, const Params& p, cu
 
 }  // namespace
 
-size_t tiles_workspace(const Problem& p) { return lists_bytes(p) + static_cast<size_t>(parts_of(p)) * part_floats(p) * sizeof(float); }
+size_t tiles_workspace(const Problem& p) { return lists_bytes(p) + records_bytes(p) + static_cast<size_t>(parts_of(p)) * part_floats(p) * sizeof(float); }
 
 mla_status launch_tiles(const Problem& x, cudaStream_t s) {
   int sms = 0, cta_pairs = 0;
@@ -1520,9 +1507,9 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
   p.head = reinterpret_cast<Head*>(ws);
   p.first = reinterpret_cast<int*>(ws + sizeof(Head));
   p.part0 = p.first + x.B + 1;
-  p.merge0 = p.part0 + x.B;
-  p.order = p.merge0 + x.B + 1;
-  p.parts = reinterpret_cast<float*>(ws + lists_bytes(x));
+  p.order = p.part0 + x.B;
+  p.records = reinterpret_cast<Record*>(ws + lists_bytes(x));
+  p.parts = reinterpret_cast<float*>(ws + lists_bytes(x) + records_bytes(x));
   p.part_floats = part_floats(x);
   p.max_parts = parts_of(x);
   p.G = x.n_q / x.n_kv;
