@@ -681,22 +681,30 @@ def mla_rope_table(positions, cos, sin, *, params: RopeParams, stream=None):
 
 
 def _rope_tensor(x, out, rows, T: int, rot_off: int, dev: int, what: str) -> RopeTensor:
-    out = x if out is None else out
-    xs, os_ = x.shape, out.shape
-    if len(xs) != 3 or len(os_) != 3 or xs[1:] != os_[1:] or xs[0] != T or x.dtype is not out.dtype:
+    xs, xst, p = x.shape, x.stride(), x.data_ptr()
+    if out is None:
+        os_, ost, o = xs, xst, p
+    else:
+        os_, ost, o = out.shape, out.stride(), out.data_ptr()
+        if x.dtype is not out.dtype or out.get_device() != dev:
+            raise ValueError(f"{what} and its output must be of one type, on the current device, cuda:{dev}")
+    if len(xs) != 3 or len(os_) != 3:
         raise ValueError(f"{what} and its output must be (tokens, heads, head_dim) tensors of one type")
-    xst, ost = x.stride(), out.stride()
-    if xs[2] > 1 and (xst[2] != 1 or ost[2] != 1):
+    n, heads, D = xs
+    rows_out, out_heads, out_D = os_
+    if n != T or out_heads != heads or out_D != D:
+        raise ValueError(f"{what} and its output must be (tokens, heads, head_dim) tensors of one type")
+    if D > 1 and (xst[2] != 1 or ost[2] != 1):
         raise ValueError(f"{what}: the values of a head must be adjacent")
-    if rows is None and os_[0] != T:
+    if rows is None and rows_out != T:
         raise ValueError(f"{what}: the output has another number of tokens")
-    if x.get_device() != dev or out.get_device() != dev:
+    if x.get_device() != dev:
         raise ValueError(f"{what} and its output must be on the current device, cuda:{dev}")
-    if (xs[1] | xs[2] | rot_off) >> 31:
-        _check_sizes(what, xs[1], xs[2], rot_off)
-    return RopeTensor(x.data_ptr(), out.data_ptr(), xst[0], xst[1], ost[0], ost[1],
+    if (heads | D | rot_off) >> 31:
+        _check_sizes(what, heads, D, rot_off)
+    return RopeTensor(p, o, xst[0], xst[1], ost[0], ost[1],
                       None if rows is None else _need(rows, torch.int64, (T,), dev, what + "'s rows"),
-                      os_[0], xs[1], xs[2], rot_off, 0)
+                      rows_out, heads, D, rot_off, 0)
 
 
 def mla_rope_apply(positions, q, k=None, *, params: RopeParams, rot_dim: int, rot_off: int = 0, k_rot_off: int = 0,
@@ -815,6 +823,13 @@ def _heads_fail(st: int):
     raise MlaError(st, load_library().mla_heads_last_error().decode())
 
 
+def _need_row(t, dtype, n: int, dev: int, what: str):
+    """_need of a vector of n values."""
+    if t.dtype is dtype and t.numel() == n and t.dim() == 1 and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _need(t, dtype, (n,), dev, what)
+
+
 _NORM_KINDS = {"rms": 1, "layer": 2}
 
 
@@ -833,14 +848,21 @@ def head_norm(kind: str, weight=None, bias=None, eps: float = 1e-6) -> HeadNorm:
     norm = HeadNorm(None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
                     _NORM_KINDS[kind], fp32, eps, 0)
     norm.tensors = given
+    _keep_norm(norm)
     return norm
 
 
-def _check_norm(norm, x, dev: int, what: str):
-    if norm is not None:
-        for t in norm.tensors:
-            if t.numel() != x.shape[2] or t.get_device() != dev or (t.dtype is not torch.float32 and t.dtype is not x.dtype):
-                raise ValueError(f"{what}'s norm must have {x.shape[2]} weights of fp32 or {x.dtype} on cuda:{dev}")
+def _keep_norm(norm):
+    """What calls compare of a norm's tensors, read once: (values, dtype, device), None without weights."""
+    t = norm.tensors[0] if norm.tensors else None
+    norm.of = None if t is None else (t.numel(), t.dtype, t.get_device())
+
+
+def _check_norm(norm, D: int, dtype, dev: int, what: str):
+    if norm is not None and norm.of is not None:
+        n, t, on = norm.of
+        if n != D or on != dev or (t is not torch.float32 and t is not dtype):
+            raise ValueError(f"{what}'s norm must have {D} weights of fp32 or {dtype} on cuda:{dev}")
     return norm
 
 
@@ -854,43 +876,45 @@ def mla_norm_rope(positions, q, k=None, *, params: RopeParams | None = None, rot
     are those of mla_rope_apply.  rot_dim 0 rotates nothing (positions and
     params may be None)."""
     lib = load_library()
-    T = q.shape[0]
-    if q.dtype not in _ROPE_DTYPES or (k is not None and k.dtype != q.dtype):
+    dtype, sh = q.dtype, q.shape
+    T = sh[0]
+    if dtype not in _ROPE_DTYPES or (k is not None and k.dtype is not dtype):
         raise ValueError("q and k must both be bf16, fp16 or fp32")
     if k_rows is not None and (k is None or k_out is None):
         raise ValueError("k_rows needs k and k_out")
     if (T | rot_dim) >> 31:
         _check_sizes("mla_norm_rope", T, rot_dim)
-    dims = RopeDims(T, rot_dim, 1 if half else 0, 0, _ROPE_DTYPES[q.dtype])
+    dims = RopeDims(T, rot_dim, 1 if half else 0, 0, _ROPE_DTYPES[dtype])
     dev = torch.cuda.current_device()
     qt = _rope_tensor(q, out, None, T, rot_off, dev, "q")
     kt = None if k is None else _rope_tensor(k, k_out, k_rows, T, k_rot_off, dev, "k")
-    pos = None if positions is None else _need(positions, torch.int32, (T,), dev, "positions")
-    st = lib.mla_norm_rope(dims, params, pos, qt, _check_norm(q_norm, q, dev, "q"), kt,
-                           None if k is None else _check_norm(k_norm, k, dev, "k"), _raw_stream(stream, dev))
+    pos = None if positions is None else _need_row(positions, torch.int32, T, dev, "positions")
+    st = lib.mla_norm_rope(dims, params, pos, qt, _check_norm(q_norm, sh[2], dtype, dev, "q"), kt,
+                           None if k is None else _check_norm(k_norm, kt.head_dim, dtype, dev, "k"),
+                           _raw_stream(stream, dev))
     if st != MLA_OK:
         _heads_fail(st)
     _debug_status(heads_device_status, "mla_norm_rope", stream)
     return (q if out is None else out), (k if k_out is None else k_out)
 
 
-def _heads_tensor(x, dtype, dev: int, what: str) -> HeadsTensor:
-    if x.dim() != 3 or x.dtype is not dtype or x.get_device() != dev:
+def _heads_tensor(x, shape, dtype, dev: int, what: str) -> HeadsTensor:
+    """x, whose shape the caller has read: small calls feel every microsecond."""
+    if len(shape) != 3 or x.dtype is not dtype or x.get_device() != dev:
         raise ValueError(f"{what} must be a (tokens, heads, values) tensor of {dtype} on cuda:{dev}")
-    st = x.stride()
-    if st[2] != 1 and x.shape[2] > 1:
+    token, head, value = x.stride()
+    if value != 1 and shape[2] > 1:
         raise ValueError(f"{what}: the values of a head must be adjacent")
-    return HeadsTensor(x.data_ptr(), st[0], st[1])
+    return HeadsTensor(x.data_ptr(), token, head)
 
 
-def _kv_cache(x, heads: int, dtype, dev: int, what: str) -> KvCache:
-    sh = x.shape
-    if len(sh) != 4 or sh[1] != 128 or sh[2] != heads or x.dtype is not dtype or x.get_device() != dev:
+def _kv_cache(x, shape, heads: int, dtype, dev: int, what: str) -> KvCache:
+    if len(shape) != 4 or shape[1] != 128 or shape[2] != heads or x.dtype is not dtype or x.get_device() != dev:
         raise ValueError(f"{what} must be a (blocks, 128, {heads}, values) tensor of {dtype} on cuda:{dev}")
-    st = x.stride()
-    if st[3] != 1 and sh[3] > 1:
+    block, row, head, value = x.stride()
+    if value != 1 and shape[3] > 1:
         raise ValueError(f"{what}: the values of a head must be adjacent")
-    return KvCache(x.data_ptr(), st[0], st[1], st[2])
+    return KvCache(x.data_ptr(), block, row, head)
 
 
 def mla_kv_append(positions, rows, k, v, k_cache, v_cache, *, params: RopeParams | None = None, rot_dim: int = 0,
@@ -903,28 +927,29 @@ def mla_kv_append(positions, rows, k, v, k_cache, v_cache, *, params: RopeParams
     skipped.  q (T, H, Dq): the tokens' queries, normed and rotated in the same
     launch to q_out (None: in place).  Norms are made by head_norm()."""
     lib = load_library()
-    T, heads = k.shape[0], k.shape[1]
-    if k.dtype not in _ROPE_DTYPES:
-        raise ValueError("k must be bf16, fp16 or fp32")
     dev, dtype = torch.cuda.current_device(), k.dtype
-    kt, vt = _heads_tensor(k, dtype, dev, "k"), _heads_tensor(v, dtype, dev, "v")
-    kc, vc = _kv_cache(k_cache, heads, dtype, dev, "k_cache"), _kv_cache(v_cache, heads, dtype, dev, "v_cache")
-    if v.shape[:2] != k.shape[:2] or k_cache.shape[3] != k.shape[2] or v_cache.shape[3] != v.shape[2] \
-            or k_cache.shape[0] != v_cache.shape[0]:
+    if dtype not in _ROPE_DTYPES:
+        raise ValueError("k must be bf16, fp16 or fp32")
+    ks, vs, kcs, vcs = k.shape, v.shape, k_cache.shape, v_cache.shape
+    kt, vt = _heads_tensor(k, ks, dtype, dev, "k"), _heads_tensor(v, vs, dtype, dev, "v")
+    T, heads, D = ks
+    Tv, v_heads, Dv = vs
+    kc, vc = _kv_cache(k_cache, kcs, heads, dtype, dev, "k_cache"), _kv_cache(v_cache, vcs, heads, dtype, dev, "v_cache")
+    blocks = kcs[0]
+    if Tv != T or v_heads != heads or kcs[3] != D or vcs[3] != Dv or vcs[0] != blocks:
         raise ValueError("k, v and the caches must agree in tokens, heads, values and blocks")
-    sizes = (T, heads, k.shape[2], v.shape[2], rot_dim, rot_off, k_cache.shape[0])
-    if (T | heads | sizes[2] | sizes[3] | rot_dim | rot_off | sizes[6] | q_rot_off) >> 31:
-        _check_sizes("mla_kv_append", *sizes, q_rot_off)
-    dims = AppendDims(T, heads, sizes[2], sizes[3], rot_dim, rot_off, 1 if half else 0, _ROPE_DTYPES[dtype], sizes[6])
-    qt = None
+    if (T | heads | D | Dv | rot_dim | rot_off | blocks | q_rot_off) >> 31:
+        _check_sizes("mla_kv_append", T, heads, D, Dv, rot_dim, rot_off, blocks, q_rot_off)
+    dims = AppendDims(T, heads, D, Dv, rot_dim, rot_off, 1 if half else 0, _ROPE_DTYPES[dtype], blocks)
+    qt = qn = None
     if q is not None:
         if q.dtype is not dtype:
             raise ValueError("q and k must have one type")
         qt = _rope_tensor(q, q_out, None, T, q_rot_off, dev, "q")
-    pos = None if positions is None else _need(positions, torch.int32, (T,), dev, "positions")
-    st = lib.mla_kv_append(dims, params, pos, _need(rows, torch.int64, (T,), dev, "rows"), kt,
-                           _check_norm(k_norm, k, dev, "k"), kc, vt, vc, qt,
-                           None if q is None else _check_norm(q_norm, q, dev, "q"), _raw_stream(stream, dev))
+        qn = _check_norm(q_norm, qt.head_dim, dtype, dev, "q")
+    pos = None if positions is None else _need_row(positions, torch.int32, T, dev, "positions")
+    st = lib.mla_kv_append(dims, params, pos, _need_row(rows, torch.int64, T, dev, "rows"), kt,
+                           _check_norm(k_norm, D, dtype, dev, "k"), kc, vt, vc, qt, qn, _raw_stream(stream, dev))
     if st != MLA_OK:
         _heads_fail(st)
     _debug_status(heads_device_status, "mla_kv_append", stream)
@@ -955,17 +980,27 @@ def mla_prompt_workspace_bytes(dims: PromptDims) -> int:
     return int(load_library().mla_prompt_workspace_bytes(dims))
 
 
-def _need_output(out, lse, q, d_v: int, dev: int):
-    T, H = q.shape[0], q.shape[1]
-    return (_need(out, q.dtype, (T, H, d_v), dev, "out"),
+def _need_output(out, lse, dtype, T: int, H: int, d_v: int, dev: int):
+    return (_need(out, dtype, (T, H, d_v), dev, "out"),
             None if lse is None else _need(lse, torch.float32, (T, H), dev, "lse"))
 
 
-def _need_cache(x, d: int, dims, dtype, dev: int, what: str) -> KvCache:
-    t = _kv_cache(x, dims.n_kv, dtype, dev, what)
-    if x.shape[0] < dims.num_blocks or x.shape[3] != d:
+def _need_cache(x, d: int, n_kv: int, num_blocks: int, dtype, dev: int, what: str) -> KvCache:
+    sh = x.shape
+    t = _kv_cache(x, sh, n_kv, dtype, dev, what)
+    if sh[0] < num_blocks or sh[3] != d:
         raise ValueError(f"{what} must hold dims.num_blocks pages of {d} values to a head")
     return t
+
+
+def _need_packed(x, shape, dtype, dev: int, what: str) -> KvCache:
+    """Packed keys or values as a cache of one block."""
+    if x.shape != shape or x.dtype is not dtype or x.get_device() != dev:
+        raise ValueError(f"packed {what} must be {shape} of dims, {dtype} on cuda:{dev}")
+    token, head, value = x.stride()
+    if value != 1 and shape[2] > 1:
+        raise ValueError(f"{what}: the values of a head must be adjacent")
+    return KvCache(x.data_ptr(), 0, token, head)
 
 
 def _need_workspace(workspace, dev: int):
@@ -991,23 +1026,22 @@ def mla_prompt_attn_fwd(q, k, v, cu_q, out, lse, workspace, *, cu_k=None, block_
     lib = load_library()
     if dims is None:
         dims = prompt_dims(q, k, v, cu_q, block_table=block_table, causal=causal)
-    dev, i32, dtype, B, D, Dv = torch.cuda.current_device(), torch.int32, q.dtype, dims.B, dims.d_qk, dims.d_v
-    if _attn_dtype(q) != dims.dtype or q.shape != (dims.T, dims.n_q, D):
+    dev, i32, dtype, sh = torch.cuda.current_device(), torch.int32, q.dtype, q.shape
+    B, T, H, Hkv, D, Dv, blocks = dims.B, dims.T, dims.n_q, dims.n_kv, dims.d_qk, dims.d_v, dims.num_blocks
+    if _attn_dtype(q) != dims.dtype or sh != (T, H, D):
         raise ValueError("q must be (T, n_q, d_qk) of dims and of its type")
-    qt = _heads_tensor(q, dtype, dev, "q")
-    if dims.num_blocks > 0:
-        kt, vt = _need_cache(k, D, dims, dtype, dev, "k"), _need_cache(v, Dv, dims, dtype, dev, "v")
+    qt = _heads_tensor(q, sh, dtype, dev, "q")
+    if blocks > 0:
+        kt, vt = _need_cache(k, D, Hkv, blocks, dtype, dev, "k"), _need_cache(v, Dv, Hkv, blocks, dtype, dev, "v")
     else:
-        if k.shape != (dims.Tk, dims.n_kv, D) or v.shape != (dims.Tk, dims.n_kv, Dv):
-            raise ValueError("packed k and v must be (Tk, n_kv, d_qk) and (Tk, n_kv, d_v) of dims")
-        kh, vh = _heads_tensor(k, dtype, dev, "k"), _heads_tensor(v, dtype, dev, "v")
-        kt, vt = KvCache(kh.data, 0, kh.token_stride, kh.head_stride), KvCache(vh.data, 0, vh.token_stride, vh.head_stride)
-        if cu_k is None and dims.Tk < dims.T:
+        Tk = dims.Tk
+        kt, vt = _need_packed(k, (Tk, Hkv, D), dtype, dev, "k"), _need_packed(v, (Tk, Hkv, Dv), dtype, dev, "v")
+        if cu_k is None and Tk < T:
             raise ValueError("without cu_k, k and v must have q's rows")
-    ptrs = (_need(cu_q, i32, (B + 1,), dev, "cu_q"), None if cu_k is None else _need(cu_k, i32, (B + 1,), dev, "cu_k"),
+    ptrs = (_need_row(cu_q, i32, B + 1, dev, "cu_q"), None if cu_k is None else _need_row(cu_k, i32, B + 1, dev, "cu_k"),
             None if block_table is None else _need(block_table, i32, (B, dims.max_blocks_per_seq), dev, "block_table"),
-            None if act_seqs is None else _need(act_seqs, i32, (B,), dev, "act_seqs"))
-    o, l = _need_output(out, lse, q, Dv, dev)
+            None if act_seqs is None else _need_row(act_seqs, i32, B, dev, "act_seqs"))
+    o, l = _need_output(out, lse, dtype, T, H, Dv, dev)
     if softmax_scale is None:
         softmax_scale = D ** -0.5
     st = lib.mla_prompt_attn_fwd(dims, qt, kt, vt, *ptrs, o, l, softmax_scale, *_need_workspace(workspace, dev),
@@ -1046,16 +1080,19 @@ def mla_paged_attn_fwd(q, k_cache, v_cache, block_table, act_seqs, out, lse, wor
     lib = load_library()
     if dims is None:
         dims = paged_dims(q, k_cache, v_cache, block_table, S1=S1)
-    dev, i32, dtype, B = torch.cuda.current_device(), torch.int32, q.dtype, dims.B
-    if _attn_dtype(q) != dims.dtype or q.shape != (B * dims.S1, dims.n_q, dims.d_qk):
+    dev, i32, dtype, sh = torch.cuda.current_device(), torch.int32, q.dtype, q.shape
+    B, H, Hkv, D, Dv, blocks = dims.B, dims.n_q, dims.n_kv, dims.d_qk, dims.d_v, dims.num_blocks
+    T = B * dims.S1
+    if _attn_dtype(q) != dims.dtype or sh != (T, H, D):
         raise ValueError("q must be (B*S1, n_q, d_qk) of dims and of its type")
-    qt = _heads_tensor(q, dtype, dev, "q")
-    kt, vt = _need_cache(k_cache, dims.d_qk, dims, dtype, dev, "k_cache"), _need_cache(v_cache, dims.d_v, dims, dtype, dev, "v_cache")
+    qt = _heads_tensor(q, sh, dtype, dev, "q")
+    kt, vt = (_need_cache(k_cache, D, Hkv, blocks, dtype, dev, "k_cache"),
+              _need_cache(v_cache, Dv, Hkv, blocks, dtype, dev, "v_cache"))
     ptrs = (_need(block_table, i32, (B, dims.max_blocks_per_seq), dev, "block_table"),
-            _need(act_seqs, i32, (B,), dev, "act_seqs"), None if q_lens is None else _need(q_lens, i32, (B,), dev, "q_lens"))
-    o, l = _need_output(out, lse, q, dims.d_v, dev)
+            _need_row(act_seqs, i32, B, dev, "act_seqs"), None if q_lens is None else _need_row(q_lens, i32, B, dev, "q_lens"))
+    o, l = _need_output(out, lse, dtype, T, H, Dv, dev)
     if softmax_scale is None:
-        softmax_scale = dims.d_qk ** -0.5
+        softmax_scale = D ** -0.5
     st = lib.mla_paged_attn_fwd(dims, qt, kt, vt, *ptrs, o, l, softmax_scale, *_need_workspace(workspace, dev),
                                 _raw_stream(stream, dev))
     if st != MLA_OK:
