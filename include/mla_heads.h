@@ -79,7 +79,7 @@ typedef struct mla_head_norm {
  * strides) whole heads are read and written; rows of out must be distinct.
  * Heads of any size, stride and alignment of whole elements work; those whose
  * parts are multiples of 16 bytes run in 16-byte accesses.  One launch, two
- * where only one of the tensors is that aligned.
+ * where the tensors need accesses of different kinds.
  */
 mla_status mla_norm_rope(const mla_rope_dims* dims, const mla_rope_params* params, const int32_t* positions,
                          const mla_rope_tensor* q, const mla_head_norm* q_norm, const mla_rope_tensor* k,
@@ -118,7 +118,9 @@ typedef struct mla_append_input {
  * q->rows must be NULL.  rows int64 [T], positions int32 [T] (may be NULL where
  * rot_dim is 0).  Caches and outputs may have no byte in common with one
  * another or with an input; views that interleave are told apart by their
- * strides.  One launch, two where only some of the tensors are 16-byte aligned.
+ * strides.  Of tokens with the same row, the row holds values of one or of
+ * several.  One launch, up to three where the tensors need accesses of
+ * different kinds (16 bytes, single values of smaller and of larger heads).
  */
 mla_status mla_kv_append(const mla_append_dims* dims, const mla_rope_params* params, const int32_t* positions,
                          const int64_t* rows, const mla_append_input* k, const mla_head_norm* k_norm,
@@ -165,10 +167,11 @@ size_t mla_prompt_workspace_bytes(const mla_prompt_dims* dims);
  * out         dense [T, n_q, d_v], 16-byte aligned; lse fp32 [T, n_q] or NULL
  * workspace   >= mla_prompt_workspace_bytes(dims) bytes, 256-byte aligned
  * out, lse and the workspace may not overlap one another or the inputs
- * (MLA_ERR_UNSUPPORTED).  Three launches on `stream` (the plan of the work, the
- * attention, the merge of rows whose keys several SMs shared), capturable into
- * a CUDA graph; the first call on each device sets kernel attributes: make it
- * before any stream capture begins.
+ * (MLA_ERR_UNSUPPORTED).  Two launches on `stream` (the plan of the work, the
+ * attention), three where sequences may have more than 512 keys (the join of
+ * rows whose keys several SMs shared), capturable into a CUDA graph; the first
+ * call on each device sets kernel attributes: make it before any stream capture
+ * begins.  T * n_q below 2^31 - 1024, Tk below 2^31 - 257.
  */
 mla_status mla_prompt_attn_fwd(const mla_prompt_dims* dims, const mla_heads_tensor* q, const mla_kv_cache* k,
                                const mla_kv_cache* v, const int32_t* cu_q, const int32_t* cu_k,
@@ -192,8 +195,11 @@ size_t mla_paged_workspace_bytes(const mla_paged_dims* dims);
  * chain of S1) over its pages.  Row b * S1 + s of q, out and lse is token s of
  * sequence b; q_lens int32 [B] (NULL: S1 each; negative counts as 0, more than
  * S1 as S1) are the tokens that there are, the rows behind them get out = 0 and
- * lse = -inf.  act_seqs counts the new tokens too.  Tensors, workspace and
- * overlaps as mla_prompt_attn_fwd.
+ * lse = -inf.  act_seqs counts the new tokens too.  Tensors, workspace,
+ * overlaps and the first call as mla_prompt_attn_fwd; B * S1 * n_q below 2^31 -
+ * 1024.  Up to 64 rows (S1 * n_q / n_kv) of a key head: two launches (the
+ * attention, the join of heads that several SMs shared); more go through the
+ * kernels of prompts.
  */
 mla_status mla_paged_attn_fwd(const mla_paged_dims* dims, const mla_heads_tensor* q, const mla_kv_cache* k,
                               const mla_kv_cache* v, const int32_t* block_table, const int32_t* act_seqs,

@@ -8,10 +8,10 @@
 // heads, so angles and weights are made once.  Everything is read once and
 // written once: bound by memory.
 // Measured (graph replay): 8192 tokens of 32 + 8 heads of 128 in bf16, RMS norms and
-// rotation, 42 us (168 MB, 4.0 TB/s); 16384 new tokens to the cache, 28 + 4 + 4 heads of
-// 128 of which 64 turn, no norm, 62 us (302 MB, 4.9 TB/s); 64 new tokens 5.9 us, of which
-// the launch is most; 4099 tokens of 17 fp32 heads of 107, LayerNorm, 40 us: single
-// values and two sums that follow one another, bound by instructions.
+// rotation, 33 us (168 MB, 5.1 TB/s), with 64 + 8 heads 52 (5.8 TB/s); 16384 new tokens to
+// the cache, 28 + 4 + 4 heads of 128 of which 64 turn, no norm, 54 us (302 MB, 5.6 TB/s); 64 new tokens 5.6 us, of which
+// the launch is most; 4099 tokens of 17 fp32 heads of 107, LayerNorm, 36 us: single
+// values and two sums that follow one another, bound by latency and instructions.
 #include <cuda_runtime.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -27,10 +27,16 @@ using mlarp::Freqs;
 using mlarp::Pack;
 
 constexpr int kThreads = 128;
-constexpr int kMaxPasses = 16;  // heads of a group (8: 16384 new tokens to the cache 67 -> 72 us)
-// Heads whose loads are in flight while one is worked on.  2 / 3 / 4 / 5: norms of 8192
-// tokens 44.6 / 44.3 / 42.2 / 48.3 us, 16384 new tokens to the cache 72.7 / 67 / 62 / 61.
-constexpr int kHeadsAhead = 4;
+constexpr int kMaxPasses = 16;  // heads of a group (8: 16384 new tokens to the cache 54 -> 57 us)
+// Heads in flight and the one that is worked on, in shared memory: in registers, four ahead,
+// norms of 8192 tokens took 42 us and 16384 new tokens to the cache 60.  2 / 3 / 4 / 6 / 8:
+// 36 / 34 / 33 / 34 / 39 and 63 / 57 / 54 / 60 / 67.
+constexpr int kStages = 4;
+constexpr int kHeadsAhead = 2;  // of single values, in registers
+// Blocks of an SM: 5 to 7 alike, 8 (64 registers) 38 and 54 us.  Of single values, with or
+// without a mean: latency binds, so as many as the registers let go (5 and 6: 4099 tokens of 17
+// fp32 heads of 107 25 us instead of 21, with LayerNorm 37 and 36).
+constexpr int kBlocks = 5, kLayerBlocks = 7, kSingleBlocks = 8;
 
 __device__ unsigned int g_prep_status = 0;
 
@@ -49,6 +55,7 @@ struct Tensor {
   int pairs, half;     // of the rotation; 0 pairs: none
   int rot_units;       // units of a head that hold rotated values
   int units;           // all units of a head
+  int per_lane;        // units of a lane
   int lanes;           // of a group, a power of two
   int chunks;          // times that the group's lanes go over a head
   int tok_rows;        // tokens of a block
@@ -186,6 +193,10 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
   Two r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from) : "memory");
 }
 
 // The rotation of a normed pair is linear in the pair: weights go into the cosines
@@ -364,27 +375,63 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
   const int64_t x_step = w.head_rows * w.xh, o_step = w.head_rows * w.oh;
   const int heads = live ? min(w.passes, (w.n_heads - h0 + w.head_rows - 1) / w.head_rows) : 0;  // of this group
   if (w.chunks == 1) {
-    // heads ahead of the one that is worked on: what is in flight carries the rate
-    constexpr int kSets = kHeadsAhead + 1;
-    Pack<E, V> a[kSets][KU], b[kSets][KU];
+    float mean = 0.f, inv = 1.f;
+    auto sums = [&](const Pack<E, V>(&a)[KU], const Pack<E, V>(&b)[KU]) {
+      if (layer) mean = group_sum(part(a, b, 0.f, false)) * w.inv_d;
+      if (normed) inv = root(group_sum(part(a, b, mean, true)));
+    };
+    if constexpr (V > 1) {
+      // copies ahead of the head that is worked on, each lane's into places of its own
+      __shared__ uint4 stage[kStages][2][kThreads];
+      static_assert(KU == 1 && sizeof(Pack<E, V>) == 16, "a unit of a lane");
+      auto fetch = [&](int slot, bool on) {
+        if (on && at.in[0]) {
+          copy_async(&stage[slot][0][tid], x + at.d[0]);
+          if (kTwo && at.rot[0]) copy_async(&stage[slot][1][tid], x + at.d[0] + at.second);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        x += x_step;
+      };
+      auto fetched = [&](const uint4& from, bool on, Pack<E, V>& a) {  // what was not copied is zero
+        const uint4 v = on ? from : make_uint4(0, 0, 0, 0);
+        a.w[0] = v.x;
+        a.w[1] = v.y;
+        a.w[2] = v.z;
+        a.w[3] = v.w;
+      };
+      for (int u = 0; u < kStages - 1; ++u) fetch(u, u < heads);
+      if (normed || w.rot_units > 0) coefficients();  // while the copies are on their way
+#pragma unroll 1
+      for (int it = 0; it < w.passes; ++it, out += o_step) {
+        fetch((it + kStages - 1) % kStages, it + kStages - 1 < heads);
+        asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+        Pack<E, V> a[1], b[1];
+        fetched(stage[it % kStages][0][tid], at.in[0], a[0]);
+        fetched(stage[it % kStages][1][tid], kTwo && at.rot[0], b[0]);
+        sums(a, b);
+        finish(a, b, mean, inv, out, it < heads);
+      }
+    } else {
+      // single values may be too small to copy: heads ahead in registers
+      constexpr int kSets = kHeadsAhead + 1;
+      Pack<E, V> a[kSets][KU], b[kSets][KU];
 #pragma unroll
-    for (int u = 0; u < kSets; ++u)
+      for (int u = 0; u < kSets; ++u)
 #pragma unroll
-      for (int i = 0; i < KU; ++i)
+        for (int i = 0; i < KU; ++i)
 #pragma unroll
-        for (int k = 0; k < Pack<E, V>::W; ++k) a[u][i].w[k] = b[u][i].w[k] = 0;
+          for (int k = 0; k < Pack<E, V>::W; ++k) a[u][i].w[k] = b[u][i].w[k] = 0;
 #pragma unroll
-    for (int u = 0; u < kSets - 1; ++u, x += x_step) at.load(x, u < heads, a[u], b[u]);
-    if (normed || w.rot_units > 0) coefficients();  // while the loads are on their way
-    for (int it = 0; it < w.passes; it += kSets) {
+      for (int u = 0; u < kSets - 1; ++u, x += x_step) at.load(x, u < heads, a[u], b[u]);
+      if (normed || w.rot_units > 0) coefficients();
+      for (int it = 0; it < w.passes; it += kSets) {
 #pragma unroll
-      for (int u = 0; u < kSets; ++u, x += x_step, out += o_step) {
-        if (it + u >= w.passes) break;
-        at.load(x, it + u + kSets - 1 < heads, a[(u + kSets - 1) % kSets], b[(u + kSets - 1) % kSets]);
-        float mean = 0.f, inv = 1.f;
-        if (layer) mean = group_sum(part(a[u], b[u], 0.f, false)) * w.inv_d;
-        if (normed) inv = root(group_sum(part(a[u], b[u], mean, true)));
-        finish(a[u], b[u], mean, inv, out, it + u < heads);
+        for (int u = 0; u < kSets; ++u, x += x_step, out += o_step) {
+          if (it + u >= w.passes) break;
+          at.load(x, it + u + kSets - 1 < heads, a[(u + kSets - 1) % kSets], b[(u + kSets - 1) % kSets]);
+          sums(a[u], b[u]);
+          finish(a[u], b[u], mean, inv, out, it + u < heads);
+        }
       }
     }
     return;
@@ -423,7 +470,7 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
 
 // One block works on one of the tensors.
 template <typename E, int V, int KU, bool kLayer>
-__global__ void __launch_bounds__(kThreads, kLayer ? 4 : 5) head_prep_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, V > 1 ? kBlocks : kLayer ? kLayerBlocks : kSingleBlocks) head_prep_kernel(const __grid_constant__ Params p) {
   int block = static_cast<int>(blockIdx.x), i = 0;
   while (i < 2 && block >= p.t[i].blocks) block -= p.t[i++].blocks;
   const Tensor& w = p.t[i];
@@ -525,8 +572,9 @@ mla_status check_overlaps(const Job* jobs, int n, int T, const int32_t* position
   return MLA_OK;
 }
 
-constexpr int kUnits = 1;        // units of a lane, 16-byte accesses
-constexpr int kSingleUnits = 4;  // single values
+// Units of a lane: one of 16 bytes; of single values two where 64 hold a head, else four (4096
+// tokens of 32 bf16 heads of 128, unaligned: 46 us with four, 30 with two).
+constexpr int kUnits = 1, kFewUnits = 2, kSingleUnits = 4;
 
 // Splits a checked tensor's heads into groups and blocks.
 mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
@@ -554,10 +602,10 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
   const int width = !j.vec ? 1 : (dtype == MLA_ROPE_FP32 ? 4 : 8);
   w->rot_units = j.vec && !half ? j.rot_dim / width : j.rot_dim / 2 / width;
   w->units = w->rot_units + (j.head_dim - j.rot_dim) / width;
-  const int per_lane = j.vec ? kUnits : kSingleUnits;
+  w->per_lane = j.vec ? kUnits : w->units <= 32 * kFewUnits ? kFewUnits : kSingleUnits;
   w->lanes = 1;
   while (w->lanes < 32 && w->lanes < w->units) w->lanes *= 2;
-  w->chunks = (w->units + w->lanes * per_lane - 1) / (w->lanes * per_lane);
+  w->chunks = (w->units + w->lanes * w->per_lane - 1) / (w->lanes * w->per_lane);
   const int rows = kThreads / w->lanes;
   w->tok_rows = std::min(rows, T);
   w->head_rows = std::min(rows / w->tok_rows, j.n_heads);
@@ -575,33 +623,39 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
 }
 
 typedef void (*Kernel)(Params);
+template <typename E>
+Kernel kernel_of(int per_lane, bool layer) {
+  constexpr int V = 16 / sizeof(E);
+  if (per_lane == kUnits) return layer ? head_prep_kernel<E, V, kUnits, true> : head_prep_kernel<E, V, kUnits, false>;
+  if (per_lane == kFewUnits) return layer ? head_prep_kernel<E, 1, kFewUnits, true> : head_prep_kernel<E, 1, kFewUnits, false>;
+  return layer ? head_prep_kernel<E, 1, kSingleUnits, true> : head_prep_kernel<E, 1, kSingleUnits, false>;
+}
 
 mla_status launch(const Job* jobs, int n, int T, int dtype, bool half, Params& p, cudaStream_t s) {
-  static const Kernel kernels[3][2][2] = {
-      {{head_prep_kernel<__nv_bfloat16, 1, kSingleUnits, false>, head_prep_kernel<__nv_bfloat16, 1, kSingleUnits, true>},
-       {head_prep_kernel<__nv_bfloat16, 8, kUnits, false>, head_prep_kernel<__nv_bfloat16, 8, kUnits, true>}},
-      {{head_prep_kernel<__half, 1, kSingleUnits, false>, head_prep_kernel<__half, 1, kSingleUnits, true>},
-       {head_prep_kernel<__half, 8, kUnits, false>, head_prep_kernel<__half, 8, kUnits, true>}},
-      {{head_prep_kernel<float, 1, kSingleUnits, false>, head_prep_kernel<float, 1, kSingleUnits, true>},
-       {head_prep_kernel<float, 4, kUnits, false>, head_prep_kernel<float, 4, kUnits, true>}}};
   p.T = T;
-  for (int vec = 1; vec >= 0; --vec) {
-    int taken = 0;
+  // a launch for the tensors of each kind of access
+  for (int per_lane : {kUnits, kSingleUnits, kFewUnits}) {
+    int taken = 0, by[3] = {0, 1, 2};
     int64_t grid = 0;
     bool layer = false;
-    for (int i = 0; i < 3; ++i) p.t[i].blocks = 0;
-    int by[3] = {0, 1, 2};
+    // those of most heads first: their blocks take longest
     std::sort(by, by + n, [&](int a, int b) { return jobs[a].n_heads > jobs[b].n_heads; });
+    for (int i = 0; i < 3; ++i) p.t[i].blocks = 0;
     for (int o = 0; o < n; ++o) {
-      const int i = by[o];
-      if (jobs[i].vec != (vec != 0)) continue;
-      const mla_status st = split_job(jobs[i], T, dtype, half, &p.t[taken]);
+      const Job& j = jobs[by[o]];
+      Tensor w = {};
+      const mla_status st = split_job(j, T, dtype, half, &w);
       if (st != MLA_OK) return st;
-      layer = layer || jobs[i].norm.kind == MLA_NORM_LAYER;
-      grid += p.t[taken++].blocks;
+      if (w.per_lane != per_lane) continue;
+      layer = layer || j.norm.kind == MLA_NORM_LAYER;
+      grid += w.blocks;
+      p.t[taken++] = w;
     }
     if (taken == 0) continue;
-    kernels[dtype][vec][layer ? 1 : 0]<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
+    const Kernel kernel = dtype == MLA_ROPE_BF16   ? kernel_of<__nv_bfloat16>(per_lane, layer)
+                          : dtype == MLA_ROPE_FP16 ? kernel_of<__half>(per_lane, layer)
+                                                   : kernel_of<float>(per_lane, layer);
+    kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
     HEADS_CUDA(cudaGetLastError(), "launch");
   }
   return MLA_OK;
