@@ -73,9 +73,15 @@ struct Maps {
   CUtensorMap k, v;
 };
 
+// What a head costs beside its units, in units: queries on their way in, rows on their way out.
+// Shares are equal in both: 24 sequences of 500 to 20000 keys, some without new tokens, 71 us
+// -> 61 (0 / 1 / 2 / 3 / 4: 71 / 67 / 62 / 61 / 61), 64 of 100 to 8192 90 -> 87.
+constexpr int kHeadCost = 3;
+
 struct Seq {
-  int n, len, pos, units;  // query tokens, keys within the table, position of token 0
+  int n, len, pos, units;  // query tokens, keys within the table, position of token 0, units of a head
   bool cut_table;
+  __device__ __forceinline__ int steps() const { return units + kHeadCost; }  // of the stream, of a head
 };
 __device__ __forceinline__ Seq make_seq(const Params& p, int act, int q_len) {
   Seq s;
@@ -100,24 +106,25 @@ struct Ctx {
   __device__ volatile uint32_t* mended() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffMended); }
 };
 
-// The stream in equal shares: the first `more` of them have `each` + 1 units, the others `each`.
+// The stream in equal shares: the first `more` of them have `each` + 1 steps, the others `each`.
 struct Split {
   int64_t each, more;
   int groups;
   __device__ __forceinline__ int64_t begin(int g) const { return g * each + min(static_cast<int64_t>(g), more); }
-  __device__ __forceinline__ int group_of(int64_t unit) const {
+  __device__ __forceinline__ int group_of(int64_t step) const {
     int64_t rest;
     const int64_t wide = more * (each + 1);
-    return static_cast<int>(unit < wide ? divide(unit, each + 1, rest) : more + divide(unit - wide, each, rest));
+    return static_cast<int>(step < wide ? divide(step, each + 1, rest) : more + divide(step - wide, each, rest));
   }
 };
 
-// Units of a share at least: fewer parts to join where there is little to read.
-constexpr int kMinUnits = 4;
+// Steps of a share at least: fewer parts to join where there is little to read.
+constexpr int kMinSteps = 4;
+static_assert(kMinSteps > kHeadCost, "a share has a unit");
 
 __device__ __forceinline__ Split split_of(const Params& p, int64_t total) {
   Split s;
-  s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.groups), total / kMinUnits)));
+  s.groups = static_cast<int>(max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.groups), total / kMinSteps)));
   s.each = divide(total, s.groups, s.more);
   return s;
 }
@@ -156,7 +163,7 @@ __device__ Split find_shares(const Params& p, const Ctx& c) {
     len = 0;
     if (b < B) {
       const Seq s = load_seq(p, b);
-      len = static_cast<int64_t>(s.units) * p.x.n_kv;
+      len = static_cast<int64_t>(s.steps()) * p.x.n_kv;
       cut = cut || s.cut_table;
     }
     mine += len;
@@ -169,7 +176,7 @@ __device__ Split find_shares(const Params& p, const Ctx& c) {
     const int b = k * kThreads + tid;
     int64_t sum = total;
     if (chunks > 1) {
-      len = b < B ? static_cast<int64_t>(load_seq(p, b).units) * p.x.n_kv : 0;
+      len = b < B ? static_cast<int64_t>(load_seq(p, b).steps()) * p.x.n_kv : 0;
       pre = carry + scan(len, sum);
     }
     if (b < B) {
@@ -188,11 +195,11 @@ __device__ Split find_shares(const Params& p, const Ctx& c) {
   return split;
 }
 
-// A share of the stream, unit by unit.  Lane i keeps the lengths of sequence b0 + i.
+// A share of the stream, head by head.  Lane i keeps the lengths of sequence b0 + i.
 struct Walk {
   int b, b0, act, q_len;
-  int hk, u;       // the unit is u of sequence b's key head hk
-  int64_t left;    // units that follow, this one among them
+  int hk, at;      // the share goes on at this step of sequence b's key head hk
+  int64_t left;    // steps that follow, this one among them
   Seq s;
   __device__ __forceinline__ void load_lengths(const Params& p, int lane) {
     const int i = min(b0 + lane, p.x.B - 1);
@@ -205,12 +212,19 @@ struct Walk {
     load_lengths(p, lane);
     s = make_seq(p, uniform(act), uniform(q_len));
     int64_t rest;
-    hk = static_cast<int>(divide(off, s.units, rest));
-    u = static_cast<int>(rest);
+    hk = static_cast<int>(divide(off, s.steps(), rest));
+    at = static_cast<int>(rest);
   }
-  // the head's first unit, behind the current head
+  // The share's units [u0, u1) of the head; none where it ends before the first.
+  __device__ __forceinline__ void take(int& u0, int& u1) {
+    const int end = static_cast<int>(min(static_cast<int64_t>(s.steps()), at + left));
+    left -= end - at;
+    u0 = max(0, at - kHeadCost);
+    u1 = max(0, end - kHeadCost);
+  }
+  // the head behind the current one
   __device__ __forceinline__ void next_head(const Params& p, int lane) {
-    u = 0;
+    at = 0;
     if (++hk < p.x.n_kv) return;
     hk = 0;
     if (++b >= p.x.B) return;  // the end of the stream
@@ -289,25 +303,47 @@ __device__ __noinline__ void mend_values(const Ctx& c, uint32_t vs, int chunks, 
   __syncwarp();
 }
 
-// The share of a pipeline; false: it has none.
+// The share of a pipeline.
 struct Share {
-  int g, b;
-  int64_t from, count, off;  // of the stream, of sequence b
+  int g, b;                  // b < 0: there is none
+  int64_t from, count, off;  // in steps, of the stream, of sequence b
 };
-__device__ __forceinline__ bool share_of(const Params& p, const Ctx& c, int pipe, const Split& split, Share& s) {
+// `b` and `at`: the sequence in which the share begins, and where that sequence does.
+__device__ __forceinline__ Share share_of(const Params& p, int pipe, const Split& split, int b, int64_t at) {
+  Share s;
   s.g = group_id(pipe);
-  if (pipe >= p.pipes || s.g >= split.groups) return false;
+  s.b = pipe < p.pipes && s.g < split.groups ? b : -1;
+  if (s.b < 0) return s;
   s.from = split.begin(s.g);
   s.count = split.begin(s.g + 1) - s.from;
-  const int64_t* at = reinterpret_cast<const int64_t*>(c.smem + kOffWalk) + 2 * pipe;
-  s.b = static_cast<int>(at[0]);
-  s.off = s.from - at[1];
-  return true;
+  s.off = s.from - at;
+  return s;
+}
+__device__ __forceinline__ Share share_of(const Params& p, const Ctx& c, int pipe, const Split& split) {
+  const int64_t* at = reinterpret_cast<const int64_t*>(c.smem + kOffWalk) + 2 * min(pipe, kWarps - 1);
+  return share_of(p, pipe, split, static_cast<int>(at[0]), at[1]);
+}
+// Of up to 32 sequences, one to a lane: every warp finds its pipeline's share, without the block.
+__device__ __forceinline__ Share find_share(const Params& p, int pipe, int lane, Split& split) {
+  int64_t len = 0;
+  if (lane < p.x.B) {
+    const Seq s = load_seq(p, lane);
+    len = static_cast<int64_t>(s.steps()) * p.x.n_kv;
+    if (s.cut_table && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(&g_paged_status, MLA_DEVICE_BAD_BLOCK);
+  }
+  int64_t upto = len;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  split = split_of(p, __shfl_sync(0xffffffffu, upto, 31));
+  const int64_t from = split.begin(group_id(pipe));
+  const int b = max(0, __ffs(__ballot_sync(0xffffffffu, from >= upto - len && from < upto)) - 1);
+  return share_of(p, pipe, split, b, __shfl_sync(0xffffffffu, upto - len, b));
 }
 
-__device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int pipe, int lane, const Split& split) {
-  Share sh;
-  if (!share_of(p, c, pipe, split, sh)) return;
+__device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int pipe, int lane, const Share& sh) {
   const int slot0 = pipe * p.slots;
   const uint32_t slots = c.sb + kOffSlots + slot0 * p.unit_bytes;
   volatile int* good_of = reinterpret_cast<volatile int*>(c.smem + kOffGood) + slot0;
@@ -317,12 +353,12 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int p
   uint32_t phase = 1;
   bool bad = false;
   while (w.left > 0) {
-    const int end = static_cast<int>(min(static_cast<int64_t>(w.s.units), w.u + w.left));
-    w.left -= end - w.u;
-    const int page0 = w.u / (kPage / kUnit);
-    for (int u = w.u; u < end; ++u) {
+    int u0, end;
+    w.take(u0, end);
+    const int page0 = u0 / (kPage / kUnit);
+    for (int u = u0; u < end; ++u) {
       const int page = u / (kPage / kUnit) - page0;
-      if (u == w.u || (page % 32 == 0 && u % (kPage / kUnit) == 0)) {  // the next 32 pages, one to a lane
+      if (u == u0 || (page % 32 == 0 && u % (kPage / kUnit) == 0)) {  // the next 32 pages, one to a lane
         const int i = page0 + page + lane;
         ids = i < p.x.W && i * kPage < w.s.len ? __ldg(p.x.block_table + static_cast<int64_t>(w.b) * p.x.W + i) : -1;
       }
@@ -352,10 +388,8 @@ __device__ void load_role(const Params& p, const Ctx& c, const Maps& maps, int p
 
 // kS: 16-column steps of keys, kV: 8-column tiles of values.
 template <typename E, int kS, int kV>
-__device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, const Split& split) {
+__device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, const Split& split, const Share& sh) {
   const int pipe = warp / p.tiles, tile = warp % p.tiles;
-  Share sh;
-  if (!share_of(p, c, pipe, split, sh)) return;
   const int quad = lane & 3, row0 = lane >> 2;  // the thread's rows: row0 and row0 + 8 of the tile
   const int rows = min(16, p.rows - tile * 16);
   const float scale = p.x.scale_log2;
@@ -372,7 +406,11 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
   uint32_t phase = 0;
   while (w.left > 0) {
     const Seq s = w.s;
-    const int b = w.b, hk = w.hk, u0 = w.u, u1 = static_cast<int>(min(static_cast<int64_t>(s.units), u0 + w.left));
+    const int b = w.b, hk = w.hk;
+    const int64_t begin = sh.from + (sh.count - w.left) - w.at;  // of the head in the stream
+    int u0, u1;
+    w.take(u0, u1);
+    if (u0 == u1) break;  // the share ends before the head's first unit
     int vis[2], tok[2];
     uint32_t q[kS][4];
 #pragma unroll
@@ -537,11 +575,9 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
       }
     }
     if (u1 < s.units && tile == 0 && lane == 0) {  // the share ends inside the head
-      const int64_t begin = sh.from + (sh.count - w.left) - u0;  // of the head in the stream
-      const int first = u0 > 0 ? split.group_of(begin) : sh.g;
-      p.records[sh.g] = make_int4(b, hk, split.group_of(begin + s.units - 1) - first, 1 + sh.g - first);
+      const int first = u0 > 0 ? split.group_of(begin + kHeadCost) : sh.g;
+      p.records[sh.g] = make_int4(b, hk, split.group_of(begin + s.steps() - 1) - first, 1 + sh.g - first);
     }
-    w.left -= u1 - u0;
     w.next_head(p, lane);
   }
 }
@@ -561,13 +597,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   fence_mbarrier_init_cluster();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
-  const Split split = find_shares(p, c);
+  const int pipe = warp < kWarps ? warp / p.tiles : warp - kWarps;
+  Split split;
+  Share sh;
+  if (p.x.B <= 32) {
+    sh = find_share(p, pipe, lane, split);
+  } else {
+    split = find_shares(p, c);
+    sh = share_of(p, c, pipe, split);
+  }
   if (warp < kWarps) {
     regs_increase<kConsumerRegs>();
-    consume_role<E, kS, kV>(p, c, warp, lane, split);
+    if (sh.b >= 0) consume_role<E, kS, kV>(p, c, warp, lane, split, sh);
   } else {
     regs_decrease<kLoadRegs>();
-    load_role(p, c, maps, warp - kWarps, lane, split);
+    if (sh.b >= 0) load_role(p, c, maps, pipe, lane, sh);
   }
   if (*c.abort) {
     if (lane == 0) atomicOr(&g_paged_status, MLA_DEVICE_TIMEOUT);
@@ -723,7 +767,7 @@ int part_floats(const Problem& p) { return (std::min(16, rows_of(p)) * (p.d_v + 
 // Groups that the longest stream of these dims feeds.
 int64_t most_groups(const Problem& p) {
   const int64_t heads = std::min<int64_t>(int64_t(1) << 20, static_cast<int64_t>(p.B) * p.n_kv);
-  return std::max<int64_t>(1, std::min<int64_t>(kMaxGroups / tiles_of(p), heads * (kPage / kUnit) * p.W / kMinUnits));
+  return std::max<int64_t>(1, std::min<int64_t>(kMaxGroups / tiles_of(p), heads * (kPage / kUnit) * p.W / kMinSteps));
 }
 size_t records_bytes(const Problem& p) { return (most_groups(p) * sizeof(int4) + 255) & ~size_t(255); }
 size_t workspace_of(const Problem& p) {
