@@ -77,8 +77,9 @@ typedef struct mla_head_norm {
  * mla_rope_apply, with these differences: inverse must be 0; rot_dim 0 rotates
  * nothing (params and positions may then be NULL); in place (out is x, same
  * strides) whole heads are read and written; rows of out must be distinct.
- * Heads of any size, stride and alignment of whole elements work; those whose
- * parts are multiples of 16 bytes run in 16-byte accesses.  One launch, two
+ * Heads of any size, stride and alignment of whole elements work; those of
+ * which head, strides and, in the half layout, the rotation's halves are
+ * multiples of 16 bytes run in 16-byte accesses.  One launch, two
  * where the tensors need accesses of different kinds.
  */
 mla_status mla_norm_rope(const mla_rope_dims* dims, const mla_rope_params* params, const int32_t* positions,

@@ -131,7 +131,8 @@ __device__ __forceinline__ void values(const void* p, int at, int fp32, int vec,
 }
 
 // A lane's units of a head.  kTwo: a rotated unit is two packs, V values and the
-// V that turn with them; otherwise one pack of V / 2 adjacent pairs.
+// V that turn with them, and comes before those that are copied; otherwise units
+// lie as the values do, V / 2 adjacent pairs of which any may turn.
 template <typename E, int V, bool kTwo, int KU>
 struct Lane {
   static constexpr int kVals = kTwo ? 2 * V : V;
@@ -139,15 +140,24 @@ struct Lane {
   int d[KU];   // first value
   int second;  // distance of a rotated unit's other pack
   bool in[KU], rot[KU];
+  uint32_t turns[KU];  // a bit for each of a unit's pairs
   __device__ __forceinline__ void place(const Tensor& w, int first_unit, int lane) {
     second = kTwo ? (w.half ? w.pairs : 1) : 0;
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       const int k = first_unit + lane + i * w.lanes;
       in[i] = k < w.units;
+      if constexpr (!kTwo) {
+        d[i] = k * V;
+        // pairs [first, end) of the unit
+        const int first = min(max((w.rot_off - d[i]) / 2, 0), kPairs), end = min(max((w.rot_off + 2 * w.pairs - d[i]) / 2, 0), kPairs);
+        turns[i] = w.rot_units > 0 ? (1u << end) - (1u << min(first, end)) : 0u;
+        rot[i] = turns[i] != 0;
+        continue;
+      }
       rot[i] = k < w.rot_units;
       if (rot[i]) {
-        d[i] = w.rot_off + (kTwo && w.half ? k * V : 2 * kPairs * k);
+        d[i] = w.rot_off + (w.half ? k * V : 2 * k);
       } else {
         const int c = (k - w.rot_units) * V;  // copied values, in order
         d[i] = c < w.rot_off ? c : c + 2 * w.pairs;
@@ -255,8 +265,9 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
       }
     }
     auto angle = [&](int i, int j) {
-      return at.rot[i] ? mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale)
-                       : make_float2(1.f, 0.f);
+      return (kTwo ? at.rot[i] : (at.turns[i] >> j & 1u) != 0)
+                 ? mlarp::cos_sin(pos, p.f.turn[(at.d[i] - w.rot_off) / (kTwo && w.half ? 1 : 2) + j], p.f.mscale)
+                 : make_float2(1.f, 0.f);
     };
 #pragma unroll
     for (int k = 0; k < kCoefs; ++k) {
@@ -341,8 +352,7 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
         const int i = k / L::kPairs, j = k % L::kPairs;
         const Two x = two(v[i][2 * j], v[i][2 * j + 1]), y = two(v[i][2 * j + 1], v[i][2 * j]);
         // what does not turn keeps apart from its neighbour
-        const Two turned = mul2(y, co[k].cross);
-        Two r = fma2(x, co[k].straight, at.rot[i] ? turned : two(0.f, 0.f));
+        Two r = (at.turns[i] >> j & 1u) != 0 ? fma2(y, co[k].cross, mul2(x, co[k].straight)) : mul2(x, co[k].straight);
         if constexpr (kLayer) r = fma2(r, inv2, ba[k]);
         else r = mul2(r, inv2);
         const float2 f = halves(r);
@@ -546,9 +556,10 @@ mla_status check_job(Job& j, int T, int dtype, bool half, bool paged) {
     j.to = {reinterpret_cast<uintptr_t>(j.out), {1, j.rows ? j.num_rows : T, j.n_heads}, {0, j.orow * size, j.oh * size}, bytes};
   if (!mlasp::distinct(j.to)) return fail(MLA_ERR_SHAPE, "%s: the output's strides make heads overlap", j.name);
   const bool heads = j.n_heads > 1, tokens = T > 1;  // strides that are taken
+  // interleaved pairs may begin and end anywhere, but not lie in two units
   const int64_t parts[] = {tokens ? j.xt : 0, heads ? j.xh : 0, tokens || j.rows ? j.orow : 0, j.rows ? j.ob : 0,
-                           heads ? j.oh : 0, j.head_dim, j.rot_off, half ? j.rot_dim / 2 : j.rot_dim};
-  j.vec = aligned(j.x, 16) && aligned(j.out, 16);
+                           heads ? j.oh : 0, j.head_dim, half ? j.rot_off : 0, half ? j.rot_dim / 2 : 0};
+  j.vec = aligned(j.x, 16) && aligned(j.out, 16) && (half || j.rot_dim == 0 || j.rot_off % 2 == 0);
   for (int64_t v : parts) j.vec = j.vec && v % V == 0;
   return MLA_OK;
 }
@@ -600,8 +611,13 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
   w->pairs = j.rot_dim / 2;
   w->half = half ? 1 : 0;
   const int width = !j.vec ? 1 : (dtype == MLA_ROPE_FP32 ? 4 : 8);
-  w->rot_units = j.vec && !half ? j.rot_dim / width : j.rot_dim / 2 / width;
-  w->units = w->rot_units + (j.head_dim - j.rot_dim) / width;
+  if (j.vec && !half) {
+    w->rot_units = j.rot_dim > 0 ? 1 : 0;  // there are some
+    w->units = j.head_dim / width;
+  } else {
+    w->rot_units = j.rot_dim / 2 / width;
+    w->units = w->rot_units + (j.head_dim - j.rot_dim) / width;
+  }
   w->per_lane = j.vec ? kUnits : w->units <= 32 * kFewUnits ? kFewUnits : kSingleUnits;
   w->lanes = 1;
   while (w->lanes < 32 && w->lanes < w->units) w->lanes *= 2;

@@ -79,7 +79,8 @@ def make_norm(kind, D, dtype, fp32, seed=0, eps=1e-6):
 
 SHAPES = [(1, 1, 64, 0, 64, 0), (1, 32, 128, 0, 128, 0), (33, 5, 192, 128, 64, 0), (7, 3, 107, 7, 36, 5), (100, 1, 2, 0, 2, 0),
           (5, 2, 300, 20, 256, 4), (9, 5, 128, 64, 16, 8), (300, 40, 96, 0, 96, 0), (3, 9, 1000, 8, 64, 0), (2, 3, 2500, 0, 128, 0),
-          (4, 2, 1111, 3, 30, 1), (1200, 20, 64, 0, 0, 0), (6, 400, 24, 8, 16, 0), (3, 2, 1, 0, 0, 0), (700, 16, 128, 0, 64, 0)]
+          (4, 2, 1111, 3, 30, 1), (1200, 20, 64, 0, 0, 0), (6, 400, 24, 8, 16, 0), (3, 2, 1, 0, 0, 0), (700, 16, 128, 0, 64, 0),
+          (40, 6, 96, 0, 30, 0), (900, 12, 64, 6, 20, 8), (5, 2, 128, 122, 6, 0), (3, 4, 48, 9, 14, 0), (21, 3, 600, 10, 202, 8)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
