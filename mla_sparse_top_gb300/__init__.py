@@ -1,7 +1,10 @@
 """GB300-native sparse MLA attention over a paged KV cache, the Lightning
 Indexer + top-k that selects its entries, the writer that puts new rows into
-that cache (bf16 or INT8), and the MLA Prolog that produces the absorbed query
-and the new cache rows from hidden states.
+that cache (bf16 or INT8), the MLA Prolog that produces the absorbed query
+and the new cache rows from hidden states, the page plan, rotary positions and
+the attention of drafted tokens, and the same steps for ordinary (grouped)
+heads: norms with rotation, the append of keys and values to pages, attention
+of prompts and of new tokens.
 
 The computation lives in ``libmla_sparse.so`` (CUDA for sm_103a, C ABI in
 ``include/mla_sparse.h``); this package builds it in-tree and exposes it

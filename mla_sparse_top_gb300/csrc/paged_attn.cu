@@ -12,11 +12,18 @@
 // through goes from its registers to memory.  More than 16 rows go to two or four
 // pipelines side by side, which read the same units, from L2 but for the first.
 //
-// The units of all sequences and heads are one stream of which every pipeline (or
-// group of them side by side) takes an equal share.  A head cut between them
-// leaves partial states in the workspace, and a second launch joins them.  Who
-// takes what follows from the lengths alone, so results do not depend on timing.
+// The units of all sequences and heads, and what a head costs beside them, are one
+// stream of which every pipeline (or group of them side by side) takes an equal
+// share.  A head cut between them leaves partial states in the workspace, and a
+// second launch joins them.  Who takes what follows from the lengths alone, so
+// results do not depend on timing.
 // Calls of more than 64 rows to a key head go through the 128-row tiles of prompts.
+//
+// Measured (graph replay): 64 sequences of 8192, 32 heads on 8 key heads of 128, 317 to 325 us
+// (6.6 to 6.8 TB/s, the copy rate); of 100 to 8192 87 us (5.6 TB/s); chains of up to five
+// tokens, 24 sequences of 500 to 20000, heads of 96, 61 us (4.8 TB/s); one token of one
+// sequence of 1000 9.5 to 10.9 us, of 100000 76.  Some 12 us of a call are launches, first loads
+// and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
