@@ -650,7 +650,7 @@ __device__ __forceinline__ int page_of(const Params& p, int b, int t) {
 }
 
 template <bool kPair>
-__device__ void plan_role(const Params& p, const Ctx& c) {
+__device__ void plan_role(const Params& p, const Ctx& c, const WarpPlan& w) {
   const int lane = threadIdx.x & 31, B = p.x.B;
   uint32_t count = 0;
   constexpr int kCtas = Shape<kPair>::kCtas;
@@ -666,7 +666,6 @@ __device__ void plan_role(const Params& p, const Ctx& c) {
     mine = load_seq(p, seq);
   };
   if (kept) {
-    const WarpPlan w = plan_warp(p);
     total = w.items;
     cap = w.cap;
     first = w.first;
@@ -1244,27 +1243,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   c.wait_ns = p.wait_ns;
   c.abort = reinterpret_cast<volatile uint32_t*>(c.smem + kOffAbort);
   constexpr int kCtas = Shape<kPair>::kCtas;
-  if (tid == 0) {
-    *c.abort = 0u;
-    *c.mended() = 0u;
-    for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(c.bar(kFull + i), kCtas);
-      mbar_init(c.bar(kEmpty + i), 1);
-      mbar_init(c.bar(kLocal + i), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(c.bar(kQFull + i), kCtas);
-      mbar_init(c.bar(kQFree + i), 1);
-      mbar_init(c.bar(kSFull + i), 1);
-      mbar_init(c.bar(kPReady + i), 4 * kCtas);
-      mbar_init(c.bar(kOFull + i), 1);
-    }
-    for (int i = 0; i < kItemSlots; ++i) {
-      mbar_init(c.bar(kItemFull + i), 1);
-      mbar_init(c.bar(kItemEmpty + i), kPair ? 2 * kItemReaders - 1 : kItemReaders);  // one MMA warp
-    }
-    mbar_init(c.bar(kDraw), 1);
-    mbar_init(c.bar(kFinal), 1);
+  if (tid < kNumBars) {  // arrivals of each phase
+    const int i = tid;
+    const int count = i < kEmpty ? kCtas                                     // kFull
+                      : i >= kQFull && i < kQFree ? kCtas
+                      : i >= kPReady && i < kOFull ? 4 * kCtas
+                      : i >= kItemEmpty && i < kDraw ? (kPair ? 2 * kItemReaders - 1 : kItemReaders)  // a pair has one MMA warp
+                                                     : 1;
+    mbar_init(c.bar(i), count);
+    if (tid == 0) *c.abort = *c.mended() = 0u;
     fence_mbarrier_init_cluster();
   }
   if (warp == kLoadWarp && lane < 3) {
@@ -1280,6 +1267,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
       tmem_relinquish();
     }
   }
+  // while tensor memory is allocated; nothing begins before the first item
+  WarpPlan plan = {};
+  if (warp == kPlanWarp && c.rank == 0 && p.x.B <= kWarpSeqs) plan = plan_warp(p);
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) {  // the other CTA's barriers are in place
@@ -1300,7 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     } else if (warp == kLoadWarp) {
       load_role<kPair>(p, c, maps);
     } else if (warp == kPlanWarp) {
-      if (c.rank == 0) plan_role<kPair>(p, c);
+      if (c.rank == 0) plan_role<kPair>(p, c, plan);
     } else if (warp == kMendWarp) {
       mend_role<E, kPair>(p, c);
     }
