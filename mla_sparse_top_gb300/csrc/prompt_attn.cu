@@ -96,12 +96,22 @@ struct Item {
   int t0, ta, tb;  // key tiles [t0, ta) of a CTA's row tile 0, [t0, tb) of row tile 1
   int lo;          // keys from here on are not seen by every row
   int part;        // slot of a partial state, -1: the item is whole
-  int pad[2];
   __device__ __forceinline__ int t1(int h) const { return h ? tb : ta; }
+  // as four 16-byte words, field by field: through pointers it would live in local memory
+  __device__ __forceinline__ void unpack(int4 w0, int4 w1, int4 w2, int4 w3) {
+    live = w0.x; b = w0.y; hk = w0.z; m = w0.w;
+    n = w1.x; len = w1.y; pos = w1.z; q0 = w1.w;
+    key0 = w2.x; t0 = w2.y; ta = w2.z; tb = w2.w;
+    lo = w3.x; part = w3.y;
+  }
+  __device__ __forceinline__ int4 word(int i) const {
+    return i == 0 ? make_int4(live, b, hk, m) : i == 1 ? make_int4(n, len, pos, q0) : i == 2 ? make_int4(key0, t0, ta, tb) : make_int4(lo, part, 0, 0);
+  }
 };
+constexpr int kItemBytes = 64;
 
 constexpr int kOffItems = kTileSmem;
-constexpr int kOffBars = kOffItems + kItemSlots * static_cast<int>(sizeof(Item));
+constexpr int kOffBars = kOffItems + kItemSlots * kItemBytes;
 constexpr int kOffTmem = kOffBars + 8 * kNumBars;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kOffMended = kOffAbort + 4;
@@ -630,10 +640,8 @@ struct Items {
   __device__ __forceinline__ bool next(const Ctx& c, Item& it) {
     const int s = count % kItemSlots;
     if (!__all_sync(0xffffffffu, mbar_wait<kPair>(c.bar(kItemFull + s), (count / kItemSlots) & 1, c.abort, c.wait_ns))) return false;
-    const int4* src = reinterpret_cast<const int4*>(c.smem + kOffItems) + s * (sizeof(Item) / 16);
-    int4* dst = reinterpret_cast<int4*>(&it);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(Item) / 16); ++i) dst[i] = src[i];
+    const int4* src = reinterpret_cast<const int4*>(c.smem + kOffItems) + 4 * s;
+    it.unpack(src[0], src[1], src[2], src[3]);
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
       if constexpr (kPair) arrive_cluster(lead<true>(c.bar(kItemEmpty + s)));
@@ -657,7 +665,7 @@ __device__ void plan_role(const Params& p, const Ctx& c, const WarpPlan& w) {
   int i = blockIdx.x / kCtas, drawn = 0;
   // a lane keeps a sequence, where there are no more than 32: no item waits for its description then
   const bool kept = B <= kWarpSeqs;
-  int total, cap, first, part0, seq;
+  int total, states, cap, first, part0, seq;
   Seq mine;
   auto load = [&](int at) {
     seq = __ldcg(p.order + at);
@@ -667,6 +675,7 @@ __device__ void plan_role(const Params& p, const Ctx& c, const WarpPlan& w) {
   };
   if (kept) {
     total = w.items;
+    states = w.states;
     cap = w.cap;
     first = w.first;
     part0 = w.part0;
@@ -675,10 +684,11 @@ __device__ void plan_role(const Params& p, const Ctx& c, const WarpPlan& w) {
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan
     total = __ldcg(&p.head->items);
+    states = __ldcg(&p.head->states);
     cap = __ldcg(&p.head->cap);
   }
   while (true) {
-    Item it;
+    Item it = {};
     it.live = i < total ? 1 : 0;
     if (it.live) {
       int from = 0;  // the lane that has the sequence
@@ -694,19 +704,31 @@ __device__ void plan_role(const Params& p, const Ctx& c, const WarpPlan& w) {
       s.pairs = of(mine.pairs);
       s.bad_len = s.bad_table = false;
       const int b = of(seq), Hkv = p.x.n_kv;
-      const Cuts how = cuts_of(p, s, cap);
       int k = i - of(first), m, hk, cut = 0, cuts = 1;
-      if (how.at_least(2) > 0) {
-        how.find(k / Hkv, m, cut, cuts);
-        hk = k % Hkv;
-      } else {
+      bool whole = states == 0;
+      if (!whole) {
+        const Cuts how = cuts_of(p, s, cap);
+        whole = how.at_least(2) == 0;
+        if (!whole) {
+          how.find(k / Hkv, m, cut, cuts);
+          hk = k % Hkv;
+        }
+      }
+      if (whole) {
         // heads whose keys and values fill about a third of L2 go side by side
         const int64_t bytes = static_cast<int64_t>(max(1, s.len)) * (p.x.d_qk + p.x.d_v) * 2;
-        const int group = bytes > (40 << 20) ? 1 : min(Hkv, (40 << 20) / static_cast<int>(bytes));
-        const int per_group = s.pairs * group;  // no more than there are items
-        const int g = k / per_group, heads = min(group, Hkv - g * group), r = k - g * per_group;
-        m = s.pairs - 1 - r / heads;
-        hk = g * group + r % heads;
+        int g = 0, heads = Hkv, r = k;
+        if (bytes * Hkv > (40 << 20)) {
+          const int group = bytes > (40 << 20) ? 1 : min(Hkv, (40 << 20) / static_cast<int>(bytes));
+          const int per_group = s.pairs * group;  // no more than there are items
+          g = k / per_group;
+          r = k - g * per_group;
+          g *= group;
+          heads = min(group, Hkv - g);
+        }
+        const int row = r / heads;
+        m = s.pairs - 1 - row;
+        hk = g + r - row * heads;
       }
       it.b = b;
       it.hk = hk;
@@ -733,14 +755,17 @@ __device__ void plan_role(const Params& p, const Ctx& c, const WarpPlan& w) {
     const int s = count % kItemSlots;
     if (!__all_sync(0xffffffffu, mbar_wait<kPair>(c.bar(kItemEmpty + s), ((count / kItemSlots) & 1) ^ 1, c.abort, c.wait_ns))) return;
     if (lane == 0) {
-      reinterpret_cast<Item*>(c.smem + kOffItems)[s] = it;
+      int4* to = reinterpret_cast<int4*>(c.smem + kOffItems) + 4 * s;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) to[k] = it.word(k);
       mbar_arrive(c.bar(kItemFull + s));
       if constexpr (kPair) {
-        const uint32_t at = mapa_shared(c.sb + kOffItems + s * static_cast<uint32_t>(sizeof(Item)), 1);
-        const int* word = reinterpret_cast<const int*>(&it);
+        const uint32_t at = mapa_shared(c.sb + kOffItems + s * kItemBytes, 1);
 #pragma unroll
-        for (int k = 0; k < static_cast<int>(sizeof(Item) / 4); ++k)
-          asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(at + 4 * k), "r"(word[k]) : "memory");
+        for (int k = 0; k < 4; ++k) {
+          const int4 w = it.word(k);
+          asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(at + 16 * k), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+        }
         arrive_cluster(mapa_shared(c.bar(kItemFull + s), 1));
       }
     }
@@ -1027,16 +1052,16 @@ __device__ __forceinline__ void mma_role(const Params& p, const Ctx& c) {
 // hi) of the sequence, put into what the calling thread has stored, its row of out
 // or of a partial state.  Rare: such values lay where not every row sees them.
 template <typename E>
-__device__ __noinline__ void infinite_columns(const Params& p, const Item& it, int lo, int hi, E* out, float* part) {
+__device__ __noinline__ void infinite_columns(const Params& p, int b, int hk, int key0, int lo, int hi, E* out, float* part) {
   constexpr uint32_t kExp = __is_same(E, __half) ? 0x7C00u : 0x7F80u;
   for (int key = lo; key < hi; ++key) {
-    int64_t at = it.hk * p.x.v.head_stride;
+    int64_t at = hk * p.x.v.head_stride;
     if (p.x.num_blocks > 0) {
-      const int page = page_of(p, it.b, key / kPage);
+      const int page = page_of(p, b, key / kPage);
       if (page < 0) continue;
       at += page * p.x.v.block_stride + (key % kPage) * p.x.v.row_stride;
     } else {
-      at += static_cast<int64_t>(it.key0 + key) * p.x.v.row_stride;
+      at += static_cast<int64_t>(key0 + key) * p.x.v.row_stride;
     }
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x.v.data) + at);
     for (int u = 0; u < p.x.d_v / 8; ++u) {
@@ -1138,6 +1163,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
         sum[k & 1] = add2(sum[k & 1], pair(e.x, e.y));
         // one 16-bit weight: half a step of it, as one rounding of the output costs
         w[k] = pack16<E>(e.x, e.y);
+        if (k == 31) tmem_st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(w));
       }
       const float2 sums = unpair(add2(sum[0], sum[1]));
       l += sums.x + sums.y;
@@ -1153,7 +1179,6 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
           tmem_st_32x32b_x32(tO + k, o);
         }
       }
-      tmem_st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(w));
       tmem_st_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
       tmem_wait_st();
       tc_fence_before();
@@ -1204,7 +1229,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
         }
       }
       __syncwarp();  // infinite columns go over what other lanes have written
-      if (*c.mended() && live && !nothing) infinite_columns<E>(p, it, it.lo, vis, out, nullptr);
+      if (*c.mended() && live && !nothing) infinite_columns<E>(p, it.b, it.hk, it.key0, it.lo, vis, out, nullptr);
       if (put && p.x.lse != nullptr) p.x.lse[at] = nothing ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     } else {
       float* dst = p.parts + static_cast<int64_t>(it.part) * p.part_floats + tile * (p.part_floats / Shape<kPair>::kTiles);
@@ -1220,7 +1245,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
               reinterpret_cast<uint4*>(dst)[((k >> 2) + u) * 128 + row] = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
         }
         if (*c.mended() && live)
-          infinite_columns<E>(p, it, max(it.lo, kTile * it.t0), min(vis, kTile * it.t1(h)), nullptr, dst + row * 4);
+          infinite_columns<E>(p, it.b, it.hk, it.key0, max(it.lo, kTile * it.t0), min(vis, kTile * it.t1(h)), nullptr, dst + row * 4);
       }
       // -inf says that the part is not the row's; the lowest maximum joins with weight 0 and
       // brings along the NaN of infinite values whose scores are all -inf
@@ -1302,7 +1327,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
   __syncthreads();
   if (*c.abort) {
     // a wait ran out: loads may still be in flight to shared memory; they take microseconds
-    if (tid == 0) atomicOr(&g_prompt_status, MLA_DEVICE_TIMEOUT);
+    if (tid == 0) {
+      atomicOr(&g_prompt_status, MLA_DEVICE_TIMEOUT);
+      p.head->states = 0;  // not every part was written, nor described: nothing is joined
+    }
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 200000) {
     }

@@ -307,7 +307,8 @@ def test_many_rows_with_values_that_are_not_finite():
     assert torch.equal(hit[..., rest], clean[0][900:1400, 56:][..., rest])
 
 
-@pytest.mark.parametrize("case", [dict(lens=[1400, 300], H=112, Hkv=2, D=128, Dv=128), dict(lens=[900], H=4, Hkv=2)])
+@pytest.mark.parametrize("case", [dict(lens=[1400, 300], H=112, Hkv=2, D=128, Dv=128), dict(lens=[900], H=4, Hkv=2),
+                                  dict(lens=[100, 40], ctx=[30000, 9000], H=16, Hkv=2, D=128, Dv=128, paged=True)])
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_runs(case):
     """A bound far below what a whole call waits: a launch that gives up reports it, and the next one does the whole job.
 
