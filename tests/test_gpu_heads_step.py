@@ -186,3 +186,47 @@ def test_chunks_write_the_keys_of_the_whole_prompt():
         cut.check(c, 0)
     k1, k2 = gather(whole.k, whole.table.cpu(), 0, 500), gather(cut.k, cut.table.cpu(), 0, 500)
     assert torch.equal(k1, k2)
+
+
+def test_two_graphs_share_a_workspace():
+    """Prompts that are cut, prompts that are not and new tokens, captured with one workspace, replayed in any order."""
+    import test_gpu_heads_paged as paged
+    import test_gpu_heads_prompt as prompt
+    import mla_sparse_top_gb300 as mla
+    calls = [(prompt, prompt.make([60, 9], ctx=[20000, 300], paged=True, H=8, Hkv=2, D=128, Dv=128)),
+             (prompt, prompt.make([500, 1, 700], H=8, Hkv=2, D=128, Dv=128)),
+             (paged, paged.make([5000, 0, 300], H=8, Hkv=2, S1=2)), (paged, paged.make([700] * 40, H=4, Hkv=2, D=64, Dv=64))]
+    want = [mod.run(m) for mod, m in calls]
+    ws = torch.full((1 << 27,), 255, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for mod, m in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = mod.run(m, workspace=ws)
+        graphs.append((g, out))
+    for i in (0, 2, 1, 3, 3, 0, 1, 2, 0):
+        g, (out, lse) = graphs[i]
+        out.fill_(7.0), lse.fill_(7.0)
+        g.replay()
+        a, b = want[i]
+        live = ~torch.isnan(b) if calls[i][0] is paged else b != 7  # rows behind the last sequence stay
+        assert torch.equal(lse[live], b[live]) and torch.equal(out[live], a[live])
+    assert mla.heads_device_status(clear=True) == 0
+
+
+def test_calls_on_two_streams():
+    """The same kinds of calls side by side, a workspace each: results to the bit."""
+    import test_gpu_heads_prompt as prompt
+    import mla_sparse_top_gb300 as mla
+    ms = [prompt.make([300, 90], ctx=[9000, 0], paged=True, H=8, Hkv=2, D=128, Dv=128), prompt.make([900, 1100], H=16, Hkv=4, D=64, Dv=64)]
+    want = [prompt.run(m) for m in ms]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in ms], []
+    for _ in range(4):
+        for m, s in zip(ms, streams):
+            with torch.cuda.stream(s):
+                got.append(prompt.run(m))
+    torch.cuda.synchronize()
+    assert mla.heads_device_status(clear=True) == 0
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
