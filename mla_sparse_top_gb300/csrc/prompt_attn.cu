@@ -8,7 +8,8 @@
 //   P_i                over S_i in tensor memory, two 16-bit weights to a column
 //   O_i += P_i V       128 x d_v in tensor memory, P from there, V from shared memory
 // in the order P_0 V(t), Q_0 K(t+1), P_1 V(t), Q_1 K(t+1), so that a softmax has
-// the length of two products.  The 512 columns of tensor memory hold two of each.
+// the length of two products.  The 512 columns of tensor memory hold two of each;
+// where d_v is at most 64, P has columns of its own, and Q K(t+1) comes before P V(t).
 // A score product of one CTA reads both operands from shared memory, which takes
 // 96 clocks of an MMA's 64; where there are rows enough, pairs of CTAs hold half of
 // the keys and of the values' columns each and issue MMAs of 256 rows (in_pairs).
@@ -85,7 +86,9 @@ constexpr int kOFull = kPReady + 2;          // [2] the item's MMAs are complete
 constexpr int kItemFull = kOFull + 2;        // [kItemSlots]
 constexpr int kItemEmpty = kItemFull + kItemSlots;
 constexpr int kDraw = kItemEmpty + kItemSlots;  // the item's loads are nearly all issued
-constexpr int kFinal = kDraw + 1;
+constexpr int kSFree = kDraw + 1;             // [2] apart: scores are in registers
+constexpr int kPFree = kSFree + 2;             // [2] apart: the MMAs that read the weights, and wrote O, are complete
+constexpr int kFinal = kPFree + 2;
 constexpr int kNumBars = kFinal + 1;
 
 struct Item {
@@ -118,7 +121,15 @@ constexpr int kOffMended = kOffAbort + 4;
 constexpr int kSmemBytes = kOffMended + 4 + 1024;  // 1024: the base is aligned by hand
 static_assert(kSmemBytes <= 232448 && kOffBars % 8 == 0, "shared memory");
 
-constexpr uint32_t kTmemS = 0, kTmemO = 256;  // two of 128 columns each
+// Columns of tensor memory: two S of 128, two O, and where values have up to 64 columns, P
+// apart from S, so that the next S of a row tile is made while the softmax of this one runs
+// (16 heads of 64, 300 tokens 14.1 -> 13.4 us; 32 heads, four prompts of 4096 333 -> 326).
+constexpr uint32_t kTmemS = 0;
+template <bool kApart>
+struct Tmem {
+  static constexpr uint32_t kO = kApart ? 384 : 256, kOStep = kApart ? 64 : 128;
+  static constexpr uint32_t kP = kApart ? 256 : kTmemS, kPStep = kApart ? 64 : 128;
+};
 
 // What the plan leaves for the other kernels, followed by three int32 arrays over the sequences.
 struct Head {
@@ -939,7 +950,7 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
   Item it;
   int slot = 0;  // the next that no MMA has used
   uint32_t phase = 0;
-  uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0};
+  uint32_t q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, s_uses[2] = {0, 0};
   auto after = [&](int s, int n) { return s + n >= kSlots ? s + n - kSlots : s + n; };
   auto take = [&](int n) {  // waits for the next n slots
 #pragma unroll
@@ -972,9 +983,11 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
     __syncwarp();
   };
   // O_h += P_h V
+  constexpr bool kApart = kVc == 1;
+  using Cols = Tmem<kApart>;
   auto values = [&](int h, int at, bool first, bool free_values, bool last) {
     if (elect_one()) {
-      const uint32_t d = c.tmem + kTmemO + 128 * h, a = c.tmem + kTmemS + 128 * h;
+      const uint32_t d = c.tmem + Cols::kO + Cols::kOStep * h, a = c.tmem + Cols::kP + Cols::kPStep * h;
 #pragma unroll
       for (int k = 0; k < kVc; ++k) {
         const uint64_t b = desc_v + static_cast<uint32_t>(after(at, k)) * kSlot;
@@ -986,6 +999,7 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
 #pragma unroll
         for (int k = 0; k < kVc; ++k) commit<kPair>(c.bar(kEmpty) + 8 * after(at, k));
       }
+      if (kApart) commit<kPair>(c.bar(kPFree + h));
       if (last) commit<kPair>(c.bar(kOFull + h));
     }
     __syncwarp();
@@ -1009,6 +1023,17 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
       ok = take(kVc);
       key = slot;
       if (ok && t + 1 < end) ok = take(kKc);
+      if constexpr (kApart) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t1 = h == 0 ? ta : tb;
+          if (!ok || t + 1 >= t1) continue;
+          ok = warp_wait(c, kSFree + h, s_uses[h]++ & 1);
+          if (!ok) continue;
+          tc_fence_after();
+          scores(h, key, h == (t + 1 < tb ? 1 : 0), t + 2 == t1);
+        }
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int t1 = h == 0 ? ta : tb;
@@ -1018,7 +1043,7 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
         tc_fence_after();
         // the last row tile that reads a key or value tile gives its slots up
         values(h, value, t == t0, h == (t < tb ? 1 : 0), t + 1 == t1);
-        if (t + 1 < t1) scores(h, key, h == (t + 1 < tb ? 1 : 0), t + 2 == t1);
+        if (!kApart && t + 1 < t1) scores(h, key, h == (t + 1 < tb ? 1 : 0), t + 2 == t1);
       }
     }
   }
@@ -1030,22 +1055,12 @@ __device__ void mma_role(const Params& p, const Ctx& c) {
   __syncwarp();
 }
 
-template <bool kPair>
+template <bool kPair, bool kApart>
 __device__ __forceinline__ void mma_role(const Params& p, const Ctx& c) {
-  if constexpr (kPair) {  // values of more than 64 columns
-    if (p.kc == 1) return mma_role<true, 1, 2>(p, c);
-    if (p.kc == 2) return mma_role<true, 2, 2>(p, c);
-    return mma_role<true, 3, 2>(p, c);
-  } else {
-    switch (2 * p.kc + p.vc) {
-      case 3: return mma_role<false, 1, 1>(p, c);
-      case 4: return mma_role<false, 1, 2>(p, c);
-      case 5: return mma_role<false, 2, 1>(p, c);
-      case 6: return mma_role<false, 2, 2>(p, c);
-      case 7: return mma_role<false, 3, 1>(p, c);
-      default: return mma_role<false, 3, 2>(p, c);
-    }
-  }
+  constexpr int kVc = kApart ? 1 : 2;
+  if (p.kc == 1) return mma_role<kPair, 1, kVc>(p, c);
+  if (p.kc == 2) return mma_role<kPair, 2, kVc>(p, c);
+  return mma_role<kPair, 3, kVc>(p, c);
 }
 
 // The NaN of values that are not finite, which mending took from a row: keys [lo,
@@ -1094,11 +1109,13 @@ __device__ __forceinline__ void turn_units(uint32_t (&y)[32], int lane) {
   }
 }
 
-template <typename E, bool kPair>
+template <typename E, bool kPair, bool kApart>
 __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) {
   const int h = warp >> 2, row = (warp & 3) * 32 + lane;  // row tile, row of it
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const uint32_t tS = c.tmem + lanes + kTmemS + 128 * h, tO = c.tmem + lanes + kTmemO + 128 * h;
+  using Cols = Tmem<kApart>;
+  const uint32_t tS = c.tmem + lanes + kTmemS + 128 * h, tO = c.tmem + lanes + Cols::kO + Cols::kOStep * h;
+  const uint32_t tP = c.tmem + lanes + Cols::kP + Cols::kPStep * h;
   // a positive scale leaves the order of scores alone: the maximum is taken of
   // the raw ones, and the scale goes into the exponent's multiply-add
   const float scale = p.x.scale_log2;
@@ -1106,7 +1123,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
   const float mul = raw ? scale : 1.f;
   const int tok_in = row / p.G, head_in = row - tok_in * p.G;
   const bool paged = p.x.num_blocks > 0;
-  uint32_t uses = 0, outs = 0;
+  uint32_t uses = 0, outs = 0, products = 0;
   bool bad = false;
   Items<kPair> items;
   Item it;
@@ -1127,6 +1144,11 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
 #pragma unroll
       for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tS + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(z + 32 * k));
       tmem_wait_ld();
+      if (kApart && t + 1 < it.t1(h)) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar(kSFree + h));
+      }
       if (!raw) {
 #pragma unroll
         for (int k = 0; k < 128; ++k) z[k] *= scale;
@@ -1163,11 +1185,17 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
         sum[k & 1] = add2(sum[k & 1], pair(e.x, e.y));
         // one 16-bit weight: half a step of it, as one rounding of the output costs
         w[k] = pack16<E>(e.x, e.y);
-        if (k == 31) tmem_st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(w));
+        if (k == 31) {
+          if (kApart && t > it.t0) {  // the product before this one is through with the weights, and with O
+            if (!warp_wait(c, kPFree + h, products++ & 1)) return;
+            tc_fence_after();
+          }
+          tmem_st_32x32b_x32(tP, *reinterpret_cast<uint32_t(*)[32]>(w));
+        }
       }
       const float2 sums = unpair(add2(sum[0], sum[1]));
       l += sums.x + sums.y;
-      // the MMAs before these scores are complete, the one before on O among them
+      // the MMAs before these scores are complete, the one before on O among them (apart: see above)
       if (t > it.t0 && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
         for (int k = 0; k < p.x.d_v; k += 32) {
@@ -1179,7 +1207,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
           tmem_st_32x32b_x32(tO + k, o);
         }
       }
-      tmem_st_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
+      tmem_st_32x32b_x32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -1189,6 +1217,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
     if (any) {
       if (!warp_wait(c, kOFull + h, outs++ & 1)) return;
       tc_fence_after();
+      ++products;  // the last one's, whose barrier nobody waits for
     }
     if (!any || !live) {
       l = 0.f;
@@ -1257,7 +1286,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
   if (bad) atomicOr(&g_prompt_status, MLA_DEVICE_BAD_BLOCK);
 }
 
-template <typename E, bool kPair>
+template <typename E, bool kPair, bool kApart>
 __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   extern __shared__ uint8_t raw[];
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -1273,6 +1302,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     const int count = i < kEmpty ? kCtas                                     // kFull
                       : i >= kQFull && i < kQFree ? kCtas
                       : i >= kPReady && i < kOFull ? 4 * kCtas
+                      : i >= kSFree && i < kPFree ? 4
                       : i >= kItemEmpty && i < kDraw ? (kPair ? 2 * kItemReaders - 1 : kItemReaders)  // a pair has one MMA warp
                                                      : 1;
     mbar_init(c.bar(i), count);
@@ -1307,11 +1337,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
 
   if (warp < kSoftmaxWarps) {
     regs_increase<kSoftmaxRegs>();
-    softmax_role<E, kPair>(p, c, warp, lane);
+    softmax_role<E, kPair, kApart>(p, c, warp, lane);
   } else {
     regs_decrease<kOtherRegs>();
     if (warp == kMmaWarp) {
-      mma_role<kPair>(p, c);
+      mma_role<kPair, kApart>(p, c);
     } else if (warp == kLoadWarp) {
       load_role<kPair>(p, c, maps);
     } else if (warp == kPlanWarp) {
@@ -1469,23 +1499,31 @@ cudaLaunchConfig_t config_of(unsigned ctas, bool pair, cudaStream_t s, cudaLaunc
   return cfg;
 }
 
-template <typename E, bool kPair>
+template <typename E, bool kPair, bool kApart>
 mla_status prepare_kernel(Device& d) {
-  HEADS_CUDA(cudaFuncSetAttribute(prompt_attn_kernel<E, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes), "kernel set-up");
+  HEADS_CUDA(cudaFuncSetAttribute(prompt_attn_kernel<E, kPair, kApart>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes), "kernel set-up");
   cudaFuncAttributes fa;
-  HEADS_CUDA(cudaFuncGetAttributes(&fa, prompt_attn_kernel<E, kPair>), "kernel attributes");
+  HEADS_CUDA(cudaFuncGetAttributes(&fa, prompt_attn_kernel<E, kPair, kApart>), "kernel attributes");
   if constexpr (kPair) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = config_of(2, true, nullptr, attr);
     attr[0] = attr[1];
     cfg.numAttrs = 1;
     int n = 0;
-    HEADS_CUDA(cudaOccupancyMaxActiveClusters(&n, prompt_attn_kernel<E, kPair>, &cfg), "kernel occupancy");
+    HEADS_CUDA(cudaOccupancyMaxActiveClusters(&n, prompt_attn_kernel<E, kPair, kApart>, &cfg), "kernel occupancy");
     if (n < 1) return fail(MLA_ERR_CUDA, "the kernel does not fit this device");
     d.pairs = n;
   }
   if (fa.numRegs < kRegs) return fail(MLA_ERR_CUDA, "the kernel was built with %d registers", fa.numRegs);  // what the warpgroups divide
   return MLA_OK;
+}
+
+template <typename E>
+mla_status prepare_kernels(Device& d) {
+  mla_status st = prepare_kernel<E, false, false>(d);
+  if (st == MLA_OK) st = prepare_kernel<E, false, true>(d);
+  if (st == MLA_OK) st = prepare_kernel<E, true, false>(d);
+  return st;
 }
 
 // Kernel attributes and the tensor-map encoder; the first call on a device.
@@ -1499,10 +1537,8 @@ mla_status init_device(int* sms, int* pairs) {
     mla_status st = tensor_map_encoder(&g_encode);
     if (st != MLA_OK) return st;
     HEADS_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev), "device attributes");
-    st = prepare_kernel<__nv_bfloat16, false>(d);
-    if (st == MLA_OK) st = prepare_kernel<__half, false>(d);
-    if (st == MLA_OK) st = prepare_kernel<__nv_bfloat16, true>(d);
-    if (st == MLA_OK) st = prepare_kernel<__half, true>(d);
+    st = prepare_kernels<__nv_bfloat16>(d);
+    if (st == MLA_OK) st = prepare_kernels<__half>(d);
     if (st != MLA_OK) return st;
     d.ready = true;
   }
@@ -1511,11 +1547,14 @@ mla_status init_device(int* sms, int* pairs) {
   return MLA_OK;
 }
 
-template <typename E, bool kPair>
-mla_status launch_attention(unsigned ctas, const Maps& maps, const Params& p, cudaStream_t s) {
+template <typename E>
+mla_status launch_attention(bool pair, unsigned workers, const Maps& maps, const Params& p, cudaStream_t s) {
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config_of(ctas, kPair, s, attr);
-  HEADS_CUDA(cudaLaunchKernelEx(&cfg, prompt_attn_kernel<E, kPair>, maps, p), "kernel launch");
+  const cudaLaunchConfig_t cfg = config_of(pair ? 2 * workers : workers, pair, s, attr);
+  HEADS_CUDA(pair ? cudaLaunchKernelEx(&cfg, prompt_attn_kernel<E, true, false>, maps, p)
+             : p.vc == 1 ? cudaLaunchKernelEx(&cfg, prompt_attn_kernel<E, false, true>, maps, p)
+                         : cudaLaunchKernelEx(&cfg, prompt_attn_kernel<E, false, false>, maps, p),
+             "kernel launch");
   return MLA_OK;
 }
 
@@ -1577,8 +1616,7 @@ mla_status launch_tiles(const Problem& x, cudaStream_t s) {
   const int64_t groups = x.S1 > 0 ? static_cast<int64_t>(x.B) * ((x.S1 + p.span - 1) / p.span) : x.T / p.span + x.B;
   const int64_t most = std::min<int64_t>(p.sms, groups) * x.n_kv + p.max_parts;
   const unsigned workers = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(p.sms, most)));
-  const mla_status ls = bf ? (pair ? launch_attention<__nv_bfloat16, true>(2 * workers, maps, p, s) : launch_attention<__nv_bfloat16, false>(workers, maps, p, s))
-                           : (pair ? launch_attention<__half, true>(2 * workers, maps, p, s) : launch_attention<__half, false>(workers, maps, p, s));
+  const mla_status ls = bf ? launch_attention<__nv_bfloat16>(pair, workers, maps, p, s) : launch_attention<__half>(pair, workers, maps, p, s);
   if (ls != MLA_OK) return ls;
   if (p.max_parts > 0)
     HEADS_CUDA(bf ? launch_after(prompt_merge_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(4 * sms)), kMergeThreads, 0, s, p)
