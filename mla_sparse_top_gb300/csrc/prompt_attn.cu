@@ -1140,63 +1140,32 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
       const int here = page ? vis - kTile * t : 0;
       if (!warp_wait(c, kSFull + h, uses++ & 1)) return;
       tc_fence_after();
-      float z[128];
+      auto load = [&](float (&z)[128]) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tS + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(z + 32 * k));
-      tmem_wait_ld();
-      if (kApart && t + 1 < it.t1(h)) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c.bar(kSFree + h));
-      }
-      if (!raw) {
+        for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(tS + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(z + 32 * k));
+        tmem_wait_ld();
+      };
+      auto mask = [&](float (&z)[128]) {
+        if (!raw) {
 #pragma unroll
-        for (int k = 0; k < 128; ++k) z[k] *= scale;
-      }
-      if (__any_sync(0xffffffffu, here < kTile)) {
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k >= here) z[k] = -INFINITY;
-      }
-      float mx[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-      for (int k = 4; k < 128; k += 8) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], z[k + j]), k + 4 + j < 128 ? z[k + 4 + j] : -INFINITY);
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
-      // the maximum moves only when a tile exceeds it by more than 2^8: weights stay
-      // below 2^8 and O is rarely rescaled
-      const bool grow = top > m + 8.f;
-      const float f = grow ? fast_exp2(m - top) : 1.f;
-      if (grow) {
-        l *= f;
-        m = top;
-      }
-      const float mm = m == -INFINITY ? 0.f : m;
-      uint64_t sum[2] = {0, 0};
-      const uint64_t mul_2 = pair(mul, mul), mm_2 = pair(-mm, -mm);
-      uint32_t w[64];
-#pragma unroll
-      for (int k = 0; k < 64; ++k) {
-        float2 e = unpair(fma2(pair(z[2 * k], z[2 * k + 1]), mul_2, mm_2));
-        e.x = fast_exp2(e.x);
-        e.y = fast_exp2(e.y);
-        sum[k & 1] = add2(sum[k & 1], pair(e.x, e.y));
-        // one 16-bit weight: half a step of it, as one rounding of the output costs
-        w[k] = pack16<E>(e.x, e.y);
-        if (k == 31) {
-          if (kApart && t > it.t0) {  // the product before this one is through with the weights, and with O
-            if (!warp_wait(c, kPFree + h, products++ & 1)) return;
-            tc_fence_after();
-          }
-          tmem_st_32x32b_x32(tP, *reinterpret_cast<uint32_t(*)[32]>(w));
+          for (int k = 0; k < 128; ++k) z[k] *= scale;
         }
-      }
-      const float2 sums = unpair(add2(sum[0], sum[1]));
-      l += sums.x + sums.y;
-      // the MMAs before these scores are complete, the one before on O among them (apart: see above)
-      if (t > it.t0 && __any_sync(0xffffffffu, grow)) {
+        if (__any_sync(0xffffffffu, here < kTile)) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (k >= here) z[k] = -INFINITY;
+        }
+      };
+      auto maximum = [&](const float (&z)[128]) {
+        float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int k = 4; k < 128; k += 8) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(fmaxf(mx[j], z[k + j]), k + 4 + j < 128 ? z[k + 4 + j] : -INFINITY);
+        }
+        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+      };
+      auto rescale = [&](float f) {  // O
 #pragma unroll 1
         for (int k = 0; k < p.x.d_v; k += 32) {
           uint32_t o[32];
@@ -1206,7 +1175,87 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
           for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
           tmem_st_32x32b_x32(tO + k, o);
         }
+      };
+      uint32_t w[64];
+      // one pair's weights, and their part of the sum; 16 bits: half a step, as one rounding of the output costs
+      auto weigh = [&](const float (&z)[128], int k, uint64_t mul_2, uint64_t mm_2, uint64_t& sum) {
+        float2 e = unpair(fma2(pair(z[2 * k], z[2 * k + 1]), mul_2, mm_2));
+        e.x = fast_exp2(e.x);
+        e.y = fast_exp2(e.y);
+        sum = add2(sum, pair(e.x, e.y));
+        w[k] = pack16<E>(e.x, e.y);
+      };
+      const uint64_t mul_2 = pair(mul, mul);
+      uint64_t sum[2];
+      // The maximum moves only when a tile exceeds it by more than 2^8: weights stay below
+      // 2^8 and O is rarely rescaled.
+      if constexpr (kPair) {
+        // So weights are made of the maximum so far while the tile's is found beside them, and in the
+        // rare case again from the scores, which stay in tensor memory until then: 8192 tokens, 32 heads
+        // on 8 of 128 372 -> 342 us.  A CTA alone is bound by shared memory or, with small heads, by the
+        // softmax warps together, whose phases then mix worse: prompts of 4096, heads of 64, 329 -> 359.
+        bool first = t == it.t0, again;
+        do {
+          float z[128];
+          load(z);
+          mask(z);
+          if (first) m = maximum(z);
+          first = false;
+          const float mm = m == -INFINITY ? 0.f : m;
+          const uint64_t mm_2 = pair(-mm, -mm);
+          sum[0] = sum[1] = 0;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            mx[k & 3] = fmaxf(fmaxf(mx[k & 3], z[2 * k]), z[2 * k + 1]);
+            weigh(z, k, mul_2, mm_2, sum[k & 1]);
+          }
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+          const bool grow = top > m + 8.f;
+          again = __any_sync(0xffffffffu, grow);
+          if (again) {  // the MMAs before these scores are complete, the one before on O among them
+            const float f = grow ? fast_exp2(m - top) : 1.f;
+            l *= f;
+            if (grow) m = top;
+            if (t > it.t0) rescale(f);
+          }
+        } while (again);
+        tmem_st_32x32b_x32(tP, *reinterpret_cast<uint32_t(*)[32]>(w));
+      } else {
+        float z[128];
+        load(z);
+        if (kApart && t + 1 < it.t1(h)) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c.bar(kSFree + h));
+        }
+        mask(z);
+        const float top = maximum(z);
+        const bool grow = top > m + 8.f;
+        const float f = grow ? fast_exp2(m - top) : 1.f;
+        if (grow) {
+          l *= f;
+          m = top;
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        const uint64_t mm_2 = pair(-mm, -mm);
+        sum[0] = sum[1] = 0;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          weigh(z, k, mul_2, mm_2, sum[k & 1]);
+          if (k == 31) {
+            if (kApart && t > it.t0) {  // the product before this one is through with the weights, and with O
+              if (!warp_wait(c, kPFree + h, products++ & 1)) return;
+              tc_fence_after();
+            }
+            tmem_st_32x32b_x32(tP, *reinterpret_cast<uint32_t(*)[32]>(w));
+          }
+        }
+        // the MMAs before these scores are complete, the one before on O among them (apart: see above)
+        if (t > it.t0 && __any_sync(0xffffffffu, grow)) rescale(f);
       }
+      const float2 sums = unpair(add2(sum[0], sum[1]));
+      l += sums.x + sums.y;
       tmem_st_32x32b_x32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
       tmem_wait_st();
       tc_fence_before();
