@@ -291,6 +291,27 @@ def test_many_rows(case):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("rise", [1.0, -1.0, 0.0])
+def test_many_rows_with_scores_that_grow(rise):
+    """Maxima that move with every tile, by far more than weights may grow, and rows that score -inf at first."""
+    import mla_sparse_top_gb300 as mla
+    m = make([1400], H=112, Hkv=2, D=64, Dv=128, seed=3)
+    n = 1400
+    m["q"][:n] = m["q"][:n].abs()  # so that a key's scores have its sign
+    steps = (torch.arange(n, device="cuda") // 100).float()
+    m["k"][:n] = (m["k"][:n].float() * 0.1 + (rise * steps)[:, None, None]).to(m["dtype"])
+    if rise == 0:
+        m["k"][:300] = -float("inf")  # three tiles, the first rows see nothing else
+    out, lse = run(m)
+    assert mla.heads_device_status(clear=True) == 0
+    if rise == 0:
+        assert (out[:300] == 0).all() and torch.isneginf(lse[:300]).all()
+        live = slice(300, n)  # their softmax is that over the finite keys
+        check_gpu(out[live], lse[live], m["q"][live], m["k"][live], m["v"][live], m["scale"], True, "behind -inf")
+    else:
+        check_gpu(out[:n], lse[:n], m["q"][:n], m["k"][:n], m["v"][:n], m["scale"], True, f"rise {rise}")
+
+
 def test_many_rows_with_values_that_are_not_finite():
     """A value in the half of the columns that the other SM of the pair holds reaches both SMs' rows, and no others."""
     m = make([1400], H=112, Hkv=2, D=128, Dv=128)
