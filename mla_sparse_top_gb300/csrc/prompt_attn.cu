@@ -33,7 +33,8 @@
 // product, 2900 to 3000 clocks a key tile where the MMAs of both tiles take 2560) and,
 // in long runs, by the power cap.  Measured (graph replay): 8192 tokens, 128 heads of 192
 // and 128, causal, 1600 to 1720 us (1.60 to 1.72 PFLOP/s; tensor cores active 75% of the
-// time); 32 heads of 128 on 8 key heads 365 (1.51 PFLOP/s), every key seen 682 (1.61).
+// time before maxima were found beside the weights); 32 heads of 128 on 8 key heads 344
+// (1.60 PFLOP/s), every key seen 660 (1.67).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1507,13 +1508,15 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 constexpr int kMaxParts = 640;  // partial states in the workspace at most
 
 // Whether pairs of CTAs run: they hold half of the keys and values each, which eases
-// shared memory, the bound of a CTA alone, but take 512 rows at a time.  Alone and in
-// pairs: one prompt of 8192, 128 heads of 192 and 128, 1888 and 1680 us; 32 heads of 128
-// on 8 key heads 382 and 366; 16 prompts of 512 (2048 rows to a key head) 77.6 and 81.1;
-// 40 of 20 to 2000 174 and 183.
+// shared memory, the bound of a CTA alone, but take 512 rows at a time, so they need
+// rows for two rounds.  Alone and in pairs: one prompt of 8192, 128 heads of 192 and 128,
+// 1888 and 1600 to 1670 us; 32 heads of 128 on 8 key heads 382 and 344, of 4096 127 and
+// 123; 64 heads on 8, 2048 tokens, 74 and 72; 16 prompts of 512 (2048 rows to a key head)
+// 72 and 73.  Chunks over long contexts, which are cut, gain 3 to 7%, but the host sees the
+// table's width, not their lengths, and 8 chunks of 300 over 2000 take 98 instead of 75.
 bool in_pairs(const Problem& p) {
   const int64_t rows = static_cast<int64_t>(p.T) * (p.n_q / p.n_kv);  // of a key head
-  return p.d_v > 64 && rows >= 4096 * static_cast<int64_t>(p.B) && rows * p.n_kv >= 4 * 512 * 76;
+  return p.d_v > 64 && rows >= 4096 * static_cast<int64_t>(p.B) && rows * p.n_kv >= 2 * 512 * 76;
 }
 int item_tiles(const Problem& p) { return in_pairs(p) ? 4 : 2; }
 

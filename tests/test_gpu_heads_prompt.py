@@ -263,7 +263,7 @@ def test_other_stream_and_captured():
     assert np.isfinite(np64(out)).all()
 
 
-# Calls with rows enough for pairs of SMs (512 rows at a time, at least 4096 of a key head for each sequence), or nearly
+# Calls with rows enough for pairs of SMs (512 rows at a time, at least 4096 of a key head for each sequence, two rounds in all), or nearly
 LARGE = [
     dict(lens=[1300], H=128, Hkv=128, D=192, Dv=128, pad=8), dict(lens=[2049], H=80, Hkv=2, D=128, Dv=128, spare=40, begin=3),
     dict(lens=[1025, 1030, 2000], H=48, Hkv=16, D=96, Dv=80, dtype="fp16"), dict(lens=[5, 1500, 0, 1200], H=128, Hkv=4, D=64, Dv=72),
