@@ -125,7 +125,8 @@ struct Split {
   }
 };
 
-// Steps of a share at least: fewer parts to join where there is little to read.
+// Steps of a share at least: fewer parts to join where there is little to read.  4 / 5 / 6 / 8:
+// one token over 1000 keys 9.4 / 10.4 / 10.8 / 10.7 us, 16 sequences of 100 9.7 / 14.5 / 15.9 / 15.
 constexpr int kMinSteps = 4;
 static_assert(kMinSteps > kHeadCost, "a share has a unit");
 
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 // shared out among a block's warps, and their slices among the groups that hold them.
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 constexpr int kAhead = 4;        // parts in flight
-constexpr int kFewParts = 8;
+constexpr int kFewParts = 8;     // 4 / 8 / 16: 24 chains of 500 to 20000 62 / 60.5 / 63 us
 constexpr int kMaxGroups = 152 * kWarps;
 
 struct State {
