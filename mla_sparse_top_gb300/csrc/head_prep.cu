@@ -165,7 +165,8 @@ struct Lane {
     }
   }
   __device__ __forceinline__ void load(const E* x, bool live, Pack<E, V> (&a)[KU], Pack<E, V> (&b)[KU]) const {
-    // what is not loaded holds zero from the start, or another head's values, whose results go nowhere
+    // what is never loaded holds zero from the start, which a norm's sums count on; behind the last head
+    // there are another head's values, whose results go nowhere
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       if (live && in[i]) {
@@ -316,7 +317,7 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
     return h.x + h.y;
   };
   // norm, rotation and store of a chunk
-  auto finish = [&](Pack<E, V>(&a)[KU], Pack<E, V>(&b)[KU], float mean, float inv, E* o, bool put) {
+  auto finish = [&](const Pack<E, V>(&a)[KU], const Pack<E, V>(&b)[KU], float mean, float inv, E* o, bool put) {
     const Two inv2 = two(inv, inv);
     float v[KU][L::kVals];
 #pragma unroll
@@ -360,15 +361,17 @@ __device__ __forceinline__ void work(const Params& p, const Tensor& w, int block
         v[i][2 * j + 1] = f.y;
       }
     }
+    // a and b stay as they came: a place that no load fills holds its zero for the heads that follow
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
+      Pack<E, V> first = a[i], second = b[i];
       if (normed || at.rot[i]) {  // else the values go as they came
-        pack<E, V>(a[i], v[i]);
-        if constexpr (kTwo) pack<E, V>(b[i], v[i] + V);
+        pack<E, V>(first, v[i]);
+        if constexpr (kTwo) pack<E, V>(second, v[i] + V);
       }
       if (put && at.in[i]) {
-        a[i].store(o + at.d[i]);
-        if (kTwo && at.rot[i]) b[i].store(o + at.d[i] + at.second);
+        first.store(o + at.d[i]);
+        if (kTwo && at.rot[i]) second.store(o + at.d[i] + at.second);
       }
     }
   };
