@@ -138,7 +138,8 @@ struct Head {
   int next;     // drawn so far
   int states;   // partial states
   int cap;      // key tiles of a part at most
-  int pad[4];
+  int failed;   // a wait ran out: not every part was written, nothing is joined
+  int pad[3];
 };
 // Of a partial state: the item that it is a part of.
 struct Record {
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
   const int chunks = (B + kPlanThreads - 1) / kPlanThreads;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (B <= kWarpSeqs) {  // one warp was launched
-    if (lane == 0) p.head->next = 0;
+    if (lane == 0) p.head->next = p.head->failed = 0;
     const WarpPlan w = plan_warp(p);
     if (lane < B) report_seq(w.s.bad_len, w.s.bad_table);
     if (lane == 0) p.head->states = w.states;
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const __grid_
     p.first[B] = static_cast<int>(carry[0]);
     p.head->items = few ? static_cast<int>(carry[0]) : 0;
     p.head->states = few ? static_cast<int>(carry[1]) : 0;
-    p.head->next = 0;
+    p.head->next = p.head->failed = 0;
     p.head->cap = cap;
   }
 }
@@ -1409,7 +1410,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attn_kernel(const __grid_c
     // a wait ran out: loads may still be in flight to shared memory; they take microseconds
     if (tid == 0) {
       atomicOr(&g_prompt_status, MLA_DEVICE_TIMEOUT);
-      p.head->states = 0;  // not every part was written, nor described: nothing is joined
+      // for the join alone: what the plan wrote may still be read by CTAs that come later
+      p.head->failed = 1;
     }
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 200000) {
@@ -1436,7 +1438,7 @@ constexpr int kMergeQuads = kMaxDv / 4 / kMergeSlices / 2;          // four colu
 template <typename E>
 __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int states = __ldcg(&p.head->states);
+  const int states = __ldcg(&p.head->failed) != 0 ? 0 : __ldcg(&p.head->states);
   const int row = threadIdx.x & 127, side = threadIdx.x >> 7, quads = p.x.d_v / 4;
   const int per_slice = (quads + kMergeSlices - 1) / kMergeSlices;  // at most 2 * kMergeQuads
   const int64_t step = static_cast<int64_t>(p.part_floats) * p.x.n_kv;      // an item's parts: heads lie between them
