@@ -276,13 +276,16 @@ __device__ __noinline__ bool infinite_column(const Params& p, int b, int hk, int
   return false;
 }
 
-// Rows of a unit's values that not every token sees, from row `first` on: those
+// Rows of a unit's values that not every token sees, from row `first` on (which may
+// lie far behind the unit: a page that does not exist): those
 // behind the sequence (from row `live` on) become zero, the others lose their NaN
 // and infinities, which a weight of 0 would carry into the product.  Warps that
 // share a unit write the same; the flag is up before a value is gone.
 template <typename E>
 __device__ __noinline__ void mend_values(const Ctx& c, uint32_t vs, int chunks, int first, int live, int lane) {
   const int units = 8 * chunks;
+  first = max(0, min(first, kUnit));  // before it is multiplied: a sequence may have 2^30 keys
+  live = max(first, min(live, kUnit));
   auto at = [&](int i) {
     const int r = i / units, col = i - r * units;
     return vs + (col >> 3) * kChunk + r * 128 + (((col & 7) ^ (r & 7)) << 4);
@@ -295,7 +298,7 @@ __device__ __noinline__ void mend_values(const Ctx& c, uint32_t vs, int chunks, 
   auto store = [&](int i, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at(i)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
   };
-  const int begin = max(0, first) * units, middle = max(max(0, first), min(live, kUnit)) * units;
+  const int begin = first * units, middle = live * units;
   bool good = true;
   for (int i = begin + lane; i < middle; i += 32) good = good && finite4<E>(load(i));
   if (__any_sync(0xffffffffu, !good)) {
