@@ -33,8 +33,10 @@
  * Numerics: products of 16-bit values are exact and summed in fp32; the softmax
  * runs in fp32 with a running maximum and sum; the weights enter the second
  * product rounded once to the heads' type (at most 2^-8 (bf16) or 2^-11 (fp16)
- * relative each; they are summed unrounded), so an output is off by up to that
- * times sum_p softmax_p |v_p| on top of its own rounding.  The result of a call
+ * relative each; in fp16 a weight below 2^-21 of the row's largest may be off by
+ * 2^-32 of that instead; they are summed unrounded), so an output is off by up
+ * to that times sum_p softmax_p |v_p|, and in fp16 by 2^-32 max_p |v_p| for each
+ * key at most, on top of its own rounding.  The result of a call
  * does not depend on timing: a repeated call gives the same bits.
  *
  * Conventions are those of mla_sparse.h: device pointers owned by the caller,

@@ -501,12 +501,13 @@ __device__ void consume_role(const Params& p, const Ctx& c, int warp, int lane, 
         top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
         top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2)) * mul;
       }
-      // the maximum moves only when a unit exceeds it by more than 2^8: weights stay below 2^8
-      const bool grow0 = top[0] > m[0] + 8.f, grow1 = top[1] > m[1] + 8.f;
+      // the maximum moves only when a unit exceeds it by more than 2^8: weights stay below 2^8 (lifted, 2^15)
+      const bool grow0 = top[0] > m[0] + (8.f + kLift<E>), grow1 = top[1] > m[1] + (8.f + kLift<E>);
       if (__any_sync(0xffffffffu, grow0 || grow1)) {
-        const float f0 = grow0 ? fast_exp2(m[0] - top[0]) : 1.f, f1 = grow1 ? fast_exp2(m[1] - top[1]) : 1.f;
-        if (grow0) m[0] = top[0];
-        if (grow1) m[1] = top[1];
+        const float m0 = top[0] - kLift<E>, m1 = top[1] - kLift<E>;
+        const float f0 = grow0 ? fast_exp2(m[0] - m0) : 1.f, f1 = grow1 ? fast_exp2(m[1] - m1) : 1.f;
+        if (grow0) m[0] = m0;
+        if (grow1) m[1] = m1;
         l[0] *= f0;
         l[1] *= f1;
 #pragma unroll

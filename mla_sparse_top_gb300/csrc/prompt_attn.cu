@@ -1190,7 +1190,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
       const uint64_t mul_2 = pair(mul, mul);
       uint64_t sum[2];
       // The maximum moves only when a tile exceeds it by more than 2^8: weights stay below
-      // 2^8 and O is rarely rescaled.
+      // 2^8 (lifted, 2^15) and O is rarely rescaled.
       if constexpr (kPair) {
         // So weights are made of the maximum so far while the tile's is found beside them, and in the
         // rare case again from the scores, which stay in tensor memory until then: 8192 tokens, 32 heads
@@ -1201,7 +1201,7 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
           float z[128];
           load(z);
           mask(z);
-          if (first) m = maximum(z);
+          if (first) m = maximum(z) - kLift<E>;
           first = false;
           const float mm = m == -INFINITY ? 0.f : m;
           const uint64_t mm_2 = pair(-mm, -mm);
@@ -1213,12 +1213,12 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
             weigh(z, k, mul_2, mm_2, sum[k & 1]);
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
-          const bool grow = top > m + 8.f;
+          const bool grow = top > m + (8.f + kLift<E>);
           again = __any_sync(0xffffffffu, grow);
           if (again) {  // the MMAs before these scores are complete, the one before on O among them
-            const float f = grow ? fast_exp2(m - top) : 1.f;
+            const float to = top - kLift<E>, f = grow ? fast_exp2(m - to) : 1.f;
             l *= f;
-            if (grow) m = top;
+            if (grow) m = to;
             if (t > it.t0) rescale(f);
           }
         } while (again);
@@ -1233,11 +1233,11 @@ __device__ void softmax_role(const Params& p, const Ctx& c, int warp, int lane) 
         }
         mask(z);
         const float top = maximum(z);
-        const bool grow = top > m + 8.f;
-        const float f = grow ? fast_exp2(m - top) : 1.f;
+        const bool grow = top > m + (8.f + kLift<E>);
+        const float to = top - kLift<E>, f = grow ? fast_exp2(m - to) : 1.f;
         if (grow) {
           l *= f;
-          m = top;
+          m = to;
         }
         const float mm = m == -INFINITY ? 0.f : m;
         const uint64_t mm_2 = pair(-mm, -mm);
