@@ -137,8 +137,8 @@ struct Head {
   int items;    // parts of all items
   int next;     // drawn so far
   int states;   // partial states
-  int cap;      // key tiles of a part at most
   int failed;   // a wait ran out: not every part was written, nothing is joined
+  int cap;      // key tiles of a part at most
   int pad[3];
 };
 // Of a partial state: the item that it is a part of.
@@ -1438,7 +1438,8 @@ constexpr int kMergeQuads = kMaxDv / 4 / kMergeSlices / 2;          // four colu
 template <typename E>
 __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int states = __ldcg(&p.head->failed) != 0 ? 0 : __ldcg(&p.head->states);
+  const int4 head = __ldcg(reinterpret_cast<const int4*>(p.head));  // items, next, states, failed
+  const int states = head.w != 0 ? 0 : head.z;
   const int row = threadIdx.x & 127, side = threadIdx.x >> 7, quads = p.x.d_v / 4;
   const int per_slice = (quads + kMergeSlices - 1) / kMergeSlices;  // at most 2 * kMergeQuads
   const int64_t step = static_cast<int64_t>(p.part_floats) * p.x.n_kv;      // an item's parts: heads lie between them
