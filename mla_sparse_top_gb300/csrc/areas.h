@@ -3,6 +3,8 @@
 #pragma once
 #include <stdint.h>
 
+#include <initializer_list>
+
 namespace mlasp {
 
 inline bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }

@@ -10,7 +10,7 @@
 // Measured (graph replay): 8192 tokens of 32 + 8 heads of 128 in bf16, RMS norms and
 // rotation, 33 us (168 MB, 5.1 TB/s), with 64 + 8 heads 52 (5.8 TB/s); 16384 new tokens to
 // the cache, 28 + 4 + 4 heads of 128 of which 64 turn, no norm, 54 us (302 MB, 5.6 TB/s); 64 new tokens 5.6 us, of which
-// the launch is most; 4099 tokens of 17 fp32 heads of 107, LayerNorm, 36 us: single
+// the launch is most; 4099 tokens of 17 fp32 heads of 107, LayerNorm, 35 us: single
 // values and two sums that follow one another, bound by latency and instructions.
 #include <cuda_runtime.h>
 #include <stdarg.h>
@@ -51,7 +51,7 @@ struct Tensor {
   const void* bias;
   float eps, inv_d;
   int kind, weight_fp32, weight_vec;  // vec: weights are read 16 bytes at a time
-  int n_heads, rot_off, head_dim;
+  int n_heads, rot_off;
   int pairs, half;     // of the rotation; 0 pairs: none
   int rot_units;       // units of a head that hold rotated values
   int units;           // all units of a head
@@ -610,7 +610,6 @@ mla_status split_job(const Job& j, int T, int dtype, bool half, Tensor* w) {
   w->weight_vec = j.vec && aligned(j.norm.weight, 16) && aligned(j.norm.bias, 16) ? 1 : 0;
   w->n_heads = j.n_heads;
   w->rot_off = j.rot_off;
-  w->head_dim = j.head_dim;
   w->pairs = j.rot_dim / 2;
   w->half = half ? 1 : 0;
   const int width = !j.vec ? 1 : (dtype == MLA_ROPE_FP32 ? 4 : 8);
@@ -707,11 +706,8 @@ Job rope_job(const char* name, const mla_rope_tensor& q, const mla_head_norm* no
 }
 
 // The scheme of a call that may rotate nothing.
-mla_status make_scheme(const mla_rope_params* params, const int32_t* positions, int rot_dim, Freqs* f) {
-  if (rot_dim == 0) return MLA_OK;
-  const mla_status st = mlarp::make_freqs(params, rot_dim, f, fail);
-  if (st != MLA_OK) return st;
-  return MLA_OK;
+mla_status make_scheme(const mla_rope_params* params, int rot_dim, Freqs* f) {
+  return rot_dim == 0 ? MLA_OK : mlarp::make_freqs(params, rot_dim, f, fail);
 }
 
 }  // namespace
@@ -730,7 +726,7 @@ mla_status mla_norm_rope(const mla_rope_dims* dims, const mla_rope_params* param
   if (d.T < 0 || d.half < 0 || d.half > 1) return fail(MLA_ERR_SHAPE, "T must be >= 0, half 0 or 1");
   if (d.inverse != 0) return fail(MLA_ERR_UNSUPPORTED, "inverse must be 0");
   Params p;
-  mla_status st = make_scheme(params, positions, d.rot_dim, &p.f);
+  mla_status st = make_scheme(params, d.rot_dim, &p.f);
   if (st != MLA_OK) return st;
   if (d.T == 0) return MLA_OK;
   if (d.rot_dim > 0 && !positions) return fail(MLA_ERR_NULL, "positions is NULL");
@@ -760,7 +756,7 @@ mla_status mla_kv_append(const mla_append_dims* dims, const mla_rope_params* par
     return fail(MLA_ERR_SHAPE, "num_blocks=%d outside [1, 2^24)", d.num_blocks);
   if (q != nullptr && q->rows != nullptr) return fail(MLA_ERR_UNSUPPORTED, "q's rows must be NULL");
   Params p;
-  mla_status st = make_scheme(params, positions, d.rot_dim, &p.f);
+  mla_status st = make_scheme(params, d.rot_dim, &p.f);
   if (st != MLA_OK) return st;
   if (d.T == 0) return MLA_OK;
   if (!rows || (d.rot_dim > 0 && !positions)) return fail(MLA_ERR_NULL, "rows or positions is NULL");
