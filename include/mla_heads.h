@@ -150,7 +150,11 @@ typedef struct mla_prompt_dims {
 
 /* Bytes of workspace mla_prompt_attn_fwd needs for these dims; 0 for invalid
  * dims.  It needs no initialisation and carries nothing from call to call;
- * calls that may overlap in time need one each. */
+ * calls that may overlap in time need one each.  Some 12 bytes a sequence and,
+ * where sequences may have more than 512 keys, room for the parts of items that
+ * are cut along their keys, whether or not any is: as many as the dims allow, at
+ * most 640 of 1024 * d_v + 2048 bytes (85 MB at d_v = 128), twice that size with
+ * d_v above 64 and 4096 rows (T * n_q / n_kv) or more of a key head a sequence. */
 size_t mla_prompt_workspace_bytes(const mla_prompt_dims* dims);
 
 /*
@@ -191,6 +195,8 @@ typedef struct mla_paged_dims {
   int32_t max_blocks_per_seq; /* block_table row width, in [1, 2^23] */
 } mla_paged_dims;
 
+/* As mla_prompt_workspace_bytes; up to 64 rows (S1 * n_q / n_kv) of a key head
+ * at most 20 MB (5 MB for 4 rows at d_v = 128), with more what prompts need. */
 size_t mla_paged_workspace_bytes(const mla_paged_dims* dims);
 
 /*

@@ -2,8 +2,10 @@
 // (sm_103a); formulas in mla_heads.h.
 //
 // The keys and values of a sequence are read once and meet few rows (the S1 new
-// tokens of the G heads that share them), so memory binds.  A CTA holds eight
-// pipelines of two warps: one streams units of 32 keys, keys and values together,
+// tokens of the G heads that share them), so memory binds.  A CTA holds up to eight
+// pipelines of two warps (as many as get two slots each: eight where keys and values
+// have at most three 64-column chunks together, seven at 128 and 128, five at 192 and
+// 128; the warps left over idle): one streams units of 32 keys, keys and values together,
 // by TMA into slots of shared memory that no other pipeline touches, the other
 // takes 16 rows through them with the running maximum, sum and output in
 // registers, as accumulators of mma.sync (m16n8k16: the 128-row tiles of tcgen05

@@ -33,8 +33,7 @@
 // product, 2900 to 3000 clocks a key tile where the MMAs of both tiles take 2560) and,
 // in long runs, by the power cap.  Measured (graph replay): 8192 tokens, 128 heads of 192
 // and 128, causal, 1600 to 1720 us (1.60 to 1.72 PFLOP/s; tensor cores active 75% of the
-// time before maxima were found beside the weights); 32 heads of 128 on 8 key heads 344
-// (1.60 PFLOP/s), every key seen 660 (1.67).
+// time); 32 heads of 128 on 8 key heads 344 (1.60 PFLOP/s), every key seen 660 (1.67).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1509,6 +1508,7 @@ std::mutex g_lock;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 constexpr int kMaxParts = 640;  // partial states in the workspace at most
+constexpr int kSmPairs = 76;    // of a GB300; a constant, since the workspace's size is asked for without a device
 
 // Whether pairs of CTAs run: they hold half of the keys and values each, which eases
 // shared memory, the bound of a CTA alone, but take 512 rows at a time, so they need
@@ -1519,7 +1519,7 @@ constexpr int kMaxParts = 640;  // partial states in the workspace at most
 // table's width, not their lengths, and 8 chunks of 300 over 2000 take 98 instead of 75.
 bool in_pairs(const Problem& p) {
   const int64_t rows = static_cast<int64_t>(p.T) * (p.n_q / p.n_kv);  // of a key head
-  return p.d_v > 64 && rows >= 4096 * static_cast<int64_t>(p.B) && rows * p.n_kv >= 2 * 512 * 76;
+  return p.d_v > 64 && rows >= 4096 * static_cast<int64_t>(p.B) && rows * p.n_kv >= 2 * 512 * kSmPairs;
 }
 int item_tiles(const Problem& p) { return in_pairs(p) ? 4 : 2; }
 
